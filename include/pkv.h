@@ -186,6 +186,61 @@ pkv_status pkv_set_block_table(pkv_seq* seq, const int32_t* bt, int64_t n);
  * after a partial page (then the partial page is completed first). */
 pkv_status pkv_append(pkv_seq* seq, const void* k, const void* v, int64_t n_tok, void* stream);
 
+/* ---------------------------------------------------------------- rotation
+ * Rotary position embedding of Q and K rows. Pair i of a row at position p,
+ * i < rotary_dim / 2, turns by the angle p * inv_freq[i]:
+ *   (x, y) -> (x cos - y sin, y cos + x sin);
+ * dims rotary_dim .. head_dim - 1 pass through. The angle is formed exactly
+ * modulo one turn (64-bit fixed point) for any int64 position; cos, sin and the
+ * products are float32, rounded once to the pool's dtype.
+ * rotary_dim must be even and at most head_dim (else PKV_ERR_INVALID) and a
+ * multiple of 16 (else PKV_ERR_UNSUPPORTED).
+ *
+ * Row operands of the calls below have a stride, in elements, between
+ * consecutive tokens' rows (0 = dense): the Q, K and V of one projection's
+ * [n, (Hq + 2 Hkv) * d] output are passed as its slices. Pointers must be 16-byte
+ * aligned, strides at least heads * head_dim and a multiple of 16 bytes. An
+ * output may be its own input (same pointer and stride); other overlaps are
+ * not allowed. */
+typedef struct pkv_rope {
+    const float* inv_freq;     /* device float32 [rotary_dim / 2], radians per position   */
+    const int64_t* positions;  /* device int64 [n], one per row of the call (documents
+                                  that count from 0 again), or NULL: pos0 + row           */
+    int64_t pos0;
+    int32_t rotary_dim;
+    int32_t interleaved;       /* 0: dim i pairs with i + rotary_dim / 2; 1: 2i with 2i + 1 */
+} pkv_rope;
+
+/* pkv_append with the rotation applied on the way: k's rows are turned, rounded
+ * and stored in the pages, v's are stored as they are; page representatives
+ * (means of the keys as stored), zero-filled rows and zeroed gradient pages as
+ * for pkv_append. If q is not NULL its [n_tok, Hq, d] rows are turned by the
+ * same positions into q_out (dense). One launch. The sequence advances on the
+ * host, so the call is refused (PKV_ERR_INVALID) on a capturing stream. */
+pkv_status pkv_append_rope(pkv_seq* seq, const void* q, int64_t q_stride, void* q_out,
+                           const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                           int64_t n_tok, const pkv_rope* rope, void* stream);
+
+/* The rotation alone: rows x [n, n_heads, d] (pool dtype) -> out, by the
+ * opposite angles if inverse is 1. For activation recomputation, where Q is
+ * projected again and its keys are in the cache already. */
+pkv_status pkv_rope_rows(const pkv_pool* pool, const void* x, int64_t x_stride, void* out,
+                         int64_t out_stride, int64_t n, int32_t n_heads, const pkv_rope* rope,
+                         int32_t inverse, void* stream);
+
+/* The gradient of pkv_append_rope for rows [row0, row0 + n_rows) of the
+ * sequence (any row0 >= 0, row0 + n_rows <= length): dq [n_rows, Hq, d] (pool
+ * dtype, the attention backward's output) and the rows' fp32 dK from the
+ * gradient pages are turned by the opposite angles, dV is taken as it is, and
+ * all three are rounded once and written in the pool's dtype. rope->positions
+ * (or pos0) are those of the rows. dq and dq_out may both be NULL, dk_out and
+ * dv_out each. For a PINNED_HOST pool it reads the host gradient pages, as
+ * pkv_gather_rows does. */
+pkv_status pkv_rope_grad(pkv_seq* seq, int64_t row0, int64_t n_rows, const pkv_rope* rope,
+                         const void* dq, int64_t dq_stride, void* dq_out, int64_t dq_out_stride,
+                         void* dk_out, int64_t dk_stride, void* dv_out, int64_t dv_stride,
+                         void* stream);
+
 /* ---------------------------------------------------------------- attention (a3, a4, a6)
  * One query chunk: queries at positions q_start..q_start+n_q-1, with
  * q_start % P == 0 and q_start + n_q <= the sequence length (the chunk's own

@@ -43,6 +43,12 @@ class pkv_sel(ctypes.Structure):
                 ("reserved", ctypes.c_int32), ("n_qp", ctypes.c_int64)]
 
 
+class pkv_rope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("pos0", ctypes.c_int64), ("rotary_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
+
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
@@ -63,6 +69,11 @@ _SIGS = {
     "pkv_get_block_table": (_ST, [_P, _P, _I64, ctypes.POINTER(_I64)]),
     "pkv_set_block_table": (_ST, [_P, _P, _I64]),
     "pkv_append": (_ST, [_P, _P, _P, _I64, _P]),
+    "pkv_append_rope": (_ST, [_P, _P, _I64, _P, _P, _I64, _P, _I64, _I64,
+                              ctypes.POINTER(pkv_rope), _P]),
+    "pkv_rope_rows": (_ST, [_P, _P, _I64, _P, _I64, _I64, _I32, ctypes.POINTER(pkv_rope), _I32, _P]),
+    "pkv_rope_grad": (_ST, [_P, _I64, _I64, ctypes.POINTER(pkv_rope), _P, _I64, _P, _I64, _P, _I64,
+                            _P, _I64, _P]),
     "pkv_chunk_attn_fwd": (_ST, [_P, _P, _I64, _I64, _P, _P, ctypes.POINTER(pkv_sel), _P]),
     "pkv_chunk_attn_bwd": (_ST, [_P, _P, _P, _P, _P, _I64, _I64, _P, ctypes.POINTER(pkv_sel), _P]),
     "pkv_chunk_attn_bwd_noalloc": (_ST, [_P, _P, _P, _P, _P, _I64, _I64, _P,
@@ -115,6 +126,51 @@ def ptr(x) -> Optional[int]:
         raise ValueError(f"tensor of shape {tuple(x.shape)} with strides {x.stride()} is not "
                          "contiguous; pass .contiguous()")
     return x.data_ptr()
+
+
+def rows_ptr(x, n: int):
+    """(address, row stride in elements) of a tensor [n, heads, d] whose rows are
+    dense and may lie apart, such as a slice of a wider projection's output; an
+    int address is taken as dense (stride 0)."""
+    if x is None or isinstance(x, int):
+        return x, 0
+    if x.dim() != 3 or x.shape[0] != n:
+        raise ValueError(f"expected a tensor [{n}, heads, d], got shape {tuple(x.shape)}")
+    _, h, d = x.shape
+    if x.numel() and (x.stride(2) != 1 or (h > 1 and x.stride(1) != d) or
+                      (n > 1 and x.stride(0) < h * d)):
+        raise ValueError(f"tensor of shape {tuple(x.shape)} with strides {x.stride()}: every row "
+                         "must be dense [heads, d] memory of its own")
+    return x.data_ptr(), (x.stride(0) if n > 1 else 0)
+
+
+def _typed(x, name: str, dtype: str, n=None):
+    """Address of a tensor that must have this dtype (and number of elements), an int, or None."""
+    if x is None or isinstance(x, int):
+        return x
+    if str(x.dtype) != "torch." + dtype:
+        raise ValueError(f"{name} must be {dtype}, got {x.dtype}")
+    if n is not None and x.numel() != n:
+        raise ValueError(f"{name} must have {n} elements, got {x.numel()}")
+    return ptr(x)
+
+
+def rope(inv_freq, pos0: int = 0, positions=None, interleaved: bool = False) -> pkv_rope:
+    """The rotation of a call: inv_freq float32 [rotary_dim / 2], positions int64
+    [n] (one per row) or None for pos0 + row. Keeps the tensors alive."""
+    r = pkv_rope(_typed(inv_freq, "inv_freq", "float32"), _typed(positions, "positions", "int64"),
+                 int(pos0), 2 * inv_freq.numel(), 1 if interleaved else 0)
+    r.tensors = (inv_freq, positions)
+    return r
+
+
+def _rope(r: Optional[pkv_rope], n: int):
+    if r is None:
+        return None
+    pos = getattr(r, "tensors", (None, None))[1]
+    if pos is not None and pos.numel() != n:
+        raise ValueError(f"positions must have one entry per row ({n}), got {pos.numel()}")
+    return ctypes.byref(r)
 
 
 def stream_ptr(stream) -> Optional[int]:
@@ -215,6 +271,29 @@ def pkv_set_block_table(seq, bt) -> None:
 
 def pkv_append(seq, k, v, n_tok, stream=None) -> None:
     _check(lib().pkv_append(seq, ptr(k), ptr(v), n_tok, stream_ptr(stream)))
+
+
+def pkv_append_rope(seq, q, q_out, k, v, n_tok, rope, stream=None) -> None:
+    """q, k, v: tensors [n_tok, heads, d] whose rows may lie apart (slices of one
+    projection's output); q and q_out may be None."""
+    (qp, qs), (kp, ks), (vp, vs) = (rows_ptr(x, n_tok) for x in (q, k, v))
+    _check(lib().pkv_append_rope(seq, qp, qs, ptr(q_out), kp, ks, vp, vs, n_tok, _rope(rope, n_tok),
+                                 stream_ptr(stream)))
+
+
+def pkv_rope_rows(pool, x, out, n, n_heads, rope, inverse=False, stream=None) -> None:
+    (xp, xs), (op, os_) = rows_ptr(x, n), rows_ptr(out, n)
+    _check(lib().pkv_rope_rows(pool, xp, xs, op, os_, n, n_heads, _rope(rope, n),
+                               1 if inverse else 0, stream_ptr(stream)))
+
+
+def pkv_rope_grad(seq, row0, n_rows, rope, dq=None, dq_out=None, dk_out=None, dv_out=None,
+                  stream=None) -> None:
+    """dq and the outputs: tensors [n_rows, heads, d] whose rows may lie apart."""
+    (qp, qs), (op, os_), (kp, ks), (vp, vs) = (rows_ptr(x, n_rows)
+                                                for x in (dq, dq_out, dk_out, dv_out))
+    _check(lib().pkv_rope_grad(seq, row0, n_rows, _rope(rope, n_rows), qp, qs, op, os_, kp, ks, vp, vs,
+                               stream_ptr(stream)))
 
 
 def pkv_chunk_attn_fwd(seq, q, q_start, n_q, o, lse, sel=None, stream=None) -> None:

@@ -122,7 +122,7 @@ static pkv_status validate_desc(const pkv_pool_desc* d) {
     return PKV_OK;
 }
 
-static bool is_device(const pkv_pool* p) { return p->desc.residency != PKV_RES_META; }
+bool pkv::is_device(const pkv_pool* p) { return p->desc.residency != PKV_RES_META; }
 
 // Claims pages so that the sequence covers new_len tokens. Host-only; on
 // failure nothing changes.
@@ -189,7 +189,7 @@ static pkv_status upload_bt(pkv_seq* s, int64_t from, cudaStream_t st) {
     return PKV_OK;
 }
 
-static pkv_status check_stream_device(const pkv_pool* p) {
+pkv_status pkv::check_stream_device(const pkv_pool* p) {
     int dev = -1;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
@@ -510,39 +510,53 @@ pkv_status pkv_set_block_table(pkv_seq* s, const int32_t* bt, int64_t n) {
     return PKV_OK;
 }
 
-pkv_status pkv_append(pkv_seq* s, const void* k, const void* v, int64_t n_tok, void* stream) {
-    if (!s || n_tok < 0) return fail(PKV_ERR_INVALID, "pkv_append: bad argument");
-    if (n_tok == 0) return PKV_OK;
-    if (!k || !v) return fail(PKV_ERR_INVALID, "pkv_append: k or v is NULL");
+}  // extern "C"
+
+pkv_status pkv::append_begin(pkv_seq* s, int64_t n_tok, cudaStream_t cs, AppendArgs* a, const char* who) {
     pkv_pool* p = s->pool;
-    if (!is_device(p)) return fail(PKV_ERR_INVALID, "pkv_append: META pool holds no data");
     pkv_status st = check_stream_device(p);
     if (st != PKV_OK) return st;
     const int64_t old_pages = (int64_t)s->bt.size();
     st = claim_pages(s, s->len + n_tok);
     if (st != PKV_OK) return st;
-    cudaStream_t cs = static_cast<cudaStream_t>(stream);
     st = upload_bt(s, old_pages, cs);
     if (st != PKV_OK) return st;
     if (s->d_slot_of && s->len % p->desc.page_size != 0) {
         // Extending a partial page that may be staged: its slot's K/V goes stale.
         cudaError_t e = cudaStreamWaitEvent(cs, s->staged, 0);
         if (e == cudaSuccess) e = launch_stage_invalidate_kv(s, s->len / p->desc.page_size, cs);
-        if (e != cudaSuccess) return cuda_fail(e, "pkv_append: slot invalidation");
+        if (e != cudaSuccess) return cuda_fail(e, (std::string(who) + ": slot invalidation").c_str());
     }
-    AppendArgs a{};
-    a.P = p->desc.page_size; a.Hkv = p->desc.n_kv_heads; a.d = p->desc.head_dim;
-    a.dtype = p->desc.dtype;
-    a.k_in = k; a.v_in = v;
-    a.kpool = p->k; a.vpool = p->v; a.dkpool = p->dk; a.dvpool = p->dv; a.rep = p->rep;
-    a.bt = s->d_bt; a.num_phys = p->desc.num_phys_pages;
-    a.old_len = s->len; a.n_tok = n_tok; a.gzero = p->gzero; a.err = p->d_err;
+    *a = AppendArgs{};
+    a->P = p->desc.page_size; a->Hkv = p->desc.n_kv_heads; a->d = p->desc.head_dim;
+    a->dtype = p->desc.dtype;
+    a->kpool = p->k; a->vpool = p->v; a->dkpool = p->dk; a->dvpool = p->dv; a->rep = p->rep;
+    a->bt = s->d_bt; a->num_phys = p->desc.num_phys_pages;
+    a->old_len = s->len; a->n_tok = n_tok; a->gzero = p->gzero; a->err = p->d_err;
     if (p->gzero) s->gzero_possible = true;              // fresh pages are recorded as zero
-    cudaError_t e = launch_append(a, cs);
+    return PKV_OK;
+}
+
+pkv_status pkv::append_end(pkv_seq* s, int64_t n_tok, cudaError_t e, cudaStream_t cs, const char* who) {
     if (e == cudaSuccess && s->used) e = cudaEventRecord(s->used, cs);
-    if (e != cudaSuccess) return cuda_fail(e, "pkv_append: launch");
+    if (e != cudaSuccess) return cuda_fail(e, (std::string(who) + ": launch").c_str());
     s->len += n_tok;
     return PKV_OK;
+}
+
+extern "C" {
+
+pkv_status pkv_append(pkv_seq* s, const void* k, const void* v, int64_t n_tok, void* stream) {
+    if (!s || n_tok < 0) return fail(PKV_ERR_INVALID, "pkv_append: bad argument");
+    if (n_tok == 0) return PKV_OK;
+    if (!k || !v) return fail(PKV_ERR_INVALID, "pkv_append: k or v is NULL");
+    if (!is_device(s->pool)) return fail(PKV_ERR_INVALID, "pkv_append: META pool holds no data");
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    AppendArgs a{};
+    const pkv_status st = append_begin(s, n_tok, cs, &a, "pkv_append");
+    if (st != PKV_OK) return st;
+    a.k_in = k; a.v_in = v;
+    return append_end(s, n_tok, launch_append(a, cs), cs, "pkv_append");
 }
 
 }  // extern "C"

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <exception>
 #include <string>
 #include <vector>
 
@@ -104,6 +105,22 @@ struct ProfScope {
 // Sets the thread's last-error message and returns the status.
 pkv_status fail(pkv_status s, const std::string& msg);
 pkv_status cuda_fail(cudaError_t e, const char* what);
+// Runs the body of a C entry point; what it throws (host memory) becomes a status.
+template <typename F> pkv_status guarded(const char* who, F&& body) noexcept {
+    try {
+        return body();
+    } catch (const std::exception& e) {
+        try {
+            return fail(PKV_ERR_OOM, std::string(who) + ": " + e.what());
+        } catch (...) {
+            return PKV_ERR_OOM;
+        }
+    }
+}
+
+bool is_device(const pkv_pool* p);                   // the pool has page memory (not META)
+// PKV_ERR_INVALID unless the current CUDA device is the pool's.
+pkv_status check_stream_device(const pkv_pool* p);
 
 struct AppendArgs {
     int P, Hkv, d, dtype;
@@ -121,6 +138,11 @@ struct AppendArgs {
     int* err;
 };
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t s);
+// The host side of an append of n_tok tokens: claims and uploads pages and fills
+// a (all but the inputs); append_end takes the launch's result and advances the
+// sequence.
+pkv_status append_begin(pkv_seq* s, int64_t n_tok, cudaStream_t cs, AppendArgs* a, const char* who);
+pkv_status append_end(pkv_seq* s, int64_t n_tok, cudaError_t launched, cudaStream_t cs, const char* who);
 
 // dst[i] = src[i], i < n, src in mapped pinned host memory (no copy engine).
 cudaError_t launch_bt_upload(const int32_t* src, int32_t* dst, int64_t n, cudaStream_t s);
