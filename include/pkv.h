@@ -265,6 +265,51 @@ pkv_status pkv_chunk_attn_bwd(pkv_seq* seq, const void* q, const void* o, const 
                               const float* lse, int64_t q_start, int64_t n_q, void* dq,
                               const pkv_sel* sel, void* stream);
 
+/* ---- modified scores
+ * The attention calls with scores that are capped, lowered with distance and
+ * restricted to a range of keys per query:
+ *   s_ij = q_i . k_j / sqrt(d)
+ *   softcap c > 0:  s_ij <- c tanh(s_ij / c)
+ *   slopes:         s_ij <- s_ij - slopes[h] * |i - j|     (i, j: positions)
+ *   key j is visible to query i iff k_begin[i] <= j < k_end[i], both clipped to
+ *   the sequence; k_begin NULL is 0, k_end NULL is i + 1 (causal).
+ * One range per query holds packed documents (k_begin = the document's first
+ * token), a prefix seen as a whole (k_end = max(i + 1, prefix length)), a
+ * sliding window, and padding rows (k_end = 0); ranges need not be monotone. A
+ * query that sees no key gets O = 0, LSE = -inf, dQ = 0 and adds nothing to
+ * dK/dV. LSE is that of the modified scores. The arrays are device memory and
+ * are read when the kernels run; the [n_q] ones hold the chunk's queries in order.
+ * A hidden key or query is hidden by a zero weight: K, V of the pages a call
+ * reads and Q, O, dO of its rows must be finite there too (0 * inf is NaN). */
+typedef struct pkv_score_mod {
+    float softcap;             /* 0: none; else in [1e-3, 1e6]                            */
+    int32_t reserved;
+    const float* slopes;       /* device float32 [Hq] or NULL                             */
+    const int64_t* k_begin;    /* device int64 [n_q] or NULL                              */
+    const int64_t* k_end;      /* device int64 [n_q] or NULL                              */
+} pkv_score_mod;
+
+/* pkv_chunk_attn_fwd with modified scores. Unlike there, q_start may be any
+ * position when sel is NULL (a decoding step asks for the last token alone) and
+ * n_q may be 0; with k_end, keys behind the chunk's own (up to the sequence's
+ * length) may be visible. q and o must be 16-byte aligned. Short calls against
+ * long caches split the keys over CTAs and join the parts in scratch memory of
+ * the sequence: calls with modified scores on one sequence must not overlap on
+ * the GPU, and a stream capture needs an earlier call of the same size (else
+ * PKV_ERR_INVALID). Calls on a PINNED_HOST pool cannot be captured. */
+pkv_status pkv_chunk_attn_mod_fwd(pkv_seq* seq, const void* q, int64_t q_start, int64_t n_q,
+                                  void* o, float* lse, const pkv_score_mod* mod,
+                                  const pkv_sel* sel, void* stream);
+
+/* pkv_chunk_attn_bwd with modified scores: dQ written, dK/dV of every visible
+ * key added into the gradient pages; dS carries the cap's derivative
+ * 1 - tanh^2. mod is the forward's. Scratch, capture and alignment (q, o, dout,
+ * dq: 16 bytes) as for the forward; the page size must be a multiple of 16
+ * (else PKV_ERR_UNSUPPORTED). No gradient of slopes is computed. */
+pkv_status pkv_chunk_attn_mod_bwd(pkv_seq* seq, const void* q, const void* o, const void* dout,
+                                  const float* lse, int64_t q_start, int64_t n_q, void* dq,
+                                  const pkv_score_mod* mod, const pkv_sel* sel, void* stream);
+
 /* pkv_chunk_attn_bwd without any allocation. Same arguments, outputs and
  * results as pkv_chunk_attn_bwd; the paper has no counterpart: it exists for
  * callers that cannot let the library allocate device memory at call time

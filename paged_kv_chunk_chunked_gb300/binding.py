@@ -49,6 +49,12 @@ class pkv_rope(ctypes.Structure):
                 ("interleaved", ctypes.c_int32)]
 
 
+class pkv_score_mod(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("slopes", ctypes.c_void_p), ("k_begin", ctypes.c_void_p),
+                ("k_end", ctypes.c_void_p)]
+
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
@@ -76,6 +82,10 @@ _SIGS = {
                             _P, _I64, _P]),
     "pkv_chunk_attn_fwd": (_ST, [_P, _P, _I64, _I64, _P, _P, ctypes.POINTER(pkv_sel), _P]),
     "pkv_chunk_attn_bwd": (_ST, [_P, _P, _P, _P, _P, _I64, _I64, _P, ctypes.POINTER(pkv_sel), _P]),
+    "pkv_chunk_attn_mod_fwd": (_ST, [_P, _P, _I64, _I64, _P, _P, ctypes.POINTER(pkv_score_mod),
+                                     ctypes.POINTER(pkv_sel), _P]),
+    "pkv_chunk_attn_mod_bwd": (_ST, [_P, _P, _P, _P, _P, _I64, _I64, _P,
+                                     ctypes.POINTER(pkv_score_mod), ctypes.POINTER(pkv_sel), _P]),
     "pkv_chunk_attn_bwd_noalloc": (_ST, [_P, _P, _P, _P, _P, _I64, _I64, _P,
                                          ctypes.POINTER(pkv_sel), _P]),
     "pkv_grad_zero": (_ST, [_P, _P]),
@@ -171,6 +181,28 @@ def _rope(r: Optional[pkv_rope], n: int):
     if pos is not None and pos.numel() != n:
         raise ValueError(f"positions must have one entry per row ({n}), got {pos.numel()}")
     return ctypes.byref(r)
+
+
+def score_mod(softcap: float = 0.0, slopes=None, k_begin=None, k_end=None) -> pkv_score_mod:
+    """The score modification of a call: softcap (0: none), slopes float32 [Hq],
+    k_begin / k_end int64 [n_q] (first visible key of each query, one past its
+    last). Keeps the tensors alive."""
+    m = pkv_score_mod(float(softcap), 0, _typed(slopes, "slopes", "float32"),
+                      _typed(k_begin, "k_begin", "int64"), _typed(k_end, "k_end", "int64"))
+    m.tensors = (slopes, k_begin, k_end)
+    return m
+
+
+def _mod(m: Optional[pkv_score_mod], n_q: int, q):
+    if m is None:
+        return None
+    slopes, *ranges = getattr(m, "tensors", (None, None, None))
+    for x in ranges:
+        if hasattr(x, "numel") and x.numel() != n_q:
+            raise ValueError(f"k_begin and k_end must have one entry per query ({n_q}), got {x.numel()}")
+    if hasattr(slopes, "numel") and hasattr(q, "dim") and q.dim() == 3 and slopes.numel() != q.shape[1]:
+        raise ValueError(f"slopes must have one entry per query head ({q.shape[1]}), got {slopes.numel()}")
+    return ctypes.byref(m)
 
 
 def stream_ptr(stream) -> Optional[int]:
@@ -304,6 +336,16 @@ def pkv_chunk_attn_fwd(seq, q, q_start, n_q, o, lse, sel=None, stream=None) -> N
 def pkv_chunk_attn_bwd(seq, q, o, dout, lse, q_start, n_q, dq, sel=None, stream=None) -> None:
     _check(lib().pkv_chunk_attn_bwd(seq, ptr(q), ptr(o), ptr(dout), ptr(lse), q_start, n_q,
                                     ptr(dq), _sel(sel), stream_ptr(stream)))
+
+
+def pkv_chunk_attn_mod_fwd(seq, q, q_start, n_q, o, lse, mod, sel=None, stream=None) -> None:
+    _check(lib().pkv_chunk_attn_mod_fwd(seq, ptr(q), q_start, n_q, ptr(o), ptr(lse), _mod(mod, n_q, q),
+                                        _sel(sel), stream_ptr(stream)))
+
+
+def pkv_chunk_attn_mod_bwd(seq, q, o, dout, lse, q_start, n_q, dq, mod, sel=None, stream=None) -> None:
+    _check(lib().pkv_chunk_attn_mod_bwd(seq, ptr(q), ptr(o), ptr(dout), ptr(lse), q_start, n_q, ptr(dq),
+                                        _mod(mod, n_q, q), _sel(sel), stream_ptr(stream)))
 
 
 def pkv_chunk_attn_bwd_noalloc(seq, q, o, dout, lse, q_start, n_q, dq, sel=None,

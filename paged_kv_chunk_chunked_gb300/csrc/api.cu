@@ -435,6 +435,8 @@ void pkv_seq_free(pkv_seq* s) {
     auto& v = s->pool->seqs;
     v.erase(std::remove(v.begin(), v.end(), s), v.end());
     if (is_device(s->pool)) {
+        cudaFree(s->scratch);
+        for (float* old : s->retired) cudaFree(old);
         cudaFreeHost(s->h_bt);
         cudaFree(s->d_bt);
         cudaFree(s->d_slot_of); cudaFree(s->d_slot_page); cudaFree(s->d_flags);
@@ -562,12 +564,12 @@ pkv_status pkv_append(pkv_seq* s, const void* k, const void* v, int64_t n_tok, v
 }  // extern "C"
 
 pkv_status pkv::attn_common(pkv_seq* s, const void* q, int64_t q_start, int64_t n_q,
-                            const pkv_sel* sel, AttnArgs* a, const char* who) {
+                            const pkv_sel* sel, AttnArgs* a, const char* who, bool any_start) {
     if (!s || !q) return fail(PKV_ERR_INVALID, std::string(who) + ": NULL argument");
     pkv_pool* p = s->pool;
     if (!is_device(p)) return fail(PKV_ERR_INVALID, std::string(who) + ": META pool");
     const int64_t P = p->desc.page_size;
-    if (n_q <= 0 || q_start < 0 || q_start % P != 0 || q_start + n_q > s->len)
+    if (n_q <= 0 || q_start < 0 || (q_start % P != 0 && !any_start) || q_start + n_q > s->len)
         return fail(PKV_ERR_INVALID,
                     std::string(who) + ": need q_start % P == 0 and q_start + n_q <= length (" +
                         std::to_string(q_start) + " + " + std::to_string(n_q) +

@@ -38,6 +38,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "mod.cuh"
 #include "tc.cuh"
 
 namespace pkv {
@@ -73,7 +74,34 @@ struct BwdParams {
     const void* o;             // forward output (the dQ kernel computes D = rowsum(dO * O))
     const uint64_t* selmask;   // sparse, or null: [key page][KV head][words] query pages listing the page
     int* err;
+    ModArgs m;                 // modified scores (MOD kernels)
+    int4* bounds;              // MOD: TileRange of each 64-query tile, written by the dQ kernel
 };
+
+// One score of the MOD kernels: raw logit x -> y, the score in log2 units, and
+// its derivative's factor f (1 - tanh^2, or 1). `dist`: key minus query position.
+struct ModScore {
+    float sl2, cap_k, c2, slope2;      // cap_k = scale / cap, 0 without a cap
+    bool big;                          // some |x| cap_k of this tile's elements exceeds 1
+    __device__ __forceinline__ void score(float x, float dist, float& y, float& f) const {
+        if (cap_k > 0.f) {
+            const float u = x * cap_k;
+            const float t = big ? tanh_any(u) : tanh_small(u);
+            y = c2 * t;
+            f = fmaf(-t, t, 1.f);
+        } else {
+            y = x * sl2;
+            f = 1.f;
+        }
+        if (slope2 != 0.f) y = fmaf(-slope2, fabsf(dist), y);
+    }
+};
+template <int N> __device__ __forceinline__ float abs_max(const uint32_t (&r)[N]) {
+    float b = 0.f;
+#pragma unroll
+    for (int c = 0; c < N; ++c) b = fmaxf(b, fabsf(__uint_as_float(r[c])));
+    return b;
+}
 
 // Query pages per chunk the sparse dK/dV kernel lists in shared memory (3
 // bytes each): chunks of up to 262144 tokens at page 128. Longer chunks run
@@ -104,7 +132,11 @@ template <int D> struct KVLayout {
     static constexpr uint32_t kdO = kQ + kv_STAGES * kQStage;
     static constexpr uint32_t kSTAT = kdO + kv_STAGES * kQStage;   // stages x (64 lse*log2e + 64 D) floats
     static constexpr uint32_t kSMEM = kSTAT + kv_STAGES * 512 + 1024;
+    // MOD kernels: and each query's range (64 + 64 ints)
+    static constexpr uint32_t kSMEM_MOD = kSTAT + kv_STAGES * 1024 + 1024;
 };
+// MOD: bit of a listed tile some of whose rows do not see the whole key page.
+constexpr int kTileMasked = 0x4000;
 // Tensor-memory columns: S^T, dP^T (64 fp32 each), P^T, dS^T (64 bf16 = 32
 // each), K (D bf16 = D/2), dK, dV accumulators (D fp32 each).
 constexpr uint32_t kv_TS = 0, kv_TDP = 64, kv_TP = 128, kv_TDS = 160, kv_TK = 192, kv_TDK = 256,
@@ -125,7 +157,9 @@ struct __align__(8) KVBar {
     uint8_t sel_flag[kMaxSelQp];
 };
 
-template <int D>
+// MOD: modified scores (mod.cuh). The page's query tiles are those whose rows'
+// ranges (p.bounds) touch it; dS carries the cap's derivative.
+template <int D, bool MOD>
 __global__ void __launch_bounds__(kThreads, 1)
 bwd_kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_dk,
@@ -162,6 +196,7 @@ bwd_kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const int64_t kfirst = (int64_t)j * 128;
     const int n_qt = (int)((p.n_q + 63) / 64);
     const int i0 = kfirst > p.q_start ? (int)((kfirst - p.q_start) / 64) : 0;
+    constexpr int kStat = MOD ? 256 : 128;           // floats of a stage's statistics
     const int32_t pp = p.bt[j];
     const bool page_ok = pp >= 0 && pp < p.num_phys;
 
@@ -275,10 +310,32 @@ bwd_kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
             if (lane == 0) B.n_i = n - (((n_qt & 1) && B.sel_flag[n_qp - 1]) ? 1 : 0);
         }
+    } else if (MOD) {
+        if (warp == 0) {
+            // Compaction, 32 tiles per ballot.
+            int n = 0;
+            for (int t0 = 0; t0 < n_qt; t0 += 32) {
+                const int t = t0 + lane;
+                const int4 b = t < n_qt ? p.bounds[t] : make_int4(0, 0, 0, 0);
+                const bool f = b.x < (int)kfirst + 128 && b.y > (int)kfirst;
+                const unsigned m = __ballot_sync(0xffffffffu, f);
+                if (f) B.tiles[n + __popc(m & ((1u << lane) - 1u))] = (int16_t)t;
+                n += __popc(m);
+            }
+            if (lane == 0) B.n_i = n;
+        }
     } else if (threadIdx.x == 0) {
         B.n_i = n_qt - i0;
     }
     __syncthreads();
+    if constexpr (MOD) {
+        // Which listed tiles need their elements masked.
+        for (int u = threadIdx.x; u < B.n_i; u += kThreads) {
+            const int4 b = p.bounds[B.tiles[u]];
+            if ((int)kfirst < b.z || (int)kfirst + 128 > b.w) B.tiles[u] |= (int16_t)kTileMasked;
+        }
+        __syncthreads();
+    }
     const uint32_t tmem = B.tmem_base;
     const int n_i = B.n_i;
     // A page no query tile uses needs no valid slot (sparse, staged pools).
@@ -291,6 +348,7 @@ bwd_kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const int T = (int)(((int64_t)t_all * (split + 1)) / n_split) - t_base;
     auto tile_of = [&](int t) -> int {
         const int u = (t_base + t) % n_i;
+        if constexpr (MOD) return (int)B.tiles[u] & (kTileMasked - 1);
         return p.sel ? (int)B.tiles[u] : i0 + u;
     };
     auto head_of = [&](int t) -> int { return kvh * g + (t_base + t) / n_i; };
@@ -303,7 +361,8 @@ bwd_kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         // Per-query statistics of tile t (log2e * LSE, +inf past the chunk, and D),
         // two columns per lane; loaded one tile ahead so their latency overlaps
         // the wait for the next free stage.
-        auto load_stats = [&](int t, float (&s)[4]) {
+        constexpr int NS = MOD ? 8 : 4;
+        auto load_stats = [&](int t, float (&s)[NS]) {
             if (t >= T) return;
             const int h = head_of(t);
             const int i = tile_of(t);
@@ -313,10 +372,16 @@ bwd_kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 const bool v = q < p.n_q;
                 s[e] = v ? __ldg(p.lse + (size_t)h * p.n_q + q) * kLog2e : INFINITY;
                 s[2 + e] = v ? __ldg(p.Dbuf + (size_t)h * p.n_q + q) : 0.f;
+                if constexpr (MOD) {
+                    if (s[e] == -INFINITY) s[e] = INFINITY;    // a row that sees nothing: P = 0
+                    const int2 r = v ? row_range(p.m, p.q_start, q) : make_int2(0, 0);
+                    s[4 + e] = __int_as_float(r.x);
+                    s[6 + e] = __int_as_float(r.y);
+                }
             }
         };
         int issued = 0;
-        auto step = [&](int t, const float (&use)[4], float (&fill)[4]) -> bool {
+        auto step = [&](int t, const float (&use)[NS], float (&fill)[NS]) -> bool {
             const int st = t % kv_STAGES;
             if (t >= kv_STAGES &&
                 !__all_sync(0xffffffffu, tc::mbar_wait(&B.qdo_empty[st], ((t / kv_STAGES) - 1) & 1, p.err)))
@@ -334,16 +399,22 @@ bwd_kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 }
             }
             load_stats(t + 1, fill);
-            float* sst = stat + st * 128;
+            float* sst = stat + st * kStat;
             sst[lane * 2] = use[0];
             sst[lane * 2 + 1] = use[1];
             sst[64 + lane * 2] = use[2];
             sst[64 + lane * 2 + 1] = use[3];
+            if constexpr (MOD) {
+                sst[128 + lane * 2] = use[4];
+                sst[128 + lane * 2 + 1] = use[5];
+                sst[192 + lane * 2] = use[6];
+                sst[192 + lane * 2 + 1] = use[7];
+            }
             tc::mbar_arrive(&B.qdo_full[st]);           // 32 arrivals + the tx bytes
             issued = t + 1;
             return true;
         };
-        float sa[4], sb[4];
+        float sa[NS], sb[NS];
         load_stats(0, sa);
         for (int t = 0; t < T; t += 2) {
             if (!step(t, sa, sb)) break;
@@ -439,6 +510,7 @@ bwd_kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const int64_t kpos = kfirst + r;
         const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
         const float sl2 = rsqrtf((float)D) * kLog2e;
+        const float cap_k = MOD && p.m.cap > 0.f ? rsqrtf((float)D) / p.m.cap : 0.f;
         {
             // K row r, head dims [D/2 wg, D/2 wg + D/2) -> TMEM columns kv_TK + D/4 wg ..
             if constexpr (D == 128) tc::tmem_st32(lane_base + kv_TK + wg * 32, kw);
@@ -457,7 +529,7 @@ bwd_kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             tc::tc_fence_after();
             const int i = tile_of(t);
             const int64_t q0 = p.q_start + (int64_t)i * 64 + wg * 32;   // position of my column 0
-            const float* sst = stat + st * 128 + wg * 32;
+            const float* sst = stat + st * kStat + wg * 32;
             uint32_t sv[32], dv[32];
             tc::tmem_ld32(lane_base + kv_TS + wg * 32, sv);
             tc::tmem_ld32(lane_base + kv_TDP + wg * 32, dv);
@@ -485,7 +557,46 @@ bwd_kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 dw[c / 2] = pack_bf16x2(dr[0], dr[1]);
                 dw[c / 2 + 1] = pack_bf16x2(dr[2], dr[3]);
             };
-            if (kfirst + 127 > q0) {                         // crosses the diagonal: mask
+            if constexpr (MOD) {
+                ModScore ms{sl2, cap_k, p.m.cap * kLog2e, 0.f, false};
+                if (p.m.slopes) ms.slope2 = __ldg(p.m.slopes + head_of(t)) * kLog2e;
+                if (cap_k > 0.f) ms.big = __any_sync(0xffffffffu, abs_max(sv) * cap_k > 1.f);
+                const float dist0 = (float)(kpos - q0);
+                const int4* lo4 = reinterpret_cast<const int4*>(sst + 128);
+                const int4* hi4 = reinterpret_cast<const int4*>(sst + 192);
+                auto mod4 = [&](int c, bool mask) {
+                    const float4 l = l4[c / 4], dd = d4[c / 4];
+                    const float lv[4] = {l.x, l.y, l.z, l.w}, dl[4] = {dd.x, dd.y, dd.z, dd.w};
+                    int lo[4], hi[4];
+                    if (mask) {
+                        const int4 a = lo4[c / 4], b = hi4[c / 4];
+                        lo[0] = a.x; lo[1] = a.y; lo[2] = a.z; lo[3] = a.w;
+                        hi[0] = b.x; hi[1] = b.y; hi[2] = b.z; hi[3] = b.w;
+                    }
+                    float pr[4], dr[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float y, f;
+                        ms.score(__uint_as_float(sv[c + e]), dist0 - (float)(c + e), y, f);
+                        float pv = fast_exp2(y - lv[e]);
+                        float dsv = pv * (__uint_as_float(dv[c + e]) - dl[e]) * f;
+                        if (mask && ((int)kpos < lo[e] || (int)kpos >= hi[e])) pv = dsv = 0.f;
+                        pr[e] = pv;
+                        dr[e] = dsv;
+                    }
+                    pw[c / 2] = pack_bf16x2(pr[0], pr[1]);
+                    pw[c / 2 + 1] = pack_bf16x2(pr[2], pr[3]);
+                    dw[c / 2] = pack_bf16x2(dr[0], dr[1]);
+                    dw[c / 2 + 1] = pack_bf16x2(dr[2], dr[3]);
+                };
+                if ((int)B.tiles[(t_base + t) % n_i] & kTileMasked) {
+#pragma unroll
+                    for (int c = 0; c < 32; c += 4) mod4(c, true);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 32; c += 4) mod4(c, false);
+                }
+            } else if (kfirst + 127 > q0) {                  // crosses the diagonal: mask
 #pragma unroll
                 for (int c = 0; c < 32; c += 4) grad4(c, true);
             } else {
@@ -517,7 +628,7 @@ bwd_kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         uint8_t* stage = smem + kv_Q + wg * (D / 32) * 16 * KB;   // D/32 boxes [128 rows][32 fp32]
         if (ok) {
             tc::tc_fence_after();
-            const bool live = kpos < p.q_start + p.n_q;
+            const bool live = kpos < (MOD ? p.m.n_keys : p.q_start + p.n_q);
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t a[32];
@@ -593,7 +704,7 @@ struct __align__(8) QBar {
     float dpart[2][128];             // the two warpgroups' halves of each row's D
 };
 
-template <int D>
+template <int D, bool MOD>
 __global__ void __launch_bounds__(kThreads, 1)
 bwd_q_tc_kernel(const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, BwdParams p) {
@@ -610,7 +721,23 @@ bwd_q_tc_kernel(const __grid_constant__ CUtensorMap tm_do, const __grid_constant
     const int kvh = h / (p.Hq / p.Hkv);
     // Key tiles = visible pages (dense: pages 0..own; sparse: the listed pages).
     const int32_t* sel_row = p.sel ? p.sel + ((size_t)qt * p.Hkv + kvh) * p.kmax : nullptr;
-    const int T = sel_row ? sel_count_warp(sel_row, p.kmax, lane) : (int)(p.q_start / 128) + qt + 1;
+    // (MOD: the pages the tile's ranges touch.)
+    TileRange tr{};
+    int first = 0;
+    int T;
+    if constexpr (MOD) {
+        tr = tile_range<128>(p.m, p.q_start, (int64_t)qt * 128, p.n_q, lane);
+        first = tr.lo / 128;
+        T = sel_row ? sel_count_warp(sel_row, p.kmax, lane) : tr.hi > 0 ? (tr.hi + 127) / 128 - first : 0;
+        // The bounds of the two 64-query halves, for the dK/dV kernel.
+        const int64_t half = 2 * (int64_t)qt + warp;
+        if (h == 0 && warp < 2 && half * 64 < p.n_q) {
+            const TileRange b = tile_range<64>(p.m, p.q_start, half * 64, p.n_q, lane);
+            if (lane == 0) p.bounds[half] = make_int4(b.lo, b.hi, b.full_lo, b.full_hi);
+        }
+    } else {
+        T = sel_row ? sel_count_warp(sel_row, p.kmax, lane) : (int)(p.q_start / 128) + qt + 1;
+    }
 
     if (threadIdx.x == 0) {
         tc::mbar_init(&B.q_full, 1);
@@ -653,7 +780,7 @@ bwd_q_tc_kernel(const __grid_constant__ CUtensorMap tm_do, const __grid_constant
                 tc::tma_load_3d(smem + q_dO + b * 16 * KB, &tm_do, &B.q_full, 64 * b, h, q_row0);
         }
         tc::PageBatch pages;
-        pages.init(p.bt, sel_row, T, lane);
+        pages.init(p.bt, sel_row, T, lane, first);
         int k_issued = 0, v_issued = 0;
         for (int t = 0; t < T; ++t) {
             const int ks = t % q_KST, vs = t % q_VST;
@@ -771,7 +898,17 @@ bwd_q_tc_kernel(const __grid_constant__ CUtensorMap tm_do, const __grid_constant
         const int64_t q_local = (int64_t)qt * 128 + r;
         const int64_t qpos = p.q_start + q_local;
         const bool valid = q_local < p.n_q;
-        const float lse2 = valid ? p.lse[(size_t)h * p.n_q + q_local] * kLog2e : INFINITY;
+        float lse2 = valid ? p.lse[(size_t)h * p.n_q + q_local] * kLog2e : INFINITY;
+        int2 range = make_int2(0, 0);
+        ModScore ms{};
+        if constexpr (MOD) {
+            if (lse2 == -INFINITY) lse2 = INFINITY;              // the row sees nothing: P = 0
+            if (valid) range = row_range(p.m, p.q_start, q_local);
+            ms.sl2 = rsqrtf((float)D) * kLog2e;
+            ms.cap_k = p.m.cap > 0.f ? rsqrtf((float)D) / p.m.cap : 0.f;
+            ms.c2 = p.m.cap * kLog2e;
+            ms.slope2 = p.m.slopes ? __ldg(p.m.slopes + h) * kLog2e : 0.f;
+        }
         const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
         const float sl2 = rsqrtf((float)D) * kLog2e;
         const int64_t first_diag = p.q_start + (int64_t)qt * 128;   // first key of the own page
@@ -838,7 +975,7 @@ bwd_q_tc_kernel(const __grid_constant__ CUtensorMap tm_do, const __grid_constant
             ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.s_full, t & 1, p.err));
             if (!ok) break;
             tc::tc_fence_after();
-            const int64_t kbase = (int64_t)(sel_row ? sel_row[t] : t) * 128 + wg * 64;
+            const int64_t kbase = (int64_t)(sel_row ? sel_row[t] : first + t) * 128 + wg * 64;
             uint32_t s0[32], s1[32], d0[32], d1[32];
             tc::tmem_ld32(lane_base + q_TS + wg * 64, s0);
             tc::tmem_ld32(lane_base + q_TS + wg * 64 + 32, s1);
@@ -864,7 +1001,33 @@ bwd_q_tc_kernel(const __grid_constant__ CUtensorMap tm_do, const __grid_constant
                     dw[(c0 + c) / 2] = pack_bf16x2(dr[0], dr[1]);
                 }
             };
-            if (kbase + 63 > first_diag) {                   // crosses the diagonal: mask
+            if constexpr (MOD) {
+                if (ms.cap_k > 0.f)
+                    ms.big = __any_sync(0xffffffffu, fmaxf(abs_max(s0), abs_max(s1)) * ms.cap_k > 1.f);
+                const float dist0 = (float)(kbase - qpos);
+                const int lo = range.x - (int)kbase, hi = range.y - (int)kbase;
+                auto mod_half = [&](const uint32_t (&sv)[32], const uint32_t (&dv)[32], int c0, bool mask) {
+#pragma unroll
+                    for (int c = 0; c < 32; c += 2) {
+                        float dr[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float y, f;
+                            ms.score(__uint_as_float(sv[c + e]), dist0 + (float)(c0 + c + e), y, f);
+                            dr[e] = fast_exp2(y - lse2) * (__uint_as_float(dv[c + e]) - Dr) * f;
+                            if (mask && (c0 + c + e < lo || c0 + c + e >= hi)) dr[e] = 0.f;
+                        }
+                        dw[(c0 + c) / 2] = pack_bf16x2(dr[0], dr[1]);
+                    }
+                };
+                if ((int)kbase < tr.full_lo || (int)kbase + 64 > tr.full_hi) {
+                    mod_half(s0, d0, 0, true);
+                    mod_half(s1, d1, 32, true);
+                } else {
+                    mod_half(s0, d0, 0, false);
+                    mod_half(s1, d1, 32, false);
+                }
+            } else if (kbase + 63 > first_diag) {            // crosses the diagonal: mask
                 grad_half(s0, d0, 0, true);
                 grad_half(s1, d1, 32, true);
             } else {
@@ -881,6 +1044,11 @@ bwd_q_tc_kernel(const __grid_constant__ CUtensorMap tm_do, const __grid_constant
             tc::mbar_arrive(&B.ds_full);
         }
         if (ok && T > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.acc_done, 0, p.err));
+        if (MOD && ok && T == 0 && valid) {                  // no row of the tile sees a key
+            uint4* row = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dq) + ((size_t)q_local * p.Hq + h) * D);
+#pragma unroll
+            for (int v = 0; v < D / 16; ++v) row[wg * (D / 16) + v] = make_uint4(0, 0, 0, 0);
+        }
         if (ok && T > 0) {
             tc::tc_fence_after();
             const float scale = rsqrtf((float)D);
@@ -988,7 +1156,7 @@ __global__ void __launch_bounds__(kUnionThreads) sel_union_kernel(const int32_t*
         for (int64_t i = tid; i < n_words; i += kUnionThreads) masks[i] = mk[i];
 }
 
-template <int D>
+template <int D, bool MOD>
 static cudaError_t launch_bwd(const AttnArgs& a, cudaStream_t s) {
     CUtensorMap tq64, tdo64, tdo128;
     std::string why;
@@ -997,12 +1165,13 @@ static cudaError_t launch_bwd(const AttnArgs& a, cudaStream_t s) {
         !make_tmap_3d(&tdo64, a.dout, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, D, a.Hq, a.n_q, s1, s2, 64, 1, 64, &why) ||
         !make_tmap_3d(&tdo128, a.dout, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, D, a.Hq, a.n_q, s1, s2, 64, 1, 128, &why))
         return cudaErrorInvalidValue;
+    constexpr uint32_t kv_smem = MOD ? KVLayout<D>::kSMEM_MOD : KVLayout<D>::kSMEM;
     static bool attr = false;
     if (!attr) {
-        cudaError_t e = cudaFuncSetAttribute(bwd_kv_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)KVLayout<D>::kSMEM);
+        cudaError_t e = cudaFuncSetAttribute(bwd_kv_tc_kernel<D, MOD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)kv_smem);
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(bwd_q_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            e = cudaFuncSetAttribute(bwd_q_tc_kernel<D, MOD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      (int)QLayout<D>::kSMEM);
         if (e != cudaSuccess) return e;
         attr = true;
@@ -1012,16 +1181,17 @@ static cudaError_t launch_bwd(const AttnArgs& a, cudaStream_t s) {
     p.lse = a.lse_in; p.Dbuf = a.Dbuf; p.dq = a.dq; p.dkpool = a.dkpool; p.dvpool = a.dvpool;
     p.o = a.o_in;
     p.bt = a.bt; p.num_phys = a.num_phys; p.err = a.err;
-    p.sel = a.sel; p.kmax = a.kmax;
+    p.sel = a.sel; p.kmax = a.kmax; p.m = a.m; p.bounds = a.bounds;
     // The dQ kernel first: it computes D = rowsum(dO * O), which the dK/dV kernel reads.
     {
         dim3 g_q((unsigned)((a.n_q + 127) / 128), a.Hq);
-        ProfScope ps("bwd_q_tc_kernel", s);
-        bwd_q_tc_kernel<D><<<g_q, kThreads, QLayout<D>::kSMEM, s>>>(tdo128, *a.tmap_k, *a.tmap_v, p);
+        ProfScope ps(MOD ? "bwd_q_mod_tc_kernel" : "bwd_q_tc_kernel", s);
+        bwd_q_tc_kernel<D, MOD><<<g_q, kThreads, QLayout<D>::kSMEM, s>>>(tdo128, *a.tmap_k, *a.tmap_v, p);
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    const int64_t n_keys = a.q_start + a.n_q;
+    // (With a selection no key past the chunk is listed.)
+    const int64_t n_keys = MOD && !a.sel ? a.m.n_keys : a.q_start + a.n_q;
     const int64_t n_key_pages = (n_keys + 127) / 128;
     // Key pages the dK/dV grid covers: every page (dense), or at most the
     // selection union's upper bound (its CTAs beyond the union's size exit).
@@ -1074,8 +1244,8 @@ static cudaError_t launch_bwd(const AttnArgs& a, cudaStream_t s) {
     const dim3 g_kv = use_list ? dim3(a.Hkv, (unsigned)grid_pages)
                                : dim3((unsigned)(grid_pages * splits), a.Hkv);
     {
-        ProfScope ps("bwd_kv_tc_kernel", s);
-        bwd_kv_tc_kernel<D><<<g_kv, kThreads, KVLayout<D>::kSMEM, s>>>(tq64, tdo64, *a.tmap_v, *a.tmap_dk,
+        ProfScope ps(MOD ? "bwd_kv_mod_tc_kernel" : "bwd_kv_tc_kernel", s);
+        bwd_kv_tc_kernel<D, MOD><<<g_kv, kThreads, kv_smem, s>>>(tq64, tdo64, *a.tmap_v, *a.tmap_dk,
                                                                        *a.tmap_dv, p);
     }
     return cudaGetLastError();
@@ -1098,14 +1268,16 @@ int64_t bwd_selmask_words(const AttnArgs& a) {
 }
 
 cudaError_t launch_attn_bwd_tc(const AttnArgs& a, cudaStream_t s) {
-    // The sparse dK/dV kernel lists the selecting query pages in shared memory.
-    if (a.sel && (a.n_q + 127) / 128 > kMaxSelQp) {
+    // The sparse dK/dV kernel lists the selecting query pages in shared memory,
+    // that of modified scores the query tiles.
+    if ((a.sel || a.mod) && (a.n_q + 127) / 128 > kMaxSelQp) {
         const cudaError_t e = launch_bwd_rowdot(a, s);
-        return e != cudaSuccess ? e : launch_attn_bwd_simt(a, s);
+        return e != cudaSuccess ? e : a.mod ? launch_attn_bwd_mod_simt(a, s) : launch_attn_bwd_simt(a, s);
     }
     if ((reinterpret_cast<uintptr_t>(a.dout) & 15) || !a.tmap_k || (a.sel && !a.pagelist))
         return cudaErrorInvalidValue;
-    return a.d == 64 ? launch_bwd<64>(a, s) : launch_bwd<128>(a, s);
+    if (a.mod) return a.d == 64 ? launch_bwd<64, true>(a, s) : launch_bwd<128, true>(a, s);
+    return a.d == 64 ? launch_bwd<64, false>(a, s) : launch_bwd<128, false>(a, s);
 }
 
 }  // namespace pkv

@@ -37,8 +37,11 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
+#include "mod.cuh"
 #include "tc.cuh"
 
 namespace pkv {
@@ -80,6 +83,8 @@ struct FwdParams {
     const int32_t* sel;
     int kmax;
     int* err;
+    ModArgs m;                       // modified scores (MOD kernels)
+    float* part;                     // MOD, split: partial results (attn_part_floats), else null
 };
 
 struct __align__(8) FwdBarriers {
@@ -94,6 +99,7 @@ struct __align__(8) FwdBarriers {
     uint32_t tmem_base;
     int n_tiles;
     float red[2][2][kTile];          // [parity][warpgroup][row]
+    float lsum[2][kTile];            // MOD: [warpgroup][row] sums of the unrounded weights
 };
 
 
@@ -108,8 +114,8 @@ using tc::drain_wait;
 // the copies. A K load never waits behind a V stage in use.
 template <int D>
 __device__ __forceinline__ void produce_ring(const FwdParams& p, uint8_t* smem, FwdBarriers& B,
-                                             const CUtensorMap& tmap, bool is_k, int qt, int kvh,
-                                             int nt, int lane, tc::PageBatch& pages) {
+                                             const CUtensorMap& tmap, bool is_k, int kvh, const int32_t* sel_row,
+                                             int first, int nt, int lane, tc::PageBatch& pages) {
     using L = FwdLayout<D>;
     const int nst = is_k ? kKStages : kVStages;
     uint64_t* full = is_k ? B.k_full : B.v_full;
@@ -121,7 +127,7 @@ __device__ __forceinline__ void produce_ring(const FwdParams& p, uint8_t* smem, 
     int issued = 0;
     bool ok = true;
     for (int hi = 0; ok && hi < p.heads_per_cta; ++hi) {
-        if (hi > 0) pages.init(p.bt, p.sel ? p.sel + ((size_t)qt * p.Hkv + kvh) * p.kmax : nullptr, nt, lane);
+        if (hi > 0) pages.init(p.bt, sel_row, nt, lane, first);
         for (int j = 0; j < nt; ++j) {
             const int it = hi * nt + j;
             const int st = it % nst;
@@ -152,7 +158,13 @@ __device__ __forceinline__ void produce_ring(const FwdParams& p, uint8_t* smem, 
         for (int j = max(0, issued - nst); j < issued; ++j) drain_wait(&full[j % nst], (j / nst) & 1);
 }
 
-template <int D>
+// MOD: modified scores (a cap, a distance bias, a key range per query, see
+// mod.cuh). The tile's pages are those its rows' ranges touch, each element is
+// masked by its own row's range where a tile is not wholly inside all of them,
+// gridDim.z CTAs may share a tile's pages (partial results joined afterwards),
+// and the LSE comes from an fp32 sum of the unrounded weights, exact enough to
+// recompute P from (the plain kernel takes the bf16-weight sum O is divided by).
+template <int D, bool MOD>
 __global__ void __launch_bounds__(kThreads, 1)
 fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
               FwdParams p) {
@@ -186,7 +198,19 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
     const int32_t* sel_row = p.sel ? p.sel + ((size_t)qt * p.Hkv + kvh) * p.kmax : nullptr;
     tc::PageBatch pages;
     int n_pre = 0;
-    if (warp == 0 || warp == kThreads / 32 - 1) {
+    TileRange tr{};
+    int first = 0;                                       // MOD: logical page of tile 0 (dense)
+    if constexpr (MOD) {
+        tr = tile_range<kTile>(p.m, p.q_start, (int64_t)qt * kTile, p.n_q, lane);
+        const int p0 = tr.lo / kTile;
+        int n = sel_row ? sel_count_warp(sel_row, p.kmax, lane) : tr.hi > 0 ? (tr.hi + kTile - 1) / kTile - p0 : 0;
+        // This CTA's share of the tile's pages.
+        const int s0 = (int)((int64_t)n * blockIdx.z / gridDim.z), s1 = (int)((int64_t)n * (blockIdx.z + 1) / gridDim.z);
+        n_pre = s1 - s0;
+        first = p0 + s0;
+        if (sel_row) sel_row += s0;
+        if (warp == 0 || warp == kThreads / 32 - 1) pages.init(p.bt, sel_row, n_pre, lane, first);
+    } else if (warp == 0 || warp == kThreads / 32 - 1) {
         n_pre = sel_row ? sel_count_warp(sel_row, p.kmax, lane) : (int)(p.q_start / kTile) + qt + 1;
         pages.init(p.bt, sel_row, n_pre, lane);
     }
@@ -243,10 +267,10 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
 
     if (warp == 0) {
         // ------------------------------------------------------------ K producer
-        produce_ring<D>(p, smem, B, tmap_k, true, qt, kvh, nt, lane, pages);
+        produce_ring<D>(p, smem, B, tmap_k, true, kvh, sel_row, first, nt, lane, pages);
     } else if (warp == kThreads / 32 - 1) {
         // ------------------------------------------------------------ V producer
-        produce_ring<D>(p, smem, B, tmap_v, false, qt, kvh, nt, lane, pages);
+        produce_ring<D>(p, smem, B, tmap_v, false, kvh, sel_row, first, nt, lane, pages);
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         // The whole warp runs the loop (warp-uniform descriptors); one elected
@@ -323,9 +347,16 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
         const int quad = warp & 3;                    // TMEM lane quadrant of this warp
         const int row = quad * 32 + lane;             // query row within the tile
         const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
+        // Scores x leave the tile loop's head in units of 1 / ms log2: raw logits
+        // times sl2, or (MOD) already scaled by the cap or the bias.
         const float sl2 = rsqrtf((float)D) * kLog2e;
         const int64_t q_local = (int64_t)qt * kTile + row;
         const bool valid = q_local < p.n_q;
+        int2 range = make_int2(0, 0);
+        if constexpr (MOD) {
+            if (valid) range = row_range(p.m, p.q_start, q_local);
+        }
+        const float ms = MOD && (p.m.cap > 0.f || p.m.slopes) ? 1.f : sl2;
         bool ok = true;
         // Named barrier of the two warps (one per warpgroup) that own rows 32 quad ..
         const uint32_t pair_bar = 1 + quad;
@@ -341,7 +372,8 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
             tc::tc_fence_before();
         }
         tc::mbar_arrive(&B.q_full);
-        float m = -INFINITY;
+        float m = -INFINITY, lsum = 0.f;
+        const float slope2 = MOD && p.m.slopes ? p.m.slopes[h] * kLog2e : 0.f;
         for (int j = 0; j < nt; ++j) {
             const int it = hi * nt + j;
             const int st = it & 1;
@@ -363,7 +395,34 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
                     x[32 + e] = __uint_as_float(r1[e]);
                 }
             }
-            if (j == nt - 1) {                        // own page: causal mask (key col > row)
+            if constexpr (MOD) {
+                const int kb = (sel_row ? sel_row[j] : first + j) * kTile + wg * 64;   // my first key
+                if (p.m.cap > 0.f) {
+                    const float k = rsqrtf((float)D) / p.m.cap, c2 = p.m.cap * kLog2e;
+                    float big = 0.f;
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) big = fmaxf(big, fabsf(x[c]));
+                    if (__any_sync(0xffffffffu, big * k > 1.f)) {
+#pragma unroll
+                        for (int c = 0; c < 64; ++c) x[c] = c2 * tanh_any(x[c] * k);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 64; ++c) x[c] = c2 * tanh_small(x[c] * k);
+                    }
+                }
+                if (p.m.slopes) {
+                    const float pre = p.m.cap > 0.f ? 1.f : sl2;
+                    const float off = (float)(kb - (int)(p.q_start + q_local));
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) x[c] = fmaf(-slope2, fabsf(off + (float)c), x[c] * pre);
+                }
+                if (kb < tr.full_lo || kb + 63 >= tr.full_hi) {
+                    const int lo = range.x - kb, hi_ = range.y - kb;
+#pragma unroll
+                    for (int c = 0; c < 64; ++c)
+                        if (c < lo || c >= hi_) x[c] = -INFINITY;
+                }
+            } else if (j == nt - 1) {                 // own page: causal mask (key col > row)
 #pragma unroll
                 for (int c = 0; c < 64; ++c)
                     if (wg * 64 + c > row) x[c] = -INFINITY;
@@ -384,7 +443,7 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
             B.red[st][wg][row] = part;
             asm volatile("bar.sync %0, 64;" :: "r"(pair_bar) : "memory");
             if (!ok) continue;                        // keep meeting the partner warp
-            const float mx = fmaxf(part, B.red[st][wg ^ 1][row]) * sl2;   // scaled, log2 units
+            const float mx = fmaxf(part, B.red[st][wg ^ 1][row]) * ms;   // scaled, log2 units
             float alpha = 1.f;
             bool rescale = false;
             if (mx > m + kRescaleThreshold) {
@@ -393,13 +452,21 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
                 rescale = true;
             }
             uint32_t pk[32];
-            const float neg_m = -m;
+            // (MOD: a row that has seen nothing yet keeps m = -inf; its weights are 0.)
+            const float neg_m = MOD && m == -INFINITY ? 0.f : -m;
+            if constexpr (MOD) lsum *= alpha;
+            float ls[2] = {0.f, 0.f};
 #pragma unroll
             for (int c = 0; c < 32; ++c) {
-                const float p0 = fast_exp2(fmaf(x[2 * c], sl2, neg_m));
-                const float p1 = fast_exp2(fmaf(x[2 * c + 1], sl2, neg_m));
+                const float p0 = fast_exp2(fmaf(x[2 * c], ms, neg_m));
+                const float p1 = fast_exp2(fmaf(x[2 * c + 1], ms, neg_m));
+                if constexpr (MOD) {
+                    ls[0] += p0;
+                    ls[1] += p1;
+                }
                 pk[c] = pack_bf16x2(p0, p1);
             }
+            if constexpr (MOD) lsum += ls[0] + ls[1];
             if (j > 0 && __any_sync(0xffffffffu, rescale)) {
                 // PV_{j-1} must be done before O is touched (PV_j waits for this tile's P).
                 ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.o_done, (it - 1) & 1, p.err));
@@ -431,7 +498,56 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
         // found; issued here, repeated calls are bit-identical.)
         if (hi + 1 < nh) load_q(h + 1);
         if (ok && nt > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.o_done, (hi * nt + nt - 1) & 1, p.err));
-        if (ok && nt > 0) {
+        if constexpr (MOD) {
+            // Row statistics of both warpgroups meet (every warp passes, error or not).
+            B.lsum[wg][row] = lsum;
+            asm volatile("bar.sync %0, 64;" :: "r"(pair_bar) : "memory");
+            lsum += B.lsum[wg ^ 1][row];
+        }
+        if (MOD && ok) {
+            float l = 0.f;
+            if (nt > 0) {
+                tc::tc_fence_after();
+                l = __uint_as_float(tc::tmem_ld1(lane_base + kColL));
+            }
+            const float inv = l == 0.f ? 0.f : 1.f / l;      // a row that saw nothing: O = 0
+            const float lse2 = lsum == 0.f ? -INFINITY : m + log2f(lsum);
+            const size_t hrow = (size_t)h * p.n_q + q_local;
+            const size_t prow = (size_t)blockIdx.z * p.Hq * p.n_q + hrow;
+#pragma unroll
+            for (int c = (D / 64) * wg; c < (D / 64) * (wg + 1); ++c) {
+                uint32_t r[32];
+                if (nt > 0) {
+                    tc::tmem_ld32(lane_base + kColO + c * 32, r);
+                    tc::tmem_wait_ld(r);
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    r[e] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(r[e]) * inv);
+                if (!valid) continue;
+                if (p.part) {
+                    float4* dst = reinterpret_cast<float4*>(p.part + prow * D + c * 32);
+#pragma unroll
+                    for (int v = 0; v < 8; ++v)
+                        dst[v] = make_float4(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]),
+                                             __uint_as_float(r[4 * v + 2]), __uint_as_float(r[4 * v + 3]));
+                } else {
+                    __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.o) + ((size_t)q_local * p.Hq + h) * D;
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        *reinterpret_cast<uint4*>(orow + c * 32 + v * 8) = make_uint4(
+                            pack_bf16x2(__uint_as_float(r[8 * v]), __uint_as_float(r[8 * v + 1])),
+                            pack_bf16x2(__uint_as_float(r[8 * v + 2]), __uint_as_float(r[8 * v + 3])),
+                            pack_bf16x2(__uint_as_float(r[8 * v + 4]), __uint_as_float(r[8 * v + 5])),
+                            pack_bf16x2(__uint_as_float(r[8 * v + 6]), __uint_as_float(r[8 * v + 7])));
+                }
+            }
+            if (valid && wg == 0) {
+                if (p.part) p.part[(size_t)gridDim.z * p.Hq * p.n_q * D + prow] = lse2;
+                else p.lse[hrow] = lse2 * kLn2;
+            }
+        }
+        if (!MOD && ok && nt > 0) {
             tc::tc_fence_after();
             // Normalise by the sum of the bf16 weights the tensor core multiplied, so
             // O is a convex combination of values whatever the rounding of P.
@@ -477,12 +593,12 @@ bool tc_supported(const AttnArgs& a) {
            a.tmap_v && (reinterpret_cast<uintptr_t>(a.q) & 15) == 0;
 }
 
-template <int D>
+template <int D, bool MOD>
 static cudaError_t launch_fwd(const AttnArgs& a, cudaStream_t s) {
     constexpr uint32_t smem = FwdLayout<D>::kSmemBytes;
     static bool attr_set = false;
     if (!attr_set) {
-        cudaError_t e = cudaFuncSetAttribute(fwd_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(fwd_tc_kernel<D, MOD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)smem);
         if (e != cudaSuccess) return e;
         attr_set = true;
@@ -490,19 +606,34 @@ static cudaError_t launch_fwd(const AttnArgs& a, cudaStream_t s) {
     FwdParams p{};
     p.Hq = a.Hq; p.Hkv = a.Hkv; p.q_start = a.q_start; p.n_q = a.n_q;
     p.q = a.q; p.o = a.o; p.lse = a.lse; p.bt = a.bt; p.num_phys = a.num_phys;
-    p.sel = a.sel; p.kmax = a.kmax; p.err = a.err;
+    p.sel = a.sel; p.kmax = a.kmax; p.err = a.err; p.m = a.m;
+    const int splits = MOD ? a.splits : 1;
+    p.part = splits > 1 ? a.part : nullptr;
     // Short page lists (local layers): one CTA takes every query head of a KV
     // group, so its start-up (tensor memory, barriers, pipeline fill) is paid
     // once for the group's g heads instead of once per head.
     p.heads_per_cta = (a.sel && a.kmax <= kShortList) ? a.Hq / a.Hkv : 1;
-    dim3 grid((unsigned)((a.n_q + kTile - 1) / kTile), a.Hq / p.heads_per_cta);
-    ProfScope ps("fwd_tc_kernel", s);
-    fwd_tc_kernel<D><<<grid, kThreads, smem, s>>>(*a.tmap_k, *a.tmap_v, p);
+    dim3 grid((unsigned)((a.n_q + kTile - 1) / kTile), a.Hq / p.heads_per_cta, splits);
+    ProfScope ps(MOD ? "fwd_mod_tc_kernel" : "fwd_tc_kernel", s);
+    fwd_tc_kernel<D, MOD><<<grid, kThreads, smem, s>>>(*a.tmap_k, *a.tmap_v, p);
     return cudaGetLastError();
 }
 
 cudaError_t launch_attn_fwd_tc(const AttnArgs& a, cudaStream_t s) {
-    return a.d == 64 ? launch_fwd<64>(a, s) : launch_fwd<128>(a, s);
+    if (a.mod) return a.d == 64 ? launch_fwd<64, true>(a, s) : launch_fwd<128, true>(a, s);
+    return a.d == 64 ? launch_fwd<64, false>(a, s) : launch_fwd<128, false>(a, s);
+}
+
+// Few query tiles against a long cache leave most SMs idle: split the keys so
+// that about two CTAs per SM run, each with at least 4 pages of its own.
+int attn_fwd_tc_splits(const AttnArgs& a) {
+    if (a.sel) return 1;
+    int dev = 0, sms = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const int64_t ctas = (a.n_q + kTile - 1) / kTile * a.Hq, pages = (a.m.n_keys + kTile - 1) / kTile;
+    if (ctas >= sms) return 1;
+    return (int)std::max<int64_t>(1, std::min<int64_t>({pages / 4, 2 * (int64_t)sms / ctas, 64}));
 }
 
 }  // namespace pkv

@@ -66,6 +66,11 @@ struct pkv_seq {
     cudaEvent_t bt_sent = nullptr;
     bool bt_pending = false;
     int64_t len = 0;
+    // Scratch of the calls with modified scores, grown on demand; outgrown
+    // buffers stay until the sequence is freed (a captured graph may use them).
+    float* scratch = nullptr;
+    size_t scratch_floats = 0;
+    std::vector<float*> retired;
     // PINNED_HOST pools: the slot cache (device), capacity num_phys_pages.
     int32_t* d_slot_of = nullptr;    // logical page -> device slot, or -1
     int32_t* d_slot_page = nullptr;  // device slot -> logical page or -1 [n_slots]
@@ -118,6 +123,7 @@ template <typename F> pkv_status guarded(const char* who, F&& body) noexcept {
     }
 }
 
+bool capturing(cudaStream_t s);                      // the stream is being captured into a graph
 bool is_device(const pkv_pool* p);                   // the pool has page memory (not META)
 // PKV_ERR_INVALID unless the current CUDA device is the pool's.
 pkv_status check_stream_device(const pkv_pool* p);
@@ -157,6 +163,15 @@ cudaError_t launch_grad_accumulate(const pkv_pool* pool, const int32_t* d_bt, in
 cudaError_t launch_gather(const pkv_pool* pool, const int32_t* d_bt, int64_t lp0, int64_t len,
                           void* k, void* v, float* dk, float* dv, float* rep, cudaStream_t s);
 
+// Modified scores (see mod.cuh), as the kernels take them.
+struct ModArgs {
+    const int64_t* k_begin;          // [n_q] or null (0): first visible key of each query
+    const int64_t* k_end;            // [n_q] or null (own position + 1): one past the last
+    const float* slopes;             // [Hq] or null: s -= slope |i - j|, after the cap
+    float cap;                       // c > 0, or 0: no cap
+    int64_t n_keys;                  // keys a call may see: the sequence's length, or q_start + n_q without k_end
+};
+
 struct AttnArgs {
     int P, Hq, Hkv, d, dtype;
     int64_t q_start, n_q;            // keys 0 .. q_start + n_q - 1
@@ -183,20 +198,39 @@ struct AttnArgs {
     const CUtensorMap* tmap_v;
     const CUtensorMap* tmap_dk;      // tensor-core path only: fp32 gradient rows,
     const CUtensorMap* tmap_dv;      // boxes of 32 columns x 128 rows (reduce-add)
+    // Modified scores (pkv_chunk_attn_mod_*); the plain calls leave these unset.
+    bool mod;
+    ModArgs m;
+    int splits;                      // forward: CTAs over one tile's keys
+    float* part;                     // forward scratch with splits > 1: [attn_part_floats(a)]
+    int4* bounds;                    // bwd scratch: TileRange of each 64-query tile
 };
+// Floats of the split forward's partial results: O [splits, Hq, n_q, d], then
+// LSE (log2 units) [splits, Hq, n_q].
+inline size_t attn_part_floats(const AttnArgs& a) {
+    return a.splits > 1 ? (size_t)a.splits * a.Hq * a.n_q * (a.d + 1) : 0;
+}
+// CTAs over one tile's keys that the tensor-core forward wants for a.
+int attn_fwd_tc_splits(const AttnArgs& a);
+// Joins the partial results of a split forward into a.o and a.lse.
+cudaError_t launch_attn_join(const AttnArgs& a, cudaStream_t s);
 
 // Validates the arguments shared by the attention entry points and fills a
 // with the sequence's pools, block table (or slot table for PINNED_HOST pools),
-// tensor maps and selection. Host-only; returns PKV_OK or an error with the
+// tensor maps and selection (any_start: q_start need not begin a page). Host-only; returns PKV_OK or an error with the
 // last-error message set, naming `who`.
 pkv_status attn_common(pkv_seq* s, const void* q, int64_t q_start, int64_t n_q,
-                       const pkv_sel* sel, AttnArgs* a, const char* who);
+                       const pkv_sel* sel, AttnArgs* a, const char* who, bool any_start = false);
 // True when the tensor-core kernels take this call.
 bool use_tc(const pkv_pool* p, const AttnArgs& a);
 
 cudaError_t launch_attn_fwd_simt(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_attn_bwd_simt(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_bwd_rowdot(const AttnArgs& a, cudaStream_t s);
+// The same with modified scores; the backward wants D from launch_bwd_rowdot.
+int attn_fwd_mod_simt_splits(const AttnArgs& a);
+cudaError_t launch_attn_fwd_mod_simt(const AttnArgs& a, cudaStream_t s);
+cudaError_t launch_attn_bwd_mod_simt(const AttnArgs& a, cudaStream_t s);
 
 // Page selection of one chunk in one launch (topk_fused_kernel). scratch:
 // page_topk_scratch_floats() floats; state: page_topk_state_ints(Hkv) ints,

@@ -487,11 +487,6 @@ pkv_status rows_check(const pkv_pool* p, const void* x, int H, int64_t* stride, 
     return PKV_OK;
 }
 
-bool capturing(cudaStream_t s) {
-    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
-    return cudaStreamIsCapturing(s, &st) == cudaSuccess && st != cudaStreamCaptureStatusNone;
-}
-
 }  // namespace
 }  // namespace pkv
 

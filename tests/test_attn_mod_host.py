@@ -1,0 +1,63 @@
+"""Argument refusals of the attention with modified scores, on a pool without
+page memory: nothing here reaches a GPU."""
+import ctypes
+
+import pytest
+import torch
+
+from paged_kv_chunk_chunked_gb300 import binding as B
+from paged_kv_chunk_chunked_gb300 import build as pkv_build
+
+
+@pytest.fixture(scope="module")
+def seq():
+    pkv_build.build()
+    pool = B.pkv_pool_create(16, 2, 4, 64, B.PKV_BF16, 8, residency=B.PKV_RES_META)
+    yield B.pkv_seq_create(pool)
+    B.pkv_pool_destroy(pool)
+
+
+def _both(seq, mod, q=64, q_start=0, n=0, sel=None):
+    l, m = B.lib(), None if mod is None else ctypes.byref(mod)
+    a = l.pkv_chunk_attn_mod_fwd(seq, q, q_start, n, 64, 64, m, sel, None)
+    why = B.pkv_last_error()
+    b = l.pkv_chunk_attn_mod_bwd(seq, q, 64, 64, 64, q_start, n, 64, m, sel, None)
+    assert a == b and why.split(": ", 1)[1] == B.pkv_last_error().split(": ", 1)[1]
+    return a, why
+
+
+@pytest.mark.parametrize("kw,why", [
+    (dict(softcap=-1.0), "softcap"), (dict(softcap=float("nan")), "softcap"), (dict(softcap=float("inf")), "softcap"),
+    (dict(softcap=1e-4), "softcap"), (dict(softcap=1e7), "softcap"), (dict(slopes=66), "misaligned"),
+    (dict(k_begin=68), "misaligned"), (dict(k_end=68), "misaligned"),
+])
+def test_bad_modification(seq, kw, why):
+    m = B.score_mod()
+    for k, v in kw.items():
+        setattr(m, k, v)
+    st, msg = _both(seq, m)
+    assert st == B.PKV_ERR_INVALID and why in msg
+
+
+def test_bad_calls(seq):
+    m = B.score_mod(30.0)
+    assert _both(seq, None)[0] == B.PKV_ERR_INVALID
+    assert _both(None, m)[0] == B.PKV_ERR_INVALID
+    for q_start, n in ((-1, 0), (0, -1), (0, 1), (1, 0), (1 << 62, 1 << 62)):
+        assert _both(seq, m, q_start=q_start, n=n)[0] == B.PKV_ERR_INVALID, (q_start, n)
+    assert _both(seq, m)[0] == B.PKV_OK                     # an empty chunk is no error
+
+
+def test_binding_checks_the_arrays(seq):
+    with pytest.raises(ValueError):
+        B.score_mod(slopes=torch.zeros(4, dtype=torch.float64))
+    with pytest.raises(ValueError):
+        B.score_mod(k_begin=torch.zeros(4, dtype=torch.int32))
+    with pytest.raises(ValueError):
+        B.score_mod(k_end=torch.zeros(8, dtype=torch.int64)[::2])
+    q = torch.zeros(4, 4, 64, dtype=torch.bfloat16)
+    for m in (B.score_mod(k_begin=torch.zeros(3, dtype=torch.int64)), B.score_mod(slopes=torch.zeros(5))):
+        with pytest.raises(ValueError):
+            B.pkv_chunk_attn_mod_fwd(seq, q, 0, 4, q, q, m)
+        with pytest.raises(ValueError):
+            B.pkv_chunk_attn_mod_bwd(seq, q, q, q, q, 0, 4, q, m)
