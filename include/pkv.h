@@ -282,7 +282,7 @@ pkv_status pkv_chunk_attn_bwd(pkv_seq* seq, const void* q, const void* o, const 
  * A hidden key or query is hidden by a zero weight: K, V of the pages a call
  * reads and Q, O, dO of its rows must be finite there too (0 * inf is NaN). */
 typedef struct pkv_score_mod {
-    float softcap;             /* 0: none; else in [1e-3, 1e6]                            */
+    float softcap;             /* 0: none; else in [1e-3, 1e4]                            */
     int32_t reserved;
     const float* slopes;       /* device float32 [Hq] or NULL                             */
     const int64_t* k_begin;    /* device int64 [n_q] or NULL                              */

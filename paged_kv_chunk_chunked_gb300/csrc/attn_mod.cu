@@ -7,6 +7,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "mod.cuh"
 
 namespace pkv {
 namespace {
@@ -19,8 +20,8 @@ pkv_status mod_common(pkv_seq* s, const void* q, int64_t q_start, int64_t n_q, c
     const std::string w(who);
     if (!s) return fail(PKV_ERR_INVALID, w + ": seq is NULL");
     if (!mod) return fail(PKV_ERR_INVALID, w + ": mod is NULL");
-    if (!(mod->softcap == 0.f || (mod->softcap >= 1e-3f && mod->softcap <= 1e6f)))
-        return fail(PKV_ERR_INVALID, w + ": softcap must be 0 (none) or in [1e-3, 1e6]");
+    if (!(mod->softcap == 0.f || (mod->softcap >= 1e-3f && mod->softcap <= 1e4f)))
+        return fail(PKV_ERR_INVALID, w + ": softcap must be 0 (none) or in [1e-3, 1e4]");
     if (misaligned(mod->slopes, 4) || misaligned(mod->k_begin, 8) || misaligned(mod->k_end, 8))
         return fail(PKV_ERR_INVALID, w + ": slopes, k_begin or k_end is misaligned");
     if (q_start < 0 || n_q < 0 || q_start > s->len || n_q > s->len - q_start)
@@ -36,7 +37,7 @@ pkv_status mod_common(pkv_seq* s, const void* q, int64_t q_start, int64_t n_q, c
     a->m.k_begin = mod->k_begin;
     a->m.k_end = mod->k_end;
     a->m.slopes = mod->slopes;
-    a->m.cap = mod->softcap;
+    set_cap(&a->m, mod->softcap, s->pool->desc.head_dim);
     a->m.n_keys = mod->k_end ? s->len : q_start + n_q;
     a->splits = 1;
     return PKV_OK;

@@ -78,29 +78,18 @@ struct BwdParams {
     int4* bounds;              // MOD: TileRange of each 64-query tile, written by the dQ kernel
 };
 
-// One score of the MOD kernels: raw logit x -> y, the score in log2 units, and
-// its derivative's factor f (1 - tanh^2, or 1). `dist`: key minus query position.
-struct ModScore {
-    float sl2, cap_k, c2, slope2;      // cap_k = scale / cap, 0 without a cap
-    bool big;                          // some |x| cap_k of this tile's elements exceeds 1
-    __device__ __forceinline__ void score(float x, float dist, float& y, float& f) const {
-        if (cap_k > 0.f) {
-            const float u = x * cap_k;
-            const float t = big ? tanh_any(u) : tanh_small(u);
-            y = c2 * t;
-            f = fmaf(-t, t, 1.f);
-        } else {
-            y = x * sl2;
-            f = 1.f;
-        }
-        if (slope2 != 0.f) y = fmaf(-slope2, fabsf(dist), y);
-    }
-};
-template <int N> __device__ __forceinline__ float abs_max(const uint32_t (&r)[N]) {
-    float b = 0.f;
-#pragma unroll
-    for (int c = 0; c < N; ++c) b = fmaxf(b, fabsf(__uint_as_float(r[c])));
-    return b;
+// The MOD kernels' cap over a row of a tile, in place: raw logits x -> scores in
+// log2 units; g, the gradient factor dP - D, takes the derivative
+// 1 - tanh^2 = 1 - (y / c2)^2.
+template <int N>
+__device__ __forceinline__ void cap_grad(uint32_t (&x)[N], uint32_t (&g)[N], const ModArgs& m) {
+    const f32x2 nc = pack2(m.neg_c2sq, m.neg_c2sq), one = pack2(1.f, 1.f);
+    cap_pairs(x, m, warp_top(abs_max(x)), [&](int c, f32x2 y) {
+        float a, b;
+        unpack2(mul2(pack2(__uint_as_float(g[c]), __uint_as_float(g[c + 1])), fma2(mul2(y, y), nc, one)), a, b);
+        g[c] = __float_as_uint(a);
+        g[c + 1] = __float_as_uint(b);
+    });
 }
 
 // Query pages per chunk the sparse dK/dV kernel lists in shared memory (3
@@ -510,7 +499,6 @@ bwd_kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const int64_t kpos = kfirst + r;
         const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
         const float sl2 = rsqrtf((float)D) * kLog2e;
-        const float cap_k = MOD && p.m.cap > 0.f ? rsqrtf((float)D) / p.m.cap : 0.f;
         {
             // K row r, head dims [D/2 wg, D/2 wg + D/2) -> TMEM columns kv_TK + D/4 wg ..
             if constexpr (D == 128) tc::tmem_st32(lane_base + kv_TK + wg * 32, kw);
@@ -558,43 +546,60 @@ bwd_kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 dw[c / 2 + 1] = pack_bf16x2(dr[2], dr[3]);
             };
             if constexpr (MOD) {
-                ModScore ms{sl2, cap_k, p.m.cap * kLog2e, 0.f, false};
-                if (p.m.slopes) ms.slope2 = __ldg(p.m.slopes + head_of(t)) * kLog2e;
-                if (cap_k > 0.f) ms.big = __any_sync(0xffffffffu, abs_max(sv) * cap_k > 1.f);
-                const float dist0 = (float)(kpos - q0);
-                const int4* lo4 = reinterpret_cast<const int4*>(sst + 128);
-                const int4* hi4 = reinterpret_cast<const int4*>(sst + 192);
-                auto mod4 = [&](int c, bool mask) {
-                    const float4 l = l4[c / 4], dd = d4[c / 4];
-                    const float lv[4] = {l.x, l.y, l.z, l.w}, dl[4] = {dd.x, dd.y, dd.z, dd.w};
-                    int lo[4], hi[4];
-                    if (mask) {
-                        const int4 a = lo4[c / 4], b = hi4[c / 4];
-                        lo[0] = a.x; lo[1] = a.y; lo[2] = a.z; lo[3] = a.w;
-                        hi[0] = b.x; hi[1] = b.y; hi[2] = b.z; hi[3] = b.w;
-                    }
-                    float pr[4], dr[4];
+                const f32x2 neg = pack2(-1.f, -1.f);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float y, f;
-                        ms.score(__uint_as_float(sv[c + e]), dist0 - (float)(c + e), y, f);
-                        float pv = fast_exp2(y - lv[e]);
-                        float dsv = pv * (__uint_as_float(dv[c + e]) - dl[e]) * f;
-                        if (mask && ((int)kpos < lo[e] || (int)kpos >= hi[e])) pv = dsv = 0.f;
-                        pr[e] = pv;
-                        dr[e] = dsv;
+                for (int c = 0; c < 32; c += 4) {            // dP - D, D of four columns per load
+                    const float4 dd = d4[c / 4];
+                    float a, b;
+                    unpack2(fma2(pack2(dd.x, dd.y), neg, pack2(__uint_as_float(dv[c]), __uint_as_float(dv[c + 1]))), a, b);
+                    dv[c] = __float_as_uint(a);
+                    dv[c + 1] = __float_as_uint(b);
+                    unpack2(fma2(pack2(dd.z, dd.w), neg, pack2(__uint_as_float(dv[c + 2]), __uint_as_float(dv[c + 3]))), a, b);
+                    dv[c + 2] = __float_as_uint(a);
+                    dv[c + 3] = __float_as_uint(b);
+                }
+                float pre = sl2;                             // score in log2 units: pre x
+                if (p.m.cap > 0.f) {
+                    cap_grad(sv, dv, p.m);
+                    pre = 1.f;
+                }
+                if (p.m.slopes) {
+                    // Distance key - query; the queries grow with c.
+                    const int side = (int)kfirst + 127 <= (int)q0 ? -1 : (int)kfirst >= (int)q0 + 31 ? 1 : 0;
+                    add_bias(sv, pre, __ldg(p.m.slopes + head_of(t)) * kLog2e, (float)((int)kpos - (int)q0), -1.f, side);
+                    pre = 1.f;
+                }
+                const f32x2 pre2 = pack2(pre, pre);
+                if ((int)B.tiles[(t_base + t) % n_i] & kTileMasked) {
+                    // Hidden: score -inf, and nothing of the gradient factor (it may not be finite).
+                    const int4* lo4 = reinterpret_cast<const int4*>(sst + 128);
+                    const int4* hi4 = reinterpret_cast<const int4*>(sst + 192);
+#pragma unroll
+                    for (int c = 0; c < 32; c += 4) {
+                        const int4 a = lo4[c / 4], b = hi4[c / 4];
+                        const int lo[4] = {a.x, a.y, a.z, a.w}, hi[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if ((int)kpos < lo[e] || (int)kpos >= hi[e]) {
+                                sv[c + e] = 0xff800000u;
+                                dv[c + e] = 0u;
+                            }
                     }
+                }
+#pragma unroll
+                for (int c = 0; c < 32; c += 4) {
+                    const float4 l = l4[c / 4];
+                    float y[4], pr[4], dr[4];
+                    unpack2(fma2(pack2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), pre2, pack2(-l.x, -l.y)), y[0], y[1]);
+                    unpack2(fma2(pack2(__uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3])), pre2, pack2(-l.z, -l.w)), y[2], y[3]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) pr[e] = fast_exp2(y[e]);
+                    unpack2(mul2(pack2(pr[0], pr[1]), pack2(__uint_as_float(dv[c]), __uint_as_float(dv[c + 1]))), dr[0], dr[1]);
+                    unpack2(mul2(pack2(pr[2], pr[3]), pack2(__uint_as_float(dv[c + 2]), __uint_as_float(dv[c + 3]))), dr[2], dr[3]);
                     pw[c / 2] = pack_bf16x2(pr[0], pr[1]);
                     pw[c / 2 + 1] = pack_bf16x2(pr[2], pr[3]);
                     dw[c / 2] = pack_bf16x2(dr[0], dr[1]);
                     dw[c / 2 + 1] = pack_bf16x2(dr[2], dr[3]);
-                };
-                if ((int)B.tiles[(t_base + t) % n_i] & kTileMasked) {
-#pragma unroll
-                    for (int c = 0; c < 32; c += 4) mod4(c, true);
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 32; c += 4) mod4(c, false);
                 }
             } else if (kfirst + 127 > q0) {                  // crosses the diagonal: mask
 #pragma unroll
@@ -900,14 +905,11 @@ bwd_q_tc_kernel(const __grid_constant__ CUtensorMap tm_do, const __grid_constant
         const bool valid = q_local < p.n_q;
         float lse2 = valid ? p.lse[(size_t)h * p.n_q + q_local] * kLog2e : INFINITY;
         int2 range = make_int2(0, 0);
-        ModScore ms{};
+        float slope2 = 0.f;
         if constexpr (MOD) {
             if (lse2 == -INFINITY) lse2 = INFINITY;              // the row sees nothing: P = 0
             if (valid) range = row_range(p.m, p.q_start, q_local);
-            ms.sl2 = rsqrtf((float)D) * kLog2e;
-            ms.cap_k = p.m.cap > 0.f ? rsqrtf((float)D) / p.m.cap : 0.f;
-            ms.c2 = p.m.cap * kLog2e;
-            ms.slope2 = p.m.slopes ? __ldg(p.m.slopes + h) * kLog2e : 0.f;
+            slope2 = p.m.slopes ? __ldg(p.m.slopes + h) * kLog2e : 0.f;
         }
         const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
         const float sl2 = rsqrtf((float)D) * kLog2e;
@@ -1002,31 +1004,51 @@ bwd_q_tc_kernel(const __grid_constant__ CUtensorMap tm_do, const __grid_constant
                 }
             };
             if constexpr (MOD) {
-                if (ms.cap_k > 0.f)
-                    ms.big = __any_sync(0xffffffffu, fmaxf(abs_max(s0), abs_max(s1)) * ms.cap_k > 1.f);
-                const float dist0 = (float)(kbase - qpos);
+                const int q0 = (int)(p.q_start + (int64_t)qt * 128);
+                const int side = (int)kbase + 63 <= q0 ? -1 : (int)kbase >= q0 + 127 ? 1 : 0;
+                const float dist0 = (float)((int)kbase - (int)qpos);
                 const int lo = range.x - (int)kbase, hi = range.y - (int)kbase;
-                auto mod_half = [&](const uint32_t (&sv)[32], const uint32_t (&dv)[32], int c0, bool mask) {
+                const bool mask = (int)kbase < tr.full_lo || (int)kbase + 64 > tr.full_hi;
+                float pre = sl2;                             // score in log2 units: pre x
+                const f32x2 nD = pack2(-Dr, -Dr), nl = pack2(-lse2, -lse2);
+                auto mod_half = [&](uint32_t (&sv)[32], uint32_t (&dv)[32], int c0) {
 #pragma unroll
                     for (int c = 0; c < 32; c += 2) {
-                        float dr[2];
+                        float a, b;
+                        unpack2(add2(pack2(__uint_as_float(dv[c]), __uint_as_float(dv[c + 1])), nD), a, b);
+                        dv[c] = __float_as_uint(a);
+                        dv[c + 1] = __float_as_uint(b);
+                    }
+                    if (p.m.cap > 0.f) {
+                        cap_grad(sv, dv, p.m);
+                        pre = 1.f;
+                    }
+                    if (p.m.slopes) {
+                        add_bias(sv, pre, slope2, dist0 + (float)c0, 1.f, side);
+                        pre = 1.f;
+                    }
+                    const f32x2 pre2 = pack2(pre, pre);
+                    if (mask) {
+                        // Hidden: score -inf, and nothing of the gradient factor (it may not be finite).
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float y, f;
-                            ms.score(__uint_as_float(sv[c + e]), dist0 + (float)(c0 + c + e), y, f);
-                            dr[e] = fast_exp2(y - lse2) * (__uint_as_float(dv[c + e]) - Dr) * f;
-                            if (mask && (c0 + c + e < lo || c0 + c + e >= hi)) dr[e] = 0.f;
-                        }
-                        dw[(c0 + c) / 2] = pack_bf16x2(dr[0], dr[1]);
+                        for (int c = 0; c < 32; ++c)
+                            if (c0 + c < lo || c0 + c >= hi) {
+                                sv[c] = 0xff800000u;
+                                dv[c] = 0u;
+                            }
+                    }
+#pragma unroll
+                    for (int c = 0; c < 32; c += 2) {
+                        float a, b;
+                        unpack2(fma2(pack2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), pre2, nl), a, b);
+                        unpack2(mul2(pack2(fast_exp2(a), fast_exp2(b)),
+                                     pack2(__uint_as_float(dv[c]), __uint_as_float(dv[c + 1]))), a, b);
+                        dw[(c0 + c) / 2] = pack_bf16x2(a, b);
                     }
                 };
-                if ((int)kbase < tr.full_lo || (int)kbase + 64 > tr.full_hi) {
-                    mod_half(s0, d0, 0, true);
-                    mod_half(s1, d1, 32, true);
-                } else {
-                    mod_half(s0, d0, 0, false);
-                    mod_half(s1, d1, 32, false);
-                }
+                mod_half(s0, d0, 0);
+                pre = sl2;
+                mod_half(s1, d1, 32);
             } else if (kbase + 63 > first_diag) {            // crosses the diagonal: mask
                 grad_half(s0, d0, 0, true);
                 grad_half(s1, d1, 32, true);

@@ -389,40 +389,38 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
                 tc::tmem_ld32(lane_base + st * 128 + wg * 64 + 32, r1);
                 tc::tmem_wait_ld(r0);
                 tc::tmem_wait_ld(r1);
+                if constexpr (MOD) {
+                    const int kb = (sel_row ? sel_row[j] : first + j) * kTile + wg * 64;   // my first key
+                    float pre = sl2;                  // y = pre x, in log2 units
+                    if (p.m.cap > 0.f) {
+                        const float top = warp_top(fmaxf(abs_max(r0), abs_max(r1)));
+                        cap_pairs(r0, p.m, top, [](int, f32x2) {});
+                        cap_pairs(r1, p.m, top, [](int, f32x2) {});
+                        pre = 1.f;
+                    }
+                    if (p.m.slopes) {
+                        const int q0 = (int)(p.q_start + (int64_t)qt * kTile);
+                        const int side = kb + 63 <= q0 ? -1 : kb >= q0 + kTile - 1 ? 1 : 0;
+                        const float d0 = (float)(kb - (int)(p.q_start + q_local));
+                        add_bias(r0, pre, slope2, d0, 1.f, side);
+                        add_bias(r1, pre, slope2, d0 + 32.f, 1.f, side);
+                    }
+                    if (kb < tr.full_lo || kb + 63 >= tr.full_hi) {
+                        const int lo = range.x - kb, hi_ = range.y - kb;
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) {
+                            if (c < lo || c >= hi_) r0[c] = 0xff800000u;
+                            if (c + 32 < lo || c + 32 >= hi_) r1[c] = 0xff800000u;
+                        }
+                    }
+                }
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
                     x[e] = __uint_as_float(r0[e]);
                     x[32 + e] = __uint_as_float(r1[e]);
                 }
             }
-            if constexpr (MOD) {
-                const int kb = (sel_row ? sel_row[j] : first + j) * kTile + wg * 64;   // my first key
-                if (p.m.cap > 0.f) {
-                    const float k = rsqrtf((float)D) / p.m.cap, c2 = p.m.cap * kLog2e;
-                    float big = 0.f;
-#pragma unroll
-                    for (int c = 0; c < 64; ++c) big = fmaxf(big, fabsf(x[c]));
-                    if (__any_sync(0xffffffffu, big * k > 1.f)) {
-#pragma unroll
-                        for (int c = 0; c < 64; ++c) x[c] = c2 * tanh_any(x[c] * k);
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 64; ++c) x[c] = c2 * tanh_small(x[c] * k);
-                    }
-                }
-                if (p.m.slopes) {
-                    const float pre = p.m.cap > 0.f ? 1.f : sl2;
-                    const float off = (float)(kb - (int)(p.q_start + q_local));
-#pragma unroll
-                    for (int c = 0; c < 64; ++c) x[c] = fmaf(-slope2, fabsf(off + (float)c), x[c] * pre);
-                }
-                if (kb < tr.full_lo || kb + 63 >= tr.full_hi) {
-                    const int lo = range.x - kb, hi_ = range.y - kb;
-#pragma unroll
-                    for (int c = 0; c < 64; ++c)
-                        if (c < lo || c >= hi_) x[c] = -INFINITY;
-                }
-            } else if (j == nt - 1) {                 // own page: causal mask (key col > row)
+            if (!MOD && j == nt - 1) {                // own page: causal mask (key col > row)
 #pragma unroll
                 for (int c = 0; c < 64; ++c)
                     if (wg * 64 + c > row) x[c] = -INFINITY;
@@ -431,8 +429,17 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
             float mpart[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) mpart[k] = x[k];
+            if constexpr (MOD) {
 #pragma unroll
-            for (int c = 8; c < 64; ++c) mpart[c & 7] = fmaxf(mpart[c & 7], x[c]);
+                for (int c = 8; c < 56; c += 16)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) mpart[k] = max3(mpart[k], x[c + k], x[c + 8 + k]);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) mpart[k] = fmaxf(mpart[k], x[56 + k]);
+            } else {
+#pragma unroll
+                for (int c = 8; c < 64; ++c) mpart[c & 7] = fmaxf(mpart[c & 7], x[c]);
+            }
 #pragma unroll
             for (int k = 4; k > 0; k >>= 1)
 #pragma unroll
@@ -455,18 +462,29 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
             // (MOD: a row that has seen nothing yet keeps m = -inf; its weights are 0.)
             const float neg_m = MOD && m == -INFINITY ? 0.f : -m;
             if constexpr (MOD) lsum *= alpha;
-            float ls[2] = {0.f, 0.f};
+            if constexpr (MOD) {
+                const f32x2 ms2 = pack2(ms, ms), nm2 = pack2(neg_m, neg_m);
+                f32x2 sum[2] = {0ull, 0ull};
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-                const float p0 = fast_exp2(fmaf(x[2 * c], ms, neg_m));
-                const float p1 = fast_exp2(fmaf(x[2 * c + 1], ms, neg_m));
-                if constexpr (MOD) {
-                    ls[0] += p0;
-                    ls[1] += p1;
+                for (int c = 0; c < 32; ++c) {
+                    float p0, p1;
+                    unpack2(fma2(pack2(x[2 * c], x[2 * c + 1]), ms2, nm2), p0, p1);
+                    p0 = fast_exp2(p0);
+                    p1 = fast_exp2(p1);
+                    sum[c & 1] = add2(sum[c & 1], pack2(p0, p1));
+                    pk[c] = pack_bf16x2(p0, p1);
                 }
-                pk[c] = pack_bf16x2(p0, p1);
+                float s0, s1;
+                unpack2(add2(sum[0], sum[1]), s0, s1);
+                lsum += s0 + s1;
+            } else {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    const float p0 = fast_exp2(fmaf(x[2 * c], sl2, neg_m));
+                    const float p1 = fast_exp2(fmaf(x[2 * c + 1], sl2, neg_m));
+                    pk[c] = pack_bf16x2(p0, p1);
+                }
             }
-            if constexpr (MOD) lsum += ls[0] + ls[1];
             if (j > 0 && __any_sync(0xffffffffu, rescale)) {
                 // PV_{j-1} must be done before O is touched (PV_j waits for this tile's P).
                 ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.o_done, (it - 1) & 1, p.err));

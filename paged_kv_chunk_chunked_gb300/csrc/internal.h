@@ -169,6 +169,11 @@ struct ModArgs {
     const int64_t* k_end;            // [n_q] or null (own position + 1): one past the last
     const float* slopes;             // [Hq] or null: s -= slope |i - j|, after the cap
     float cap;                       // c > 0, or 0: no cap
+    // Of the cap, for the tensor-core kernels (set_cap): u = s / c = k x of a raw
+    // logit x, scores in log2 units c2 tanh(u), and the scaled coefficients of
+    // the short polynomial: c2 tanh(k x) = x (a0 + a1 x^2 + a2 x^4 + a3 x^6).
+    float k, c2, a0, a1, a2, a3;
+    float neg_c2sq;                  // -1 / c2^2: 1 - tanh^2 = 1 + neg_c2sq y^2
     int64_t n_keys;                  // keys a call may see: the sequence's length, or q_start + n_q without k_end
 };
 

@@ -15,6 +15,26 @@
 
 namespace pkv {
 
+// The polynomials of tanh (see tanh_long2): ranges, and the short one's coefficients.
+constexpr float kTanhShort = 0.4f, kTanhLong = 0.75f;
+constexpr float kTanhA[4] = {0.9999998807907104f, -0.33331361413002014f, 0.13270977139472961f, -0.04755360260605812f};
+
+// Sets the cap c (0: none) for head dimension d.
+inline void set_cap(ModArgs* m, float c, int d) {
+    m->cap = c;
+    m->k = m->c2 = m->a0 = m->a1 = m->a2 = m->a3 = m->neg_c2sq = 0.f;
+    if (!(c > 0.f)) return;
+    const double k = 1.0 / sqrt((double)d) / c, c2 = (double)c * 1.4426950408889634;
+    const double u2 = k * k;
+    m->k = (float)k;
+    m->c2 = (float)c2;
+    m->a0 = (float)(kTanhA[0] * c2 * k);
+    m->a1 = (float)(kTanhA[1] * c2 * k * u2);
+    m->a2 = (float)(kTanhA[2] * c2 * k * u2 * u2);
+    m->a3 = (float)(kTanhA[3] * c2 * k * u2 * u2 * u2);
+    m->neg_c2sq = (float)(-1.0 / (c2 * c2));
+}
+
 // The keys [lo, hi) visible to query row i of the chunk; (0, 0) if none.
 // Positions fit 32 bits: a pool holds fewer than 2^31 rows.
 __device__ __forceinline__ int2 row_range(const ModArgs& m, int64_t q_start, int64_t i) {
@@ -60,24 +80,137 @@ __device__ __forceinline__ TileRange tile_range(const ModArgs& m, int64_t q_star
     return t;
 }
 
-// tanh(u) for |u| <= 1: u times a polynomial in u^2 fitted to tanh(u) / u by
-// iteratively reweighted least squares (a minimax fit), within 1.2e-7 in fp32.
-__device__ __forceinline__ float tanh_small(float u) {
-    const float w = u * u;
-    float p = 0.0010410224786028266f;
-    p = fmaf(p, w, -0.006203378550708294f);
-    p = fmaf(p, w, 0.020289979875087738f);
-    p = fmaf(p, w, -0.05345702916383743f);
-    p = fmaf(p, w, 0.13325203955173492f);
-    p = fmaf(p, w, -0.33332839608192444f);
-    p = fmaf(p, w, 0.9999999403953552f);
-    return u * p;
+// Pairs of floats: one instruction for two elements (sm_100 on). Sums, products
+// and fmas are the single ones', element by element.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 x, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
-// tanh(u) for any u: 1 - 2 / (1 + e^(2u)), absolute error below 3e-7 (the
-// division is exact to an ulp; u = +-inf gives +-1).
+// tanh(u) = u p(u^2), p a polynomial fitted to tanh(u) / u by iteratively
+// reweighted least squares (a minimax fit). The fp32 pipe bounds the capped
+// kernels, so the degree follows the largest |u| of a warp's tile rows: capped
+// logits are mostly far below their cap.
+//   |u| <= 0.4:  4 terms, relative error 9.8e-8, with the cap's constants folded
+//                into the coefficients (ModArgs): 5 operations from the raw logit
+//                to the score in log2 units;
+//   |u| <= 0.75: 6 terms, relative error 2.9e-8, 9 operations;
+//   beyond:      through the exponential, two special-function operations.
+// Measured, 28 heads, d 128, 4096 queries on 16384 keys, forward: see the
+// forward kernel.
+__device__ __forceinline__ f32x2 tanh_long2(f32x2 u) {
+    const f32x2 w = mul2(u, u);
+    f32x2 p = pack2(-0.004716257099062204f, -0.004716257099062204f);
+    p = fma2(p, w, pack2(0.01958290860056877f, 0.01958290860056877f));
+    p = fma2(p, w, pack2(-0.05334442853927612f, -0.05334442853927612f));
+    p = fma2(p, w, pack2(0.1332540661096573f, 0.1332540661096573f));
+    p = fma2(p, w, pack2(-0.33332958817481995f, -0.33332958817481995f));
+    p = fma2(p, w, pack2(1.f, 1.f));
+    return mul2(u, p);
+}
+
+// tanh(u) for any u: 1 - 2 / (1 + e^(2u)), absolute error below 3e-7;
+// u = +-inf gives +-1.
 __device__ __forceinline__ float tanh_any(float u) {
     return 1.f - __fdividef(2.f, 1.f + fast_exp2(u * (2.f * kLog2e)));
+}
+
+// Largest of three, and of three magnitudes (one instruction, sm_100 on).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+    float r;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+template <int N> __device__ __forceinline__ float abs_max(const uint32_t (&x)[N]) {
+    float b[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < N; c += 2)
+        b[(c >> 1) & 3] = max3_abs(b[(c >> 1) & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+    return max3(fmaxf(b[0], b[1]), b[2], b[3]);
+}
+
+// The cap over a row of a tile, in place: raw logits x -> scores y in log2
+// units; use(c, y) sees elements c, c + 1. `top`: the largest |x| of the warp's
+// rows, which picks the form for the whole warp.
+template <int N, typename F>
+__device__ __forceinline__ void cap_pairs(uint32_t (&x)[N], const ModArgs& m, float top, F&& use) {
+    auto put = [&](int c, f32x2 y) {
+        float a, b;
+        unpack2(y, a, b);
+        x[c] = __float_as_uint(a);
+        x[c + 1] = __float_as_uint(b);
+        use(c, y);
+    };
+    auto get = [&](int c) { return pack2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])); };
+    if (top * m.k <= kTanhShort) {
+        const f32x2 a0 = pack2(m.a0, m.a0), a1 = pack2(m.a1, m.a1), a2 = pack2(m.a2, m.a2), a3 = pack2(m.a3, m.a3);
+#pragma unroll
+        for (int c = 0; c < N; c += 2) {
+            const f32x2 v = get(c), w = mul2(v, v);
+            put(c, mul2(v, fma2(fma2(fma2(a3, w, a2), w, a1), w, a0)));
+        }
+    } else if (top * m.k <= kTanhLong) {
+        const f32x2 k = pack2(m.k, m.k), c2 = pack2(m.c2, m.c2);
+#pragma unroll
+        for (int c = 0; c < N; c += 2) put(c, mul2(tanh_long2(mul2(get(c), k)), c2));
+    } else {
+#pragma unroll
+        for (int c = 0; c < N; c += 2)
+            put(c, pack2(m.c2 * tanh_any(__uint_as_float(x[c]) * m.k), m.c2 * tanh_any(__uint_as_float(x[c + 1]) * m.k)));
+    }
+}
+// Every lane's largest over the warp (of values >= 0; their bits order as integers).
+__device__ __forceinline__ float warp_top(float x) {
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
+}
+
+// The distance bias over a row of a tile, in place: x <- x * pre + bias, where
+// element c's key (or query) lies at distance d0 + dir * c from the row's own
+// position. Where the whole tile lies on one side the bias is linear in c (one
+// operation to form it); only tiles across the diagonal need the magnitude.
+template <int N>
+__device__ __forceinline__ void add_bias(uint32_t (&x)[N], float pre, float slope2, float d0, float dir, int side) {
+    const f32x2 pp = pack2(pre, pre);
+    auto run = [&](auto&& bias) {
+#pragma unroll
+        for (int c = 0; c < N; c += 2) {
+            float a, b;
+            unpack2(fma2(pack2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), pp, pack2(bias(c), bias(c + 1))), a, b);
+            x[c] = __float_as_uint(a);
+            x[c + 1] = __float_as_uint(b);
+        }
+    };
+    if (side != 0) {                                  // sign of the distance, the same for all elements
+        const float base = -slope2 * (float)side * d0, step = -slope2 * (float)side * dir;
+        run([&](int c) { return fmaf(step, (float)c, base); });
+    } else {
+        run([&](int c) { return -slope2 * fabsf(fmaf(dir, (float)c, d0)); });
+    }
 }
 
 }  // namespace pkv

@@ -157,7 +157,7 @@ def test_masks(dtype, P, mask):
 
 @pytest.mark.parametrize("mask", ["causal", "random"])
 @pytest.mark.parametrize("cap,bias,q_scale", [(15.0, False, 1.0), (0.0, True, 1.0), (2.0, True, 4.0), (30.0, True, 8.0),
-                                              (1e6, False, 1.0), (1e-3, False, 1.0)])
+                                              (1e4, False, 1.0), (1e-3, False, 1.0), (6.0, False, 1.0), (4.0, True, 1.0)])
 @pytest.mark.parametrize("dtype,d,P", [("bf16", 128, 128), ("bf16", 64, 128), ("bf16", 64, 16), ("f32", 128, 32)])
 def test_cap_and_bias(dtype, d, P, cap, bias, q_scale, mask):
     Case(dtype, 4, 2, d, P, 133, 140, extra=11, cap=cap, bias=bias, mask=mask, q_scale=q_scale, seed=3).check()
