@@ -78,20 +78,6 @@ struct BwdParams {
     int4* bounds;              // MOD: TileRange of each 64-query tile, written by the dQ kernel
 };
 
-// The MOD kernels' cap over a row of a tile, in place: raw logits x -> scores in
-// log2 units; g, the gradient factor dP - D, takes the derivative
-// 1 - tanh^2 = 1 - (y / c2)^2.
-template <int N>
-__device__ __forceinline__ void cap_grad(uint32_t (&x)[N], uint32_t (&g)[N], const ModArgs& m) {
-    const f32x2 nc = pack2(m.neg_c2sq, m.neg_c2sq), one = pack2(1.f, 1.f);
-    cap_pairs(x, m, warp_top(abs_max(x)), [&](int c, f32x2 y) {
-        float a, b;
-        unpack2(mul2(pack2(__uint_as_float(g[c]), __uint_as_float(g[c + 1])), fma2(mul2(y, y), nc, one)), a, b);
-        g[c] = __float_as_uint(a);
-        g[c + 1] = __float_as_uint(b);
-    });
-}
-
 // Query pages per chunk the sparse dK/dV kernel lists in shared memory (3
 // bytes each): chunks of up to 262144 tokens at page 128. Longer chunks run
 // on the CUDA-core kernel.
@@ -546,60 +532,75 @@ bwd_kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 dw[c / 2 + 1] = pack_bf16x2(dr[2], dr[3]);
             };
             if constexpr (MOD) {
-                const f32x2 neg = pack2(-1.f, -1.f);
-#pragma unroll
-                for (int c = 0; c < 32; c += 4) {            // dP - D, D of four columns per load
-                    const float4 dd = d4[c / 4];
+                // Columns c, c + 1: weights P = 2^(pre v - LSE) and dS = P (dP - D) f, f the
+                // cap's derivative 1 - tanh^2 = 1 - (y / c2)^2. The cap's products and the
+                // exponentials go through one pass, so that the two pipes overlap.
+                const bool capped = p.m.cap > 0.f;
+                const f32x2 neg = pack2(-1.f, -1.f), one = pack2(1.f, 1.f), nc = pack2(p.m.neg_c2sq, p.m.neg_c2sq);
+                const float2* l2 = reinterpret_cast<const float2*>(sst);
+                const float2* dd2 = reinterpret_cast<const float2*>(sst + 64);
+                auto grad = [&](int c) {                         // dP - D
+                    const float2 d = dd2[c / 2];
+                    return fma2(pack2(d.x, d.y), neg, pair_at(dv, c));
+                };
+                auto emit = [&](int c, f32x2 v, f32x2 pre2, f32x2 g) {
+                    const float2 l = l2[c / 2];
                     float a, b;
-                    unpack2(fma2(pack2(dd.x, dd.y), neg, pack2(__uint_as_float(dv[c]), __uint_as_float(dv[c + 1]))), a, b);
-                    dv[c] = __float_as_uint(a);
-                    dv[c + 1] = __float_as_uint(b);
-                    unpack2(fma2(pack2(dd.z, dd.w), neg, pack2(__uint_as_float(dv[c + 2]), __uint_as_float(dv[c + 3]))), a, b);
-                    dv[c + 2] = __float_as_uint(a);
-                    dv[c + 3] = __float_as_uint(b);
-                }
-                float pre = sl2;                             // score in log2 units: pre x
-                if (p.m.cap > 0.f) {
-                    cap_grad(sv, dv, p.m);
-                    pre = 1.f;
-                }
-                if (p.m.slopes) {
-                    // Distance key - query; the queries grow with c.
-                    const int side = (int)kfirst + 127 <= (int)q0 ? -1 : (int)kfirst >= (int)q0 + 31 ? 1 : 0;
-                    add_bias(sv, pre, __ldg(p.m.slopes + head_of(t)) * kLog2e, (float)((int)kpos - (int)q0), -1.f, side);
-                    pre = 1.f;
-                }
-                const f32x2 pre2 = pack2(pre, pre);
-                if ((int)B.tiles[(t_base + t) % n_i] & kTileMasked) {
-                    // Hidden: score -inf, and nothing of the gradient factor (it may not be finite).
-                    const int4* lo4 = reinterpret_cast<const int4*>(sst + 128);
-                    const int4* hi4 = reinterpret_cast<const int4*>(sst + 192);
-#pragma unroll
-                    for (int c = 0; c < 32; c += 4) {
-                        const int4 a = lo4[c / 4], b = hi4[c / 4];
-                        const int lo[4] = {a.x, a.y, a.z, a.w}, hi[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if ((int)kpos < lo[e] || (int)kpos >= hi[e]) {
-                                sv[c + e] = 0xff800000u;
-                                dv[c + e] = 0u;
-                            }
+                    unpack2(fma2(v, pre2, pack2(-l.x, -l.y)), a, b);
+                    a = fast_exp2(a);
+                    b = fast_exp2(b);
+                    pw[c / 2] = pack_bf16x2(a, b);
+                    unpack2(mul2(pack2(a, b), g), a, b);
+                    dw[c / 2] = pack_bf16x2(a, b);
+                };
+                // Distance key - query; the queries grow with c.
+                const int side = (int)kfirst + 127 <= (int)q0 ? -1 : (int)kfirst >= (int)q0 + 31 ? 1 : 0;
+                const float d0 = (float)((int)kpos - (int)q0);
+                const float slope2 = p.m.slopes ? __ldg(p.m.slopes + head_of(t)) * kLog2e : 0.f;
+                const f32x2 sl22 = pack2(sl2, sl2);
+                const bool mask = (int)B.tiles[(t_base + t) % n_i] & kTileMasked;
+                if (mask || (capped && p.m.slopes)) {
+                    float pre = sl2;                             // score in log2 units: pre x
+                    if (capped) {
+                        const float top = warp_top(abs_max(sv));
+                        cap_pairs(sv, p.m, top, [&](int c, f32x2 y) {
+                            put_pair(sv, c, y);
+                            put_pair(dv, c, mul2(grad(c), fma2(mul2(y, y), nc, one)));
+                        });
+                        pre = 1.f;
+                    } else {
+                        each_pair(dv, [&](int c, f32x2) { put_pair(dv, c, grad(c)); });
                     }
-                }
+                    if (p.m.slopes) {
+                        bias_pairs(sv, pre, slope2, d0, -1.f, 0, [&](int c, f32x2 y) { put_pair(sv, c, y); });
+                        pre = 1.f;
+                    }
+                    if (mask) {
+                        // Hidden: score -inf, and nothing of the gradient factor (it may not be finite).
+                        const int4* lo4 = reinterpret_cast<const int4*>(sst + 128);
+                        const int4* hi4 = reinterpret_cast<const int4*>(sst + 192);
 #pragma unroll
-                for (int c = 0; c < 32; c += 4) {
-                    const float4 l = l4[c / 4];
-                    float y[4], pr[4], dr[4];
-                    unpack2(fma2(pack2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), pre2, pack2(-l.x, -l.y)), y[0], y[1]);
-                    unpack2(fma2(pack2(__uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3])), pre2, pack2(-l.z, -l.w)), y[2], y[3]);
+                        for (int c = 0; c < 32; c += 4) {
+                            const int4 a = lo4[c / 4], b = hi4[c / 4];
+                            const int lo[4] = {a.x, a.y, a.z, a.w}, hi[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) pr[e] = fast_exp2(y[e]);
-                    unpack2(mul2(pack2(pr[0], pr[1]), pack2(__uint_as_float(dv[c]), __uint_as_float(dv[c + 1]))), dr[0], dr[1]);
-                    unpack2(mul2(pack2(pr[2], pr[3]), pack2(__uint_as_float(dv[c + 2]), __uint_as_float(dv[c + 3]))), dr[2], dr[3]);
-                    pw[c / 2] = pack_bf16x2(pr[0], pr[1]);
-                    pw[c / 2 + 1] = pack_bf16x2(pr[2], pr[3]);
-                    dw[c / 2] = pack_bf16x2(dr[0], dr[1]);
-                    dw[c / 2 + 1] = pack_bf16x2(dr[2], dr[3]);
+                            for (int e = 0; e < 4; ++e)
+                                if ((int)kpos < lo[e] || (int)kpos >= hi[e]) {
+                                    sv[c + e] = 0xff800000u;
+                                    dv[c + e] = 0u;
+                                }
+                        }
+                    }
+                    const f32x2 pre2 = pack2(pre, pre);
+                    each_pair(sv, [&](int c, f32x2 v) { emit(c, v, pre2, pair_at(dv, c)); });
+                } else if (capped) {
+                    cap_pairs(sv, p.m, warp_top(abs_max(sv)), [&](int c, f32x2 y) {
+                        emit(c, y, one, mul2(grad(c), fma2(mul2(y, y), nc, one)));
+                    });
+                } else if (p.m.slopes) {
+                    bias_pairs(sv, sl2, slope2, d0, -1.f, side, [&](int c, f32x2 y) { emit(c, y, one, grad(c)); });
+                } else {
+                    each_pair(sv, [&](int c, f32x2 v) { emit(c, v, sl22, grad(c)); });
                 }
             } else if (kfirst + 127 > q0) {                  // crosses the diagonal: mask
 #pragma unroll
@@ -785,7 +786,8 @@ bwd_q_tc_kernel(const __grid_constant__ CUtensorMap tm_do, const __grid_constant
                 tc::tma_load_3d(smem + q_dO + b * 16 * KB, &tm_do, &B.q_full, 64 * b, h, q_row0);
         }
         tc::PageBatch pages;
-        pages.init(p.bt, sel_row, T, lane, first);
+        pages.init(p.bt, sel_row, T, lane, sel_row ? 0 : first, 1,
+                   MOD ? (int)((p.m.n_keys + 127) / 128) : 0x7fffffff);
         int k_issued = 0, v_issued = 0;
         for (int t = 0; t < T; ++t) {
             const int ks = t % q_KST, vs = t % q_VST;
@@ -1009,45 +1011,56 @@ bwd_q_tc_kernel(const __grid_constant__ CUtensorMap tm_do, const __grid_constant
                 const float dist0 = (float)((int)kbase - (int)qpos);
                 const int lo = range.x - (int)kbase, hi = range.y - (int)kbase;
                 const bool mask = (int)kbase < tr.full_lo || (int)kbase + 64 > tr.full_hi;
-                float pre = sl2;                             // score in log2 units: pre x
-                const f32x2 nD = pack2(-Dr, -Dr), nl = pack2(-lse2, -lse2);
+                // As in the dK/dV kernel: dS = 2^(pre v - LSE) (dP - D) f in one pass.
+                const bool capped = p.m.cap > 0.f;
+                const f32x2 nD = pack2(-Dr, -Dr), nl = pack2(-lse2, -lse2), one = pack2(1.f, 1.f),
+                            nc = pack2(p.m.neg_c2sq, p.m.neg_c2sq), sl22 = pack2(sl2, sl2);
+                const float top = capped ? warp_top(fmaxf(abs_max(s0), abs_max(s1))) : 0.f;
                 auto mod_half = [&](uint32_t (&sv)[32], uint32_t (&dv)[32], int c0) {
-#pragma unroll
-                    for (int c = 0; c < 32; c += 2) {
+                    auto grad = [&](int c) { return add2(pair_at(dv, c), nD); };
+                    auto emit = [&](int c, f32x2 v, f32x2 pre2, f32x2 g) {
                         float a, b;
-                        unpack2(add2(pack2(__uint_as_float(dv[c]), __uint_as_float(dv[c + 1])), nD), a, b);
-                        dv[c] = __float_as_uint(a);
-                        dv[c + 1] = __float_as_uint(b);
-                    }
-                    if (p.m.cap > 0.f) {
-                        cap_grad(sv, dv, p.m);
-                        pre = 1.f;
-                    }
-                    if (p.m.slopes) {
-                        add_bias(sv, pre, slope2, dist0 + (float)c0, 1.f, side);
-                        pre = 1.f;
-                    }
-                    const f32x2 pre2 = pack2(pre, pre);
-                    if (mask) {
-                        // Hidden: score -inf, and nothing of the gradient factor (it may not be finite).
-#pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (c0 + c < lo || c0 + c >= hi) {
-                                sv[c] = 0xff800000u;
-                                dv[c] = 0u;
-                            }
-                    }
-#pragma unroll
-                    for (int c = 0; c < 32; c += 2) {
-                        float a, b;
-                        unpack2(fma2(pack2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), pre2, nl), a, b);
-                        unpack2(mul2(pack2(fast_exp2(a), fast_exp2(b)),
-                                     pack2(__uint_as_float(dv[c]), __uint_as_float(dv[c + 1]))), a, b);
+                        unpack2(fma2(v, pre2, nl), a, b);
+                        unpack2(mul2(pack2(fast_exp2(a), fast_exp2(b)), g), a, b);
                         dw[(c0 + c) / 2] = pack_bf16x2(a, b);
+                    };
+                    if (mask || (capped && p.m.slopes)) {
+                        float pre = sl2;                     // score in log2 units: pre x
+                        if (capped) {
+                            cap_pairs(sv, p.m, top, [&](int c, f32x2 y) {
+                                put_pair(sv, c, y);
+                                put_pair(dv, c, mul2(grad(c), fma2(mul2(y, y), nc, one)));
+                            });
+                            pre = 1.f;
+                        } else {
+                            each_pair(dv, [&](int c, f32x2) { put_pair(dv, c, grad(c)); });
+                        }
+                        if (p.m.slopes) {
+                            bias_pairs(sv, pre, slope2, dist0 + (float)c0, 1.f, 0, [&](int c, f32x2 y) { put_pair(sv, c, y); });
+                            pre = 1.f;
+                        }
+                        if (mask) {
+                            // Hidden: score -inf, and nothing of the gradient factor (it may not be finite).
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (c0 + c < lo || c0 + c >= hi) {
+                                    sv[c] = 0xff800000u;
+                                    dv[c] = 0u;
+                                }
+                        }
+                        const f32x2 pre2 = pack2(pre, pre);
+                        each_pair(sv, [&](int c, f32x2 v) { emit(c, v, pre2, pair_at(dv, c)); });
+                    } else if (capped) {
+                        cap_pairs(sv, p.m, top, [&](int c, f32x2 y) {
+                            emit(c, y, one, mul2(grad(c), fma2(mul2(y, y), nc, one)));
+                        });
+                    } else if (p.m.slopes) {
+                        bias_pairs(sv, sl2, slope2, dist0 + (float)c0, 1.f, side, [&](int c, f32x2 y) { emit(c, y, one, grad(c)); });
+                    } else {
+                        each_pair(sv, [&](int c, f32x2 v) { emit(c, v, sl22, grad(c)); });
                     }
                 };
                 mod_half(s0, d0, 0);
-                pre = sl2;
                 mod_half(s1, d1, 32);
             } else if (kbase + 63 > first_diag) {            // crosses the diagonal: mask
                 grad_half(s0, d0, 0, true);

@@ -93,8 +93,11 @@ struct __align__(8) FwdBarriers {
     uint64_t o_free;                 // a head's O read by the epilogue (256 arrivals)
     uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
     uint64_t s_full[2];
-    uint64_t p_full;
-    uint64_t o_done;
+    // By tile parity, like s_full: a warp may be a tile ahead of another (which rescales
+    // O, or repeats its pass), and neither its arrival for the next tile nor a wait for
+    // the last PV may fall into the phase of the tile before.
+    uint64_t p_full[2];
+    uint64_t o_done[2];
     uint64_t drain;
     uint32_t tmem_base;
     int n_tiles;
@@ -115,7 +118,8 @@ using tc::drain_wait;
 template <int D>
 __device__ __forceinline__ void produce_ring(const FwdParams& p, uint8_t* smem, FwdBarriers& B,
                                              const CUtensorMap& tmap, bool is_k, int kvh, const int32_t* sel_row,
-                                             int first, int nt, int lane, tc::PageBatch& pages) {
+                                             int first, int step, int limit, int nt, int lane,
+                                             tc::PageBatch& pages) {
     using L = FwdLayout<D>;
     const int nst = is_k ? kKStages : kVStages;
     uint64_t* full = is_k ? B.k_full : B.v_full;
@@ -127,7 +131,7 @@ __device__ __forceinline__ void produce_ring(const FwdParams& p, uint8_t* smem, 
     int issued = 0;
     bool ok = true;
     for (int hi = 0; ok && hi < p.heads_per_cta; ++hi) {
-        if (hi > 0) pages.init(p.bt, sel_row, nt, lane, first);
+        if (hi > 0) pages.init(p.bt, sel_row, nt, lane, first, step, limit);
         for (int j = 0; j < nt; ++j) {
             const int it = hi * nt + j;
             const int st = it % nst;
@@ -199,7 +203,11 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
     tc::PageBatch pages;
     int n_pre = 0;
     TileRange tr{};
-    int first = 0;                                       // MOD: logical page of tile 0 (dense)
+    // Tile j is entry first + step * j of the page list (dense: that page). MOD walks
+    // back from the last page: the distance bias lets the maximum grow towards the
+    // query's own position, and each growth costs a rescaling.
+    int first = 0, step = 1;
+    const int limit = MOD ? (int)((p.m.n_keys + kTile - 1) / kTile) : 0x7fffffff;
     if constexpr (MOD) {
         tr = tile_range<kTile>(p.m, p.q_start, (int64_t)qt * kTile, p.n_q, lane);
         const int p0 = tr.lo / kTile;
@@ -207,9 +215,9 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
         // This CTA's share of the tile's pages.
         const int s0 = (int)((int64_t)n * blockIdx.z / gridDim.z), s1 = (int)((int64_t)n * (blockIdx.z + 1) / gridDim.z);
         n_pre = s1 - s0;
-        first = p0 + s0;
-        if (sel_row) sel_row += s0;
-        if (warp == 0 || warp == kThreads / 32 - 1) pages.init(p.bt, sel_row, n_pre, lane, first);
+        first = (sel_row ? 0 : p0) + s1 - 1;
+        step = -1;
+        if (warp == 0 || warp == kThreads / 32 - 1) pages.init(p.bt, sel_row, n_pre, lane, first, step, limit);
     } else if (warp == 0 || warp == kThreads / 32 - 1) {
         n_pre = sel_row ? sel_count_warp(sel_row, p.kmax, lane) : (int)(p.q_start / kTile) + qt + 1;
         pages.init(p.bt, sel_row, n_pre, lane);
@@ -246,9 +254,11 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
             tc::mbar_init(&B.v_full[s], 1);
             tc::mbar_init(&B.v_empty[s], 1);
         }
-        for (int s = 0; s < 2; ++s) tc::mbar_init(&B.s_full[s], 1);
-        tc::mbar_init(&B.p_full, kSoftmaxThreads);
-        tc::mbar_init(&B.o_done, 1);
+        for (int s = 0; s < 2; ++s) {
+            tc::mbar_init(&B.s_full[s], 1);
+            tc::mbar_init(&B.p_full[s], kSoftmaxThreads);
+            tc::mbar_init(&B.o_done[s], 1);
+        }
         tc::mbar_init(&B.drain, 1);
         tc::fence_barrier_init();
     }
@@ -267,10 +277,10 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
 
     if (warp == 0) {
         // ------------------------------------------------------------ K producer
-        produce_ring<D>(p, smem, B, tmap_k, true, kvh, sel_row, first, nt, lane, pages);
+        produce_ring<D>(p, smem, B, tmap_k, true, kvh, sel_row, first, step, limit, nt, lane, pages);
     } else if (warp == kThreads / 32 - 1) {
         // ------------------------------------------------------------ V producer
-        produce_ring<D>(p, smem, B, tmap_v, false, kvh, sel_row, first, nt, lane, pages);
+        produce_ring<D>(p, smem, B, tmap_v, false, kvh, sel_row, first, step, limit, nt, lane, pages);
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         // The whole warp runs the loop (warp-uniform descriptors); one elected
@@ -290,7 +300,7 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
             const int vs = i % kVStages;
             const int hi = i / nt;
             const bool first = (i % nt) == 0;
-            if (!tc::warp_wait(&B.p_full, i & 1, p.err)) return false;
+            if (!tc::warp_wait(&B.p_full[i & 1], (i >> 1) & 1, p.err)) return false;
             if (!tc::warp_wait(&B.v_full[vs], (i / kVStages) & 1, p.err)) return false;
             if (first && hi > 0 && !tc::warp_wait(&B.o_free, (hi - 1) & 1, p.err)) return false;
             tc::tc_fence_after();
@@ -303,7 +313,7 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
                 for (int kk = 0; kk < 8; ++kk)
                     tc::mma_bf16_ts(tmem_o, tmem_p + p_col(kk), tc::sdesc_at(dv0, vs * kVStageBytes + kk * 2048),
                                     idesc_pv, (!first || kk > 0) ? 1u : 0u);
-                tc::mma_commit(&B.o_done);
+                tc::mma_commit(&B.o_done[i & 1]);
                 tc::mma_commit(&B.v_empty[vs]);
             }
             __syncwarp();
@@ -373,6 +383,8 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
         }
         tc::mbar_arrive(&B.q_full);
         float m = -INFINITY, lsum = 0.f;
+        bool short_cap = MOD && p.m.cap > 0.f;
+        const int qtile = (int)(p.q_start + (int64_t)qt * kTile), qpos = qtile + row;
         const float slope2 = MOD && p.m.slopes ? p.m.slopes[h] * kLog2e : 0.f;
         for (int j = 0; j < nt; ++j) {
             const int it = hi * nt + j;
@@ -382,6 +394,121 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
             // (After a failed wait the loads just read stale columns: the loop goes
             // on only to keep meeting the partner warp, and writes nothing.)
             tc::tc_fence_after();
+            float alpha = 1.f;
+            bool rescale = false;
+            uint32_t pk[MOD ? 1 : 32];
+            if constexpr (MOD) {
+                const int kb = (sel_row ? sel_row[first - j] : first - j) * kTile + wg * 64;   // my first key
+                const float dist = (float)(kb - qpos);
+                const int side = kb + 63 <= qtile ? -1 : kb >= qtile + kTile - 1 ? 1 : 0;
+                const bool mask = kb < tr.full_lo || kb + 63 >= tr.full_hi;
+                const bool capped = p.m.cap > 0.f, biased = p.m.slopes != nullptr;
+                // One tile from S to P. `score` turns the raw logits into scores in units of
+                // 1 / ms, in place; `late(r, emit)` hands their pairs to the exponentials
+                // (under a cap with the cap's products, so that the two pipes overlap: the
+                // maximum of capped scores is the capped maximum, `cap_max`). Each kind of
+                // tile has this code to itself: a step that is skipped at run time inside a
+                // common one still costs a move of its 64 registers (28 heads, d 128, 4096
+                // queries on 16384 keys, no cap, no bias: 772 us with a mask step that is
+                // hardly ever taken, 635 us without it). False: `fits` refused the tile,
+                // nothing has happened.
+                auto tile = [&](auto&& fits, auto&& score, auto&& cap_max, auto&& late) -> bool {
+                    uint32_t r0[32], r1[32], pk[32];
+                    tc::tmem_ld32(lane_base + st * 128 + wg * 64, r0);
+                    tc::tmem_ld32(lane_base + st * 128 + wg * 64 + 32, r1);
+                    tc::tmem_wait_ld(r0);
+                    tc::tmem_wait_ld(r1);
+                    if (!fits(r0, r1)) return false;
+                    score(r0, r1);
+                    float mp[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) mp[k] = fmaxf(__uint_as_float(r0[k]), __uint_as_float(r1[k]));
+#pragma unroll
+                    for (int c = 8; c < 32; ++c) mp[c & 7] = max3(mp[c & 7], __uint_as_float(r0[c]), __uint_as_float(r1[c]));
+                    const float part = cap_max(fmaxf(max3(max3(mp[0], mp[1], mp[2]), mp[3], mp[4]), max3(mp[5], mp[6], mp[7])));
+                    // The other warpgroup's half of the row (double-buffered by tile parity:
+                    // a slot is rewritten only after both warps have passed the next barrier).
+                    B.red[st][wg][row] = part;
+                    asm volatile("bar.sync %0, 64;" :: "r"(pair_bar) : "memory");
+                    if (!ok) return true;             // keep meeting the partner warp
+                    const float mx = fmaxf(part, B.red[st][wg ^ 1][row]) * ms;   // log2 units
+                    if (mx > m + kRescaleThreshold) {
+                        alpha = (m == -INFINITY) ? 0.f : fast_exp2(m - mx);
+                        m = mx;
+                        rescale = true;
+                    }
+                    // (A row that has seen nothing yet keeps m = -inf; its weights are 0.)
+                    const float neg_m = m == -INFINITY ? 0.f : -m;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    auto emit = [&](int c, float x0, float x1) {
+                        const float a = fast_exp2(fmaf(x0, ms, neg_m)), b = fast_exp2(fmaf(x1, ms, neg_m));
+                        sum[c & 2] += a;
+                        sum[(c & 2) + 1] += b;
+                        pk[c >> 1] = pack_bf16x2(a, b);
+                    };
+                    late(r0, [&](int c, float x0, float x1) { emit(c, x0, x1); });
+                    late(r1, [&](int c, float x0, float x1) { emit(c + 32, x0, x1); });
+                    lsum = fmaf(lsum, alpha, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+                    // P over the first 32 of the 64 S columns this thread read.
+                    tc::tmem_st32(lane_base + st * 128 + wg * 64, pk);
+                    return true;
+                };
+                auto always = [](const uint32_t (&)[32], const uint32_t (&)[32]) { return true; };
+                auto nothing = [](uint32_t (&)[32], uint32_t (&)[32]) {};
+                auto same = [](float x) { return x; };
+                auto plain = [](const uint32_t (&r)[32], auto&& emit) {
+#pragma unroll
+                    for (int c = 0; c < 32; c += 2) emit(c, __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
+                };
+                auto bias = [&](uint32_t (&r)[32], float pre, float d0, int sd) {
+                    bias_pairs(r, pre, slope2, d0, 1.f, sd, [&](int c, f32x2 y) { put_pair(r, c, y); });
+                };
+                bool done = false;
+                if (!mask && !capped && !biased) {
+                    done = tile(always, nothing, same, plain);
+                } else if (!mask && !capped && side == -1) {
+                    done = tile(always, [&](uint32_t (&r0)[32], uint32_t (&r1)[32]) {
+                        bias(r0, sl2, dist, -1);
+                        bias(r1, sl2, dist + 32.f, -1);
+                    }, same, plain);
+                } else if (!mask && !biased && short_cap) {
+                    // (Once a tile's logits reach beyond the short polynomial, no more trying.)
+                    done = tile([&](const uint32_t (&r0)[32], const uint32_t (&r1)[32]) {
+                        short_cap = warp_top(fmaxf(abs_max(r0), abs_max(r1))) * p.m.k <= kTanhShort;
+                        return short_cap;
+                    }, nothing, [&](float x) {
+                        const float w = x * x;
+                        return x * fmaf(fmaf(fmaf(p.m.a3, w, p.m.a2), w, p.m.a1), w, p.m.a0);
+                    }, [&](const uint32_t (&r)[32], auto&& emit) {
+                        cap_short(r, p.m, [&](int c, f32x2 y) {
+                            float a, b;
+                            unpack2(y, a, b);
+                            emit(c, a, b);
+                        });
+                    });
+                }
+                if (!done)
+                    tile(always, [&](uint32_t (&r0)[32], uint32_t (&r1)[32]) {
+                        if (capped) {
+                            const float top = warp_top(fmaxf(abs_max(r0), abs_max(r1)));
+                            cap_pairs(r0, p.m, top, [&](int c, f32x2 y) { put_pair(r0, c, y); });
+                            cap_pairs(r1, p.m, top, [&](int c, f32x2 y) { put_pair(r1, c, y); });
+                        }
+                        if (biased) {
+                            bias(r0, capped ? 1.f : sl2, dist, side);
+                            bias(r1, capped ? 1.f : sl2, dist + 32.f, side);
+                        }
+                        if (mask) {
+                            const int lo = range.x - kb, hi_ = range.y - kb;
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) {
+                                if (c < lo || c >= hi_) r0[c] = 0xff800000u;
+                                if (c + 32 < lo || c + 32 >= hi_) r1[c] = 0xff800000u;
+                            }
+                        }
+                    }, same, plain);
+                if (!ok) continue;
+            } else {
             float x[64];
             {
                 uint32_t r0[32], r1[32];
@@ -389,38 +516,13 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
                 tc::tmem_ld32(lane_base + st * 128 + wg * 64 + 32, r1);
                 tc::tmem_wait_ld(r0);
                 tc::tmem_wait_ld(r1);
-                if constexpr (MOD) {
-                    const int kb = (sel_row ? sel_row[j] : first + j) * kTile + wg * 64;   // my first key
-                    float pre = sl2;                  // y = pre x, in log2 units
-                    if (p.m.cap > 0.f) {
-                        const float top = warp_top(fmaxf(abs_max(r0), abs_max(r1)));
-                        cap_pairs(r0, p.m, top, [](int, f32x2) {});
-                        cap_pairs(r1, p.m, top, [](int, f32x2) {});
-                        pre = 1.f;
-                    }
-                    if (p.m.slopes) {
-                        const int q0 = (int)(p.q_start + (int64_t)qt * kTile);
-                        const int side = kb + 63 <= q0 ? -1 : kb >= q0 + kTile - 1 ? 1 : 0;
-                        const float d0 = (float)(kb - (int)(p.q_start + q_local));
-                        add_bias(r0, pre, slope2, d0, 1.f, side);
-                        add_bias(r1, pre, slope2, d0 + 32.f, 1.f, side);
-                    }
-                    if (kb < tr.full_lo || kb + 63 >= tr.full_hi) {
-                        const int lo = range.x - kb, hi_ = range.y - kb;
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) {
-                            if (c < lo || c >= hi_) r0[c] = 0xff800000u;
-                            if (c + 32 < lo || c + 32 >= hi_) r1[c] = 0xff800000u;
-                        }
-                    }
-                }
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
                     x[e] = __uint_as_float(r0[e]);
                     x[32 + e] = __uint_as_float(r1[e]);
                 }
             }
-            if (!MOD && j == nt - 1) {                // own page: causal mask (key col > row)
+            if (j == nt - 1) {                        // own page: causal mask (key col > row)
 #pragma unroll
                 for (int c = 0; c < 64; ++c)
                     if (wg * 64 + c > row) x[c] = -INFINITY;
@@ -429,17 +531,8 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
             float mpart[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) mpart[k] = x[k];
-            if constexpr (MOD) {
 #pragma unroll
-                for (int c = 8; c < 56; c += 16)
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) mpart[k] = max3(mpart[k], x[c + k], x[c + 8 + k]);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) mpart[k] = fmaxf(mpart[k], x[56 + k]);
-            } else {
-#pragma unroll
-                for (int c = 8; c < 64; ++c) mpart[c & 7] = fmaxf(mpart[c & 7], x[c]);
-            }
+            for (int c = 8; c < 64; ++c) mpart[c & 7] = fmaxf(mpart[c & 7], x[c]);
 #pragma unroll
             for (int k = 4; k > 0; k >>= 1)
 #pragma unroll
@@ -450,44 +543,23 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
             B.red[st][wg][row] = part;
             asm volatile("bar.sync %0, 64;" :: "r"(pair_bar) : "memory");
             if (!ok) continue;                        // keep meeting the partner warp
-            const float mx = fmaxf(part, B.red[st][wg ^ 1][row]) * ms;   // scaled, log2 units
-            float alpha = 1.f;
-            bool rescale = false;
+            const float mx = fmaxf(part, B.red[st][wg ^ 1][row]) * sl2;   // scaled, log2 units
             if (mx > m + kRescaleThreshold) {
                 alpha = (m == -INFINITY) ? 0.f : fast_exp2(m - mx);
                 m = mx;
                 rescale = true;
             }
-            uint32_t pk[32];
-            // (MOD: a row that has seen nothing yet keeps m = -inf; its weights are 0.)
-            const float neg_m = MOD && m == -INFINITY ? 0.f : -m;
-            if constexpr (MOD) lsum *= alpha;
-            if constexpr (MOD) {
-                const f32x2 ms2 = pack2(ms, ms), nm2 = pack2(neg_m, neg_m);
-                f32x2 sum[2] = {0ull, 0ull};
+            const float neg_m = -m;
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    float p0, p1;
-                    unpack2(fma2(pack2(x[2 * c], x[2 * c + 1]), ms2, nm2), p0, p1);
-                    p0 = fast_exp2(p0);
-                    p1 = fast_exp2(p1);
-                    sum[c & 1] = add2(sum[c & 1], pack2(p0, p1));
-                    pk[c] = pack_bf16x2(p0, p1);
-                }
-                float s0, s1;
-                unpack2(add2(sum[0], sum[1]), s0, s1);
-                lsum += s0 + s1;
-            } else {
-#pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    const float p0 = fast_exp2(fmaf(x[2 * c], sl2, neg_m));
-                    const float p1 = fast_exp2(fmaf(x[2 * c + 1], sl2, neg_m));
-                    pk[c] = pack_bf16x2(p0, p1);
-                }
+            for (int c = 0; c < 32; ++c) {
+                const float p0 = fast_exp2(fmaf(x[2 * c], sl2, neg_m));
+                const float p1 = fast_exp2(fmaf(x[2 * c + 1], sl2, neg_m));
+                pk[c] = pack_bf16x2(p0, p1);
+            }
             }
             if (j > 0 && __any_sync(0xffffffffu, rescale)) {
                 // PV_{j-1} must be done before O is touched (PV_j waits for this tile's P).
-                ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.o_done, (it - 1) & 1, p.err));
+                ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.o_done[st ^ 1], ((it - 1) >> 1) & 1, p.err));
                 if (!ok) continue;
                 tc::tc_fence_after();
                 const float f = rescale ? alpha : 1.f;
@@ -505,17 +577,18 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
                                  __float_as_uint(__uint_as_float(tc::tmem_ld1(lane_base + kColL)) * f));
             }
             // P over the first 32 of the 64 S columns this thread read.
-            tc::tmem_st32(lane_base + st * 128 + wg * 64, pk);
+            if constexpr (!MOD) tc::tmem_st32(lane_base + st * 128 + wg * 64, pk);
             tc::tmem_wait_st();
             tc::tc_fence_before();
-            tc::mbar_arrive(&B.p_full);
+            tc::mbar_arrive(&B.p_full[st]);
         }
         // The next head's Q rows load while this head's last PV and epilogue run.
         // (Loads issued before the tile loop, and left in flight during it, gave
         // nondeterministic O in a few tiles of multi-head CTAs, for a reason not
         // found; issued here, repeated calls are bit-identical.)
         if (hi + 1 < nh) load_q(h + 1);
-        if (ok && nt > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.o_done, (hi * nt + nt - 1) & 1, p.err));
+        const int last = hi * nt + nt - 1;
+        if (ok && nt > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.o_done[last & 1], (last >> 1) & 1, p.err));
         if constexpr (MOD) {
             // Row statistics of both warpgroups meet (every warp passes, error or not).
             B.lsum[wg][row] = lsum;

@@ -154,34 +154,44 @@ template <int N> __device__ __forceinline__ float abs_max(const uint32_t (&x)[N]
     return max3(fmaxf(b[0], b[1]), b[2], b[3]);
 }
 
-// The cap over a row of a tile, in place: raw logits x -> scores y in log2
-// units; use(c, y) sees elements c, c + 1. `top`: the largest |x| of the warp's
-// rows, which picks the form for the whole warp.
-template <int N, typename F>
-__device__ __forceinline__ void cap_pairs(uint32_t (&x)[N], const ModArgs& m, float top, F&& use) {
-    auto put = [&](int c, f32x2 y) {
-        float a, b;
-        unpack2(y, a, b);
-        x[c] = __float_as_uint(a);
-        x[c + 1] = __float_as_uint(b);
-        use(c, y);
-    };
-    auto get = [&](int c) { return pack2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])); };
-    if (top * m.k <= kTanhShort) {
-        const f32x2 a0 = pack2(m.a0, m.a0), a1 = pack2(m.a1, m.a1), a2 = pack2(m.a2, m.a2), a3 = pack2(m.a3, m.a3);
+template <int N> __device__ __forceinline__ f32x2 pair_at(const uint32_t (&x)[N], int c) {
+    return pack2(__uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+}
+template <int N> __device__ __forceinline__ void put_pair(uint32_t (&x)[N], int c, f32x2 v) {
+    float a, b;
+    unpack2(v, a, b);
+    x[c] = __float_as_uint(a);
+    x[c + 1] = __float_as_uint(b);
+}
+template <int N, typename F> __device__ __forceinline__ void each_pair(const uint32_t (&x)[N], F&& use) {
 #pragma unroll
-        for (int c = 0; c < N; c += 2) {
-            const f32x2 v = get(c), w = mul2(v, v);
-            put(c, mul2(v, fma2(fma2(fma2(a3, w, a2), w, a1), w, a0)));
-        }
+    for (int c = 0; c < N; c += 2) use(c, pair_at(x, c));
+}
+
+// The cap over a row of a tile: use(c, y) gets the scores of raw logits x[c],
+// x[c + 1] in log2 units. `top`: the largest |x| of the warp's rows, which picks
+// the form for the whole warp.
+template <int N, typename F>
+__device__ __forceinline__ void cap_short(const uint32_t (&x)[N], const ModArgs& m, F&& use) {
+    const f32x2 a0 = pack2(m.a0, m.a0), a1 = pack2(m.a1, m.a1), a2 = pack2(m.a2, m.a2), a3 = pack2(m.a3, m.a3);
+#pragma unroll
+    for (int c = 0; c < N; c += 2) {
+        const f32x2 v = pair_at(x, c), w = mul2(v, v);
+        use(c, mul2(v, fma2(fma2(fma2(a3, w, a2), w, a1), w, a0)));
+    }
+}
+template <int N, typename F>
+__device__ __forceinline__ void cap_pairs(const uint32_t (&x)[N], const ModArgs& m, float top, F&& use) {
+    if (top * m.k <= kTanhShort) {
+        cap_short(x, m, use);
     } else if (top * m.k <= kTanhLong) {
         const f32x2 k = pack2(m.k, m.k), c2 = pack2(m.c2, m.c2);
 #pragma unroll
-        for (int c = 0; c < N; c += 2) put(c, mul2(tanh_long2(mul2(get(c), k)), c2));
+        for (int c = 0; c < N; c += 2) use(c, mul2(tanh_long2(mul2(pair_at(x, c), k)), c2));
     } else {
 #pragma unroll
         for (int c = 0; c < N; c += 2)
-            put(c, pack2(m.c2 * tanh_any(__uint_as_float(x[c]) * m.k), m.c2 * tanh_any(__uint_as_float(x[c + 1]) * m.k)));
+            use(c, pack2(m.c2 * tanh_any(__uint_as_float(x[c]) * m.k), m.c2 * tanh_any(__uint_as_float(x[c + 1]) * m.k)));
     }
 }
 // Every lane's largest over the warp (of values >= 0; their bits order as integers).
@@ -189,27 +199,25 @@ __device__ __forceinline__ float warp_top(float x) {
     return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
 }
 
-// The distance bias over a row of a tile, in place: x <- x * pre + bias, where
-// element c's key (or query) lies at distance d0 + dir * c from the row's own
-// position. Where the whole tile lies on one side the bias is linear in c (one
-// operation to form it); only tiles across the diagonal need the magnitude.
-template <int N>
-__device__ __forceinline__ void add_bias(uint32_t (&x)[N], float pre, float slope2, float d0, float dir, int side) {
+// The distance bias over a row of a tile: use(c, y) gets x * pre + bias of
+// elements c, c + 1, where element c lies at distance d0 + dir * c from the row's
+// own position. Where the whole tile lies on one side (`side`, the sign of the
+// distance) the bias is linear in c, one operation to form it; tiles across the
+// diagonal (side 0) need the magnitude.
+template <int N, typename F>
+__device__ __forceinline__ void bias_pairs(const uint32_t (&x)[N], float pre, float slope2, float d0, float dir, int side,
+                                           F&& use) {
     const f32x2 pp = pack2(pre, pre);
-    auto run = [&](auto&& bias) {
-#pragma unroll
-        for (int c = 0; c < N; c += 2) {
-            float a, b;
-            unpack2(fma2(pack2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), pp, pack2(bias(c), bias(c + 1))), a, b);
-            x[c] = __float_as_uint(a);
-            x[c + 1] = __float_as_uint(b);
-        }
-    };
-    if (side != 0) {                                  // sign of the distance, the same for all elements
+    if (side != 0) {
         const float base = -slope2 * (float)side * d0, step = -slope2 * (float)side * dir;
-        run([&](int c) { return fmaf(step, (float)c, base); });
+#pragma unroll
+        for (int c = 0; c < N; c += 2)
+            use(c, fma2(pair_at(x, c), pp, pack2(fmaf(step, (float)c, base), fmaf(step, (float)(c + 1), base))));
     } else {
-        run([&](int c) { return -slope2 * fabsf(fmaf(dir, (float)c, d0)); });
+#pragma unroll
+        for (int c = 0; c < N; c += 2)
+            use(c, fma2(pair_at(x, c), pp, pack2(-slope2 * fabsf(fmaf(dir, (float)c, d0)),
+                                                 -slope2 * fabsf(fmaf(dir, (float)(c + 1), d0)))));
     }
 }
 

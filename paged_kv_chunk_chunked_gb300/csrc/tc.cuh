@@ -162,7 +162,7 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
 // ------------------------------------------------------------------ page index stream
 
 // Warp-cooperative stream of physical page indices for a CTA's tiles 0..n-1:
-// tile j reads logical page sel[j] (or first + j when sel is null) through the block
+// tile j reads logical page k = first + step * j (or sel[k]) through the block
 // table. Lane l loads the entry of tile base + l, 32 tiles per coalesced load,
 // one batch ahead, so the block-table reads never sit in front of a TMA
 // issue. Every lane of the warp calls get() with the same j, j = 0, 1, 2, ...
@@ -171,18 +171,20 @@ struct PageBatch {
     const int32_t* sel;
     int n;
     int lane;
-    int first;
+    int first, step;
+    int limit;                // logical pages from here on are bad (a caller's list may hold any)
     int32_t cur, nxt;
 
     __device__ __forceinline__ int32_t load(int base) const {
         const int j = base + lane;
         if (j >= n) return -1;
-        const int32_t lp = sel ? sel[j] : first + j;
-        return lp >= 0 ? bt[lp] : -1;
+        const int k = first + step * j;
+        const int32_t lp = sel ? sel[k] : k;
+        return lp >= 0 && lp < limit ? bt[lp] : -1;
     }
     __device__ __forceinline__ void init(const int32_t* bt_, const int32_t* sel_, int n_, int lane_,
-                                         int first_ = 0) {
-        bt = bt_; sel = sel_; n = n_; lane = lane_; first = first_;
+                                         int first_ = 0, int step_ = 1, int limit_ = 0x7fffffff) {
+        bt = bt_; sel = sel_; n = n_; lane = lane_; first = first_; step = step_; limit = limit_;
         cur = load(0);
         nxt = load(32);
     }

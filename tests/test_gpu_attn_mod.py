@@ -163,6 +163,14 @@ def test_cap_and_bias(dtype, d, P, cap, bias, q_scale, mask):
     Case(dtype, 4, 2, d, P, 133, 140, extra=11, cap=cap, bias=bias, mask=mask, q_scale=q_scale, seed=3).check()
 
 
+@pytest.mark.parametrize("mask", MASKS)
+@pytest.mark.parametrize("kw", [dict(cap=30.0), dict(cap=3.0), dict(bias=True), dict(cap=30.0, bias=True)])
+def test_hidden_and_whole_halves_of_one_tile(kw, mask):
+    """Ranges that end inside a page and inside its halves: tiles whose halves
+    take different ways through the kernels share their rows' statistics."""
+    Case("bf16", 4, 2, 128, 128, 530, 200, extra=100, mask=mask, seed=21, **kw).check()
+
+
 @pytest.mark.parametrize("n", [1, 2, 5, 15, 16, 17, 63, 64, 65, 127, 128, 129, 257])
 @pytest.mark.parametrize("dtype,Hq,Hkv,d,P,q_start", [
     ("bf16", 7, 1, 128, 128, 300), ("bf16", 8, 8, 64, 128, 0), ("f32", 6, 3, 64, 48, 61)])
