@@ -217,6 +217,10 @@ inline size_t attn_part_floats(const AttnArgs& a) {
 }
 // CTAs over one tile's keys that the tensor-core forward wants for a.
 int attn_fwd_tc_splits(const AttnArgs& a);
+// The forward of a few queries against a long cache (bf16).
+bool few_supported(const AttnArgs& a);
+int attn_few_splits(const AttnArgs& a);
+cudaError_t launch_attn_few(const AttnArgs& a, cudaStream_t s);
 // Joins the partial results of a split forward into a.o and a.lse.
 cudaError_t launch_attn_join(const AttnArgs& a, cudaStream_t s);
 

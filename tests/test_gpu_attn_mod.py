@@ -185,6 +185,15 @@ def test_single_tokens_against_long_caches(Hq, Hkv, d, n, q_start, mask):
     Case("bf16", Hq, Hkv, d, 128, q_start, n, cap=50.0, bias=True, mask=mask, seed=9).check()
 
 
+@pytest.mark.parametrize("P", [16, 48, 64])
+@pytest.mark.parametrize("Hq,Hkv,d,n,q_start,mask", [(28, 4, 128, 1, 1500, "causal"), (12, 4, 64, 9, 700, "random"),
+                                                     (5, 1, 128, 16, 403, "docs"), (16, 8, 64, 7, 0, "future"),
+                                                     (40, 2, 64, 2, 900, "pad"), (6, 6, 128, 3, 250, "empty")])
+def test_few_queries_with_other_pages(P, Hq, Hkv, d, n, q_start, mask):
+    """The few-query forward on pages smaller than a step of its keys (the backward on CUDA cores)."""
+    Case("bf16", Hq, Hkv, d, P, q_start, n, extra=30, cap=40.0, bias=True, mask=mask, seed=10, q_scale=3.0).check()
+
+
 @pytest.mark.parametrize("P", [8, 24])
 def test_forward_with_small_pages(P):
     """Pages that are no multiple of 16 tokens: the forward takes them, the backward refuses."""
