@@ -7,9 +7,14 @@
 // 16 keys each of every 128, with online softmax states of their own that meet
 // in shared memory at the end. Shares of the keys meet in attn_join.
 //
-// K and V go from global memory straight to the operand registers of the
-// 16x8x16 bf16 MMA, 16 bytes per load, with no shared memory in between. That
-// works because the order of the products' inner index is free:
+// A page's rows of one KV head are contiguous, so a producer warp streams K and
+// V by untiled bulk copies into a ring of steps of 128 keys (192 KB of it: HBM's
+// latency and rate ask for 45 KB in flight per SM, and registers, at 64 KB, gave
+// 4.5 TB/s where the ring gives ...). The rows keep their order, without padding:
+// the lanes' 16-byte reads then meet two to a bank, 1024 cycles of a step's 2700.
+//
+// The 16x8x16 bf16 MMA takes its operands from 16-byte reads because the order
+// of the products' inner index is free:
 //   S = Q K^T   lane (n = lane / 4, t = lane % 4) holds dims 8t .. 8t + 7 of a
 //               32-dim block of key n: two k-steps' worth of its B operand, if
 //               Q's fragments take the same dims;
@@ -17,10 +22,8 @@
 //               of keys 2t, 2t + 1, 2t + 8, 2t + 9: the B operands of the 8
 //               products whose column v stands for dim 8v + j, j = 0 .. 7, after
 //               pairing neighbouring keys' halves with byte permutes.
-// The tensor core idles mostly (16 rows), so the legacy MMA serves: operands in
-// tensor or shared memory would only add steps. The next 16 keys' 16 loads are
-// in flight while a block is computed: 8 KB per warp, 64 KB per SM, above the
-// 45 KB that HBM's latency and rate ask for per SM.
+// The tensor core idles mostly (16 rows), so the legacy MMA serves: tensor memory
+// would only add steps.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -29,11 +32,12 @@
 #include "common.cuh"
 #include "internal.h"
 #include "mod.cuh"
+#include "tc.cuh"
 
 namespace pkv {
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kWarps = 8, kThreads = 32 * (kWarps + 1);   // and the producer warp
 constexpr int kRows = 16, kKeys = 16;                 // rows of a tile, keys of a warp's block
 constexpr int kStep = kWarps * kKeys;                 // keys of a CTA's step
 
@@ -45,41 +49,21 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// A warp's 16 keys: K of keys lane / 4 and 8 + lane / 4, V of keys 2t, 2t + 1,
-// 2t + 8, 2t + 9.
-template <int D> struct Block {
-    uint4 k[2][D / 32];
-    uint4 v[4][D / 64];
-    int key0;                                         // first key, or -1: no keys (past the share, or a bad page)
+template <int D> struct Ring {
+    static constexpr int kTile = kStep * D * 2;               // K or V of a step, bytes
+    static constexpr int kStages = 96 * 1024 / kTile;         // 3 (d 128) or 6 (d 64)
+    static constexpr int kBytes = 2 * kStages * kTile;
+    static_assert(kBytes >= kWarps * kRows * (D + 4) * 4, "the warps' results fit the ring");
 };
 
 template <int D>
-__device__ __forceinline__ void load_block(Block<D>& b, const AttnArgs& a, int key0, int end, int32_t pp, int kvh, int lane) {
-    b.key0 = -1;
-    if (key0 >= end) return;
-    if (pp < 0 || pp >= a.num_phys) {
-        if (lane == 0) report_error(a.err, kErrBadPage);
-        return;
-    }
-    b.key0 = key0;
-    const size_t base = (((size_t)pp * a.Hkv + kvh) * a.P + key0 % a.P) * D;
-    const uint4* kp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.kpool) + base);
-    const uint4* vp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.vpool) + base);
-    const int g = lane / 4, t = lane % 4;
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) b.k[n][c] = __ldcs(kp + (8 * n + g) * (D / 8) + c * 4 + t);
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) b.v[r][c] = __ldcs(vp + (2 * t + (r & 1) + 8 * (r >> 1)) * (D / 8) + c * 8 + g);
-}
-
-template <int D>
-__global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) few_kernel(AttnArgs a) {
-    extern __shared__ __align__(16) float part[];     // [kWarps][kRows][D + 4]
+__global__ void __launch_bounds__(kThreads, 1) few_kernel(AttnArgs a) {
+    using R = Ring<D>;
+    extern __shared__ __align__(128) uint8_t ring[];  // stages of K, V; then [kWarps][kRows][D + 4] floats
+    float* part = reinterpret_cast<float*>(ring);
     __shared__ float wm[kWarps][kRows], wl[kWarps][kRows];
+    __shared__ uint64_t full[R::kStages], empty[R::kStages];
+    __shared__ int good[R::kStages];                  // the stage's step holds its keys
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     const int kvh = blockIdx.y, group = a.Hq / a.Hkv;
     const int row0 = (int)blockIdx.x * kRows, rows = (int)min64(kRows, a.n_q * group - row0);
@@ -105,16 +89,52 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) few_kernel(AttnArgs
     const int s0 = hi > 0 ? lo / kStep : 0, n = hi > 0 ? (hi + kStep - 1) / kStep - s0 : 0;
     const int b0 = s0 + (int)((int64_t)n * blockIdx.z / gridDim.z), b1 = s0 + (int)((int64_t)n * (blockIdx.z + 1) / gridDim.z);
     const int end = min(hi, b1 * kStep);
-    const int off = warp * kKeys;
+    // The join of the shares may take its place beside these CTAs (it waits for their end).
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (threadIdx.x == 0) {
+        for (int st = 0; st < R::kStages; ++st) {
+            tc::mbar_init(&full[st], 1);
+            tc::mbar_init(&empty[st], kWarps);
+        }
+        tc::fence_barrier_init();
+    }
+    __syncthreads();
 
-    auto page = [&](int step) -> int32_t {
-        const int key = step * kStep + off;
-        return key < end ? a.bt[key / a.P] : -1;
-    };
-    Block<D> x, y;
-    int32_t next = page(b0 + 1);
-    load_block(x, a, b0 * kStep + off, end, page(b0), kvh, lane);
-
+    if (warp == kWarps) {
+        // ------------------------------------------------------------ producer
+        int issued = b0;
+        for (int b = b0; b < b1; ++b) {
+            const int st = (b - b0) % R::kStages, turn = (b - b0) / R::kStages;
+            if (turn > 0 && !tc::warp_wait(&empty[st], (turn - 1) & 1, a.err)) break;
+            // The step's keys in runs that lie in one page, up to a whole block past `end`
+            // (pages are whole blocks): lane l looks up the l-th run's page.
+            const int k0 = b * kStep, k1 = min(k0 + kStep, (end + kKeys - 1) / kKeys * kKeys);
+            const int first = k0 / a.P, runs = (k1 - 1) / a.P - first + 1;       // at most 9 (pages of 16)
+            int32_t pp = -1;
+            if (lane < runs) pp = a.bt[first + lane];
+            const bool ok = __all_sync(0xffffffffu, lane >= runs || (pp >= 0 && pp < a.num_phys));
+            if (lane == 0) {
+                if (!ok) report_error(a.err, kErrBadPage);
+                good[st] = ok;
+                if (ok) tc::mbar_arrive_expect_tx(&full[st], 2u * (uint32_t)(k1 - k0) * D * 2);
+                else tc::mbar_arrive(&full[st]);
+            }
+            __syncwarp();
+            if (ok && lane < runs) {
+                const int from = max(k0, (first + lane) * a.P), to = min(k1, (first + lane + 1) * a.P);
+                const size_t src = (((size_t)pp * a.Hkv + kvh) * a.P + from % a.P) * D;
+                uint8_t* dst = ring + 2 * st * R::kTile + (from - k0) * D * 2;
+                const uint32_t bytes = (uint32_t)(to - from) * D * 2;
+                tc::bulk_load(dst, static_cast<const __nv_bfloat16*>(a.kpool) + src, bytes, &full[st]);
+                tc::bulk_load(dst + R::kTile, static_cast<const __nv_bfloat16*>(a.vpool) + src, bytes, &full[st]);
+            }
+            issued = b + 1;
+        }
+        // None of this CTA's copies may still be landing when it goes on.
+        for (int b = max(b0, issued - R::kStages); b < issued; ++b)
+            tc::drain_wait(&full[(b - b0) % R::kStages], ((b - b0) / R::kStages) & 1);
+    }
+    // ---------------------------------------------------------------- consumers
     uint32_t q[D / 16][4];
 #pragma unroll
     for (int c = 0; c < D / 32; ++c)
@@ -141,8 +161,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) few_kernel(AttnArgs
         for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
     const float sl2 = rsqrtf((float)D) * kLog2e;
 
-    auto compute = [&](const Block<D>& b) {
-        if (b.key0 < 0) return;                       // the same for the whole warp
+    auto compute = [&](int key0, const uint4* ks, const uint4* vs) {
         float s[2][4];
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
@@ -150,8 +169,9 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) few_kernel(AttnArgs
             for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
-                mma16816(s[nt], q[2 * c], b.k[nt][c].x, b.k[nt][c].y);
-                mma16816(s[nt], q[2 * c + 1], b.k[nt][c].z, b.k[nt][c].w);
+                const uint4 k = ks[(8 * nt + g) * (D / 8) + c * 4 + t];
+                mma16816(s[nt], q[2 * c], k.x, k.y);
+                mma16816(s[nt], q[2 * c + 1], k.z, k.w);
             }
         }
         // Element e of tile nt: row g + 8 (e >> 1), key key0 + 8 nt + 2 t + (e & 1).
@@ -176,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) few_kernel(AttnArgs
         float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int u = (e & 3) >> 1, key = b.key0 + 8 * (e >> 2) + 2 * t + (e & 1);
+            const int u = (e & 3) >> 1, key = key0 + 8 * (e >> 2) + 2 * t + (e & 1);
             float& z = s[e >> 2][e & 3];
             if (a.m.slopes) z = fmaf(-slope2[u], fabsf((float)(key - pos[u])), z);
             if (key < range[u].x || key >= range[u].y) z = -INFINITY;
@@ -214,10 +234,13 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) few_kernel(AttnArgs
             }
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
-            const uint32_t* w0 = reinterpret_cast<const uint32_t*>(&b.v[0][c]);
-            const uint32_t* w1 = reinterpret_cast<const uint32_t*>(&b.v[1][c]);
-            const uint32_t* w2 = reinterpret_cast<const uint32_t*>(&b.v[2][c]);
-            const uint32_t* w3 = reinterpret_cast<const uint32_t*>(&b.v[3][c]);
+            uint4 v[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = vs[(2 * t + (r & 1) + 8 * (r >> 1)) * (D / 8) + c * 8 + g];
+            const uint32_t* w0 = reinterpret_cast<const uint32_t*>(&v[0]);
+            const uint32_t* w1 = reinterpret_cast<const uint32_t*>(&v[1]);
+            const uint32_t* w2 = reinterpret_cast<const uint32_t*>(&v[2]);
+            const uint32_t* w3 = reinterpret_cast<const uint32_t*>(&v[3]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const uint32_t sel = j & 1 ? 0x7632 : 0x5410;          // high or low halves of two keys
@@ -226,16 +249,24 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) few_kernel(AttnArgs
             }
         }
     };
-    for (int b = b0; b < b1; b += 2) {
-        load_block(y, a, b + 1 < b1 ? (b + 1) * kStep + off : end, end, next, kvh, lane);
-        next = page(b + 2);
-        compute(x);
-        load_block(x, a, b + 2 < b1 ? (b + 2) * kStep + off : end, end, next, kvh, lane);
-        next = page(b + 3);
-        compute(y);
+    if (warp < kWarps) {
+        bool ok = true;
+        for (int b = b0; ok && b < b1; ++b) {
+            const int st = (b - b0) % R::kStages;
+            ok = tc::warp_wait(&full[st], ((b - b0) / R::kStages) & 1, a.err);
+            const int key0 = b * kStep + warp * kKeys;
+            if (ok && good[st] && key0 < end) {
+                const uint8_t* base = ring + 2 * st * R::kTile + warp * kKeys * D * 2;
+                compute(key0, reinterpret_cast<const uint4*>(base), reinterpret_cast<const uint4*>(base + R::kTile));
+            }
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&empty[st]);
+        }
     }
+    __syncthreads();                                  // the ring is free
 
     // The warps' states meet: row r's maximum, sum and O.
+    if (warp < kWarps)
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
         l[u] += __shfl_xor_sync(0xffffffffu, l[u], 1);
@@ -290,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) few_kernel(AttnArgs
 
 template <int D>
 cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
-    constexpr int smem = kWarps * kRows * (D + 4) * (int)sizeof(float);
+    constexpr int smem = Ring<D>::kBytes;
     cudaError_t e = cudaFuncSetAttribute(few_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const unsigned tiles = (unsigned)((a.n_q * (a.Hq / a.Hkv) + kRows - 1) / kRows);
@@ -314,7 +345,7 @@ int attn_few_splits(const AttnArgs& a) {
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const int64_t ctas = (a.n_q * (a.Hq / a.Hkv) + kRows - 1) / kRows * a.Hkv, steps = (a.m.n_keys + kStep - 1) / kStep;
-    const int64_t room = std::max<int64_t>(1, sms * (a.d == 64 ? 2 : 1) / ctas);
+    const int64_t room = std::max<int64_t>(1, sms / ctas);
     return steps <= 4 ? 1 : (int)std::min<int64_t>({steps, room, 512});
 }
 

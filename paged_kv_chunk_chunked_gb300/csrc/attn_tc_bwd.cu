@@ -722,8 +722,9 @@ bwd_q_tc_kernel(const __grid_constant__ CUtensorMap tm_do, const __grid_constant
     __shared__ QBar B;
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int qt = (int)gridDim.x - 1 - (int)blockIdx.x;        // longest tiles first
-    const int h = blockIdx.y;
+    // Longest tiles first; MOD over all heads, the plain grid within a head.
+    const int qt = MOD ? (int)gridDim.y - 1 - (int)blockIdx.y : (int)gridDim.x - 1 - (int)blockIdx.x;
+    const int h = MOD ? blockIdx.x : blockIdx.y;
     const int kvh = h / (p.Hq / p.Hkv);
     // Key tiles = visible pages (dense: pages 0..own; sparse: the listed pages).
     const int32_t* sel_row = p.sel ? p.sel + ((size_t)qt * p.Hkv + kvh) * p.kmax : nullptr;
@@ -1219,7 +1220,8 @@ static cudaError_t launch_bwd(const AttnArgs& a, cudaStream_t s) {
     p.sel = a.sel; p.kmax = a.kmax; p.m = a.m; p.bounds = a.bounds;
     // The dQ kernel first: it computes D = rowsum(dO * O), which the dK/dV kernel reads.
     {
-        dim3 g_q((unsigned)((a.n_q + 127) / 128), a.Hq);
+        const unsigned tiles = (unsigned)((a.n_q + 127) / 128);
+        const dim3 g_q = MOD ? dim3(a.Hq, tiles) : dim3(tiles, a.Hq);
         ProfScope ps(MOD ? "bwd_q_mod_tc_kernel" : "bwd_q_tc_kernel", s);
         bwd_q_tc_kernel<D, MOD><<<g_q, kThreads, QLayout<D>::kSMEM, s>>>(tdo128, *a.tmap_k, *a.tmap_v, p);
         cudaError_t e = cudaGetLastError();

@@ -182,8 +182,10 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
     __shared__ FwdBarriers B;
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int qt = (int)gridDim.x - 1 - (int)blockIdx.x;        // longest tiles first
-    const int h0 = (int)blockIdx.y * p.heads_per_cta;           // this CTA's first query head
+    // Longest tiles first; MOD over all heads (ranges of packed documents make the
+    // last wave's length count), the plain grid within a head.
+    const int qt = MOD ? (int)gridDim.y - 1 - (int)blockIdx.y : (int)gridDim.x - 1 - (int)blockIdx.x;
+    const int h0 = (int)(MOD ? blockIdx.x : blockIdx.y) * p.heads_per_cta;   // this CTA's first query head
     const int kvh = h0 / (p.Hq / p.Hkv);
     const int nh = p.heads_per_cta;
 
@@ -704,7 +706,8 @@ static cudaError_t launch_fwd(const AttnArgs& a, cudaStream_t s) {
     // group, so its start-up (tensor memory, barriers, pipeline fill) is paid
     // once for the group's g heads instead of once per head.
     p.heads_per_cta = (a.sel && a.kmax <= kShortList) ? a.Hq / a.Hkv : 1;
-    dim3 grid((unsigned)((a.n_q + kTile - 1) / kTile), a.Hq / p.heads_per_cta, splits);
+    const unsigned tiles = (unsigned)((a.n_q + kTile - 1) / kTile), heads = a.Hq / p.heads_per_cta;
+    const dim3 grid = MOD ? dim3(heads, tiles, splits) : dim3(tiles, heads, 1);
     ProfScope ps(MOD ? "fwd_mod_tc_kernel" : "fwd_tc_kernel", s);
     fwd_tc_kernel<D, MOD><<<grid, kThreads, smem, s>>>(*a.tmap_k, *a.tmap_v, p);
     return cudaGetLastError();
