@@ -129,9 +129,9 @@ pkv_status pkv_chunk_attn_mod_bwd(pkv_seq* s, const void* q, const void* o, cons
         cudaStream_t cs = static_cast<cudaStream_t>(stream);
         if (s->used && capturing(cs))
             return fail(PKV_ERR_INVALID, std::string(who) + ": calls on a PINNED_HOST pool cannot be captured");
-        // Scratch: the bounds of the 64-query tiles, D [Hq * n_q] and, with a
-        // selection, the page list and the query-page masks (8-byte aligned).
-        const size_t n_b = 4 * (size_t)((n_q + 63) / 64), n_d = (size_t)a.Hq * n_q;
+        // Scratch: the bounds of the 64-query tiles, the queries' ranges, D [Hq * n_q]
+        // and, with a selection, the page list and the query-page masks (8-byte aligned).
+        const size_t n_b = 4 * (size_t)((n_q + 63) / 64) + 2 * (size_t)n_q, n_d = (size_t)a.Hq * n_q;
         const size_t n_list = sel ? 1 + (size_t)bwd_pagelist_cap(a) : 0;
         const size_t n_mask = sel ? 1 + 2 * (size_t)bwd_selmask_words(a) : 0;
         float* scratch = nullptr;
@@ -139,6 +139,7 @@ pkv_status pkv_chunk_attn_mod_bwd(pkv_seq* s, const void* q, const void* o, cons
         if (st != PKV_OK) return st;
         a.o_in = o; a.dout = dout; a.lse_in = lse; a.dq = dq;
         a.bounds = reinterpret_cast<int4*>(scratch);
+        a.ranges = reinterpret_cast<int2*>(scratch + 4 * (size_t)((n_q + 63) / 64));
         a.Dbuf = scratch + n_b;
         a.pagelist = sel ? reinterpret_cast<int32_t*>(a.Dbuf + n_d) : nullptr;
         a.selmask = sel ? reinterpret_cast<uint64_t*>(

@@ -76,6 +76,7 @@ struct BwdParams {
     int* err;
     ModArgs m;                 // modified scores (MOD kernels)
     int4* bounds;              // MOD: TileRange of each 64-query tile, written by the dQ kernel
+    int2* ranges;              // MOD: each query's visible keys, likewise
 };
 
 // Query pages per chunk the sparse dK/dV kernel lists in shared memory (3
@@ -107,8 +108,8 @@ template <int D> struct KVLayout {
     static constexpr uint32_t kdO = kQ + kv_STAGES * kQStage;
     static constexpr uint32_t kSTAT = kdO + kv_STAGES * kQStage;   // stages x (64 lse*log2e + 64 D) floats
     static constexpr uint32_t kSMEM = kSTAT + kv_STAGES * 512 + 1024;
-    // MOD kernels: and each query's range (64 + 64 ints)
-    static constexpr uint32_t kSMEM_MOD = kSTAT + kv_STAGES * 1024 + 1024;
+    static constexpr uint32_t kRANGE = kSTAT + kv_STAGES * 512;    // MOD: stages x 64 query ranges (masked tiles)
+    static constexpr uint32_t kSMEM_MOD = kSMEM + kv_STAGES * 512;
 };
 // MOD: bit of a listed tile some of whose rows do not see the whole key page.
 constexpr int kTileMasked = 0x4000;
@@ -171,7 +172,6 @@ bwd_kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const int64_t kfirst = (int64_t)j * 128;
     const int n_qt = (int)((p.n_q + 63) / 64);
     const int i0 = kfirst > p.q_start ? (int)((kfirst - p.q_start) / 64) : 0;
-    constexpr int kStat = MOD ? 256 : 128;           // floats of a stage's statistics
     const int32_t pp = p.bt[j];
     const bool page_ok = pp >= 0 && pp < p.num_phys;
 
@@ -326,6 +326,7 @@ bwd_kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         if constexpr (MOD) return (int)B.tiles[u] & (kTileMasked - 1);
         return p.sel ? (int)B.tiles[u] : i0 + u;
     };
+    auto masked = [&](int t) -> bool { return (int)B.tiles[(t_base + t) % n_i] & kTileMasked; };
     auto head_of = [&](int t) -> int { return kvh * g + (t_base + t) / n_i; };
 
     if (!page_ok || T == 0) {
@@ -336,8 +337,7 @@ bwd_kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         // Per-query statistics of tile t (log2e * LSE, +inf past the chunk, and D),
         // two columns per lane; loaded one tile ahead so their latency overlaps
         // the wait for the next free stage.
-        constexpr int NS = MOD ? 8 : 4;
-        auto load_stats = [&](int t, float (&s)[NS]) {
+        auto load_stats = [&](int t, float (&s)[4]) {
             if (t >= T) return;
             const int h = head_of(t);
             const int i = tile_of(t);
@@ -347,16 +347,10 @@ bwd_kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 const bool v = q < p.n_q;
                 s[e] = v ? __ldg(p.lse + (size_t)h * p.n_q + q) * kLog2e : INFINITY;
                 s[2 + e] = v ? __ldg(p.Dbuf + (size_t)h * p.n_q + q) : 0.f;
-                if constexpr (MOD) {
-                    if (s[e] == -INFINITY) s[e] = INFINITY;    // a row that sees nothing: P = 0
-                    const int2 r = v ? row_range(p.m, p.q_start, q) : make_int2(0, 0);
-                    s[4 + e] = __int_as_float(r.x);
-                    s[6 + e] = __int_as_float(r.y);
-                }
             }
         };
         int issued = 0;
-        auto step = [&](int t, const float (&use)[NS], float (&fill)[NS]) -> bool {
+        auto step = [&](int t, const float (&use)[4], float (&fill)[4]) -> bool {
             const int st = t % kv_STAGES;
             if (t >= kv_STAGES &&
                 !__all_sync(0xffffffffu, tc::mbar_wait(&B.qdo_empty[st], ((t / kv_STAGES) - 1) & 1, p.err)))
@@ -374,26 +368,91 @@ bwd_kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 }
             }
             load_stats(t + 1, fill);
-            float* sst = stat + st * kStat;
+            float* sst = stat + st * 128;
             sst[lane * 2] = use[0];
             sst[lane * 2 + 1] = use[1];
             sst[64 + lane * 2] = use[2];
             sst[64 + lane * 2 + 1] = use[3];
-            if constexpr (MOD) {
-                sst[128 + lane * 2] = use[4];
-                sst[128 + lane * 2 + 1] = use[5];
-                sst[192 + lane * 2] = use[6];
-                sst[192 + lane * 2 + 1] = use[7];
-            }
             tc::mbar_arrive(&B.qdo_full[st]);           // 32 arrivals + the tx bytes
             issued = t + 1;
             return true;
         };
-        float sa[NS], sb[NS];
-        load_stats(0, sa);
-        for (int t = 0; t < T; t += 2) {
-            if (!step(t, sa, sb)) break;
-            if (t + 1 < T && !step(t + 1, sb, sa)) break;
+        // MOD: the same with the tiles' list, and with the queries' ranges where a tile
+        // needs them. Only one of the four stages is free ahead of the tensor core's
+        // three, so whatever stands between a stage's release and its copies shows in the
+        // kernel's time: the next tile is looked up before the wait, and a tile's values
+        // stay as loaded until they are stored (28 heads, 4096 queries on 16384 keys:
+        // 1500 us with the arithmetic at the loads, ... us so).
+        struct Stats {
+            float lse[2], d[2];
+            int2 range[2];
+            int tile, h;
+            bool mask;
+        };
+        auto look_up = [&](int t, Stats& x) {
+            const int u = (t_base + t) % n_i, e = (int)B.tiles[u];
+            x.tile = e & (kTileMasked - 1);
+            x.mask = (e & kTileMasked) != 0;
+            x.h = head_of(t);
+        };
+        auto fetch = [&](Stats& x) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int64_t q = (int64_t)x.tile * 64 + lane * 2 + e;
+                x.lse[e] = INFINITY;
+                x.d[e] = 0.f;
+                x.range[e] = make_int2(0, 0);
+                if (q < p.n_q) {
+                    x.lse[e] = __ldg(p.lse + (size_t)x.h * p.n_q + q);
+                    x.d[e] = __ldg(p.Dbuf + (size_t)x.h * p.n_q + q);
+                    if (x.mask) x.range[e] = __ldg(p.ranges + q);
+                }
+            }
+        };
+        auto mod_step = [&](int t, const Stats& use, Stats& fill) -> bool {
+            const int st = t % kv_STAGES;
+            if (t + 1 < T) look_up(t + 1, fill);
+            if (t >= kv_STAGES &&
+                !__all_sync(0xffffffffu, tc::mbar_wait(&B.qdo_empty[st], ((t / kv_STAGES) - 1) & 1, p.err)))
+                return false;
+            if (lane == 0) {
+                uint8_t* q_dst = smem + kv_Q + st * kQS;
+                uint8_t* do_dst = smem + kv_dO + st * kQS;
+                tc::mbar_expect_tx(&B.qdo_full[st], 2 * kQS);
+#pragma unroll
+                for (int b = 0; b < D / 64; ++b) {
+                    tc::tma_load_3d(q_dst + b * 8 * KB, &tm_q, &B.qdo_full[st], 64 * b, use.h, use.tile * 64);
+                    tc::tma_load_3d(do_dst + b * 8 * KB, &tm_do, &B.qdo_full[st], 64 * b, use.h, use.tile * 64);
+                }
+            }
+            __syncwarp();
+            if (t + 1 < T) fetch(fill);
+            float* sst = stat + st * 128;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {                // negated, as addends; a row that sees nothing: P = 0
+                sst[lane * 2 + e] = use.lse[e] == -INFINITY ? -INFINITY : -use.lse[e] * kLog2e;
+                sst[64 + lane * 2 + e] = -use.d[e];
+                if (use.mask) reinterpret_cast<int2*>(smem + L::kRANGE)[st * 64 + lane * 2 + e] = use.range[e];
+            }
+            tc::mbar_arrive(&B.qdo_full[st]);            // 32 arrivals + the tx bytes
+            issued = t + 1;
+            return true;
+        };
+        if constexpr (MOD) {
+            Stats xa, xb;
+            look_up(0, xa);
+            fetch(xa);
+            for (int t = 0; t < T; t += 2) {
+                if (!mod_step(t, xa, xb)) break;
+                if (t + 1 < T && !mod_step(t + 1, xb, xa)) break;
+            }
+        } else {
+            float sa[4], sb[4];
+            load_stats(0, sa);
+            for (int t = 0; t < T; t += 2) {
+                if (!step(t, sa, sb)) break;
+                if (t + 1 < T && !step(t + 1, sb, sa)) break;
+            }
         }
         if (lane == 0) {
             drain_wait(&B.kv_full, 0);
@@ -503,7 +562,7 @@ bwd_kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             tc::tc_fence_after();
             const int i = tile_of(t);
             const int64_t q0 = p.q_start + (int64_t)i * 64 + wg * 32;   // position of my column 0
-            const float* sst = stat + st * kStat + wg * 32;
+            const float* sst = stat + st * 128 + wg * 32;
             uint32_t sv[32], dv[32];
             tc::tmem_ld32(lane_base + kv_TS + wg * 32, sv);
             tc::tmem_ld32(lane_base + kv_TDP + wg * 32, dv);
@@ -534,19 +593,19 @@ bwd_kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if constexpr (MOD) {
                 // Columns c, c + 1: weights P = 2^(pre v - LSE) and dS = P (dP - D) f, f the
                 // cap's derivative 1 - tanh^2 = 1 - (y / c2)^2. The cap's products and the
-                // exponentials go through one pass, so that the two pipes overlap.
+                // exponentials go through one pass, so that the two pipes overlap. (-LSE and
+                // -D of four columns per 16-byte broadcast read.)
                 const bool capped = p.m.cap > 0.f;
-                const f32x2 neg = pack2(-1.f, -1.f), one = pack2(1.f, 1.f), nc = pack2(p.m.neg_c2sq, p.m.neg_c2sq);
-                const float2* l2 = reinterpret_cast<const float2*>(sst);
-                const float2* dd2 = reinterpret_cast<const float2*>(sst + 64);
+                const f32x2 one = pack2(1.f, 1.f), nc = pack2(p.m.neg_c2sq, p.m.neg_c2sq);
+                float4 nl, nd;
                 auto grad = [&](int c) {                         // dP - D
-                    const float2 d = dd2[c / 2];
-                    return fma2(pack2(d.x, d.y), neg, pair_at(dv, c));
+                    if ((c & 3) == 0) nd = d4[c / 4];
+                    return add2(c & 2 ? pack2(nd.z, nd.w) : pack2(nd.x, nd.y), pair_at(dv, c));
                 };
                 auto emit = [&](int c, f32x2 v, f32x2 pre2, f32x2 g) {
-                    const float2 l = l2[c / 2];
+                    if ((c & 3) == 0) nl = l4[c / 4];
                     float a, b;
-                    unpack2(fma2(v, pre2, pack2(-l.x, -l.y)), a, b);
+                    unpack2(fma2(v, pre2, c & 2 ? pack2(nl.z, nl.w) : pack2(nl.x, nl.y)), a, b);
                     a = fast_exp2(a);
                     b = fast_exp2(b);
                     pw[c / 2] = pack_bf16x2(a, b);
@@ -558,7 +617,7 @@ bwd_kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 const float d0 = (float)((int)kpos - (int)q0);
                 const float slope2 = p.m.slopes ? __ldg(p.m.slopes + head_of(t)) * kLog2e : 0.f;
                 const f32x2 sl22 = pack2(sl2, sl2);
-                const bool mask = (int)B.tiles[(t_base + t) % n_i] & kTileMasked;
+                const bool mask = masked(t);
                 if (mask || (capped && p.m.slopes)) {
                     float pre = sl2;                             // score in log2 units: pre x
                     if (capped) {
@@ -577,18 +636,18 @@ bwd_kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     }
                     if (mask) {
                         // Hidden: score -inf, and nothing of the gradient factor (it may not be finite).
-                        const int4* lo4 = reinterpret_cast<const int4*>(sst + 128);
-                        const int4* hi4 = reinterpret_cast<const int4*>(sst + 192);
+                        const int4* r2 = reinterpret_cast<const int4*>(smem + L::kRANGE) + st * 32 + wg * 16;
 #pragma unroll
-                        for (int c = 0; c < 32; c += 4) {
-                            const int4 a = lo4[c / 4], b = hi4[c / 4];
-                            const int lo[4] = {a.x, a.y, a.z, a.w}, hi[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if ((int)kpos < lo[e] || (int)kpos >= hi[e]) {
-                                    sv[c + e] = 0xff800000u;
-                                    dv[c + e] = 0u;
-                                }
+                        for (int c = 0; c < 32; c += 2) {
+                            const int4 r = r2[c / 2];
+                            if ((int)kpos < r.x || (int)kpos >= r.y) {
+                                sv[c] = 0xff800000u;
+                                dv[c] = 0u;
+                            }
+                            if ((int)kpos < r.z || (int)kpos >= r.w) {
+                                sv[c + 1] = 0xff800000u;
+                                dv[c + 1] = 0u;
+                            }
                         }
                     }
                     const f32x2 pre2 = pack2(pre, pre);
@@ -912,6 +971,7 @@ bwd_q_tc_kernel(const __grid_constant__ CUtensorMap tm_do, const __grid_constant
         if constexpr (MOD) {
             if (lse2 == -INFINITY) lse2 = INFINITY;              // the row sees nothing: P = 0
             if (valid) range = row_range(p.m, p.q_start, q_local);
+            if (valid && h == 0 && wg == 0) p.ranges[q_local] = range;      // for the dK/dV kernel
             slope2 = p.m.slopes ? __ldg(p.m.slopes + h) * kLog2e : 0.f;
         }
         const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
@@ -1217,7 +1277,7 @@ static cudaError_t launch_bwd(const AttnArgs& a, cudaStream_t s) {
     p.lse = a.lse_in; p.Dbuf = a.Dbuf; p.dq = a.dq; p.dkpool = a.dkpool; p.dvpool = a.dvpool;
     p.o = a.o_in;
     p.bt = a.bt; p.num_phys = a.num_phys; p.err = a.err;
-    p.sel = a.sel; p.kmax = a.kmax; p.m = a.m; p.bounds = a.bounds;
+    p.sel = a.sel; p.kmax = a.kmax; p.m = a.m; p.bounds = a.bounds; p.ranges = a.ranges;
     // The dQ kernel first: it computes D = rowsum(dO * O), which the dK/dV kernel reads.
     {
         const unsigned tiles = (unsigned)((a.n_q + 127) / 128);

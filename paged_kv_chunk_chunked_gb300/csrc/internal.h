@@ -209,6 +209,7 @@ struct AttnArgs {
     int splits;                      // forward: CTAs over one tile's keys
     float* part;                     // forward scratch with splits > 1: [attn_part_floats(a)]
     int4* bounds;                    // bwd scratch: TileRange of each 64-query tile
+    int2* ranges;                    // bwd scratch: each query's visible keys [n_q]
 };
 // Floats of the split forward's partial results: O [splits, Hq, n_q, d], then
 // LSE (log2 units) [splits, Hq, n_q].
