@@ -111,6 +111,7 @@ template <int D> struct KVLayout {
     static constexpr uint32_t kRANGE = kSTAT + kv_STAGES * 512;    // MOD: stages x 64 query ranges (masked tiles)
     static constexpr uint32_t kSMEM_MOD = kSMEM + kv_STAGES * 512;
 };
+constexpr int kMaxSplits = 8;            // CTAs of a page at most: each adds the page's gradients once
 // MOD: bit of a listed tile some of whose rows do not see the whole key page.
 constexpr int kTileMasked = 0x4000;
 // Tensor-memory columns: S^T, dP^T (64 fp32 each), P^T, dS^T (64 bf16 = 32
@@ -155,7 +156,7 @@ bwd_kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     // than in DRAM. Sparse: grid (KV head, position in the chunk's selection
     // union) -- the union's CTAs are dispatched first, those past its end exit
     // at once.
-    const int n_split = (int)p.kv_splits;
+    int n_split = (int)p.kv_splits;
     int j, split, kvh;
     if (p.pagelist) {
         const int idx = (int)blockIdx.y;
@@ -164,7 +165,27 @@ bwd_kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         split = 0;
         kvh = (int)blockIdx.x;
     } else {
-        j = (int)blockIdx.x / n_split;               // logical key page
+        int first = 0;
+        if (MOD && !p.sel && (p.m.k_begin || p.m.k_end)) {
+            // The pages between the chunk's first and last visible key share the grid
+            // (more CTAs to a page where documents leave few pages); the rest of it exits.
+            int lo = 0x7fffffff, hi = 0;
+            for (int t = lane; t < (int)((p.n_q + 63) / 64); t += 32) {
+                const int4 b = p.bounds[t];
+                if (b.y > 0) {
+                    lo = min(lo, b.x);
+                    hi = max(hi, b.y);
+                }
+            }
+            lo = __reduce_min_sync(0xffffffffu, lo);
+            hi = __reduce_max_sync(0xffffffffu, hi);
+            first = hi > 0 ? lo / 128 : 0;
+            const int pages = (hi + 127) / 128 - first;
+            if (pages <= 0) return;                  // the whole CTA, before any barrier
+            n_split = min(kMaxSplits, max(1, (int)gridDim.x / pages));
+            if ((int)blockIdx.x >= pages * n_split) return;
+        }
+        j = first + (int)blockIdx.x / n_split;       // logical key page
         split = (int)blockIdx.x % n_split;
         kvh = (int)blockIdx.y;
     }
