@@ -99,12 +99,12 @@ pkv_status pkv_chunk_attn_mod_fwd(pkv_seq* s, const void* q, int64_t q_start, in
         a.o = o;
         a.lse = lse;
         const bool few = !(s->pool->desc.flags & PKV_FLAG_SIMT_ONLY) && few_supported(a), tc = use_tc(s->pool, a);
-        a.splits = few ? attn_few_splits(a) : tc ? attn_fwd_tc_splits(a) : attn_fwd_mod_simt_splits(a);
+        a.splits = few ? attn_few_splits(a) : tc ? attn_fwd_mod_tc_splits(a) : attn_fwd_mod_simt_splits(a);
         if (a.splits > 1) {
             st = seq_scratch(s, attn_part_floats(a), cs, &a.part, who);
             if (st != PKV_OK) return st;
         }
-        cudaError_t e = few ? launch_attn_few(a, cs) : tc ? launch_attn_fwd_tc(a, cs) : launch_attn_fwd_mod_simt(a, cs);
+        cudaError_t e = few ? launch_attn_few(a, cs) : tc ? launch_attn_fwd_mod_tc(a, cs) : launch_attn_fwd_mod_simt(a, cs);
         if (e == cudaSuccess && a.splits > 1) e = launch_attn_join(a, cs);
         if (e == cudaSuccess && s->used) e = cudaEventRecord(s->used, cs);
         return e == cudaSuccess ? PKV_OK : cuda_fail(e, "pkv_chunk_attn_mod_fwd: launch");

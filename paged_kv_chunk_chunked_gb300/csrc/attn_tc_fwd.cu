@@ -37,11 +37,8 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
-#include <algorithm>
-
 #include "common.cuh"
 #include "internal.h"
-#include "mod.cuh"
 #include "tc.cuh"
 
 namespace pkv {
@@ -83,8 +80,6 @@ struct FwdParams {
     const int32_t* sel;
     int kmax;
     int* err;
-    ModArgs m;                       // modified scores (MOD kernels)
-    float* part;                     // MOD, split: partial results (attn_part_floats), else null
 };
 
 struct __align__(8) FwdBarriers {
@@ -94,15 +89,14 @@ struct __align__(8) FwdBarriers {
     uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
     uint64_t s_full[2];
     // By tile parity, like s_full: a warp may be a tile ahead of another (which rescales
-    // O, or repeats its pass), and neither its arrival for the next tile nor a wait for
-    // the last PV may fall into the phase of the tile before.
+    // O), and neither its arrival for the next tile nor a wait for the last PV may fall
+    // into the phase of the tile before.
     uint64_t p_full[2];
     uint64_t o_done[2];
     uint64_t drain;
     uint32_t tmem_base;
     int n_tiles;
     float red[2][2][kTile];          // [parity][warpgroup][row]
-    float lsum[2][kTile];            // MOD: [warpgroup][row] sums of the unrounded weights
 };
 
 
@@ -117,9 +111,8 @@ using tc::drain_wait;
 // the copies. A K load never waits behind a V stage in use.
 template <int D>
 __device__ __forceinline__ void produce_ring(const FwdParams& p, uint8_t* smem, FwdBarriers& B,
-                                             const CUtensorMap& tmap, bool is_k, int kvh, const int32_t* sel_row,
-                                             int first, int step, int limit, int nt, int lane,
-                                             tc::PageBatch& pages) {
+                                             const CUtensorMap& tmap, bool is_k, int qt, int kvh,
+                                             int nt, int lane, tc::PageBatch& pages) {
     using L = FwdLayout<D>;
     const int nst = is_k ? kKStages : kVStages;
     uint64_t* full = is_k ? B.k_full : B.v_full;
@@ -131,7 +124,7 @@ __device__ __forceinline__ void produce_ring(const FwdParams& p, uint8_t* smem, 
     int issued = 0;
     bool ok = true;
     for (int hi = 0; ok && hi < p.heads_per_cta; ++hi) {
-        if (hi > 0) pages.init(p.bt, sel_row, nt, lane, first, step, limit);
+        if (hi > 0) pages.init(p.bt, p.sel ? p.sel + ((size_t)qt * p.Hkv + kvh) * p.kmax : nullptr, nt, lane);
         for (int j = 0; j < nt; ++j) {
             const int it = hi * nt + j;
             const int st = it % nst;
@@ -162,13 +155,7 @@ __device__ __forceinline__ void produce_ring(const FwdParams& p, uint8_t* smem, 
         for (int j = max(0, issued - nst); j < issued; ++j) drain_wait(&full[j % nst], (j / nst) & 1);
 }
 
-// MOD: modified scores (a cap, a distance bias, a key range per query, see
-// mod.cuh). The tile's pages are those its rows' ranges touch, each element is
-// masked by its own row's range where a tile is not wholly inside all of them,
-// gridDim.z CTAs may share a tile's pages (partial results joined afterwards),
-// and the LSE comes from an fp32 sum of the unrounded weights, exact enough to
-// recompute P from (the plain kernel takes the bf16-weight sum O is divided by).
-template <int D, bool MOD>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
               FwdParams p) {
@@ -182,10 +169,8 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
     __shared__ FwdBarriers B;
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    // Longest tiles first; MOD over all heads (ranges of packed documents make the
-    // last wave's length count), the plain grid within a head.
-    const int qt = MOD ? (int)gridDim.y - 1 - (int)blockIdx.y : (int)gridDim.x - 1 - (int)blockIdx.x;
-    const int h0 = (int)(MOD ? blockIdx.x : blockIdx.y) * p.heads_per_cta;   // this CTA's first query head
+    const int qt = (int)gridDim.x - 1 - (int)blockIdx.x;        // longest tiles first
+    const int h0 = (int)blockIdx.y * p.heads_per_cta;           // this CTA's first query head
     const int kvh = h0 / (p.Hq / p.Hkv);
     const int nh = p.heads_per_cta;
 
@@ -204,23 +189,7 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
     const int32_t* sel_row = p.sel ? p.sel + ((size_t)qt * p.Hkv + kvh) * p.kmax : nullptr;
     tc::PageBatch pages;
     int n_pre = 0;
-    TileRange tr{};
-    // Tile j is entry first + step * j of the page list (dense: that page). MOD walks
-    // back from the last page: the distance bias lets the maximum grow towards the
-    // query's own position, and each growth costs a rescaling.
-    int first = 0, step = 1;
-    const int limit = MOD ? (int)((p.m.n_keys + kTile - 1) / kTile) : 0x7fffffff;
-    if constexpr (MOD) {
-        tr = tile_range<kTile>(p.m, p.q_start, (int64_t)qt * kTile, p.n_q, lane);
-        const int p0 = tr.lo / kTile;
-        int n = sel_row ? sel_count_warp(sel_row, p.kmax, lane) : tr.hi > 0 ? (tr.hi + kTile - 1) / kTile - p0 : 0;
-        // This CTA's share of the tile's pages.
-        const int s0 = (int)((int64_t)n * blockIdx.z / gridDim.z), s1 = (int)((int64_t)n * (blockIdx.z + 1) / gridDim.z);
-        n_pre = s1 - s0;
-        first = (sel_row ? 0 : p0) + s1 - 1;
-        step = -1;
-        if (warp == 0 || warp == kThreads / 32 - 1) pages.init(p.bt, sel_row, n_pre, lane, first, step, limit);
-    } else if (warp == 0 || warp == kThreads / 32 - 1) {
+    if (warp == 0 || warp == kThreads / 32 - 1) {
         n_pre = sel_row ? sel_count_warp(sel_row, p.kmax, lane) : (int)(p.q_start / kTile) + qt + 1;
         pages.init(p.bt, sel_row, n_pre, lane);
     }
@@ -279,10 +248,10 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
 
     if (warp == 0) {
         // ------------------------------------------------------------ K producer
-        produce_ring<D>(p, smem, B, tmap_k, true, kvh, sel_row, first, step, limit, nt, lane, pages);
+        produce_ring<D>(p, smem, B, tmap_k, true, qt, kvh, nt, lane, pages);
     } else if (warp == kThreads / 32 - 1) {
         // ------------------------------------------------------------ V producer
-        produce_ring<D>(p, smem, B, tmap_v, false, kvh, sel_row, first, step, limit, nt, lane, pages);
+        produce_ring<D>(p, smem, B, tmap_v, false, qt, kvh, nt, lane, pages);
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         // The whole warp runs the loop (warp-uniform descriptors); one elected
@@ -359,16 +328,9 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
         const int quad = warp & 3;                    // TMEM lane quadrant of this warp
         const int row = quad * 32 + lane;             // query row within the tile
         const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
-        // Scores x leave the tile loop's head in units of 1 / ms log2: raw logits
-        // times sl2, or (MOD) already scaled by the cap or the bias.
         const float sl2 = rsqrtf((float)D) * kLog2e;
         const int64_t q_local = (int64_t)qt * kTile + row;
         const bool valid = q_local < p.n_q;
-        int2 range = make_int2(0, 0);
-        if constexpr (MOD) {
-            if (valid) range = row_range(p.m, p.q_start, q_local);
-        }
-        const float ms = MOD && (p.m.cap > 0.f || p.m.slopes) ? 1.f : sl2;
         bool ok = true;
         // Named barrier of the two warps (one per warpgroup) that own rows 32 quad ..
         const uint32_t pair_bar = 1 + quad;
@@ -384,10 +346,7 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
             tc::tc_fence_before();
         }
         tc::mbar_arrive(&B.q_full);
-        float m = -INFINITY, lsum = 0.f;
-        bool short_cap = MOD && p.m.cap > 0.f;
-        const int qtile = (int)(p.q_start + (int64_t)qt * kTile), qpos = qtile + row;
-        const float slope2 = MOD && p.m.slopes ? p.m.slopes[h] * kLog2e : 0.f;
+        float m = -INFINITY;
         for (int j = 0; j < nt; ++j) {
             const int it = hi * nt + j;
             const int st = it & 1;
@@ -396,121 +355,6 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
             // (After a failed wait the loads just read stale columns: the loop goes
             // on only to keep meeting the partner warp, and writes nothing.)
             tc::tc_fence_after();
-            float alpha = 1.f;
-            bool rescale = false;
-            uint32_t pk[MOD ? 1 : 32];
-            if constexpr (MOD) {
-                const int kb = (sel_row ? sel_row[first - j] : first - j) * kTile + wg * 64;   // my first key
-                const float dist = (float)(kb - qpos);
-                const int side = kb + 63 <= qtile ? -1 : kb >= qtile + kTile - 1 ? 1 : 0;
-                const bool mask = kb < tr.full_lo || kb + 63 >= tr.full_hi;
-                const bool capped = p.m.cap > 0.f, biased = p.m.slopes != nullptr;
-                // One tile from S to P. `score` turns the raw logits into scores in units of
-                // 1 / ms, in place; `late(r, emit)` hands their pairs to the exponentials
-                // (under a cap with the cap's products, so that the two pipes overlap: the
-                // maximum of capped scores is the capped maximum, `cap_max`). Each kind of
-                // tile has this code to itself: a step that is skipped at run time inside a
-                // common one still costs a move of its 64 registers (28 heads, d 128, 4096
-                // queries on 16384 keys, no cap, no bias: 772 us with a mask step that is
-                // hardly ever taken, 635 us without it). False: `fits` refused the tile,
-                // nothing has happened.
-                auto tile = [&](auto&& fits, auto&& score, auto&& cap_max, auto&& late) -> bool {
-                    uint32_t r0[32], r1[32], pk[32];
-                    tc::tmem_ld32(lane_base + st * 128 + wg * 64, r0);
-                    tc::tmem_ld32(lane_base + st * 128 + wg * 64 + 32, r1);
-                    tc::tmem_wait_ld(r0);
-                    tc::tmem_wait_ld(r1);
-                    if (!fits(r0, r1)) return false;
-                    score(r0, r1);
-                    float mp[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) mp[k] = fmaxf(__uint_as_float(r0[k]), __uint_as_float(r1[k]));
-#pragma unroll
-                    for (int c = 8; c < 32; ++c) mp[c & 7] = max3(mp[c & 7], __uint_as_float(r0[c]), __uint_as_float(r1[c]));
-                    const float part = cap_max(fmaxf(max3(max3(mp[0], mp[1], mp[2]), mp[3], mp[4]), max3(mp[5], mp[6], mp[7])));
-                    // The other warpgroup's half of the row (double-buffered by tile parity:
-                    // a slot is rewritten only after both warps have passed the next barrier).
-                    B.red[st][wg][row] = part;
-                    asm volatile("bar.sync %0, 64;" :: "r"(pair_bar) : "memory");
-                    if (!ok) return true;             // keep meeting the partner warp
-                    const float mx = fmaxf(part, B.red[st][wg ^ 1][row]) * ms;   // log2 units
-                    if (mx > m + kRescaleThreshold) {
-                        alpha = (m == -INFINITY) ? 0.f : fast_exp2(m - mx);
-                        m = mx;
-                        rescale = true;
-                    }
-                    // (A row that has seen nothing yet keeps m = -inf; its weights are 0.)
-                    const float neg_m = m == -INFINITY ? 0.f : -m;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                    auto emit = [&](int c, float x0, float x1) {
-                        const float a = fast_exp2(fmaf(x0, ms, neg_m)), b = fast_exp2(fmaf(x1, ms, neg_m));
-                        sum[c & 2] += a;
-                        sum[(c & 2) + 1] += b;
-                        pk[c >> 1] = pack_bf16x2(a, b);
-                    };
-                    late(r0, [&](int c, float x0, float x1) { emit(c, x0, x1); });
-                    late(r1, [&](int c, float x0, float x1) { emit(c + 32, x0, x1); });
-                    lsum = fmaf(lsum, alpha, (sum[0] + sum[1]) + (sum[2] + sum[3]));
-                    // P over the first 32 of the 64 S columns this thread read.
-                    tc::tmem_st32(lane_base + st * 128 + wg * 64, pk);
-                    return true;
-                };
-                auto always = [](const uint32_t (&)[32], const uint32_t (&)[32]) { return true; };
-                auto nothing = [](uint32_t (&)[32], uint32_t (&)[32]) {};
-                auto same = [](float x) { return x; };
-                auto plain = [](const uint32_t (&r)[32], auto&& emit) {
-#pragma unroll
-                    for (int c = 0; c < 32; c += 2) emit(c, __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
-                };
-                auto bias = [&](uint32_t (&r)[32], float pre, float d0, int sd) {
-                    bias_pairs(r, pre, slope2, d0, 1.f, sd, [&](int c, f32x2 y) { put_pair(r, c, y); });
-                };
-                bool done = false;
-                if (!mask && !capped && !biased) {
-                    done = tile(always, nothing, same, plain);
-                } else if (!mask && !capped && side == -1) {
-                    done = tile(always, [&](uint32_t (&r0)[32], uint32_t (&r1)[32]) {
-                        bias(r0, sl2, dist, -1);
-                        bias(r1, sl2, dist + 32.f, -1);
-                    }, same, plain);
-                } else if (!mask && !biased && short_cap) {
-                    // (Once a tile's logits reach beyond the short polynomial, no more trying.)
-                    done = tile([&](const uint32_t (&r0)[32], const uint32_t (&r1)[32]) {
-                        short_cap = warp_top(fmaxf(abs_max(r0), abs_max(r1))) * p.m.k <= kTanhShort;
-                        return short_cap;
-                    }, nothing, [&](float x) {
-                        const float w = x * x;
-                        return x * fmaf(fmaf(fmaf(p.m.a3, w, p.m.a2), w, p.m.a1), w, p.m.a0);
-                    }, [&](const uint32_t (&r)[32], auto&& emit) {
-                        cap_short(r, p.m, [&](int c, f32x2 y) {
-                            float a, b;
-                            unpack2(y, a, b);
-                            emit(c, a, b);
-                        });
-                    });
-                }
-                if (!done)
-                    tile(always, [&](uint32_t (&r0)[32], uint32_t (&r1)[32]) {
-                        if (capped) {
-                            const float top = warp_top(fmaxf(abs_max(r0), abs_max(r1)));
-                            cap_pairs(r0, p.m, top, [&](int c, f32x2 y) { put_pair(r0, c, y); });
-                            cap_pairs(r1, p.m, top, [&](int c, f32x2 y) { put_pair(r1, c, y); });
-                        }
-                        if (biased) {
-                            bias(r0, capped ? 1.f : sl2, dist, side);
-                            bias(r1, capped ? 1.f : sl2, dist + 32.f, side);
-                        }
-                        if (mask) {
-                            const int lo = range.x - kb, hi_ = range.y - kb;
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) {
-                                if (c < lo || c >= hi_) r0[c] = 0xff800000u;
-                                if (c + 32 < lo || c + 32 >= hi_) r1[c] = 0xff800000u;
-                            }
-                        }
-                    }, same, plain);
-                if (!ok) continue;
-            } else {
             float x[64];
             {
                 uint32_t r0[32], r1[32];
@@ -546,18 +390,20 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
             asm volatile("bar.sync %0, 64;" :: "r"(pair_bar) : "memory");
             if (!ok) continue;                        // keep meeting the partner warp
             const float mx = fmaxf(part, B.red[st][wg ^ 1][row]) * sl2;   // scaled, log2 units
+            float alpha = 1.f;
+            bool rescale = false;
             if (mx > m + kRescaleThreshold) {
                 alpha = (m == -INFINITY) ? 0.f : fast_exp2(m - mx);
                 m = mx;
                 rescale = true;
             }
+            uint32_t pk[32];
             const float neg_m = -m;
 #pragma unroll
             for (int c = 0; c < 32; ++c) {
                 const float p0 = fast_exp2(fmaf(x[2 * c], sl2, neg_m));
                 const float p1 = fast_exp2(fmaf(x[2 * c + 1], sl2, neg_m));
                 pk[c] = pack_bf16x2(p0, p1);
-            }
             }
             if (j > 0 && __any_sync(0xffffffffu, rescale)) {
                 // PV_{j-1} must be done before O is touched (PV_j waits for this tile's P).
@@ -579,7 +425,7 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
                                  __float_as_uint(__uint_as_float(tc::tmem_ld1(lane_base + kColL)) * f));
             }
             // P over the first 32 of the 64 S columns this thread read.
-            if constexpr (!MOD) tc::tmem_st32(lane_base + st * 128 + wg * 64, pk);
+            tc::tmem_st32(lane_base + st * 128 + wg * 64, pk);
             tc::tmem_wait_st();
             tc::tc_fence_before();
             tc::mbar_arrive(&B.p_full[st]);
@@ -591,56 +437,7 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant_
         if (hi + 1 < nh) load_q(h + 1);
         const int last = hi * nt + nt - 1;
         if (ok && nt > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.o_done[last & 1], (last >> 1) & 1, p.err));
-        if constexpr (MOD) {
-            // Row statistics of both warpgroups meet (every warp passes, error or not).
-            B.lsum[wg][row] = lsum;
-            asm volatile("bar.sync %0, 64;" :: "r"(pair_bar) : "memory");
-            lsum += B.lsum[wg ^ 1][row];
-        }
-        if (MOD && ok) {
-            float l = 0.f;
-            if (nt > 0) {
-                tc::tc_fence_after();
-                l = __uint_as_float(tc::tmem_ld1(lane_base + kColL));
-            }
-            const float inv = l == 0.f ? 0.f : 1.f / l;      // a row that saw nothing: O = 0
-            const float lse2 = lsum == 0.f ? -INFINITY : m + log2f(lsum);
-            const size_t hrow = (size_t)h * p.n_q + q_local;
-            const size_t prow = (size_t)blockIdx.z * p.Hq * p.n_q + hrow;
-#pragma unroll
-            for (int c = (D / 64) * wg; c < (D / 64) * (wg + 1); ++c) {
-                uint32_t r[32];
-                if (nt > 0) {
-                    tc::tmem_ld32(lane_base + kColO + c * 32, r);
-                    tc::tmem_wait_ld(r);
-                }
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    r[e] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(r[e]) * inv);
-                if (!valid) continue;
-                if (p.part) {
-                    float4* dst = reinterpret_cast<float4*>(p.part + prow * D + c * 32);
-#pragma unroll
-                    for (int v = 0; v < 8; ++v)
-                        dst[v] = make_float4(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]),
-                                             __uint_as_float(r[4 * v + 2]), __uint_as_float(r[4 * v + 3]));
-                } else {
-                    __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.o) + ((size_t)q_local * p.Hq + h) * D;
-#pragma unroll
-                    for (int v = 0; v < 4; ++v)
-                        *reinterpret_cast<uint4*>(orow + c * 32 + v * 8) = make_uint4(
-                            pack_bf16x2(__uint_as_float(r[8 * v]), __uint_as_float(r[8 * v + 1])),
-                            pack_bf16x2(__uint_as_float(r[8 * v + 2]), __uint_as_float(r[8 * v + 3])),
-                            pack_bf16x2(__uint_as_float(r[8 * v + 4]), __uint_as_float(r[8 * v + 5])),
-                            pack_bf16x2(__uint_as_float(r[8 * v + 6]), __uint_as_float(r[8 * v + 7])));
-                }
-            }
-            if (valid && wg == 0) {
-                if (p.part) p.part[(size_t)gridDim.z * p.Hq * p.n_q * D + prow] = lse2;
-                else p.lse[hrow] = lse2 * kLn2;
-            }
-        }
-        if (!MOD && ok && nt > 0) {
+        if (ok && nt > 0) {
             tc::tc_fence_after();
             // Normalise by the sum of the bf16 weights the tensor core multiplied, so
             // O is a convex combination of values whatever the rounding of P.
@@ -686,12 +483,12 @@ bool tc_supported(const AttnArgs& a) {
            a.tmap_v && (reinterpret_cast<uintptr_t>(a.q) & 15) == 0;
 }
 
-template <int D, bool MOD>
+template <int D>
 static cudaError_t launch_fwd(const AttnArgs& a, cudaStream_t s) {
     constexpr uint32_t smem = FwdLayout<D>::kSmemBytes;
     static bool attr_set = false;
     if (!attr_set) {
-        cudaError_t e = cudaFuncSetAttribute(fwd_tc_kernel<D, MOD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(fwd_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)smem);
         if (e != cudaSuccess) return e;
         attr_set = true;
@@ -699,35 +496,19 @@ static cudaError_t launch_fwd(const AttnArgs& a, cudaStream_t s) {
     FwdParams p{};
     p.Hq = a.Hq; p.Hkv = a.Hkv; p.q_start = a.q_start; p.n_q = a.n_q;
     p.q = a.q; p.o = a.o; p.lse = a.lse; p.bt = a.bt; p.num_phys = a.num_phys;
-    p.sel = a.sel; p.kmax = a.kmax; p.err = a.err; p.m = a.m;
-    const int splits = MOD ? a.splits : 1;
-    p.part = splits > 1 ? a.part : nullptr;
+    p.sel = a.sel; p.kmax = a.kmax; p.err = a.err;
     // Short page lists (local layers): one CTA takes every query head of a KV
     // group, so its start-up (tensor memory, barriers, pipeline fill) is paid
     // once for the group's g heads instead of once per head.
     p.heads_per_cta = (a.sel && a.kmax <= kShortList) ? a.Hq / a.Hkv : 1;
-    const unsigned tiles = (unsigned)((a.n_q + kTile - 1) / kTile), heads = a.Hq / p.heads_per_cta;
-    const dim3 grid = MOD ? dim3(heads, tiles, splits) : dim3(tiles, heads, 1);
-    ProfScope ps(MOD ? "fwd_mod_tc_kernel" : "fwd_tc_kernel", s);
-    fwd_tc_kernel<D, MOD><<<grid, kThreads, smem, s>>>(*a.tmap_k, *a.tmap_v, p);
+    dim3 grid((unsigned)((a.n_q + kTile - 1) / kTile), a.Hq / p.heads_per_cta);
+    ProfScope ps("fwd_tc_kernel", s);
+    fwd_tc_kernel<D><<<grid, kThreads, smem, s>>>(*a.tmap_k, *a.tmap_v, p);
     return cudaGetLastError();
 }
 
 cudaError_t launch_attn_fwd_tc(const AttnArgs& a, cudaStream_t s) {
-    if (a.mod) return a.d == 64 ? launch_fwd<64, true>(a, s) : launch_fwd<128, true>(a, s);
-    return a.d == 64 ? launch_fwd<64, false>(a, s) : launch_fwd<128, false>(a, s);
-}
-
-// Few query tiles against a long cache leave most SMs idle: split the keys so
-// that about two CTAs per SM run, each with at least 4 pages of its own.
-int attn_fwd_tc_splits(const AttnArgs& a) {
-    if (a.sel) return 1;
-    int dev = 0, sms = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const int64_t ctas = (a.n_q + kTile - 1) / kTile * a.Hq, pages = (a.m.n_keys + kTile - 1) / kTile;
-    if (ctas >= sms) return 1;
-    return (int)std::max<int64_t>(1, std::min<int64_t>({pages / 4, 2 * (int64_t)sms / ctas, 64}));
+    return a.d == 64 ? launch_fwd<64>(a, s) : launch_fwd<128>(a, s);
 }
 
 }  // namespace pkv

@@ -216,8 +216,10 @@ struct AttnArgs {
 inline size_t attn_part_floats(const AttnArgs& a) {
     return a.splits > 1 ? (size_t)a.splits * a.Hq * a.n_q * (a.d + 1) : 0;
 }
-// CTAs over one tile's keys that the tensor-core forward wants for a.
-int attn_fwd_tc_splits(const AttnArgs& a);
+// The tensor-core forward with modified scores, and the CTAs over one tile's keys
+// that it wants for a.
+int attn_fwd_mod_tc_splits(const AttnArgs& a);
+cudaError_t launch_attn_fwd_mod_tc(const AttnArgs& a, cudaStream_t s);
 // The forward of a few queries against a long cache (bf16).
 bool few_supported(const AttnArgs& a);
 int attn_few_splits(const AttnArgs& a);

@@ -181,17 +181,25 @@ __device__ __forceinline__ void cap_short(const uint32_t (&x)[N], const ModArgs&
     }
 }
 template <int N, typename F>
+__device__ __forceinline__ void cap_long(const uint32_t (&x)[N], const ModArgs& m, F&& use) {
+    const f32x2 k = pack2(m.k, m.k), c2 = pack2(m.c2, m.c2);
+#pragma unroll
+    for (int c = 0; c < N; c += 2) use(c, mul2(tanh_long2(mul2(pair_at(x, c), k)), c2));
+}
+template <int N, typename F>
+__device__ __forceinline__ void cap_any(const uint32_t (&x)[N], const ModArgs& m, F&& use) {
+#pragma unroll
+    for (int c = 0; c < N; c += 2)
+        use(c, pack2(m.c2 * tanh_any(__uint_as_float(x[c]) * m.k), m.c2 * tanh_any(__uint_as_float(x[c + 1]) * m.k)));
+}
+template <int N, typename F>
 __device__ __forceinline__ void cap_pairs(const uint32_t (&x)[N], const ModArgs& m, float top, F&& use) {
     if (top * m.k <= kTanhShort) {
         cap_short(x, m, use);
     } else if (top * m.k <= kTanhLong) {
-        const f32x2 k = pack2(m.k, m.k), c2 = pack2(m.c2, m.c2);
-#pragma unroll
-        for (int c = 0; c < N; c += 2) use(c, mul2(tanh_long2(mul2(pair_at(x, c), k)), c2));
+        cap_long(x, m, use);
     } else {
-#pragma unroll
-        for (int c = 0; c < N; c += 2)
-            use(c, pack2(m.c2 * tanh_any(__uint_as_float(x[c]) * m.k), m.c2 * tanh_any(__uint_as_float(x[c + 1]) * m.k)));
+        cap_any(x, m, use);
     }
 }
 // Every lane's largest over the warp (of values >= 0; their bits order as integers).
