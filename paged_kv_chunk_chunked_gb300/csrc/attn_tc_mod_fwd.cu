@@ -26,6 +26,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -42,6 +43,7 @@ constexpr int kThreads = 320;
 constexpr uint32_t kHalfBytes = 128 * 128;   // [128 rows][64 bf16] = 16 KB
 constexpr int kKStages = 2, kVStages = 2;
 constexpr float kRescaleThreshold = 8.0f;    // log2 units
+constexpr int kShort = 1, kLong = 2, kAny = 3;   // forms of tanh
 
 template <int D> struct Layout {
     static_assert(D == 64 || D == 128, "head dim 64 or 128");
@@ -303,17 +305,15 @@ fwd_mod_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
             auto each_chunk = [&](auto&& use) {
                 uint32_t ra[32], rb[32];
                 tc::tmem_ld32(t_s, ra);
-                tc::tmem_wait_ld(ra);
-                tc::tmem_ld32(t_s + 32, rb);
-                use(ra, 0);
-                tc::tmem_wait_ld(rb);
-                tc::tmem_ld32(t_s + 64, ra);
-                use(rb, 32);
-                tc::tmem_wait_ld(ra);
-                tc::tmem_ld32(t_s + 96, rb);
-                use(ra, 64);
-                tc::tmem_wait_ld(rb);
-                use(rb, 96);
+#pragma unroll 1
+                for (int c0 = 0; c0 < kTile; c0 += 64) {
+                    tc::tmem_wait_ld(ra);
+                    tc::tmem_ld32(t_s + c0 + 32, rb);
+                    use(ra, c0);
+                    tc::tmem_wait_ld(rb);
+                    if (c0 == 0) tc::tmem_ld32(t_s + 64, ra);
+                    use(rb, c0 + 32);
+                }
             };
             float neg_m = 0.f, sum[4] = {0.f, 0.f, 0.f, 0.f};
             // Weights of 32 keys into P, whose columns lie over keys that have been read by
@@ -350,71 +350,95 @@ fwd_mod_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                 // (A row that has seen nothing yet keeps m = -inf; its weights are 0.)
                 neg_m = m == -INFINITY ? 0.f : -m;
             };
+            // Cap, bias and mask compiled in. CAP: 0, or the form of tanh; BIAS: 0, the side
+            // of a tile that lies wholly before the queries (-1), or 1: any side.
+            auto hide = [&](uint32_t (&r)[32], int c0) {
+                const int lo = range.x - kb - c0, hi = range.y - kb - c0;
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                    if (c < lo || c >= hi) r[c] = 0xff800000u;
+            };
+            auto capped_pairs = [&](const uint32_t (&r)[32], auto form, auto&& use) {
+                if constexpr (decltype(form)::value == kShort) cap_short(r, p.m, use);
+                else if constexpr (decltype(form)::value == kLong) cap_long(r, p.m, use);
+                else cap_any(r, p.m, use);
+            };
+            auto biased_pairs = [&](const uint32_t (&r)[32], float pre, int c0, auto kind, auto&& use) {
+                bias_pairs(r, pre, slope2, dist + (float)c0, 1.f, decltype(kind)::value == -1 ? -1 : 0, use);
+            };
+            auto run = [&](auto cap_, auto bias_, auto mask_) {
+                constexpr int CAP = decltype(cap_)::value, BIAS = decltype(bias_)::value;
+                constexpr bool MASK = decltype(mask_)::value;
+                // Scores of 32 keys from their raw logits, in place.
+                auto scores = [&](uint32_t (&r)[32], int c0) {
+                    if constexpr (CAP != 0) capped_pairs(r, cap_, [&](int c, f32x2 y) { put_pair(r, c, y); });
+                    if constexpr (BIAS != 0)
+                        biased_pairs(r, CAP != 0 ? 1.f : sl2, c0, bias_, [&](int c, f32x2 y) { put_pair(r, c, y); });
+                    if constexpr (MASK) hide(r, c0);
+                };
+                if constexpr (CAP == 0 || BIAS != 0) {
+                    each_chunk([&](uint32_t (&r)[32], int c0) {
+                        scores(r, c0);
+                        most(r, mp);
+                    });
+                    start(fmaxf(max3(mp[0], mp[1], mp[2]), mp[3]) * ms);
+                } else {
+                    // The capped maximum of the raw logits (which the caller has taken, for
+                    // the form: of all the tile's keys, hidden ones too, unless MASK).
+                    const float top = fmaxf(max3(mp[0], mp[1], mp[2]), mp[3]);
+                    start(top == -INFINITY ? top : p.m.c2 * tanh_any(top * p.m.k));
+                }
+                each_chunk([&](uint32_t (&r)[32], int c0) {
+                    if constexpr (MASK || (CAP != 0 && BIAS != 0)) {
+                        scores(r, c0);
+                        weights(c0, [&](auto&& emit) { plain(r, emit); });
+                    } else if constexpr (CAP != 0) {
+                        // (The cap's products go with the exponentials, on another pipe.)
+                        weights(c0, [&](auto&& emit) { capped_pairs(r, cap_, pairs(emit)); });
+                    } else if constexpr (BIAS != 0) {
+                        weights(c0, [&](auto&& emit) { biased_pairs(r, sl2, c0, bias_, pairs(emit)); });
+                    } else {
+                        weights(c0, [&](auto&& emit) { plain(r, emit); });
+                    }
+                });
+            };
+            using std::integral_constant;
+            const integral_constant<int, 0> no{};
+            const integral_constant<int, -1> before{};
+            const integral_constant<int, 1> any_side{};
+            const integral_constant<bool, false> whole{};
+            const integral_constant<bool, true> parts{};
+            const integral_constant<int, kShort> short_form{};
+            const integral_constant<int, kLong> long_form{};
+            const integral_constant<int, kAny> any_form{};
             // Each kind of tile has its code to itself: a step that is skipped at run time
             // inside a common one still costs a move of its registers.
-            if (!mask && !biased && !capped) {
-                each_chunk([&](uint32_t (&r)[32], int) { most(r, mp); });
-                start(fmaxf(max3(mp[0], mp[1], mp[2]), mp[3]) * sl2);
-                each_chunk([&](uint32_t (&r)[32], int c0) { weights(c0, [&](auto&& emit) { plain(r, emit); }); });
-            } else if (!mask && !capped && side == -1) {
-                each_chunk([&](uint32_t (&r)[32], int c0) {
-                    bias_pairs(r, sl2, slope2, dist + (float)c0, 1.f, -1, [&](int c, f32x2 y) { put_pair(r, c, y); });
-                    most(r, mp);
-                });
-                start(fmaxf(max3(mp[0], mp[1], mp[2]), mp[3]));
-                each_chunk([&](uint32_t (&r)[32], int c0) {
-                    weights(c0, [&](auto&& emit) { bias_pairs(r, sl2, slope2, dist + (float)c0, 1.f, -1, pairs(emit)); });
-                });
-            } else if (!mask && !biased) {
-                // Capped scores' maximum is the capped maximum, so the cap's products go with
-                // the exponentials, on another pipe.
+            if (!capped) {
+                if (!biased) mask ? run(no, no, parts) : run(no, no, whole);
+                else if (mask || side != -1) run(no, any_side, parts);
+                else run(no, before, whole);
+            } else {
+                // The cap's form goes by the largest logit of the warp's rows.
                 float top = 0.f;
-                each_chunk([&](uint32_t (&r)[32], int) {
+                each_chunk([&](uint32_t (&r)[32], int c0) {
                     top = fmaxf(top, abs_max(r));
+                    if (mask) hide(r, c0);
                     most(r, mp);
                 });
                 top = warp_top(top) * p.m.k;
-                start(p.m.c2 * tanh_any(fmaxf(max3(mp[0], mp[1], mp[2]), mp[3]) * p.m.k));
-                if (top <= kTanhShort)
-                    each_chunk([&](uint32_t (&r)[32], int c0) {
-                        weights(c0, [&](auto&& emit) { cap_short(r, p.m, pairs(emit)); });
-                    });
-                else if (top <= kTanhLong)
-                    each_chunk([&](uint32_t (&r)[32], int c0) {
-                        weights(c0, [&](auto&& emit) { cap_long(r, p.m, pairs(emit)); });
-                    });
-                else
-                    each_chunk([&](uint32_t (&r)[32], int c0) {
-                        weights(c0, [&](auto&& emit) { cap_any(r, p.m, pairs(emit)); });
-                    });
-            } else {
-                // Any of cap, bias and mask.
-                auto scores = [&](uint32_t (&r)[32], int c0) {
-                    tc::tmem_ld32(t_s + c0, r);
-                    tc::tmem_wait_ld(r);
-                    if (capped) cap_pairs(r, p.m, warp_top(abs_max(r)), [&](int c, f32x2 y) { put_pair(r, c, y); });
-                    if (biased)
-                        bias_pairs(r, capped ? 1.f : sl2, slope2, dist + (float)c0, 1.f, side,
-                                   [&](int c, f32x2 y) { put_pair(r, c, y); });
-                    if (mask) {
-                        const int lo = range.x - kb - c0, hi = range.y - kb - c0;
-#pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (c < lo || c >= hi) r[c] = 0xff800000u;
+                if (!biased) {
+                    if (mask) top <= kTanhShort ? run(short_form, no, parts) : run(any_form, no, parts);
+                    else if (top <= kTanhShort) run(short_form, no, whole);
+                    else if (top <= kTanhLong) run(long_form, no, whole);
+                    else run(any_form, no, whole);
+                } else {
+                    mp[0] = mp[1] = mp[2] = mp[3] = -INFINITY;
+                    if (top <= kTanhShort) {
+                        if (mask || side != -1) run(short_form, any_side, parts);
+                        else run(short_form, before, whole);
+                    } else {
+                        run(any_form, any_side, parts);
                     }
-                };
-#pragma unroll 1
-                for (int c0 = 0; c0 < kTile; c0 += 32) {
-                    uint32_t r[32];
-                    scores(r, c0);
-                    most(r, mp);
-                }
-                start(fmaxf(max3(mp[0], mp[1], mp[2]), mp[3]) * ms);
-#pragma unroll 1
-                for (int c0 = 0; c0 < kTile; c0 += 32) {
-                    uint32_t r[32];
-                    scores(r, c0);
-                    weights(c0, [&](auto&& emit) { plain(r, emit); });
                 }
             }
             lsum += (sum[0] + sum[1]) + (sum[2] + sum[3]);
@@ -508,7 +532,7 @@ int attn_fwd_mod_tc_splits(const AttnArgs& a) {
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const int64_t streams = (a.n_q + kTile - 1) / kTile * (a.Hq / a.Hkv);
     const int64_t ctas = (streams + 1) / 2 * a.Hkv, pages = (a.m.n_keys + kTile - 1) / kTile;
-    if (ctas >= sms) return 1;
+    if (2 * ctas > sms) return 1;
     return (int)std::max<int64_t>(1, std::min<int64_t>({pages / 4, 2 * (int64_t)sms / ctas, 64}));
 }
 
