@@ -144,14 +144,15 @@ def rows_ptr(x, n: int):
     int address is taken as dense (stride 0)."""
     if x is None or isinstance(x, int):
         return x, 0
-    if x.dim() != 3 or x.shape[0] != n:
-        raise ValueError(f"expected a tensor [{n}, heads, d], got shape {tuple(x.shape)}")
-    _, h, d = x.shape
-    if x.numel() and (x.stride(2) != 1 or (h > 1 and x.stride(1) != d) or
-                      (n > 1 and x.stride(0) < h * d)):
-        raise ValueError(f"tensor of shape {tuple(x.shape)} with strides {x.stride()}: every row "
+    shape, stride = x.shape, x.stride()
+    if len(shape) != 3 or shape[0] != n:
+        raise ValueError(f"expected a tensor [{n}, heads, d], got shape {tuple(shape)}")
+    _, h, d = shape
+    if stride != (h * d, d, 1) and n * h * d and (stride[2] != 1 or (h > 1 and stride[1] != d) or
+                                                  (n > 1 and stride[0] < h * d)):
+        raise ValueError(f"tensor of shape {tuple(shape)} with strides {stride}: every row "
                          "must be dense [heads, d] memory of its own")
-    return x.data_ptr(), (x.stride(0) if n > 1 else 0)
+    return x.data_ptr(), (stride[0] if n > 1 else 0)
 
 
 def _typed(x, name: str, dtype: str, n=None):
@@ -308,7 +309,9 @@ def pkv_append(seq, k, v, n_tok, stream=None) -> None:
 def pkv_append_rope(seq, q, q_out, k, v, n_tok, rope, stream=None) -> None:
     """q, k, v: tensors [n_tok, heads, d] whose rows may lie apart (slices of one
     projection's output); q and q_out may be None."""
-    (qp, qs), (kp, ks), (vp, vs) = (rows_ptr(x, n_tok) for x in (q, k, v))
+    qp, qs = rows_ptr(q, n_tok)
+    kp, ks = rows_ptr(k, n_tok)
+    vp, vs = rows_ptr(v, n_tok)
     _check(lib().pkv_append_rope(seq, qp, qs, ptr(q_out), kp, ks, vp, vs, n_tok, _rope(rope, n_tok),
                                  stream_ptr(stream)))
 
@@ -322,8 +325,10 @@ def pkv_rope_rows(pool, x, out, n, n_heads, rope, inverse=False, stream=None) ->
 def pkv_rope_grad(seq, row0, n_rows, rope, dq=None, dq_out=None, dk_out=None, dv_out=None,
                   stream=None) -> None:
     """dq and the outputs: tensors [n_rows, heads, d] whose rows may lie apart."""
-    (qp, qs), (op, os_), (kp, ks), (vp, vs) = (rows_ptr(x, n_rows)
-                                                for x in (dq, dq_out, dk_out, dv_out))
+    qp, qs = rows_ptr(dq, n_rows)
+    op, os_ = rows_ptr(dq_out, n_rows)
+    kp, ks = rows_ptr(dk_out, n_rows)
+    vp, vs = rows_ptr(dv_out, n_rows)
     _check(lib().pkv_rope_grad(seq, row0, n_rows, _rope(rope, n_rows), qp, qs, op, os_, kp, ks, vp, vs,
                                stream_ptr(stream)))
 

@@ -11,6 +11,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <chrono>
 #include <cstdio>
 #include <cstdlib>
@@ -141,18 +142,22 @@ static pkv_status claim_pages(pkv_seq* s, int64_t new_len) {
         p->free_list.pop_back();
         p->in_use[pg] = 1;
         s->bt.push_back(pg);
-        if (s->h_bt) s->h_bt[have + i] = pg;
+        if (!s->h_bt) continue;
+        if (have + i < s->n_sent && s->h_bt[have + i] != pg) {
+            // Rewriting an entry that was sent: uploads still queued must have read it.
+            if (s->bt_pending) {
+                cudaEventSynchronize(s->bt_sent);
+                s->bt_pending = false;
+            }
+            s->n_sent = have + i;
+        }
+        s->h_bt[have + i] = pg;
     }
     return PKV_OK;
 }
 
 static void release_pages(pkv_seq* s) {
     pkv_pool* p = s->pool;
-    // Later claims rewrite h_bt from entry 0: uploads still queued must have read it.
-    if (s->bt_pending) {
-        cudaEventSynchronize(s->bt_sent);
-        s->bt_pending = false;
-    }
     // Push back in reverse so a fresh sequence gets the same pages in the same order.
     for (auto it = s->bt.rbegin(); it != s->bt.rend(); ++it) {
         p->in_use[*it] = 0;
@@ -174,18 +179,28 @@ static void release_pages(pkv_seq* s) {
     }
 }
 
-// Uploads block-table entries [from, bt.size()) to the device copy on stream.
-// A kernel reads them from the mapped pinned mirror: a copy-engine transfer on
-// the compute stream would queue behind bulk host-to-device copies issued on
-// other streams (the inputs of later chunks) and hold the next kernel back.
+// Uploads block-table entries [from, bt.size()) to the device copy on stream,
+// but for those the device copy holds already (a reset sequence that gets the
+// same pages again). A kernel reads them from the mapped pinned mirror: a
+// copy-engine transfer on the compute stream would queue behind bulk
+// host-to-device copies issued on other streams (the inputs of later chunks) and
+// hold the next kernel back.
 static pkv_status upload_bt(pkv_seq* s, int64_t from, cudaStream_t st) {
     if (!is_device(s->pool)) return PKV_OK;
-    const int64_t n = (int64_t)s->bt.size() - from;
-    if (n <= 0) return PKV_OK;
-    cudaError_t e = launch_bt_upload(s->h_bt_dev + from, s->d_bt + from, n, st);
-    if (e == cudaSuccess) e = cudaEventRecord(s->bt_sent, st);
+    const int64_t end = (int64_t)s->bt.size(), start = std::max(from, s->n_sent);
+    if (end <= from) return PKV_OK;
+    cudaError_t e = cudaSuccess;
+    // Entries sent before, perhaps on another stream.
+    if (start > from && s->bt_pending) e = cudaStreamWaitEvent(st, s->bt_sent, 0);
+    if (e == cudaSuccess && end > start) {
+        e = launch_bt_upload(s->h_bt_dev + start, s->d_bt + start, end - start, st);
+        if (e == cudaSuccess) e = cudaEventRecord(s->bt_sent, st);
+        if (e == cudaSuccess) {
+            s->bt_pending = true;
+            s->n_sent = end;
+        }
+    }
     if (e != cudaSuccess) return cuda_fail(e, "block-table upload");
-    s->bt_pending = true;
     return PKV_OK;
 }
 
@@ -435,6 +450,7 @@ void pkv_seq_free(pkv_seq* s) {
     auto& v = s->pool->seqs;
     v.erase(std::remove(v.begin(), v.end(), s), v.end());
     if (is_device(s->pool)) {
+        if (s->bt_pending) cudaEventSynchronize(s->bt_sent);   // the mirror's last reader
         cudaFree(s->scratch);
         for (float* old : s->retired) cudaFree(old);
         cudaFreeHost(s->h_bt);
@@ -506,8 +522,10 @@ pkv_status pkv_set_block_table(pkv_seq* s, const int32_t* bt, int64_t n) {
             s->bt_pending = false;
         }
         std::memcpy(s->h_bt, bt, n * sizeof(int32_t));
+        s->n_sent = 0;
         cudaError_t e = cudaMemcpy(s->d_bt, s->h_bt, n * sizeof(int32_t), cudaMemcpyHostToDevice);
         if (e != cudaSuccess) return cuda_fail(e, "pkv_set_block_table: upload");
+        s->n_sent = n;
     }
     return PKV_OK;
 }
@@ -601,6 +619,16 @@ pkv_status pkv::attn_common(pkv_seq* s, const void* q, int64_t q_start, int64_t 
         a->kmax = sel->kmax;
     }
     return PKV_OK;
+}
+
+int pkv::sm_count() {
+    static std::atomic<int> known[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+    if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 1;
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+    return n;
 }
 
 bool pkv::use_tc(const pkv_pool* p, const AttnArgs& a) {

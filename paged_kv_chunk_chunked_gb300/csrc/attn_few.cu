@@ -322,7 +322,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(AttnArgs a) {
 template <int D>
 cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     constexpr int smem = Ring<D>::kBytes;
-    cudaError_t e = cudaFuncSetAttribute(few_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> allowed;
+    const cudaError_t e = allow_smem(few_kernel<D>, smem, allowed);
     if (e != cudaSuccess) return e;
     const unsigned tiles = (unsigned)((a.n_q * (a.Hq / a.Hkv) + kRows - 1) / kRows);
     ProfScope ps("few_kernel", s);
@@ -341,9 +342,7 @@ bool few_supported(const AttnArgs& a) {
 int attn_few_splits(const AttnArgs& a) {
     // One wave of CTAs, each with a step of 128 keys at least; up to 4 steps are
     // not worth a second kernel.
-    int dev = 0, sms = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const int sms = sm_count();
     const int64_t ctas = (a.n_q * (a.Hq / a.Hkv) + kRows - 1) / kRows * a.Hkv, steps = (a.m.n_keys + kStep - 1) / kStep;
     const int64_t room = std::max<int64_t>(1, sms / ctas);
     return steps <= 4 ? 1 : (int)std::min<int64_t>({steps, room, 512});

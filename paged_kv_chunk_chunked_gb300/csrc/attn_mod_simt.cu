@@ -526,15 +526,10 @@ __global__ void __launch_bounds__(NT) bwd_dkdv_mod_simt(AttnArgs a, int64_t tile
     }
 }
 
-template <typename K>
-cudaError_t allow_smem(K kernel, size_t bytes) {
-    return bytes > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)
-                             : cudaSuccess;
-}
-
 template <typename T, int D>
 cudaError_t fwd_launch(const AttnArgs& a, cudaStream_t s) {
-    cudaError_t e = allow_smem(fwd_mod_simt<T, D>, sizeof(FwdSmem<T, D>));
+    static std::atomic<uint64_t> allowed;
+    const cudaError_t e = allow_smem(fwd_mod_simt<T, D>, sizeof(FwdSmem<T, D>), allowed);
     if (e != cudaSuccess) return e;
     dim3 grid((unsigned)row_tiles(a), a.Hkv, a.splits);
     ProfScope ps("fwd_mod_simt", s);
@@ -544,8 +539,9 @@ cudaError_t fwd_launch(const AttnArgs& a, cudaStream_t s) {
 
 template <typename T, int D>
 cudaError_t bwd_launch(const AttnArgs& a, cudaStream_t s) {
-    cudaError_t e = allow_smem(bwd_dq_mod_simt<T, D>, sizeof(DqSmem<T, D>));
-    if (e == cudaSuccess) e = allow_smem(bwd_dkdv_mod_simt<T, D>, sizeof(DkvSmem<T, D>));
+    static std::atomic<uint64_t> allowed[2];
+    cudaError_t e = allow_smem(bwd_dq_mod_simt<T, D>, sizeof(DqSmem<T, D>), allowed[0]);
+    if (e == cudaSuccess) e = allow_smem(bwd_dkdv_mod_simt<T, D>, sizeof(DkvSmem<T, D>), allowed[1]);
     if (e != cudaSuccess) return e;
     {
         ProfScope ps("bwd_dq_mod_simt", s);
@@ -563,9 +559,7 @@ cudaError_t bwd_launch(const AttnArgs& a, cudaStream_t s) {
 int attn_fwd_mod_simt_splits(const AttnArgs& a) {
     if (a.sel) return 1;
     // Few row tiles leave SMs idle: about two CTAs per SM, each with a key tile at least.
-    int dev = 0, sms = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const int sms = sm_count();
     const int64_t ctas = row_tiles(a) * a.Hkv;
     return (int)std::max<int64_t>(1, std::min<int64_t>({(a.m.n_keys + BN - 1) / BN, 2 * (int64_t)sms / ctas, 128}));
 }

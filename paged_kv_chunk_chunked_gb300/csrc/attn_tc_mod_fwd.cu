@@ -497,7 +497,8 @@ fwd_mod_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
 template <int D>
 cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     constexpr uint32_t smem = Layout<D>::kSmemBytes;
-    cudaError_t e = cudaFuncSetAttribute(fwd_mod_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<uint64_t> allowed;
+    const cudaError_t e = allow_smem(fwd_mod_tc_kernel<D>, smem, allowed);
     if (e != cudaSuccess) return e;
     CUtensorMap tq;
     std::string why;
@@ -527,9 +528,7 @@ cudaError_t launch_attn_fwd_mod_tc(const AttnArgs& a, cudaStream_t s) {
 // that about two CTAs per SM run, each with at least 4 pages of its own.
 int attn_fwd_mod_tc_splits(const AttnArgs& a) {
     if (a.sel) return 1;
-    int dev = 0, sms = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const int sms = sm_count();
     const int64_t streams = (a.n_q + kTile - 1) / kTile * (a.Hq / a.Hkv);
     const int64_t ctas = (streams + 1) / 2 * a.Hkv, pages = (a.m.n_keys + kTile - 1) / kTile;
     if (2 * ctas > sms) return 1;

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <exception>
 #include <string>
 #include <vector>
@@ -65,6 +66,7 @@ struct pkv_seq {
     // are rewritten (after a reset) only once the last upload has executed.
     cudaEvent_t bt_sent = nullptr;
     bool bt_pending = false;
+    int64_t n_sent = 0;              // leading entries that d_bt holds, or will once bt_sent is reached
     int64_t len = 0;
     // Scratch of the calls with modified scores, grown on demand; outgrown
     // buffers stay until the sequence is freed (a captured graph may use them).
@@ -123,6 +125,19 @@ template <typename F> pkv_status guarded(const char* who, F&& body) noexcept {
     }
 }
 
+int sm_count();                                      // of the current device
+// Lets the kernel use `bytes` of dynamic shared memory, once per device. `done`:
+// the call site's bits, one per device.
+template <typename K> cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 bool capturing(cudaStream_t s);                      // the stream is being captured into a graph
 bool is_device(const pkv_pool* p);                   // the pool has page memory (not META)
 // PKV_ERR_INVALID unless the current CUDA device is the pool's.

@@ -135,22 +135,22 @@ struct RowsArgs {
     int H;
 };
 
-// Rows of a [n, H, D] tensor rotated: thread (token, group of heads, slot).
+// Rows of a [n, H, D] tensor rotated: thread (token, group of heads, slot). The
+// CTA's angle table is filled while the rows' loads are on their way.
 template <typename T, int D, int SIGN>
-__device__ __forceinline__ void rotate_rows(const RowsArgs& a, const RopeArgs& r, const uint64_t* fix, int64_t unit) {
+__device__ __forceinline__ void rotate_rows(const RowsArgs& a, const RopeArgs& r, uint64_t* fix, int64_t unit) {
     constexpr int EPV = 16 / (int)sizeof(T), SL = D / (2 * EPV);
     const int v = (int)(unit % SL);
     const int groups = (a.H + kHeadGroup - 1) / kHeadGroup;
     const int64_t tg = unit / SL;
     const int64_t t = tg / groups;
     const int h0 = (int)(tg - t * groups) * kHeadGroup;
-    if (t >= a.n) return;
     int va, vb;
     slot_vectors<T>(v, r, va, vb);
     const bool rot = v < r.half / EPV;
     const T* src = static_cast<const T*>(a.x) + t * a.x_stride + (size_t)h0 * D;
     T* dst = static_cast<T*>(a.out) + t * a.out_stride + (size_t)h0 * D;
-    const int nh = min(kHeadGroup, a.H - h0);
+    const int nh = t < a.n ? min(kHeadGroup, a.H - h0) : 0;
     uint4 xa[kHeadGroup], xb[kHeadGroup];
 #pragma unroll
     for (int h = 0; h < kHeadGroup; ++h)
@@ -158,9 +158,11 @@ __device__ __forceinline__ void rotate_rows(const RowsArgs& a, const RopeArgs& r
             xa[h] = reinterpret_cast<const uint4*>(src + h * D)[va];
             xb[h] = reinterpret_cast<const uint4*>(src + h * D)[vb];
         }
-    if (rot) {
+    const int64_t pos = r.positions && nh > 0 ? r.positions[t] : r.pos0 + t;
+    fill_turns(fix, r);
+    if (rot && nh > 0) {
         float c[EPV], s[EPV];
-        cos_sin<EPV, SIGN>(fix, v * EPV, r.positions ? r.positions[t] : r.pos0 + t, c, s);
+        cos_sin<EPV, SIGN>(fix, v * EPV, pos, c, s);
 #pragma unroll
         for (int h = 0; h < kHeadGroup; ++h)
             if (h < nh) {
@@ -189,7 +191,6 @@ int64_t rows_units(const RowsArgs& a) {
 template <typename T, int D, int SIGN>
 __global__ void __launch_bounds__(kThreads) rope_rows_kernel(RowsArgs a, RopeArgs r) {
     __shared__ uint64_t fix[D / 2];
-    fill_turns(fix, r);
     rotate_rows<T, D, SIGN>(a, r, fix, (int64_t)blockIdx.x * kThreads + threadIdx.x);
 }
 
@@ -209,7 +210,6 @@ __global__ void __launch_bounds__(kThreads) append_rope_kernel(AppendArgs a, int
     const int P = a.P, tid = threadIdx.x;
     int b = (int)blockIdx.x;
     if (b >= kv_ctas + zero_ctas) {
-        fill_turns(fix, r);
         rotate_rows<T, D, 1>(q, r, fix, (int64_t)(b - kv_ctas - zero_ctas) * kThreads + tid);
         return;
     }
@@ -247,7 +247,6 @@ __global__ void __launch_bounds__(kThreads) append_rope_kernel(AppendArgs a, int
         }
         return;
     }
-    fill_turns(fix, r);
     const int v = tid % SL, r0 = tid / SL;
     int va, vb;
     slot_vectors<T>(v, r, va, vb);
@@ -259,7 +258,9 @@ __global__ void __launch_bounds__(kThreads) append_rope_kernel(AppendArgs a, int
 #pragma unroll
     for (int e = 0; e < EPV; ++e) acc_a[e] = acc_b[e] = 0.f;
     constexpr int U = 2;                          // rows in flight per thread
-    for (int rb = r0; rb < P; rb += U * RSTEP) {
+    bool table = false;
+    for (int rb0 = 0; rb0 < P; rb0 += U * RSTEP) {
+        const int rb = rb0 + r0;
         uint4 ka[U], kb[U], wa[U], wb[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -279,6 +280,8 @@ __global__ void __launch_bounds__(kThreads) append_rope_kernel(AppendArgs a, int
                 kb[u] = reinterpret_cast<const uint4*>(kpage + (size_t)row * D)[vb];
             }
         }
+        if (!table) fill_turns(fix, r);           // while the first rows' loads are on their way
+        table = true;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int row = rb + u * RSTEP;
@@ -360,7 +363,6 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) rope_grad_kernel(GradArgs a, RowsArgs q, RopeArgs r, int kv_ctas) {
     constexpr int EPV = 16 / (int)sizeof(T), SL = D / (2 * EPV);
     __shared__ uint64_t fix[D / 2];
-    fill_turns(fix, r);
     if ((int)blockIdx.x >= kv_ctas) {
         rotate_rows<T, D, -1>(q, r, fix, (int64_t)((int)blockIdx.x - kv_ctas) * kThreads + threadIdx.x);
         return;
@@ -370,35 +372,37 @@ __global__ void __launch_bounds__(kThreads) rope_grad_kernel(GradArgs a, RowsArg
     const int64_t th = unit / SL;
     const int64_t t = th / a.Hkv;
     const int h = (int)(th - t * a.Hkv);
-    if (t >= a.n) return;
-    const int64_t row = a.row0 + t, lp = row / a.P;
+    const bool live = t < a.n;
+    const int64_t row = a.row0 + (live ? t : 0), lp = row / a.P;
     const int32_t pp = a.bt[lp];
-    if (pp < 0 || pp >= a.num_phys) {
-        report_error(a.err, kErrBadPage);
-        return;
-    }
+    const bool ok = live && pp >= 0 && pp < a.num_phys;
+    if (live && !ok) report_error(a.err, kErrBadPage);
     int va, vb;
     slot_vectors<T>(v, r, va, vb);
-    const size_t tile = (size_t)pp * a.Hkv + h;
-    const size_t off = (tile * a.P + (size_t)(row - lp * a.P)) * D;
-    const bool stale = a.gzero && a.gzero[tile];
     float fa[EPV], fb[EPV], ga[EPV], gb[EPV];
 #pragma unroll
     for (int e = 0; e < EPV; ++e) fa[e] = fb[e] = ga[e] = gb[e] = 0.f;
-    if (!stale) {
-        if (a.dk) {
-            load_f32<EPV>(a.dkpool + off + va * EPV, fa);
-            load_f32<EPV>(a.dkpool + off + vb * EPV, fb);
-        }
-        if (a.dv) {
-            load_f32<EPV>(a.dvpool + off + va * EPV, ga);
-            load_f32<EPV>(a.dvpool + off + vb * EPV, gb);
+    if (ok) {
+        const size_t tile = (size_t)pp * a.Hkv + h;
+        const size_t off = (tile * a.P + (size_t)(row - lp * a.P)) * D;
+        if (!(a.gzero && a.gzero[tile])) {         // else recorded as zero, the memory is stale
+            if (a.dk) {
+                load_f32<EPV>(a.dkpool + off + va * EPV, fa);
+                load_f32<EPV>(a.dkpool + off + vb * EPV, fb);
+            }
+            if (a.dv) {
+                load_f32<EPV>(a.dvpool + off + va * EPV, ga);
+                load_f32<EPV>(a.dvpool + off + vb * EPV, gb);
+            }
         }
     }
+    const int64_t pos = r.positions && live ? r.positions[t] : r.pos0 + t;
+    fill_turns(fix, r);
+    if (!ok) return;
     if (a.dk) {
         if (v < r.half / EPV) {
             float c[EPV], s[EPV];
-            cos_sin<EPV, -1>(fix, v * EPV, r.positions ? r.positions[t] : r.pos0 + t, c, s);
+            cos_sin<EPV, -1>(fix, v * EPV, pos, c, s);
             turn<EPV>(fa, fb, c, s, r.interleaved);
         }
         uint4* d = reinterpret_cast<uint4*>(static_cast<T*>(a.dk) + t * a.dk_stride + (size_t)h * D);
