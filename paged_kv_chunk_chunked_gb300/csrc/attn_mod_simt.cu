@@ -11,9 +11,13 @@
 //   fwd     CTA per (16 rows, KV head, share of the keys): online softmax over
 //           tiles of 64 keys, O in registers. Thread (rg, kg): rows rg, rg + 8,
 //           keys kg + 16 j; its O columns are float4s kg * 4 + 64 j.
-//   dQ      the same shape; P from LSE, dS through shared memory.
-//   dK/dV   CTA per (16 keys, KV head) over the rows that see them, one plain
-//           addition per gradient element (every key has one owner).
+//   dQ      CTA per (16 rows, KV head), four groups of 128 threads on tiles of 32
+//           keys in turn; P from LSE, dS through shared memory.
+//   dK/dV   CTA per (16 keys, KV head), four groups on the row tiles that see them
+//           in turn; one plain addition per gradient element (a key has one owner).
+// The backward's groups add their parts in a fixed order at the end: the sizes
+// this path is for make few CTAs, and one group's tiles one after another took
+// three times as long (2 heads, 64 queries on 256 keys: dQ 28 us, dK/dV 35 us).
 // Rows of K in shared memory are D + 4 floats apart: the 8 threads of a
 // 128-byte phase read 8 consecutive rows' 16 bytes from 8 different bank groups.
 #include <cuda_bf16.h>
@@ -79,9 +83,9 @@ __device__ __forceinline__ size_t row_offset(const AttnArgs& a, int64_t r, int k
 
 template <typename T, int D>
 __device__ __forceinline__ void load_row_tile(float (*dst)[D + 4], const void* src, const AttnArgs& a, const RowTile& t,
-                                              int kvh) {
+                                              int kvh, int tid, int threads = NT) {
     constexpr int EPV = 16 / (int)sizeof(T), VPR = D / EPV;
-    for (int i = threadIdx.x; i < BM * VPR; i += NT) {
+    for (int i = tid; i < BM * VPR; i += threads) {
         const int r = i / VPR, v = i % VPR;
         float f[EPV];
 #pragma unroll
@@ -98,9 +102,9 @@ __device__ __forceinline__ void load_row_tile(float (*dst)[D + 4], const void* s
 // a block-table entry is out of range (recorded; the tile then holds zeros).
 template <typename T, int D, int N>
 __device__ __forceinline__ void load_key_tile(float (*Ks)[D + 4], float (*Vs)[D + 4], const AttnArgs& a, int64_t k0, int n,
-                                              int kvh) {
+                                              int kvh, int tid, int threads = NT) {
     constexpr int EPV = 16 / (int)sizeof(T), VPR = D / EPV;
-    for (int i = threadIdx.x; i < N * VPR; i += NT) {
+    for (int i = tid; i < N * VPR; i += threads) {
         const int r = i / VPR, v = i % VPR;
         float fk[EPV], fv[EPV];
 #pragma unroll
@@ -140,14 +144,14 @@ __device__ __forceinline__ int2 tile_keys(const int2 (&range)[BM]) {
     return hi ? make_int2(lo, hi) : make_int2(0, 0);
 }
 
-// Calls f(k0, n) for the key tiles of up to BN keys that a row tile sees: of
+// Calls f(k0, n) for the key tiles of up to N keys that a row tile sees: of
 // the share blockIdx.z of its range (dense), or of its query page's list.
-template <typename F>
+template <int N, typename F>
 __device__ __forceinline__ void for_key_tiles(const AttnArgs& a, const RowTile& t, int kvh, int2 keys, F&& f) {
     if (!a.sel) {
-        const int n = (keys.y - keys.x + BN - 1) / BN;
+            const int n = (keys.y - keys.x + N - 1) / N;
         const int t0 = (int)((int64_t)n * blockIdx.z / gridDim.z), t1 = (int)((int64_t)n * (blockIdx.z + 1) / gridDim.z);
-        for (int j = t0; j < t1; ++j) f((int64_t)keys.x + j * BN, min(BN, keys.y - keys.x - j * BN));
+        for (int j = t0; j < t1; ++j) f((int64_t)keys.x + j * N, min(N, keys.y - keys.x - j * N));
         return;
     }
     const int32_t* row = a.sel + ((size_t)t.qp * a.Hkv + kvh) * a.kmax;
@@ -155,7 +159,7 @@ __device__ __forceinline__ void for_key_tiles(const AttnArgs& a, const RowTile& 
         const int32_t lp = row[i];
         if (lp < 0) break;
         const int p0 = max(lp * a.P, keys.x), p1 = min((lp + 1) * a.P, keys.y);
-        for (int k0 = p0; k0 < p1; k0 += BN) f((int64_t)k0, min(BN, p1 - k0));
+        for (int k0 = p0; k0 < p1; k0 += N) f((int64_t)k0, min(N, p1 - k0));
     }
 }
 
@@ -174,7 +178,7 @@ __global__ void __launch_bounds__(NT) fwd_mod_simt(AttnArgs a) {
     const int kvh = blockIdx.y, g = a.Hq / a.Hkv;
     const RowTile t = row_tile(a, blockIdx.x);
     if (t.n <= 0) return;
-    load_row_tile<T, D>(S.Q, a.q, a, t, kvh);
+    load_row_tile<T, D>(S.Q, a.q, a, t, kvh, tid);
     if (tid < BM) S.range[tid] = tid < t.n ? row_range(a.m, a.q_start, (t.r0 + tid) / g) : make_int2(0, 0);
     __syncthreads();
     const int2 keys = tile_keys(S.range);
@@ -195,9 +199,9 @@ __global__ void __launch_bounds__(NT) fwd_mod_simt(AttnArgs a) {
 #pragma unroll
         for (int c = 0; c < CV; ++c) o[u][c] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    for_key_tiles(a, t, kvh, keys, [&](int64_t k0, int n) {
+    for_key_tiles<BN>(a, t, kvh, keys, [&](int64_t k0, int n) {
         __syncthreads();
-        load_key_tile<T, D, BN>(S.K, S.V, a, k0, n, kvh);
+        load_key_tile<T, D, BN>(S.K, S.V, a, k0, n, kvh, tid);
         __syncthreads();
         float s[2][4];
 #pragma unroll
@@ -300,24 +304,31 @@ __global__ void __launch_bounds__(NT) fwd_mod_simt(AttnArgs a) {
     }
 }
 
+constexpr int kGroups = 4, GT = kGroups * NT;         // the backward's thread groups
+constexpr int BNG = 32;                               // keys of a group's tile (dQ)
+
+__device__ __forceinline__ void group_sync(int gi) { asm volatile("bar.sync %0, 128;" :: "r"(1 + gi) : "memory"); }
+
 template <typename T, int D>
 struct DqSmem {
-    float Q[BM][D + 4], dO[BM][D + 4], K[BN][D + 4], V[BN][D + 4], S[BM][BN + 4];
+    float Q[BM][D + 4], dO[BM][D + 4];
+    float K[kGroups][BNG][D + 4], V[kGroups][BNG][D + 4], S[kGroups][BM][BNG + 4];
     int2 range[BM];
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(NT) bwd_dq_mod_simt(AttnArgs a) {
+__global__ void __launch_bounds__(GT) bwd_dq_mod_simt(AttnArgs a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     auto& S = *reinterpret_cast<DqSmem<T, D>*>(smem_raw);
     constexpr int CV = D / 64;
-    const int tid = threadIdx.x, rg = tid / 16, kg = tid % 16;
+    const int gi = threadIdx.x / NT, tid = threadIdx.x % NT, rg = tid / 16, kg = tid % 16;
     const int kvh = blockIdx.y, g = a.Hq / a.Hkv;
     const RowTile t = row_tile(a, blockIdx.x);
     if (t.n <= 0) return;
-    load_row_tile<T, D>(S.Q, a.q, a, t, kvh);
-    load_row_tile<T, D>(S.dO, a.dout, a, t, kvh);
-    if (tid < BM) S.range[tid] = tid < t.n ? row_range(a.m, a.q_start, (t.r0 + tid) / g) : make_int2(0, 0);
+    load_row_tile<T, D>(S.Q, a.q, a, t, kvh, threadIdx.x, GT);
+    load_row_tile<T, D>(S.dO, a.dout, a, t, kvh, threadIdx.x, GT);
+    if (threadIdx.x < BM)
+        S.range[tid] = tid < t.n ? row_range(a.m, a.q_start, (t.r0 + tid) / g) : make_int2(0, 0);
     __syncthreads();
     const int2 keys = tile_keys(S.range);
     const float scale = rsqrtf((float)D);
@@ -338,16 +349,18 @@ __global__ void __launch_bounds__(NT) bwd_dq_mod_simt(AttnArgs a) {
 #pragma unroll
         for (int c = 0; c < CV; ++c) dq[u][c] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    for_key_tiles(a, t, kvh, keys, [&](int64_t k0, int n) {
-        __syncthreads();
-        load_key_tile<T, D, BN>(S.K, S.V, a, k0, n, kvh);
-        __syncthreads();
-        float s[2][4], dp[2][4];
+    int turn = 0;
+    for_key_tiles<BNG>(a, t, kvh, keys, [&](int64_t k0, int n) {
+        if (turn++ % kGroups != gi) return;
+        group_sync(gi);
+        load_key_tile<T, D, BNG>(S.K[gi], S.V[gi], a, k0, n, kvh, tid);
+        group_sync(gi);
+        float s[2][2], dp[2][2];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[u][j] = dp[u][j] = 0.f;
-#pragma unroll 2
+            for (int j = 0; j < 2; ++j) s[u][j] = dp[u][j] = 0.f;
+#pragma unroll 4
         for (int d = 0; d < D; d += 4) {
             float4 qv[2], ov[2];
 #pragma unroll
@@ -356,9 +369,9 @@ __global__ void __launch_bounds__(NT) bwd_dq_mod_simt(AttnArgs a) {
                 ov[u] = *reinterpret_cast<const float4*>(&S.dO[rg + 8 * u][d]);
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float4 kv = *reinterpret_cast<const float4*>(&S.K[kg + 16 * j][d]);
-                const float4 vv = *reinterpret_cast<const float4*>(&S.V[kg + 16 * j][d]);
+            for (int j = 0; j < 2; ++j) {
+                const float4 kv = *reinterpret_cast<const float4*>(&S.K[gi][kg + 16 * j][d]);
+                const float4 vv = *reinterpret_cast<const float4*>(&S.V[gi][kg + 16 * j][d]);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     s[u][j] = dot4(qv[u], kv, s[u][j]);
@@ -369,24 +382,24 @@ __global__ void __launch_bounds__(NT) bwd_dq_mod_simt(AttnArgs a) {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 2; ++j) {
                 const int key = (int)k0 + kg + 16 * j;
                 float y, f;
                 mod_score(a.m, slope[u], scale, s[u][j], pos[u] - key, y, f);
                 const bool vis = key >= rr[u].x && key < rr[u].y && kg + 16 * j < n;
-                S.S[rg + 8 * u][kg + 16 * j] = vis ? expf(y - lse[u]) * (dp[u][j] - Dr[u]) * f : 0.f;
+                S.S[gi][rg + 8 * u][kg + 16 * j] = vis ? expf(y - lse[u]) * (dp[u][j] - Dr[u]) * f : 0.f;
             }
-        __syncwarp();
+        __syncwarp();                                           // a row's 16 threads are half a warp
 #pragma unroll 2
-        for (int k = 0; k < BN; k += 4) {
+        for (int k = 0; k < BNG; k += 4) {
             float4 w4[2];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) w4[u] = *reinterpret_cast<const float4*>(&S.S[rg + 8 * u][k]);
+            for (int u = 0; u < 2; ++u) w4[u] = *reinterpret_cast<const float4*>(&S.S[gi][rg + 8 * u][k]);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
 #pragma unroll
                 for (int c = 0; c < CV; ++c) {
-                    const float4 v = *reinterpret_cast<const float4*>(&S.K[k + e][kg * 4 + 64 * c]);
+                    const float4 v = *reinterpret_cast<const float4*>(&S.K[gi][k + e][kg * 4 + 64 * c]);
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         const float w = e == 0 ? w4[u].x : e == 1 ? w4[u].y : e == 2 ? w4[u].z : w4[u].w;
@@ -398,18 +411,18 @@ __global__ void __launch_bounds__(NT) bwd_dq_mod_simt(AttnArgs a) {
                 }
         }
     });
+    __syncthreads();
+    float(*part)[BM][D] = reinterpret_cast<float(*)[BM][D]>(&S.K[0][0][0]);   // [kGroups], over the key tiles
+    static_assert(sizeof(S.K) >= kGroups * BM * D * sizeof(float), "the groups' parts fit the key tiles");
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        const int r = rg + 8 * u;
-        if (r >= t.n) continue;
-        T* dst = static_cast<T*>(a.dq) + row_offset(a, t.r0 + r, kvh, D);
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int c = 0; c < CV; ++c) {
-            Elem<T>::store(dst + kg * 4 + 64 * c, dq[u][c].x * scale);
-            Elem<T>::store(dst + kg * 4 + 64 * c + 1, dq[u][c].y * scale);
-            Elem<T>::store(dst + kg * 4 + 64 * c + 2, dq[u][c].z * scale);
-            Elem<T>::store(dst + kg * 4 + 64 * c + 3, dq[u][c].w * scale);
-        }
+        for (int c = 0; c < CV; ++c) *reinterpret_cast<float4*>(&part[gi][rg + 8 * u][kg * 4 + 64 * c]) = dq[u][c];
+    __syncthreads();
+    for (int i = threadIdx.x; i < t.n * D; i += GT) {
+        const int r = i / D, c = i % D;
+        Elem<T>::store(static_cast<T*>(a.dq) + row_offset(a, t.r0 + r, kvh, D) + c,
+                       ((part[0][r][c] + part[1][r][c]) + (part[2][r][c] + part[3][r][c])) * scale);
     }
 }
 
@@ -417,11 +430,12 @@ constexpr int KN = 16;                                          // keys per CTA 
 
 template <typename T, int D>
 struct DkvSmem {
-    float K[KN][D + 4], V[KN][D + 4], Q[BM][D + 4], dO[BM][D + 4];
-    float P[KN][BM + 4], S[KN][BM + 4];                         // [key][row]
-    int2 range[BM];
-    float lse[BM], Dr[BM], slope[BM];
-    int pos[BM];
+    float K[KN][D + 4], V[KN][D + 4];
+    float Q[kGroups][BM][D + 4], dO[kGroups][BM][D + 4];
+    float P[kGroups][KN][BM + 4], S[kGroups][KN][BM + 4];       // [key][row]
+    int2 range[kGroups][BM];
+    float lse[kGroups][BM], Dr[kGroups][BM], slope[kGroups][BM];
+    int pos[kGroups][BM];
 };
 
 // Whether logical page lp is listed for (query page qp, KV head kvh).
@@ -436,11 +450,11 @@ __device__ __forceinline__ bool page_listed(const AttnArgs& a, int qp, int kvh, 
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(NT) bwd_dkdv_mod_simt(AttnArgs a, int64_t tiles) {
+__global__ void __launch_bounds__(GT) bwd_dkdv_mod_simt(AttnArgs a, int64_t tiles) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     auto& S = *reinterpret_cast<DkvSmem<T, D>*>(smem_raw);
     constexpr int CV = D / 32;                                  // float4 columns per thread: 8 threads per key
-    const int tid = threadIdx.x;
+    const int gi = threadIdx.x / NT, tid = threadIdx.x % NT, lane = threadIdx.x % 32;
     const int kvh = blockIdx.y, g = a.Hq / a.Hkv;
     const int64_t k0 = (int64_t)blockIdx.x * KN;                // keys of one page: KN divides the page size
     const int64_t lp = k0 / a.P;
@@ -448,30 +462,37 @@ __global__ void __launch_bounds__(NT) bwd_dkdv_mod_simt(AttnArgs a, int64_t tile
     const int key = tid / 8, sub = tid % 8;                     // score rows sub, sub + 8; columns sub * 4 + 32 c
     const int kpos = (int)k0 + key;
     const float scale = rsqrtf((float)D);
-    bool loaded = false;
+    // Keys that no query sees are not touched (their page need not be staged).
+    bool any = false;
+    for (int64_t i = threadIdx.x; i < a.n_q && !any; i += GT) {
+        const int2 r = row_range(a.m, a.q_start, i);
+        any = r.x < (int)k0 + n && r.y > (int)k0 && (!a.sel || page_listed(a, (int)(i / a.P), kvh, lp));
+    }
+    if (!__syncthreads_or(any)) return;
+    load_key_tile<T, D, KN>(S.K, S.V, a, k0, n, kvh, threadIdx.x, GT);
+    __syncthreads();
     float4 dk[CV], dv[CV];
 #pragma unroll
     for (int c = 0; c < CV; ++c) dk[c] = dv[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int64_t ti = 0; ti < tiles; ++ti) {
+    for (int64_t ti = gi; ti < tiles; ti += kGroups) {
         const RowTile t = row_tile(a, ti);
-        if (t.n <= 0 || (a.sel && !page_listed(a, t.qp, kvh, lp))) continue;   // the same for every thread
+        if (t.n <= 0 || (a.sel && !page_listed(a, t.qp, kvh, lp))) continue;   // the same for every thread of the group
         int2 r = make_int2(0, 0);
-        if (tid < t.n) r = row_range(a.m, a.q_start, (t.r0 + tid) / g);
-        if (!__syncthreads_or(r.x < (int)k0 + n && r.y > (int)k0)) continue;   // no row sees these keys
-        if (!loaded) load_key_tile<T, D, KN>(S.K, S.V, a, k0, n, kvh);
-        loaded = true;
-        load_row_tile<T, D>(S.Q, a.q, a, t, kvh);
-        load_row_tile<T, D>(S.dO, a.dout, a, t, kvh);
+        if (lane < t.n) r = row_range(a.m, a.q_start, (t.r0 + lane) / g);
+        if (!__any_sync(0xffffffffu, r.x < (int)k0 + n && r.y > (int)k0)) continue;   // no row sees these keys
+        group_sync(gi);                                         // the group is done with its last tile
+        load_row_tile<T, D>(S.Q[gi], a.q, a, t, kvh, tid);
+        load_row_tile<T, D>(S.dO[gi], a.dout, a, t, kvh, tid);
         if (tid < BM) {
             const int64_t row = t.r0 + min(tid, t.n - 1);
             const int h = kvh * g + (int)(row % g);
-            S.range[tid] = r;
-            S.pos[tid] = (int)(a.q_start + row / g);
-            S.slope[tid] = a.m.slopes ? a.m.slopes[h] : 0.f;
-            S.lse[tid] = a.lse_in[(size_t)h * a.n_q + row / g];
-            S.Dr[tid] = a.Dbuf[(size_t)h * a.n_q + row / g];
+            S.range[gi][tid] = r;
+            S.pos[gi][tid] = (int)(a.q_start + row / g);
+            S.slope[gi][tid] = a.m.slopes ? a.m.slopes[h] : 0.f;
+            S.lse[gi][tid] = a.lse_in[(size_t)h * a.n_q + row / g];
+            S.Dr[gi][tid] = a.Dbuf[(size_t)h * a.n_q + row / g];
         }
-        __syncthreads();
+        group_sync(gi);
         float s[2] = {0.f, 0.f}, dp[2] = {0.f, 0.f};
 #pragma unroll 4
         for (int d = 0; d < D; d += 4) {
@@ -479,50 +500,52 @@ __global__ void __launch_bounds__(NT) bwd_dkdv_mod_simt(AttnArgs a, int64_t tile
             const float4 vv = *reinterpret_cast<const float4*>(&S.V[key][d]);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                s[u] = dot4(kv, *reinterpret_cast<const float4*>(&S.Q[sub + 8 * u][d]), s[u]);
-                dp[u] = dot4(vv, *reinterpret_cast<const float4*>(&S.dO[sub + 8 * u][d]), dp[u]);
+                s[u] = dot4(kv, *reinterpret_cast<const float4*>(&S.Q[gi][sub + 8 * u][d]), s[u]);
+                dp[u] = dot4(vv, *reinterpret_cast<const float4*>(&S.dO[gi][sub + 8 * u][d]), dp[u]);
             }
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int i = sub + 8 * u;
             float y, f;
-            mod_score(a.m, S.slope[i], scale, s[u], S.pos[i] - kpos, y, f);
-            const bool vis = key < n && kpos >= S.range[i].x && kpos < S.range[i].y;
-            const float p = vis ? expf(y - S.lse[i]) : 0.f;
-            S.P[key][i] = p;
-            S.S[key][i] = vis ? p * (dp[u] - S.Dr[i]) * f : 0.f;
+            mod_score(a.m, S.slope[gi][i], scale, s[u], S.pos[gi][i] - kpos, y, f);
+            const bool vis = key < n && kpos >= S.range[gi][i].x && kpos < S.range[gi][i].y;
+            const float p = vis ? expf(y - S.lse[gi][i]) : 0.f;
+            S.P[gi][key][i] = p;
+            S.S[gi][key][i] = vis ? p * (dp[u] - S.Dr[gi][i]) * f : 0.f;
         }
         __syncwarp();                                           // a key's 8 threads share a warp
 #pragma unroll 4
         for (int i = 0; i < BM; ++i) {
-            const float p = S.P[key][i], ds = S.S[key][i];
+            const float p = S.P[gi][key][i], ds = S.S[gi][key][i];
 #pragma unroll
             for (int c = 0; c < CV; ++c) {
-                const float4 ov = *reinterpret_cast<const float4*>(&S.dO[i][sub * 4 + 32 * c]);
-                const float4 qv = *reinterpret_cast<const float4*>(&S.Q[i][sub * 4 + 32 * c]);
+                const float4 ov = *reinterpret_cast<const float4*>(&S.dO[gi][i][sub * 4 + 32 * c]);
+                const float4 qv = *reinterpret_cast<const float4*>(&S.Q[gi][i][sub * 4 + 32 * c]);
                 dv[c].x = fmaf(p, ov.x, dv[c].x); dv[c].y = fmaf(p, ov.y, dv[c].y);
                 dv[c].z = fmaf(p, ov.z, dv[c].z); dv[c].w = fmaf(p, ov.w, dv[c].w);
                 dk[c].x = fmaf(ds, qv.x, dk[c].x); dk[c].y = fmaf(ds, qv.y, dk[c].y);
                 dk[c].z = fmaf(ds, qv.z, dk[c].z); dk[c].w = fmaf(ds, qv.w, dk[c].w);
             }
         }
-        __syncthreads();
     }
-    if (!loaded || key >= n) return;
-    const int32_t pp = a.bt[lp];
-    if (pp < 0 || pp >= a.num_phys) return;                     // recorded by load_key_tile
-    const size_t off = (((size_t)pp * a.Hkv + kvh) * a.P + (size_t)(kpos - lp * a.P)) * D;
+    // The groups' parts meet over their Q and dO tiles.
+    __syncthreads();
+    float(*pk)[KN][D] = reinterpret_cast<float(*)[KN][D]>(&S.Q[0][0][0]);
+    float(*pv)[KN][D] = reinterpret_cast<float(*)[KN][D]>(&S.dO[0][0][0]);
 #pragma unroll
     for (int c = 0; c < CV; ++c) {
-        float4* gk = reinterpret_cast<float4*>(a.dkpool + off + sub * 4 + 32 * c);
-        float4* gv = reinterpret_cast<float4*>(a.dvpool + off + sub * 4 + 32 * c);
-        float4 x = *gk, y = *gv;
-        x.x = fmaf(dk[c].x, scale, x.x); x.y = fmaf(dk[c].y, scale, x.y);
-        x.z = fmaf(dk[c].z, scale, x.z); x.w = fmaf(dk[c].w, scale, x.w);
-        y.x += dv[c].x; y.y += dv[c].y; y.z += dv[c].z; y.w += dv[c].w;
-        *gk = x;
-        *gv = y;
+        *reinterpret_cast<float4*>(&pk[gi][key][sub * 4 + 32 * c]) = dk[c];
+        *reinterpret_cast<float4*>(&pv[gi][key][sub * 4 + 32 * c]) = dv[c];
+    }
+    __syncthreads();
+    const int32_t pp = a.bt[lp];
+    if (pp < 0 || pp >= a.num_phys) return;                     // recorded by load_key_tile
+    const size_t off = (((size_t)pp * a.Hkv + kvh) * a.P + (size_t)(k0 - lp * a.P)) * D;
+    for (int i = threadIdx.x; i < n * D; i += GT) {
+        const int r = i / D, c = i % D;
+        a.dkpool[off + i] = fmaf((pk[0][r][c] + pk[1][r][c]) + (pk[2][r][c] + pk[3][r][c]), scale, a.dkpool[off + i]);
+        a.dvpool[off + i] += (pv[0][r][c] + pv[1][r][c]) + (pv[2][r][c] + pv[3][r][c]);
     }
 }
 
@@ -545,11 +568,11 @@ cudaError_t bwd_launch(const AttnArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     {
         ProfScope ps("bwd_dq_mod_simt", s);
-        bwd_dq_mod_simt<T, D><<<dim3((unsigned)row_tiles(a), a.Hkv), NT, sizeof(DqSmem<T, D>), s>>>(a);
+        bwd_dq_mod_simt<T, D><<<dim3((unsigned)row_tiles(a), a.Hkv), GT, sizeof(DqSmem<T, D>), s>>>(a);
     }
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     ProfScope ps("bwd_dkdv_mod_simt", s);
-    bwd_dkdv_mod_simt<T, D><<<dim3((unsigned)((a.m.n_keys + KN - 1) / KN), a.Hkv), NT, sizeof(DkvSmem<T, D>), s>>>(
+    bwd_dkdv_mod_simt<T, D><<<dim3((unsigned)((a.m.n_keys + KN - 1) / KN), a.Hkv), GT, sizeof(DkvSmem<T, D>), s>>>(
         a, row_tiles(a));
     return cudaGetLastError();
 }
