@@ -43,6 +43,7 @@ constexpr int kThreads = 320;
 constexpr uint32_t kHalfBytes = 128 * 128;   // [128 rows][64 bf16] = 16 KB
 constexpr int kKStages = 2, kVStages = 2;
 constexpr float kRescaleThreshold = 8.0f;    // log2 units
+constexpr float kBiasSlack = 64.0f;          // log2 units, of fp32's 126 below 1
 constexpr int kShort = 1, kLong = 2, kAny = 3;   // forms of tanh
 
 template <int D> struct Layout {
@@ -376,7 +377,14 @@ fwd_mod_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                         biased_pairs(r, CAP != 0 ? 1.f : sl2, c0, bias_, [&](int c, f32x2 y) { put_pair(r, c, y); });
                     if constexpr (MASK) hide(r, c0);
                 };
-                if constexpr (CAP == 0 || BIAS != 0) {
+                if (CAP == 0 && BIAS == -1 && slope2 >= 0.f && slope2 * (kTile - 1) <= kBiasSlack) {
+                    // The largest logit with the nearest key's bias bounds the maximum from
+                    // above by at most the bias's span over the tile. The weights are floats:
+                    // a reference 2^64 too high costs them nothing, and the tile's biases are
+                    // formed once instead of twice.
+                    each_chunk([&](uint32_t (&r)[32], int) { most(r, mp); });
+                    start(fmaf(fmaxf(max3(mp[0], mp[1], mp[2]), mp[3]), sl2, slope2 * (dist + (kTile - 1))));
+                } else if constexpr (CAP == 0 || BIAS != 0) {
                     each_chunk([&](uint32_t (&r)[32], int c0) {
                         scores(r, c0);
                         most(r, mp);
