@@ -179,18 +179,17 @@ static void release_pages(pkv_seq* s) {
     }
 }
 
-// Uploads block-table entries [from, bt.size()) to the device copy on stream,
-// but for those the device copy holds already (a reset sequence that gets the
-// same pages again). A kernel reads them from the mapped pinned mirror: a
-// copy-engine transfer on the compute stream would queue behind bulk
-// host-to-device copies issued on other streams (the inputs of later chunks) and
-// hold the next kernel back.
+// Uploads what the device copy of the block table lacks, on stream: entries that a
+// reset sequence gets back are there already, entries that pkv_seq_reserve claimed
+// are not. `from`: the first entry that this call claimed. A kernel reads them from
+// the mapped pinned mirror: a copy-engine transfer on the compute stream would queue
+// behind bulk host-to-device copies issued on other streams (the inputs of later
+// chunks) and hold the next kernel back.
 static pkv_status upload_bt(pkv_seq* s, int64_t from, cudaStream_t st) {
     if (!is_device(s->pool)) return PKV_OK;
-    const int64_t end = (int64_t)s->bt.size(), start = std::max(from, s->n_sent);
-    if (end <= from) return PKV_OK;
+    const int64_t end = (int64_t)s->bt.size(), start = std::min(s->n_sent, end);
     cudaError_t e = cudaSuccess;
-    // Entries sent before, perhaps on another stream.
+    // Claimed now but sent before, perhaps on another stream.
     if (start > from && s->bt_pending) e = cudaStreamWaitEvent(st, s->bt_sent, 0);
     if (e == cudaSuccess && end > start) {
         e = launch_bt_upload(s->h_bt_dev + start, s->d_bt + start, end - start, st);

@@ -68,7 +68,7 @@ struct Params {
     int kmax;
     int* err;
     ModArgs m;
-    float* part;                     // keys split over gridDim.z CTAs: partial results (attn_part_floats), else null
+    float* part;                     // keys split over gridDim.y CTAs: partial results (attn_part_floats), else null
 };
 
 struct __align__(8) Barriers {
@@ -91,14 +91,14 @@ fwd_mod_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
     __shared__ Barriers B;
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int kvh = blockIdx.x, g = p.Hq / p.Hkv;
+    const int kvh = (int)(blockIdx.x % p.Hkv), pair = (int)(blockIdx.x / p.Hkv), g = p.Hq / p.Hkv;
     const int n_qt = (int)((p.n_q + kTile - 1) / kTile);
     // Stream s: longest query tiles first; an odd one out repeats the other (`live` false).
     int qt[2], head[2];
     bool live[2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-        const int idx = 2 * (int)blockIdx.y + s;
+        const int idx = 2 * pair + s;
         const int back = idx / p.per_tile, hh = idx - back * p.per_tile;
         live[s] = back < n_qt && hh < g;
         qt[s] = live[s] ? n_qt - 1 - back : qt[0];
@@ -115,7 +115,7 @@ fwd_mod_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
         const int hi = max(tr[0].hi, tr[1].hi);
         const int p0 = sel_row ? 0 : lo / kTile;
         const int n = sel_row ? sel_count_warp(sel_row, p.kmax, lane) : (hi + kTile - 1) / kTile - p0;
-        const int s0 = (int)((int64_t)n * blockIdx.z / gridDim.z), s1 = (int)((int64_t)n * (blockIdx.z + 1) / gridDim.z);
+        const int s0 = (int)((int64_t)n * blockIdx.y / gridDim.y), s1 = (int)((int64_t)n * (blockIdx.y + 1) / gridDim.y);
         nt = s1 - s0;
         first = p0 + s1 - 1;
     }
@@ -460,7 +460,7 @@ fwd_mod_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
             const float inv = lsum == 0.f ? 0.f : 1.f / lsum;            // a row that saw nothing: O = 0
             const float lse2 = lsum == 0.f ? -INFINITY : m + log2f(lsum);
             const size_t hrow = (size_t)h * p.n_q + q_local;
-            const size_t prow = (size_t)blockIdx.z * p.Hq * p.n_q + hrow;
+            const size_t prow = (size_t)blockIdx.y * p.Hq * p.n_q + hrow;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t r[32];
@@ -489,7 +489,7 @@ fwd_mod_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                 }
             }
             if (valid) {
-                if (p.part) p.part[(size_t)gridDim.z * p.Hq * p.n_q * D + prow] = lse2;
+                if (p.part) p.part[(size_t)gridDim.y * p.Hq * p.n_q * D + prow] = lse2;
                 else p.lse[hrow] = lse2 * kLn2;
             }
         }
@@ -522,7 +522,8 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     p.per_tile = a.sel ? (g + 1) / 2 * 2 : g;
     const int64_t streams = (a.n_q + kTile - 1) / kTile * p.per_tile;
     ProfScope ps("fwd_mod_tc_kernel", s);
-    fwd_mod_tc_kernel<D><<<dim3(a.Hkv, (unsigned)((streams + 1) / 2), a.splits), kThreads, smem, s>>>(tq, *a.tmap_k, *a.tmap_v, p);
+    const dim3 grid((unsigned)((streams + 1) / 2 * a.Hkv), a.splits);
+    fwd_mod_tc_kernel<D><<<grid, kThreads, smem, s>>>(tq, *a.tmap_k, *a.tmap_v, p);
     return cudaGetLastError();
 }
 
