@@ -9,9 +9,10 @@
 //
 // A page's rows of one KV head are contiguous, so a producer warp streams K and
 // V by untiled bulk copies into a ring of steps of 128 keys (192 KB of it: HBM's
-// latency and rate ask for 45 KB in flight per SM, and registers, at 64 KB, gave
-// 4.5 TB/s where the ring gives ...). The rows keep their order, without padding:
-// the lanes' 16-byte reads then meet two to a bank, 1024 cycles of a step's 2700.
+// latency and rate ask for 45 KB in flight per SM). One token on 131072 keys, 28/4
+// heads, d 128: 44 us for 268 MB, 6.1 TB/s, 0.90 of the measured rate, and 6 us for
+// the join. The rows keep their order, without padding: K's 16-byte reads meet two to
+// a bank, V's four, 1500 cycles of the 2700 that a step's bytes take to arrive.
 //
 // The 16x8x16 bf16 MMA takes its operands from 16-byte reads because the order
 // of the products' inner index is free:

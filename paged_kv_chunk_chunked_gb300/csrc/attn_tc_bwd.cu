@@ -116,7 +116,7 @@ template <int D, bool MOD> struct KVLayout {
     static constexpr uint32_t kRANGE = kSTAT + kv_STAGES * 512;    // MOD: stages x 64 query ranges (masked tiles)
     static constexpr uint32_t kSMEM_MOD = kSMEM + kv_STAGES * 512;
 };
-constexpr int kMaxSplits = 8;            // CTAs of a page at most: each adds the page's gradients once
+constexpr int kMaxSplits = 6;            // CTAs of a page at most (documents, capped: 4 356 us, 6 347 us, 8 358 us)
 // MOD: bit of a listed tile some of whose rows do not see the whole key page.
 constexpr int kTileMasked = 0x4000;
 // Tensor-memory columns: S^T, dP^T (64 fp32 each), P^T, dS^T (64 bf16 = 32
@@ -409,7 +409,7 @@ bwd_kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         // three, so whatever stands between a stage's release and its copies shows in the
         // kernel's time: the next tile is looked up before the wait, and a tile's values
         // stay as loaded until they are stored (28 heads, 4096 queries on 16384 keys:
-        // 1500 us with the arithmetic at the loads, ... us so).
+        // 1500 us with the arithmetic at the loads, 1172 us so).
         struct Stats {
             float lse[2], d[2];
             int2 range[2];

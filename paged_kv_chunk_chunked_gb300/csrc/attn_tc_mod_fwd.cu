@@ -8,7 +8,10 @@
 // neither waits for the other's latency. (One stream per CTA with its rows'
 // halves on two warpgroups in step left the tensor core idle for the length of
 // each softmax: 28 heads, d 128, 4096 queries on 16384 keys took 665 us, 985 us
-// with a cap, against ... us, ... us.)
+// with a cap, against 562 us, 774 us: 0.80 and 0.58 of the measured bf16 rate.
+// What bounds it now: with a cap the fp32 pipe and the two warps a scheduler has
+// to hide latency with (tensor pipe 40% active, fp32 pipe 38%, issue slots 48%);
+// and about 13 us a CTA of start-up, masked first tile and epilogue.)
 //   warps 0..3    softmax of stream 0, thread = query row, all 128 keys of a tile
 //   warps 4..7    softmax of stream 1
 //   warp 8        TMA: both Q tiles, then K and V pages into rings
@@ -303,19 +306,22 @@ fwd_mod_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
             // The row is read twice, 32 keys at a time and the next 32 on their way: once for
             // the maximum, once for the weights. That keeps 64 scores in registers where all
             // 128 would spill, and the other stream fills the reads' latency.
-            auto each_chunk = [&](auto&& use) {
-                uint32_t ra[32], rb[32];
-                tc::tmem_ld32(t_s, ra);
+            // (`again`: another reading follows, whose first load starts here.)
+            uint32_t ra[32], rb[32];
+            tc::tmem_ld32(t_s, ra);
+            auto each_chunk = [&](auto again, auto&& use) {
 #pragma unroll 1
                 for (int c0 = 0; c0 < kTile; c0 += 64) {
                     tc::tmem_wait_ld(ra);
                     tc::tmem_ld32(t_s + c0 + 32, rb);
                     use(ra, c0);
                     tc::tmem_wait_ld(rb);
-                    if (c0 == 0) tc::tmem_ld32(t_s + 64, ra);
+                    if (decltype(again)::value || c0 == 0) tc::tmem_ld32(t_s + (c0 == 0 ? 64 : 0), ra);
                     use(rb, c0 + 32);
                 }
             };
+            const std::true_type more{};
+            const std::false_type last{};
             float neg_m = 0.f, sum[4] = {0.f, 0.f, 0.f, 0.f};
             // Weights of 32 keys into P, whose columns lie over keys that have been read by
             // then. late(emit) hands over the keys' scores, in units of 1 / ms.
@@ -382,10 +388,10 @@ fwd_mod_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     // above by at most the bias's span over the tile. The weights are floats:
                     // a reference 2^64 too high costs them nothing, and the tile's biases are
                     // formed once instead of twice.
-                    each_chunk([&](uint32_t (&r)[32], int) { most(r, mp); });
+                    each_chunk(more, [&](uint32_t (&r)[32], int) { most(r, mp); });
                     start(fmaf(fmaxf(max3(mp[0], mp[1], mp[2]), mp[3]), sl2, slope2 * (dist + (kTile - 1))));
                 } else if constexpr (CAP == 0 || BIAS != 0) {
-                    each_chunk([&](uint32_t (&r)[32], int c0) {
+                    each_chunk(more, [&](uint32_t (&r)[32], int c0) {
                         scores(r, c0);
                         most(r, mp);
                     });
@@ -396,7 +402,7 @@ fwd_mod_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     const float top = fmaxf(max3(mp[0], mp[1], mp[2]), mp[3]);
                     start(top == -INFINITY ? top : p.m.c2 * tanh_any(top * p.m.k));
                 }
-                each_chunk([&](uint32_t (&r)[32], int c0) {
+                each_chunk(last, [&](uint32_t (&r)[32], int c0) {
                     if constexpr (MASK || (CAP != 0 && BIAS != 0)) {
                         scores(r, c0);
                         weights(c0, [&](auto&& emit) { plain(r, emit); });
@@ -428,7 +434,7 @@ fwd_mod_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
             } else {
                 // The cap's form goes by the largest logit of the warp's rows.
                 float top = 0.f;
-                each_chunk([&](uint32_t (&r)[32], int c0) {
+                each_chunk(more, [&](uint32_t (&r)[32], int c0) {
                     top = fmaxf(top, abs_max(r));
                     if (mask) hide(r, c0);
                     most(r, mp);

@@ -116,8 +116,9 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
 //                to the score in log2 units;
 //   |u| <= 0.75: 6 terms, relative error 2.9e-8, 9 operations;
 //   beyond:      through the exponential, two special-function operations.
-// Measured, 28 heads, d 128, 4096 queries on 16384 keys, forward: see the
-// forward kernel.
+// 28 heads, d 128, 4096 queries on 16384 keys: without a cap the forward takes
+// 562 us and the backward 1843 us; with the short form 774 and 2280 us, through the
+// exponential 1193 and 3060 us.
 __device__ __forceinline__ f32x2 tanh_long2(f32x2 u) {
     const f32x2 w = mul2(u, u);
     f32x2 p = pack2(-0.004716257099062204f, -0.004716257099062204f);
