@@ -138,21 +138,62 @@ def ptr(x) -> Optional[int]:
     return x.data_ptr()
 
 
-def rows_ptr(x, n: int):
+# What a handle's tensors must be, for the calls that check them: pool or sequence
+# handle -> (torch dtype, Hq, Hkv, d). Entered at creation.
+_KIND: dict = {}
+_ANY = (None, None, None, None)
+
+
+def _torch_dtype(dtype):
+    try:
+        import torch
+    except ImportError:                       # raw addresses only
+        return None
+    return torch.bfloat16 if dtype == PKV_BF16 else torch.float32
+
+
+def _device(stream):
+    """The stream's device, which a call's tensors must be on; None: any GPU."""
+    return getattr(stream, "device_index", None)
+
+
+def _on_device(x, dev) -> None:
+    at = x.get_device()                       # -1: host memory
+    if at != dev and (dev is not None or at < 0):
+        raise ValueError(f"expected a CUDA tensor on {'the current device' if dev is None else f'cuda:{dev}'}, "
+                         f"got one on {x.device}")
+
+
+def rows_ptr(x, n: int, heads=None, d=None, dtype=None):
     """(address, row stride in elements) of a tensor [n, heads, d] whose rows are
     dense and may lie apart, such as a slice of a wider projection's output; an
     int address is taken as dense (stride 0)."""
     if x is None or isinstance(x, int):
         return x, 0
     shape, stride = x.shape, x.stride()
-    if len(shape) != 3 or shape[0] != n:
-        raise ValueError(f"expected a tensor [{n}, heads, d], got shape {tuple(shape)}")
-    _, h, d = shape
-    if stride != (h * d, d, 1) and n * h * d and (stride[2] != 1 or (h > 1 and stride[1] != d) or
-                                                  (n > 1 and stride[0] < h * d)):
+    if len(shape) != 3 or shape[0] != n or (heads and shape[1] != heads) or (d and shape[2] != d):
+        raise ValueError(f"expected a tensor [{n}, {heads or 'heads'}, {d or 'd'}], got shape {tuple(shape)}")
+    if dtype is not None and x.dtype != dtype:
+        raise ValueError(f"expected {dtype} like the pool's pages, got {x.dtype}")
+    _, h, w = shape
+    if stride != (h * w, w, 1) and n * h * w and (stride[2] != 1 or (h > 1 and stride[1] != w) or
+                                                  (n > 1 and stride[0] < h * w)):
         raise ValueError(f"tensor of shape {tuple(shape)} with strides {stride}: every row "
                          "must be dense [heads, d] memory of its own")
     return x.data_ptr(), (stride[0] if n > 1 else 0)
+
+
+def _rows(x, n, heads, d, dtype, dev, dense=False):
+    """rows_ptr of a call's operand, on its device; dense: without gaps."""
+    if x is None or isinstance(x, int):
+        return x, 0
+    p = rows_ptr(x, n, heads, d, dtype)
+    if x.get_device() != dev:
+        _on_device(x, dev)
+    if dense and p[1] and p[1] != x.shape[1] * x.shape[2]:
+        raise ValueError(f"tensor of shape {tuple(x.shape)} with strides {x.stride()} is not "
+                         "contiguous; pass .contiguous()")
+    return p
 
 
 def _typed(x, name: str, dtype: str, n=None):
@@ -175,12 +216,16 @@ def rope(inv_freq, pos0: int = 0, positions=None, interleaved: bool = False) -> 
     return r
 
 
-def _rope(r: Optional[pkv_rope], n: int):
+def _rope(r: Optional[pkv_rope], n: int, dev=None):
     if r is None:
         return None
-    pos = getattr(r, "tensors", (None, None))[1]
-    if pos is not None and pos.numel() != n:
-        raise ValueError(f"positions must have one entry per row ({n}), got {pos.numel()}")
+    inv_freq, pos = getattr(r, "tensors", (None, None))
+    if inv_freq is not None:
+        _on_device(inv_freq, dev)
+    if pos is not None:
+        _on_device(pos, dev)
+        if pos.numel() != n:
+            raise ValueError(f"positions must have one entry per row ({n}), got {pos.numel()}")
     return ctypes.byref(r)
 
 
@@ -194,16 +239,27 @@ def score_mod(softcap: float = 0.0, slopes=None, k_begin=None, k_end=None) -> pk
     return m
 
 
-def _mod(m: Optional[pkv_score_mod], n_q: int, q):
+def _mod(m: Optional[pkv_score_mod], n_q: int, heads, dev):
     if m is None:
         return None
-    slopes, *ranges = getattr(m, "tensors", (None, None, None))
-    for x in ranges:
-        if hasattr(x, "numel") and x.numel() != n_q:
-            raise ValueError(f"k_begin and k_end must have one entry per query ({n_q}), got {x.numel()}")
-    if hasattr(slopes, "numel") and hasattr(q, "dim") and q.dim() == 3 and slopes.numel() != q.shape[1]:
-        raise ValueError(f"slopes must have one entry per query head ({q.shape[1]}), got {slopes.numel()}")
+    for x, n, what in zip(getattr(m, "tensors", (None, None, None)), (heads, n_q, n_q),
+                          ("slopes: one entry per query head", "k_begin: one entry per query",
+                           "k_end: one entry per query")):
+        if x is None or isinstance(x, int):
+            continue
+        if n is not None and x.numel() != n:
+            raise ValueError(f"{what} ({n}), got {x.numel()}")
+        _on_device(x, dev)
     return ctypes.byref(m)
+
+
+def _lse_ptr(x, heads, n_q, dev):
+    if x is None or isinstance(x, int):
+        return x
+    if x.element_size() != 4 or not x.is_floating_point() or (heads and x.shape != (heads, n_q)):
+        raise ValueError(f"lse must be float32 [{heads or 'heads'}, {n_q}], got {x.dtype} {tuple(x.shape)}")
+    _on_device(x, dev)
+    return ptr(x)
 
 
 def stream_ptr(stream) -> Optional[int]:
@@ -246,10 +302,12 @@ def pkv_pool_create(page_size, n_kv_heads, n_q_heads, head_dim, dtype=PKV_BF16,
                       num_phys_pages, n_device_slots, flags, 0)
     out = _P()
     _check(lib().pkv_pool_create(ctypes.byref(d), ctypes.byref(out)))
+    _KIND[out.value] = (_torch_dtype(dtype), n_q_heads, n_kv_heads, head_dim)
     return out.value
 
 
 def pkv_pool_destroy(pool) -> None:
+    _KIND.pop(pool, None)
     lib().pkv_pool_destroy(pool)
 
 
@@ -268,10 +326,12 @@ def pkv_pool_arrays(pool) -> dict:
 def pkv_seq_create(pool) -> int:
     out = _P()
     _check(lib().pkv_seq_create(pool, ctypes.byref(out)))
+    _KIND[out.value] = _KIND.get(pool, _ANY)
     return out.value
 
 
 def pkv_seq_free(seq) -> None:
+    _KIND.pop(seq, None)
     lib().pkv_seq_free(seq)
 
 
@@ -308,28 +368,33 @@ def pkv_append(seq, k, v, n_tok, stream=None) -> None:
 
 def pkv_append_rope(seq, q, q_out, k, v, n_tok, rope, stream=None) -> None:
     """q, k, v: tensors [n_tok, heads, d] whose rows may lie apart (slices of one
-    projection's output); q and q_out may be None."""
-    qp, qs = rows_ptr(q, n_tok)
-    kp, ks = rows_ptr(k, n_tok)
-    vp, vs = rows_ptr(v, n_tok)
-    _check(lib().pkv_append_rope(seq, qp, qs, ptr(q_out), kp, ks, vp, vs, n_tok, _rope(rope, n_tok),
+    projection's output); q and q_out (dense) may be None."""
+    (dt, hq, hkv, d), dev = _KIND.get(seq, _ANY), _device(stream)
+    qp, qs = _rows(q, n_tok, hq, d, dt, dev)
+    op, _ = _rows(q_out, n_tok, hq, d, dt, dev, dense=True)
+    kp, ks = _rows(k, n_tok, hkv, d, dt, dev)
+    vp, vs = _rows(v, n_tok, hkv, d, dt, dev)
+    _check(lib().pkv_append_rope(seq, qp, qs, op, kp, ks, vp, vs, n_tok, _rope(rope, n_tok, dev),
                                  stream_ptr(stream)))
 
 
 def pkv_rope_rows(pool, x, out, n, n_heads, rope, inverse=False, stream=None) -> None:
-    (xp, xs), (op, os_) = rows_ptr(x, n), rows_ptr(out, n)
-    _check(lib().pkv_rope_rows(pool, xp, xs, op, os_, n, n_heads, _rope(rope, n),
+    (dt, _, _, d), dev = _KIND.get(pool, _ANY), _device(stream)
+    xp, xs = _rows(x, n, n_heads, d, dt, dev)
+    op, os_ = _rows(out, n, n_heads, d, dt, dev)
+    _check(lib().pkv_rope_rows(pool, xp, xs, op, os_, n, n_heads, _rope(rope, n, dev),
                                1 if inverse else 0, stream_ptr(stream)))
 
 
 def pkv_rope_grad(seq, row0, n_rows, rope, dq=None, dq_out=None, dk_out=None, dv_out=None,
                   stream=None) -> None:
     """dq and the outputs: tensors [n_rows, heads, d] whose rows may lie apart."""
-    qp, qs = rows_ptr(dq, n_rows)
-    op, os_ = rows_ptr(dq_out, n_rows)
-    kp, ks = rows_ptr(dk_out, n_rows)
-    vp, vs = rows_ptr(dv_out, n_rows)
-    _check(lib().pkv_rope_grad(seq, row0, n_rows, _rope(rope, n_rows), qp, qs, op, os_, kp, ks, vp, vs,
+    (dt, hq, hkv, d), dev = _KIND.get(seq, _ANY), _device(stream)
+    qp, qs = _rows(dq, n_rows, hq, d, dt, dev)
+    op, os_ = _rows(dq_out, n_rows, hq, d, dt, dev)
+    kp, ks = _rows(dk_out, n_rows, hkv, d, dt, dev)
+    vp, vs = _rows(dv_out, n_rows, hkv, d, dt, dev)
+    _check(lib().pkv_rope_grad(seq, row0, n_rows, _rope(rope, n_rows, dev), qp, qs, op, os_, kp, ks, vp, vs,
                                stream_ptr(stream)))
 
 
@@ -344,13 +409,18 @@ def pkv_chunk_attn_bwd(seq, q, o, dout, lse, q_start, n_q, dq, sel=None, stream=
 
 
 def pkv_chunk_attn_mod_fwd(seq, q, q_start, n_q, o, lse, mod, sel=None, stream=None) -> None:
-    _check(lib().pkv_chunk_attn_mod_fwd(seq, ptr(q), q_start, n_q, ptr(o), ptr(lse), _mod(mod, n_q, q),
-                                        _sel(sel), stream_ptr(stream)))
+    (dt, hq, _, d), dev = _KIND.get(seq, _ANY), _device(stream)
+    (qp, _), (op, _) = (_rows(x, n_q, hq, d, dt, dev, dense=True) for x in (q, o))
+    _check(lib().pkv_chunk_attn_mod_fwd(seq, qp, q_start, n_q, op, _lse_ptr(lse, hq, n_q, dev),
+                                        _mod(mod, n_q, hq, dev), _sel(sel), stream_ptr(stream)))
 
 
 def pkv_chunk_attn_mod_bwd(seq, q, o, dout, lse, q_start, n_q, dq, mod, sel=None, stream=None) -> None:
-    _check(lib().pkv_chunk_attn_mod_bwd(seq, ptr(q), ptr(o), ptr(dout), ptr(lse), q_start, n_q, ptr(dq),
-                                        _mod(mod, n_q, q), _sel(sel), stream_ptr(stream)))
+    (dt, hq, _, d), dev = _KIND.get(seq, _ANY), _device(stream)
+    (qp, _), (op, _), (gp, _), (dp, _) = (_rows(x, n_q, hq, d, dt, dev, dense=True)
+                                          for x in (q, o, dout, dq))
+    _check(lib().pkv_chunk_attn_mod_bwd(seq, qp, op, gp, _lse_ptr(lse, hq, n_q, dev), q_start, n_q, dp,
+                                        _mod(mod, n_q, hq, dev), _sel(sel), stream_ptr(stream)))
 
 
 def pkv_chunk_attn_bwd_noalloc(seq, q, o, dout, lse, q_start, n_q, dq, sel=None,

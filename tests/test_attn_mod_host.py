@@ -55,9 +55,18 @@ def test_binding_checks_the_arrays(seq):
         B.score_mod(k_begin=torch.zeros(4, dtype=torch.int32))
     with pytest.raises(ValueError):
         B.score_mod(k_end=torch.zeros(8, dtype=torch.int64)[::2])
-    q = torch.zeros(4, 4, 64, dtype=torch.bfloat16)
-    for m in (B.score_mod(k_begin=torch.zeros(3, dtype=torch.int64)), B.score_mod(slopes=torch.zeros(5))):
+    q, lse = torch.zeros(4, 4, 64, dtype=torch.bfloat16), torch.zeros(4, 4)
+    for bad in (q.float(), q[:3], q[:, :2], q[:, :, :32], q.transpose(0, 1), q):     # the last: not on a GPU
         with pytest.raises(ValueError):
-            B.pkv_chunk_attn_mod_fwd(seq, q, 0, 4, q, q, m)
+            B.pkv_chunk_attn_mod_fwd(seq, bad, 0, 4, 64, 64, B.score_mod())
         with pytest.raises(ValueError):
-            B.pkv_chunk_attn_mod_bwd(seq, q, q, q, q, 0, 4, q, m)
+            B.pkv_chunk_attn_mod_bwd(seq, 64, 64, bad, 64, 0, 4, 64, B.score_mod())
+    for bad in (lse.double(), lse[:, :3], lse):
+        with pytest.raises(ValueError):
+            B.pkv_chunk_attn_mod_fwd(seq, 64, 0, 4, 64, bad, B.score_mod())
+    for m in (B.score_mod(k_begin=torch.zeros(3, dtype=torch.int64)), B.score_mod(slopes=torch.zeros(5)),
+              B.score_mod(k_end=torch.zeros(4, dtype=torch.int64))):
+        with pytest.raises(ValueError):
+            B.pkv_chunk_attn_mod_fwd(seq, 64, 0, 4, 64, 64, m)
+        with pytest.raises(ValueError):
+            B.pkv_chunk_attn_mod_bwd(seq, 64, 64, 64, 64, 0, 4, 64, m)

@@ -89,24 +89,28 @@ def test_bad_rows_and_gradient_operands(seq):
 
 
 def test_binding_refuses_tensors_it_cannot_describe(seq):
+    """Shapes, strides, types and places that the pool's kernels would misread."""
     pool, s = seq
     x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
     inv = torch.ones(32)
     r = B.rope(inv)
     assert r.rotary_dim == 64 and r.interleaved == 0
-    for bad in (x.transpose(0, 1), x[:, :, ::2], x[:, 0], x[:1].expand(4, 2, 64), x[:3]):
-        with pytest.raises(ValueError):
-            B.pkv_append_rope(s, None, None, bad, x, 4, r)
-        with pytest.raises(ValueError):
-            B.pkv_rope_rows(pool, x, bad, 4, 2, r)
-        with pytest.raises(ValueError):
+    for bad in (x.transpose(0, 1), x[:, :, ::2], x[:, 0], x[:1].expand(4, 2, 64), x[:3], x.float(),
+                torch.zeros(4, 3, 64, dtype=torch.bfloat16), torch.zeros(4, 2, 32, dtype=torch.bfloat16), x):
+        why = "CUDA" if bad is x else ""
+        with pytest.raises(ValueError, match=why):
+            B.pkv_append_rope(s, None, None, bad, bad, 4, r)
+        with pytest.raises(ValueError, match=why):
+            B.pkv_rope_rows(pool, bad, bad, 4, 2, r)
+        with pytest.raises(ValueError, match=why):
             B.pkv_rope_grad(s, 0, 4, r, dk_out=bad)
     for bad in (inv.double(), torch.ones(64)[::2]):
         with pytest.raises(ValueError):
             B.rope(bad)
     with pytest.raises(ValueError):
         B.rope(inv, positions=torch.zeros(4))
-    with pytest.raises(ValueError):
-        B.pkv_append_rope(s, None, None, x, x, 4, B.rope(inv, positions=torch.zeros(3, dtype=torch.int64)))
+    for r in (B.rope(inv), B.rope(inv, positions=torch.zeros(3, dtype=torch.int64))):
+        with pytest.raises(ValueError):                      # the rotation's own arrays
+            B.pkv_append_rope(s, None, None, 64, 64, 4, r)
     assert B.rows_ptr(torch.zeros(4, 8, 64)[:, 2:5], 4)[1] == 512
     assert B.rows_ptr(torch.zeros(1, 8, 64)[:, 2:5], 1)[1] == 0
