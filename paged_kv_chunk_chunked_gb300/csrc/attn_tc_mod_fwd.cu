@@ -306,8 +306,7 @@ fwd_mod_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
             // The row is read twice, 32 keys at a time and the next 32 on their way: once for
             // the maximum, once for the weights. That keeps 64 scores in registers where all
             // 128 would spill, and the other stream fills the reads' latency.
-            // (`again`: another reading follows, whose first load starts here; with a bias,
-            // where the scores of the first need the registers, it starts after it.)
+            // (`again`: another reading follows, whose first load starts here.)
             uint32_t ra[32], rb[32];
             tc::tmem_ld32(t_s, ra);
             auto each_chunk = [&](auto again, auto&& use) {
@@ -389,15 +388,13 @@ fwd_mod_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                     // above by at most the bias's span over the tile. The weights are floats:
                     // a reference 2^64 too high costs them nothing, and the tile's biases are
                     // formed once instead of twice.
-                    each_chunk(last, [&](uint32_t (&r)[32], int) { most(r, mp); });
-                    tc::tmem_ld32(t_s, ra);
+                    each_chunk(more, [&](uint32_t (&r)[32], int) { most(r, mp); });
                     start(fmaf(fmaxf(max3(mp[0], mp[1], mp[2]), mp[3]), sl2, slope2 * (dist + (kTile - 1))));
                 } else if constexpr (CAP == 0 || BIAS != 0) {
-                    each_chunk(last, [&](uint32_t (&r)[32], int c0) {
+                    each_chunk(more, [&](uint32_t (&r)[32], int c0) {
                         scores(r, c0);
                         most(r, mp);
                     });
-                    tc::tmem_ld32(t_s, ra);
                     start(fmaxf(max3(mp[0], mp[1], mp[2]), mp[3]) * ms);
                 } else {
                     // The capped maximum of the raw logits (which the caller has taken, for
