@@ -153,13 +153,18 @@ def _torch_dtype(dtype):
 
 
 def _device(stream):
-    """The stream's device, which a call's tensors must be on; None: any GPU."""
+    """The stream's device, which a call's tensors must be on; None: the current one."""
     return getattr(stream, "device_index", None)
 
 
 def _on_device(x, dev) -> None:
     at = x.get_device()                       # -1: host memory
-    if at != dev and (dev is not None or at < 0):
+    if dev is None and at >= 0:
+        import torch
+        want = torch.cuda.current_device()
+    else:
+        want = dev
+    if at < 0 or at != want:
         raise ValueError(f"expected a CUDA tensor on {'the current device' if dev is None else f'cuda:{dev}'}, "
                          f"got one on {x.device}")
 

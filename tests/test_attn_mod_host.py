@@ -70,3 +70,21 @@ def test_binding_checks_the_arrays(seq):
             B.pkv_chunk_attn_mod_fwd(seq, 64, 0, 4, 64, 64, m)
         with pytest.raises(ValueError):
             B.pkv_chunk_attn_mod_bwd(seq, 64, 64, 64, 64, 0, 4, 64, m)
+
+
+@pytest.mark.parametrize("stream", [None, 1 << 20])
+def test_binding_refuses_another_gpus_tensors_without_a_stream_object(monkeypatch, stream):
+    """A call without a stream, or with a raw handle, runs on the current device:
+    a tensor on another GPU is refused, one on the current GPU is not."""
+    class Stand:                                            # a tensor on GPU 1, without a GPU
+        device = torch.device("cuda", 1)
+
+        def get_device(self):
+            return 1
+
+    dev = B._device(stream)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(ValueError, match="current device"):
+        B._on_device(Stand(), dev)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    B._on_device(Stand(), dev)
