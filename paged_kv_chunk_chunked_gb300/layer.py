@@ -58,7 +58,7 @@ class ChunkRecurrentBlock:
             if starts.numel() == 0 or starts[0] != 0 or (starts.diff() <= 0).any() or starts[-1] >= w.N:
                 raise ValueError("doc_starts must ascend from 0 and stay below the sequence's length")
             self.first = starts[torch.searchsorted(starts, torch.arange(w.N), right=True) - 1].cuda()
-        self.modified = self.softcap > 0 or slopes is not None or doc_starts is not None
+        self.modified = self.softcap != 0 or slopes is not None or doc_starts is not None
         self.dt = torch.bfloat16 if w.dtype == "bf16" else torch.float32
         self.weights = {n: to_device(a, w.dtype) for n, a in synth.block_weights(w, hidden).items()}
         pdt = B.PKV_BF16 if w.dtype == "bf16" else B.PKV_F32

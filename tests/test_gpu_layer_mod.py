@@ -4,7 +4,7 @@ the whole sequence: the rotated append, attention, its backward and the rotated
 gradients together, with activation recomputation.
 
 Tolerances (relative Frobenius) as for the plain block: 1e-4 in fp32, 2e-2 in
-bf16 (bf16 projections whose inputs are rounded once, 2^-9 relative, several
+bf16 (bf16 projections whose inputs are rounded once, by 2^-8 relative at most, several
 times in a row)."""
 import math
 
@@ -136,3 +136,16 @@ def test_bad_documents_are_refused():
     for starts in ([], [1, 5], [0, 5, 5], [0, 256]):
         with pytest.raises(ValueError):
             ChunkRecurrentBlock(w, 32, doc_starts=starts)
+
+
+@pytest.mark.parametrize("cap", [-1.0, float("nan")])
+def test_a_bad_cap_is_refused(cap):
+    """Not run as the plain attention."""
+    w = synth.workload("tiny_dense_f32")
+    blk = ChunkRecurrentBlock(w, 32, softcap=cap)
+    try:
+        xs = [torch.zeros(w.C, 32, device="cuda")]
+        with pytest.raises(B.PkvError, match="softcap"):
+            blk.forward(xs)
+    finally:
+        blk.close()
