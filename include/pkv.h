@@ -305,7 +305,9 @@ pkv_status pkv_chunk_attn_mod_fwd(pkv_seq* seq, const void* q, int64_t q_start, 
  * key added into the gradient pages; dS carries the cap's derivative
  * 1 - tanh^2. mod is the forward's. Scratch, capture and alignment (q, o, dout,
  * dq: 16 bytes) as for the forward; the page size must be a multiple of 16
- * (else PKV_ERR_UNSUPPORTED). No gradient of slopes is computed. */
+ * (else PKV_ERR_UNSUPPORTED). No gradient of slopes is computed. Several CTAs may
+ * add to one gradient page: the order of those float32 additions is not fixed, so
+ * dK/dV can differ in their last bits between runs. */
 pkv_status pkv_chunk_attn_mod_bwd(pkv_seq* seq, const void* q, const void* o, const void* dout,
                                   const float* lse, int64_t q_start, int64_t n_q, void* dq,
                                   const pkv_score_mod* mod, const pkv_sel* sel, void* stream);
