@@ -76,7 +76,6 @@ class ChunkRecurrentBlock:
         self.dv = torch.empty_like(self.dk)
         if self.inv_freq is not None:
             heads = w.Hq + 2 * w.Hkv
-            self.wqkv = torch.cat([self.weights[n] for n in ("wq", "wk", "wv")], dim=1).contiguous()
             self.q = torch.empty((C, w.Hq, w.d), dtype=self.dt, device="cuda")
             self.dqkv = torch.empty((C, heads, w.d), dtype=self.dt, device="cuda")
 
@@ -86,10 +85,15 @@ class ChunkRecurrentBlock:
         pos = torch.arange(s, e, device="cuda") - self.first[s:e]
         return B.rope(self.inv_freq, positions=pos, interleaved=self.interleaved)
 
-    def _qkv(self, x):
+    def _wqkv(self):
+        """wq, wk and wv side by side, as they are now: formed once per forward or
+        backward of the sequence, never kept, since training changes ``weights``."""
+        return torch.cat([self.weights[n] for n in ("wq", "wk", "wv")], dim=1)
+
+    def _qkv(self, x, wqkv):
         """Q, K and V [n, heads, d] as slices of one projection's output."""
         w = self.w
-        return (x @ self.wqkv).view(len(x), -1, w.d).split([w.Hq, w.Hkv, w.Hkv], dim=1)
+        return (x @ wqkv).view(len(x), -1, w.d).split([w.Hq, w.Hkv, w.Hkv], dim=1)
 
     def _attend(self, q, s: int, e: int, stream):
         n = e - s
@@ -117,12 +121,13 @@ class ChunkRecurrentBlock:
         w, W = self.w, self.weights
         stream = torch.cuda.current_stream()
         self._reset()
+        wqkv = self._wqkv() if self.inv_freq is not None else None
         ys = []
         for c, x in enumerate(xs):
             s, e = w.chunk_range(c)
             n = e - s
             if self.inv_freq is not None:
-                xq, k, v = self._qkv(x)
+                xq, k, v = self._qkv(x, wqkv)
                 q = self.q[:n]
                 B.pkv_append_rope(self.seq, xq, q, k, v, n, self._rope(s, e), stream)
             else:
@@ -142,6 +147,7 @@ class ChunkRecurrentBlock:
         stream = torch.cuda.current_stream()
         g = {n: torch.zeros(t.shape, dtype=torch.float32, device="cuda") for n, t in W.items()}
         dxs = [None] * len(xs)
+        wqkv = self._wqkv() if self.inv_freq is not None else None
         for c in reversed(range(len(xs))):
             s, e = w.chunk_range(c)
             n = e - s
@@ -164,7 +170,7 @@ class ChunkRecurrentBlock:
                 parts = self.dqkv[:n].split([w.Hq, w.Hkv, w.Hkv], dim=1)
                 B.pkv_rope_grad(self.seq, s, n, self._rope(s, e), dq, *parts, stream=stream)
                 d = self.dqkv[:n].view(n, -1)
-                dxs[c] = dy + d @ self.wqkv.t()
+                dxs[c] = dy + d @ wqkv.t()
                 gw = (xt @ d).float().split([W[name].shape[1] for name in ("wq", "wk", "wv")], dim=1)
                 for name, part in zip(("wq", "wk", "wv"), gw):
                     g[name] += part

@@ -100,6 +100,38 @@ def test_block_matches_whole_sequence(key, kw, hidden, tol, rotary, inter, softc
         blk.close()
 
 
+def test_changed_weights_are_used_at_once():
+    """Weights updated in place and replaced between two steps: the second step's
+    outputs and gradients are those of the new weights throughout."""
+    w, hidden = synth.workload("tiny_dense_f32", N=200), 48
+    xs = [synth.block_x(w, c, hidden) for c in range(w.n_chunks)]
+    dys = [synth.block_dy(w, c, hidden) for c in range(w.n_chunks)]
+    inv_freq = torch.tensor([1e4 ** (-2.0 * i / w.d) for i in range(w.d // 2)])
+    blk = ChunkRecurrentBlock(w, hidden, inv_freq=inv_freq, softcap=2.0)
+    try:
+        xd, dyd = ([to_device(x, w.dtype) for x in a] for a in (xs, dys))
+        blk.forward(xd)
+        blk.backward(xd, dyd)
+        g = torch.Generator().manual_seed(7)
+        for name in ("wq", "wk", "wo"):                      # as an optimiser's step
+            t = blk.weights[name]
+            t.add_((torch.randn(t.shape, generator=g) * t.std().item()).cuda())
+        blk.weights["wv"] = blk.weights["wv"] * -0.5         # as a loaded checkpoint
+        y_ref, g_ref = _whole_sequence(w, np.concatenate(xs), {n: to_numpy(t) for n, t in blk.weights.items()},
+                                       np.concatenate(dys), inv_freq, False, 2.0, None, None)
+        ys = blk.forward(xd)
+        dxs, grads = blk.backward(xd, dyd)
+        torch.cuda.synchronize()
+        B.pkv_check(blk.pool)
+        err = {"y": _rel(np.concatenate([to_numpy(y) for y in ys]), y_ref),
+               "x": _rel(np.concatenate([to_numpy(d) for d in dxs]), g_ref["x"])}
+        for name in ("wq", "wk", "wv", "wo"):
+            err[name] = _rel(to_numpy(grads[name]), g_ref[name])
+        assert max(err.values()) <= 1e-4, err
+    finally:
+        blk.close()
+
+
 def test_generation_after_a_prefilled_chunk():
     """A chunk appended and attended at once, then tokens one at a time: each step's
     output is the whole sequence's row. Bounds as between two bf16 runs of the same
