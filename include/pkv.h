@@ -280,7 +280,10 @@ pkv_status pkv_chunk_attn_bwd(pkv_seq* seq, const void* q, const void* o, const 
  * dK/dV. LSE is that of the modified scores. The arrays are device memory and
  * are read when the kernels run; the [n_q] ones hold the chunk's queries in order.
  * A hidden key or query is hidden by a zero weight: K, V of the pages a call
- * reads and Q, O, dO of its rows must be finite there too (0 * inf is NaN). */
+ * reads and Q, O, dO of its rows must be finite there too (0 * inf is NaN).
+ * Of a PINNED_HOST pool the pages must be staged that hold a key visible to some
+ * query of the call (and, with a selection, are listed for it), for the backward
+ * with their gradients; no other page needs a slot. */
 typedef struct pkv_score_mod {
     float softcap;             /* 0: none; else in [1e-3, 1e4]                            */
     int32_t reserved;

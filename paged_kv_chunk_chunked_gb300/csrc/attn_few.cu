@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(AttnArgs a) {
     float* part = reinterpret_cast<float*>(ring);
     __shared__ float wm[kWarps][kRows], wl[kWarps][kRows];
     __shared__ uint64_t full[R::kStages], empty[R::kStages];
-    __shared__ int good[R::kStages];                  // the stage's step holds its keys
+    __shared__ uint32_t good[R::kStages];             // bit w: the stage holds the keys of warp w's block
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     const int kvh = blockIdx.y, group = a.Hq / a.Hkv;
     const int row0 = (int)blockIdx.x * kRows, rows = (int)min64(kRows, a.n_q * group - row0);
@@ -113,16 +113,30 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(AttnArgs a) {
             const int first = k0 / a.P, runs = (k1 - 1) / a.P - first + 1;       // at most 9 (pages of 16)
             int32_t pp = -1;
             if (lane < runs) pp = a.bt[first + lane];
-            const bool ok = __all_sync(0xffffffffu, lane >= runs || (pp >= 0 && pp < a.num_phys));
+            const int from = max(k0, (first + lane) * a.P), to = min(k1, (first + lane + 1) * a.P);
+            const bool ok = lane < runs && pp >= 0 && pp < a.num_phys;
+            uint32_t blocks = (1u << kWarps) - 1, rows_in = (uint32_t)(k1 - k0);
+            if (!__all_sync(0xffffffffu, ok || lane >= runs)) {
+                // Runs without a usable page are left out: fine where no row sees their keys.
+                for (uint32_t bad = __ballot_sync(0xffffffffu, lane < runs && !ok); bad; bad &= bad - 1) {
+                    const int l = __ffs(bad) - 1;
+                    const int f = __shfl_sync(0xffffffffu, from, l), e = __shfl_sync(0xffffffffu, to, l);
+                    if (__any_sync(0xffffffffu, (range[0].x < e && range[0].y > f) || (range[1].x < e && range[1].y > f)) &&
+                        lane == 0)
+                        report_error(a.err, kErrBadPage);
+                }
+                // (Runs begin and end at blocks: pages are whole blocks.)
+                blocks = __reduce_or_sync(0xffffffffu,
+                                          ok ? (2u << ((to - k0 - 1) / kKeys)) - (1u << ((from - k0) / kKeys)) : 0u);
+                rows_in = __reduce_add_sync(0xffffffffu, ok ? (uint32_t)(to - from) : 0u);
+            }
             if (lane == 0) {
-                if (!ok) report_error(a.err, kErrBadPage);
-                good[st] = ok;
-                if (ok) tc::mbar_arrive_expect_tx(&full[st], 2u * (uint32_t)(k1 - k0) * D * 2);
+                good[st] = blocks;
+                if (rows_in) tc::mbar_arrive_expect_tx(&full[st], 2u * rows_in * D * 2);
                 else tc::mbar_arrive(&full[st]);
             }
             __syncwarp();
-            if (ok && lane < runs) {
-                const int from = max(k0, (first + lane) * a.P), to = min(k1, (first + lane + 1) * a.P);
+            if (ok) {
                 const size_t src = (((size_t)pp * a.Hkv + kvh) * a.P + from % a.P) * D;
                 uint8_t* dst = ring + 2 * st * R::kTile + (from - k0) * D * 2;
                 const uint32_t bytes = (uint32_t)(to - from) * D * 2;
@@ -256,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(AttnArgs a) {
             const int st = (b - b0) % R::kStages;
             ok = tc::warp_wait(&full[st], ((b - b0) / R::kStages) & 1, a.err);
             const int key0 = b * kStep + warp * kKeys;
-            if (ok && good[st] && key0 < end) {
+            if (ok && (good[st] >> warp & 1) && key0 < end) {
                 const uint8_t* base = ring + 2 * st * R::kTile + warp * kKeys * D * 2;
                 compute(key0, reinterpret_cast<const uint4*>(base), reinterpret_cast<const uint4*>(base + R::kTile));
             }

@@ -98,12 +98,25 @@ __device__ __forceinline__ void load_row_tile(float (*dst)[D + 4], const void* s
     }
 }
 
-// Keys k0 .. k0 + n - 1 (n <= N; rows behind read as zero) of K and V. False if
-// a block-table entry is out of range (recorded; the tile then holds zeros).
+// Keys of [k0, k0 + n) have no usable page: an error where a row of the tile sees one.
+__device__ __noinline__ void bad_keys(const int32_t* bt, int64_t num_phys, int P, int64_t k0, int n, const int2* range, int* err) {
+    for (int64_t key = k0; key < k0 + n; ++key) {
+        const int32_t pp = bt[key / P];
+        if (pp >= 0 && pp < num_phys) continue;
+        bool seen = !range;
+        for (int u = 0; range && u < BM; ++u) seen |= (int)key >= range[u].x && (int)key < range[u].y;
+        if (seen) report_error(err, kErrBadPage);
+    }
+}
+
+// Keys k0 .. k0 + n - 1 (n <= N; rows behind read as zero) of K and V. Keys whose
+// block-table entry is out of range read as zero, which is an error where a row of
+// the tile sees the key (`range`: the rows' keys; null: some row does).
 template <typename T, int D, int N>
 __device__ __forceinline__ void load_key_tile(float (*Ks)[D + 4], float (*Vs)[D + 4], const AttnArgs& a, int64_t k0, int n,
-                                              int kvh, int tid, int threads = NT) {
+                                              int kvh, const int2* range, int tid, int threads = NT) {
     constexpr int EPV = 16 / (int)sizeof(T), VPR = D / EPV;
+    bool bad = false;
     for (int i = tid; i < N * VPR; i += threads) {
         const int r = i / VPR, v = i % VPR;
         float fk[EPV], fv[EPV];
@@ -113,7 +126,7 @@ __device__ __forceinline__ void load_key_tile(float (*Ks)[D + 4], float (*Vs)[D 
             const int64_t key = k0 + r, lp = key / a.P;
             const int32_t pp = a.bt[lp];
             if (pp < 0 || pp >= a.num_phys) {
-                report_error(a.err, kErrBadPage);
+                bad = true;
             } else {
                 const size_t off = (((size_t)pp * a.Hkv + kvh) * a.P + (size_t)(key - lp * a.P)) * D;
                 widen16<T>(__ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.kpool) + off) + v), fk);
@@ -126,6 +139,7 @@ __device__ __forceinline__ void load_key_tile(float (*Ks)[D + 4], float (*Vs)[D 
             *reinterpret_cast<float4*>(&Vs[r][v * EPV + e]) = make_float4(fv[e], fv[e + 1], fv[e + 2], fv[e + 3]);
         }
     }
+    if (bad) bad_keys(a.bt, a.num_phys, a.P, k0, n, range, a.err);
 }
 
 __device__ __forceinline__ float dot4(const float4& x, const float4& y, float acc) {
@@ -169,8 +183,10 @@ struct FwdSmem {
     int2 range[BM];
 };
 
+// (4 CTAs per SM: left to itself the compiler takes 80 to 96 registers and spills. bf16,
+// 8/2 heads, 512 queries on 2048 keys, pages of 32: d 64 177 -> 171 us.)
 template <typename T, int D>
-__global__ void __launch_bounds__(NT) fwd_mod_simt(AttnArgs a) {
+__global__ void __launch_bounds__(NT, 4) fwd_mod_simt(AttnArgs a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     auto& S = *reinterpret_cast<FwdSmem<T, D>*>(smem_raw);
     constexpr int CV = D / 64;                                  // float4 columns per thread
@@ -201,7 +217,7 @@ __global__ void __launch_bounds__(NT) fwd_mod_simt(AttnArgs a) {
     }
     for_key_tiles<BN>(a, t, kvh, keys, [&](int64_t k0, int n) {
         __syncthreads();
-        load_key_tile<T, D, BN>(S.K, S.V, a, k0, n, kvh, tid);
+        load_key_tile<T, D, BN>(S.K, S.V, a, k0, n, kvh, S.range, tid);
         __syncthreads();
         float s[2][4];
 #pragma unroll
@@ -353,7 +369,7 @@ __global__ void __launch_bounds__(GT) bwd_dq_mod_simt(AttnArgs a) {
     for_key_tiles<BNG>(a, t, kvh, keys, [&](int64_t k0, int n) {
         if (turn++ % kGroups != gi) return;
         group_sync(gi);
-        load_key_tile<T, D, BNG>(S.K[gi], S.V[gi], a, k0, n, kvh, tid);
+        load_key_tile<T, D, BNG>(S.K[gi], S.V[gi], a, k0, n, kvh, S.range, tid);
         group_sync(gi);
         float s[2][2], dp[2][2];
 #pragma unroll
@@ -469,7 +485,7 @@ __global__ void __launch_bounds__(GT) bwd_dkdv_mod_simt(AttnArgs a, int64_t tile
         any = r.x < (int)k0 + n && r.y > (int)k0 && (!a.sel || page_listed(a, (int)(i / a.P), kvh, lp));
     }
     if (!__syncthreads_or(any)) return;
-    load_key_tile<T, D, KN>(S.K, S.V, a, k0, n, kvh, threadIdx.x, GT);
+    load_key_tile<T, D, KN>(S.K, S.V, a, k0, n, kvh, nullptr, threadIdx.x, GT);
     __syncthreads();
     float4 dk[CV], dv[CV];
 #pragma unroll

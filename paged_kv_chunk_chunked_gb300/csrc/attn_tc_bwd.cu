@@ -340,8 +340,20 @@ bwd_kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     }
     const uint32_t tmem = B.tmem_base;
     const int n_i = B.n_i;
-    // A page no query tile uses needs no valid slot (sparse, staged pools).
-    if (threadIdx.x == 0 && !page_ok && n_i > 0) report_error(p.err, kErrBadPage);
+    // A page no query tile uses needs no valid slot (sparse, staged pools). MOD: nor
+    // does one that lies between the ranges of a listed tile's rows.
+    bool wanted = n_i > 0;
+    if (MOD && !page_ok) {
+        bool any = false;
+        for (int u = threadIdx.x; u < n_i * 64; u += kThreads) {
+            const int64_t q = (int64_t)((int)B.tiles[u / 64] & (kTileMasked - 1)) * 64 + u % 64;
+            if (q >= p.n_q) continue;
+            const int2 r = p.ranges[q];
+            any |= r.x < (int)kfirst + 128 && r.y > (int)kfirst;
+        }
+        wanted = __syncthreads_or(any);
+    }
+    if (threadIdx.x == 0 && !page_ok && wanted) report_error(p.err, kErrBadPage);
     // Iterations (head, 64-query tile), t = head * n_i + tile; split takes the
     // share [t_base, t_base + T) of them (the gradient epilogue adds, so any
     // partition of the iterations gives the same sums).
@@ -882,11 +894,17 @@ bwd_q_tc_kernel(const __grid_constant__ CUtensorMap tm_do, const __grid_constant
                 !__all_sync(0xffffffffu, tc::mbar_wait(&B.k_empty[ks], ((t / q_KST) - 1) & 1, p.err)))
                 break;
             const int32_t pp = pages.get(t);
+            int row = (int)(((int64_t)pp * p.Hkv + kvh) * 128);
             if (pp < 0 || pp >= p.num_phys) {
-                if (lane == 0) report_error(p.err, kErrBadPage);
-                break;
+                // MOD: fine where no row of the tile sees the page, as in the forward.
+                const int64_t k0 = (int64_t)(sel_row ? sel_row[t] : first + t) * 128;
+                if (!MOD || k0 >= p.m.n_keys ||
+                    tile_sees<128>(p.m, p.q_start, (int64_t)qt * 128, p.n_q, (int)k0, (int)k0 + 128)) {
+                    if (lane == 0) report_error(p.err, kErrBadPage);
+                    break;
+                }
+                row = -128;
             }
-            const int row = (int)(((int64_t)pp * p.Hkv + kvh) * 128);
             if (lane == 0) {
                 uint8_t* kd = smem + q_K + ks * kT;
                 tc::mbar_arrive_expect_tx(&B.k_full[ks], kT);

@@ -169,11 +169,19 @@ fwd_mod_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
             const int ks = j % kKStages, vs = j % kVStages;
             if (j >= kKStages && !tc::warp_wait(&B.k_empty[ks], ((j / kKStages) - 1) & 1, p.err)) break;
             const int32_t pp = pages.get(j);
+            int row = (int)(((int64_t)pp * p.Hkv + kvh) * kTile);
             if (pp < 0 || pp >= p.num_phys) {
-                if (lane == 0) report_error(p.err, kErrBadPage);
-                break;
+                // Fine where neither tile sees the page: all its keys are masked, and
+                // the rows before the first of the pool read as zero.
+                const int64_t lp = sel_row ? sel_row[first - j] : first - j, k0 = lp * kTile;
+                if (k0 >= p.m.n_keys ||
+                    tile_sees<kTile>(p.m, p.q_start, (int64_t)qt[0] * kTile, p.n_q, (int)k0, (int)k0 + kTile) ||
+                    tile_sees<kTile>(p.m, p.q_start, (int64_t)qt[1] * kTile, p.n_q, (int)k0, (int)k0 + kTile)) {
+                    if (lane == 0) report_error(p.err, kErrBadPage);
+                    break;
+                }
+                row = -kTile;
             }
-            const int row = (int)(((int64_t)pp * p.Hkv + kvh) * kTile);
             if (lane == 0) {
                 tc::mbar_arrive_expect_tx(&B.k_full[ks], L::kTileBytes);
 #pragma unroll

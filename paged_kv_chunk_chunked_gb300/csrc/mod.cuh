@@ -37,10 +37,14 @@ inline void set_cap(ModArgs* m, float c, int d) {
 
 // The keys [lo, hi) visible to query row i of the chunk; (0, 0) if none.
 // Positions fit 32 bits: a pool holds fewer than 2^31 rows.
-__device__ __forceinline__ int2 row_range(const ModArgs& m, int64_t q_start, int64_t i) {
-    const int64_t lo = m.k_begin ? max64(m.k_begin[i], 0) : 0;
-    const int64_t hi = m.k_end ? min64(m.k_end[i], m.n_keys) : q_start + i + 1;
+__device__ __forceinline__ int2 row_range(const int64_t* k_begin, const int64_t* k_end, int64_t n_keys, int64_t q_start,
+                                          int64_t i) {
+    const int64_t lo = k_begin ? max64(k_begin[i], 0) : 0;
+    const int64_t hi = k_end ? min64(k_end[i], n_keys) : q_start + i + 1;
     return hi > lo ? make_int2((int)lo, (int)hi) : make_int2(0, 0);
+}
+__device__ __forceinline__ int2 row_range(const ModArgs& m, int64_t q_start, int64_t i) {
+    return row_range(m.k_begin, m.k_end, m.n_keys, q_start, i);
 }
 
 // Bounds over a tile of query rows: keys outside [lo, hi) are visible to none
@@ -78,6 +82,24 @@ __device__ __forceinline__ TileRange tile_range(const ModArgs& m, int64_t q_star
     t.full_hi = __reduce_min_sync(0xffffffffu, t.full_hi);
     if (t.hi == 0) t.lo = 0;
     return t;
+}
+
+// Whether a row of [row0, row1) of the chunk sees a key of [k0, k1); by one warp, the
+// same result in every lane. For pages whose block-table entry is unusable: the hull of
+// a tile's ranges may hold pages that no row sees, and those need no slot. (Out of
+// line: inside, it cost the kernels spilled registers.)
+static __device__ __noinline__ bool rows_see(const int64_t* k_begin, const int64_t* k_end, int64_t n_keys, int64_t q_start,
+                                             int64_t row0, int64_t row1, int k0, int k1) {
+    bool any = false;
+    for (int64_t i = row0 + threadIdx.x % 32; i < row1; i += 32) {
+        const int2 r = row_range(k_begin, k_end, n_keys, q_start, i);
+        any |= r.x < k1 && r.y > k0;
+    }
+    return __any_sync(0xffffffffu, any);
+}
+template <int ROWS>
+__device__ __forceinline__ bool tile_sees(const ModArgs& m, int64_t q_start, int64_t row0, int64_t n_q, int k0, int k1) {
+    return rows_see(m.k_begin, m.k_end, m.n_keys, q_start, row0, min64(row0 + ROWS, n_q), k0, k1);
 }
 
 // Pairs of floats: one instruction for two elements (sm_100 on). Sums, products
