@@ -183,7 +183,11 @@ pkv_status pkv_set_block_table(pkv_seq* seq, const int32_t* bt, int64_t n);
  *   - zeroes the dK/dV gradient rows of every newly claimed page, so a page
  *     starts with zero gradient.
  * The current length must be a multiple of P unless it is the first append
- * after a partial page (then the partial page is completed first). */
+ * after a partial page (then the partial page is completed first).
+ * On a capturing stream the sequence advances once, at the capture: each replay
+ * stores k's and v's rows of that moment into the same pages again, and sends
+ * their block-table entries itself. No replay may be running while the sequence
+ * is reset or given other pages. */
 pkv_status pkv_append(pkv_seq* seq, const void* k, const void* v, int64_t n_tok, void* stream);
 
 /* ---------------------------------------------------------------- rotation

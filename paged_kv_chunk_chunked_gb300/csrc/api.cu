@@ -125,6 +125,18 @@ static pkv_status validate_desc(const pkv_pool_desc* d) {
 
 bool pkv::is_device(const pkv_pool* p) { return p->desc.residency != PKV_RES_META; }
 
+// Waits on the host until the last upload has read h_bt. (Also while this thread
+// captures a stream: the event is never recorded in a capture, and waiting for it
+// cannot touch one.)
+static void wait_bt_sent(pkv_seq* s) {
+    if (!s->bt_pending) return;
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    cudaEventSynchronize(s->bt_sent);
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    s->bt_pending = false;
+}
+
 // Claims pages so that the sequence covers new_len tokens. Host-only; on
 // failure nothing changes.
 static pkv_status claim_pages(pkv_seq* s, int64_t new_len) {
@@ -144,11 +156,7 @@ static pkv_status claim_pages(pkv_seq* s, int64_t new_len) {
         s->bt.push_back(pg);
         if (!s->h_bt) continue;
         if (have + i < s->n_sent && s->h_bt[have + i] != pg) {
-            // Rewriting an entry that was sent: uploads still queued must have read it.
-            if (s->bt_pending) {
-                cudaEventSynchronize(s->bt_sent);
-                s->bt_pending = false;
-            }
+            wait_bt_sent(s);          // rewriting an entry that was sent
             s->n_sent = have + i;
         }
         s->h_bt[have + i] = pg;
@@ -189,6 +197,13 @@ static pkv_status upload_bt(pkv_seq* s, int64_t from, cudaStream_t st) {
     if (!is_device(s->pool)) return PKV_OK;
     const int64_t end = (int64_t)s->bt.size(), start = std::min(s->n_sent, end);
     cudaError_t e = cudaSuccess;
+    if (capturing(st)) {
+        // The graph uploads what this call claimed, whenever it is replayed. Nothing has
+        // been sent yet, and an event of the capture would mean nothing outside it.
+        const int64_t first = std::min(start, from);
+        if (end > first) e = launch_bt_upload(s->h_bt_dev + first, s->d_bt + first, end - first, st);
+        return e == cudaSuccess ? PKV_OK : cuda_fail(e, "block-table upload");
+    }
     // Claimed now but sent before, perhaps on another stream.
     if (start > from && s->bt_pending) e = cudaStreamWaitEvent(st, s->bt_sent, 0);
     if (e == cudaSuccess && end > start) {
@@ -449,7 +464,7 @@ void pkv_seq_free(pkv_seq* s) {
     auto& v = s->pool->seqs;
     v.erase(std::remove(v.begin(), v.end(), s), v.end());
     if (is_device(s->pool)) {
-        if (s->bt_pending) cudaEventSynchronize(s->bt_sent);   // the mirror's last reader
+        wait_bt_sent(s);                             // the mirror's last reader
         cudaFree(s->scratch);
         for (float* old : s->retired) cudaFree(old);
         cudaFreeHost(s->h_bt);
@@ -516,10 +531,7 @@ pkv_status pkv_set_block_table(pkv_seq* s, const int32_t* bt, int64_t n) {
     for (int64_t i = 0; i < n; ++i) p->in_use[bt[i]] = 1;
     s->n_reserved_pages = n;
     if (is_device(p) && n > 0) {
-        if (s->bt_pending) {                         // h_bt may still be a queued copy's source
-            cudaEventSynchronize(s->bt_sent);
-            s->bt_pending = false;
-        }
+        wait_bt_sent(s);                             // h_bt may still be a queued copy's source
         std::memcpy(s->h_bt, bt, n * sizeof(int32_t));
         s->n_sent = 0;
         cudaError_t e = cudaMemcpy(s->d_bt, s->h_bt, n * sizeof(int32_t), cudaMemcpyHostToDevice);

@@ -82,3 +82,93 @@ def test_reserved_pages_and_another_stream():
         B.pkv_check(pool)
     finally:
         B.pkv_pool_destroy(pool)
+
+
+def _captured_append(s, kb, vb, n, side):
+    """The append in a graph, with K and V gathered behind it."""
+    a, b = torch.empty_like(kb), torch.empty_like(vb)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        B.pkv_append(s, kb, vb, n, side)
+        B.pkv_gather(s, a, b, stream=side)
+    return g, a, b
+
+
+def test_append_captured_after_a_reset():
+    """The graph holds an upload of its own: replays store new rows into the same
+    pages, also after other appends of the sequence have run."""
+    pool = B.pkv_pool_create(16, 1, 2, 64, B.PKV_F32, 8)
+    try:
+        s, side = B.pkv_seq_create(pool), torch.cuda.Stream()
+        k, v = _rows(60, 1)
+        B.pkv_append(s, k, v, 60, torch.cuda.current_stream())
+        torch.cuda.synchronize()
+        B.pkv_seq_reset(s)
+        kb, vb = k.clone(), v.clone()
+        g, a, b = _captured_append(s, kb, vb, 60, side)
+        assert B.pkv_seq_length(s) == 60
+        for seed in (2, 3):
+            k, v = _rows(60, seed)
+            kb.copy_(k), vb.copy_(v)
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(a, k) and torch.equal(b, v) and _holds(s, k, v)
+            B.pkv_seq_reset(s)                               # the same pages, without the graph
+            k, v = _rows(60, 10 + seed)
+            B.pkv_append(s, k, v, 60, torch.cuda.current_stream())
+            assert _holds(s, k, v)
+            torch.cuda.synchronize()
+        B.pkv_check(pool)
+    finally:
+        B.pkv_pool_destroy(pool)
+
+
+def test_a_captured_upload_counts_only_where_it_runs():
+    """A first append that was captured and never replayed has sent nothing."""
+    pool = B.pkv_pool_create(16, 1, 2, 64, B.PKV_F32, 8)
+    try:
+        s, side = B.pkv_seq_create(pool), torch.cuda.Stream()
+        k, v = _rows(60, 4)
+        kb, vb = k.clone(), v.clone()
+        torch.cuda.synchronize()
+        g, a, b = _captured_append(s, kb, vb, 60, side)
+        B.pkv_seq_reset(s)
+        B.pkv_append(s, k, v, 60, torch.cuda.current_stream())
+        assert _holds(s, k, v)
+        k, v = _rows(30, 5)
+        B.pkv_append(s, k, v, 30, torch.cuda.current_stream())
+        torch.cuda.synchronize()
+        B.pkv_check(pool)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a, kb) and torch.equal(b, vb)
+        B.pkv_check(pool)
+    finally:
+        B.pkv_pool_destroy(pool)
+
+
+def test_append_captured_with_other_pages_than_before():
+    """Entries that were sent change while the stream is being captured."""
+    pool = B.pkv_pool_create(16, 1, 2, 64, B.PKV_F32, 8)
+    try:
+        s, t, side = B.pkv_seq_create(pool), B.pkv_seq_create(pool), torch.cuda.Stream()
+        st = torch.cuda.current_stream()
+        k, v = _rows(60, 6)
+        B.pkv_append(s, k, v, 60, st)
+        B.pkv_seq_reset(s)
+        kt, vt = _rows(30, 7)
+        B.pkv_append(t, kt, vt, 30, st)                      # takes pages 0 and 1
+        torch.cuda.synchronize()
+        g, a, b = _captured_append(s, k, v, 60, side)
+        assert B.pkv_get_block_table(s) == [2, 3, 4, 5]
+        for _ in range(2):
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(a, k) and torch.equal(b, v)
+            assert _holds(s, k, v) and _holds(t, kt, vt)
+        k2, v2 = _rows(20, 8)
+        B.pkv_append(s, k2, v2, 20, st)                      # goes on behind the captured rows
+        assert _holds(s, torch.cat([k, k2]), torch.cat([v, v2]))
+        B.pkv_check(pool)
+    finally:
+        B.pkv_pool_destroy(pool)
