@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(AttnArgs a) {
 template <int D>
 cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     constexpr int smem = Ring<D>::kBytes;
-    static std::atomic<uint64_t> allowed;
+    static SmemGrant allowed;
     const cudaError_t e = allow_smem(few_kernel<D>, smem, allowed);
     if (e != cudaSuccess) return e;
     const unsigned tiles = (unsigned)((a.n_q * (a.Hq / a.Hkv) + kRows - 1) / kRows);

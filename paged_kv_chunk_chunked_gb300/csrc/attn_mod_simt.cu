@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(GT) bwd_dkdv_mod_simt(AttnArgs a, int64_t tile
 
 template <typename T, int D>
 cudaError_t fwd_launch(const AttnArgs& a, cudaStream_t s) {
-    static std::atomic<uint64_t> allowed;
+    static SmemGrant allowed;
     const cudaError_t e = allow_smem(fwd_mod_simt<T, D>, sizeof(FwdSmem<T, D>), allowed);
     if (e != cudaSuccess) return e;
     dim3 grid((unsigned)row_tiles(a), a.Hkv, a.splits);
@@ -578,7 +578,7 @@ cudaError_t fwd_launch(const AttnArgs& a, cudaStream_t s) {
 
 template <typename T, int D>
 cudaError_t bwd_launch(const AttnArgs& a, cudaStream_t s) {
-    static std::atomic<uint64_t> allowed[2];
+    static SmemGrant allowed[2];
     cudaError_t e = allow_smem(bwd_dq_mod_simt<T, D>, sizeof(DqSmem<T, D>), allowed[0]);
     if (e == cudaSuccess) e = allow_smem(bwd_dkdv_mod_simt<T, D>, sizeof(DkvSmem<T, D>), allowed[1]);
     if (e != cudaSuccess) return e;

@@ -1307,16 +1307,10 @@ static cudaError_t launch_bwd(const AttnArgs& a, cudaStream_t s) {
         !make_tmap_3d(&tdo128, a.dout, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, D, a.Hq, a.n_q, s1, s2, 64, 1, 128, &why))
         return cudaErrorInvalidValue;
     constexpr uint32_t kv_smem = MOD ? KVLayout<D, MOD>::kSMEM_MOD : KVLayout<D, MOD>::kSMEM;
-    static bool attr = false;
-    if (!attr) {
-        cudaError_t e = cudaFuncSetAttribute(bwd_kv_tc_kernel<D, MOD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)kv_smem);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(bwd_q_tc_kernel<D, MOD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)QLayout<D>::kSMEM);
-        if (e != cudaSuccess) return e;
-        attr = true;
-    }
+    static SmemGrant kv_allowed, q_allowed;
+    cudaError_t e = allow_smem(bwd_kv_tc_kernel<D, MOD>, kv_smem, kv_allowed);
+    if (e == cudaSuccess) e = allow_smem(bwd_q_tc_kernel<D, MOD>, QLayout<D>::kSMEM, q_allowed);
+    if (e != cudaSuccess) return e;
     BwdParams p{};
     p.Hq = a.Hq; p.Hkv = a.Hkv; p.q_start = a.q_start; p.n_q = a.n_q; p.q = a.q; p.kpool = a.kpool;
     p.lse = a.lse_in; p.Dbuf = a.Dbuf; p.dq = a.dq; p.dkpool = a.dkpool; p.dvpool = a.dvpool;
@@ -1329,7 +1323,7 @@ static cudaError_t launch_bwd(const AttnArgs& a, cudaStream_t s) {
         const dim3 g_q = MOD ? dim3(a.Hq, tiles) : dim3(tiles, a.Hq);
         ProfScope ps(MOD ? "bwd_q_mod_tc_kernel" : "bwd_q_tc_kernel", s);
         bwd_q_tc_kernel<D, MOD><<<g_q, kThreads, QLayout<D>::kSMEM, s>>>(tdo128, *a.tmap_k, *a.tmap_v, p);
-        cudaError_t e = cudaGetLastError();
+        e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
     // (With a selection no key past the chunk is listed.)
@@ -1351,18 +1345,16 @@ static cudaError_t launch_bwd(const AttnArgs& a, cudaStream_t s) {
         const size_t flags_bytes = ((size_t)n_key_pages + 15) & ~size_t(15);
         const int masks_in_smem = a.selmask && flags_bytes + mask_bytes <= 200 * 1024;
         const size_t fl = masks_in_smem ? flags_bytes + mask_bytes : (size_t)n_key_pages;
-        static size_t attr_u = 0;
-        if (fl > 48 * 1024 && fl > attr_u) {
-            cudaError_t e = cudaFuncSetAttribute(sel_union_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (int)fl);
+        static SmemGrant allowed;
+        if (fl > 48 * 1024) {
+            e = allow_smem(sel_union_kernel, fl, allowed);
             if (e != cudaSuccess) return e;
-            attr_u = fl;
         }
         ProfScope ps("sel_union_kernel", s);
         sel_union_kernel<<<1, kUnionThreads, fl, s>>>(a.sel, (int64_t)n_qp * a.Hkv * a.kmax,
                                                       (int)n_key_pages, a.pagelist, a.Hkv, a.kmax,
                                                       a.selmask, W, masks_in_smem);
-        cudaError_t e = cudaGetLastError();
+        e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         p.pagelist = a.pagelist;
         p.selmask = a.selmask;

@@ -486,13 +486,9 @@ bool tc_supported(const AttnArgs& a) {
 template <int D>
 static cudaError_t launch_fwd(const AttnArgs& a, cudaStream_t s) {
     constexpr uint32_t smem = FwdLayout<D>::kSmemBytes;
-    static bool attr_set = false;
-    if (!attr_set) {
-        cudaError_t e = cudaFuncSetAttribute(fwd_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)smem);
-        if (e != cudaSuccess) return e;
-        attr_set = true;
-    }
+    static SmemGrant allowed;
+    const cudaError_t e = allow_smem(fwd_tc_kernel<D>, smem, allowed);
+    if (e != cudaSuccess) return e;
     FwdParams p{};
     p.Hq = a.Hq; p.Hkv = a.Hkv; p.q_start = a.q_start; p.n_q = a.n_q;
     p.q = a.q; p.o = a.o; p.lse = a.lse; p.bt = a.bt; p.num_phys = a.num_phys;

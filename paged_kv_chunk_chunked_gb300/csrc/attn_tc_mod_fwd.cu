@@ -519,7 +519,7 @@ fwd_mod_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
 template <int D>
 cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     constexpr uint32_t smem = Layout<D>::kSmemBytes;
-    static std::atomic<uint64_t> allowed;
+    static SmemGrant allowed;
     const cudaError_t e = allow_smem(fwd_mod_tc_kernel<D>, smem, allowed);
     if (e != cudaSuccess) return e;
     CUtensorMap tq;

@@ -8,6 +8,7 @@
 
 #include <atomic>
 #include <exception>
+#include <mutex>
 #include <string>
 #include <vector>
 
@@ -126,16 +127,23 @@ template <typename F> pkv_status guarded(const char* who, F&& body) noexcept {
 }
 
 int sm_count();                                      // of the current device
-// Lets the kernel use `bytes` of dynamic shared memory, once per device. `done`:
-// the call site's bits, one per device.
-template <typename K> cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<uint64_t>& done) {
+// Dynamic shared memory that a kernel has been allowed, per device: a limit set on one
+// device says nothing of another.
+struct SmemGrant {
+    std::atomic<size_t> bytes[64]{};
+    std::mutex m;
+};
+// Lets the kernel use `bytes` of dynamic shared memory on the current device. `grant`:
+// the kernel's own, static.
+template <typename K> cudaError_t allow_smem(K* kernel, size_t bytes, SmemGrant& grant) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
-    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    if (dev < 64 && grant.bytes[dev].load(std::memory_order_acquire) >= bytes) return cudaSuccess;
+    std::lock_guard<std::mutex> lock(grant.m);
+    if (dev < 64 && grant.bytes[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
+    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && dev < 64) grant.bytes[dev].store(bytes, std::memory_order_release);
     return e;
 }
 bool capturing(cudaStream_t s);                      // the stream is being captured into a graph

@@ -130,8 +130,8 @@ cudaError_t run_selftest_umma(int mode, const void* a, const void* b, float* d, 
                               int* d_err) {
     if (lbo < 0 || lbo > 16384 || sbo < 0 || sbo > 16384 || (lbo & 15) || (sbo & 15))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(umma_selftest_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    static SmemGrant allowed;
+    cudaError_t e = allow_smem(umma_selftest_kernel, kSmem, allowed);
     if (e != cudaSuccess) return e;
     umma_selftest_kernel<<<1, 128, kSmem>>>(mode, static_cast<const __nv_bfloat16*>(a),
                                             static_cast<const __nv_bfloat16*>(b), d, lbo, sbo,

@@ -35,7 +35,6 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
-#include <mutex>
 
 #include "common.cuh"
 #include "internal.h"
@@ -495,22 +494,20 @@ size_t topk_smem_bytes() {
 
 template <typename T, int D>
 cudaError_t launch_fused(const TopkArgs& a, cudaStream_t s) {
-    static int per_sm = 0;
-    static std::once_flag once;
     const size_t smem = topk_smem_bytes<T, D>();
-    static cudaError_t init = cudaSuccess;
-    std::call_once(once, [&] {
-        init = cudaFuncSetAttribute(topk_fused_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)smem);
-        if (init == cudaSuccess)
-            init = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, topk_fused_kernel<T, D>,
-                                                                 kTkThreads, smem);
-    });
-    if (init != cudaSuccess) return init;
-    int dev = 0, sms = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const int grid = std::max(1, std::min(a.total_units, std::max(1, per_sm) * std::max(1, sms)));
+    static SmemGrant allowed;
+    cudaError_t e = allow_smem(topk_fused_kernel<T, D>, smem, allowed);
+    // CTAs that fit one SM, asked for once per device (0: not yet).
+    static std::atomic<int> known[64];
+    int dev = 0, per_sm = 0;
+    if (e == cudaSuccess) e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && dev < 64) per_sm = known[dev].load(std::memory_order_relaxed);
+    if (e == cudaSuccess && per_sm == 0) {
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, topk_fused_kernel<T, D>, kTkThreads, smem);
+        if (e == cudaSuccess && dev < 64) known[dev].store(per_sm, std::memory_order_relaxed);
+    }
+    if (e != cudaSuccess) return e;
+    const int grid = std::max(1, std::min(a.total_units, std::max(1, per_sm) * sm_count()));
     ProfScope ps("topk_fused_kernel", s);
     topk_fused_kernel<T, D><<<grid, kTkThreads, smem, s>>>(a, (int)(smem / sizeof(float)));
     return cudaGetLastError();
