@@ -194,9 +194,11 @@ pkv_status pkv_append(pkv_seq* seq, const void* k, const void* v, int64_t n_tok,
  * Rotary position embedding of Q and K rows. Pair i of a row at position p,
  * i < rotary_dim / 2, turns by the angle p * inv_freq[i]:
  *   (x, y) -> (x cos - y sin, y cos + x sin);
- * dims rotary_dim .. head_dim - 1 pass through. The angle is formed exactly
- * modulo one turn (64-bit fixed point) for any int64 position; cos, sin and the
- * products are float32, rounded once to the pool's dtype.
+ * dims rotary_dim .. head_dim - 1 pass through. A frequency is rounded to 2^-64
+ * turns per position and whole turns drop out exactly, for any int64 position: the
+ * phase is off by |p| 2^-65 turns at most (1.9e-7 radians at |p| = 2^40, 1.9e-4 at
+ * 2^50; frequencies below 2^24 radians). cos, sin and the products are float32,
+ * rounded once to the pool's dtype.
  * rotary_dim must be even and at most head_dim (else PKV_ERR_INVALID) and a
  * multiple of 16 (else PKV_ERR_UNSUPPORTED).
  *

@@ -9,9 +9,10 @@
 // Angles: an fp32 product p * f is off by 2^-24 of the angle, 0.06 rad at one
 // million radians, and the fp64 units are too few to form one product per
 // (token, pair). So f is turned once per CTA into a 64-bit fixed-point
-// fraction of a turn, and p * f is an integer product modulo 2^64: whole turns
-// drop out by themselves and the phase is off by |p| * 2^-65 turns, whatever
-// the position. Its leading 32 bits give cos and sin in fp32.
+// fraction of a turn, rounded to nearest, and p * f is an integer product modulo
+// 2^64: whole turns drop out by themselves and the phase is off by at most
+// |p| * 2^-65 turns: 1.9e-7 rad at |p| = 2^40, 1.9e-4 at 2^50. Its leading 32 bits
+// give cos and sin in fp32.
 //
 // The kernels are HBM-bound copies. A thread owns two 16-byte vectors of a row
 // (slot v of SL = D / (2 * EPV)): in the rotated part the two vectors whose
@@ -51,13 +52,15 @@ __device__ __forceinline__ uint64_t turns_fixed(float f) {
     const uint64_t p0 = (uint64_t)m * 0x7f09d5f4u, p1 = (uint64_t)m * 0x9391054au, p2 = (uint64_t)m * 0x28be60dbu;
     const uint64_t lo = p0 + (p1 << 32);
     const uint64_t hi = p2 + (p1 >> 32) + (lo < p0 ? 1u : 0u);
-    // value * 2^64 = (m * K) >> (182 - ex)
+    // value * 2^64 = (m * K) / 2^s, s = 182 - ex, to nearest: the last bit shifted out rounds.
     const int s = 182 - max(ex, 1);
     uint64_t r = 0;
-    if (s >= 128) r = 0;
-    else if (s >= 64) r = hi >> (s - 64);
-    else if (s > 0) r = (hi << (64 - s)) | (lo >> s);
-    else if (s > -64) r = lo << (-s);
+    if (s > 0) {
+        const unsigned __int128 x = s <= 128 ? ((unsigned __int128)hi << 64 | lo) >> (s - 1) : 0;
+        r = (uint64_t)(x >> 1) + ((uint64_t)x & 1u);
+    } else if (s > -64) {
+        r = lo << (-s);
+    }
     return (bits >> 31) ? 0ull - r : r;
 }
 

@@ -354,3 +354,44 @@ def test_empty_calls_change_nothing():
         assert B.pkv_seq_length(seq) == 0 and B.pkv_pool_free_pages(pool) == 2
     finally:
         B.pkv_pool_destroy(pool)
+
+
+def _turns(f, pos, bits=400):
+    """pos * f / (2 pi) modulo one turn, from integers: f's own 24 bits and pi to
+    `bits` bits by Machin's formula."""
+    def atan_inv(x):
+        one, total, term, k = 1 << bits, 0, (1 << bits) // x, 0
+        while term:
+            total += (term // (2 * k + 1)) * (-1) ** k
+            term //= x * x
+            k += 1
+        return total
+    two_pi = 8 * (4 * atan_inv(5) - atan_inv(239))
+    num, den = float(f).as_integer_ratio()
+    x = pos * num * (1 << (2 * bits)) // (den * two_pi)
+    return (x % (1 << bits)) / float(1 << bits)
+
+
+@pytest.mark.parametrize("pos0", [2 ** 44 + 12345, -(2 ** 47) - 1, 2 ** 50 - 3])
+@pytest.mark.parametrize("theta", [1e4, 1e6])
+def test_far_positions_within_half_a_unit(pos0, theta):
+    """A pair's frequency is a 64-bit fraction of a turn, rounded to nearest: the
+    phase is off by |p| 2^-65 turns at most, on top of the rest of ROT."""
+    n, d = 9, 128
+    inv = _inv_freq(d, theta)
+    pool = B.pkv_pool_create(16, 1, 1, d, B.PKV_F32, 1)
+    try:
+        x = _rows(n, (1,), d, torch.float32, False, 55)[0]
+        out = torch.empty_like(x)
+        B.pkv_rope_rows(pool, x, out, n, 1, B.rope(inv.cuda(), pos0=pos0))
+        torch.cuda.synchronize()
+        a, b = _f64(x)[:, 0, :d // 2], _f64(x)[:, 0, d // 2:]
+        ang = 2 * math.pi * np.array([[_turns(f, pos0 + t) for f in inv.tolist()] for t in range(n)])
+        c, s = np.cos(ang), np.sin(ang)
+        size = np.hypot(a, b)
+        tol = 2 * math.pi * abs(pos0) * 2.0 ** -65 * size + (ROT + 2.0 ** -23) * (np.abs(a) + np.abs(b))
+        got = _f64(out)[:, 0]
+        assert (np.abs(got[:, :d // 2] - (a * c - b * s)) <= tol).all()
+        assert (np.abs(got[:, d // 2:] - (b * c + a * s)) <= tol).all()
+    finally:
+        B.pkv_pool_destroy(pool)
