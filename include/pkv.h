@@ -197,7 +197,8 @@ pkv_status pkv_append(pkv_seq* seq, const void* k, const void* v, int64_t n_tok,
  * dims rotary_dim .. head_dim - 1 pass through. A frequency is rounded to 2^-64
  * turns per position and whole turns drop out exactly, for any int64 position: the
  * phase is off by |p| 2^-65 turns at most (1.9e-7 radians at |p| = 2^40, 1.9e-4 at
- * 2^50; frequencies below 2^24 radians). cos, sin and the products are float32,
+ * 2^50; frequencies below 2^24 radians). A frequency that is infinite or NaN turns
+ * its pair into NaN at every position. cos, sin and the products are float32,
  * rounded once to the pool's dtype.
  * rotary_dim must be even and at most head_dim (else PKV_ERR_INVALID) and a
  * multiple of 16 (else PKV_ERR_UNSUPPORTED).

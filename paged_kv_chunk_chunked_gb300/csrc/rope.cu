@@ -64,20 +64,28 @@ __device__ __forceinline__ uint64_t turns_fixed(float f) {
     return (bits >> 31) ? 0ull - r : r;
 }
 
-__device__ __forceinline__ void fill_turns(uint64_t* fix, const RopeArgs& r) {
-    for (int i = threadIdx.x; i < r.half; i += blockDim.x) fix[i] = turns_fixed(r.inv_freq[i]);
-    __syncthreads();
+// Fills the CTA's table; whether a frequency is not finite, which no fraction of a turn is.
+__device__ __forceinline__ bool fill_turns(uint64_t* fix, const RopeArgs& r) {
+    bool bad = false;
+    for (int i = threadIdx.x; i < r.half; i += blockDim.x) {
+        const float f = r.inv_freq[i];
+        bad |= !isfinite(f);
+        fix[i] = turns_fixed(f);
+    }
+    return __syncthreads_or(bad);
 }
 
 // cos and sin of the N pairs from pair i0 on, at position pos (SIGN -1: of the
-// opposite angle).
+// opposite angle). bad: fill_turns'.
 template <int N, int SIGN>
-__device__ __forceinline__ void cos_sin(const uint64_t* fix, int i0, int64_t pos, float (&c)[N], float (&s)[N]) {
+__device__ __forceinline__ void cos_sin(const uint64_t* fix, const RopeArgs& r, bool bad, int i0, int64_t pos, float (&c)[N],
+                                        float (&s)[N]) {
 #pragma unroll
     for (int e = 0; e < N; ++e) {
         const uint64_t phase = (uint64_t)pos * fix[i0 + e];
         // Signed leading half: [-1/2, 1/2) turn; in half turns for sincospif.
-        const float t = (float)(int32_t)(phase >> 32) * (1.0f / 2147483648.0f);
+        float t = (float)(int32_t)(phase >> 32) * (1.0f / 2147483648.0f);
+        if (bad && !isfinite(r.inv_freq[i0 + e])) t = __uint_as_float(0x7fc00000u);      // NaN, as p * f would give
         sincospif(t, &s[e], &c[e]);
         if (SIGN < 0) s[e] = -s[e];
     }
@@ -162,10 +170,10 @@ __device__ __forceinline__ void rotate_rows(const RowsArgs& a, const RopeArgs& r
             xb[h] = reinterpret_cast<const uint4*>(src + h * D)[vb];
         }
     const int64_t pos = r.positions && nh > 0 ? r.positions[t] : r.pos0 + t;
-    fill_turns(fix, r);
+    const bool bad = fill_turns(fix, r);
     if (rot && nh > 0) {
         float c[EPV], s[EPV];
-        cos_sin<EPV, SIGN>(fix, v * EPV, pos, c, s);
+        cos_sin<EPV, SIGN>(fix, r, bad, v * EPV, pos, c, s);
 #pragma unroll
         for (int h = 0; h < kHeadGroup; ++h)
             if (h < nh) {
@@ -262,7 +270,7 @@ __global__ void __launch_bounds__(kThreads) append_rope_kernel(AppendArgs a, int
 #pragma unroll
     for (int e = 0; e < EPV; ++e) acc_a[e] = acc_b[e] = 0.f;
     constexpr int U = 2;                          // rows in flight per thread
-    bool table = false;
+    bool table = false, bad = false;
     for (int rb0 = 0; rb0 < P; rb0 += U * RSTEP) {
         const int rb = rb0 + r0;
         uint4 ka[U], kb[U], wa[U], wb[U];
@@ -284,7 +292,7 @@ __global__ void __launch_bounds__(kThreads) append_rope_kernel(AppendArgs a, int
                 kb[u] = reinterpret_cast<const uint4*>(kpage + (size_t)row * D)[vb];
             }
         }
-        if (!table) fill_turns(fix, r);           // while the first rows' loads are on their way
+        if (!table) bad = fill_turns(fix, r);           // while the first rows' loads are on their way
         table = true;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -296,7 +304,7 @@ __global__ void __launch_bounds__(kThreads) append_rope_kernel(AppendArgs a, int
                 if (rot && pos < new_len) {
                     const int64_t t = pos - a.old_len;
                     float c[EPV], s[EPV];
-                    cos_sin<EPV, 1>(fix, v * EPV, r.positions ? r.positions[t] : r.pos0 + t, c, s);
+                    cos_sin<EPV, 1>(fix, r, bad, v * EPV, r.positions ? r.positions[t] : r.pos0 + t, c, s);
                     widen16<T>(ka[u], fa);
                     widen16<T>(kb[u], fb);
                     turn<EPV>(fa, fb, c, s, r.interleaved);
@@ -401,12 +409,12 @@ __global__ void __launch_bounds__(kThreads) rope_grad_kernel(GradArgs a, RowsArg
         }
     }
     const int64_t pos = r.positions && live ? r.positions[t] : r.pos0 + t;
-    fill_turns(fix, r);
+    const bool bad = fill_turns(fix, r);
     if (!ok) return;
     if (a.dk) {
         if (v < r.half / EPV) {
             float c[EPV], s[EPV];
-            cos_sin<EPV, -1>(fix, v * EPV, pos, c, s);
+            cos_sin<EPV, -1>(fix, r, bad, v * EPV, pos, c, s);
             turn<EPV>(fa, fb, c, s, r.interleaved);
         }
         uint4* d = reinterpret_cast<uint4*>(static_cast<T*>(a.dk) + t * a.dk_stride + (size_t)h * D);

@@ -395,3 +395,39 @@ def test_far_positions_within_half_a_unit(pos0, theta):
         assert (np.abs(got[:, d // 2:] - (b * c + a * s)) <= tol).all()
     finally:
         B.pkv_pool_destroy(pool)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_a_frequency_that_is_not_finite_gives_nan(dtype, bad):
+    """In its own pair, whatever the position; the other pairs keep their values."""
+    dt, kind = DT[dtype]
+    n, Hq, Hkv, d, P = 20, 3, 1, 64, 16
+    inv = _inv_freq(d)
+    inv[5] = bad
+    q, k, v = _rows(n, (Hq, Hkv, Hkv), d, dt, True, 60)
+    pool = B.pkv_pool_create(P, Hkv, Hq, d, kind, 2)
+    try:
+        seq, rope = B.pkv_seq_create(pool), B.rope(inv.cuda())
+        out, back = torch.empty(n, Hq, d, dtype=dt, device="cuda"), torch.empty(n, Hq, d, dtype=dt, device="cuda")
+        B.pkv_append_rope(seq, q, out, k, v, n, rope)
+        kg, vg, dk = (torch.empty(n, Hkv, d, dtype=dt, device="cuda") for _ in range(3))
+        B.pkv_gather(seq, kg, vg)
+        B.pkv_rope_rows(pool, q, back, n, Hq, rope, inverse=True)
+        g = torch.randn(n, Hkv, d, device="cuda")
+        B.pkv_grad_accumulate(seq, 0, n, g, g)
+        B.pkv_rope_grad(seq, 0, n, rope, dk_out=dk)
+        torch.cuda.synchronize()
+        assert torch.equal(vg, v)
+        fine = _inv_freq(d)
+        fine[5] = 0.0
+        pair = np.zeros(d, dtype=bool)
+        pair[[5, d // 2 + 5]] = True
+        for got, x, sign in ((out, q, 1), (kg, k, 1), (back, q, -1), (dk, g, -1)):
+            got = _f64(got)
+            assert np.isnan(got[..., pair]).all()
+            want, mag = _turn(_f64(x), fine, np.arange(n), False, sign)
+            tol = ROT * mag + (torch.finfo(dt).eps / 2) * (np.abs(want) + ROT * mag)
+            assert (np.abs(got - want) <= tol)[..., ~pair].all()
+    finally:
+        B.pkv_pool_destroy(pool)
