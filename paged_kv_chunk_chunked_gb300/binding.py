@@ -212,11 +212,18 @@ def _typed(x, name: str, dtype: str, n=None):
     return ptr(x)
 
 
-def rope(inv_freq, pos0: int = 0, positions=None, interleaved: bool = False) -> pkv_rope:
+def rope(inv_freq, pos0: int = 0, positions=None, interleaved: bool = False, rotary_dim: Optional[int] = None) -> pkv_rope:
     """The rotation of a call: inv_freq float32 [rotary_dim / 2], positions int64
-    [n] (one per row) or None for pos0 + row. Keeps the tensors alive."""
-    r = pkv_rope(_typed(inv_freq, "inv_freq", "float32"), _typed(positions, "positions", "int64"),
-                 int(pos0), 2 * inv_freq.numel(), 1 if interleaved else 0)
+    [n] (one per row) or None for pos0 + row. Keeps the tensors alive. inv_freq may
+    be an address, with rotary_dim given."""
+    p = _typed(inv_freq, "inv_freq", "float32")
+    n = None if inv_freq is None or isinstance(inv_freq, int) else 2 * inv_freq.numel()
+    if n is None and rotary_dim is None:
+        raise ValueError("inv_freq is not a tensor: rotary_dim is needed")
+    if n is not None and rotary_dim not in (None, n):
+        raise ValueError(f"inv_freq must have rotary_dim / 2 = {rotary_dim // 2} elements, got {n // 2}")
+    r = pkv_rope(p, _typed(positions, "positions", "int64"), int(pos0), n if n is not None else int(rotary_dim),
+                 1 if interleaved else 0)
     r.tensors = (inv_freq, positions)
     return r
 
@@ -225,9 +232,9 @@ def _rope(r: Optional[pkv_rope], n: int, dev=None):
     if r is None:
         return None
     inv_freq, pos = getattr(r, "tensors", (None, None))
-    if inv_freq is not None:
+    if inv_freq is not None and not isinstance(inv_freq, int):
         _on_device(inv_freq, dev)
-    if pos is not None:
+    if pos is not None and not isinstance(pos, int):
         _on_device(pos, dev)
         if pos.numel() != n:
             raise ValueError(f"positions must have one entry per row ({n}), got {pos.numel()}")

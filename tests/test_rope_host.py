@@ -114,3 +114,19 @@ def test_binding_refuses_tensors_it_cannot_describe(seq):
             B.pkv_append_rope(s, None, None, 64, 64, 4, r)
     assert B.rows_ptr(torch.zeros(4, 8, 64)[:, 2:5], 4)[1] == 512
     assert B.rows_ptr(torch.zeros(1, 8, 64)[:, 2:5], 1)[1] == 0
+
+
+def test_rotation_from_addresses(seq):
+    """inv_freq and positions as addresses, like every other operand of the binding."""
+    pool, s = seq
+    r = B.rope(1 << 20, pos0=7, positions=1 << 21, rotary_dim=32)
+    assert (r.inv_freq, r.positions, r.pos0, r.rotary_dim, r.interleaved) == (1 << 20, 1 << 21, 7, 32, 0)
+    with pytest.raises(B.PkvError, match="META"):             # every check before the pool's passes
+        B.pkv_rope_rows(pool, 64, 64, 4, 2, r)
+    inv = torch.ones(32)
+    assert B.rope(inv, rotary_dim=64).rotary_dim == 64
+    for bad in (lambda: B.rope(1 << 20), lambda: B.rope(None), lambda: B.rope(inv, rotary_dim=32)):
+        with pytest.raises(ValueError, match="inv_freq"):
+            bad()
+    with pytest.raises(B.PkvError, match="rotary_dim"):
+        B.pkv_rope_rows(pool, 64, 64, 4, 2, B.rope(1 << 20, rotary_dim=80))
