@@ -314,12 +314,15 @@ def pkv_pool_create(page_size, n_kv_heads, n_q_heads, head_dim, dtype=PKV_BF16,
                       num_phys_pages, n_device_slots, flags, 0)
     out = _P()
     _check(lib().pkv_pool_create(ctypes.byref(d), ctypes.byref(out)))
+    # (a tuple of the pool's own: its sequences' entries are the same object)
     _KIND[out.value] = (_torch_dtype(dtype), n_q_heads, n_kv_heads, head_dim)
     return out.value
 
 
 def pkv_pool_destroy(pool) -> None:
-    _KIND.pop(pool, None)
+    kind = _KIND.pop(pool, None)
+    for seq in [h for h, x in _KIND.items() if x is kind]:    # freed with the pool
+        del _KIND[seq]
     lib().pkv_pool_destroy(pool)
 
 

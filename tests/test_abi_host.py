@@ -144,3 +144,17 @@ def test_null_arguments(lib):
     lib.pkv_seq_free(None)
     n = ctypes.c_int64()
     assert lib.pkv_pool_free_pages(None, ctypes.byref(n)) == B.PKV_ERR_INVALID
+
+
+def test_the_binding_forgets_a_destroyed_pools_sequences(lib):
+    """What the binding knows of handles goes with them: a pool takes its sequences along."""
+    before = dict(B._KIND)
+    a, b = _meta_pool(), _meta_pool()
+    seqs = [B.pkv_seq_create(a) for _ in range(3)] + [B.pkv_seq_create(b)]
+    assert len(B._KIND) == len(before) + 6
+    B.pkv_seq_free(seqs[0])
+    B.pkv_pool_destroy(a)
+    assert set(B._KIND) - set(before) == {b, seqs[3]}
+    assert B._KIND[seqs[3]][1:] == (2, 1, 64)
+    B.pkv_pool_destroy(b)
+    assert B._KIND == before
