@@ -298,6 +298,16 @@ def _sel(sel) -> Optional[pkv_sel]:
     return ctypes.byref(s)
 
 
+def _mod_sel(sel, heads, dev) -> Optional[pkv_sel]:
+    """_sel of a call that checks its tensors: int32 [n_qp, Hkv, kmax], on its device."""
+    if sel is None:
+        return None
+    if str(sel.dtype) != "torch.int32" or sel.dim() != 3 or (heads and sel.shape[1] != heads):
+        raise ValueError(f"sel must be int32 [query pages, {heads or 'Hkv'}, kmax], got {sel.dtype} {tuple(sel.shape)}")
+    _on_device(sel, dev)
+    return _sel(sel)
+
+
 # ---------------------------------------------------------------- one function per entry point
 
 def pkv_last_error() -> str:
@@ -424,18 +434,18 @@ def pkv_chunk_attn_bwd(seq, q, o, dout, lse, q_start, n_q, dq, sel=None, stream=
 
 
 def pkv_chunk_attn_mod_fwd(seq, q, q_start, n_q, o, lse, mod, sel=None, stream=None) -> None:
-    (dt, hq, _, d), dev = _KIND.get(seq, _ANY), _device(stream)
+    (dt, hq, hkv, d), dev = _KIND.get(seq, _ANY), _device(stream)
     (qp, _), (op, _) = (_rows(x, n_q, hq, d, dt, dev, dense=True) for x in (q, o))
     _check(lib().pkv_chunk_attn_mod_fwd(seq, qp, q_start, n_q, op, _lse_ptr(lse, hq, n_q, dev),
-                                        _mod(mod, n_q, hq, dev), _sel(sel), stream_ptr(stream)))
+                                        _mod(mod, n_q, hq, dev), _mod_sel(sel, hkv, dev), stream_ptr(stream)))
 
 
 def pkv_chunk_attn_mod_bwd(seq, q, o, dout, lse, q_start, n_q, dq, mod, sel=None, stream=None) -> None:
-    (dt, hq, _, d), dev = _KIND.get(seq, _ANY), _device(stream)
+    (dt, hq, hkv, d), dev = _KIND.get(seq, _ANY), _device(stream)
     (qp, _), (op, _), (gp, _), (dp, _) = (_rows(x, n_q, hq, d, dt, dev, dense=True)
                                           for x in (q, o, dout, dq))
     _check(lib().pkv_chunk_attn_mod_bwd(seq, qp, op, gp, _lse_ptr(lse, hq, n_q, dev), q_start, n_q, dp,
-                                        _mod(mod, n_q, hq, dev), _sel(sel), stream_ptr(stream)))
+                                        _mod(mod, n_q, hq, dev), _mod_sel(sel, hkv, dev), stream_ptr(stream)))
 
 
 def pkv_chunk_attn_bwd_noalloc(seq, q, o, dout, lse, q_start, n_q, dq, sel=None,

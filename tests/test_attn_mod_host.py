@@ -88,3 +88,14 @@ def test_binding_refuses_another_gpus_tensors_without_a_stream_object(monkeypatc
         B._on_device(Stand(), dev)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
     B._on_device(Stand(), dev)
+
+
+def test_binding_checks_the_selection(seq):
+    """Its entries are read as int32 [query pages, Hkv, kmax] on the GPU."""
+    good = torch.zeros(1, 2, 3, dtype=torch.int32)
+    for bad, why in ((good.long(), "int32"), (good[:, :1], "sel must be"), (good[0], "sel must be"),
+                     (good.float(), "int32"), (good, "CUDA")):
+        with pytest.raises(ValueError, match=why):
+            B.pkv_chunk_attn_mod_fwd(seq, 64, 0, 4, 64, 64, B.score_mod(), bad)
+        with pytest.raises(ValueError, match=why):
+            B.pkv_chunk_attn_mod_bwd(seq, 64, 64, 64, 64, 0, 4, 64, B.score_mod(), bad)
