@@ -189,15 +189,16 @@ static void release_pages(pkv_seq* s) {
 
 // Uploads what the device copy of the block table lacks, on stream: entries that a
 // reset sequence gets back are there already, entries that pkv_seq_reserve claimed
-// are not. `from`: the first entry that this call claimed. A kernel reads them from
+// are not. `from`: the first entry that this call claimed; `captured`: the stream is
+// being captured. A kernel reads them from
 // the mapped pinned mirror: a copy-engine transfer on the compute stream would queue
 // behind bulk host-to-device copies issued on other streams (the inputs of later
 // chunks) and hold the next kernel back.
-static pkv_status upload_bt(pkv_seq* s, int64_t from, cudaStream_t st) {
+static pkv_status upload_bt(pkv_seq* s, int64_t from, bool captured, cudaStream_t st) {
     if (!is_device(s->pool)) return PKV_OK;
     const int64_t end = (int64_t)s->bt.size(), start = std::min(s->n_sent, end);
     cudaError_t e = cudaSuccess;
-    if (capturing(st)) {
+    if (captured) {
         // The graph uploads what this call claimed, whenever it is replayed. Nothing has
         // been sent yet, and an event of the capture would mean nothing outside it.
         const int64_t first = std::min(start, from);
@@ -543,14 +544,14 @@ pkv_status pkv_set_block_table(pkv_seq* s, const int32_t* bt, int64_t n) {
 
 }  // extern "C"
 
-pkv_status pkv::append_begin(pkv_seq* s, int64_t n_tok, cudaStream_t cs, AppendArgs* a, const char* who) {
+pkv_status pkv::append_begin(pkv_seq* s, int64_t n_tok, bool captured, cudaStream_t cs, AppendArgs* a, const char* who) {
     pkv_pool* p = s->pool;
     pkv_status st = check_stream_device(p);
     if (st != PKV_OK) return st;
     const int64_t old_pages = (int64_t)s->bt.size();
     st = claim_pages(s, s->len + n_tok);
     if (st != PKV_OK) return st;
-    st = upload_bt(s, old_pages, cs);
+    st = upload_bt(s, old_pages, captured, cs);
     if (st != PKV_OK) return st;
     if (s->d_slot_of && s->len % p->desc.page_size != 0) {
         // Extending a partial page that may be staged: its slot's K/V goes stale.
@@ -584,7 +585,7 @@ pkv_status pkv_append(pkv_seq* s, const void* k, const void* v, int64_t n_tok, v
     if (!is_device(s->pool)) return fail(PKV_ERR_INVALID, "pkv_append: META pool holds no data");
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     AppendArgs a{};
-    const pkv_status st = append_begin(s, n_tok, cs, &a, "pkv_append");
+    const pkv_status st = append_begin(s, n_tok, capturing(cs), cs, &a, "pkv_append");
     if (st != PKV_OK) return st;
     a.k_in = k; a.v_in = v;
     return append_end(s, n_tok, launch_append(a, cs), cs, "pkv_append");

@@ -533,7 +533,7 @@ pkv_status pkv_append_rope(pkv_seq* s, const void* q, int64_t q_stride, void* q_
         if (capturing(cs))
             return fail(PKV_ERR_INVALID, "pkv_append_rope: an append advances the sequence on the host and cannot be captured");
         AppendArgs a{};
-        st = append_begin(s, n_tok, cs, &a, who);
+        st = append_begin(s, n_tok, false, cs, &a, who);
         if (st != PKV_OK) return st;
         a.k_in = k;
         a.v_in = v;
