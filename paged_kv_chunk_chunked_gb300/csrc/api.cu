@@ -190,10 +190,9 @@ static void release_pages(pkv_seq* s) {
 // Uploads what the device copy of the block table lacks, on stream: entries that a
 // reset sequence gets back are there already, entries that pkv_seq_reserve claimed
 // are not. `from`: the first entry that this call claimed; `captured`: the stream is
-// being captured. A kernel reads them from
-// the mapped pinned mirror: a copy-engine transfer on the compute stream would queue
-// behind bulk host-to-device copies issued on other streams (the inputs of later
-// chunks) and hold the next kernel back.
+// being captured. A kernel reads them from the mapped pinned mirror: a copy-engine
+// transfer on the compute stream would queue behind bulk host-to-device copies issued
+// on other streams (the inputs of later chunks) and hold the next kernel back.
 static pkv_status upload_bt(pkv_seq* s, int64_t from, bool captured, cudaStream_t st) {
     if (!is_device(s->pool)) return PKV_OK;
     const int64_t end = (int64_t)s->bt.size(), start = std::min(s->n_sent, end);

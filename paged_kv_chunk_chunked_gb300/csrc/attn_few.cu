@@ -349,7 +349,13 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
 }  // namespace
 
 // Up to 16 queries: their 16-row tiles read each key ceil(n_q g / 16) times (from
-// L2 but for the first), the tensor-core kernel's 128-row tiles once per head.
+// L2 but for the first), the tensor-core kernel's 128-row tiles once per head. Both
+// sides on 131072 keys, this kernel and the tensor-core one, us (cap 50):
+//              n_q = 8       16         24
+//   28/4 d 128  138  257   237  259   384  257
+//   64/8 d 64   204  507   400  507   789  508
+//   8/8 d 128    87  142    90  142   139  142
+//   32/2 d 128  138  259   292  257   384  257   (groups of 16 cross over at 14)
 bool few_supported(const AttnArgs& a) {
     return a.dtype == PKV_BF16 && !a.sel && a.n_q <= 16 && a.P % kKeys == 0;
 }

@@ -633,7 +633,9 @@ bwd_kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 // Columns c, c + 1: weights P = 2^(pre v - LSE) and dS = P (dP - D) f, f the
                 // cap's derivative 1 - tanh^2 = 1 - (y / c2)^2. The cap's products and the
                 // exponentials go through one pass, so that the two pipes overlap. (-LSE and
-                // -D of four columns per 16-byte broadcast read.)
+                // -D of four columns per 16-byte broadcast read.) P and dS are rounded to
+                // bf16 here, as the plain kernels round them: what the tensor core takes,
+                // and 2^-8 of a weight at most, of either sign, under fp32 sums.
                 const bool capped = p.m.cap > 0.f;
                 const f32x2 one = pack2(1.f, 1.f), nc = pack2(p.m.neg_c2sq, p.m.neg_c2sq);
                 float4 nl, nd;

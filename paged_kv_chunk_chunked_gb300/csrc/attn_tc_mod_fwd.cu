@@ -21,8 +21,13 @@
 // Q stays in shared memory, where the A operand costs the tensor core a third
 // more per instruction. O is rescaled in tensor memory only when a row's maximum
 // grows by more than 2^8; S(j) complete says that PV(j-1) is, so no wait of its
-// own stands before that. Weights are rounded to bf16 for the product; their sum
-// l, and the LSE, come from the unrounded ones.
+// own stands before that. Weights are rounded to bf16 for the product (what the tensor
+// core takes); their sum l comes from the unrounded ones, so that the LSE, which the
+// backward forms P from, is fp32's. O is divided by the same l: where values share a
+// large common part it is off by the mean rounding of its row's weights, up to 2^-8 of
+// that part, which the plain kernel, dividing by the rounded weights' sum, is not; the
+// plain LSE carries that rounding instead. (Both sums would cost four more operations
+// a pair of keys in a loop that the softmax bounds.)
 // Pages are walked from the last to the first: the distance bias lets the maximum
 // grow towards the query's own position, and each growth costs a rescaling.
 #include <cuda_bf16.h>

@@ -168,8 +168,8 @@ struct AppendArgs {
 };
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t s);
 // The host side of an append of n_tok tokens: claims and uploads pages and fills
-// a (all but the inputs; captured: cs is being captured); append_end takes the launch's result and advances the
-// sequence.
+// a (all but the inputs; `captured`: cs is being captured); append_end takes the
+// launch's result and advances the sequence.
 pkv_status append_begin(pkv_seq* s, int64_t n_tok, bool captured, cudaStream_t cs, AppendArgs* a, const char* who);
 pkv_status append_end(pkv_seq* s, int64_t n_tok, cudaError_t launched, cudaStream_t cs, const char* who);
 
