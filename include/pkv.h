@@ -187,7 +187,8 @@ pkv_status pkv_set_block_table(pkv_seq* seq, const int32_t* bt, int64_t n);
  * On a capturing stream the sequence advances once, at the capture: each replay
  * stores k's and v's rows of that moment into the same pages again, and sends
  * their block-table entries itself. No replay may be running while the sequence
- * is reset or given other pages. */
+ * is reset or given other pages. Calls on a PINNED_HOST pool cannot be captured
+ * (PKV_ERR_INVALID). */
 pkv_status pkv_append(pkv_seq* seq, const void* k, const void* v, int64_t n_tok, void* stream);
 
 /* ---------------------------------------------------------------- rotation

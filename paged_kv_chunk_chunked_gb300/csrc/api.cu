@@ -583,8 +583,12 @@ pkv_status pkv_append(pkv_seq* s, const void* k, const void* v, int64_t n_tok, v
     if (!k || !v) return fail(PKV_ERR_INVALID, "pkv_append: k or v is NULL");
     if (!is_device(s->pool)) return fail(PKV_ERR_INVALID, "pkv_append: META pool holds no data");
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const bool captured = capturing(cs);
+    // (Prefetches wait for the event that an append records, and could not wait for a captured one.)
+    if (captured && s->used)
+        return fail(PKV_ERR_INVALID, "pkv_append: calls on a PINNED_HOST pool cannot be captured");
     AppendArgs a{};
-    const pkv_status st = append_begin(s, n_tok, capturing(cs), cs, &a, "pkv_append");
+    const pkv_status st = append_begin(s, n_tok, captured, cs, &a, "pkv_append");
     if (st != PKV_OK) return st;
     a.k_in = k; a.v_in = v;
     return append_end(s, n_tok, launch_append(a, cs), cs, "pkv_append");

@@ -172,3 +172,33 @@ def test_append_captured_with_other_pages_than_before():
         B.pkv_check(pool)
     finally:
         B.pkv_pool_destroy(pool)
+
+
+def test_append_to_a_pinned_pool_refuses_a_capture():
+    """Staging waits for the last append, which a captured one would never be: the
+    call claims nothing, and the capture and the sequence go on."""
+    pool = B.pkv_pool_create(16, 1, 2, 64, B.PKV_F32, 8, residency=B.PKV_RES_PINNED_HOST, n_device_slots=4)
+    try:
+        s, side = B.pkv_seq_create(pool), torch.cuda.Stream()
+        k, v = _rows(60, 1)
+        x, y = torch.zeros(4, device="cuda"), torch.ones(4, device="cuda")
+        torch.cuda.synchronize()
+        g, why = torch.cuda.CUDAGraph(), None
+        with torch.cuda.graph(g, stream=side):
+            try:
+                B.pkv_append(s, k, v, 60, side)
+            except B.PkvError as e:
+                why = e
+            x.add_(y)
+        length, free = B.pkv_seq_length(s), B.pkv_pool_free_pages(pool)
+        g.replay()
+        if not length:
+            B.pkv_append(s, k, v, 60, torch.cuda.current_stream())
+        B.pkv_prefetch(s, None, 0, 1, torch.cuda.current_stream())
+        B.pkv_wait(s, torch.cuda.current_stream())
+        assert _holds(s, k, v) and x.eq(1).all()
+        B.pkv_check(pool)
+        assert why is not None and why.status == B.PKV_ERR_INVALID and "captured" in str(why)
+        assert length == 0 and free == 8
+    finally:
+        B.pkv_pool_destroy(pool)
