@@ -98,9 +98,11 @@ __device__ __forceinline__ void load_row_tile(float (*dst)[D + 4], const void* s
     }
 }
 
-// Keys of [k0, k0 + n) have no usable page: an error where a row of the tile sees one.
-__device__ __noinline__ void bad_keys(const int32_t* bt, int64_t num_phys, int P, int64_t k0, int n, const int2* range, int* err) {
-    for (int64_t key = k0; key < k0 + n; ++key) {
+// Keys first, first + step, .. below end, some of them without a usable page: an error
+// where a row of the tile sees one.
+__device__ __noinline__ void bad_keys(const int32_t* bt, int64_t num_phys, int P, int64_t first, int64_t end, int step,
+                                      const int2* range, int* err) {
+    for (int64_t key = first; key < end; key += step) {
         const int32_t pp = bt[key / P];
         if (pp >= 0 && pp < num_phys) continue;
         bool seen = !range;
@@ -139,7 +141,8 @@ __device__ __forceinline__ void load_key_tile(float (*Ks)[D + 4], float (*Vs)[D 
             *reinterpret_cast<float4*>(&Vs[r][v * EPV + e]) = make_float4(fv[e], fv[e + 1], fv[e + 2], fv[e + 3]);
         }
     }
-    if (bad) bad_keys(a.bt, a.num_phys, a.P, k0, n, range, a.err);
+    // (Of the threads that share a row, the first.)
+    if (bad && tid % VPR == 0) bad_keys(a.bt, a.num_phys, a.P, k0 + tid / VPR, k0 + n, threads / VPR, range, a.err);
 }
 
 __device__ __forceinline__ float dot4(const float4& x, const float4& y, float acc) {
