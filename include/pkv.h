@@ -485,6 +485,131 @@ pkv_status pkv_wait(pkv_seq* seq, void* main, int64_t timeout_us);
  * Synchronizes the device. PINNED_HOST pools only (else PKV_ERR_INVALID). */
 pkv_status pkv_stage_stats(pkv_seq* seq, int64_t* kv_in, int64_t* grads_in, int64_t* grads_out);
 
+/* ---------------------------------------------------------------- linear attention
+ * The mixer of layers whose memory does not grow: one state S [d, d] (key x
+ * value) per KV head instead of pages. Token t of a sequence does
+ *   S_t = l S_{t-1} + k_t v_t^T        l = exp(log_decay[head]), float32 S
+ *   o_t = q_t^T S_t / sqrt(d)          query head h reads the state of KV head h / (Hq / Hkv)
+ * Long inputs are computed in chunks by matrix products, one token at a time by
+ * the recurrence itself. Products, sums and states are float32; bf16 calls on
+ * the tensor cores round the weighted scores of a chunk and the states that
+ * chunks start from to bf16 once, as operands of the products, and states (and
+ * their gradients) themselves not at all.
+ *
+ * pkv_lin is a store of states, as pkv_pool is one of pages: n_slots states of
+ * all KV heads, float32 [n_slots, Hkv, d, d], and with grads = 1 as many
+ * gradients of states. What a slot holds is up to the caller: a running
+ * request's state; in chunk-recurrent training slot c the state that chunk c
+ * starts from, so that the backward sweep finds it again. Calls on one store
+ * must not overlap on the GPU, but for pkv_lin_attn_step calls on different
+ * slots: the others share its scratch memory, grown on demand (a stream
+ * capture needs an earlier call of the same sizes, else PKV_ERR_INVALID). */
+typedef struct pkv_lin_desc {
+    int32_t n_kv_heads;        /* Hkv                                                    */
+    int32_t n_q_heads;         /* Hq, a multiple of Hkv                                  */
+    int32_t head_dim;          /* d; 64 or 128                                           */
+    int32_t dtype;             /* pkv_dtype of Q, K, V, O and their gradients            */
+    int32_t residency;         /* PKV_RES_DEVICE, or PKV_RES_META: argument checks only  */
+    int32_t grads;             /* 1: room for the states' gradients (pkv_lin_attn_bwd)   */
+    int64_t n_slots;
+    uint32_t flags;            /* PKV_FLAG_*                                             */
+    int32_t reserved;
+} pkv_lin_desc;
+
+typedef struct pkv_lin pkv_lin;
+
+/* Creates a store on the current CUDA device, all states and gradients zero.
+ * Synchronous. *out is NULL on failure. */
+pkv_status pkv_lin_create(const pkv_lin_desc* desc, pkv_lin** out);
+/* Frees the store. NULL-safe. Work on its memory must be complete. */
+void pkv_lin_destroy(pkv_lin* lin);
+/* Device addresses of the states and of their gradients (NULL without grads);
+ * either output may be NULL. Callers read, fill and copy slots through them. */
+pkv_status pkv_lin_arrays(const pkv_lin* lin, float** state, float** dstate);
+/* pkv_check of a store. */
+pkv_status pkv_lin_check(pkv_lin* lin);
+
+/* The sequences in the n rows of a call, and their states. Sequence b is rows
+ * cu[b] .. cu[b + 1] - 1 (it may be empty); rows before cu[0] and from
+ * cu[n_seq] on are not read, and their outputs left as they were. It starts from
+ * the state of slot slot_in[b] (-1: from zero) and leaves its last state in slot
+ * slot_out[b] (-1: nowhere); the two may be the same. The arrays are device
+ * memory, read when the kernels run: a range that is not in 0 .. n or descends
+ * and a slot that is not in -1 .. n_slots - 1 are recorded for pkv_lin_check (that
+ * sequence is left out, others of the call may come out wrong; the slot counts
+ * as -1). A slot must not be written for
+ * two sequences of a call, nor be written for one and read for another; several
+ * may start from one slot in the forward. */
+typedef struct pkv_lin_batch {
+    const int64_t* cu;         /* device int64 [n_seq + 1], or NULL: one sequence, all rows */
+    const int32_t* slot_in;    /* device int32 [n_seq], or NULL: all start from zero     */
+    const int32_t* slot_out;   /* device int32 [n_seq], or NULL: no last state is kept   */
+    int64_t n_seq;             /* 1 if cu is NULL                                        */
+} pkv_lin_batch;
+
+/* O [n, Hq, d] of Q [n, Hq, d], K, V [n, Hkv, d]. Operands have row strides as
+ * for the rotation calls (0 = dense; 16-byte alignment; no overlap of an output
+ * with anything). log_decay: device float32 [Hkv], or NULL for no decay; 0 is no
+ * decay, -inf a memory of the token itself alone. */
+pkv_status pkv_lin_attn_fwd(pkv_lin* lin, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                            const void* v, int64_t v_stride, void* o, int64_t o_stride, int64_t n,
+                            const float* log_decay, const pkv_lin_batch* batch, void* stream);
+
+/* The gradients of pkv_lin_attn_fwd: dQ, dK, dV written (rows of the sequences).
+ * batch is the forward's, and slot_in's states must be those that it started
+ * from (a forward that wrote slot_out = slot_in has overwritten them). The
+ * gradient of a sequence's last state is read from slot_out's gradient (-1:
+ * zero), that of its first one written to slot_in's. No gradient of log_decay is
+ * computed. The order of all sums is fixed. */
+pkv_status pkv_lin_attn_bwd(pkv_lin* lin, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                            const void* v, int64_t v_stride, const void* dout, int64_t dout_stride, void* dq,
+                            int64_t dq_stride, void* dk, int64_t dk_stride, void* dv, int64_t dv_stride,
+                            int64_t n, const float* log_decay, const pkv_lin_batch* batch, void* stream);
+
+/* One token for each of n sequences: row i advances the state of slot slots[i]
+ * (device int32 [n]) in place and writes o's row i. A row with slot -1 is
+ * padding: its o is left as it was. No slot may appear twice. */
+pkv_status pkv_lin_attn_step(pkv_lin* lin, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                             const void* v, int64_t v_stride, void* o, int64_t o_stride, int64_t n,
+                             const float* log_decay, const int32_t* slots, void* stream);
+
+/* ---------------------------------------------------------------- layer norm
+ * y = (x - mean) rstd w + b over each group of `width` consecutive columns of a
+ * row: groups = 1 normalises whole rows, groups = heads each head of the
+ * mixer's output with its own weights. mean and rstd = 1 / sqrt(var + eps) are
+ * float32 (var: the mean square of x - mean). */
+typedef struct pkv_norm {
+    int32_t dtype;             /* pkv_dtype of x, y and their gradients                  */
+    int32_t w_dtype;           /* pkv_dtype of weight and bias                           */
+    int32_t groups;
+    float eps;                 /* >= 0                                                   */
+    int64_t width;             /* columns of a group, 1 .. 32768                         */
+    const void* weight;        /* device [groups * width], or NULL: 1                    */
+    const void* bias;          /* device [groups * width], or NULL: 0                    */
+} pkv_norm;
+
+/* y [n, groups * width] of x; mean and rstd (float32 [n, groups], for the
+ * backward) may both be NULL. Rows may lie apart (strides in elements, 0 =
+ * dense, at least groups * width). Addresses need their type's alignment only;
+ * 16-byte aligned rows of whole 16-byte vectors are read by vectors. y may be x
+ * itself (same pointer and stride). Runs on the current device. */
+pkv_status pkv_layer_norm_fwd(const void* x, int64_t x_stride, void* y, int64_t y_stride, float* mean,
+                              float* rstd, int64_t n, const pkv_norm* norm, void* stream);
+
+/* Floats of scratch that pkv_layer_norm_bwd needs for n rows. */
+pkv_status pkv_layer_norm_scratch(const pkv_norm* norm, int64_t n, int64_t* floats);
+
+/* dx (NULL: not wanted; may be dy itself) and the gradients of weight and bias,
+ * dw and db float32 [groups * width] (each may be NULL): written, or with
+ * accumulate = 1 added to what they hold (chunks of a sweep, as dK/dV in their
+ * pages). mean and rstd are the forward's. scratch: the caller's, 16-byte
+ * aligned, as long as pkv_layer_norm_scratch says; only calls that may overlap
+ * need scratch of their own. The order of all sums is fixed. */
+pkv_status pkv_layer_norm_bwd(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,
+                              const float* mean, const float* rstd, void* dx, int64_t dx_stride, float* dw,
+                              float* db, int32_t accumulate, float* scratch, int64_t n, const pkv_norm* norm,
+                              void* stream);
+
 /* ---------------------------------------------------------------- profiling
  * Per-kernel device time, for benchmarks. pkv_profile_enable(1) clears old
  * records and makes every later kernel launch record a CUDA event pair on its

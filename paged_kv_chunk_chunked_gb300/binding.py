@@ -7,6 +7,7 @@ fallback: ``lib()`` raises if libpkv.so is missing or does not load.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -55,6 +56,26 @@ class pkv_score_mod(ctypes.Structure):
                 ("k_end", ctypes.c_void_p)]
 
 
+class pkv_lin_desc(ctypes.Structure):
+    _fields_ = [("n_kv_heads", ctypes.c_int32), ("n_q_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("residency", ctypes.c_int32), ("grads", ctypes.c_int32),
+                ("n_slots", ctypes.c_int64), ("flags", ctypes.c_uint32),
+                ("reserved", ctypes.c_int32)]
+
+
+class pkv_lin_batch(ctypes.Structure):
+    _fields_ = [("cu", ctypes.c_void_p), ("slot_in", ctypes.c_void_p),
+                ("slot_out", ctypes.c_void_p), ("n_seq", ctypes.c_int64)]
+
+
+class pkv_norm(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("width", ctypes.c_int64), ("weight", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p)]
+
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
@@ -100,6 +121,17 @@ _SIGS = {
     "pkv_stage_stats": (_ST, [_P, ctypes.POINTER(_I64), ctypes.POINTER(_I64), ctypes.POINTER(_I64)]),
     "pkv_wait": (_ST, [_P, _P, _I64]),
     "pkv_selftest_umma": (_ST, [_I32, _P, _P, _P, _I32, _I32]),
+    "pkv_lin_create": (_ST, [ctypes.POINTER(pkv_lin_desc), ctypes.POINTER(_P)]),
+    "pkv_lin_destroy": (None, [_P]),
+    "pkv_lin_arrays": (_ST, [_P] + [ctypes.POINTER(_P)] * 2),
+    "pkv_lin_check": (_ST, [_P]),
+    "pkv_lin_attn_fwd": (_ST, [_P] + [_P, _I64] * 4 + [_I64, _P, ctypes.POINTER(pkv_lin_batch), _P]),
+    "pkv_lin_attn_bwd": (_ST, [_P] + [_P, _I64] * 7 + [_I64, _P, ctypes.POINTER(pkv_lin_batch), _P]),
+    "pkv_lin_attn_step": (_ST, [_P] + [_P, _I64] * 4 + [_I64, _P, _P, _P]),
+    "pkv_layer_norm_fwd": (_ST, [_P, _I64, _P, _I64, _P, _P, _I64, ctypes.POINTER(pkv_norm), _P]),
+    "pkv_layer_norm_scratch": (_ST, [ctypes.POINTER(pkv_norm), _I64, ctypes.POINTER(_I64)]),
+    "pkv_layer_norm_bwd": (_ST, [_P, _I64, _P, _I64, _P, _P, _P, _I64, _P, _P, _I32, _P, _I64,
+                                 ctypes.POINTER(pkv_norm), _P]),
     "pkv_profile_enable": (_ST, [_I32]),
     "pkv_profile_collect": (_ST, [_I32, _P, _P, _P, ctypes.POINTER(_I32)]),
 }
@@ -155,6 +187,15 @@ def _torch_dtype(dtype):
 def _device(stream):
     """The stream's device, which a call's tensors must be on; None: the current one."""
     return getattr(stream, "device_index", None)
+
+
+def _current(dev):
+    """The stream's device as the current one, for calls without a handle (whose
+    kernels run on the current device); None leaves it as it is."""
+    if dev is None:
+        return contextlib.nullcontext()
+    import torch
+    return torch.cuda.device(dev)
 
 
 def _on_device(x, dev) -> None:
@@ -507,6 +548,161 @@ def pkv_stage_stats(seq) -> dict:
 
 def pkv_wait(seq, main=None, timeout_us=10_000_000) -> None:
     _check(lib().pkv_wait(seq, stream_ptr(main), timeout_us))
+
+
+def pkv_lin_create(n_kv_heads, n_q_heads, head_dim, dtype=PKV_BF16, n_slots=1, grads=False,
+                   residency=PKV_RES_DEVICE, flags=0) -> int:
+    d = pkv_lin_desc(n_kv_heads, n_q_heads, head_dim, dtype, residency, 1 if grads else 0, n_slots, flags, 0)
+    out = _P()
+    _check(lib().pkv_lin_create(ctypes.byref(d), ctypes.byref(out)))
+    _KIND[out.value] = (_torch_dtype(dtype), n_q_heads, n_kv_heads, head_dim)
+    return out.value
+
+
+def pkv_lin_destroy(lin) -> None:
+    _KIND.pop(lin, None)
+    lib().pkv_lin_destroy(lin)
+
+
+def pkv_lin_arrays(lin) -> dict:
+    """Addresses of the float32 [n_slots, Hkv, d, d] states and of their gradients (None without)."""
+    s, g = _P(), _P()
+    _check(lib().pkv_lin_arrays(lin, ctypes.byref(s), ctypes.byref(g)))
+    return {"state": s.value, "dstate": g.value}
+
+
+def pkv_lin_check(lin) -> None:
+    _check(lib().pkv_lin_check(lin))
+
+
+def lin_batch(n_seq: int = 1, cu=None, slot_in=None, slot_out=None) -> pkv_lin_batch:
+    """The sequences of a call: cu int64 [n_seq + 1] (None: one sequence of all
+    rows), slot_in and slot_out int32 [n_seq] or None. Keeps the tensors alive."""
+    b = pkv_lin_batch(_typed(cu, "cu", "int64", n_seq + 1), _typed(slot_in, "slot_in", "int32", n_seq),
+                      _typed(slot_out, "slot_out", "int32", n_seq), int(n_seq))
+    b.tensors = (cu, slot_in, slot_out)
+    return b
+
+
+def _lin_arrays(dev, *arrays) -> None:
+    for x in arrays:
+        if x is not None and not isinstance(x, int):
+            _on_device(x, dev)
+
+
+def _decay(x, heads):
+    return _typed(x, "log_decay", "float32", heads)
+
+
+def pkv_lin_attn_fwd(lin, q, k, v, o, n, log_decay, batch, stream=None) -> None:
+    """q, k, v, o: tensors [n, heads, d] whose rows may lie apart."""
+    (dt, hq, hkv, d), dev = _KIND.get(lin, _ANY), _device(stream)
+    at = [y for x, h in ((q, hq), (k, hkv), (v, hkv), (o, hq)) for y in _rows(x, n, h, d, dt, dev)]
+    _lin_arrays(dev, log_decay, *getattr(batch, "tensors", ()))
+    _check(lib().pkv_lin_attn_fwd(lin, *at, n, _decay(log_decay, hkv), ctypes.byref(batch), stream_ptr(stream)))
+
+
+def pkv_lin_attn_bwd(lin, q, k, v, dout, dq, dk, dv, n, log_decay, batch, stream=None) -> None:
+    """All seven: tensors [n, heads, d] whose rows may lie apart."""
+    (dt, hq, hkv, d), dev = _KIND.get(lin, _ANY), _device(stream)
+    at = [y for x, h in ((q, hq), (k, hkv), (v, hkv), (dout, hq), (dq, hq), (dk, hkv), (dv, hkv))
+          for y in _rows(x, n, h, d, dt, dev)]
+    _lin_arrays(dev, log_decay, *getattr(batch, "tensors", ()))
+    _check(lib().pkv_lin_attn_bwd(lin, *at, n, _decay(log_decay, hkv), ctypes.byref(batch), stream_ptr(stream)))
+
+
+def pkv_lin_attn_step(lin, q, k, v, o, n, log_decay, slots, stream=None) -> None:
+    """q, k, v, o: tensors [n, heads, d] whose rows may lie apart; slots int32 [n]."""
+    (dt, hq, hkv, d), dev = _KIND.get(lin, _ANY), _device(stream)
+    at = [y for x, h in ((q, hq), (k, hkv), (v, hkv), (o, hq)) for y in _rows(x, n, h, d, dt, dev)]
+    _lin_arrays(dev, log_decay, slots)
+    _check(lib().pkv_lin_attn_step(lin, *at, n, _decay(log_decay, hkv), _typed(slots, "slots", "int32", n),
+                                   stream_ptr(stream)))
+
+
+def norm(width, groups: int = 1, eps: float = 1e-5, weight=None, bias=None, dtype=PKV_BF16, w_dtype=None) -> pkv_norm:
+    """The normalisation of a call: rows of groups * width columns in `dtype`; weight
+    and bias [groups * width], both bfloat16 or both float32 (w_dtype, where they are
+    addresses), or None. Keeps the tensors alive."""
+    kinds = {"torch.bfloat16": PKV_BF16, "torch.float32": PKV_F32}
+    for name, x in (("weight", weight), ("bias", bias)):
+        if x is None or isinstance(x, int):
+            continue
+        if str(x.dtype) not in kinds or w_dtype not in (None, kinds[str(x.dtype)]):
+            raise ValueError(f"weight and bias must both be bfloat16 or both float32, got {x.dtype} for {name}")
+        w_dtype = kinds[str(x.dtype)]
+        if x.numel() != groups * width:
+            raise ValueError(f"{name} must have groups * width = {groups * width} elements, got {x.numel()}")
+    m = pkv_norm(int(dtype), dtype if w_dtype is None else w_dtype, int(groups), float(eps), int(width), ptr(weight), ptr(bias))
+    m.tensors = (weight, bias)
+    return m
+
+
+def _norm_rows(x, n: int, m: pkv_norm, dev, name: str):
+    """(address, row stride) of a tensor [n, columns] (any shape that has these
+    columns in its trailing dimensions), an int, or None."""
+    if x is None or isinstance(x, int):
+        return x, 0
+    cols = m.groups * m.width
+    if x.dtype != _torch_dtype(m.dtype):
+        raise ValueError(f"{name} must be {_torch_dtype(m.dtype)}, got {x.dtype}")
+    if x.dim() < 1 or x.shape[0] != n or x.numel() != n * cols:
+        raise ValueError(f"{name} must have {n} rows of {cols} columns, got shape {tuple(x.shape)}")
+    dense = 1                                 # every row dense memory of its own
+    for size, stride in zip(reversed(x.shape[1:]), reversed(x.stride()[1:])):
+        if size > 1 and stride != dense and n:
+            raise ValueError(f"{name} of shape {tuple(x.shape)} with strides {x.stride()}: rows must be dense")
+        dense *= size
+    if n > 1 and x.stride(0) < cols:
+        raise ValueError(f"{name} of shape {tuple(x.shape)} with strides {x.stride()}: rows overlap")
+    _on_device(x, dev)
+    return x.data_ptr(), (x.stride(0) if n > 1 else 0)
+
+
+def _floats(x, n: int, dev, name: str):
+    p = _typed(x, name, "float32", n)
+    if x is not None and not isinstance(x, int):
+        _on_device(x, dev)
+    return p
+
+
+def _norm_vectors(m: pkv_norm, dev) -> None:
+    _lin_arrays(dev, *getattr(m, "tensors", ()))
+
+
+def pkv_layer_norm_fwd(x, y, mean, rstd, n, norm, stream=None) -> None:
+    """x, y: tensors of n rows that may lie apart; mean, rstd float32 [n, groups] or None."""
+    dev = _device(stream)
+    (xp, xs), (yp, ys) = _norm_rows(x, n, norm, dev, "x"), _norm_rows(y, n, norm, dev, "y")
+    _norm_vectors(norm, dev)
+    m, r = (_floats(t, n * norm.groups, dev, w) for t, w in ((mean, "mean"), (rstd, "rstd")))
+    with _current(dev):
+        _check(lib().pkv_layer_norm_fwd(xp, xs, yp, ys, m, r, n, ctypes.byref(norm), stream_ptr(stream)))
+
+
+def pkv_layer_norm_scratch(norm, n) -> int:
+    """Floats of scratch that pkv_layer_norm_bwd needs for n rows."""
+    f = _I64()
+    _check(lib().pkv_layer_norm_scratch(ctypes.byref(norm), n, ctypes.byref(f)))
+    return f.value
+
+
+def pkv_layer_norm_bwd(dy, x, mean, rstd, dx, dw, db, n, norm, scratch, accumulate=False, stream=None) -> None:
+    """dy, x, dx: tensors of n rows that may lie apart; mean, rstd the forward's;
+    dw, db float32 [groups * width], each or dx may be None."""
+    dev = _device(stream)
+    at = [y for t, w in ((dy, "dy"), (x, "x"), (dx, "dx")) for y in _norm_rows(t, n, norm, dev, w)]
+    _norm_vectors(norm, dev)
+    m, r = (_floats(t, n * norm.groups, dev, w) for t, w in ((mean, "mean"), (rstd, "rstd")))
+    gw, gb = (_floats(t, norm.groups * norm.width, dev, w) for t, w in ((dw, "dw"), (db, "db")))
+    if scratch is not None and not isinstance(scratch, int):
+        need = pkv_layer_norm_scratch(norm, n) if gw or gb else 0
+        if scratch.numel() < need:
+            raise ValueError(f"scratch must have {need} floats, got {scratch.numel()}")
+        scratch = _floats(scratch, None, dev, "scratch")
+    with _current(dev):
+        _check(lib().pkv_layer_norm_bwd(*at[:4], m, r, *at[4:], gw, gb, 1 if accumulate else 0, scratch, n,
+                                        ctypes.byref(norm), stream_ptr(stream)))
 
 
 def pkv_profile_enable(on: bool) -> None:

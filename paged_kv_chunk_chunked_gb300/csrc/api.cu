@@ -227,6 +227,25 @@ pkv_status pkv::check_stream_device(const pkv_pool* p) {
     return PKV_OK;
 }
 
+pkv_status pkv::take_device_error(int* d_err, const char* who) {
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e != cudaSuccess) return cuda_fail(e, (std::string(who) + ": cudaDeviceSynchronize").c_str());
+    int h = 0;
+    e = cudaMemcpy(&h, d_err, sizeof(int), cudaMemcpyDeviceToHost);
+    if (e != cudaSuccess) return cuda_fail(e, (std::string(who) + ": read error word").c_str());
+    if (h == 0) return PKV_OK;
+    int zero = 0;
+    cudaMemcpy(d_err, &zero, sizeof(int), cudaMemcpyHostToDevice);
+    const char* what = h == pkv::kErrWaitTimeout ? "a bounded wait expired"
+                     : h == pkv::kErrBadPage     ? "a page index was out of range"
+                     : h == pkv::kErrTmemAlloc   ? "tensor-memory allocation failed"
+                     : h == pkv::kErrSlots       ? "more pages staged than device slots"
+                     : h == pkv::kErrBadSeq      ? "a sequence's rows were not a range of the call's rows"
+                     : h == pkv::kErrBadSlot     ? "a state slot was out of range"
+                                                 : "unknown device error";
+    return fail(PKV_ERR_DEVICE_FAULT, std::string("device error ") + std::to_string(h) + ": " + what);
+}
+
 // ---------------------------------------------------------------- C ABI
 
 extern "C" {
@@ -236,23 +255,7 @@ const char* pkv_last_error(void) { return g_last_error.c_str(); }
 pkv_status pkv_check(pkv_pool* pool) {
     if (!pool) return fail(PKV_ERR_INVALID, "pkv_check: pool is NULL");
     if (!is_device(pool)) return PKV_OK;
-    cudaError_t e = cudaDeviceSynchronize();
-    if (e != cudaSuccess) return cuda_fail(e, "pkv_check: cudaDeviceSynchronize");
-    int h = 0;
-    e = cudaMemcpy(&h, pool->d_err, sizeof(int), cudaMemcpyDeviceToHost);
-    if (e != cudaSuccess) return cuda_fail(e, "pkv_check: read error word");
-    if (h != 0) {
-        int zero = 0;
-        cudaMemcpy(pool->d_err, &zero, sizeof(int), cudaMemcpyHostToDevice);
-        const char* what = h == pkv::kErrWaitTimeout ? "a bounded wait expired"
-                         : h == pkv::kErrBadPage     ? "a page index was out of range"
-                         : h == pkv::kErrTmemAlloc   ? "tensor-memory allocation failed"
-                         : h == pkv::kErrSlots       ? "more pages staged than device slots"
-                                                : "unknown device error";
-        return fail(PKV_ERR_DEVICE_FAULT, std::string("device error ") + std::to_string(h) +
-                                              ": " + what);
-    }
-    return PKV_OK;
+    return take_device_error(pool->d_err, "pkv_check");
 }
 
 pkv_status pkv_pool_create(const pkv_pool_desc* desc, pkv_pool** out) {

@@ -15,6 +15,8 @@ enum DeviceError : int {
     kErrBadPage = 2,         // a block-table or selection entry out of range
     kErrTmemAlloc = 3,       // tensor-memory allocation returned an unusable address
     kErrSlots = 4,           // more pages requested for staging than device slots
+    kErrBadSeq = 5,          // a sequence's rows are no range of the call's rows
+    kErrBadSlot = 6,         // a state slot out of range
 };
 
 __device__ __forceinline__ void report_error(int* err, int code) {

@@ -113,6 +113,9 @@ struct ProfScope {
 // Sets the thread's last-error message and returns the status.
 pkv_status fail(pkv_status s, const std::string& msg);
 pkv_status cuda_fail(cudaError_t e, const char* what);
+// Reads and clears a device error word (synchronizes the device): PKV_OK, or
+// PKV_ERR_DEVICE_FAULT with what was recorded.
+pkv_status take_device_error(int* d_err, const char* who);
 // Runs the body of a C entry point; what it throws (host memory) becomes a status.
 template <typename F> pkv_status guarded(const char* who, F&& body) noexcept {
     try {

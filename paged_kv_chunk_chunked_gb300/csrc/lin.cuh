@@ -1,0 +1,120 @@
+// Linear attention with a decay per head: what its kernels share.
+//
+//   S_t = l S_{t-1} + k_t v_t^T,   o_t = scale q_t^T S_t,   scale = 1 / sqrt(d)
+//
+// A sequence is cut into chunks of L rows. With S the state before a chunk of m
+// rows, G the gradient of the state after it, and M_ij = l^(i-j) for j <= i, else 0:
+//   O  = scale [((Q K^T) o M) V + diag(l^(i+1)) Q S]
+//   dQ = scale [((dO V^T) o M) K + diag(l^(i+1)) dO S^T]
+//   dV = scale ((Q K^T) o M)^T dO + diag(l^(m-1-j)) K G
+//   dK = scale ((dO V^T) o M)^T Q + diag(l^(m-1-j)) V G^T
+// (Q, dO of every query head of the group), and from chunk to chunk
+//   S' = l^m S + sum_j l^(m-1-j) k_j v_j^T,   G' = l^m G + scale sum_i l^(i+1) q_i do_i^T.
+// All exponents are >= 0, so nothing overflows for l <= 1, however long the chunk.
+// O and dQ have one form, and dV and dK have one: "rows" and "columns" below.
+#pragma once
+
+#include "common.cuh"
+#include "internal.h"
+
+struct pkv_lin {
+    pkv_lin_desc desc{};
+    int device = 0;
+    float* state = nullptr;          // [n_slots, Hkv, d, d]
+    float* dstate = nullptr;         // the same, or null
+    int* d_err = nullptr;            // two device error words: bad arguments, expired waits
+    float* scratch = nullptr;        // chunk states, grown on demand; outgrown buffers stay until
+    size_t scratch_floats = 0;       // the store is destroyed (a captured graph may use them)
+    std::vector<float*> retired;
+};
+
+namespace pkv {
+
+struct LinRows {
+    void* p;                         // [n, heads, d], rows `stride` elements apart
+    int64_t stride;
+};
+
+struct LinArgs {
+    int Hq, Hkv, d, dtype;
+    int64_t n, n_seq, n_slots;
+    LinRows q, k, v, o, dout, dq, dk, dv;
+    const float* log_decay;          // [Hkv] or null
+    const int64_t* cu;               // [n_seq + 1] or null: one sequence of n rows
+    const int32_t* slot_in;          // [n_seq] or null
+    const int32_t* slot_out;         // [n_seq] or null
+    const int32_t* slots;            // the step's, [n]
+    float* state;
+    float* dstate;
+    float* part;                     // scratch [chunks, Hkv, d, d]: each chunk's sum, then the state before it
+    float* gpart;                    // the same of the gradients: the gradient of the state after it
+    int n_chunks;                    // lin_chunks
+    int* err;                        // word of bad arguments
+    int* wait_err;                   // word of the bounded waits: these give up once it is set
+};
+
+// Chunk numbers that n rows in n_seq sequences can take. Sequence b's chunks are
+// numbered from cu[b] / L + b on: it has at most cu[b+1] / L - cu[b] / L + 1 of
+// them, so no two sequences share a number and none needs a table.
+inline int64_t lin_chunks(int64_t n, int64_t n_seq, int L) { return n / L + n_seq; }
+
+// The sequence's rows, checked; false: not a range of 0 .. n (recorded).
+__device__ __forceinline__ bool lin_range(const LinArgs& a, int64_t b, int64_t& lo, int64_t& hi) {
+    lo = a.cu ? a.cu[b] : 0;
+    hi = a.cu ? a.cu[b + 1] : a.n;
+    if (lo >= 0 && lo <= hi && hi <= a.n) return true;
+    report_error(a.err, kErrBadSeq);
+    return false;
+}
+
+struct LinChunk {
+    int64_t row0;                    // first row
+    int rows;                        // 1 .. L
+};
+
+// The rows of chunk number f; false: there is no such chunk. Called by whole warps.
+template <int L> __device__ __forceinline__ bool lin_chunk(const LinArgs& a, int f, LinChunk& c) {
+    int64_t b = 0;
+    if (a.n_seq > 1) {
+        // The last sequence whose chunks start at or before f (numbers ascend with b).
+        const int lane = threadIdx.x % 32;
+        int64_t cnt = 0;
+        for (int64_t b0 = 0; b0 < a.n_seq; b0 += 32) {
+            const bool in = b0 + lane < a.n_seq && a.cu[b0 + lane] / L + b0 + lane <= f;
+            const int k = __popc(__ballot_sync(0xffffffffu, in));
+            cnt += k;
+            if (k < 32) break;
+        }
+        b = cnt - 1;
+    }
+    int64_t lo, hi;
+    if (b < 0 || !lin_range(a, b, lo, hi)) return false;
+    const int64_t off = ((int64_t)f - (lo / L + b)) * L;
+    if (off < 0 || off >= hi - lo) return false;
+    c.row0 = lo + off;
+    c.rows = (int)min64(L, hi - lo - off);
+    return true;
+}
+
+__device__ __forceinline__ float lin_g2(const LinArgs& a, int kvh) {
+    return a.log_decay ? a.log_decay[kvh] * kLog2e : 0.f;
+}
+// l^m, m >= 0, from log2 l (which may be -inf).
+__device__ __forceinline__ float lin_pow(float g2, int m) { return m == 0 ? 1.f : exp2f(g2 * (float)m); }
+
+// A sequence's slot, checked; -1 for none.
+__device__ __forceinline__ int64_t lin_slot(const LinArgs& a, const int32_t* slots, int64_t b) {
+    if (!slots) return -1;
+    const int32_t s = slots[b];
+    if (s >= -1 && s < a.n_slots) return s;
+    report_error(a.err, kErrBadSlot);
+    return -1;
+}
+
+// CUDA-core kernels (chunks of kLinSimtChunk rows).
+constexpr int kLinSimtChunk = 64;
+cudaError_t launch_lin_fwd_simt(const LinArgs& a, cudaStream_t s);
+cudaError_t launch_lin_bwd_simt(const LinArgs& a, cudaStream_t s);
+cudaError_t launch_lin_step(const LinArgs& a, cudaStream_t s);
+
+}  // namespace pkv
