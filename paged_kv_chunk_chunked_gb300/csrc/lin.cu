@@ -61,10 +61,15 @@ pkv_status on_device(const pkv_lin* lin, const char* who) {
     return PKV_OK;
 }
 
-// Scratch for `copies` sets of chunk states.
-pkv_status chunk_states(pkv_lin* lin, LinArgs* a, int chunk, int copies, cudaStream_t cs, const char* who) {
-    a->n_chunks = (int)lin_chunks(a->n, a->n_seq, chunk);
-    const size_t one = (size_t)a->n_chunks * a->Hkv * a->d * a->d, floats = one * copies;
+// Whether the tensor-core kernels take the store's calls.
+bool on_tensor_cores(const pkv_lin* lin) { return lin->desc.dtype == PKV_BF16 && !(lin->desc.flags & PKV_FLAG_SIMT_ONLY); }
+
+// Scratch for the chunk states, of a backward also for their gradients.
+pkv_status chunk_states(pkv_lin* lin, LinArgs* a, bool bwd, cudaStream_t cs, const char* who) {
+    const bool tc = on_tensor_cores(lin);
+    a->n_chunks = (int)lin_chunks(a->n, a->n_seq, tc ? kLinTcChunk : kLinSimtChunk);
+    if ((int64_t)a->n_chunks * a->Hkv * a->d > kMaxGrid) return fail(PKV_ERR_UNSUPPORTED, std::string(who) + ": too many rows");
+    const size_t one = (size_t)a->n_chunks * a->Hkv * a->d * a->d, set = tc ? one + one / 2 : one, floats = set * (bwd ? 2 : 1);
     if (lin->scratch_floats < floats) {
         if (capturing(cs))
             return fail(PKV_ERR_INVALID, std::string(who) + ": needs a larger scratch buffer than the store has; run the call "
@@ -81,8 +86,15 @@ pkv_status chunk_states(pkv_lin* lin, LinArgs* a, int chunk, int copies, cudaStr
         lin->scratch_floats = floats;
     }
     a->part = lin->scratch;
-    a->gpart = copies > 1 ? lin->scratch + one : nullptr;
+    a->gpart = bwd ? lin->scratch + set : nullptr;
+    a->sbf = tc ? reinterpret_cast<__nv_bfloat16*>(a->part + one) : nullptr;
+    a->gbf = tc && bwd ? reinterpret_cast<__nv_bfloat16*>(a->gpart + one) : nullptr;
     return PKV_OK;
+}
+
+pkv_status launched(cudaError_t e, const std::string& why, const char* who) {
+    if (e == cudaSuccess) return PKV_OK;
+    return why.empty() ? cuda_fail(e, (std::string(who) + ": launch").c_str()) : fail(PKV_ERR_CUDA, std::string(who) + ": " + why);
 }
 
 }  // namespace
@@ -178,9 +190,9 @@ pkv_status pkv_lin_attn_fwd(pkv_lin* lin, const void* q, int64_t q_stride, const
         }
         if ((st = on_device(lin, who)) != PKV_OK || a.n_seq == 0) return st;
         cudaStream_t cs = static_cast<cudaStream_t>(stream);
-        if ((st = chunk_states(lin, &a, kLinSimtChunk, 1, cs, who)) != PKV_OK) return st;
-        const cudaError_t e = launch_lin_fwd_simt(a, cs);
-        return e == cudaSuccess ? PKV_OK : cuda_fail(e, "pkv_lin_attn_fwd: launch");
+        if ((st = chunk_states(lin, &a, false, cs, who)) != PKV_OK) return st;
+        std::string why;
+        return launched(on_tensor_cores(lin) ? launch_lin_fwd_tc(a, cs, &why) : launch_lin_fwd_simt(a, cs), why, who);
     });
 }
 
@@ -206,9 +218,9 @@ pkv_status pkv_lin_attn_bwd(pkv_lin* lin, const void* q, int64_t q_stride, const
         }
         if ((st = on_device(lin, who)) != PKV_OK || a.n_seq == 0) return st;
         cudaStream_t cs = static_cast<cudaStream_t>(stream);
-        if ((st = chunk_states(lin, &a, kLinSimtChunk, 2, cs, who)) != PKV_OK) return st;
-        const cudaError_t e = launch_lin_bwd_simt(a, cs);
-        return e == cudaSuccess ? PKV_OK : cuda_fail(e, "pkv_lin_attn_bwd: launch");
+        if ((st = chunk_states(lin, &a, true, cs, who)) != PKV_OK) return st;
+        std::string why;
+        return launched(on_tensor_cores(lin) ? launch_lin_bwd_tc(a, cs, &why) : launch_lin_bwd_simt(a, cs), why, who);
     });
 }
 

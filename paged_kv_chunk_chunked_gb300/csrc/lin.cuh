@@ -48,6 +48,8 @@ struct LinArgs {
     float* dstate;
     float* part;                     // scratch [chunks, Hkv, d, d]: each chunk's sum, then the state before it
     float* gpart;                    // the same of the gradients: the gradient of the state after it
+    __nv_bfloat16* sbf;              // tensor-core kernels: scratch [chunks, Hkv, d, d], the states before the chunks
+    __nv_bfloat16* gbf;              // and the gradients of the states after them, in bf16 (part keeps the sums)
     int n_chunks;                    // lin_chunks
     int* err;                        // word of bad arguments
     int* wait_err;                   // word of the bounded waits: these give up once it is set
@@ -115,6 +117,10 @@ __device__ __forceinline__ int64_t lin_slot(const LinArgs& a, const int32_t* slo
 constexpr int kLinSimtChunk = 64;
 cudaError_t launch_lin_fwd_simt(const LinArgs& a, cudaStream_t s);
 cudaError_t launch_lin_bwd_simt(const LinArgs& a, cudaStream_t s);
+// Tensor-core kernels (bf16, chunks of kLinTcChunk rows); *why: what failed other than a CUDA call.
+constexpr int kLinTcChunk = 128;
+cudaError_t launch_lin_fwd_tc(const LinArgs& a, cudaStream_t s, std::string* why);
+cudaError_t launch_lin_bwd_tc(const LinArgs& a, cudaStream_t s, std::string* why);
 cudaError_t launch_lin_step(const LinArgs& a, cudaStream_t s);
 
 }  // namespace pkv
