@@ -60,13 +60,18 @@ struct LinArgs {
 // them, so no two sequences share a number and none needs a table.
 inline int64_t lin_chunks(int64_t n, int64_t n_seq, int L) { return n / L + n_seq; }
 
-// The sequence's rows, checked; false: not a range of 0 .. n (recorded).
-__device__ __forceinline__ bool lin_range(const LinArgs& a, int64_t b, int64_t& lo, int64_t& hi) {
-    lo = a.cu ? a.cu[b] : 0;
-    hi = a.cu ? a.cu[b + 1] : a.n;
+// Whether rows lo .. hi - 1 are rows of the call (recorded if not).
+__device__ __forceinline__ bool lin_good(const LinArgs& a, int64_t lo, int64_t hi) {
     if (lo >= 0 && lo <= hi && hi <= a.n) return true;
     report_error(a.err, kErrBadSeq);
     return false;
+}
+
+// The sequence's rows, checked.
+__device__ __forceinline__ bool lin_range(const LinArgs& a, int64_t b, int64_t& lo, int64_t& hi) {
+    lo = a.cu ? a.cu[b] : 0;
+    hi = a.cu ? a.cu[b + 1] : a.n;
+    return lin_good(a, lo, hi);
 }
 
 struct LinChunk {
@@ -76,21 +81,26 @@ struct LinChunk {
 
 // The rows of chunk number f; false: there is no such chunk. Called by whole warps.
 template <int L> __device__ __forceinline__ bool lin_chunk(const LinArgs& a, int f, LinChunk& c) {
-    int64_t b = 0;
-    if (a.n_seq > 1) {
-        // The last sequence whose chunks start at or before f (numbers ascend with b).
+    int64_t b = 0, lo = 0, hi = a.n;
+    if (a.cu) {
+        // The last sequence whose chunks start at or before f (numbers ascend with b): lane x
+        // holds sequence b0 + x, so one round of loads finds it and its rows.
         const int lane = threadIdx.x % 32;
-        int64_t cnt = 0;
+        b = -1;
         for (int64_t b0 = 0; b0 < a.n_seq; b0 += 32) {
-            const bool in = b0 + lane < a.n_seq && a.cu[b0 + lane] / L + b0 + lane <= f;
-            const int k = __popc(__ballot_sync(0xffffffffu, in));
-            cnt += k;
+            const bool in = b0 + lane < a.n_seq;
+            const int64_t l = in ? a.cu[b0 + lane] : 0, r = in ? a.cu[b0 + lane + 1] : 0;
+            const int k = __popc(__ballot_sync(0xffffffffu, in && l / L + b0 + lane <= f));
+            if (k > 0) {
+                b = b0 + k - 1;
+                lo = __shfl_sync(0xffffffffu, l, k - 1);
+                hi = __shfl_sync(0xffffffffu, r, k - 1);
+            }
             if (k < 32) break;
         }
-        b = cnt - 1;
+        if (b < 0) return false;
     }
-    int64_t lo, hi;
-    if (b < 0 || !lin_range(a, b, lo, hi)) return false;
+    if (!lin_good(a, lo, hi)) return false;
     const int64_t off = ((int64_t)f - (lo / L + b)) * L;
     if (off < 0 || off >= hi - lo) return false;
     c.row0 = lo + off;

@@ -23,6 +23,11 @@ namespace {
 constexpr int kL = kLinTcChunk;
 static_assert(kL == 128, "a chunk is the 128 rows of an accumulator");
 
+// Lets the stream's next kernel start while this one runs, and waits for the ones
+// before (their writes are visible then): see launch_after.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_kernels() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // 32 bytes to global memory, 32-byte aligned (whole sectors), or as two halves.
 __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8], bool wide) {
     if (wide) {
@@ -35,22 +40,25 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8], bool wi
     }
 }
 
-// D columns of this thread's accumulator row, times f, to a bf16 row.
-template <int D> __device__ __forceinline__ void store_row(uint32_t tmem, float f, __nv_bfloat16* row, bool live, bool wide) {
+// D columns of this thread's accumulator row, times f, as bf16 pairs.
+template <int D> __device__ __forceinline__ void load_row(uint32_t tmem, float f, uint32_t (&o)[D / 2]) {
 #pragma unroll
     for (int c = 0; c < D; c += 32) {
         uint32_t r[32];
         tc::tmem_ld32(tmem + c, r);
         tc::tmem_wait_ld(r);
-        if (live)
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                uint32_t w[8];
+        for (int e = 0; e < 16; ++e) o[c / 2 + e] = pack_bf16x2(__uint_as_float(r[2 * e]) * f, __uint_as_float(r[2 * e + 1]) * f);
+    }
+}
+
+template <int D> __device__ __forceinline__ void store_row(const uint32_t (&o)[D / 2], __nv_bfloat16* row, bool wide) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    w[e] = pack_bf16x2(__uint_as_float(r[16 * v + 2 * e]) * f, __uint_as_float(r[16 * v + 2 * e + 1]) * f);
-                store32(row + c + 16 * v, w, wide);
-            }
+    for (int v = 0; v < D / 16; ++v) {
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = o[8 * v + e];
+        store32(row + 16 * v, w, wide);
     }
 }
 
@@ -78,15 +86,22 @@ template <int D> __device__ __forceinline__ void zero_tail(uint8_t* tile, int m,
 
 // ------------------------------------------------------------------ sums of a chunk
 
-constexpr int kPartStages = 3, kPartRows = 32, kPartWarps = 8;
-constexpr int kPartThreads = (kPartWarps + 1) * 32;
+constexpr int kPartRows = 64, kPartRaw = 4, kPartSplit = 2, kPartWarps = 8;
+constexpr int kPartThreads = (2 + kPartWarps + 4) * 32;
 
 template <int D> struct PartLayout {
     static constexpr uint32_t kBlock = kPartRows * 128;              // 64 columns of a stage's rows
     static constexpr uint32_t kOp = D / 64 * kBlock;                 // one operand
-    static constexpr uint32_t kStage = 4 * kOp;                      // three terms of A, R
-    static constexpr uint32_t kSmem = kPartStages * kStage + 1024;
-    static constexpr uint32_t kCols = 128;                           // tensor memory
+    static constexpr uint32_t kRaw = 2 * kOp;                        // A as loaded, R
+    static constexpr uint32_t kSplit = (D == 128 ? 3 : 4) * kOp;     // A's three terms (D 64: and zeros)
+    static constexpr uint32_t kOffSplit = kPartRaw * kRaw;
+    static constexpr uint32_t kSmem = kOffSplit + kPartSplit * kSplit + 1024;
+};
+
+struct PartBarriers {
+    uint64_t raw_full[kPartRaw], raw_empty[kPartRaw], split_full[kPartSplit], split_empty[kPartSplit];
+    uint64_t acc_full[2], acc_empty[2], drain;
+    uint32_t tmem_base;
 };
 
 // x's three bf16 terms: hi, what hi leaves, what both leave (packed pairs).
@@ -98,322 +113,63 @@ __device__ __forceinline__ void split3(float x, float y, uint32_t& hi, uint32_t&
     lo = pack_bf16x2(x - bf16lo(mid), y - bf16hi(mid));
 }
 
-// part[f][h] = sum_t w_t a_t r_t^T: z 0, k v^T with w = l^(m-1-t); z 1, scale q do^T
-// over the group's heads with w = l^(t+1). Eight warps load 32 rows at a time,
-// weight and split A and lay both operands out; the ninth issues the products
-// (both operands MN-major: the rows are the inner dimension). D = 64 packs two
-// terms into the 128 rows of an instruction: accumulator rows 0 .. 63 hold hi's
-// sum and, 64 columns on, lo's; rows 64 .. 127 mid's.
-template <int D>
-__global__ void __launch_bounds__(kPartThreads, 2) lin_part_tc_kernel(const LinArgs a, int z0) {
-    using L = PartLayout<D>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ __align__(8) uint64_t full[kPartStages], empty[kPartStages], done;
-    __shared__ uint32_t tmem_base;
-    __shared__ float w[kL];
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, h = blockIdx.y;
-    const bool grad = blockIdx.z + z0;
-    LinChunk c;
-    if (!lin_chunk<kL>(a, blockIdx.x, c)) return;
-    const int g = grad ? a.Hq / a.Hkv : 1;
-    const int per_head = (c.rows + kPartRows - 1) / kPartRows, n_st = per_head * g;
-    if (threadIdx.x < kL) {
-        const int t = threadIdx.x;
-        const float g2 = lin_g2(a, h);
-        w[t] = t >= c.rows ? 0.f : grad ? rsqrtf((float)D) * lin_pow(g2, t + 1) : lin_pow(g2, c.rows - 1 - t);
-    }
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kPartStages; ++s) {
-            tc::mbar_init(&full[s], kPartWarps * 32);
-            tc::mbar_init(&empty[s], 1);
-        }
-        tc::mbar_init(&done, 1);
-        tc::fence_barrier_init();
-    }
-    if (warp == kPartWarps) {
-        tc::tmem_alloc(&tmem_base, L::kCols);
-        tc::tmem_relinquish();
-    }
-    tc::tc_fence_before();
-    __syncthreads();
-    tc::tc_fence_after();
-    const uint32_t tmem = tmem_base;
-    if (warp == kPartWarps) {
-        const bool leader = tc::elect_one_sync();
-        bool ok = true;
-        const uint32_t idesc = tc::idesc_bf16(128, D, true, true);
-        for (int i = 0; i < n_st; ++i) {
-            const int s = i % kPartStages;
-            if (!tc::warp_wait(&full[s], (i / kPartStages) & 1, a.wait_err)) { ok = false; break; }
-            tc::tc_fence_after();
-            const uint32_t base = tc::smem_u32(smem + s * L::kStage);
-            const uint64_t r0 = tc::sdesc(base + 3 * L::kOp, L::kBlock, 1024);
-            if (leader) {
-                if constexpr (D == 128) {
-#pragma unroll
-                    for (int t = 0; t < 3; ++t)
-#pragma unroll
-                        for (int k = 0; k < kPartRows / 16; ++k)
-                            tc::mma_bf16(tmem, tc::sdesc(base + t * L::kOp + k * 2048, L::kBlock, 1024), tc::sdesc_at(r0, k * 2048),
-                                         idesc, (i | t | k) ? 1u : 0u);
-                } else {
-                    // Blocks hi, mid, then lo and (its sums unused) R.
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int k = 0; k < kPartRows / 16; ++k)
-                            tc::mma_bf16(tmem + 64 * t, tc::sdesc(base + 2 * t * L::kOp + k * 2048, L::kBlock, 1024),
-                                         tc::sdesc_at(r0, k * 2048), idesc, (i | k) ? 1u : 0u);
-                }
-                tc::mma_commit(&empty[s]);
-            }
-            __syncwarp();
-        }
-        if (leader) {
-            tc::mma_commit(&done);
-            tc::drain_wait(&done, 0);
-        }
-        __syncwarp();
-        (void)ok;
-    } else {
-        constexpr int VPR = D / 8, NV = kPartRows * VPR / (kPartWarps * 32);      // 16-byte vectors a thread: 2 or 1
-        const LinRows &xa = grad ? a.q : a.k, &xr = grad ? a.dout : a.v;
-        uint4 ua[2][NV], ur[2][NV];
-        auto fetch = [&](int i, uint4 (&da)[NV], uint4 (&dr)[NV]) {
-            const int head = grad ? h * g + i / per_head : h, t0 = i % per_head * kPartRows;
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                const int id = threadIdx.x + v * kPartWarps * 32, t = t0 + id / VPR, col = id % VPR * 8;
-                da[v] = dr[v] = make_uint4(0, 0, 0, 0);
-                if (t < c.rows) {
-                    da[v] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(xa.p) + (c.row0 + t) * xa.stride + head * D + col));
-                    dr[v] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(xr.p) + (c.row0 + t) * xr.stride + head * D + col));
-                }
-            }
-        };
-        bool ok = true;
-        auto put = [&](int i, const uint4 (&da)[NV], const uint4 (&dr)[NV]) {
-            const int s = i % kPartStages;
-            if (i >= kPartStages && ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&empty[s], ((i / kPartStages) - 1) & 1, a.wait_err));
-            if (!ok) return;
-            uint8_t* st = smem + s * L::kStage;
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                const int id = threadIdx.x + v * kPartWarps * 32, t = id / VPR, col = id % VPR;
-                const uint32_t at = col / 8 * L::kBlock + tc::sw128_offset(t, col % 8);
-                const float wt = w[i % per_head * kPartRows + t];
-                float f[8];
-                widen16<__nv_bfloat16>(da[v], f);
-                uint4 hi, mid, lo;
-                split3(f[0] * wt, f[1] * wt, hi.x, mid.x, lo.x);
-                split3(f[2] * wt, f[3] * wt, hi.y, mid.y, lo.y);
-                split3(f[4] * wt, f[5] * wt, hi.z, mid.z, lo.z);
-                split3(f[6] * wt, f[7] * wt, hi.w, mid.w, lo.w);
-                *reinterpret_cast<uint4*>(st + at) = hi;
-                *reinterpret_cast<uint4*>(st + L::kOp + at) = mid;
-                *reinterpret_cast<uint4*>(st + 2 * L::kOp + at) = lo;
-                *reinterpret_cast<uint4*>(st + 3 * L::kOp + at) = dr[v];
-            }
-            tc::fence_proxy_async_smem();
-            tc::mbar_arrive(&full[s]);
-        };
-        fetch(0, ua[0], ur[0]);
-        if (n_st > 1) fetch(1, ua[1], ur[1]);
-        for (int i = 0; i < n_st; i += 2) {
-            put(i, ua[0], ur[0]);
-            if (i + 2 < n_st) fetch(i + 2, ua[0], ur[0]);
-            if (i + 1 < n_st) put(i + 1, ua[1], ur[1]);
-            if (i + 3 < n_st) fetch(i + 3, ua[1], ur[1]);
-        }
-        if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&done, 0, a.wait_err));
-        tc::tc_fence_after();
-        float* out = (grad ? a.gpart : a.part) + ((size_t)blockIdx.x * a.Hkv + h) * D * D;
-        const uint32_t base = tmem + ((uint32_t)(warp % 4 * 32) << 16);
-        const int row = warp % 4 * 32 + lane;
-        if constexpr (D == 128) {
-            if (ok)
-#pragma unroll
-                for (int cc = 0; cc < 2; ++cc) {
-                    const int col = warp / 4 * 64 + cc * 32;
-                    uint32_t r[32];
-                    tc::tmem_ld32(base + col, r);
-                    tc::tmem_wait_ld(r);
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        uint32_t q[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) q[e] = r[8 * v + e];
-                        store32(out + (size_t)row * D + col + 8 * v, q, true);
-                    }
-                }
-        } else {
-            // mid's sums cross from rows 64 .. 127 through shared memory (the stages are free by now).
-            float* x = reinterpret_cast<float*>(smem);           // [64][65]
-            uint32_t r[32], q[32];
-            const int col = warp / 4 * 32;
-            tc::tmem_ld32(base + col, r);
-            tc::tmem_ld32(base + 64 + col, q);
-            tc::tmem_wait_ld(r);
-            tc::tmem_wait_ld(q);
-            if (row >= 64)
-#pragma unroll
-                for (int e = 0; e < 32; ++e) x[(row - 64) * 65 + col + e] = __uint_as_float(r[e]);
-            asm volatile("bar.sync 1, 256;" ::: "memory");
-            if (ok && row < 64)
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    uint32_t s[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        s[e] = __float_as_uint(__uint_as_float(r[8 * v + e]) +
-                                               (x[row * 65 + col + 8 * v + e] + __uint_as_float(q[8 * v + e])));
-                    store32(out + (size_t)row * D + col + 8 * v, s, true);
-                }
-        }
-    }
-    tc::tc_fence_before();
-    __syncthreads();
-    if (warp == kPartWarps) {
-        tc::tc_fence_after();
-        tc::tmem_dealloc(tmem, L::kCols);
-    }
-}
-
-// ------------------------------------------------------------------ scan
-
-constexpr int kScanThreads = 128, kScanAhead = 8;
-
-// From a sequence's chunk sums to the states before its chunks (z 0, in order) or
-// the gradients of the states after them (z 1, in reverse), in fp32; the kernels
-// that multiply by them get them in bf16. A thread owns four elements all along
-// (so slot_in may be slot_out) and loads kScanAhead chunks' sums at once.
-template <int D>
-__global__ void __launch_bounds__(kScanThreads) lin_scan_bf16_kernel(const LinArgs a, int z0, bool keep) {
-    constexpr int V = D * D / 4;
-    const bool grad = blockIdx.y + z0;
-    const int64_t unit = (int64_t)blockIdx.x * kScanThreads + threadIdx.x;
-    const int e = (int)(unit % V), h = (int)(unit / V % a.Hkv);
-    const int64_t b = unit / V / a.Hkv;
-    int64_t lo, hi;
-    if (!lin_range(a, b, lo, hi)) return;
-    const float g2 = lin_g2(a, h), lfull = lin_pow(g2, kL);
-    const int64_t first = lin_slot(a, grad ? a.slot_out : a.slot_in, b);
-    const int64_t last = lin_slot(a, grad ? a.slot_in : a.slot_out, b);
-    float* store = grad ? a.dstate : a.state;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (first >= 0) s = reinterpret_cast<const float4*>(store + ((size_t)first * a.Hkv + h) * D * D)[e];
-    const int64_t nc = (hi - lo + kL - 1) / kL, f0 = lo / kL + b;
-    const float4* part = reinterpret_cast<const float4*>(grad ? a.gpart : a.part);
-    uint2* out = reinterpret_cast<uint2*>(grad ? a.gbf : a.sbf);
-    const int64_t step = grad ? -1 : 1, at0 = grad ? nc - 1 : 0;
-    for (int64_t i = 0; i < nc; i += kScanAhead) {
-        const int m = (int)min64(kScanAhead, nc - i);
-        float4 x[kScanAhead];
-#pragma unroll
-        for (int u = 0; u < kScanAhead; ++u)
-            if (u < m) x[u] = __ldcs(part + ((size_t)(f0 + at0 + (i + u) * step) * a.Hkv + h) * V + e);
-#pragma unroll
-        for (int u = 0; u < kScanAhead; ++u)
-            if (u < m) {
-                const int64_t c = at0 + (i + u) * step;
-                out[((size_t)(f0 + c) * a.Hkv + h) * V + e] = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
-                const int64_t rows = hi - lo - c * kL;
-                const float l = rows >= kL ? lfull : lin_pow(g2, (int)rows);
-                s.x = fmaf(l, s.x, x[u].x); s.y = fmaf(l, s.y, x[u].y);
-                s.z = fmaf(l, s.z, x[u].z); s.w = fmaf(l, s.w, x[u].w);
-            }
-    }
-    if (last >= 0 && (grad || keep)) reinterpret_cast<float4*>(store + ((size_t)last * a.Hkv + h) * D * D)[e] = s;
-}
-
-// ------------------------------------------------------------------ rows
-
-// Shared memory of the rows kernel: a ring of (C, S) pairs, R, and a ring of X tiles.
-template <int D> struct RowsLayout {
-    static constexpr uint32_t kTile = D / 64 * 16384;                // 128 rows
-    static constexpr uint32_t kState = D / 64 * D * 128;             // D rows
-    static constexpr int kPairs = 2, kX = 2;
-    static constexpr uint32_t kOffS = kTile, kPair = kTile + kState;
-    static constexpr uint32_t kOffR = kPairs * kPair, kOffX = kOffR + kTile;
-    static constexpr uint32_t kSmem = kOffX + kX * kTile + 1024;
-};
-constexpr int kRowsThreads = 320;
-
-struct RowsBarriers {
-    uint64_t pair_full[2], pair_empty[2], r_full, r_empty, x_full[2], x_empty[2];
-    uint64_t s_full[2], p_full[2], o_full[2], o_free[2];             // by warpgroup
-    uint64_t drain;
-    uint32_t tmem_base;
-};
-
-// The heads of a CTA: numbers [idx, end) of (chunk, KV head, query head of the
-// group), each role of the kernel walking them for itself.
-struct HeadWalk {
+// The units of a CTA, chunks of a KV head: numbers blockIdx.x, + gridDim.x, ...; a
+// backward's q do^T (g heads of work each) come first, then the k v^T.
+struct PartWalk {
     const LinArgs& a;
-    int64_t idx, end, unit = -1;
-    int g, it = -1, pair = -1, f = 0, h = 0, head = 0;
-    bool first = false, live = false;
+    int n, per_kind, i, it = -1;
+    bool both, grad = false;
+    int f = 0, h = 0;
     LinChunk c{};
-
-    __device__ __forceinline__ HeadWalk(const LinArgs& args, int64_t from, int64_t to) : a(args), idx(from - 1), end(to), g(args.Hq / args.Hkv) {}
-    // The next head: it counts heads, pair (chunk, KV head)s; first: the first head of its pair here.
+    __device__ __forceinline__ PartWalk(const LinArgs& args, bool both_)
+        : a(args), per_kind(args.n_chunks * args.Hkv), i((int)blockIdx.x - (int)gridDim.x), both(both_) {
+        n = both ? 2 * per_kind : per_kind;
+    }
     __device__ __forceinline__ bool next() {
-        while (++idx < end) {
-            const int64_t u = idx / g;
-            first = u != unit;
-            if (first) {
-                unit = u;
-                f = (int)(u / a.Hkv);
-                h = (int)(u - (int64_t)f * a.Hkv);
-                live = lin_chunk<kL>(a, f, c);
-                pair += live;
-            }
-            if (!live) {
-                idx = (u + 1) * g - 1;
-                continue;
-            }
+        while ((i += gridDim.x) < n) {
+            const int u = i < per_kind ? i : i - per_kind;
+            grad = both && i < per_kind;
+            f = u / a.Hkv;
+            h = u - f * a.Hkv;
+            if (!lin_chunk<kL>(a, f, c)) continue;
             ++it;
-            head = h * g + (int)(idx - u * g);
             return true;
         }
         return false;
     }
+    __device__ __forceinline__ int heads() const { return grad ? a.Hq / a.Hkv : 1; }
+    __device__ __forceinline__ int stages() const { return (c.rows + kPartRows - 1) / kPartRows; }
 };
 
-// out = scale [((X C^T) o M) R + diag(l^(i+1)) X S']. O: X, C, R, S' = Q, K, V, S;
-// dQ (GRAD): dO, V, K, S^T. A persistent CTA takes a run of heads. Warp 0 loads
-// (TMA), warp 1 issues the products, two warpgroups take the heads in turn, each
-// with 256 columns of tensor memory of its own: scores [0, 128), which the
-// weighted scores in bf16 overwrite as the A operand of the second product, and
-// the output [128, 128 + D), which is X S' first and is scaled by l^(i+1) there
-// before the second product adds to it.
-// Weights l^(i-j): for 32 x 32 blocks under the diagonal l^(i - 32 b - 31) (one per
-// row and block) times l^(31 - (j - 32 b)), both with exponents >= 0; on it from a table.
-template <int D, bool GRAD>
-__global__ void __launch_bounds__(kRowsThreads, 1)
-lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_c,
-                   const __grid_constant__ CUtensorMap map_r, const __grid_constant__ CUtensorMap map_s, const LinArgs a,
-                   int64_t heads, int wide) {
-    using L = RowsLayout<D>;
+// part[f][h] = sum_t w_t a_t r_t^T: k v^T with w = l^(m-1-t), and for a backward
+// (both) also scale q do^T over the group's heads with w = l^(t+1). Warp 0 loads 64 rows of both
+// operands at a time (TMA, four stages), eight warps weight A and split it into
+// three terms, warp 1 issues the products (both operands MN-major: the rows are
+// the inner dimension), four warps write the sums of one unit out while the next
+// unit's are formed (two accumulators). The large term has an accumulator of its
+// own: each addition to it rounds in fp32, and the small terms' additions would
+// triple their number. D = 64 packs two terms into the 128 rows of an instruction:
+// rows 0 .. 63 hold hi's sum and, 64 columns on, lo's; rows 64 .. 127 mid's.
+template <int D>
+__global__ void __launch_bounds__(kPartThreads, 1)
+lin_part_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                   const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do, const LinArgs a, bool both) {
+    using L = PartLayout<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ __align__(8) RowsBarriers B;
+    __shared__ __align__(8) PartBarriers B;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int64_t from = heads * blockIdx.x / gridDim.x, to = heads * (blockIdx.x + 1) / gridDim.x;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < 2; ++s) {
-            tc::mbar_init(&B.pair_full[s], 1);
-            tc::mbar_init(&B.pair_empty[s], 1);
-            tc::mbar_init(&B.x_full[s], 1);
-            tc::mbar_init(&B.x_empty[s], 1);
-            tc::mbar_init(&B.s_full[s], 1);
-            tc::mbar_init(&B.p_full[s], 128);
-            tc::mbar_init(&B.o_full[s], 1);
-            tc::mbar_init(&B.o_free[s], 128);
+        for (int s = 0; s < kPartRaw; ++s) {
+            tc::mbar_init(&B.raw_full[s], 1);
+            tc::mbar_init(&B.raw_empty[s], 1);
         }
-        tc::mbar_init(&B.r_full, 1);
-        tc::mbar_init(&B.r_empty, 1);
+        for (int s = 0; s < 2; ++s) {
+            tc::mbar_init(&B.split_full[s], kPartWarps * 32);
+            tc::mbar_init(&B.split_empty[s], 1);
+            tc::mbar_init(&B.acc_full[s], 1);
+            tc::mbar_init(&B.acc_empty[s], 128);
+        }
         tc::mbar_init(&B.drain, 1);
         tc::fence_barrier_init();
     }
@@ -424,37 +180,372 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
+    launch_dependents();
+    const uint32_t tmem = B.tmem_base;
+    PartWalk w(a, both);
+    int st = 0;                                  // stages so far
+    if (warp == 0) {
+        // ------------------------------------------------------------ loads
+        bool ok = true;
+        while (ok && w.next()) {
+            const int ns = w.stages(), total = w.heads() * ns;
+            const CUtensorMap *ma = w.grad ? &map_q : &map_k, *mr = w.grad ? &map_do : &map_v;
+            int head = w.grad ? w.h * w.heads() : w.h, row = (int)w.c.row0, left = ns;
+            for (int i = 0; i < total; ++i, ++st) {
+                const int s = st % kPartRaw;
+                if (st >= kPartRaw && !tc::warp_wait(&B.raw_empty[s], (st / kPartRaw - 1) & 1, a.wait_err)) { ok = false; break; }
+                if (lane == 0) {
+                    uint8_t* dst = smem + s * L::kRaw;
+                    tc::mbar_arrive_expect_tx(&B.raw_full[s], L::kRaw);
+#pragma unroll
+                    for (int b = 0; b < D / 64; ++b) {
+                        tc::tma_load_3d(dst + b * L::kBlock, ma, &B.raw_full[s], 64 * b, head, row);
+                        tc::tma_load_3d(dst + L::kOp + b * L::kBlock, mr, &B.raw_full[s], 64 * b, head, row);
+                    }
+                }
+                row += kPartRows;
+                if (--left == 0) {
+                    left = ns;
+                    ++head;
+                    row = (int)w.c.row0;
+                }
+            }
+        }
+        // None of this CTA's copies may still be landing when it exits.
+        if (lane == 0)
+            for (int i = max(0, st - kPartRaw); i < st; ++i) tc::drain_wait(&B.raw_full[i % kPartRaw], (i / kPartRaw) & 1);
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ products
+        const bool leader = tc::elect_one_sync();
+        const uint32_t idesc = tc::idesc_bf16(128, D, true, true);
+        const uint32_t sm = tc::smem_u32(smem);
+        bool ok = true;
+        while (ok && w.next()) {
+            const int total = w.heads() * w.stages();
+            const uint32_t t = tmem + (w.it & 1) * 256;
+            if (w.it >= 2 && !tc::warp_wait(&B.acc_empty[w.it & 1], ((w.it >> 1) - 1) & 1, a.wait_err)) break;
+            for (int i = 0; i < total; ++i, ++st) {
+                const int s = st % kPartRaw, p = st % kPartSplit;
+                if (!tc::warp_wait(&B.split_full[p], (st / kPartSplit) & 1, a.wait_err)) { ok = false; break; }
+                tc::tc_fence_after();
+                if (leader) {
+                    const uint64_t r0 = tc::sdesc(sm + s * L::kRaw + L::kOp, L::kBlock, 1024);
+                    const uint64_t a0 = tc::sdesc(sm + L::kOffSplit + p * L::kSplit, L::kBlock, 1024);
+                    if constexpr (D == 128) {
+#pragma unroll
+                        for (int x = 0; x < 3; ++x)
+#pragma unroll
+                            for (int k = 0; k < kPartRows / 16; ++k)
+                                tc::mma_bf16(t + (x ? 128 : 0), tc::sdesc_at(a0, x * L::kOp + k * 2048), tc::sdesc_at(r0, k * 2048),
+                                             idesc, (i | k | (x == 2)) ? 1u : 0u);
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)              // blocks hi, mid; then lo, zeros
+#pragma unroll
+                            for (int k = 0; k < kPartRows / 16; ++k)
+                                tc::mma_bf16(t + 64 * x, tc::sdesc_at(a0, 2 * x * L::kOp + k * 2048), tc::sdesc_at(r0, k * 2048), idesc,
+                                             (i | k) ? 1u : 0u);
+                    }
+                    tc::mma_commit(&B.raw_empty[s]);
+                    tc::mma_commit(&B.split_empty[p]);
+                    if (i + 1 == total) tc::mma_commit(&B.acc_full[w.it & 1]);
+                }
+                __syncwarp();
+            }
+        }
+        if (leader) {                            // nothing of ours may still run on the tensor core at exit
+            tc::mma_commit(&B.drain);
+            tc::drain_wait(&B.drain, 0);
+        }
+        __syncwarp();
+    } else if (warp < 2 + kPartWarps) {
+        // ------------------------------------------------------------ weights and terms
+        constexpr int VPR = D / 8, RPP = kPartWarps * 32 / VPR, NV = kPartRows / RPP;    // rows a pass, vectors a thread
+        const int tid = threadIdx.x - 64, t0 = tid / VPR;
+        const uint32_t at0 = tid % VPR / 8 * L::kBlock + tc::sw128_offset(t0, tid % 8);  // RPP is a multiple of 8: + v RPP 128
+        static_assert(RPP % 8 == 0, "a thread's rows share their swizzle");
+        if constexpr (D == 64) {                 // the fourth block: zeros, once
+            for (int p = 0; p < kPartSplit; ++p)
+                for (int i = tid; i < (int)L::kOp / 16; i += kPartWarps * 32)
+                    *reinterpret_cast<uint4*>(smem + L::kOffSplit + p * L::kSplit + 3 * L::kOp + i * 16) = make_uint4(0, 0, 0, 0);
+        }
+        bool ok = true;
+        while (ok && w.next()) {
+            const int ns = w.stages(), nh = w.heads(), m = w.c.rows;
+            const float g2 = lin_g2(a, w.h);
+            // This thread's weights: of rows t0 + v RPP of both stages of a chunk.
+            float wt[kL / kPartRows][NV];
+#pragma unroll
+            for (int q = 0; q < kL / kPartRows; ++q)
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    const int t = q * kPartRows + v * RPP + t0;
+                    wt[q][v] = t >= m ? 0.f : w.grad ? rsqrtf((float)D) * lin_pow(g2, t + 1) : lin_pow(g2, m - 1 - t);
+                }
+            for (int e = 0; ok && e < nh; ++e)
+#pragma unroll
+                for (int q = 0; q < kL / kPartRows; ++q) {
+                    if (q >= ns) break;
+                    const int s = st % kPartRaw, p = st % kPartSplit;
+                    if (st >= kPartSplit && ok)
+                        ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.split_empty[p], (st / kPartSplit - 1) & 1, a.wait_err));
+                    if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.raw_full[s], (st / kPartRaw) & 1, a.wait_err));
+                    if (!ok) break;
+                    uint8_t *raw = smem + s * L::kRaw + at0, *out = smem + L::kOffSplit + p * L::kSplit + at0;
+                    const int left = m - q * kPartRows;
+#pragma unroll
+                    for (int v = 0; v < NV; ++v) {
+                        uint4 u = *reinterpret_cast<const uint4*>(raw + v * RPP * 128);
+                        if (v * RPP + t0 >= left) {              // behind the sequence: anything, and 0 * NaN is NaN
+                            u = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4*>(raw + L::kOp + v * RPP * 128) = u;
+                        }
+                        float x[8];
+                        widen16<__nv_bfloat16>(u, x);
+                        const float k = wt[q][v];
+                        uint4 hi, mid, lo;
+                        split3(x[0] * k, x[1] * k, hi.x, mid.x, lo.x);
+                        split3(x[2] * k, x[3] * k, hi.y, mid.y, lo.y);
+                        split3(x[4] * k, x[5] * k, hi.z, mid.z, lo.z);
+                        split3(x[6] * k, x[7] * k, hi.w, mid.w, lo.w);
+                        *reinterpret_cast<uint4*>(out + v * RPP * 128) = hi;
+                        *reinterpret_cast<uint4*>(out + L::kOp + v * RPP * 128) = mid;
+                        *reinterpret_cast<uint4*>(out + 2 * L::kOp + v * RPP * 128) = lo;
+                    }
+                    tc::fence_proxy_async_smem();
+                    tc::mbar_arrive(&B.split_full[p]);
+                    ++st;
+                }
+        }
+    } else {
+        // ------------------------------------------------------------ sums out
+        const int quad = warp & 3, row = quad * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+        __shared__ float cross[64][33];          // D 64: mid's sums, 32 columns at a time
+        bool ok = true;
+        while (w.next()) {
+            const int b = w.it & 1;
+            if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.acc_full[b], (w.it >> 1) & 1, a.wait_err));
+            if (!ok && D == 128) break;
+            tc::tc_fence_after();
+            float* out = (w.grad ? a.gpart : a.part) + ((size_t)w.f * a.Hkv + w.h) * D * D;
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+                uint32_t r[32], q[32];
+                tc::tmem_ld32(lanes + b * 256 + c, r);
+                tc::tmem_ld32(lanes + b * 256 + D + c, q);
+                tc::tmem_wait_ld(r);
+                tc::tmem_wait_ld(q);
+                if constexpr (D == 64) {
+                    // (after a failed wait this goes on, only to keep meeting the other warps)
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    if (row >= 64)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) cross[row - 64][e] = __uint_as_float(r[e]);
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    if (row < 64)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) q[e] = __float_as_uint(__uint_as_float(q[e]) + cross[row][e]);
+                }
+                if (ok && row < D)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        uint32_t x[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            x[e] = __float_as_uint(__uint_as_float(r[8 * v + e]) + __uint_as_float(q[8 * v + e]));
+                        store32(out + (size_t)row * D + c + 8 * v, x, true);
+                    }
+            }
+            tc::tc_fence_before();
+            tc::mbar_arrive(&B.acc_empty[b]);
+        }
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------------ scan
+
+constexpr int kScanThreads = 128, kScanAhead = 16;
+
+// From a sequence's chunk sums to the states before its chunks (y 0, in order) or
+// the gradients of the states after them (y 1, in reverse), in fp32; the kernels
+// that multiply by them get them in bf16. A thread owns four elements all along
+// (so slot_in may be slot_out) and loads kScanAhead chunks' sums at once.
+template <int D>
+__global__ void __launch_bounds__(kScanThreads) lin_scan_bf16_kernel(const LinArgs a) {
+    constexpr int V = D * D / 4;
+    const bool grad = blockIdx.y;
+    const int64_t unit = (int64_t)blockIdx.x * kScanThreads + threadIdx.x;
+    const int e = (int)(unit % V), h = (int)(unit / V % a.Hkv);
+    const int64_t b = unit / V / a.Hkv;
+    launch_dependents();
+    int64_t lo, hi;
+    const bool good = lin_range(a, b, lo, hi);
+    wait_for_kernels();
+    if (!good) return;
+    const float g2 = lin_g2(a, h), lfull = lin_pow(g2, kL);
+    const int64_t first = lin_slot(a, grad ? a.slot_out : a.slot_in, b);
+    // (a backward scans k v^T for the states alone: the forward has stored the last one)
+    const int64_t last = !grad && gridDim.y > 1 ? -1 : lin_slot(a, grad ? a.slot_in : a.slot_out, b);
+    float* store = grad ? a.dstate : a.state;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (first >= 0) s = reinterpret_cast<const float4*>(store + ((size_t)first * a.Hkv + h) * D * D)[e];
+    const int64_t nc = (hi - lo + kL - 1) / kL, c0 = grad ? nc - 1 : 0;
+    const int tail = (int)(hi - lo - (nc - 1) * kL);                             // rows of the last chunk
+    const int64_t at = ((lo / kL + b + c0) * a.Hkv + h) * V + e, step = (int64_t)a.Hkv * V * (grad ? -1 : 1);
+    const float4* in = reinterpret_cast<const float4*>(grad ? a.gpart : a.part) + at;
+    uint2* out = reinterpret_cast<uint2*>(grad ? a.gbf : a.sbf) + at;
+    for (int64_t i = 0; i < nc; i += kScanAhead) {
+        const int m = (int)min64(kScanAhead, nc - i);
+        float4 x[kScanAhead];
+#pragma unroll
+        for (int u = 0; u < kScanAhead; ++u)
+            if (u < m) x[u] = __ldcs(in + u * step);
+#pragma unroll
+        for (int u = 0; u < kScanAhead; ++u)
+            if (u < m) {
+                out[u * step] = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+                const float l = i + u == (grad ? 0 : nc - 1) ? lin_pow(g2, tail) : lfull;
+                s.x = fmaf(l, s.x, x[u].x); s.y = fmaf(l, s.y, x[u].y);
+                s.z = fmaf(l, s.z, x[u].z); s.w = fmaf(l, s.w, x[u].w);
+            }
+        in += kScanAhead * step;
+        out += kScanAhead * step;
+    }
+    if (last >= 0) reinterpret_cast<float4*>(store + ((size_t)last * a.Hkv + h) * D * D)[e] = s;
+}
+
+// ------------------------------------------------------------------ rows
+
+// Shared memory of the rows kernel: a ring of (C, S) pairs, R, and an X tile for each warpgroup.
+template <int D> struct RowsLayout {
+    static constexpr uint32_t kTile = D / 64 * 16384;                // 128 rows
+    static constexpr uint32_t kState = D / 64 * D * 128;             // D rows
+    static constexpr uint32_t kOffS = kTile, kPair = kTile + kState;
+    static constexpr uint32_t kOffR = 2 * kPair, kOffX = kOffR + kTile;
+    static constexpr uint32_t kSmem = kOffX + 2 * kTile + 1024;
+};
+constexpr int kRowsThreads = 352;
+
+struct RowsBarriers {
+    uint64_t c_full[2], st_full[2], pair_empty[2], r_full, r_empty;
+    // R's tail zeroed, or none (by the warpgroup of the pair's first head). Two, in turn: an issuing
+    // warp may still have to see a pair's when the other warpgroup is at the next pair's; the one
+    // after that needs C's slot, which both warps give up only after they have seen this one.
+    uint64_t r_ready[2];
+    uint64_t x_full[2], x_empty[2], s_full[2], p_full[2], o_full[2], o_free[2], drain[2];        // by warpgroup
+    uint32_t tmem_base;
+};
+
+// The heads of a CTA: numbers [idx, end) of (chunk, KV head, query head of the
+// group), each role of the kernel walking them for itself.
+struct HeadWalk {
+    const LinArgs& a;
+    int idx, end, unit = -1;
+    int g, it = -1, pair = -1, f = 0, h = 0, head = 0;
+    bool first = false, live = false;
+    LinChunk c{};
+
+    __device__ __forceinline__ HeadWalk(const LinArgs& args, int from, int to) : a(args), idx(from - 1), end(to), g(args.Hq / args.Hkv) {}
+    // The next head: it counts heads, pair (chunk, KV head)s; first: the first head of its pair here.
+    __device__ __forceinline__ bool next() {
+        while (++idx < end) {
+            if (unit < 0 || idx >= (unit + 1) * g) {
+                unit = idx / g;
+                f = unit / a.Hkv;
+                h = unit - f * a.Hkv;
+                live = lin_chunk<kL>(a, f, c);
+                pair += live;
+                first = true;
+            } else {
+                first = false;
+            }
+            if (!live) {
+                idx = (unit + 1) * g - 1;
+                continue;
+            }
+            ++it;
+            head = h * g + (idx - unit * g);
+            return true;
+        }
+        return false;
+    }
+};
+
+// out = scale [((X C^T) o M) R + diag(l^(i+1)) X S']. O: X, C, R, S' = Q, K, V, S;
+// dQ (GRAD): dO, V, K, S^T. A persistent CTA takes a run of heads. Warp 0 loads
+// (TMA); two warpgroups take the heads in turn, each with a warp (1, 2) that issues
+// its products and 256 columns of tensor memory of its own: scores [0, 128), which
+// the weighted scores in bf16 overwrite as the A operand of the second product,
+// and the output [128, 128 + D), which is X S' first and is scaled by l^(i+1)
+// there before the second product adds to it. (One issuing warp for both made each
+// second product wait for the other warpgroup's output to be read: 2.1 us a head.)
+// Weights l^(i-j): for 32 x 32 blocks under the diagonal l^(i - 32 b - 31) (one per
+// row and block) times l^(31 - (j - 32 b)), both with exponents >= 0; on it from a table.
+template <int D, bool GRAD>
+__global__ void __launch_bounds__(kRowsThreads, 1)
+lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_c,
+                   const __grid_constant__ CUtensorMap map_r, const __grid_constant__ CUtensorMap map_s, const LinArgs a,
+                   int heads, int wide) {
+    using L = RowsLayout<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ __align__(8) RowsBarriers B;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int from = (int)((int64_t)heads * blockIdx.x / gridDim.x), to = (int)((int64_t)heads * (blockIdx.x + 1) / gridDim.x);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < 2; ++s) {
+            tc::mbar_init(&B.c_full[s], 1);
+            tc::mbar_init(&B.st_full[s], 1);
+            tc::mbar_init(&B.pair_empty[s], 2);
+            tc::mbar_init(&B.r_ready[s], 128);
+            tc::mbar_init(&B.x_full[s], 1);
+            tc::mbar_init(&B.x_empty[s], 1);
+            tc::mbar_init(&B.s_full[s], 1);
+            tc::mbar_init(&B.p_full[s], 128);
+            tc::mbar_init(&B.o_full[s], 1);
+            tc::mbar_init(&B.o_free[s], 128);
+            tc::mbar_init(&B.drain[s], 1);
+        }
+        tc::mbar_init(&B.r_full, 1);
+        tc::mbar_init(&B.r_empty, 2);
+        tc::fence_barrier_init();
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(&B.tmem_base, 512);
+        tc::tmem_relinquish();
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    launch_dependents();
     const uint32_t tmem = B.tmem_base;
     HeadWalk w(a, from, to);
     if (warp == 0) {
         // ------------------------------------------------------------ loads
-        if (lane == 0) {
-            tc::prefetch_tmap(&map_x);
-            tc::prefetch_tmap(&map_c);
-            tc::prefetch_tmap(&map_r);
-            tc::prefetch_tmap(&map_s);
-        }
-        bool ok = true;
+        bool waited = false;
         int n_x = 0, n_pair = 0, n_r = 0;
         while (w.next()) {
             const int row = (int)w.c.row0;
             if (w.first) {
                 const int s = w.pair & 1;
-                if (w.pair >= 2 && !tc::warp_wait(&B.pair_empty[s], ((w.pair >> 1) - 1) & 1, a.wait_err)) { ok = false; break; }
+                if (w.pair >= 2 && !tc::warp_wait(&B.pair_empty[s], ((w.pair >> 1) - 1) & 1, a.wait_err)) break;
                 if (lane == 0) {
-                    uint8_t* dst = smem + s * L::kPair;
-                    tc::mbar_arrive_expect_tx(&B.pair_full[s], L::kPair);
+                    tc::mbar_arrive_expect_tx(&B.c_full[s], L::kTile);
 #pragma unroll
-                    for (int b = 0; b < D / 64; ++b) {
-                        tc::tma_load_3d(dst + b * 16384, &map_c, &B.pair_full[s], 64 * b, w.h, row);
-                        tc::tma_load_2d(dst + L::kOffS + b * (D * 128), &map_s, &B.pair_full[s], 64 * b, (w.f * a.Hkv + w.h) * D);
-                    }
+                    for (int b = 0; b < D / 64; ++b)
+                        tc::tma_load_3d(smem + s * L::kPair + b * 16384, &map_c, &B.c_full[s], 64 * b, w.h, row);
                 }
-                n_pair = w.pair + 1;
             }
             {
                 const int s = w.it & 1;
-                if (w.it >= 2 && !tc::warp_wait(&B.x_empty[s], ((w.it >> 1) - 1) & 1, a.wait_err)) { ok = false; break; }
+                if (w.it >= 2 && !tc::warp_wait(&B.x_empty[s], ((w.it >> 1) - 1) & 1, a.wait_err)) break;
                 if (lane == 0) {
                     tc::mbar_arrive_expect_tx(&B.x_full[s], L::kTile);
 #pragma unroll
@@ -464,7 +555,18 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                 n_x = w.it + 1;
             }
             if (w.first) {
-                if (w.pair >= 1 && !tc::warp_wait(&B.r_empty, (w.pair - 1) & 1, a.wait_err)) { ok = false; break; }
+                const int s = w.pair & 1;
+                if (!waited) wait_for_kernels(); // the states; Q, K, V and dO are older than the kernels before
+                waited = true;
+                if (lane == 0) {
+                    tc::mbar_arrive_expect_tx(&B.st_full[s], L::kState);
+#pragma unroll
+                    for (int b = 0; b < D / 64; ++b)
+                        tc::tma_load_2d(smem + s * L::kPair + L::kOffS + b * (D * 128), &map_s, &B.st_full[s], 64 * b,
+                                        (w.f * a.Hkv + w.h) * D);
+                }
+                n_pair = w.pair + 1;
+                if (w.pair >= 1 && !tc::warp_wait(&B.r_empty, (w.pair - 1) & 1, a.wait_err)) break;
                 if (lane == 0) {
                     tc::mbar_arrive_expect_tx(&B.r_full, L::kTile);
 #pragma unroll
@@ -474,86 +576,101 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                 n_r = w.pair + 1;
             }
         }
+        if (!waited) wait_for_kernels();         // a kernel never ends before the one it may overlap
         // None of this CTA's copies may still be landing when it exits.
         if (lane == 0) {
             for (int i = max(0, n_x - 2); i < n_x; ++i) tc::drain_wait(&B.x_full[i & 1], (i >> 1) & 1);
-            for (int i = max(0, n_pair - 2); i < n_pair; ++i) tc::drain_wait(&B.pair_full[i & 1], (i >> 1) & 1);
+            for (int i = max(0, n_pair - 2); i < n_pair; ++i) {
+                tc::drain_wait(&B.c_full[i & 1], (i >> 1) & 1);
+                tc::drain_wait(&B.st_full[i & 1], (i >> 1) & 1);
+            }
             if (n_r > 0) tc::drain_wait(&B.r_full, (n_r - 1) & 1);
         }
-        (void)ok;
-    } else if (warp == 1) {
-        // ------------------------------------------------------------ products
+    } else if (warp <= 2) {
+        // ------------------------------------------------------------ products of one warpgroup
         const bool leader = tc::elect_one_sync();
+        const int wg = warp - 1;
         const uint32_t idesc_x = tc::idesc_bf16(128, 128, false, false);         // X C^T
         const uint32_t idesc_s = tc::idesc_bf16(128, D, false, !GRAD);           // X S (S [inner][columns]) or X S^T
         const uint32_t idesc_r = tc::idesc_bf16(128, D, false, true);            // P R
-        const uint32_t sm = tc::smem_u32(smem);
+        const uint32_t sm = tc::smem_u32(smem), t = tmem + wg * 256;
         const uint64_t dr = tc::sdesc(sm + L::kOffR, 16384, 1024);
-        // The second product of head i; `last`: the last one that reads this R.
-        auto second = [&](int i, int pair, bool last) -> bool {
-            if (!tc::warp_wait(&B.p_full[i & 1], (i >> 1) & 1, a.wait_err)) return false;
-            if (!tc::warp_wait(&B.r_full, pair & 1, a.wait_err)) return false;
-            tc::tc_fence_after();
-            if (leader) {
-                const uint32_t t = tmem + (i & 1) * 256;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) tc::mma_bf16_ts(t + 128, t + k * 8, tc::sdesc_at(dr, k * 2048), idesc_r, 1u);
-                tc::mma_commit(&B.o_full[i & 1]);
-                if (last) tc::mma_commit(&B.r_empty);
-            }
-            __syncwarp();
-            return true;
+        const uint64_t dx = tc::sdesc(sm + L::kOffX + wg * L::kTile, 16, 1024);
+        bool r_seen = true;                      // this walk has waited for its pair's R
+        auto wait_r = [&](int pair) -> bool {
+            r_seen = true;
+            return tc::warp_wait(&B.r_full, pair & 1, a.wait_err) &&
+                   tc::warp_wait(&B.r_ready[pair & 1], (pair >> 1) & 1, a.wait_err);
         };
-        bool ok = true;
-        int prev_pair = -1;
         while (w.next()) {
-            const int i = w.it, s = i & 1, ps = w.pair & 1;
-            if (w.first && w.pair > 0) {         // the pair before is through with C and S
-                if (leader) tc::mma_commit(&B.pair_empty[ps ^ 1]);
+            const int ps = w.pair & 1;
+            if (w.first && w.pair > 0) {
+                // This warp is through with the pair before (both warps say so of every pair, and both
+                // see every R arrive, so that no wait for a phase can fall a whole period behind).
+                if (!r_seen && !wait_r(w.pair - 1)) break;
+                if (leader) {
+                    tc::mma_commit(&B.pair_empty[ps ^ 1]);
+                    tc::mma_commit(&B.r_empty);
+                }
                 __syncwarp();
             }
-            if (w.first && !tc::warp_wait(&B.pair_full[ps], (w.pair >> 1) & 1, a.wait_err)) { ok = false; break; }
-            if (!tc::warp_wait(&B.x_full[s], (i >> 1) & 1, a.wait_err)) { ok = false; break; }
-            if (i >= 2 && !tc::warp_wait(&B.o_free[s], ((i >> 1) - 1) & 1, a.wait_err)) { ok = false; break; }
+            if (w.first) r_seen = false;
+            if ((w.it & 1) != wg) continue;
+            const int n = w.it >> 1;             // heads of this warpgroup before
+            // (X first: it is loaded after this pair's C, whose slot was free by then of the pair before the last)
+            if (!tc::warp_wait(&B.x_full[wg], n & 1, a.wait_err)) break;
+            if (!tc::warp_wait(&B.c_full[ps], (w.pair >> 1) & 1, a.wait_err)) break;
+            if (n > 0 && !tc::warp_wait(&B.o_free[wg], (n - 1) & 1, a.wait_err)) break;
             tc::tc_fence_after();
             if (leader) {
-                const uint64_t dx = tc::sdesc(sm + L::kOffX + s * L::kTile, 16, 1024);
                 const uint64_t dc = tc::sdesc(sm + ps * L::kPair, 16, 1024);
-                const uint64_t ds = GRAD ? tc::sdesc(sm + ps * L::kPair + L::kOffS, 16, 1024)
-                                         : tc::sdesc(sm + ps * L::kPair + L::kOffS, D * 128, 1024);
-                const uint32_t t = tmem + s * 256;
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint32_t at = (k >> 2) * 16384 + (k & 3) * 32;
                     tc::mma_bf16(t, tc::sdesc_at(dx, at), tc::sdesc_at(dc, at), idesc_x, k > 0);
                 }
+                tc::mma_commit(&B.s_full[wg]);
+            }
+            __syncwarp();
+            if (!tc::warp_wait(&B.st_full[ps], (w.pair >> 1) & 1, a.wait_err)) break;
+            tc::tc_fence_after();
+            if (leader) {
+                const uint64_t ds = GRAD ? tc::sdesc(sm + ps * L::kPair + L::kOffS, 16, 1024)
+                                         : tc::sdesc(sm + ps * L::kPair + L::kOffS, D * 128, 1024);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
                     tc::mma_bf16(t + 128, tc::sdesc_at(dx, (k >> 2) * 16384 + (k & 3) * 32),
                                  tc::sdesc_at(ds, GRAD ? (k >> 2) * (D * 128) + (k & 3) * 32 : k * 2048), idesc_s, k > 0);
-                tc::mma_commit(&B.s_full[s]);
-                tc::mma_commit(&B.x_empty[s]);
+                tc::mma_commit(&B.o_full[wg]);   // X S': the output's first phase of a head
+                tc::mma_commit(&B.x_empty[wg]);
             }
             __syncwarp();
-            if (i > 0 && !second(i - 1, prev_pair, w.first)) { ok = false; break; }
-            prev_pair = w.pair;
+            if (!r_seen && !wait_r(w.pair)) break;
+            if (!tc::warp_wait(&B.p_full[wg], n & 1, a.wait_err)) break;
+            tc::tc_fence_after();
+            if (leader) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) tc::mma_bf16_ts(t + 128, t + k * 8, tc::sdesc_at(dr, k * 2048), idesc_r, 1u);
+                tc::mma_commit(&B.o_full[wg]);   // the whole output: its second phase
+            }
+            __syncwarp();
         }
-        if (ok && w.it >= 0) second(w.it, prev_pair, false);
         if (leader) {                            // nothing of ours may still run on the tensor core at exit
-            tc::mma_commit(&B.drain);
-            tc::drain_wait(&B.drain, 0);
+            tc::mma_commit(&B.drain[wg]);
+            tc::drain_wait(&B.drain[wg], 0);
         }
         __syncwarp();
     } else {
         // ------------------------------------------------------------ weights and outputs
-        const int wg = (warp - 2) >> 2, quad = warp & 3, i = quad * 32 + lane;   // row of the chunk
-        const int t128 = (threadIdx.x - 64) & 127;
+        const int wg = (warp - 3) >> 2, quad = warp & 3, i = quad * 32 + lane;   // row of the chunk
+        const int t128 = (threadIdx.x - 96) & 127;
         const uint32_t t = tmem + ((uint32_t)(quad * 32) << 16) + wg * 256;
         const float scale = rsqrtf((float)D);
         const LinRows& out = GRAD ? a.dq : a.o;
         // l's powers, kept while the KV head stays; each warpgroup has tables of its own:
         // l^(x - 31) for x >= 31, else 0, and l^(31 - x).
-        __shared__ float diag[2][64], up[2][32];
+        __shared__ float diag[2][64];
+        __shared__ __align__(16) float up[2][32];
         int h_of = -1;
         float rb[3], li1 = 0.f;
         bool ok = true;
@@ -571,13 +688,15 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             }
             // (After a failed wait the walk goes on, only to keep meeting the other warps at the barriers.)
             if ((w.it & 1) != wg || !ok) continue;
-            const uint32_t ph = (w.it >> 1) & 1;
-            if (w.first && w.c.rows < kL) {      // what lies behind the sequence may be anything
-                ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.r_full, w.pair & 1, a.wait_err));
-                if (ok) zero_tail<D>(smem + L::kOffR, w.c.rows, t128, 128);
-                tc::fence_proxy_async_smem();
+            ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.s_full[wg], (w.it >> 1) & 1, a.wait_err));
+            if (ok && w.first) {
+                if (w.c.rows < kL) {             // what lies behind the sequence may be anything
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.r_full, w.pair & 1, a.wait_err));
+                    if (ok) zero_tail<D>(smem + L::kOffR, w.c.rows, t128, 128);
+                    tc::fence_proxy_async_smem();
+                }
+                tc::mbar_arrive(&B.r_ready[w.pair & 1]);
             }
-            if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.s_full[wg], ph, a.wait_err));
             if (!ok) continue;
             tc::tc_fence_after();
             uint32_t pk[4][16];
@@ -608,17 +727,23 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             }
 #pragma unroll
             for (int b = 0; b < 4; ++b) tc::tmem_st16(t + 16 * b, pk[b]);
+            ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.o_full[wg], 0, a.wait_err));
+            if (!ok) continue;
+            tc::tc_fence_after();
             scale_row<D>(t + 128, li1);
             tc::tmem_wait_st();
             tc::tc_fence_before();
             tc::mbar_arrive(&B.p_full[wg]);
-            ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.o_full[wg], ph, a.wait_err));
+            ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.o_full[wg], 1, a.wait_err));
             if (!ok) continue;
             tc::tc_fence_after();
-            store_row<D>(t + 128, scale, static_cast<__nv_bfloat16*>(out.p) + (w.c.row0 + i) * out.stride + (int64_t)w.head * D,
-                         i < w.c.rows, wide);
+            // The row leaves tensor memory first: the next head's products need not wait for the stores.
+            uint32_t o[D / 2];
+            load_row<D>(t + 128, scale, o);
             tc::tc_fence_before();
             tc::mbar_arrive(&B.o_free[wg]);
+            if (i < w.c.rows)
+                store_row<D>(o, static_cast<__nv_bfloat16*>(out.p) + (w.c.row0 + i) * out.stride + (int64_t)w.head * D, wide);
         }
     }
     tc::tc_fence_before();
@@ -637,12 +762,12 @@ template <int D> struct ColsLayout {
     static constexpr uint32_t kSmem = kOffDo + 2 * kTile + 1024;
     static constexpr uint32_t kColDv = 256, kColDk = 256 + D;
 };
-constexpr int kColsThreads = 320;
+constexpr int kColsThreads = 352;
 
 struct ColsBarriers {
-    uint64_t kvg_full, q_full[2], do_full[2], q_empty[2], do_empty[2];
+    uint64_t k_full, v_full, g_full, q_full[2], do_full[2], q_empty[2], do_empty[2];
     uint64_t q_ready[2], do_ready[2];            // their tails zeroed (a chunk of less than 128 rows)
-    uint64_t init_full, init_done, s_full[2], p_full[2], acc_full, drain;
+    uint64_t s_full[2], init_full[2], p_full[2], acc_full[2];                     // by warpgroup
     uint32_t tmem_base;
 };
 
@@ -650,10 +775,9 @@ struct ColsBarriers {
 // sum_heads ((dO V^T) o M)^T Q + diag(l^(m-1-j)) V G^T of one chunk and KV head.
 // Scores are formed transposed (keys are the accumulator's rows): K Q^T in
 // columns [0, 128) for warpgroup 0 (dV), V dO^T in [128, 256) for warpgroup 1
-// (dK); their weighted bf16 values overwrite them as A operands. dV and dK stay
-// in tensor memory over all heads; they start as K G and V G^T, scaled there by
-// l^(m-1-j) / scale. While one warpgroup weighs its scores the tensor core works
-// for the other.
+// (dK), each with an issuing warp of its own; their weighted bf16 values overwrite
+// them as A operands. dV and dK stay in tensor memory over all heads; they start as
+// K G and V G^T, scaled there by l^(m-1-j) / scale.
 template <int D>
 __global__ void __launch_bounds__(kColsThreads, 1)
 lin_cols_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -663,10 +787,15 @@ lin_cols_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ __align__(8) ColsBarriers B;
-    __shared__ float diag[64], pw[32];
+    __shared__ float diag[64];
+    __shared__ __align__(16) float pw[32];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, f = blockIdx.x, h = blockIdx.y;
+    launch_dependents();
     LinChunk c;
-    if (!lin_chunk<kL>(a, f, c)) return;
+    if (!lin_chunk<kL>(a, f, c)) {
+        wait_for_kernels();                      // a kernel never ends before the one it may overlap
+        return;
+    }
     const int g = a.Hq / a.Hkv;
     const bool tail = c.rows < kL;
     const float g2 = lin_g2(a, h);
@@ -676,18 +805,18 @@ lin_cols_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         for (int s = 0; s < 2; ++s) {
             tc::mbar_init(&B.q_full[s], 1);
             tc::mbar_init(&B.do_full[s], 1);
-            tc::mbar_init(&B.q_empty[s], 1);
-            tc::mbar_init(&B.do_empty[s], 1);
+            tc::mbar_init(&B.q_empty[s], 2);
+            tc::mbar_init(&B.do_empty[s], 2);
             tc::mbar_init(&B.q_ready[s], 128);
             tc::mbar_init(&B.do_ready[s], 128);
             tc::mbar_init(&B.s_full[s], 1);
+            tc::mbar_init(&B.init_full[s], 1);
             tc::mbar_init(&B.p_full[s], 128);
+            tc::mbar_init(&B.acc_full[s], 1);
         }
-        tc::mbar_init(&B.kvg_full, 1);
-        tc::mbar_init(&B.init_full, 1);
-        tc::mbar_init(&B.init_done, 256);
-        tc::mbar_init(&B.acc_full, 1);
-        tc::mbar_init(&B.drain, 1);
+        tc::mbar_init(&B.k_full, 1);
+        tc::mbar_init(&B.v_full, 1);
+        tc::mbar_init(&B.g_full, 1);
         tc::fence_barrier_init();
     }
     if (warp == 1) {
@@ -699,113 +828,116 @@ lin_cols_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     tc::tc_fence_after();
     const uint32_t tmem = B.tmem_base;
     if (warp == 0) {
+        // ------------------------------------------------------------ loads
         const int row = (int)c.row0;
-        if (lane == 0) {
-            tc::mbar_arrive_expect_tx(&B.kvg_full, 2 * L::kTile + L::kState);
-#pragma unroll
-            for (int b = 0; b < D / 64; ++b) {
-                tc::tma_load_3d(smem + b * 16384, &map_k, &B.kvg_full, 64 * b, h, row);
-                tc::tma_load_2d(smem + L::kOffG + b * (D * 128), &map_g, &B.kvg_full, 64 * b, (f * a.Hkv + h) * D);
-                tc::tma_load_3d(smem + L::kOffV + b * 16384, &map_v, &B.kvg_full, 64 * b, h, row);
-            }
-        }
         int n = 0;
         for (int i = 0; i < g; ++i) {
             const int s = i & 1;
             if (i >= 2 && !tc::warp_wait(&B.q_empty[s], ((i >> 1) - 1) & 1, a.wait_err)) break;
             if (i >= 2 && !tc::warp_wait(&B.do_empty[s], ((i >> 1) - 1) & 1, a.wait_err)) break;
             if (lane == 0) {
+                if (i == 0) {
+                    tc::mbar_arrive_expect_tx(&B.k_full, L::kTile);
+                    tc::mbar_arrive_expect_tx(&B.v_full, L::kTile);
+                }
                 tc::mbar_arrive_expect_tx(&B.q_full[s], L::kTile);
                 tc::mbar_arrive_expect_tx(&B.do_full[s], L::kTile);
 #pragma unroll
                 for (int b = 0; b < D / 64; ++b) {
+                    if (i == 0) tc::tma_load_3d(smem + b * 16384, &map_k, &B.k_full, 64 * b, h, row);
                     tc::tma_load_3d(smem + L::kOffQ + s * L::kTile + b * 16384, &map_q, &B.q_full[s], 64 * b, h * g + i, row);
+                }
+#pragma unroll
+                for (int b = 0; b < D / 64; ++b) {
+                    if (i == 0) tc::tma_load_3d(smem + L::kOffV + b * 16384, &map_v, &B.v_full, 64 * b, h, row);
                     tc::tma_load_3d(smem + L::kOffDo + s * L::kTile + b * 16384, &map_do, &B.do_full[s], 64 * b, h * g + i, row);
                 }
             }
             n = i + 1;
+            if (i == 0) {
+                wait_for_kernels();              // the gradients of the states
+                if (lane == 0) {
+                    tc::mbar_arrive_expect_tx(&B.g_full, L::kState);
+#pragma unroll
+                    for (int b = 0; b < D / 64; ++b)
+                        tc::tma_load_2d(smem + L::kOffG + b * (D * 128), &map_g, &B.g_full, 64 * b, (f * a.Hkv + h) * D);
+                }
+            }
         }
+        // None of this CTA's copies may still be landing when it exits.
         if (lane == 0) {
-            tc::drain_wait(&B.kvg_full, 0);
+            tc::drain_wait(&B.k_full, 0);
+            tc::drain_wait(&B.v_full, 0);
+            tc::drain_wait(&B.g_full, 0);
             for (int i = max(0, n - 2); i < n; ++i) {
                 tc::drain_wait(&B.q_full[i & 1], (i >> 1) & 1);
                 tc::drain_wait(&B.do_full[i & 1], (i >> 1) & 1);
             }
         }
-    } else if (warp == 1) {
+    } else if (warp <= 2) {
+        // ------------------------------------------------------------ products: dV's (x 0), dK's (x 1)
         const bool leader = tc::elect_one_sync();
+        const int x = warp - 1;
         const uint32_t id_s = tc::idesc_bf16(128, 128, false, false), id_acc = tc::idesc_bf16(128, D, false, true);
-        const uint32_t id_gt = tc::idesc_bf16(128, D, false, false);
-        const uint32_t sm = tc::smem_u32(smem);
-        const uint64_t dk = tc::sdesc(sm, 16, 1024), dv = tc::sdesc(sm + L::kOffV, 16, 1024);
-        const uint32_t t_dv = tmem + L::kColDv, t_dk = tmem + L::kColDk;
-        // Scores K Q^T (x 0) or V dO^T (x 1) of head i.
-        auto scores = [&](int i, int x) -> bool {
+        const uint32_t id_g = tc::idesc_bf16(128, D, false, x == 0);
+        const uint32_t sm = tc::smem_u32(smem), t = tmem + 128 * x, acc = tmem + (x ? L::kColDk : L::kColDv);
+        const uint64_t dc = tc::sdesc(sm + (x ? L::kOffV : 0), 16, 1024);        // keys' operand
+        const uint32_t own = x ? L::kOffDo : L::kOffQ, other = x ? L::kOffQ : L::kOffDo;     // scores' operand, the product's
+        uint64_t* own_full = tail ? (x ? B.do_ready : B.q_ready) : (x ? B.do_full : B.q_full);
+        uint64_t* other_full = tail ? (x ? B.q_ready : B.do_ready) : (x ? B.q_full : B.do_full);
+        uint64_t *own_empty = x ? B.do_empty : B.q_empty, *other_empty = x ? B.q_empty : B.do_empty;
+        bool ok = tc::warp_wait(x ? &B.v_full : &B.k_full, 0, a.wait_err);
+        for (int i = 0; ok && i < g; ++i) {
             const int s = i & 1;
-            uint64_t* full = tail ? (x ? B.do_ready : B.q_ready) : (x ? B.do_full : B.q_full);
-            if (!tc::warp_wait(&full[s], (i >> 1) & 1, a.wait_err)) return false;
+            if (!tc::warp_wait(&own_full[s], (i >> 1) & 1, a.wait_err)) break;
             tc::tc_fence_after();
             if (leader) {
-                const uint64_t db = tc::sdesc(sm + (x ? L::kOffDo : L::kOffQ) + s * L::kTile, 16, 1024);
+                const uint64_t db = tc::sdesc(sm + own + s * L::kTile, 16, 1024);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint32_t at = (k >> 2) * 16384 + (k & 3) * 32;
-                    tc::mma_bf16(tmem + 128 * x, tc::sdesc_at(x ? dv : dk, at), tc::sdesc_at(db, at), id_s, k > 0);
+                    tc::mma_bf16(t, tc::sdesc_at(dc, at), tc::sdesc_at(db, at), id_s, k > 0);
                 }
                 tc::mma_commit(&B.s_full[x]);
+                tc::mma_commit(&own_empty[s]);
             }
             __syncwarp();
-            return true;
-        };
-        // dV += P^T dO (x 0) or dK += P'^T Q (x 1) of head i.
-        auto add = [&](int i, int x) -> bool {
-            const int s = i & 1;
-            uint64_t* full = tail ? (x ? B.q_ready : B.do_ready) : (x ? B.q_full : B.do_full);
-            if (!tc::warp_wait(&B.p_full[x], i & 1, a.wait_err)) return false;
-            if (!tc::warp_wait(&full[s], (i >> 1) & 1, a.wait_err)) return false;
-            tc::tc_fence_after();
-            if (leader) {
-                const uint64_t db = tc::sdesc(sm + (x ? L::kOffQ : L::kOffDo) + s * L::kTile, 16384, 1024);
+            if (i == 0) {
+                if (!tc::warp_wait(&B.g_full, 0, a.wait_err)) break;
+                tc::tc_fence_after();
+                if (leader) {
+                    const uint64_t dg = x ? tc::sdesc(sm + L::kOffG, 16, 1024) : tc::sdesc(sm + L::kOffG, D * 128, 1024);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    tc::mma_bf16_ts(x ? t_dk : t_dv, tmem + 128 * x + k * 8, tc::sdesc_at(db, k * 2048), id_acc, 1u);
-                // (the same head's scores of the other kind were issued before: both readers are covered)
-                tc::mma_commit(x ? &B.q_empty[s] : &B.do_empty[s]);
+                    for (int k = 0; k < D / 16; ++k)
+                        tc::mma_bf16(acc, tc::sdesc_at(dc, (k >> 2) * 16384 + (k & 3) * 32),
+                                     tc::sdesc_at(dg, x ? (k >> 2) * (D * 128) + (k & 3) * 32 : k * 2048), id_g, k > 0);
+                    tc::mma_commit(&B.init_full[x]);
+                }
+                __syncwarp();
             }
-            __syncwarp();
-            return true;
-        };
-        bool ok = tc::warp_wait(&B.kvg_full, 0, a.wait_err);
-        if (ok) {
+            if (!tc::warp_wait(&B.p_full[x], i & 1, a.wait_err)) break;
+            if (!tc::warp_wait(&other_full[s], (i >> 1) & 1, a.wait_err)) break;
             tc::tc_fence_after();
             if (leader) {
-                const uint64_t dgn = tc::sdesc(sm + L::kOffG, D * 128, 1024), dgt = tc::sdesc(sm + L::kOffG, 16, 1024);
+                const uint64_t db = tc::sdesc(sm + other + s * L::kTile, 16384, 1024);
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    tc::mma_bf16(t_dv, tc::sdesc_at(dk, (k >> 2) * 16384 + (k & 3) * 32), tc::sdesc_at(dgn, k * 2048), id_acc, k > 0);
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    tc::mma_bf16(t_dk, tc::sdesc_at(dv, (k >> 2) * 16384 + (k & 3) * 32),
-                                 tc::sdesc_at(dgt, (k >> 2) * (D * 128) + (k & 3) * 32), id_gt, k > 0);
-                tc::mma_commit(&B.init_full);
+                for (int k = 0; k < 8; ++k) tc::mma_bf16_ts(acc, t + k * 8, tc::sdesc_at(db, k * 2048), id_acc, 1u);
+                tc::mma_commit(&other_empty[s]);
             }
             __syncwarp();
         }
-        ok = ok && scores(0, 0) && scores(0, 1);
-        ok = ok && tc::warp_wait(&B.init_done, 0, a.wait_err);
-        for (int i = 0; ok && i < g; ++i)
-            ok = add(i, 0) && (i + 1 >= g || scores(i + 1, 0)) && add(i, 1) && (i + 1 >= g || scores(i + 1, 1));
-        if (leader) {
-            tc::mma_commit(&B.acc_full);
-            tc::drain_wait(&B.acc_full, 0);
+        if (leader) {                            // (also: nothing of ours may still run on the tensor core at exit)
+            tc::mma_commit(&B.acc_full[x]);
+            tc::drain_wait(&B.acc_full[x], 0);
         }
         __syncwarp();
     } else {
-        const int x = (warp - 2) >> 2, quad = warp & 3, j = quad * 32 + lane;    // key row of the chunk
-        const int t128 = (threadIdx.x - 64) & 127;
+        // ------------------------------------------------------------ weights and outputs
+        const int x = (warp - 3) >> 2, quad = warp & 3, j = quad * 32 + lane;    // key row of the chunk
+        const int t128 = (threadIdx.x - 96) & 127;
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16), acc = lanes + (x ? L::kColDk : L::kColDv), t = lanes + 128 * x;
         const float scale = rsqrtf((float)D);
-        // Warpgroup x zeroes the tails of the operand that its own scores do not read as columns alone: Q (0), dO (1).
+        // A chunk's tail: warpgroup 0 zeroes Q's rows, warpgroup 1 dO's.
         auto tails = [&](int i) -> bool {
             const int s = i & 1;
             uint64_t* full = x ? B.do_full : B.q_full;
@@ -819,14 +951,6 @@ lin_cols_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 #pragma unroll
         for (int b = 0; b < 4; ++b) rb[b] = b > quad ? lin_pow(g2, 32 * b - j) : 0.f;
         bool ok = !tail || tails(0);
-        if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.init_full, 0, a.wait_err));
-        if (ok) {
-            tc::tc_fence_after();
-            scale_row<D>(acc, j < c.rows ? lin_pow(g2, c.rows - 1 - j) / scale : 0.f);
-            tc::tmem_wait_st();
-            tc::tc_fence_before();
-        }
-        tc::mbar_arrive(&B.init_done);
         for (int i = 0; ok && i < g; ++i) {
             if (tail && i + 1 < g && !(ok = tails(i + 1))) break;
             ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.s_full[x], i & 1, a.wait_err));
@@ -862,15 +986,24 @@ lin_cols_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             }
 #pragma unroll
             for (int b = 0; b < 4; ++b) tc::tmem_st16(t + 16 * b, pk[b]);
+            if (i == 0) {
+                ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.init_full[x], 0, a.wait_err));
+                if (!ok) break;
+                tc::tc_fence_after();
+                scale_row<D>(acc, j < c.rows ? lin_pow(g2, c.rows - 1 - j) / scale : 0.f);
+            }
             tc::tmem_wait_st();
             tc::tc_fence_before();
             tc::mbar_arrive(&B.p_full[x]);
         }
-        if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.acc_full, 0, a.wait_err));
+        if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.acc_full[x], 0, a.wait_err));
         if (ok) {
             tc::tc_fence_after();
             const LinRows& out = x ? a.dk : a.dv;
-            store_row<D>(acc, scale, static_cast<__nv_bfloat16*>(out.p) + (c.row0 + j) * out.stride + (int64_t)h * D, j < c.rows, wide >> x & 1);
+            uint32_t o[D / 2];
+            load_row<D>(acc, scale, o);
+            if (j < c.rows)
+                store_row<D>(o, static_cast<__nv_bfloat16*>(out.p) + (c.row0 + j) * out.stride + (int64_t)h * D, wide >> x & 1);
         }
     }
     tc::tc_fence_before();
@@ -883,26 +1016,50 @@ lin_cols_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 
 // ------------------------------------------------------------------ launches
 
-bool rows_map(CUtensorMap* m, const LinRows& x, int H, const LinArgs& a, std::string* why) {
-    return make_tmap_3d(m, x.p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.d, H, a.n, a.d * 2, x.stride * 2, 64, 1, kL, why);
+bool rows_map(CUtensorMap* m, const LinRows& x, int H, const LinArgs& a, int rows, std::string* why) {
+    return make_tmap_3d(m, x.p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.d, H, a.n, a.d * 2, x.stride * 2, 64, 1, rows, why);
 }
 bool states_map(CUtensorMap* m, const void* p, const LinArgs& a, std::string* why) {
     return make_tmap_2d(m, p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.d, (uint64_t)a.n_chunks * a.Hkv * a.d, a.d * 2, 64, a.d, why);
 }
 bool wide_rows(const LinRows& x) { return (reinterpret_cast<uintptr_t>(x.p) & 31) == 0 && x.stride % 16 == 0; }
 
-// Sums z0 .. z0 + nz - 1 (0: k v^T, 1: q do^T) and their scans.
-template <int D> cudaError_t states(const LinArgs& a, int z0, int nz, bool keep, cudaStream_t s) {
+// Launches a kernel that may start before the stream's last kernel, one of this
+// file's, has ended; it waits for that one itself (wait_for_kernels) before it
+// touches what that one writes.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid; cfg.blockDim = dim3(threads); cfg.dynamicSmemBytes = smem; cfg.stream = s;
+    cfg.attrs = &attr; cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// The chunks' sums and their scans: k v^T, in a backward (both) also q do^T.
+template <int D> cudaError_t states(const LinArgs& a, bool both, cudaStream_t s, std::string* why) {
     static SmemGrant grant;
     cudaError_t e = allow_smem(lin_part_tc_kernel<D>, PartLayout<D>::kSmem, grant);
     if (e != cudaSuccess) return e;
+    const int nz = both ? 2 : 1;
     if (a.n) {
+        CUtensorMap k, v, q, go;
+        if (!rows_map(&k, a.k, a.Hkv, a, kPartRows, why) || !rows_map(&v, a.v, a.Hkv, a, kPartRows, why)) return cudaErrorInvalidValue;
+        q = k;
+        go = v;
+        if (both && (!rows_map(&q, a.q, a.Hq, a, kPartRows, why) || !rows_map(&go, a.dout, a.Hq, a, kPartRows, why)))
+            return cudaErrorInvalidValue;
+        const int grid = std::min(a.n_chunks * a.Hkv * nz, sm_count());
         ProfScope ps("lin_part_tc_kernel", s);
-        lin_part_tc_kernel<D><<<dim3(a.n_chunks, a.Hkv, nz), kPartThreads, PartLayout<D>::kSmem, s>>>(a, z0);
+        lin_part_tc_kernel<D><<<grid, kPartThreads, PartLayout<D>::kSmem, s>>>(q, k, v, go, a, both);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
+    const dim3 grid((unsigned)(a.n_seq * a.Hkv * (D * D / 4 / kScanThreads)), nz);
     ProfScope ps("lin_scan_bf16_kernel", s);
-    lin_scan_bf16_kernel<D><<<dim3((unsigned)(a.n_seq * a.Hkv * (D * D / 4 / kScanThreads)), nz), kScanThreads, 0, s>>>(a, z0, keep);
+    if (a.n) return launch_after(lin_scan_bf16_kernel<D>, grid, kScanThreads, 0, s, a);
+    lin_scan_bf16_kernel<D><<<grid, kScanThreads, 0, s>>>(a);          // no sums before it
     return cudaGetLastError();
 }
 
@@ -911,36 +1068,37 @@ template <int D, bool GRAD> cudaError_t rows(const LinArgs& a, cudaStream_t s, s
     const cudaError_t e = allow_smem(lin_rows_tc_kernel<D, GRAD>, RowsLayout<D>::kSmem, grant);
     if (e != cudaSuccess) return e;
     CUtensorMap x, c, r, st;
-    if (!rows_map(&x, GRAD ? a.dout : a.q, a.Hq, a, why) || !rows_map(&c, GRAD ? a.v : a.k, a.Hkv, a, why) ||
-        !rows_map(&r, GRAD ? a.k : a.v, a.Hkv, a, why) || !states_map(&st, a.sbf, a, why))
+    if (!rows_map(&x, GRAD ? a.dout : a.q, a.Hq, a, kL, why) || !rows_map(&c, GRAD ? a.v : a.k, a.Hkv, a, kL, why) ||
+        !rows_map(&r, GRAD ? a.k : a.v, a.Hkv, a, kL, why) || !states_map(&st, a.sbf, a, why))
         return cudaErrorInvalidValue;
-    const int64_t heads = (int64_t)a.n_chunks * a.Hq;
-    const unsigned grid = (unsigned)std::min<int64_t>(heads, sm_count());
+    const int heads = a.n_chunks * a.Hq;
     ProfScope ps("lin_rows_tc_kernel", s);
-    lin_rows_tc_kernel<D, GRAD><<<grid, kRowsThreads, RowsLayout<D>::kSmem, s>>>(x, c, r, st, a, heads, wide_rows(GRAD ? a.dq : a.o));
-    return cudaGetLastError();
+    return launch_after(lin_rows_tc_kernel<D, GRAD>, dim3(std::min(heads, sm_count())), kRowsThreads, RowsLayout<D>::kSmem, s, x, c, r, st,
+                        a, heads, (int)wide_rows(GRAD ? a.dq : a.o));
+}
+
+template <int D> cudaError_t cols(const LinArgs& a, cudaStream_t s, std::string* why) {
+    static SmemGrant grant;
+    const cudaError_t e = allow_smem(lin_cols_tc_kernel<D>, ColsLayout<D>::kSmem, grant);
+    if (e != cudaSuccess) return e;
+    CUtensorMap q, k, v, go, gs;
+    if (!rows_map(&q, a.q, a.Hq, a, kL, why) || !rows_map(&k, a.k, a.Hkv, a, kL, why) || !rows_map(&v, a.v, a.Hkv, a, kL, why) ||
+        !rows_map(&go, a.dout, a.Hq, a, kL, why) || !states_map(&gs, a.gbf, a, why))
+        return cudaErrorInvalidValue;
+    ProfScope ps("lin_cols_tc_kernel", s);
+    return launch_after(lin_cols_tc_kernel<D>, dim3(a.n_chunks, a.Hkv), kColsThreads, ColsLayout<D>::kSmem, s, q, k, v, go, gs, a,
+                        (wide_rows(a.dv) ? 1 : 0) | (wide_rows(a.dk) ? 2 : 0));
 }
 
 template <int D> cudaError_t fwd(const LinArgs& a, cudaStream_t s, std::string* why) {
-    const cudaError_t e = states<D>(a, 0, 1, true, s);
+    const cudaError_t e = states<D>(a, false, s, why);
     return e != cudaSuccess || !a.n ? e : rows<D, false>(a, s, why);
 }
 
 template <int D> cudaError_t bwd(const LinArgs& a, cudaStream_t s, std::string* why) {
-    cudaError_t e = states<D>(a, 0, 2, false, s);        // the forward's states again, not its result
-    if (e == cudaSuccess && a.n) e = rows<D, true>(a, s, why);
-    if (e != cudaSuccess || !a.n) return e;
-    static SmemGrant grant;
-    e = allow_smem(lin_cols_tc_kernel<D>, ColsLayout<D>::kSmem, grant);
-    if (e != cudaSuccess) return e;
-    CUtensorMap q, k, v, go, gs;
-    if (!rows_map(&q, a.q, a.Hq, a, why) || !rows_map(&k, a.k, a.Hkv, a, why) || !rows_map(&v, a.v, a.Hkv, a, why) ||
-        !rows_map(&go, a.dout, a.Hq, a, why) || !states_map(&gs, a.gbf, a, why))
-        return cudaErrorInvalidValue;
-    ProfScope ps("lin_cols_tc_kernel", s);
-    lin_cols_tc_kernel<D><<<dim3(a.n_chunks, a.Hkv), kColsThreads, ColsLayout<D>::kSmem, s>>>(
-        q, k, v, go, gs, a, (wide_rows(a.dv) ? 1 : 0) | (wide_rows(a.dk) ? 2 : 0));
-    return cudaGetLastError();
+    cudaError_t e = states<D>(a, true, s, why);
+    if (e == cudaSuccess && a.n) e = cols<D>(a, s, why);
+    return e != cudaSuccess || !a.n ? e : rows<D, true>(a, s, why);
 }
 
 }  // namespace
