@@ -81,7 +81,7 @@ bool make_tmap_2d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint
 
 bool make_tmap_3d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t d0,
                   uint64_t d1, uint64_t d2, uint64_t stride1_bytes, uint64_t stride2_bytes,
-                  uint32_t b0, uint32_t b1, uint32_t b2, std::string* why) {
+                  uint32_t b0, uint32_t b1, uint32_t b2, std::string* why, CUtensorMapSwizzle swizzle) {
     auto fn = encode_fn(why);
     if (!fn) return false;
     cuuint64_t dims[3] = {d0, d1, d2};
@@ -89,7 +89,7 @@ bool make_tmap_3d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint
     cuuint32_t box[3] = {b0, b1, b2};
     cuuint32_t es[3] = {1, 1, 1};
     CUresult r = fn(m, dt, 3, const_cast<void*>(base), dims, strides, box, es,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
         if (why) *why = "cuTensorMapEncodeTiled (3-D) failed with CUresult " + std::to_string(r);

@@ -327,7 +327,8 @@ bool make_tmap_2d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint
                   uint32_t box_rows, std::string* why);
 bool make_tmap_3d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t d0,
                   uint64_t d1, uint64_t d2, uint64_t stride1_bytes, uint64_t stride2_bytes,
-                  uint32_t b0, uint32_t b1, uint32_t b2, std::string* why);
+                  uint32_t b0, uint32_t b1, uint32_t b2, std::string* why,
+                  CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
 
 cudaError_t run_selftest_umma(int mode, const void* a, const void* b, float* d, int lbo, int sbo,
                               int* d_err);

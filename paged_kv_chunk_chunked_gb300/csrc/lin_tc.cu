@@ -28,22 +28,28 @@ static_assert(kL == 128, "a chunk is the 128 rows of an accumulator");
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_kernels() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// 32 bytes to global memory, 32-byte aligned (whole sectors), or as two halves.
-__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8], bool wide) {
-    if (wide) {
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-                     :: "l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                     : "memory");
-    } else {
-        reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    }
-}
+// Where byte `off` of a box with rows of ROW = 128 (64) bytes and the swizzle of that
+// size lies in shared memory (1024-byte aligned base).
+template <int ROW> __device__ __forceinline__ uint32_t swizzled(uint32_t off) { return off ^ ((off >> 3) & (ROW == 128 ? 0x70u : 0x30u)); }
 
-// D columns of this thread's accumulator row, times f, as bf16 pairs.
-template <int D> __device__ __forceinline__ void load_row(uint32_t tmem, float f, uint32_t (&o)[D / 2]) {
+// Copies a shared-memory box to global memory (the box unchanged until bulk_wait_read).
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];"
+                 :: "l"(reinterpret_cast<uint64_t>(map)), "r"(tc::smem_u32(src)), "r"(c0), "r"(c1), "r"(c2) : "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int c0, int c1) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];"
+                 :: "l"(reinterpret_cast<uint64_t>(map)), "r"(tc::smem_u32(src)), "r"(c0), "r"(c1) : "memory");
+}
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// Eight warps share an accumulator: a warp has 32 rows (its quadrant of tensor
+// memory) and half of the columns.
+
+// D / 2 columns of this thread's row, times f, as bf16 pairs.
+template <int D> __device__ __forceinline__ void load_half(uint32_t tmem, float f, uint32_t (&o)[D / 4]) {
 #pragma unroll
-    for (int c = 0; c < D; c += 32) {
+    for (int c = 0; c < D / 2; c += 32) {
         uint32_t r[32];
         tc::tmem_ld32(tmem + c, r);
         tc::tmem_wait_ld(r);
@@ -52,20 +58,36 @@ template <int D> __device__ __forceinline__ void load_row(uint32_t tmem, float f
     }
 }
 
-template <int D> __device__ __forceinline__ void store_row(const uint32_t (&o)[D / 2], __nv_bfloat16* row, bool wide) {
+// The warp's 32 rows to global memory: by TMA through `stage` (a thread's own row
+// in stores of its own, 32 rows apart from each other, kept the shared-memory
+// pipeline from the tensor core: rows of 24 us became 20), but row by row where the
+// sequence ends inside. left: rows of the chunk from this warp's first on; at: (column, head, row).
+template <int D>
+__device__ __forceinline__ void store_half(const uint32_t (&o)[D / 4], const CUtensorMap* map, uint8_t* stage, int lane, int left,
+                                           int column, int head, int64_t row, const LinRows& out) {
+    if (left >= 32) {
+        if (lane == 0) tc::bulk_wait_read();     // the last box has left the stage
+        __syncwarp();
 #pragma unroll
-    for (int v = 0; v < D / 16; ++v) {
-        uint32_t w[8];
+        for (int v = 0; v < D / 16; ++v)
+            *reinterpret_cast<uint4*>(stage + swizzled<D>(lane * D + v * 16)) = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_3d(map, stage, column, head, (int)row);
+            tc::bulk_commit();
+        }
+    } else if (lane < left) {
+        uint4* p = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out.p) + (row + lane) * out.stride + (int64_t)head * D + column);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = o[8 * v + e];
-        store32(row + 16 * v, w, wide);
+        for (int v = 0; v < D / 16; ++v) p[v] = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
     }
 }
 
-// D columns of this thread's accumulator row, times f, in place.
-template <int D> __device__ __forceinline__ void scale_row(uint32_t tmem, float f) {
+// D / 2 columns of this thread's row, times f, in place.
+template <int D> __device__ __forceinline__ void scale_half(uint32_t tmem, float f) {
 #pragma unroll
-    for (int c = 0; c < D; c += 32) {
+    for (int c = 0; c < D / 2; c += 32) {
         uint32_t r[32];
         tc::tmem_ld32(tmem + c, r);
         tc::tmem_wait_ld(r);
@@ -74,6 +96,10 @@ template <int D> __device__ __forceinline__ void scale_row(uint32_t tmem, float 
         tc::tmem_st32(tmem + c, r);
     }
 }
+
+// Tensor-memory column, within a tile of scores, of the weighted scores' inner
+// indices 16 k .. 16 k + 15: each half of the columns overwrites its own.
+__device__ __forceinline__ constexpr uint32_t p_col(int k) { return (k >> 2) * 64 + (k & 3) * 8; }
 
 // Zeroes rows [m, 128) of a 128-row tile of D / 64 blocks, by `threads` threads:
 // what lies behind a sequence may be anything, and 0 * NaN is NaN.
@@ -86,7 +112,7 @@ template <int D> __device__ __forceinline__ void zero_tail(uint8_t* tile, int m,
 
 // ------------------------------------------------------------------ sums of a chunk
 
-constexpr int kPartRows = 64, kPartRaw = 4, kPartSplit = 2, kPartWarps = 8;
+constexpr int kPartRows = 64, kPartRaw = 3, kPartSplit = 2, kPartWarps = 8;
 constexpr int kPartThreads = (2 + kPartWarps + 4) * 32;
 
 template <int D> struct PartLayout {
@@ -95,7 +121,8 @@ template <int D> struct PartLayout {
     static constexpr uint32_t kRaw = 2 * kOp;                        // A as loaded, R
     static constexpr uint32_t kSplit = (D == 128 ? 3 : 4) * kOp;     // A's three terms (D 64: and zeros)
     static constexpr uint32_t kOffSplit = kPartRaw * kRaw;
-    static constexpr uint32_t kSmem = kOffSplit + kPartSplit * kSplit + 1024;
+    static constexpr uint32_t kOffStage = kOffSplit + kPartSplit * kSplit;       // two 32 x 32 boxes of sums a warp
+    static constexpr uint32_t kSmem = kOffStage + 4 * 2 * 4096 + 1024;
 };
 
 struct PartBarriers {
@@ -153,7 +180,8 @@ struct PartWalk {
 template <int D>
 __global__ void __launch_bounds__(kPartThreads, 1)
 lin_part_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                   const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do, const LinArgs a, bool both) {
+                   const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
+                   const __grid_constant__ CUtensorMap map_kv_out, const __grid_constant__ CUtensorMap map_qdo_out, const LinArgs a, bool both) {
     using L = PartLayout<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -177,17 +205,26 @@ lin_part_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         tc::tmem_alloc(&B.tmem_base, 512);
         tc::tmem_relinquish();
     }
+    if (threadIdx.x == 0) {
+        tc::prefetch_tmap(&map_k);
+        tc::prefetch_tmap(&map_v);
+        if (both) {
+            tc::prefetch_tmap(&map_q);
+            tc::prefetch_tmap(&map_do);
+        }
+    }
+    PartWalk w(a, both);
+    bool more = w.next();                        // (its loads overlap the set-up)
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
     launch_dependents();
     const uint32_t tmem = B.tmem_base;
-    PartWalk w(a, both);
     int st = 0;                                  // stages so far
     if (warp == 0) {
         // ------------------------------------------------------------ loads
         bool ok = true;
-        while (ok && w.next()) {
+        for (; ok && more; more = w.next()) {
             const int ns = w.stages(), total = w.heads() * ns;
             const CUtensorMap *ma = w.grad ? &map_q : &map_k, *mr = w.grad ? &map_do : &map_v;
             int head = w.grad ? w.h * w.heads() : w.h, row = (int)w.c.row0, left = ns;
@@ -220,7 +257,7 @@ lin_part_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         const uint32_t idesc = tc::idesc_bf16(128, D, true, true);
         const uint32_t sm = tc::smem_u32(smem);
         bool ok = true;
-        while (ok && w.next()) {
+        for (; ok && more; more = w.next()) {
             const int total = w.heads() * w.stages();
             const uint32_t t = tmem + (w.it & 1) * 256;
             if (w.it >= 2 && !tc::warp_wait(&B.acc_empty[w.it & 1], ((w.it >> 1) - 1) & 1, a.wait_err)) break;
@@ -270,7 +307,7 @@ lin_part_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     *reinterpret_cast<uint4*>(smem + L::kOffSplit + p * L::kSplit + 3 * L::kOp + i * 16) = make_uint4(0, 0, 0, 0);
         }
         bool ok = true;
-        while (ok && w.next()) {
+        for (; ok && more; more = w.next()) {
             const int ns = w.stages(), nh = w.heads(), m = w.c.rows;
             const float g2 = lin_g2(a, w.h);
             // This thread's weights: of rows t0 + v RPP of both stages of a chunk.
@@ -322,13 +359,14 @@ lin_part_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         const int quad = warp & 3, row = quad * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
         __shared__ float cross[64][33];          // D 64: mid's sums, 32 columns at a time
+        uint8_t* stage = smem + L::kOffStage + (warp - 2 - kPartWarps) * 8192;
         bool ok = true;
-        while (w.next()) {
+        int box = 0;
+        for (; more; more = w.next()) {
             const int b = w.it & 1;
             if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.acc_full[b], (w.it >> 1) & 1, a.wait_err));
             if (!ok && D == 128) break;
             tc::tc_fence_after();
-            float* out = (w.grad ? a.gpart : a.part) + ((size_t)w.f * a.Hkv + w.h) * D * D;
 #pragma unroll
             for (int c = 0; c < D; c += 32) {
                 uint32_t r[32], q[32];
@@ -336,6 +374,10 @@ lin_part_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 tc::tmem_ld32(lanes + b * 256 + D + c, q);
                 tc::tmem_wait_ld(r);
                 tc::tmem_wait_ld(q);
+                if (c + 32 == D) {               // all of it is in registers
+                    tc::tc_fence_before();
+                    tc::mbar_arrive(&B.acc_empty[b]);
+                }
                 if constexpr (D == 64) {
                     // (after a failed wait this goes on, only to keep meeting the other warps)
                     asm volatile("bar.sync 1, 128;" ::: "memory");
@@ -347,19 +389,29 @@ lin_part_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 #pragma unroll
                         for (int e = 0; e < 32; ++e) q[e] = __float_as_uint(__uint_as_float(q[e]) + cross[row][e]);
                 }
-                if (ok && row < D)
+                if (ok && quad * 32 < D) {
+                    uint8_t* at = stage + (box++ & 1) * 4096;
+                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");    // the box before the last has left
+                    __syncwarp();
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        uint32_t x[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            x[e] = __float_as_uint(__uint_as_float(r[8 * v + e]) + __uint_as_float(q[8 * v + e]));
-                        store32(out + (size_t)row * D + c + 8 * v, x, true);
+                    for (int v = 0; v < 8; ++v) {
+                        float4 x;
+                        x.x = __uint_as_float(r[4 * v]) + __uint_as_float(q[4 * v]);
+                        x.y = __uint_as_float(r[4 * v + 1]) + __uint_as_float(q[4 * v + 1]);
+                        x.z = __uint_as_float(r[4 * v + 2]) + __uint_as_float(q[4 * v + 2]);
+                        x.w = __uint_as_float(r[4 * v + 3]) + __uint_as_float(q[4 * v + 3]);
+                        *reinterpret_cast<float4*>(at + swizzled<128>(lane * 128 + v * 16)) = x;
                     }
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d(w.grad ? &map_qdo_out : &map_kv_out, at, c, (w.f * a.Hkv + w.h) * D + quad * 32);
+                        tc::bulk_commit();
+                    }
+                }
             }
-            tc::tc_fence_before();
-            tc::mbar_arrive(&B.acc_empty[b]);
         }
+        if (lane == 0) bulk_wait();
     }
     tc::tc_fence_before();
     __syncthreads();
@@ -371,75 +423,82 @@ lin_part_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 
 // ------------------------------------------------------------------ scan
 
-constexpr int kScanThreads = 128, kScanAhead = 16;
+constexpr int kScanThreads = 128, kScanAhead = 32;
 
 // From a sequence's chunk sums to the states before its chunks (y 0, in order) or
 // the gradients of the states after them (y 1, in reverse), in fp32; the kernels
-// that multiply by them get them in bf16. A thread owns four elements all along
-// (so slot_in may be slot_out) and loads kScanAhead chunks' sums at once.
+// that multiply by them get them in bf16. A thread owns two elements all along
+// (so slot_in may be slot_out) and has kScanAhead chunks' sums on their way at once:
+// what bounds the scan is the latency of these rounds (four elements and eight
+// chunks took 10 us for 32 chunks of 4 heads).
 template <int D>
 __global__ void __launch_bounds__(kScanThreads) lin_scan_bf16_kernel(const LinArgs a) {
-    constexpr int V = D * D / 4;
+    constexpr int V = D * D / 2;
     const bool grad = blockIdx.y;
     const int64_t unit = (int64_t)blockIdx.x * kScanThreads + threadIdx.x;
-    const int e = (int)(unit % V), h = (int)(unit / V % a.Hkv);
-    const int64_t b = unit / V / a.Hkv;
+    const int e = (int)(unit % V);
+    const int64_t bh = unit / V, b = bh / a.Hkv;
+    const int h = (int)(bh - b * a.Hkv);
     launch_dependents();
     int64_t lo, hi;
     const bool good = lin_range(a, b, lo, hi);
-    wait_for_kernels();
-    if (!good) return;
-    const float g2 = lin_g2(a, h), lfull = lin_pow(g2, kL);
+    const float g2 = lin_g2(a, h);
     const int64_t first = lin_slot(a, grad ? a.slot_out : a.slot_in, b);
     // (a backward scans k v^T for the states alone: the forward has stored the last one)
     const int64_t last = !grad && gridDim.y > 1 ? -1 : lin_slot(a, grad ? a.slot_in : a.slot_out, b);
-    float* store = grad ? a.dstate : a.state;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (first >= 0) s = reinterpret_cast<const float4*>(store + ((size_t)first * a.Hkv + h) * D * D)[e];
-    const int64_t nc = (hi - lo + kL - 1) / kL, c0 = grad ? nc - 1 : 0;
-    const int tail = (int)(hi - lo - (nc - 1) * kL);                             // rows of the last chunk
-    const int64_t at = ((lo / kL + b + c0) * a.Hkv + h) * V + e, step = (int64_t)a.Hkv * V * (grad ? -1 : 1);
-    const float4* in = reinterpret_cast<const float4*>(grad ? a.gpart : a.part) + at;
-    uint2* out = reinterpret_cast<uint2*>(grad ? a.gbf : a.sbf) + at;
+    float2* store = reinterpret_cast<float2*>(grad ? a.dstate : a.state);
+    float2 s = make_float2(0.f, 0.f);
+    if (good && first >= 0) s = store[((size_t)first * a.Hkv + h) * V + e];      // (older than the kernel before)
+    wait_for_kernels();
+    if (!good) return;
+    const int64_t nc = (hi - lo + kL - 1) / kL;
+    const float lfull = lin_pow(g2, kL), ltail = lin_pow(g2, (int)(hi - lo - (nc - 1) * kL));    // the last chunk's rows
+    const int64_t at = ((lo / kL + b + (grad ? nc - 1 : 0)) * a.Hkv + h) * V + e, step = (int64_t)a.Hkv * V * (grad ? -1 : 1);
+    const float2* in = reinterpret_cast<const float2*>(grad ? a.gpart : a.part) + at;
+    uint32_t* out = reinterpret_cast<uint32_t*>(grad ? a.gbf : a.sbf) + at;
     for (int64_t i = 0; i < nc; i += kScanAhead) {
         const int m = (int)min64(kScanAhead, nc - i);
-        float4 x[kScanAhead];
+        float2 x[kScanAhead];
+        const float2* p = in;
 #pragma unroll
-        for (int u = 0; u < kScanAhead; ++u)
-            if (u < m) x[u] = __ldcs(in + u * step);
+        for (int u = 0; u < kScanAhead; ++u) {
+            if (u < m) x[u] = __ldcs(p);
+            p += step;
+        }
 #pragma unroll
         for (int u = 0; u < kScanAhead; ++u)
             if (u < m) {
-                out[u * step] = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
-                const float l = i + u == (grad ? 0 : nc - 1) ? lin_pow(g2, tail) : lfull;
-                s.x = fmaf(l, s.x, x[u].x); s.y = fmaf(l, s.y, x[u].y);
-                s.z = fmaf(l, s.z, x[u].z); s.w = fmaf(l, s.w, x[u].w);
+                *out = pack_bf16x2(s.x, s.y);
+                out += step;
+                const float l = i + u == (grad ? 0 : nc - 1) ? ltail : lfull;
+                s.x = fmaf(l, s.x, x[u].x);
+                s.y = fmaf(l, s.y, x[u].y);
             }
-        in += kScanAhead * step;
-        out += kScanAhead * step;
+        in = p;
     }
-    if (last >= 0) reinterpret_cast<float4*>(store + ((size_t)last * a.Hkv + h) * D * D)[e] = s;
+    if (last >= 0) store[((size_t)last * a.Hkv + h) * V + e] = s;
 }
 
 // ------------------------------------------------------------------ rows
 
-// Shared memory of the rows kernel: a ring of (C, S) pairs, R, and an X tile for each warpgroup.
+// Shared memory of the rows kernel: C, S and R of a (chunk, KV head) pair, an X
+// tile for each group of warps, a box of outputs for each warp.
 template <int D> struct RowsLayout {
     static constexpr uint32_t kTile = D / 64 * 16384;                // 128 rows
     static constexpr uint32_t kState = D / 64 * D * 128;             // D rows
-    static constexpr uint32_t kOffS = kTile, kPair = kTile + kState;
-    static constexpr uint32_t kOffR = 2 * kPair, kOffX = kOffR + kTile;
-    static constexpr uint32_t kSmem = kOffX + 2 * kTile + 1024;
+    static constexpr uint32_t kOffS = kTile, kOffR = kOffS + kState, kOffX = kOffR + kTile, kOffStage = kOffX + 2 * kTile;
+    static constexpr uint32_t kStage = 32 * D;
+    static constexpr uint32_t kSmem = kOffStage + 16 * kStage + 1024;
 };
-constexpr int kRowsThreads = 352;
+constexpr int kRowsThreads = 3 * 32 + 2 * 256;
 
 struct RowsBarriers {
-    uint64_t c_full[2], st_full[2], pair_empty[2], r_full, r_empty;
-    // R's tail zeroed, or none (by the warpgroup of the pair's first head). Two, in turn: an issuing
-    // warp may still have to see a pair's when the other warpgroup is at the next pair's; the one
-    // after that needs C's slot, which both warps give up only after they have seen this one.
+    uint64_t c_full, st_full, pair_empty, r_full, r_empty;
+    // R's tail zeroed, or none (by the group of the pair's first head). Two, in turn: an issuing warp
+    // may still have to see a pair's when the other group is at the next pair's; the one after that
+    // needs C's place, which both warps give up only after they have seen this one.
     uint64_t r_ready[2];
-    uint64_t x_full[2], x_empty[2], s_full[2], p_full[2], o_full[2], o_free[2], drain[2];        // by warpgroup
+    uint64_t x_full[2], x_empty[2], s_full[2], p_full[2], o_full[2], o_free[2], drain[2];        // by group
     uint32_t tmem_base;
 };
 
@@ -480,19 +539,19 @@ struct HeadWalk {
 
 // out = scale [((X C^T) o M) R + diag(l^(i+1)) X S']. O: X, C, R, S' = Q, K, V, S;
 // dQ (GRAD): dO, V, K, S^T. A persistent CTA takes a run of heads. Warp 0 loads
-// (TMA); two warpgroups take the heads in turn, each with a warp (1, 2) that issues
-// its products and 256 columns of tensor memory of its own: scores [0, 128), which
-// the weighted scores in bf16 overwrite as the A operand of the second product,
-// and the output [128, 128 + D), which is X S' first and is scaled by l^(i+1)
-// there before the second product adds to it. (One issuing warp for both made each
-// second product wait for the other warpgroup's output to be read: 2.1 us a head.)
+// (TMA); two groups of eight warps take the heads in turn, each with a warp (1, 2)
+// that issues its products and 256 columns of tensor memory of its own: scores
+// [0, 128), which the weighted scores in bf16 overwrite as the A operand of the
+// second product, and the output [128, 128 + D), which is X S' first and is scaled
+// by l^(i+1) there before the second product adds to it. (One issuing warp for both
+// made each second product wait for the other group's output to be read: 2.1 us a head.)
 // Weights l^(i-j): for 32 x 32 blocks under the diagonal l^(i - 32 b - 31) (one per
 // row and block) times l^(31 - (j - 32 b)), both with exponents >= 0; on it from a table.
 template <int D, bool GRAD>
 __global__ void __launch_bounds__(kRowsThreads, 1)
 lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_c,
-                   const __grid_constant__ CUtensorMap map_r, const __grid_constant__ CUtensorMap map_s, const LinArgs a,
-                   int heads, int wide) {
+                   const __grid_constant__ CUtensorMap map_r, const __grid_constant__ CUtensorMap map_s,
+                   const __grid_constant__ CUtensorMap map_out, const LinArgs a, int heads) {
     using L = RowsLayout<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -501,18 +560,18 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     const int from = (int)((int64_t)heads * blockIdx.x / gridDim.x), to = (int)((int64_t)heads * (blockIdx.x + 1) / gridDim.x);
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
-            tc::mbar_init(&B.c_full[s], 1);
-            tc::mbar_init(&B.st_full[s], 1);
-            tc::mbar_init(&B.pair_empty[s], 2);
-            tc::mbar_init(&B.r_ready[s], 128);
+            tc::mbar_init(&B.r_ready[s], 256);
             tc::mbar_init(&B.x_full[s], 1);
             tc::mbar_init(&B.x_empty[s], 1);
             tc::mbar_init(&B.s_full[s], 1);
-            tc::mbar_init(&B.p_full[s], 128);
+            tc::mbar_init(&B.p_full[s], 256);
             tc::mbar_init(&B.o_full[s], 1);
-            tc::mbar_init(&B.o_free[s], 128);
+            tc::mbar_init(&B.o_free[s], 256);
             tc::mbar_init(&B.drain[s], 1);
         }
+        tc::mbar_init(&B.c_full, 1);
+        tc::mbar_init(&B.st_full, 1);
+        tc::mbar_init(&B.pair_empty, 2);
         tc::mbar_init(&B.r_full, 1);
         tc::mbar_init(&B.r_empty, 2);
         tc::fence_barrier_init();
@@ -521,26 +580,31 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         tc::tmem_alloc(&B.tmem_base, 512);
         tc::tmem_relinquish();
     }
+    if (threadIdx.x == 0) {
+        tc::prefetch_tmap(&map_x);
+        tc::prefetch_tmap(&map_c);
+        tc::prefetch_tmap(&map_r);
+        tc::prefetch_tmap(&map_s);
+    }
+    HeadWalk w(a, from, to);
+    bool more = w.next();                        // (its loads overlap the set-up)
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
     launch_dependents();
     const uint32_t tmem = B.tmem_base;
-    HeadWalk w(a, from, to);
     if (warp == 0) {
         // ------------------------------------------------------------ loads
         bool waited = false;
         int n_x = 0, n_pair = 0, n_r = 0;
-        while (w.next()) {
+        for (; more; more = w.next()) {
             const int row = (int)w.c.row0;
             if (w.first) {
-                const int s = w.pair & 1;
-                if (w.pair >= 2 && !tc::warp_wait(&B.pair_empty[s], ((w.pair >> 1) - 1) & 1, a.wait_err)) break;
+                if (w.pair >= 1 && !tc::warp_wait(&B.pair_empty, (w.pair - 1) & 1, a.wait_err)) break;
                 if (lane == 0) {
-                    tc::mbar_arrive_expect_tx(&B.c_full[s], L::kTile);
+                    tc::mbar_arrive_expect_tx(&B.c_full, L::kTile);
 #pragma unroll
-                    for (int b = 0; b < D / 64; ++b)
-                        tc::tma_load_3d(smem + s * L::kPair + b * 16384, &map_c, &B.c_full[s], 64 * b, w.h, row);
+                    for (int b = 0; b < D / 64; ++b) tc::tma_load_3d(smem + b * 16384, &map_c, &B.c_full, 64 * b, w.h, row);
                 }
             }
             {
@@ -555,15 +619,13 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                 n_x = w.it + 1;
             }
             if (w.first) {
-                const int s = w.pair & 1;
                 if (!waited) wait_for_kernels(); // the states; Q, K, V and dO are older than the kernels before
                 waited = true;
                 if (lane == 0) {
-                    tc::mbar_arrive_expect_tx(&B.st_full[s], L::kState);
+                    tc::mbar_arrive_expect_tx(&B.st_full, L::kState);
 #pragma unroll
                     for (int b = 0; b < D / 64; ++b)
-                        tc::tma_load_2d(smem + s * L::kPair + L::kOffS + b * (D * 128), &map_s, &B.st_full[s], 64 * b,
-                                        (w.f * a.Hkv + w.h) * D);
+                        tc::tma_load_2d(smem + L::kOffS + b * (D * 128), &map_s, &B.st_full, 64 * b, (w.f * a.Hkv + w.h) * D);
                 }
                 n_pair = w.pair + 1;
                 if (w.pair >= 1 && !tc::warp_wait(&B.r_empty, (w.pair - 1) & 1, a.wait_err)) break;
@@ -580,14 +642,14 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         // None of this CTA's copies may still be landing when it exits.
         if (lane == 0) {
             for (int i = max(0, n_x - 2); i < n_x; ++i) tc::drain_wait(&B.x_full[i & 1], (i >> 1) & 1);
-            for (int i = max(0, n_pair - 2); i < n_pair; ++i) {
-                tc::drain_wait(&B.c_full[i & 1], (i >> 1) & 1);
-                tc::drain_wait(&B.st_full[i & 1], (i >> 1) & 1);
+            if (n_pair > 0) {
+                tc::drain_wait(&B.c_full, (n_pair - 1) & 1);
+                tc::drain_wait(&B.st_full, (n_pair - 1) & 1);
             }
             if (n_r > 0) tc::drain_wait(&B.r_full, (n_r - 1) & 1);
         }
     } else if (warp <= 2) {
-        // ------------------------------------------------------------ products of one warpgroup
+        // ------------------------------------------------------------ products of one group
         const bool leader = tc::elect_one_sync();
         const int wg = warp - 1;
         const uint32_t idesc_x = tc::idesc_bf16(128, 128, false, false);         // X C^T
@@ -596,34 +658,35 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         const uint32_t sm = tc::smem_u32(smem), t = tmem + wg * 256;
         const uint64_t dr = tc::sdesc(sm + L::kOffR, 16384, 1024);
         const uint64_t dx = tc::sdesc(sm + L::kOffX + wg * L::kTile, 16, 1024);
-        bool r_seen = true;                      // this walk has waited for its pair's R
+        bool r_seen = true;                      // this warp has waited for its pair's C, S and R
+        auto wait_cs = [&](int pair) -> bool {
+            return tc::warp_wait(&B.c_full, pair & 1, a.wait_err) && tc::warp_wait(&B.st_full, pair & 1, a.wait_err);
+        };
         auto wait_r = [&](int pair) -> bool {
             r_seen = true;
             return tc::warp_wait(&B.r_full, pair & 1, a.wait_err) &&
                    tc::warp_wait(&B.r_ready[pair & 1], (pair >> 1) & 1, a.wait_err);
         };
-        while (w.next()) {
-            const int ps = w.pair & 1;
+        for (; more; more = w.next()) {
             if (w.first && w.pair > 0) {
                 // This warp is through with the pair before (both warps say so of every pair, and both
-                // see every R arrive, so that no wait for a phase can fall a whole period behind).
-                if (!r_seen && !wait_r(w.pair - 1)) break;
+                // see every pair arrive, so that no wait for a phase can fall a whole period behind).
+                if (!r_seen && !(wait_cs(w.pair - 1) && wait_r(w.pair - 1))) break;
                 if (leader) {
-                    tc::mma_commit(&B.pair_empty[ps ^ 1]);
+                    tc::mma_commit(&B.pair_empty);
                     tc::mma_commit(&B.r_empty);
                 }
                 __syncwarp();
             }
             if (w.first) r_seen = false;
             if ((w.it & 1) != wg) continue;
-            const int n = w.it >> 1;             // heads of this warpgroup before
-            // (X first: it is loaded after this pair's C, whose slot was free by then of the pair before the last)
+            const int n = w.it >> 1;             // heads of this group before
+            if (!tc::warp_wait(&B.c_full, w.pair & 1, a.wait_err)) break;
             if (!tc::warp_wait(&B.x_full[wg], n & 1, a.wait_err)) break;
-            if (!tc::warp_wait(&B.c_full[ps], (w.pair >> 1) & 1, a.wait_err)) break;
             if (n > 0 && !tc::warp_wait(&B.o_free[wg], (n - 1) & 1, a.wait_err)) break;
             tc::tc_fence_after();
             if (leader) {
-                const uint64_t dc = tc::sdesc(sm + ps * L::kPair, 16, 1024);
+                const uint64_t dc = tc::sdesc(sm, 16, 1024);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint32_t at = (k >> 2) * 16384 + (k & 3) * 32;
@@ -632,11 +695,10 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                 tc::mma_commit(&B.s_full[wg]);
             }
             __syncwarp();
-            if (!tc::warp_wait(&B.st_full[ps], (w.pair >> 1) & 1, a.wait_err)) break;
+            if (!tc::warp_wait(&B.st_full, w.pair & 1, a.wait_err)) break;
             tc::tc_fence_after();
             if (leader) {
-                const uint64_t ds = GRAD ? tc::sdesc(sm + ps * L::kPair + L::kOffS, 16, 1024)
-                                         : tc::sdesc(sm + ps * L::kPair + L::kOffS, D * 128, 1024);
+                const uint64_t ds = GRAD ? tc::sdesc(sm + L::kOffS, 16, 1024) : tc::sdesc(sm + L::kOffS, D * 128, 1024);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
                     tc::mma_bf16(t + 128, tc::sdesc_at(dx, (k >> 2) * 16384 + (k & 3) * 32),
@@ -650,7 +712,7 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             tc::tc_fence_after();
             if (leader) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) tc::mma_bf16_ts(t + 128, t + k * 8, tc::sdesc_at(dr, k * 2048), idesc_r, 1u);
+                for (int k = 0; k < 8; ++k) tc::mma_bf16_ts(t + 128, t + p_col(k), tc::sdesc_at(dr, k * 2048), idesc_r, 1u);
                 tc::mma_commit(&B.o_full[wg]);   // the whole output: its second phase
             }
             __syncwarp();
@@ -662,29 +724,30 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         __syncwarp();
     } else {
         // ------------------------------------------------------------ weights and outputs
-        const int wg = (warp - 3) >> 2, quad = warp & 3, i = quad * 32 + lane;   // row of the chunk
-        const int t128 = (threadIdx.x - 96) & 127;
+        const int wg = (warp - 3) >> 3, half = (warp - 3) >> 2 & 1, quad = warp & 3, i = quad * 32 + lane;     // row of the chunk
+        const int t256 = (threadIdx.x - 96) & 255;
         const uint32_t t = tmem + ((uint32_t)(quad * 32) << 16) + wg * 256;
         const float scale = rsqrtf((float)D);
         const LinRows& out = GRAD ? a.dq : a.o;
-        // l's powers, kept while the KV head stays; each warpgroup has tables of its own:
+        uint8_t* stage = smem + L::kOffStage + (warp - 3) * L::kStage;
+        // l's powers, kept while the KV head stays; each group has tables of its own:
         // l^(x - 31) for x >= 31, else 0, and l^(31 - x).
         __shared__ float diag[2][64];
         __shared__ __align__(16) float up[2][32];
         int h_of = -1;
-        float rb[3], li1 = 0.f;
+        float rb[2], li1 = 0.f;                  // of blocks 2 half, 2 half + 1
         bool ok = true;
-        while (w.next()) {
+        for (; more; more = w.next()) {
             if (w.h != h_of) {
                 h_of = w.h;
                 const float g2 = lin_g2(a, w.h);
-                asm volatile("bar.sync %0, 128;" :: "r"(1 + wg) : "memory");     // nobody reads the old table any more
-                if (t128 < 64) diag[wg][t128] = t128 >= 31 ? lin_pow(g2, t128 - 31) : 0.f;
-                else if (t128 < 96) up[wg][t128 - 64] = lin_pow(g2, 95 - t128);
+                asm volatile("bar.sync %0, 256;" :: "r"(1 + wg) : "memory");     // nobody reads the old table any more
+                if (t256 < 64) diag[wg][t256] = t256 >= 31 ? lin_pow(g2, t256 - 31) : 0.f;
+                else if (t256 < 96) up[wg][t256 - 64] = lin_pow(g2, 95 - t256);
 #pragma unroll
-                for (int b = 0; b < 3; ++b) rb[b] = b < quad ? lin_pow(g2, i - 32 * b - 31) : 0.f;
+                for (int b = 0; b < 2; ++b) rb[b] = 2 * half + b < quad ? lin_pow(g2, i - 32 * (2 * half + b) - 31) : 0.f;
                 li1 = lin_pow(g2, i + 1);
-                asm volatile("bar.sync %0, 128;" :: "r"(1 + wg) : "memory");
+                asm volatile("bar.sync %0, 256;" :: "r"(1 + wg) : "memory");
             }
             // (After a failed wait the walk goes on, only to keep meeting the other warps at the barriers.)
             if ((w.it & 1) != wg || !ok) continue;
@@ -692,59 +755,59 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             if (ok && w.first) {
                 if (w.c.rows < kL) {             // what lies behind the sequence may be anything
                     ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.r_full, w.pair & 1, a.wait_err));
-                    if (ok) zero_tail<D>(smem + L::kOffR, w.c.rows, t128, 128);
+                    if (ok) zero_tail<D>(smem + L::kOffR, w.c.rows, t256, 256);
                     tc::fence_proxy_async_smem();
                 }
                 tc::mbar_arrive(&B.r_ready[w.pair & 1]);
             }
             if (!ok) continue;
             tc::tc_fence_after();
-            uint32_t pk[4][16];
+            uint32_t pk[32];
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                if (b > quad) {
+            for (int b = 0; b < 2; ++b) {
+                const int block = 2 * half + b;
+                if (block > quad) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) pk[b][e] = 0u;
+                    for (int e = 0; e < 16; ++e) pk[16 * b + e] = 0u;
                     continue;
                 }
                 uint32_t r[32];
-                tc::tmem_ld32(t + 32 * b, r);
+                tc::tmem_ld32(t + 32 * block, r);
                 tc::tmem_wait_ld(r);
-                if (b < quad) {
-                    const float f = b < 3 ? rb[b < 3 ? b : 0] : 0.f;
+                if (block < quad) {
+                    const float f = rb[b];
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
-                        pk[b][e] = pack_bf16x2(__uint_as_float(r[2 * e]) * (up[wg][2 * e] * f),
-                                               __uint_as_float(r[2 * e + 1]) * (up[wg][2 * e + 1] * f));
+                        pk[16 * b + e] = pack_bf16x2(__uint_as_float(r[2 * e]) * (up[wg][2 * e] * f),
+                                                     __uint_as_float(r[2 * e + 1]) * (up[wg][2 * e + 1] * f));
                 } else {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const float x = 2 * e <= lane ? __uint_as_float(r[2 * e]) * diag[wg][lane - 2 * e + 31] : 0.f;
                         const float y = 2 * e + 1 <= lane ? __uint_as_float(r[2 * e + 1]) * diag[wg][lane - 2 * e + 30] : 0.f;
-                        pk[b][e] = pack_bf16x2(x, y);
+                        pk[16 * b + e] = pack_bf16x2(x, y);
                     }
                 }
             }
-#pragma unroll
-            for (int b = 0; b < 4; ++b) tc::tmem_st16(t + 16 * b, pk[b]);
+            tc::tmem_st32(t + 64 * half, pk);
             ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.o_full[wg], 0, a.wait_err));
             if (!ok) continue;
             tc::tc_fence_after();
-            scale_row<D>(t + 128, li1);
+            scale_half<D>(t + 128 + D / 2 * half, li1);
             tc::tmem_wait_st();
             tc::tc_fence_before();
             tc::mbar_arrive(&B.p_full[wg]);
             ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.o_full[wg], 1, a.wait_err));
             if (!ok) continue;
             tc::tc_fence_after();
-            // The row leaves tensor memory first: the next head's products need not wait for the stores.
-            uint32_t o[D / 2];
-            load_row<D>(t + 128, scale, o);
+            // The rows leave tensor memory first: the next head's products need not wait for the stores.
+            uint32_t o[D / 4];
+            load_half<D>(t + 128 + D / 2 * half, scale, o);
             tc::tc_fence_before();
             tc::mbar_arrive(&B.o_free[wg]);
-            if (i < w.c.rows)
-                store_row<D>(o, static_cast<__nv_bfloat16*>(out.p) + (w.c.row0 + i) * out.stride + (int64_t)w.head * D, wide);
+            store_half<D>(o, &map_out, stage, lane, w.c.rows - 32 * quad, D / 2 * half, w.head, w.c.row0 + 32 * quad, out);
         }
+        if (lane == 0) bulk_wait();
     }
     tc::tc_fence_before();
     __syncthreads();
@@ -762,27 +825,28 @@ template <int D> struct ColsLayout {
     static constexpr uint32_t kSmem = kOffDo + 2 * kTile + 1024;
     static constexpr uint32_t kColDv = 256, kColDk = 256 + D;
 };
-constexpr int kColsThreads = 352;
+constexpr int kColsThreads = 3 * 32 + 2 * 256;
 
 struct ColsBarriers {
     uint64_t k_full, v_full, g_full, q_full[2], do_full[2], q_empty[2], do_empty[2];
     uint64_t q_ready[2], do_ready[2];            // their tails zeroed (a chunk of less than 128 rows)
-    uint64_t s_full[2], init_full[2], p_full[2], acc_full[2];                     // by warpgroup
+    uint64_t s_full[2], init_full[2], p_full[2], acc_full[2];                     // by group
     uint32_t tmem_base;
 };
 
 // dV = scale sum_heads ((Q K^T) o M)^T dO + diag(l^(m-1-j)) K G and dK = scale
 // sum_heads ((dO V^T) o M)^T Q + diag(l^(m-1-j)) V G^T of one chunk and KV head.
 // Scores are formed transposed (keys are the accumulator's rows): K Q^T in
-// columns [0, 128) for warpgroup 0 (dV), V dO^T in [128, 256) for warpgroup 1
-// (dK), each with an issuing warp of its own; their weighted bf16 values overwrite
-// them as A operands. dV and dK stay in tensor memory over all heads; they start as
+// columns [0, 128) for one group of eight warps (dV), V dO^T in [128, 256) for
+// another (dK), each with an issuing warp of its own; their weighted bf16 values
+// overwrite them as A operands. dV and dK stay in tensor memory over all heads; they start as
 // K G and V G^T, scaled there by l^(m-1-j) / scale.
 template <int D>
 __global__ void __launch_bounds__(kColsThreads, 1)
 lin_cols_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
-                   const __grid_constant__ CUtensorMap map_g, const LinArgs a, int wide) {
+                   const __grid_constant__ CUtensorMap map_g, const __grid_constant__ CUtensorMap map_dv,
+                   const __grid_constant__ CUtensorMap map_dk, const LinArgs a) {
     using L = ColsLayout<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -807,11 +871,11 @@ lin_cols_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             tc::mbar_init(&B.do_full[s], 1);
             tc::mbar_init(&B.q_empty[s], 2);
             tc::mbar_init(&B.do_empty[s], 2);
-            tc::mbar_init(&B.q_ready[s], 128);
-            tc::mbar_init(&B.do_ready[s], 128);
+            tc::mbar_init(&B.q_ready[s], 256);
+            tc::mbar_init(&B.do_ready[s], 256);
             tc::mbar_init(&B.s_full[s], 1);
             tc::mbar_init(&B.init_full[s], 1);
-            tc::mbar_init(&B.p_full[s], 128);
+            tc::mbar_init(&B.p_full[s], 256);
             tc::mbar_init(&B.acc_full[s], 1);
         }
         tc::mbar_init(&B.k_full, 1);
@@ -921,7 +985,7 @@ lin_cols_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             if (leader) {
                 const uint64_t db = tc::sdesc(sm + other + s * L::kTile, 16384, 1024);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) tc::mma_bf16_ts(acc, t + k * 8, tc::sdesc_at(db, k * 2048), id_acc, 1u);
+                for (int k = 0; k < 8; ++k) tc::mma_bf16_ts(acc, t + p_col(k), tc::sdesc_at(db, k * 2048), id_acc, 1u);
                 tc::mma_commit(&other_empty[s]);
             }
             __syncwarp();
@@ -933,64 +997,67 @@ lin_cols_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         __syncwarp();
     } else {
         // ------------------------------------------------------------ weights and outputs
-        const int x = (warp - 3) >> 2, quad = warp & 3, j = quad * 32 + lane;    // key row of the chunk
-        const int t128 = (threadIdx.x - 96) & 127;
-        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16), acc = lanes + (x ? L::kColDk : L::kColDv), t = lanes + 128 * x;
+        const int x = (warp - 3) >> 3, half = (warp - 3) >> 2 & 1, quad = warp & 3, j = quad * 32 + lane;      // key row of the chunk
+        const int t256 = (threadIdx.x - 96) & 255;
+        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16), t = lanes + 128 * x;
+        const uint32_t acc = lanes + (x ? L::kColDk : L::kColDv) + D / 2 * half;
         const float scale = rsqrtf((float)D);
-        // A chunk's tail: warpgroup 0 zeroes Q's rows, warpgroup 1 dO's.
+        // A chunk's tail: group 0 zeroes Q's rows, group 1 dO's.
         auto tails = [&](int i) -> bool {
             const int s = i & 1;
             uint64_t* full = x ? B.do_full : B.q_full;
             if (!__all_sync(0xffffffffu, tc::mbar_wait(&full[s], (i >> 1) & 1, a.wait_err))) return false;
-            zero_tail<D>(smem + (x ? L::kOffDo : L::kOffQ) + s * L::kTile, c.rows, t128, 128);
+            zero_tail<D>(smem + (x ? L::kOffDo : L::kOffQ) + s * L::kTile, c.rows, t256, 256);
             tc::fence_proxy_async_smem();
             tc::mbar_arrive(x ? &B.do_ready[s] : &B.q_ready[s]);
             return true;
         };
-        float rb[4];
+        float rb[2];                             // of blocks 2 half, 2 half + 1
 #pragma unroll
-        for (int b = 0; b < 4; ++b) rb[b] = b > quad ? lin_pow(g2, 32 * b - j) : 0.f;
+        for (int b = 0; b < 2; ++b) rb[b] = 2 * half + b > quad ? lin_pow(g2, 32 * (2 * half + b) - j) : 0.f;
         bool ok = !tail || tails(0);
         for (int i = 0; ok && i < g; ++i) {
             if (tail && i + 1 < g && !(ok = tails(i + 1))) break;
             ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.s_full[x], i & 1, a.wait_err));
             if (!ok) break;
             tc::tc_fence_after();
-            uint32_t pk[4][16];
+            uint32_t pk[32];
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {                // queries 32 b ..
-                if (b < quad) {
+            for (int b = 0; b < 2; ++b) {
+                const int block = 2 * half + b;  // queries 32 block ..
+                if (block < quad) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) pk[b][e] = 0u;
+                    for (int e = 0; e < 16; ++e) pk[16 * b + e] = 0u;
                     continue;
                 }
                 uint32_t r[32];
-                tc::tmem_ld32(t + 32 * b, r);
+                tc::tmem_ld32(t + 32 * block, r);
                 tc::tmem_wait_ld(r);
-                const int left = c.rows - 32 * b;
-                if (b > quad) {
+                const int left = c.rows - 32 * block;
+                if (left < 32) {                 // queries behind the sequence: anything
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float p0 = 2 * e < left ? __uint_as_float(r[2 * e]) * (pw[2 * e] * rb[b]) : 0.f;
-                        const float p1 = 2 * e + 1 < left ? __uint_as_float(r[2 * e + 1]) * (pw[2 * e + 1] * rb[b]) : 0.f;
-                        pk[b][e] = pack_bf16x2(p0, p1);
-                    }
+                    for (int e = 0; e < 32; ++e) r[e] = e < left ? r[e] : 0u;
+                }
+                if (block > quad) {
+                    const float f = rb[b];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        pk[16 * b + e] = pack_bf16x2(__uint_as_float(r[2 * e]) * (pw[2 * e] * f), __uint_as_float(r[2 * e + 1]) * (pw[2 * e + 1] * f));
                 } else {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const float p0 = 2 * e >= lane && 2 * e < left ? __uint_as_float(r[2 * e]) * diag[2 * e - lane + 31] : 0.f;
-                        const float p1 = 2 * e + 1 >= lane && 2 * e + 1 < left ? __uint_as_float(r[2 * e + 1]) * diag[2 * e + 32 - lane] : 0.f;
-                        pk[b][e] = pack_bf16x2(p0, p1);
+                        const float p0 = 2 * e >= lane ? __uint_as_float(r[2 * e]) * diag[2 * e - lane + 31] : 0.f;
+                        const float p1 = 2 * e + 1 >= lane ? __uint_as_float(r[2 * e + 1]) * diag[2 * e + 32 - lane] : 0.f;
+                        pk[16 * b + e] = pack_bf16x2(p0, p1);
                     }
                 }
             }
-#pragma unroll
-            for (int b = 0; b < 4; ++b) tc::tmem_st16(t + 16 * b, pk[b]);
+            tc::tmem_st32(t + 64 * half, pk);
             if (i == 0) {
                 ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.init_full[x], 0, a.wait_err));
                 if (!ok) break;
                 tc::tc_fence_after();
-                scale_row<D>(acc, j < c.rows ? lin_pow(g2, c.rows - 1 - j) / scale : 0.f);
+                scale_half<D>(acc, j < c.rows ? lin_pow(g2, c.rows - 1 - j) / scale : 0.f);
             }
             tc::tmem_wait_st();
             tc::tc_fence_before();
@@ -999,12 +1066,13 @@ lin_cols_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.acc_full[x], 0, a.wait_err));
         if (ok) {
             tc::tc_fence_after();
-            const LinRows& out = x ? a.dk : a.dv;
-            uint32_t o[D / 2];
-            load_row<D>(acc, scale, o);
-            if (j < c.rows)
-                store_row<D>(o, static_cast<__nv_bfloat16*>(out.p) + (c.row0 + j) * out.stride + (int64_t)h * D, wide >> x & 1);
+            uint32_t o[D / 4];
+            load_half<D>(acc, scale, o);
+            // (staged where K lay for group 0, V for group 1: no other product has read them)
+            store_half<D>(o, x ? &map_dk : &map_dv, smem + (x ? L::kOffV : 0) + ((warp - 3) & 7) * (32 * D), lane, c.rows - 32 * quad,
+                          D / 2 * half, h, c.row0 + 32 * quad, x ? a.dk : a.dv);
         }
+        if (lane == 0) bulk_wait();
     }
     tc::tc_fence_before();
     __syncthreads();
@@ -1019,10 +1087,17 @@ lin_cols_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 bool rows_map(CUtensorMap* m, const LinRows& x, int H, const LinArgs& a, int rows, std::string* why) {
     return make_tmap_3d(m, x.p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.d, H, a.n, a.d * 2, x.stride * 2, 64, 1, rows, why);
 }
+// Of an output, as store_half writes it.
+bool half_map(CUtensorMap* m, const LinRows& x, int H, const LinArgs& a, std::string* why) {
+    return make_tmap_3d(m, x.p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.d, H, a.n, a.d * 2, x.stride * 2, a.d / 2, 1, 32, why,
+                        a.d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+bool sums_map(CUtensorMap* m, const float* p, const LinArgs& a, std::string* why) {
+    return make_tmap_2d(m, p, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.d, (uint64_t)a.n_chunks * a.Hkv * a.d, a.d * 4, 32, 32, why);
+}
 bool states_map(CUtensorMap* m, const void* p, const LinArgs& a, std::string* why) {
     return make_tmap_2d(m, p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.d, (uint64_t)a.n_chunks * a.Hkv * a.d, a.d * 2, 64, a.d, why);
 }
-bool wide_rows(const LinRows& x) { return (reinterpret_cast<uintptr_t>(x.p) & 31) == 0 && x.stride % 16 == 0; }
 
 // Launches a kernel that may start before the stream's last kernel, one of this
 // file's, has ended; it waits for that one itself (wait_for_kernels) before it
@@ -1045,18 +1120,19 @@ template <int D> cudaError_t states(const LinArgs& a, bool both, cudaStream_t s,
     if (e != cudaSuccess) return e;
     const int nz = both ? 2 : 1;
     if (a.n) {
-        CUtensorMap k, v, q, go;
-        if (!rows_map(&k, a.k, a.Hkv, a, kPartRows, why) || !rows_map(&v, a.v, a.Hkv, a, kPartRows, why)) return cudaErrorInvalidValue;
-        q = k;
-        go = v;
-        if (both && (!rows_map(&q, a.q, a.Hq, a, kPartRows, why) || !rows_map(&go, a.dout, a.Hq, a, kPartRows, why)))
+        CUtensorMap k, v, q, go, out, gout;
+        if (!rows_map(&k, a.k, a.Hkv, a, kPartRows, why) || !rows_map(&v, a.v, a.Hkv, a, kPartRows, why) || !sums_map(&out, a.part, a, why))
+            return cudaErrorInvalidValue;
+        q = k; go = v; gout = out;               // (unused by a forward)
+        if (both && (!rows_map(&q, a.q, a.Hq, a, kPartRows, why) || !rows_map(&go, a.dout, a.Hq, a, kPartRows, why) ||
+                     !sums_map(&gout, a.gpart, a, why)))
             return cudaErrorInvalidValue;
         const int grid = std::min(a.n_chunks * a.Hkv * nz, sm_count());
         ProfScope ps("lin_part_tc_kernel", s);
-        lin_part_tc_kernel<D><<<grid, kPartThreads, PartLayout<D>::kSmem, s>>>(q, k, v, go, a, both);
+        lin_part_tc_kernel<D><<<grid, kPartThreads, PartLayout<D>::kSmem, s>>>(q, k, v, go, out, gout, a, both);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    const dim3 grid((unsigned)(a.n_seq * a.Hkv * (D * D / 4 / kScanThreads)), nz);
+    const dim3 grid((unsigned)(a.n_seq * a.Hkv * (D * D / 2 / kScanThreads)), nz);
     ProfScope ps("lin_scan_bf16_kernel", s);
     if (a.n) return launch_after(lin_scan_bf16_kernel<D>, grid, kScanThreads, 0, s, a);
     lin_scan_bf16_kernel<D><<<grid, kScanThreads, 0, s>>>(a);          // no sums before it
@@ -1067,27 +1143,29 @@ template <int D, bool GRAD> cudaError_t rows(const LinArgs& a, cudaStream_t s, s
     static SmemGrant grant;
     const cudaError_t e = allow_smem(lin_rows_tc_kernel<D, GRAD>, RowsLayout<D>::kSmem, grant);
     if (e != cudaSuccess) return e;
-    CUtensorMap x, c, r, st;
+    CUtensorMap x, c, r, st, out;
     if (!rows_map(&x, GRAD ? a.dout : a.q, a.Hq, a, kL, why) || !rows_map(&c, GRAD ? a.v : a.k, a.Hkv, a, kL, why) ||
-        !rows_map(&r, GRAD ? a.k : a.v, a.Hkv, a, kL, why) || !states_map(&st, a.sbf, a, why))
+        !rows_map(&r, GRAD ? a.k : a.v, a.Hkv, a, kL, why) || !states_map(&st, a.sbf, a, why) ||
+        !half_map(&out, GRAD ? a.dq : a.o, a.Hq, a, why))
         return cudaErrorInvalidValue;
     const int heads = a.n_chunks * a.Hq;
     ProfScope ps("lin_rows_tc_kernel", s);
     return launch_after(lin_rows_tc_kernel<D, GRAD>, dim3(std::min(heads, sm_count())), kRowsThreads, RowsLayout<D>::kSmem, s, x, c, r, st,
-                        a, heads, (int)wide_rows(GRAD ? a.dq : a.o));
+                        out, a, heads);
 }
 
 template <int D> cudaError_t cols(const LinArgs& a, cudaStream_t s, std::string* why) {
     static SmemGrant grant;
     const cudaError_t e = allow_smem(lin_cols_tc_kernel<D>, ColsLayout<D>::kSmem, grant);
     if (e != cudaSuccess) return e;
-    CUtensorMap q, k, v, go, gs;
+    CUtensorMap q, k, v, go, gs, dv, dk;
     if (!rows_map(&q, a.q, a.Hq, a, kL, why) || !rows_map(&k, a.k, a.Hkv, a, kL, why) || !rows_map(&v, a.v, a.Hkv, a, kL, why) ||
-        !rows_map(&go, a.dout, a.Hq, a, kL, why) || !states_map(&gs, a.gbf, a, why))
+        !rows_map(&go, a.dout, a.Hq, a, kL, why) || !states_map(&gs, a.gbf, a, why) ||
+        !half_map(&dv, a.dv, a.Hkv, a, why) || !half_map(&dk, a.dk, a.Hkv, a, why))
         return cudaErrorInvalidValue;
     ProfScope ps("lin_cols_tc_kernel", s);
-    return launch_after(lin_cols_tc_kernel<D>, dim3(a.n_chunks, a.Hkv), kColsThreads, ColsLayout<D>::kSmem, s, q, k, v, go, gs, a,
-                        (wide_rows(a.dv) ? 1 : 0) | (wide_rows(a.dk) ? 2 : 0));
+    return launch_after(lin_cols_tc_kernel<D>, dim3(a.n_chunks, a.Hkv), kColsThreads, ColsLayout<D>::kSmem, s, q, k, v, go, gs, dv,
+                        dk, a);
 }
 
 template <int D> cudaError_t fwd(const LinArgs& a, cudaStream_t s, std::string* why) {
