@@ -68,7 +68,7 @@ bool on_tensor_cores(const pkv_lin* lin) { return lin->desc.dtype == PKV_BF16 &&
 pkv_status chunk_states(pkv_lin* lin, LinArgs* a, bool bwd, cudaStream_t cs, const char* who) {
     const bool tc = on_tensor_cores(lin);
     a->n_chunks = (int)lin_chunks(a->n, a->n_seq, tc ? kLinTcChunk : kLinSimtChunk);
-    if ((int64_t)a->n_chunks * std::max(a->Hkv * a->d, a->Hq) > kMaxGrid / 2) return fail(PKV_ERR_UNSUPPORTED, std::string(who) + ": too many rows");
+    if ((int64_t)a->n_chunks * std::max(a->Hkv * a->d, a->Hkv + a->Hq) > kMaxGrid / 2) return fail(PKV_ERR_UNSUPPORTED, std::string(who) + ": too many rows");
     const size_t one = (size_t)a->n_chunks * a->Hkv * a->d * a->d, set = tc ? one + one / 2 : one, floats = set * (bwd ? 2 : 1);
     if (lin->scratch_floats < floats) {
         if (capturing(cs))

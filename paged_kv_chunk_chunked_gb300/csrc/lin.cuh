@@ -79,8 +79,21 @@ struct LinChunk {
     int rows;                        // 1 .. L
 };
 
+// The first 32 sequences' rows, a sequence a lane: kernels that look many chunks up
+// load them once.
+struct LinCuts {
+    int64_t lo = 0, hi = 0;
+    __device__ __forceinline__ explicit LinCuts(const LinArgs& a, int64_t b0 = 0) {
+        const int64_t b = b0 + threadIdx.x % 32;
+        if (a.cu && b < a.n_seq) {
+            lo = a.cu[b];
+            hi = a.cu[b + 1];
+        }
+    }
+};
+
 // The rows of chunk number f; false: there is no such chunk. Called by whole warps.
-template <int L> __device__ __forceinline__ bool lin_chunk(const LinArgs& a, int f, LinChunk& c) {
+template <int L> __device__ __forceinline__ bool lin_chunk(const LinArgs& a, const LinCuts& first, int f, LinChunk& c) {
     int64_t b = 0, lo = 0, hi = a.n;
     if (a.cu) {
         // The last sequence whose chunks start at or before f (numbers ascend with b): lane x
@@ -88,13 +101,12 @@ template <int L> __device__ __forceinline__ bool lin_chunk(const LinArgs& a, int
         const int lane = threadIdx.x % 32;
         b = -1;
         for (int64_t b0 = 0; b0 < a.n_seq; b0 += 32) {
-            const bool in = b0 + lane < a.n_seq;
-            const int64_t l = in ? a.cu[b0 + lane] : 0, r = in ? a.cu[b0 + lane + 1] : 0;
-            const int k = __popc(__ballot_sync(0xffffffffu, in && l / L + b0 + lane <= f));
+            const LinCuts x = b0 ? LinCuts(a, b0) : first;
+            const int k = __popc(__ballot_sync(0xffffffffu, b0 + lane < a.n_seq && x.lo / L + b0 + lane <= f));
             if (k > 0) {
                 b = b0 + k - 1;
-                lo = __shfl_sync(0xffffffffu, l, k - 1);
-                hi = __shfl_sync(0xffffffffu, r, k - 1);
+                lo = __shfl_sync(0xffffffffu, x.lo, k - 1);
+                hi = __shfl_sync(0xffffffffu, x.hi, k - 1);
             }
             if (k < 32) break;
         }
@@ -107,6 +119,7 @@ template <int L> __device__ __forceinline__ bool lin_chunk(const LinArgs& a, int
     c.rows = (int)min64(L, hi - lo - off);
     return true;
 }
+template <int L> __device__ __forceinline__ bool lin_chunk(const LinArgs& a, int f, LinChunk& c) { return lin_chunk<L>(a, LinCuts(a), f, c); }
 
 __device__ __forceinline__ float lin_g2(const LinArgs& a, int kvh) {
     return a.log_decay ? a.log_decay[kvh] * kLog2e : 0.f;
@@ -115,12 +128,13 @@ __device__ __forceinline__ float lin_g2(const LinArgs& a, int kvh) {
 __device__ __forceinline__ float lin_pow(float g2, int m) { return m == 0 ? 1.f : exp2f(g2 * (float)m); }
 
 // A sequence's slot, checked; -1 for none.
-__device__ __forceinline__ int64_t lin_slot(const LinArgs& a, const int32_t* slots, int64_t b) {
-    if (!slots) return -1;
-    const int32_t s = slots[b];
+__device__ __forceinline__ int64_t lin_good_slot(const LinArgs& a, int32_t s) {
     if (s >= -1 && s < a.n_slots) return s;
     report_error(a.err, kErrBadSlot);
     return -1;
+}
+__device__ __forceinline__ int64_t lin_slot(const LinArgs& a, const int32_t* slots, int64_t b) {
+    return slots ? lin_good_slot(a, slots[b]) : -1;
 }
 
 // CUDA-core kernels (chunks of kLinSimtChunk rows).

@@ -15,6 +15,7 @@
 #include <algorithm>
 
 #include "lin.cuh"
+#include "mod.cuh"
 #include "tc.cuh"
 
 namespace pkv {
@@ -112,17 +113,16 @@ template <int D> __device__ __forceinline__ void zero_tail(uint8_t* tile, int m,
 
 // ------------------------------------------------------------------ sums of a chunk
 
-constexpr int kPartRows = 64, kPartRaw = 3, kPartSplit = 2, kPartWarps = 8;
+constexpr int kPartRows = 64, kPartRaw = 5, kPartSplit = 2, kPartWarps = 8;
 constexpr int kPartThreads = (2 + kPartWarps + 4) * 32;
 
 template <int D> struct PartLayout {
     static constexpr uint32_t kBlock = kPartRows * 128;              // 64 columns of a stage's rows
     static constexpr uint32_t kOp = D / 64 * kBlock;                 // one operand
     static constexpr uint32_t kRaw = 2 * kOp;                        // A as loaded, R
-    static constexpr uint32_t kSplit = (D == 128 ? 3 : 4) * kOp;     // A's three terms (D 64: and zeros)
-    static constexpr uint32_t kOffSplit = kPartRaw * kRaw;
-    static constexpr uint32_t kOffStage = kOffSplit + kPartSplit * kSplit;       // two 32 x 32 boxes of sums a warp
-    static constexpr uint32_t kSmem = kOffStage + 4 * 2 * 4096 + 1024;
+    static constexpr uint32_t kOffStage = kPartRaw * kRaw;           // a unit's sums, in boxes of 32 x 32
+    static constexpr uint32_t kSmem = kOffStage + D * D * 4 + 1024;
+    static constexpr uint32_t kColA = 256;                           // tensor memory: A's terms, 128 columns a stage
 };
 
 struct PartBarriers {
@@ -131,57 +131,85 @@ struct PartBarriers {
     uint32_t tmem_base;
 };
 
-// x's three bf16 terms: hi, what hi leaves, what both leave (packed pairs).
-__device__ __forceinline__ void split3(float x, float y, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
-    hi = pack_bf16x2(x, y);
-    x -= bf16lo(hi);
-    y -= bf16hi(hi);
-    mid = pack_bf16x2(x, y);
-    lo = pack_bf16x2(x - bf16lo(mid), y - bf16hi(mid));
+// Three bf16 terms of each of two floats, by truncation: their leading 8 bits, the
+// next 8 and the last 8. The differences are exact, so the terms add up to the
+// floats (cutting takes fewer instructions than rounding, and the sum is what counts).
+__device__ __forceinline__ void split3(f32x2 p, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+    const f32x2 minus = pack2(-1.f, -1.f);
+    auto cut = [&]() -> uint32_t {               // p's leading terms, which leave p
+        float x, y;
+        unpack2(p, x, y);
+        const uint32_t u = __float_as_uint(x), v = __float_as_uint(y);
+        p = fma2(pack2(__uint_as_float(u & 0xffff0000u), __uint_as_float(v & 0xffff0000u)), minus, p);
+        return __byte_perm(u, v, 0x7632);
+    };
+    hi = cut();
+    mid = cut();
+    lo = cut();
 }
 
-// The units of a CTA, chunks of a KV head: numbers blockIdx.x, + gridDim.x, ...; a
-// backward's q do^T (g heads of work each) come first, then the k v^T.
+// Work laid end to end, cut into one length a CTA: `per` each, one more for the first `more`.
+struct Cut {
+    int per, more;
+    __device__ __forceinline__ int begin(unsigned cta) const { return per * (int)cta + min((int)cta, more); }
+};
+
+// The units of a CTA, chunks of a KV head: a backward's q do^T (g heads of work
+// each), then the k v^T (one each). A CTA has the units that begin in its length of
+// all units' work.
 struct PartWalk {
     const LinArgs& a;
-    int n, per_kind, i, it = -1;
-    bool both, grad = false;
+    int n, g, i, end, other, other_end, it = -1;
+    bool grad;
     int f = 0, h = 0;
     LinChunk c{};
-    __device__ __forceinline__ PartWalk(const LinArgs& args, bool both_)
-        : a(args), per_kind(args.n_chunks * args.Hkv), i((int)blockIdx.x - (int)gridDim.x), both(both_) {
-        n = both ? 2 * per_kind : per_kind;
+    LinCuts cuts;
+    __device__ __forceinline__ PartWalk(const LinArgs& args, bool both, Cut cut)
+        : a(args), n(args.n_chunks * args.Hkv), g(args.Hq / args.Hkv), grad(both), cuts(args) {
+        const int from = cut.begin(blockIdx.x), to = cut.begin(blockIdx.x + 1), before = both ? n * g : 0;   // work of all q do^T
+        other = max(0, from - before);
+        other_end = max(0, to - before);
+        i = both ? min(n, (from + g - 1) / g) - 1 : other - 1;
+        end = both ? min(n, (to + g - 1) / g) : other_end;
     }
     __device__ __forceinline__ bool next() {
-        while ((i += gridDim.x) < n) {
-            const int u = i < per_kind ? i : i - per_kind;
-            grad = both && i < per_kind;
-            f = u / a.Hkv;
-            h = u - f * a.Hkv;
-            if (!lin_chunk<kL>(a, f, c)) continue;
+        for (;;) {
+            if (++i >= end) {
+                if (!grad) return false;
+                grad = false;
+                i = other - 1;
+                end = other_end;
+                continue;
+            }
+            f = i / a.Hkv;
+            h = i - f * a.Hkv;
+            if (!lin_chunk<kL>(a, cuts, f, c)) continue;
             ++it;
             return true;
         }
-        return false;
     }
     __device__ __forceinline__ int heads() const { return grad ? a.Hq / a.Hkv : 1; }
     __device__ __forceinline__ int stages() const { return (c.rows + kPartRows - 1) / kPartRows; }
 };
 
 // part[f][h] = sum_t w_t a_t r_t^T: k v^T with w = l^(m-1-t), and for a backward
-// (both) also scale q do^T over the group's heads with w = l^(t+1). Warp 0 loads 64 rows of both
-// operands at a time (TMA, four stages), eight warps weight A and split it into
-// three terms, warp 1 issues the products (both operands MN-major: the rows are
-// the inner dimension), four warps write the sums of one unit out while the next
-// unit's are formed (two accumulators). The large term has an accumulator of its
-// own: each addition to it rounds in fp32, and the small terms' additions would
-// triple their number. D = 64 packs two terms into the 128 rows of an instruction:
-// rows 0 .. 63 hold hi's sum and, 64 columns on, lo's; rows 64 .. 127 mid's.
+// (both) also scale q do^T over the group's heads with w = l^(t+1). Warp 0 loads
+// 64 rows of both operands at a time (TMA). Eight warps weight A, split it into three
+// terms and put them into tensor memory, transposed: a thread has one column of A
+// (a lane) and 32 rows. Warp 1 issues the products, R (MN-major) from shared memory;
+// four warps write sums out. With A's terms in shared memory too, the products'
+// and the weighting's traffic there was the bound: 0.85 us a stage instead of 0.45.
+// The sums of q do^T have an accumulator for the large term and one for the small
+// ones: each addition rounds in fp32, and the small terms' would triple their number;
+// those of k v^T, of 128 rows alone, have one, and two units alternate between both.
+// D = 64 packs two terms into the 128 lanes of an instruction: lanes 0 .. 63 hold hi's
+// sum and, 64 columns on, lo's; lanes 64 .. 127 mid's.
 template <int D>
-__global__ void __launch_bounds__(kPartThreads, 1)
+__global__ void __maxnreg__(88)
 lin_part_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
-                   const __grid_constant__ CUtensorMap map_kv_out, const __grid_constant__ CUtensorMap map_qdo_out, const LinArgs a, bool both) {
+                   const __grid_constant__ CUtensorMap map_kv_out, const __grid_constant__ CUtensorMap map_qdo_out, const LinArgs a, bool both,
+                   Cut cut) {
     using L = PartLayout<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -213,7 +241,7 @@ lin_part_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             tc::prefetch_tmap(&map_do);
         }
     }
-    PartWalk w(a, both);
+    PartWalk w(a, both, cut);
     bool more = w.next();                        // (its loads overlap the set-up)
     tc::tc_fence_before();
     __syncthreads();
@@ -254,41 +282,45 @@ lin_part_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     } else if (warp == 1) {
         // ------------------------------------------------------------ products
         const bool leader = tc::elect_one_sync();
-        const uint32_t idesc = tc::idesc_bf16(128, D, true, true);
+        const uint32_t idesc = tc::idesc_bf16(128, D, false, true);
         const uint32_t sm = tc::smem_u32(smem);
         bool ok = true;
+        int acc = 0;                             // accumulators used so far: number n is columns 128 (n & 1) ..
         for (; ok && more; more = w.next()) {
-            const int total = w.heads() * w.stages();
-            const uint32_t t = tmem + (w.it & 1) * 256;
-            if (w.it >= 2 && !tc::warp_wait(&B.acc_empty[w.it & 1], ((w.it >> 1) - 1) & 1, a.wait_err)) break;
+            const int total = w.heads() * w.stages(), na = D == 128 && w.grad ? 2 : 1;
+            for (int n = acc; ok && n < acc + na; ++n)
+                ok = n < 2 || tc::warp_wait(&B.acc_empty[n & 1], ((n >> 1) - 1) & 1, a.wait_err);
+            if (!ok) break;
+            const uint32_t t = tmem + (acc & 1) * 128, t_small = tmem + ((acc + na - 1) & 1) * 128;
             for (int i = 0; i < total; ++i, ++st) {
                 const int s = st % kPartRaw, p = st % kPartSplit;
                 if (!tc::warp_wait(&B.split_full[p], (st / kPartSplit) & 1, a.wait_err)) { ok = false; break; }
                 tc::tc_fence_after();
                 if (leader) {
                     const uint64_t r0 = tc::sdesc(sm + s * L::kRaw + L::kOp, L::kBlock, 1024);
-                    const uint64_t a0 = tc::sdesc(sm + L::kOffSplit + p * L::kSplit, L::kBlock, 1024);
+                    const uint32_t ta = tmem + L::kColA + p * 128;
                     if constexpr (D == 128) {
 #pragma unroll
                         for (int x = 0; x < 3; ++x)
 #pragma unroll
                             for (int k = 0; k < kPartRows / 16; ++k)
-                                tc::mma_bf16(t + (x ? 128 : 0), tc::sdesc_at(a0, x * L::kOp + k * 2048), tc::sdesc_at(r0, k * 2048),
-                                             idesc, (i | k | (x == 2)) ? 1u : 0u);
+                                tc::mma_bf16_ts(x ? t_small : t, ta + 32 * x + 8 * k, tc::sdesc_at(r0, k * 2048), idesc,
+                                                (i | k | (x == 1 ? na == 1 : x)) ? 1u : 0u);
                     } else {
 #pragma unroll
-                        for (int x = 0; x < 2; ++x)              // blocks hi, mid; then lo, zeros
+                        for (int x = 0; x < 2; ++x)              // hi and mid, then lo
 #pragma unroll
                             for (int k = 0; k < kPartRows / 16; ++k)
-                                tc::mma_bf16(t + 64 * x, tc::sdesc_at(a0, 2 * x * L::kOp + k * 2048), tc::sdesc_at(r0, k * 2048), idesc,
-                                             (i | k) ? 1u : 0u);
+                                tc::mma_bf16_ts(t + 64 * x, ta + 32 * x + 8 * k, tc::sdesc_at(r0, k * 2048), idesc, (i | k) ? 1u : 0u);
                     }
                     tc::mma_commit(&B.raw_empty[s]);
                     tc::mma_commit(&B.split_empty[p]);
-                    if (i + 1 == total) tc::mma_commit(&B.acc_full[w.it & 1]);
+                    if (i + 1 == total)
+                        for (int n = acc; n < acc + na; ++n) tc::mma_commit(&B.acc_full[n & 1]);
                 }
                 __syncwarp();
             }
+            acc += na;
         }
         if (leader) {                            // nothing of ours may still run on the tensor core at exit
             tc::mma_commit(&B.drain);
@@ -297,86 +329,106 @@ lin_part_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         __syncwarp();
     } else if (warp < 2 + kPartWarps) {
         // ------------------------------------------------------------ weights and terms
-        constexpr int VPR = D / 8, RPP = kPartWarps * 32 / VPR, NV = kPartRows / RPP;    // rows a pass, vectors a thread
-        const int tid = threadIdx.x - 64, t0 = tid / VPR;
-        const uint32_t at0 = tid % VPR / 8 * L::kBlock + tc::sw128_offset(t0, tid % 8);  // RPP is a multiple of 8: + v RPP 128
-        static_assert(RPP % 8 == 0, "a thread's rows share their swizzle");
-        if constexpr (D == 64) {                 // the fourth block: zeros, once
-            for (int p = 0; p < kPartSplit; ++p)
-                for (int i = tid; i < (int)L::kOp / 16; i += kPartWarps * 32)
-                    *reinterpret_cast<uint4*>(smem + L::kOffSplit + p * L::kSplit + 3 * L::kOp + i * 16) = make_uint4(0, 0, 0, 0);
-        }
+        const int tid = threadIdx.x - 64, quad = warp & 3, half = (warp - 2) >> 2;       // rows 32 half .. of a stage
+        const int col = (quad * 32 + lane) % D;                                          // A's column; D 64: twice
+        const uint32_t base = col / 64 * L::kBlock + half * 4096 + col % 8 * 2;
+        const uint32_t chunk = col % 64 / 8;
+        const uint32_t ta = tmem + ((uint32_t)(quad * 32) << 16) + L::kColA + 16 * half;
+        __shared__ __align__(16) float wt[kL];
         bool ok = true;
-        for (; ok && more; more = w.next()) {
-            const int ns = w.stages(), nh = w.heads(), m = w.c.rows;
-            const float g2 = lin_g2(a, w.h);
-            // This thread's weights: of rows t0 + v RPP of both stages of a chunk.
-            float wt[kL / kPartRows][NV];
-#pragma unroll
-            for (int q = 0; q < kL / kPartRows; ++q)
-#pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                    const int t = q * kPartRows + v * RPP + t0;
-                    wt[q][v] = t >= m ? 0.f : w.grad ? rsqrtf((float)D) * lin_pow(g2, t + 1) : lin_pow(g2, m - 1 - t);
-                }
-            for (int e = 0; ok && e < nh; ++e)
-#pragma unroll
-                for (int q = 0; q < kL / kPartRows; ++q) {
-                    if (q >= ns) break;
-                    const int s = st % kPartRaw, p = st % kPartSplit;
-                    if (st >= kPartSplit && ok)
-                        ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.split_empty[p], (st / kPartSplit - 1) & 1, a.wait_err));
-                    if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.raw_full[s], (st / kPartRaw) & 1, a.wait_err));
-                    if (!ok) break;
-                    uint8_t *raw = smem + s * L::kRaw + at0, *out = smem + L::kOffSplit + p * L::kSplit + at0;
-                    const int left = m - q * kPartRows;
-#pragma unroll
-                    for (int v = 0; v < NV; ++v) {
-                        uint4 u = *reinterpret_cast<const uint4*>(raw + v * RPP * 128);
-                        if (v * RPP + t0 >= left) {              // behind the sequence: anything, and 0 * NaN is NaN
-                            u = make_uint4(0, 0, 0, 0);
-                            *reinterpret_cast<uint4*>(raw + L::kOp + v * RPP * 128) = u;
-                        }
-                        float x[8];
-                        widen16<__nv_bfloat16>(u, x);
-                        const float k = wt[q][v];
-                        uint4 hi, mid, lo;
-                        split3(x[0] * k, x[1] * k, hi.x, mid.x, lo.x);
-                        split3(x[2] * k, x[3] * k, hi.y, mid.y, lo.y);
-                        split3(x[4] * k, x[5] * k, hi.z, mid.z, lo.z);
-                        split3(x[6] * k, x[7] * k, hi.w, mid.w, lo.w);
-                        *reinterpret_cast<uint4*>(out + v * RPP * 128) = hi;
-                        *reinterpret_cast<uint4*>(out + L::kOp + v * RPP * 128) = mid;
-                        *reinterpret_cast<uint4*>(out + 2 * L::kOp + v * RPP * 128) = lo;
+        for (; more; more = w.next()) {
+            // (After a failed wait the walk goes on, only to keep meeting the other warps here.)
+            asm volatile("bar.sync 2, 256;" ::: "memory");                               // nobody reads the last weights any more
+            const int ns = w.stages(), total = w.heads() * ns, m = w.c.rows;
+            if (tid < kL) {
+                const float g2 = lin_g2(a, w.h);
+                wt[tid] = tid >= m ? 0.f : w.grad ? rsqrtf((float)D) * lin_pow(g2, tid + 1) : lin_pow(g2, m - 1 - tid);
+            }
+            asm volatile("bar.sync 2, 256;" ::: "memory");
+            int q = 0;                           // stage of the chunk
+            for (int i = 0; ok && i < total; ++i, ++st, q = q + 1 == ns ? 0 : q + 1) {
+                const int s = st % kPartRaw, p = st % kPartSplit;
+                ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.raw_full[s], (st / kPartRaw) & 1, a.wait_err));
+                if (!ok) break;
+                const uint8_t* raw = smem + s * L::kRaw + base;
+                const int left = m - q * kPartRows;
+                if (left < kPartRows) {          // behind the sequence: anything, and 0 * NaN is NaN
+                    uint8_t* r = smem + s * L::kRaw + L::kOp + left * 128;
+                    for (int y = tid; y < (kPartRows - left) * 8 * (D / 64); y += kPartWarps * 32) {
+                        const int bl = y / ((kPartRows - left) * 8), at = y % ((kPartRows - left) * 8);
+                        *reinterpret_cast<uint4*>(r + bl * L::kBlock + at * 16) = make_uint4(0, 0, 0, 0);
                     }
                     tc::fence_proxy_async_smem();
-                    tc::mbar_arrive(&B.split_full[p]);
-                    ++st;
                 }
+                const ulonglong2* wq = reinterpret_cast<const ulonglong2*>(wt + q * kPartRows + 32 * half);
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {    // 16 rows at a time: the kernel's registers leave room for two CTAs of the scan
+                    uint32_t x[16], hi[8], mid[8], lo[8];
+#pragma unroll
+                    for (int t = 0; t < 16; ++t) {
+                        x[t] = (uint32_t)*reinterpret_cast<const uint16_t*>(raw + (16 * z + t) * 128 + ((chunk ^ (t & 7)) << 4)) << 16;
+                        if (left < kPartRows && 32 * half + 16 * z + t >= left) x[t] = 0u;
+                    }
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const ulonglong2 k = wq[4 * z + t];
+                        split3(mul2(pack2(__uint_as_float(x[4 * t]), __uint_as_float(x[4 * t + 1])), k.x), hi[2 * t], mid[2 * t], lo[2 * t]);
+                        split3(mul2(pack2(__uint_as_float(x[4 * t + 2]), __uint_as_float(x[4 * t + 3])), k.y), hi[2 * t + 1], mid[2 * t + 1],
+                               lo[2 * t + 1]);
+                    }
+                    // (only now does the place have to be free: products ran meanwhile)
+                    if (z == 0 && st >= kPartSplit) {
+                        ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.split_empty[p], (st / kPartSplit - 1) & 1, a.wait_err));
+                        if (!ok) break;
+                        tc::tc_fence_after();
+                    }
+                    const uint32_t at = ta + p * 128 + 8 * z;
+                    if constexpr (D == 128) {
+                        tc::tmem_st8(at, hi);
+                        tc::tmem_st8(at + 32, mid);
+                        tc::tmem_st8(at + 64, lo);
+                    } else if (quad < 2) {
+                        tc::tmem_st8(at, hi);
+                        tc::tmem_st8(at + 32, lo);
+                    } else {
+                        tc::tmem_st8(at, mid);
+                    }
+                }
+                if (!ok) break;
+                tc::tmem_wait_st();
+                tc::tc_fence_before();
+                tc::mbar_arrive(&B.split_full[p]);
+            }
         }
     } else {
         // ------------------------------------------------------------ sums out
         const int quad = warp & 3, row = quad * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
         __shared__ float cross[64][33];          // D 64: mid's sums, 32 columns at a time
-        uint8_t* stage = smem + L::kOffStage + (warp - 2 - kPartWarps) * 8192;
+        uint8_t* stage = smem + L::kOffStage + quad * (D / 32 * 4096);
         bool ok = true;
-        int box = 0;
+        int acc = 0;
         for (; more; more = w.next()) {
-            const int b = w.it & 1;
-            if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.acc_full[b], (w.it >> 1) & 1, a.wait_err));
+            const int na = D == 128 && w.grad ? 2 : 1;
+            for (int n = acc; n < acc + na; ++n)
+                if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.acc_full[n & 1], (n >> 1) & 1, a.wait_err));
             if (!ok && D == 128) break;
             tc::tc_fence_after();
+            const uint32_t t = lanes + (acc & 1) * 128, t_small = lanes + ((acc + 1) & 1) * 128;
 #pragma unroll
             for (int c = 0; c < D; c += 32) {
                 uint32_t r[32], q[32];
-                tc::tmem_ld32(lanes + b * 256 + c, r);
-                tc::tmem_ld32(lanes + b * 256 + D + c, q);
+                tc::tmem_ld32(t + c, r);
+                if (D == 64) tc::tmem_ld32(t + D + c, q);
+                else if (na == 2) tc::tmem_ld32(t_small + c, q);
+                else
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) q[e] = 0u;
                 tc::tmem_wait_ld(r);
                 tc::tmem_wait_ld(q);
                 if (c + 32 == D) {               // all of it is in registers
                     tc::tc_fence_before();
-                    tc::mbar_arrive(&B.acc_empty[b]);
+                    for (int n = acc; n < acc + na; ++n) tc::mbar_arrive(&B.acc_empty[n & 1]);
                 }
                 if constexpr (D == 64) {
                     // (after a failed wait this goes on, only to keep meeting the other warps)
@@ -390,9 +442,11 @@ lin_part_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         for (int e = 0; e < 32; ++e) q[e] = __float_as_uint(__uint_as_float(q[e]) + cross[row][e]);
                 }
                 if (ok && quad * 32 < D) {
-                    uint8_t* at = stage + (box++ & 1) * 4096;
-                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");    // the box before the last has left
-                    __syncwarp();
+                    uint8_t* at = stage + c / 32 * 4096;
+                    if (c == 0) {
+                        if (lane == 0) tc::bulk_wait_read();                     // the last unit's boxes have left
+                        __syncwarp();
+                    }
 #pragma unroll
                     for (int v = 0; v < 8; ++v) {
                         float4 x;
@@ -410,6 +464,7 @@ lin_part_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     }
                 }
             }
+            acc += na;
         }
         if (lane == 0) bulk_wait();
     }
@@ -423,43 +478,44 @@ lin_part_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 
 // ------------------------------------------------------------------ scan
 
-constexpr int kScanThreads = 128, kScanAhead = 32;
+constexpr int kScanThreads = 128, kScanAhead = 16;
 
 // From a sequence's chunk sums to the states before its chunks (y 0, in order) or
 // the gradients of the states after them (y 1, in reverse), in fp32; the kernels
-// that multiply by them get them in bf16. A thread owns two elements all along
+// that multiply by them get them in bf16. A thread owns four elements all along
 // (so slot_in may be slot_out) and has kScanAhead chunks' sums on their way at once:
-// what bounds the scan is the latency of these rounds (four elements and eight
-// chunks took 10 us for 32 chunks of 4 heads).
+// what bounds the scan is the latency of these rounds and of what comes before them,
+// which overlaps the kernel before where an SM has room beside it.
 template <int D>
-__global__ void __launch_bounds__(kScanThreads) lin_scan_bf16_kernel(const LinArgs a) {
-    constexpr int V = D * D / 2;
+__global__ void __launch_bounds__(kScanThreads, 5) lin_scan_bf16_kernel(const LinArgs a) {
+    constexpr int V = D * D / 4;
     const bool grad = blockIdx.y;
     const int64_t unit = (int64_t)blockIdx.x * kScanThreads + threadIdx.x;
     const int e = (int)(unit % V);
     const int64_t bh = unit / V, b = bh / a.Hkv;
     const int h = (int)(bh - b * a.Hkv);
     launch_dependents();
-    int64_t lo, hi;
-    const bool good = lin_range(a, b, lo, hi);
-    const float g2 = lin_g2(a, h);
-    const int64_t first = lin_slot(a, grad ? a.slot_out : a.slot_in, b);
     // (a backward scans k v^T for the states alone: the forward has stored the last one)
-    const int64_t last = !grad && gridDim.y > 1 ? -1 : lin_slot(a, grad ? a.slot_in : a.slot_out, b);
-    float2* store = reinterpret_cast<float2*>(grad ? a.dstate : a.state);
-    float2 s = make_float2(0.f, 0.f);
+    const int32_t *from = grad ? a.slot_out : a.slot_in, *to = grad ? a.slot_in : gridDim.y > 1 ? nullptr : a.slot_out;
+    const int64_t lo = a.cu ? a.cu[b] : 0, hi = a.cu ? a.cu[b + 1] : a.n;        // all loads before the first check
+    const int32_t first_ = from ? from[b] : -1, last_ = to ? to[b] : -1;
+    const float g2 = lin_g2(a, h);
+    const bool good = lin_good(a, lo, hi);
+    const int64_t first = lin_good_slot(a, first_), last = lin_good_slot(a, last_);
+    float4* store = reinterpret_cast<float4*>(grad ? a.dstate : a.state);
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (good && first >= 0) s = store[((size_t)first * a.Hkv + h) * V + e];      // (older than the kernel before)
     wait_for_kernels();
     if (!good) return;
     const int64_t nc = (hi - lo + kL - 1) / kL;
     const float lfull = lin_pow(g2, kL), ltail = lin_pow(g2, (int)(hi - lo - (nc - 1) * kL));    // the last chunk's rows
     const int64_t at = ((lo / kL + b + (grad ? nc - 1 : 0)) * a.Hkv + h) * V + e, step = (int64_t)a.Hkv * V * (grad ? -1 : 1);
-    const float2* in = reinterpret_cast<const float2*>(grad ? a.gpart : a.part) + at;
-    uint32_t* out = reinterpret_cast<uint32_t*>(grad ? a.gbf : a.sbf) + at;
+    const float4* in = reinterpret_cast<const float4*>(grad ? a.gpart : a.part) + at;
+    uint2* out = reinterpret_cast<uint2*>(grad ? a.gbf : a.sbf) + at;
     for (int64_t i = 0; i < nc; i += kScanAhead) {
         const int m = (int)min64(kScanAhead, nc - i);
-        float2 x[kScanAhead];
-        const float2* p = in;
+        float4 x[kScanAhead];
+        const float4* p = in;
 #pragma unroll
         for (int u = 0; u < kScanAhead; ++u) {
             if (u < m) x[u] = __ldcs(p);
@@ -468,11 +524,13 @@ __global__ void __launch_bounds__(kScanThreads) lin_scan_bf16_kernel(const LinAr
 #pragma unroll
         for (int u = 0; u < kScanAhead; ++u)
             if (u < m) {
-                *out = pack_bf16x2(s.x, s.y);
+                *out = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
                 out += step;
                 const float l = i + u == (grad ? 0 : nc - 1) ? ltail : lfull;
                 s.x = fmaf(l, s.x, x[u].x);
                 s.y = fmaf(l, s.y, x[u].y);
+                s.z = fmaf(l, s.z, x[u].z);
+                s.w = fmaf(l, s.w, x[u].w);
             }
         in = p;
     }
@@ -510,8 +568,10 @@ struct HeadWalk {
     int g, it = -1, pair = -1, f = 0, h = 0, head = 0;
     bool first = false, live = false;
     LinChunk c{};
+    LinCuts cuts;
 
-    __device__ __forceinline__ HeadWalk(const LinArgs& args, int from, int to) : a(args), idx(from - 1), end(to), g(args.Hq / args.Hkv) {}
+    __device__ __forceinline__ HeadWalk(const LinArgs& args, int from, int to)
+        : a(args), idx(from - 1), end(to), g(args.Hq / args.Hkv), cuts(args) {}
     // The next head: it counts heads, pair (chunk, KV head)s; first: the first head of its pair here.
     __device__ __forceinline__ bool next() {
         while (++idx < end) {
@@ -519,7 +579,7 @@ struct HeadWalk {
                 unit = idx / g;
                 f = unit / a.Hkv;
                 h = unit - f * a.Hkv;
-                live = lin_chunk<kL>(a, f, c);
+                live = lin_chunk<kL>(a, cuts, f, c);
                 pair += live;
                 first = true;
             } else {
@@ -551,13 +611,12 @@ template <int D, bool GRAD>
 __global__ void __launch_bounds__(kRowsThreads, 1)
 lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_c,
                    const __grid_constant__ CUtensorMap map_r, const __grid_constant__ CUtensorMap map_s,
-                   const __grid_constant__ CUtensorMap map_out, const LinArgs a, int heads) {
+                   const __grid_constant__ CUtensorMap map_out, const LinArgs a, Cut cut) {
     using L = RowsLayout<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ __align__(8) RowsBarriers B;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int from = (int)((int64_t)heads * blockIdx.x / gridDim.x), to = (int)((int64_t)heads * (blockIdx.x + 1) / gridDim.x);
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
             tc::mbar_init(&B.r_ready[s], 256);
@@ -586,7 +645,7 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         tc::prefetch_tmap(&map_r);
         tc::prefetch_tmap(&map_s);
     }
-    HeadWalk w(a, from, to);
+    HeadWalk w(a, cut.begin(blockIdx.x), cut.begin(blockIdx.x + 1));
     bool more = w.next();                        // (its loads overlap the set-up)
     tc::tc_fence_before();
     __syncthreads();
@@ -1101,15 +1160,20 @@ bool states_map(CUtensorMap* m, const void* p, const LinArgs& a, std::string* wh
 
 // Launches a kernel that may start before the stream's last kernel, one of this
 // file's, has ended; it waits for that one itself (wait_for_kernels) before it
-// touches what that one writes.
+// touches what that one writes. Each asks for the largest split of an SM's memory in
+// favour of shared memory, as the tensor-core kernels need it: the scan, which needs
+// none, otherwise had the split changed before and after it (4 us until the next
+// kernel started).
 template <typename... P, typename... A>
 cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
     cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[2]{};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributePreferredSharedMemoryCarveout;
+    attr[1].val.sharedMemCarveout = cudaSharedmemCarveoutMaxShared;
     cfg.gridDim = grid; cfg.blockDim = dim3(threads); cfg.dynamicSmemBytes = smem; cfg.stream = s;
-    cfg.attrs = &attr; cfg.numAttrs = 1;
+    cfg.attrs = attr; cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -1127,12 +1191,13 @@ template <int D> cudaError_t states(const LinArgs& a, bool both, cudaStream_t s,
         if (both && (!rows_map(&q, a.q, a.Hq, a, kPartRows, why) || !rows_map(&go, a.dout, a.Hq, a, kPartRows, why) ||
                      !sums_map(&gout, a.gpart, a, why)))
             return cudaErrorInvalidValue;
-        const int grid = std::min(a.n_chunks * a.Hkv * nz, sm_count());
+        const int work = a.n_chunks * (a.Hkv + (both ? a.Hq : 0)), grid = std::min(a.n_chunks * a.Hkv * nz, sm_count());
         ProfScope ps("lin_part_tc_kernel", s);
-        lin_part_tc_kernel<D><<<grid, kPartThreads, PartLayout<D>::kSmem, s>>>(q, k, v, go, out, gout, a, both);
+        lin_part_tc_kernel<D><<<grid, kPartThreads, PartLayout<D>::kSmem, s>>>(q, k, v, go, out, gout, a, both,
+                                                                                     Cut{work / grid, work % grid});
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    const dim3 grid((unsigned)(a.n_seq * a.Hkv * (D * D / 2 / kScanThreads)), nz);
+    const dim3 grid((unsigned)(a.n_seq * a.Hkv * (D * D / 4 / kScanThreads)), nz);
     ProfScope ps("lin_scan_bf16_kernel", s);
     if (a.n) return launch_after(lin_scan_bf16_kernel<D>, grid, kScanThreads, 0, s, a);
     lin_scan_bf16_kernel<D><<<grid, kScanThreads, 0, s>>>(a);          // no sums before it
@@ -1148,10 +1213,10 @@ template <int D, bool GRAD> cudaError_t rows(const LinArgs& a, cudaStream_t s, s
         !rows_map(&r, GRAD ? a.k : a.v, a.Hkv, a, kL, why) || !states_map(&st, a.sbf, a, why) ||
         !half_map(&out, GRAD ? a.dq : a.o, a.Hq, a, why))
         return cudaErrorInvalidValue;
-    const int heads = a.n_chunks * a.Hq;
+    const int heads = a.n_chunks * a.Hq, grid = std::min(heads, sm_count());
     ProfScope ps("lin_rows_tc_kernel", s);
-    return launch_after(lin_rows_tc_kernel<D, GRAD>, dim3(std::min(heads, sm_count())), kRowsThreads, RowsLayout<D>::kSmem, s, x, c, r, st,
-                        out, a, heads);
+    return launch_after(lin_rows_tc_kernel<D, GRAD>, dim3(grid), kRowsThreads, RowsLayout<D>::kSmem, s, x, c, r, st,
+                        out, a, Cut{heads / grid, heads % grid});
 }
 
 template <int D> cudaError_t cols(const LinArgs& a, cudaStream_t s, std::string* why) {

@@ -6,45 +6,112 @@
 // cancellation for rows whose mean is far from zero.
 //
 // One pass over HBM each way: a team of threads holds a group's columns in
-// registers, kEPV at a time (16-byte vectors, or single elements where rows are
-// not whole vectors). A team is 1 to 32 lanes (sums by shuffles) or, for more
-// than 1024 columns, a CTA. In the backward a team keeps to one group of columns
-// and walks rows, so its share of dw and db stays in registers; the shares
-// are added by a second kernel in a fixed order.
+// registers, as loaded: 16-byte vectors, or single elements where rows are not
+// whole vectors. A team is 1 to 32 lanes with a vector each (sums by shuffles) or
+// whole warps with several vectors a thread: the sums between warps cost every
+// thread two barriers and a read per warp, so few warps a row and many rows at once
+// are better than many warps. In the backward a team keeps to one group of columns,
+// so that its share of dw and db stays in registers, and walks rows; a CTA's teams
+// add their shares in shared memory, a second kernel adds the CTAs', both in a fixed
+// order.
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
+#include "mod.cuh"
 
 namespace pkv {
 namespace {
 
 constexpr int kThreads = 256;                    // of a CTA of lane teams
+constexpr int kMaxTeam = 512;                    // threads of a CTA of teams of warps, but for the widest rows
+// Rows that a team of the backward has on the way: 128 KB of x and dy at most, and none of single
+// elements or the widest rows.
+template <int EPV, int NV> constexpr int kAhead = EPV == 1 || NV * EPV == 32 ? 0 : 8 / NV;
+constexpr int kBatch = 4;
 constexpr int64_t kMaxWidth = 32768, kMaxGrid = (int64_t(1) << 31) - 1;
 
 struct NormArgs {
     const void *x, *dy, *w, *b;
-    void *y, *dx;                                // y: forward
+    void *y, *dx;
     int64_t xs, dys, ys, dxs;                    // elements between rows
     float *mean, *rstd, *dw, *db, *part;         // part: [slots][2][groups * width]
     int64_t n;
     int groups, width;
-    int team;                                    // lanes of a team, or kThreads' whole CTA: blockDim.x
-    int slots;                                   // backward: teams that share a group's rows
-    float eps;
+    int team;                                    // threads of a team
+    int slots;                                   // lane teams, or CTAs, that share a group's rows
+    float eps, inv_width;
     bool w_f32, accumulate;
 };
 
-template <typename T, int EPV> __device__ __forceinline__ void load(const T* p, float* f) {
+// Elements are worked on in pairs where a vector holds some (f32x2: one instruction
+// for two), single ones by the same code.
+template <int EPV> using Pk = std::conditional_t<EPV == 1, float, f32x2>;
+template <int EPV> constexpr int kPk = EPV == 1 ? 1 : EPV / 2;
+using pkv::fma2;                                 // (not hidden by the single ones)
+using pkv::mul2;
+using pkv::add2;
+__device__ __forceinline__ float fma2(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float mul2(float a, float b) { return a * b; }
+__device__ __forceinline__ float add2(float a, float b) { return a + b; }
+template <typename P> __device__ __forceinline__ P both(float x) {
+    if constexpr (std::is_same_v<P, float>) return x;
+    else return pack2(x, x);
+}
+__device__ __forceinline__ float total(float x) { return x; }
+__device__ __forceinline__ float total(f32x2 x) {
+    float a, b;
+    unpack2(x, a, b);
+    return a + b;
+}
+template <int EPV> __device__ __forceinline__ void pairs(const float (&f)[EPV], Pk<EPV> (&p)[kPk<EPV>]) {
     if constexpr (EPV == 1) {
-        f[0] = Elem<T>::load(p);
+        p[0] = f[0];
     } else {
-        widen16<T>(*reinterpret_cast<const uint4*>(p), f);
+#pragma unroll
+        for (int e = 0; e < EPV / 2; ++e) p[e] = pack2(f[2 * e], f[2 * e + 1]);
     }
 }
-template <typename T, int EPV> __device__ __forceinline__ void store(T* p, const float* f) {
+template <int EPV> __device__ __forceinline__ void singles(const Pk<EPV> (&p)[kPk<EPV>], float (&f)[EPV]) {
+    if constexpr (EPV == 1) {
+        f[0] = p[0];
+    } else {
+#pragma unroll
+        for (int e = 0; e < EPV / 2; ++e) unpack2(p[e], f[2 * e], f[2 * e + 1]);
+    }
+}
+
+// EPV consecutive elements as they are in memory.
+template <typename T, int EPV> struct Raw {
+    uint4 u;
+    __device__ __forceinline__ void load(const T* p) { u = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void widen(f32x2 (&p)[EPV / 2]) const {
+        float f[EPV];
+        widen16<T>(u, f);
+        pairs<EPV>(f, p);
+    }
+};
+// 16 bytes global -> shared memory, asynchronously; groups of copies are waited for in order.
+__device__ __forceinline__ void copy16(uint4* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                 :: "r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
+
+template <typename T> struct Raw<T, 1> {
+    float x;
+    __device__ __forceinline__ void load(const T* p) { x = Elem<T>::load(p); }
+    __device__ __forceinline__ void zero() { x = 0.f; }
+    __device__ __forceinline__ void widen(float (&p)[1]) const { p[0] = x; }
+};
+template <typename T, int EPV> __device__ __forceinline__ void store(T* p, const Pk<EPV> (&x)[kPk<EPV>]) {
+    float f[EPV];
+    singles<EPV>(x, f);
     if constexpr (EPV == 1) {
         Elem<T>::store(p, f[0]);
     } else if constexpr (sizeof(T) == 4) {
@@ -54,180 +121,415 @@ template <typename T, int EPV> __device__ __forceinline__ void store(T* p, const
                                                   pack_bf16x2(f[6], f[7]));
     }
 }
-// Weight or bias, EPV columns from c on; `none` where there is none.
-template <int EPV> __device__ __forceinline__ void load_w(const void* w, bool f32, int64_t c, float none, float* f) {
-    if (!w) {
+// Weight or bias of type W, EPV columns from c on; `none` where there is none. Read-only
+// loads: they may move ahead of the stores of outputs, which could otherwise be the
+// weights. (The type is no branch here: in one, each vector's load waited for the one
+// before, 9 us for a row of 3584 columns instead of 3.)
+template <typename W, int EPV> __device__ __forceinline__ void load_w(const void* w, int64_t c, float none, Pk<EPV> (&x)[kPk<EPV>]) {
 #pragma unroll
-        for (int e = 0; e < EPV; ++e) f[e] = none;
-    } else if (f32) {
-        const float* p = static_cast<const float*>(w) + c;
-        if constexpr (EPV == 1) {
-            f[0] = *p;
-        } else {
+    for (int e = 0; e < kPk<EPV>; ++e) x[e] = both<Pk<EPV>>(none);
+    if (!w) return;
+    float f[EPV];
+    const W* p = static_cast<const W*>(w) + c;
+    if constexpr (EPV == 1) {
+        f[0] = (float)__ldg(p);
+    } else if constexpr (sizeof(W) == 4) {
 #pragma unroll
-            for (int e = 0; e < EPV; e += 4) widen16<float>(*reinterpret_cast<const uint4*>(p + e), f + e);
-        }
+        for (int e = 0; e < EPV; e += 4) widen16<float>(__ldg(reinterpret_cast<const uint4*>(p + e)), f + e);
+    } else if constexpr (EPV == 8) {
+        widen16<__nv_bfloat16>(__ldg(reinterpret_cast<const uint4*>(p)), f);
     } else {
-        const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(w) + c;
-        if constexpr (EPV == 1) {
-            f[0] = __bfloat162float(*p);
-        } else if constexpr (EPV == 8) {
-            widen16<__nv_bfloat16>(*reinterpret_cast<const uint4*>(p), f);
-        } else {
-            const uint2 u = *reinterpret_cast<const uint2*>(p);
-            f[0] = bf16lo(u.x); f[1] = bf16hi(u.x); f[2] = bf16lo(u.y); f[3] = bf16hi(u.y);
-        }
+        const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+        f[0] = bf16lo(u.x); f[1] = bf16hi(u.x); f[2] = bf16lo(u.y); f[3] = bf16hi(u.y);
     }
+    pairs<EPV>(f, x);
 }
 
-// Sum of x over the team (CTA: the whole CTA, which all its threads call).
-template <bool CTA> __device__ __forceinline__ float2 team_sum(float2 x, int team, float2* red) {
-    const int lanes = CTA ? 32 : team;
-    for (int d = 1; d < lanes; d *= 2) {
-        x.x += __shfl_xor_sync(0xffffffffu, x.x, d);
-        x.y += __shfl_xor_sync(0xffffffffu, x.y, d);
-    }
-    if (CTA) {
-        __syncthreads();                         // the last sum has been read
-        if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = x;
-        __syncthreads();
-        x = make_float2(0.f, 0.f);
-        for (int i = 0; i < (int)blockDim.x / 32; ++i) {
-            x.x += red[i].x;
-            x.y += red[i].y;
-        }
-    }
-    return x;
+// Sums of N values over a team of lanes.
+template <int N> __device__ __forceinline__ void lane_sum(float (&x)[N], int lanes) {
+    for (int d = 1; d < lanes; d *= 2)
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], d);
+}
+// Over a team of whole warps: `threads` of them meet at barrier `bar`, once. red: [32][N],
+// not used again before all of them have met at another barrier.
+template <int N> __device__ __forceinline__ void warps_sum(float (&x)[N], int threads, int bar, float* red) {
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2)
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], d);
+    if (threads == 32) return;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x % threads / 32;
+    if (lane == 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i) red[warp * N + i] = x[i];
+    asm volatile("bar.sync %0, %1;" :: "r"(bar), "r"(threads) : "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = lane * 32 < threads ? red[lane * N + i] : 0.f;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2)
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], d);
 }
 
-template <typename T, int EPV, int NV, bool CTA>
-__global__ void __launch_bounds__(CTA ? 1024 : kThreads) layer_norm_fwd_kernel(NormArgs a) {
-    __shared__ float2 red[32];
-    const int team = CTA ? (int)blockDim.x : a.team, t = CTA ? (int)threadIdx.x : (int)threadIdx.x % team;
-    const int64_t unit = CTA ? (int64_t)blockIdx.x : ((int64_t)blockIdx.x * kThreads + threadIdx.x) / team;
-    const bool live = unit < a.n * a.groups;
-    const int64_t row = unit / a.groups;
-    const int64_t c0 = (unit % a.groups) * a.width;
+// ---- rows of more than 32 vectors: a CTA a (row, group)
+template <typename T, int EPV, int NV>
+__global__ void __launch_bounds__(EPV == 1 && NV == 32 ? 1024 : kMaxTeam) layer_norm_fwd_kernel(NormArgs a) {
+    __shared__ float red[2 * 32];
+    const int64_t unit = blockIdx.x, row = a.groups == 1 ? unit : unit / a.groups;
+    const int64_t c0 = (unit - row * a.groups) * a.width;
+    const int t = threadIdx.x, team = blockDim.x;
     const T* x = static_cast<const T*>(a.x) + row * a.xs + c0;
-    float f[NV][EPV];
-    float2 s = make_float2(0.f, 0.f);
+    Raw<T, EPV> raw[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         const int c = (t + v * team) * EPV;
-        const bool in = live && c < a.width;
-        if (in) load<T, EPV>(x + c, f[v]);
-#pragma unroll
-        for (int e = 0; e < EPV; ++e) {
-            if (!in) f[v][e] = 0.f;
-            s.x += f[v][e];
-        }
+        raw[v].zero();
+        if (c < a.width) raw[v].load(x + c);
     }
-    const float mean = team_sum<CTA>(s, team, red).x / (float)a.width;
-    s = make_float2(0.f, 0.f);
+    using P = Pk<EPV>;
+    constexpr int N = kPk<EPV>;
+    P f[NV][N], sum = both<P>(0.f);
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
+    for (int v = 0; v < NV; ++v) {
+        raw[v].widen(f[v]);
 #pragma unroll
-        for (int e = 0; e < EPV; ++e) {
-            f[v][e] -= mean;
-            if ((t + v * team) * EPV < a.width) s.x = fmaf(f[v][e], f[v][e], s.x);
+        for (int e = 0; e < N; ++e) sum = add2(sum, f[v][e]);
+    }
+    float s[1] = {total(sum)};
+    warps_sum<1>(s, team, 0, red);
+    const float mean = s[0] * a.inv_width;
+    const P minus = both<P>(-mean);
+    s[0] = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        P q = both<P>(0.f);
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            f[v][e] = add2(f[v][e], minus);
+            q = fma2(f[v][e], f[v][e], q);
         }
-    const float rstd = 1.f / sqrtf(team_sum<CTA>(s, team, red).x / (float)a.width + a.eps);
-    if (!live) return;
+        if ((t + v * team) * EPV < a.width) s[0] += total(q);
+    }
+    warps_sum<1>(s, team, 0, red + 32);
+    const float rstd = rsqrtf(fmaf(s[0], a.inv_width, a.eps));
     if (t == 0 && a.mean) {
         a.mean[unit] = mean;
         a.rstd[unit] = rstd;
     }
     T* y = static_cast<T*>(a.y) + row * a.ys + c0;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const int c = (t + v * team) * EPV;
-        if (c < a.width) {
-            float w[EPV], b[EPV];
-            load_w<EPV>(a.w, a.w_f32, c0 + c, 1.f, w);
-            load_w<EPV>(a.b, a.w_f32, c0 + c, 0.f, b);
-#pragma unroll
-            for (int e = 0; e < EPV; ++e) f[v][e] = fmaf(f[v][e] * rstd, w[e], b[e]);
-            store<T, EPV>(y + c, f[v]);
-        }
-    }
-}
-
-// Teams numbered so that neighbours take neighbouring groups of one row.
-template <typename T, int EPV, int NV, bool CTA>
-__global__ void __launch_bounds__(CTA ? 1024 : kThreads) layer_norm_bwd_kernel(NormArgs a) {
-    __shared__ float2 red[32];
-    const int team = CTA ? (int)blockDim.x : a.team, t = CTA ? (int)threadIdx.x : (int)threadIdx.x % team;
-    const int64_t id = CTA ? (int64_t)blockIdx.x : ((int64_t)blockIdx.x * kThreads + threadIdx.x) / team;
-    const int grp = (int)(id % a.groups);
-    const int64_t slot = id / a.groups;
-    const int64_t c0 = (int64_t)grp * a.width;
-    float w[NV][EPV], dw[NV][EPV], db[NV][EPV];
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const int c = (t + v * team) * EPV;
-        if (c < a.width) load_w<EPV>(a.w, a.w_f32, c0 + c, 1.f, w[v]);
-#pragma unroll
-        for (int e = 0; e < EPV; ++e) {
-            if (c >= a.width) w[v][e] = 0.f;
-            dw[v][e] = db[v][e] = 0.f;
-        }
-    }
-    // Every team of a warp makes the same number of rounds: its lanes meet in the sums.
-    const int64_t rounds = (a.n + a.slots - 1) / a.slots;
-    for (int64_t it = 0; it < rounds; ++it) {
-        const int64_t row = it * a.slots + slot;
-        const bool live = slot < a.slots && row < a.n;
-        const T* x = static_cast<const T*>(a.x) + row * a.xs + c0;
-        const T* dy = static_cast<const T*>(a.dy) + row * a.dys + c0;
-        float f[NV][EPV], u[NV][EPV];
-        float2 s = make_float2(0.f, 0.f);
-        const float mean = live ? a.mean[row * a.groups + grp] : 0.f, rstd = live ? a.rstd[row * a.groups + grp] : 0.f;
+    const P scale = both<P>(rstd);
+    auto finish = [&](auto type) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (t + v * team) * EPV;
-            const bool in = live && c < a.width;
-            if (in) {
-                load<T, EPV>(x + c, f[v]);
-                load<T, EPV>(dy + c, u[v]);
-            }
+            if (c < a.width) {
+                P w[N], b[N];
+                load_w<decltype(type), EPV>(a.w, c0 + c, 1.f, w);
+                load_w<decltype(type), EPV>(a.b, c0 + c, 0.f, b);
 #pragma unroll
-            for (int e = 0; e < EPV; ++e) {
-                f[v][e] = in ? (f[v][e] - mean) * rstd : 0.f;
-                if (!in) u[v][e] = 0.f;
-                dw[v][e] = fmaf(u[v][e], f[v][e], dw[v][e]);
-                db[v][e] += u[v][e];
-                u[v][e] *= w[v][e];
-                s.x += u[v][e];
-                s.y = fmaf(u[v][e], f[v][e], s.y);
+                for (int e = 0; e < N; ++e) f[v][e] = fma2(mul2(f[v][e], scale), w[e], b[e]);
+                store<T, EPV>(y + c, f[v]);
+            }
+        }
+    };
+    if (a.w_f32) finish(float());
+    else finish(__nv_bfloat16());
+}
+
+// CTA blockIdx.x has rows blockIdx.x, + slots, ... of group blockIdx.y; its teams take
+// them in turn. A thread copies its vectors of the rows ahead into shared memory of its
+// own (no other thread reads them, so no barrier is needed): registers for one row
+// alone are in use, and with rows loaded to registers HBM idled during each row's sums.
+template <typename T, int EPV, int NV>
+__global__ void __launch_bounds__(NV * EPV == 32 ? 1024 : kMaxTeam) layer_norm_bwd_kernel(NormArgs a) {
+    constexpr int A = kAhead<EPV, NV>;
+    extern __shared__ uint4 ahead[];             // [A][2][NV][threads]; at the end float [2][width], the teams' shares
+    __shared__ float red[2][32 * 2];             // rows in turn
+    const int team = a.team, t = threadIdx.x % team, me = threadIdx.x / team, teams = blockDim.x / team;
+    const int grp = blockIdx.y;
+    const int64_t c0 = (int64_t)grp * a.width, step = (int64_t)teams * a.slots;
+    const T *x = static_cast<const T*>(a.x) + c0 + t * EPV, *dy = static_cast<const T*>(a.dy) + c0 + t * EPV;
+    auto fetch = [&](int64_t row, int at) {      // the copies of one row are one group, be they none
+        if constexpr (A > 0) {
+            if (row < a.n) {
+                const T *px = x + row * a.xs, *pd = dy + row * a.dys;
+                uint4* dst = ahead + at * 2 * NV * blockDim.x + threadIdx.x;
+#pragma unroll
+                for (int v = 0; v < NV; ++v)
+                    if ((t + v * team) * EPV < a.width) {
+                        copy16(dst + v * blockDim.x, px + v * team * EPV);
+                        copy16(dst + (NV + v) * blockDim.x, pd + v * team * EPV);
+                    }
+            }
+            copies_commit();
+        }
+    };
+    int64_t row = blockIdx.x + (int64_t)me * a.slots;
+#pragma unroll
+    for (int i = 0; i < A; ++i) fetch(row + i * step, i);
+    // A row's statistics are on the way while the row before is worked on.
+    float mean_next = row < a.n ? a.mean[row * a.groups + grp] : 0.f, rstd_next = row < a.n ? a.rstd[row * a.groups + grp] : 0.f;
+    using P = Pk<EPV>;
+    constexpr int N = kPk<EPV>;
+    P w[NV][N], dw[NV][N], db[NV][N];
+    auto weights = [&](auto type) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = (t + v * team) * EPV;
+            load_w<decltype(type), EPV>(c < a.width ? a.w : nullptr, c0 + c, 1.f, w[v]);
+        }
+    };
+    if (a.w_f32) weights(float());
+    else weights(__nv_bfloat16());
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int e = 0; e < N; ++e) dw[v][e] = db[v][e] = both<P>(0.f);
+    int at = 0;
+    for (int turn = 0; row < a.n; row += step, turn ^= 1) {
+        Raw<T, EPV> rx[NV], rd[NV];
+        if constexpr (A > 0) copies_wait<(A > 0 ? A - 1 : 0)>();
+        const uint4* src = ahead + at * 2 * NV * blockDim.x + threadIdx.x;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            rx[v].zero();
+            rd[v].zero();
+            if ((t + v * team) * EPV < a.width) {
+                if constexpr (A > 0) {
+                    rx[v].u = src[v * blockDim.x];
+                    rd[v].u = src[(NV + v) * blockDim.x];
+                } else {
+                    rx[v].load(x + row * a.xs + v * team * EPV);
+                    rd[v].load(dy + row * a.dys + v * team * EPV);
+                }
+            }
+        }
+        fetch(row + A * step, at);
+        at = at + 1 >= A ? 0 : at + 1;
+        const float mean = mean_next, rstd = rstd_next;
+        if (row + step < a.n) {
+            mean_next = a.mean[(row + step) * a.groups + grp];
+            rstd_next = a.rstd[(row + step) * a.groups + grp];
+        }
+        const P minus = both<P>(-mean), scale = both<P>(rstd);
+        P s0 = both<P>(0.f), s1 = s0;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {           // (behind the group's columns dy is zero)
+            P f[N], d[N];
+            rx[v].widen(f);
+            rd[v].widen(d);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const P h = mul2(add2(f[e], minus), scale), u = mul2(d[e], w[v][e]);
+                dw[v][e] = fma2(d[e], h, dw[v][e]);
+                db[v][e] = add2(db[v][e], d[e]);
+                s0 = add2(s0, u);
+                s1 = fma2(u, h, s1);
             }
         }
         if (!a.dx) continue;
-        s = team_sum<CTA>(s, team, red);
-        const float m1 = s.x / (float)a.width, m2 = s.y / (float)a.width;
-        if (!live) continue;
+        float s[2] = {total(s0), total(s1)};
+        warps_sum<2>(s, team, 1 + me, red[turn] + me * (team / 32) * 2);
+        const P m1 = both<P>(-s[0] * a.inv_width * rstd), m2 = both<P>(-s[1] * a.inv_width * rstd);
         T* dx = static_cast<T*>(a.dx) + row * a.dxs + c0;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (t + v * team) * EPV;
             if (c < a.width) {
+                P f[N], d[N];
+                rx[v].widen(f);
+                rd[v].widen(d);
 #pragma unroll
-                for (int e = 0; e < EPV; ++e) u[v][e] = (u[v][e] - m1 - f[v][e] * m2) * rstd;
-                store<T, EPV>(dx + c, u[v]);
+                for (int e = 0; e < N; ++e)
+                    d[e] = fma2(mul2(add2(f[e], minus), scale), m2, fma2(mul2(d[e], w[v][e]), scale, m1));
+                store<T, EPV>(dx + c, d);
             }
         }
     }
-    if (!a.part || slot >= a.slots) return;
+    if (!a.part) return;
+    // The teams' shares, one team after another.
+    float* share = reinterpret_cast<float*>(ahead);
     const int64_t cols = (int64_t)a.groups * a.width;
-    float* pw = a.part + slot * 2 * cols + c0;
+    float* pw = a.part + blockIdx.x * 2 * cols + c0;
+    for (int m = 0; m < teams; ++m) {
+        __syncthreads();
+        if (m != me) continue;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const int c = (t + v * team) * EPV;
-        if (c < a.width)
+        for (int v = 0; v < NV; ++v) {
+            float gw[EPV], gb[EPV];
+            singles<EPV>(dw[v], gw);
+            singles<EPV>(db[v], gb);
 #pragma unroll
             for (int e = 0; e < EPV; ++e) {
-                pw[c + e] = dw[v][e];
-                pw[cols + c + e] = db[v][e];
+                const int c = (t + v * team) * EPV + e;
+                if (c >= a.width) continue;
+                const float p = m ? share[c] + gw[e] : gw[e], q = m ? share[a.width + c] + gb[e] : gb[e];
+                if (m + 1 < teams) {
+                    share[c] = p;
+                    share[a.width + c] = q;
+                } else {
+                    pw[c] = p;
+                    pw[cols + c] = q;
+                }
             }
+        }
+    }
+}
+
+// ---- groups of up to 32 vectors: teams of lanes, numbered so that neighbours take
+// neighbouring groups of one row; a team has rows slot, slot + slots, ..., kBatch of
+// them at a time, to have their loads on the way together
+struct LaneTeam {
+    int t, grp;
+    int64_t slot, c0, rounds;
+    __device__ __forceinline__ explicit LaneTeam(const NormArgs& a) {
+        const int64_t id = (int64_t)blockIdx.x * (kThreads / a.team) + threadIdx.x / a.team;
+        t = threadIdx.x % a.team;
+        slot = a.groups == 1 ? id : id / a.groups;
+        grp = (int)(id - slot * a.groups);
+        c0 = (int64_t)grp * a.width;
+        // Every team of a warp makes the same number of rounds: its lanes meet in the sums.
+        rounds = (a.n + (int64_t)a.slots * kBatch - 1) / ((int64_t)a.slots * kBatch);
+    }
+};
+
+template <typename T, int EPV> __global__ void __launch_bounds__(kThreads) layer_norm_lanes_fwd_kernel(NormArgs a) {
+    const LaneTeam k(a);
+    const int c = k.t * EPV;
+    const bool mine = c < a.width && k.slot < a.slots;
+    using P = Pk<EPV>;
+    constexpr int N = kPk<EPV>;
+    P w[N], b[N];
+    auto weights = [&](auto type) {
+        load_w<decltype(type), EPV>(mine ? a.w : nullptr, k.c0 + c, 1.f, w);
+        load_w<decltype(type), EPV>(mine ? a.b : nullptr, k.c0 + c, 0.f, b);
+    };
+    for (int64_t it = 0; it < k.rounds; ++it) {
+        Raw<T, EPV> raw[kBatch];
+        float mean[kBatch], rstd[kBatch];
+#pragma unroll
+        for (int r = 0; r < kBatch; ++r) {
+            const int64_t row = (it * kBatch + r) * a.slots + k.slot;
+            raw[r].zero();
+            if (mine && row < a.n) raw[r].load(static_cast<const T*>(a.x) + row * a.xs + k.c0 + c);
+        }
+        if (it == 0) {                           // (behind the first rows' loads)
+            if (a.w_f32) weights(float());
+            else weights(__nv_bfloat16());
+        }
+#pragma unroll
+        for (int r = 0; r < kBatch; ++r) {
+            P f[N], q = both<P>(0.f);
+            raw[r].widen(f);
+#pragma unroll
+            for (int e = 0; e < N; ++e) q = add2(q, f[e]);
+            mean[r] = total(q);
+        }
+        lane_sum<kBatch>(mean, a.team);
+#pragma unroll
+        for (int r = 0; r < kBatch; ++r) {
+            P f[N], q = both<P>(0.f);
+            raw[r].widen(f);
+            mean[r] *= a.inv_width;
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const P d = add2(f[e], both<P>(-mean[r]));
+                q = fma2(d, d, q);
+            }
+            rstd[r] = mine ? total(q) : 0.f;
+        }
+        lane_sum<kBatch>(rstd, a.team);
+#pragma unroll
+        for (int r = 0; r < kBatch; ++r) {
+            const int64_t row = (it * kBatch + r) * a.slots + k.slot;
+            if (!mine || row >= a.n) continue;
+            rstd[r] = rsqrtf(fmaf(rstd[r], a.inv_width, a.eps));
+            if (k.t == 0 && a.mean) {
+                a.mean[row * a.groups + k.grp] = mean[r];
+                a.rstd[row * a.groups + k.grp] = rstd[r];
+            }
+            P f[N];
+            raw[r].widen(f);
+#pragma unroll
+            for (int e = 0; e < N; ++e) f[e] = fma2(mul2(add2(f[e], both<P>(-mean[r])), both<P>(rstd[r])), w[e], b[e]);
+            store<T, EPV>(static_cast<T*>(a.y) + row * a.ys + k.c0 + c, f);
+        }
+    }
+}
+
+template <typename T, int EPV> __global__ void __launch_bounds__(kThreads) layer_norm_lanes_bwd_kernel(NormArgs a) {
+    const LaneTeam k(a);
+    const int c = k.t * EPV;
+    const bool mine = c < a.width && k.slot < a.slots;
+    using P = Pk<EPV>;
+    constexpr int N = kPk<EPV>;
+    P w[N], dw[N], db[N];
+    auto weights = [&](auto type) { load_w<decltype(type), EPV>(mine ? a.w : nullptr, k.c0 + c, 1.f, w); };
+#pragma unroll
+    for (int e = 0; e < N; ++e) dw[e] = db[e] = both<P>(0.f);
+    for (int64_t it = 0; it < k.rounds; ++it) {
+        Raw<T, EPV> rx[kBatch], rd[kBatch];
+        float mean[kBatch], rstd[kBatch], s[2 * kBatch];
+#pragma unroll
+        for (int r = 0; r < kBatch; ++r) {
+            const int64_t row = (it * kBatch + r) * a.slots + k.slot;
+            rx[r].zero();
+            rd[r].zero();
+            mean[r] = rstd[r] = 0.f;
+            if (mine && row < a.n) {
+                rx[r].load(static_cast<const T*>(a.x) + row * a.xs + k.c0 + c);
+                rd[r].load(static_cast<const T*>(a.dy) + row * a.dys + k.c0 + c);
+                mean[r] = a.mean[row * a.groups + k.grp];
+                rstd[r] = a.rstd[row * a.groups + k.grp];
+            }
+        }
+        if (it == 0) {                           // (behind the first rows' loads)
+            if (a.w_f32) weights(float());
+            else weights(__nv_bfloat16());
+        }
+#pragma unroll
+        for (int r = 0; r < kBatch; ++r) {
+            P f[N], d[N], s0 = both<P>(0.f), s1 = s0;
+            rx[r].widen(f);
+            rd[r].widen(d);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const P h = mul2(add2(f[e], both<P>(-mean[r])), both<P>(rstd[r])), u = mul2(d[e], w[e]);
+                dw[e] = fma2(d[e], h, dw[e]);
+                db[e] = add2(db[e], d[e]);
+                s0 = add2(s0, u);
+                s1 = fma2(u, h, s1);
+            }
+            s[2 * r] = total(s0);
+            s[2 * r + 1] = total(s1);
+        }
+        if (!a.dx) continue;
+        lane_sum<2 * kBatch>(s, a.team);
+#pragma unroll
+        for (int r = 0; r < kBatch; ++r) {
+            const int64_t row = (it * kBatch + r) * a.slots + k.slot;
+            if (!mine || row >= a.n) continue;
+            const P m1 = both<P>(-s[2 * r] * a.inv_width * rstd[r]), m2 = both<P>(-s[2 * r + 1] * a.inv_width * rstd[r]);
+            P f[N], d[N];
+            rx[r].widen(f);
+            rd[r].widen(d);
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                d[e] = fma2(mul2(add2(f[e], both<P>(-mean[r])), both<P>(rstd[r])), m2, fma2(mul2(d[e], w[e]), both<P>(rstd[r]), m1));
+            store<T, EPV>(static_cast<T*>(a.dx) + row * a.dxs + k.c0 + c, d);
+        }
+    }
+    if (!a.part || !mine) return;
+    const int64_t cols = (int64_t)a.groups * a.width;
+    float* pw = a.part + k.slot * 2 * cols + k.c0 + c;
+    float gw[EPV], gb[EPV];
+    singles<EPV>(dw, gw);
+    singles<EPV>(db, gb);
+#pragma unroll
+    for (int e = 0; e < EPV; ++e) {
+        pw[e] = gw[e];
+        pw[cols + e] = gb[e];
     }
 }
 
@@ -254,54 +556,75 @@ __global__ void __launch_bounds__(256) layer_norm_sum_kernel(NormArgs a) {
     }
 }
 
-// Vectors of a thread and lanes of a team for nvec vectors; a team of more than 32 lanes is a CTA.
+// Vectors of a thread and threads of a team (lanes of a warp, or whole warps) for groups of nvec vectors.
 struct Shape {
     int nv, team;
+    bool lanes;
 };
-Shape shape_of(int64_t nvec, int max_nv) {
-    int nv = 1;
+Shape shape_for(int64_t nvec, int usual, int most, int threads) {
+    int t = 1, nv = usual;
     if (nvec <= 32) {
-        int t = 1;
         while (t < nvec) t *= 2;
-        return {1, t};
+        return {1, t, true};
     }
-    while (nv < max_nv && nvec > 32 * nv) nv *= 2;
-    if (nvec <= 32 * nv) return {nv, 32};
-    nv = 1;
-    while (nv < max_nv && nvec > 256 * nv) nv *= 2;
-    return {nv, (int)((nvec + 32 * nv - 1) / (32 * nv) * 32)};
+    while (nv < most && nvec > threads * (int64_t)nv) nv *= 2;
+    return {nv, (int)((nvec + 32 * nv - 1) / (32 * nv) * 32), false};
+}
+template <typename T> constexpr int kVec = 16 / (int)sizeof(T);
+// Of groups of `width` columns, read by vectors or by single elements.
+template <typename T> Shape shape_of(int64_t width, bool vec, bool bwd) {
+    if (!vec) return shape_for(width, 8, 32, kMaxTeam);
+    return bwd ? shape_for(width / kVec<T>, 2, 32 / kVec<T>, kMaxTeam) : shape_for(width / kVec<T>, 4, 16, kMaxTeam);
 }
 
-// Rows shared by a group's teams in the backward: enough teams for two CTAs an SM.
-int slots_of(int64_t n, int groups, int team) {
-    const int64_t teams = team > 32 ? 304 : 304 * (kThreads / team);
-    return (int)std::max<int64_t>(1, std::min<int64_t>(n, (teams + groups - 1) / groups));
+// Lane teams, or CTAs, that share a group's rows: what fills the GPU, but eight rows each
+// at least (every share of dw and db is written and read again).
+int slots_of(int64_t n, int groups, const Shape& sh) {
+    const int64_t all = sh.lanes ? 152 * 4 * (kThreads / sh.team) : 152;
+    return (int)std::max<int64_t>(1, std::min<int64_t>((n + 7) / 8, (all + groups - 1) / groups));
 }
 
-template <typename T, int EPV, int NV> cudaError_t run(NormArgs& a, bool bwd, int team, cudaStream_t s) {
-    const bool cta = team > 32;
-    const int64_t units = bwd ? (int64_t)a.slots * a.groups : a.n * a.groups;
-    const int64_t grid = cta ? units : (units + kThreads / team - 1) / (kThreads / team);
-    if (grid > kMaxGrid) return cudaErrorInvalidConfiguration;
+template <typename T, int EPV, int NV> cudaError_t run(NormArgs& a, bool bwd, cudaStream_t s) {
     ProfScope ps(bwd ? "layer_norm_bwd_kernel" : "layer_norm_fwd_kernel", s);
-    if (bwd && cta) layer_norm_bwd_kernel<T, EPV, NV, true><<<(unsigned)grid, team, 0, s>>>(a);
-    else if (bwd) layer_norm_bwd_kernel<T, EPV, NV, false><<<(unsigned)grid, kThreads, 0, s>>>(a);
-    else if (cta) layer_norm_fwd_kernel<T, EPV, NV, true><<<(unsigned)grid, team, 0, s>>>(a);
-    else layer_norm_fwd_kernel<T, EPV, NV, false><<<(unsigned)grid, kThreads, 0, s>>>(a);
+    if constexpr (NV >= 4) {                     // (shape_of)
+        if (!bwd) {
+            if (a.n * a.groups > kMaxGrid) return cudaErrorInvalidConfiguration;
+            layer_norm_fwd_kernel<T, EPV, NV><<<(unsigned)(a.n * a.groups), a.team, 0, s>>>(a);
+            return cudaGetLastError();
+        }
+    }
+    if constexpr (NV * EPV <= 32) {              // (shape_of)
+        const int teams = std::max(1, kMaxTeam / a.team), threads = teams * a.team;
+        const size_t copies = (size_t)kAhead<EPV, NV> * 2 * NV * threads * 16;
+        const size_t smem = std::max(copies, teams > 1 && a.part ? 2 * a.width * sizeof(float) : 0);
+        static SmemGrant grant;
+        const cudaError_t e = allow_smem(layer_norm_bwd_kernel<T, EPV, NV>, smem, grant);
+        if (e != cudaSuccess) return e;
+        layer_norm_bwd_kernel<T, EPV, NV><<<dim3(a.slots, a.groups), threads, smem, s>>>(a);
+    }
     return cudaGetLastError();
 }
 
-template <typename T> cudaError_t dispatch(NormArgs& a, bool bwd, bool vec, cudaStream_t s) {
-    constexpr int EPV = 16 / (int)sizeof(T), MAXV = 32 / EPV;
-    const Shape sh = vec ? shape_of(a.width / EPV, MAXV) : shape_of(a.width, 32);
+template <typename T, int EPV> cudaError_t run_lanes(NormArgs& a, bool bwd, cudaStream_t s) {
+    const int64_t units = (int64_t)a.slots * a.groups, grid = (units + kThreads / a.team - 1) / (kThreads / a.team);
+    if (grid > kMaxGrid) return cudaErrorInvalidConfiguration;
+    ProfScope ps(bwd ? "layer_norm_lanes_bwd_kernel" : "layer_norm_lanes_fwd_kernel", s);
+    if (bwd) layer_norm_lanes_bwd_kernel<T, EPV><<<(unsigned)grid, kThreads, 0, s>>>(a);
+    else layer_norm_lanes_fwd_kernel<T, EPV><<<(unsigned)grid, kThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T> cudaError_t launch(NormArgs& a, bool bwd, bool vec, cudaStream_t s) {
+    const Shape sh = shape_of<T>(a.width, vec, bwd);
     a.team = sh.team;
-    if (vec) {
-        if (sh.nv == 1) return run<T, EPV, 1>(a, bwd, sh.team, s);
-        if (sh.nv == 2) return run<T, EPV, 2>(a, bwd, sh.team, s);
-        if (sh.nv == 4) return run<T, EPV, 4>(a, bwd, sh.team, s);
-        if constexpr (MAXV == 8) return run<T, EPV, 8>(a, bwd, sh.team, s);
-    }
-    return sh.nv <= 8 ? run<T, 1, 8>(a, bwd, sh.team, s) : run<T, 1, 32>(a, bwd, sh.team, s);
+    a.slots = slots_of(a.n, a.groups, sh);
+    a.inv_width = 1.f / (float)a.width;
+    if (sh.lanes) return vec ? run_lanes<T, kVec<T>>(a, bwd, s) : run_lanes<T, 1>(a, bwd, s);
+    if (!vec) return sh.nv == 8 ? run<T, 1, 8>(a, bwd, s) : run<T, 1, 32>(a, bwd, s);
+    if (sh.nv == 2) return run<T, kVec<T>, 2>(a, bwd, s);
+    if (sh.nv == 4) return run<T, kVec<T>, 4>(a, bwd, s);
+    if (sh.nv == 8) return run<T, kVec<T>, 8>(a, bwd, s);
+    return run<T, kVec<T>, 16>(a, bwd, s);
 }
 
 bool misaligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) & (to - 1); }
@@ -311,6 +634,7 @@ pkv_status norm_args(const pkv_norm* norm, int64_t n, NormArgs* a, const char* w
     if (!norm) return fail(PKV_ERR_INVALID, w + ": norm is NULL");
     if ((norm->dtype != PKV_BF16 && norm->dtype != PKV_F32) || (norm->w_dtype != PKV_BF16 && norm->w_dtype != PKV_F32))
         return fail(PKV_ERR_INVALID, w + ": dtype and w_dtype must be PKV_BF16 or PKV_F32");
+    if (norm->groups > 65535) return fail(PKV_ERR_UNSUPPORTED, w + ": at most 65535 groups");
     if (norm->groups <= 0 || norm->width <= 0 || !(norm->eps >= 0.f) || norm->eps > 3.4e38f)
         return fail(PKV_ERR_INVALID, w + ": groups and width must be positive, eps a finite number >= 0");
     if (norm->width > kMaxWidth) return fail(PKV_ERR_UNSUPPORTED, w + ": width must be at most 32768");
@@ -341,10 +665,9 @@ bool whole_vectors(const pkv_norm* norm) {
     return norm->width % (norm->dtype == PKV_BF16 ? 8 : 4) == 0 && !misaligned(norm->weight, 16) && !misaligned(norm->bias, 16);
 }
 
-// The backward's slots do not depend on the addresses: scratch for vectors and for single elements.
 int slots_for(const pkv_norm* norm, int64_t n, bool vec) {
-    const int epv = norm->dtype == PKV_BF16 ? 8 : 4;
-    return slots_of(n, norm->groups, vec ? shape_of(norm->width / epv, 32 / epv).team : shape_of(norm->width, 32).team);
+    const Shape sh = norm->dtype == PKV_BF16 ? shape_of<__nv_bfloat16>(norm->width, vec, true) : shape_of<float>(norm->width, vec, true);
+    return slots_of(n, norm->groups, sh);
 }
 
 }  // namespace
@@ -368,7 +691,7 @@ pkv_status pkv_layer_norm_fwd(const void* x, int64_t x_stride, void* y, int64_t 
             return fail(PKV_ERR_INVALID, "pkv_layer_norm_fwd: mean and rstd go together, aligned to float32");
         a.x = x; a.xs = x_stride; a.y = y; a.ys = y_stride; a.mean = mean; a.rstd = rstd;
         cudaStream_t cs = static_cast<cudaStream_t>(stream);
-        const cudaError_t e = norm->dtype == PKV_BF16 ? dispatch<__nv_bfloat16>(a, false, vec, cs) : dispatch<float>(a, false, vec, cs);
+        const cudaError_t e = norm->dtype == PKV_BF16 ? launch<__nv_bfloat16>(a, false, vec, cs) : launch<float>(a, false, vec, cs);
         return e == cudaSuccess ? PKV_OK : cuda_fail(e, "pkv_layer_norm_fwd: launch");
     });
 }
@@ -410,9 +733,8 @@ pkv_status pkv_layer_norm_bwd(const void* dy, int64_t dy_stride, const void* x, 
             a.dy = dy; a.dys = dy_stride; a.x = x; a.xs = x_stride; a.dx = dx; a.dxs = dx_stride;
             a.mean = const_cast<float*>(mean); a.rstd = const_cast<float*>(rstd);
             a.part = dw || db ? scratch : nullptr;
-            a.slots = slots_for(norm, n, vec);
             if (!dx && !a.part) return PKV_OK;
-            const cudaError_t e = norm->dtype == PKV_BF16 ? dispatch<__nv_bfloat16>(a, true, vec, cs) : dispatch<float>(a, true, vec, cs);
+            const cudaError_t e = norm->dtype == PKV_BF16 ? launch<__nv_bfloat16>(a, true, vec, cs) : launch<float>(a, true, vec, cs);
             if (e != cudaSuccess) return cuda_fail(e, "pkv_layer_norm_bwd: launch");
         }
         if (!dw && !db) return PKV_OK;
