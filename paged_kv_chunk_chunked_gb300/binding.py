@@ -184,6 +184,9 @@ def _torch_dtype(dtype):
     return torch.bfloat16 if dtype == PKV_BF16 else torch.float32
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _device(stream):
     """The stream's device, which a call's tensors must be on; None: the current one."""
     return getattr(stream, "device_index", None)
@@ -193,9 +196,9 @@ def _current(dev):
     """The stream's device as the current one, for calls without a handle (whose
     kernels run on the current device); None leaves it as it is."""
     if dev is None:
-        return contextlib.nullcontext()
+        return _HERE
     import torch
-    return torch.cuda.device(dev)
+    return _HERE if torch.cuda.current_device() == dev else torch.cuda.device(dev)
 
 
 def _on_device(x, dev) -> None:
@@ -584,40 +587,66 @@ def lin_batch(n_seq: int = 1, cu=None, slot_in=None, slot_out=None) -> pkv_lin_b
     return b
 
 
-def _lin_arrays(dev, *arrays) -> None:
-    for x in arrays:
-        if x is not None and not isinstance(x, int):
+def _array(x, name: str, dtype: str, n, dev):
+    """_typed of a call's array, on its device."""
+    if x is None or isinstance(x, int):
+        return x
+    if x.get_device() != dev:
+        _on_device(x, dev)
+    return _typed(x, name, dtype, n)
+
+
+def _lin_operands(lin, n, operands, dev):
+    """Addresses and row strides of tensors [n, heads, d], (tensor, of the query heads)
+    each. Usual ones pass by one comparison of their shape and strides each (these calls
+    are short: a microsecond of checks a tensor shows); _rows looks at the others."""
+    dt, hq, hkv, d = _KIND.get(lin, _ANY)
+    at = []
+    for x, of_q in operands:
+        h = hq if of_q else hkv
+        if x.__class__ is not int and x is not None and d and x.shape == (n, h, d) and x.dtype is dt and x.get_device() == dev:
+            s0, s1, s2 = x.stride()
+            if s2 == 1 and s1 == d and s0 >= h * d:
+                at.append(x.data_ptr())
+                at.append(s0 if n > 1 else 0)
+                continue
+        at.extend(_rows(x, n, h, d, dt, dev))
+    return at
+
+
+def _lin_batch_ref(batch, dev):
+    for x in getattr(batch, "tensors", ()):
+        if x is not None and x.__class__ is not int and x.get_device() != dev:
             _on_device(x, dev)
+    return ctypes.byref(batch)
 
 
-def _decay(x, heads):
-    return _typed(x, "log_decay", "float32", heads)
+def _lin_heads(lin):
+    return _KIND.get(lin, _ANY)[2]
 
 
 def pkv_lin_attn_fwd(lin, q, k, v, o, n, log_decay, batch, stream=None) -> None:
     """q, k, v, o: tensors [n, heads, d] whose rows may lie apart."""
-    (dt, hq, hkv, d), dev = _KIND.get(lin, _ANY), _device(stream)
-    at = [y for x, h in ((q, hq), (k, hkv), (v, hkv), (o, hq)) for y in _rows(x, n, h, d, dt, dev)]
-    _lin_arrays(dev, log_decay, *getattr(batch, "tensors", ()))
-    _check(lib().pkv_lin_attn_fwd(lin, *at, n, _decay(log_decay, hkv), ctypes.byref(batch), stream_ptr(stream)))
+    dev = _device(stream)
+    at = _lin_operands(lin, n, ((q, True), (k, False), (v, False), (o, True)), dev)
+    _check(lib().pkv_lin_attn_fwd(lin, *at, n, _array(log_decay, "log_decay", "float32", _lin_heads(lin), dev),
+                                  _lin_batch_ref(batch, dev), stream_ptr(stream)))
 
 
 def pkv_lin_attn_bwd(lin, q, k, v, dout, dq, dk, dv, n, log_decay, batch, stream=None) -> None:
     """All seven: tensors [n, heads, d] whose rows may lie apart."""
-    (dt, hq, hkv, d), dev = _KIND.get(lin, _ANY), _device(stream)
-    at = [y for x, h in ((q, hq), (k, hkv), (v, hkv), (dout, hq), (dq, hq), (dk, hkv), (dv, hkv))
-          for y in _rows(x, n, h, d, dt, dev)]
-    _lin_arrays(dev, log_decay, *getattr(batch, "tensors", ()))
-    _check(lib().pkv_lin_attn_bwd(lin, *at, n, _decay(log_decay, hkv), ctypes.byref(batch), stream_ptr(stream)))
+    dev = _device(stream)
+    at = _lin_operands(lin, n, ((q, True), (k, False), (v, False), (dout, True), (dq, True), (dk, False), (dv, False)), dev)
+    _check(lib().pkv_lin_attn_bwd(lin, *at, n, _array(log_decay, "log_decay", "float32", _lin_heads(lin), dev),
+                                  _lin_batch_ref(batch, dev), stream_ptr(stream)))
 
 
 def pkv_lin_attn_step(lin, q, k, v, o, n, log_decay, slots, stream=None) -> None:
     """q, k, v, o: tensors [n, heads, d] whose rows may lie apart; slots int32 [n]."""
-    (dt, hq, hkv, d), dev = _KIND.get(lin, _ANY), _device(stream)
-    at = [y for x, h in ((q, hq), (k, hkv), (v, hkv), (o, hq)) for y in _rows(x, n, h, d, dt, dev)]
-    _lin_arrays(dev, log_decay, slots)
-    _check(lib().pkv_lin_attn_step(lin, *at, n, _decay(log_decay, hkv), _typed(slots, "slots", "int32", n),
-                                   stream_ptr(stream)))
+    dev = _device(stream)
+    at = _lin_operands(lin, n, ((q, True), (k, False), (v, False), (o, True)), dev)
+    _check(lib().pkv_lin_attn_step(lin, *at, n, _array(log_decay, "log_decay", "float32", _lin_heads(lin), dev),
+                                   _array(slots, "slots", "int32", n, dev), stream_ptr(stream)))
 
 
 def norm(width, groups: int = 1, eps: float = 1e-5, weight=None, bias=None, dtype=PKV_BF16, w_dtype=None) -> pkv_norm:
@@ -635,6 +664,7 @@ def norm(width, groups: int = 1, eps: float = 1e-5, weight=None, bias=None, dtyp
             raise ValueError(f"{name} must have groups * width = {groups * width} elements, got {x.numel()}")
     m = pkv_norm(int(dtype), dtype if w_dtype is None else w_dtype, int(groups), float(eps), int(width), ptr(weight), ptr(bias))
     m.tensors = (weight, bias)
+    m.torch_dtype = _torch_dtype(dtype)
     return m
 
 
@@ -644,8 +674,12 @@ def _norm_rows(x, n: int, m: pkv_norm, dev, name: str):
     if x is None or isinstance(x, int):
         return x, 0
     cols = m.groups * m.width
-    if x.dtype != _torch_dtype(m.dtype):
-        raise ValueError(f"{name} must be {_torch_dtype(m.dtype)}, got {x.dtype}")
+    if x.dtype != m.torch_dtype:
+        raise ValueError(f"{name} must be {m.torch_dtype}, got {x.dtype}")
+    if x.shape == (n, cols) and x.get_device() == dev:        # the usual ones
+        s0, s1 = x.stride()
+        if s1 == 1 and s0 >= cols:
+            return x.data_ptr(), (s0 if n > 1 else 0)
     if x.dim() < 1 or x.shape[0] != n or x.numel() != n * cols:
         raise ValueError(f"{name} must have {n} rows of {cols} columns, got shape {tuple(x.shape)}")
     dense = 1                                 # every row dense memory of its own
@@ -659,25 +693,20 @@ def _norm_rows(x, n: int, m: pkv_norm, dev, name: str):
     return x.data_ptr(), (x.stride(0) if n > 1 else 0)
 
 
-def _floats(x, n: int, dev, name: str):
-    p = _typed(x, name, "float32", n)
-    if x is not None and not isinstance(x, int):
-        _on_device(x, dev)
-    return p
-
-
-def _norm_vectors(m: pkv_norm, dev) -> None:
-    _lin_arrays(dev, *getattr(m, "tensors", ()))
+def _norm_ref(m: pkv_norm, dev):
+    for x in getattr(m, "tensors", ()):
+        if x is not None and x.__class__ is not int and x.get_device() != dev:
+            _on_device(x, dev)
+    return ctypes.byref(m)
 
 
 def pkv_layer_norm_fwd(x, y, mean, rstd, n, norm, stream=None) -> None:
     """x, y: tensors of n rows that may lie apart; mean, rstd float32 [n, groups] or None."""
     dev = _device(stream)
     (xp, xs), (yp, ys) = _norm_rows(x, n, norm, dev, "x"), _norm_rows(y, n, norm, dev, "y")
-    _norm_vectors(norm, dev)
-    m, r = (_floats(t, n * norm.groups, dev, w) for t, w in ((mean, "mean"), (rstd, "rstd")))
+    m, r = _array(mean, "mean", "float32", n * norm.groups, dev), _array(rstd, "rstd", "float32", n * norm.groups, dev)
     with _current(dev):
-        _check(lib().pkv_layer_norm_fwd(xp, xs, yp, ys, m, r, n, ctypes.byref(norm), stream_ptr(stream)))
+        _check(lib().pkv_layer_norm_fwd(xp, xs, yp, ys, m, r, n, _norm_ref(norm, dev), stream_ptr(stream)))
 
 
 def pkv_layer_norm_scratch(norm, n) -> int:
@@ -692,17 +721,16 @@ def pkv_layer_norm_bwd(dy, x, mean, rstd, dx, dw, db, n, norm, scratch, accumula
     dw, db float32 [groups * width], each or dx may be None."""
     dev = _device(stream)
     at = [y for t, w in ((dy, "dy"), (x, "x"), (dx, "dx")) for y in _norm_rows(t, n, norm, dev, w)]
-    _norm_vectors(norm, dev)
-    m, r = (_floats(t, n * norm.groups, dev, w) for t, w in ((mean, "mean"), (rstd, "rstd")))
-    gw, gb = (_floats(t, norm.groups * norm.width, dev, w) for t, w in ((dw, "dw"), (db, "db")))
+    m, r = _array(mean, "mean", "float32", n * norm.groups, dev), _array(rstd, "rstd", "float32", n * norm.groups, dev)
+    gw, gb = (_array(t, w, "float32", norm.groups * norm.width, dev) for t, w in ((dw, "dw"), (db, "db")))
     if scratch is not None and not isinstance(scratch, int):
         need = pkv_layer_norm_scratch(norm, n) if gw or gb else 0
         if scratch.numel() < need:
             raise ValueError(f"scratch must have {need} floats, got {scratch.numel()}")
-        scratch = _floats(scratch, None, dev, "scratch")
+        scratch = _array(scratch, "scratch", "float32", None, dev)
     with _current(dev):
         _check(lib().pkv_layer_norm_bwd(*at[:4], m, r, *at[4:], gw, gb, 1 if accumulate else 0, scratch, n,
-                                        ctypes.byref(norm), stream_ptr(stream)))
+                                        _norm_ref(norm, dev), stream_ptr(stream)))
 
 
 def pkv_profile_enable(on: bool) -> None:
