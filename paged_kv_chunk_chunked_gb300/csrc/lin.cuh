@@ -75,25 +75,26 @@ __device__ __forceinline__ bool lin_range(const LinArgs& a, int64_t b, int64_t& 
 }
 
 struct LinChunk {
-    int64_t row0;                    // first row
+    int row0;                        // first row (a call has less than 2^31)
     int rows;                        // 1 .. L
 };
 
-// The first 32 sequences' rows, a sequence a lane: kernels that look many chunks up
-// load them once.
+// The first 32 sequences' rows: kernels that look many chunks up load them once, into
+// shared memory (registers are short where it is read).
 struct LinCuts {
-    int64_t lo = 0, hi = 0;
-    __device__ __forceinline__ explicit LinCuts(const LinArgs& a, int64_t b0 = 0) {
-        const int64_t b = b0 + threadIdx.x % 32;
-        if (a.cu && b < a.n_seq) {
-            lo = a.cu[b];
-            hi = a.cu[b + 1];
-        }
+    int64_t lo[32], hi[32];
+    // By one warp.
+    __device__ __forceinline__ void load(const LinArgs& a) {
+        const int64_t b = threadIdx.x % 32;
+        const bool in = a.cu && b < a.n_seq;
+        lo[b] = in ? a.cu[b] : 0;
+        hi[b] = in ? a.cu[b + 1] : 0;
     }
 };
 
 // The rows of chunk number f; false: there is no such chunk. Called by whole warps.
-template <int L> __device__ __forceinline__ bool lin_chunk(const LinArgs& a, const LinCuts& first, int f, LinChunk& c) {
+// first: the first sequences' rows, or null.
+template <int L> __device__ __forceinline__ bool lin_chunk(const LinArgs& a, const LinCuts* first, int f, LinChunk& c) {
     int64_t b = 0, lo = 0, hi = a.n;
     if (a.cu) {
         // The last sequence whose chunks start at or before f (numbers ascend with b): lane x
@@ -101,12 +102,19 @@ template <int L> __device__ __forceinline__ bool lin_chunk(const LinArgs& a, con
         const int lane = threadIdx.x % 32;
         b = -1;
         for (int64_t b0 = 0; b0 < a.n_seq; b0 += 32) {
-            const LinCuts x = b0 ? LinCuts(a, b0) : first;
-            const int k = __popc(__ballot_sync(0xffffffffu, b0 + lane < a.n_seq && x.lo / L + b0 + lane <= f));
+            int64_t l = 0, r = 0;
+            if (first && b0 == 0) {
+                l = first->lo[lane];
+                r = first->hi[lane];
+            } else if (b0 + lane < a.n_seq) {
+                l = a.cu[b0 + lane];
+                r = a.cu[b0 + lane + 1];
+            }
+            const int k = __popc(__ballot_sync(0xffffffffu, b0 + lane < a.n_seq && l / L + b0 + lane <= f));
             if (k > 0) {
                 b = b0 + k - 1;
-                lo = __shfl_sync(0xffffffffu, x.lo, k - 1);
-                hi = __shfl_sync(0xffffffffu, x.hi, k - 1);
+                lo = __shfl_sync(0xffffffffu, l, k - 1);
+                hi = __shfl_sync(0xffffffffu, r, k - 1);
             }
             if (k < 32) break;
         }
@@ -115,11 +123,11 @@ template <int L> __device__ __forceinline__ bool lin_chunk(const LinArgs& a, con
     if (!lin_good(a, lo, hi)) return false;
     const int64_t off = ((int64_t)f - (lo / L + b)) * L;
     if (off < 0 || off >= hi - lo) return false;
-    c.row0 = lo + off;
+    c.row0 = (int)(lo + off);
     c.rows = (int)min64(L, hi - lo - off);
     return true;
 }
-template <int L> __device__ __forceinline__ bool lin_chunk(const LinArgs& a, int f, LinChunk& c) { return lin_chunk<L>(a, LinCuts(a), f, c); }
+template <int L> __device__ __forceinline__ bool lin_chunk(const LinArgs& a, int f, LinChunk& c) { return lin_chunk<L>(a, nullptr, f, c); }
 
 __device__ __forceinline__ float lin_g2(const LinArgs& a, int kvh) {
     return a.log_decay ? a.log_decay[kvh] * kLog2e : 0.f;

@@ -154,39 +154,31 @@ struct Cut {
     __device__ __forceinline__ int begin(unsigned cta) const { return per * (int)cta + min((int)cta, more); }
 };
 
-// The units of a CTA, chunks of a KV head: a backward's q do^T (g heads of work
-// each), then the k v^T (one each). A CTA has the units that begin in its length of
-// all units' work.
+// The units of a CTA, chunks of a KV head: numbers blockIdx.x, + gridDim.x, ...; a
+// backward's q do^T (g heads of work each) come first, then the k v^T (one each).
+// (Units cut by work instead, the short ones on the CTAs that the long ones leave:
+// 24 us instead of 20 for a training chunk, as a short unit is mostly latency.)
 struct PartWalk {
     const LinArgs& a;
-    int n, g, i, end, other, other_end, it = -1;
-    bool grad;
+    int per_kind, n, i, it = -1;
+    bool both, grad = false;
     int f = 0, h = 0;
     LinChunk c{};
-    LinCuts cuts;
-    __device__ __forceinline__ PartWalk(const LinArgs& args, bool both, Cut cut)
-        : a(args), n(args.n_chunks * args.Hkv), g(args.Hq / args.Hkv), grad(both), cuts(args) {
-        const int from = cut.begin(blockIdx.x), to = cut.begin(blockIdx.x + 1), before = both ? n * g : 0;   // work of all q do^T
-        other = max(0, from - before);
-        other_end = max(0, to - before);
-        i = both ? min(n, (from + g - 1) / g) - 1 : other - 1;
-        end = both ? min(n, (to + g - 1) / g) : other_end;
-    }
+    const LinCuts* cuts;
+    __device__ __forceinline__ PartWalk(const LinArgs& args, bool both_, const LinCuts* first)
+        : a(args), per_kind(args.n_chunks * args.Hkv), n(both_ ? 2 * per_kind : per_kind), i((int)blockIdx.x - (int)gridDim.x), both(both_),
+          cuts(first) {}
     __device__ __forceinline__ bool next() {
-        for (;;) {
-            if (++i >= end) {
-                if (!grad) return false;
-                grad = false;
-                i = other - 1;
-                end = other_end;
-                continue;
-            }
-            f = i / a.Hkv;
-            h = i - f * a.Hkv;
+        while ((i += gridDim.x) < n) {
+            grad = both && i < per_kind;
+            const int u = both && !grad ? i - per_kind : i;
+            f = u / a.Hkv;
+            h = u - f * a.Hkv;
             if (!lin_chunk<kL>(a, cuts, f, c)) continue;
             ++it;
             return true;
         }
+        return false;
     }
     __device__ __forceinline__ int heads() const { return grad ? a.Hq / a.Hkv : 1; }
     __device__ __forceinline__ int stages() const { return (c.rows + kPartRows - 1) / kPartRows; }
@@ -204,12 +196,11 @@ struct PartWalk {
 // those of k v^T, of 128 rows alone, have one, and two units alternate between both.
 // D = 64 packs two terms into the 128 lanes of an instruction: lanes 0 .. 63 hold hi's
 // sum and, 64 columns on, lo's; lanes 64 .. 127 mid's.
-template <int D>
-__global__ void __maxnreg__(88)
+template <int D, bool BOTH>
+__global__ void __maxnreg__(BOTH ? 128 : 88)
 lin_part_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
-                   const __grid_constant__ CUtensorMap map_kv_out, const __grid_constant__ CUtensorMap map_qdo_out, const LinArgs a, bool both,
-                   Cut cut) {
+                   const __grid_constant__ CUtensorMap map_kv_out, const __grid_constant__ CUtensorMap map_qdo_out, const LinArgs a) {
     using L = PartLayout<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -236,16 +227,21 @@ lin_part_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     if (threadIdx.x == 0) {
         tc::prefetch_tmap(&map_k);
         tc::prefetch_tmap(&map_v);
-        if (both) {
+        if (BOTH) {
             tc::prefetch_tmap(&map_q);
             tc::prefetch_tmap(&map_do);
         }
     }
-    PartWalk w(a, both, cut);
-    bool more = w.next();                        // (its loads overlap the set-up)
+    __shared__ LinCuts cuts;
+    constexpr int kDecays = 64;
+    __shared__ float decays[kDecays];            // log2 of the first KV heads' decays
+    if (warp == 2) cuts.load(a);
+    for (int h = threadIdx.x - 96; h >= 0 && h < min(a.Hkv, kDecays); h += kPartThreads - 96) decays[h] = lin_g2(a, h);
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
+    PartWalk w(a, BOTH, &cuts);
+    bool more = w.next();
     launch_dependents();
     const uint32_t tmem = B.tmem_base;
     int st = 0;                                  // stages so far
@@ -334,14 +330,16 @@ lin_part_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         const uint32_t base = col / 64 * L::kBlock + half * 4096 + col % 8 * 2;
         const uint32_t chunk = col % 64 / 8;
         const uint32_t ta = tmem + ((uint32_t)(quad * 32) << 16) + L::kColA + 16 * half;
-        __shared__ __align__(16) float wt[kL];
+        __shared__ __align__(16) float weights[2][kL];
         bool ok = true;
-        for (; more; more = w.next()) {
+        int unit = 0;
+        for (; more; more = w.next(), ++unit) {
+            // Weights of units in turn: who is at the second of two barriers has left the first unit's.
             // (After a failed wait the walk goes on, only to keep meeting the other warps here.)
-            asm volatile("bar.sync 2, 256;" ::: "memory");                               // nobody reads the last weights any more
+            float* wt = weights[unit & 1];
             const int ns = w.stages(), total = w.heads() * ns, m = w.c.rows;
             if (tid < kL) {
-                const float g2 = lin_g2(a, w.h);
+                const float g2 = w.h < kDecays ? decays[w.h] : lin_g2(a, w.h);
                 wt[tid] = tid >= m ? 0.f : w.grad ? rsqrtf((float)D) * lin_pow(g2, tid + 1) : lin_pow(g2, m - 1 - tid);
             }
             asm volatile("bar.sync 2, 256;" ::: "memory");
@@ -362,7 +360,7 @@ lin_part_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 }
                 const ulonglong2* wq = reinterpret_cast<const ulonglong2*>(wt + q * kPartRows + 32 * half);
 #pragma unroll
-                for (int z = 0; z < 2; ++z) {    // 16 rows at a time: the kernel's registers leave room for two CTAs of the scan
+                for (int z = 0; z < 2; ++z) {    // 16 rows at a time: few registers leave room for CTAs of the scan, see below
                     uint32_t x[16], hi[8], mid[8], lo[8];
 #pragma unroll
                     for (int t = 0; t < 16; ++t) {
@@ -548,7 +546,7 @@ template <int D> struct RowsLayout {
     static constexpr uint32_t kStage = 32 * D;
     static constexpr uint32_t kSmem = kOffStage + 16 * kStage + 1024;
 };
-constexpr int kRowsThreads = 3 * 32 + 2 * 256;
+constexpr int kRowsThreads = 3 * 32 + 2 * 128;
 
 struct RowsBarriers {
     uint64_t c_full, st_full, pair_empty, r_full, r_empty;
@@ -568,10 +566,10 @@ struct HeadWalk {
     int g, it = -1, pair = -1, f = 0, h = 0, head = 0;
     bool first = false, live = false;
     LinChunk c{};
-    LinCuts cuts;
+    const LinCuts* cuts;
 
-    __device__ __forceinline__ HeadWalk(const LinArgs& args, int from, int to)
-        : a(args), idx(from - 1), end(to), g(args.Hq / args.Hkv), cuts(args) {}
+    __device__ __forceinline__ HeadWalk(const LinArgs& args, int from, int to, const LinCuts* first)
+        : a(args), idx(from - 1), end(to), g(args.Hq / args.Hkv), cuts(first) {}
     // The next head: it counts heads, pair (chunk, KV head)s; first: the first head of its pair here.
     __device__ __forceinline__ bool next() {
         while (++idx < end) {
@@ -619,13 +617,13 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
-            tc::mbar_init(&B.r_ready[s], 256);
+            tc::mbar_init(&B.r_ready[s], 128);
             tc::mbar_init(&B.x_full[s], 1);
             tc::mbar_init(&B.x_empty[s], 1);
             tc::mbar_init(&B.s_full[s], 1);
-            tc::mbar_init(&B.p_full[s], 256);
+            tc::mbar_init(&B.p_full[s], 128);
             tc::mbar_init(&B.o_full[s], 1);
-            tc::mbar_init(&B.o_free[s], 256);
+            tc::mbar_init(&B.o_free[s], 128);
             tc::mbar_init(&B.drain[s], 1);
         }
         tc::mbar_init(&B.c_full, 1);
@@ -645,11 +643,13 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         tc::prefetch_tmap(&map_r);
         tc::prefetch_tmap(&map_s);
     }
-    HeadWalk w(a, cut.begin(blockIdx.x), cut.begin(blockIdx.x + 1));
-    bool more = w.next();                        // (its loads overlap the set-up)
+    __shared__ LinCuts cuts;
+    if (warp == 2) cuts.load(a);
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
+    HeadWalk w(a, cut.begin(blockIdx.x), cut.begin(blockIdx.x + 1), &cuts);
+    bool more = w.next();
     launch_dependents();
     const uint32_t tmem = B.tmem_base;
     if (warp == 0) {
@@ -783,30 +783,30 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         __syncwarp();
     } else {
         // ------------------------------------------------------------ weights and outputs
-        const int wg = (warp - 3) >> 3, half = (warp - 3) >> 2 & 1, quad = warp & 3, i = quad * 32 + lane;     // row of the chunk
-        const int t256 = (threadIdx.x - 96) & 255;
+        const int wg = (warp - 3) >> 2, quad = warp & 3, i = quad * 32 + lane;   // row of the chunk
+        const int t128 = (threadIdx.x - 96) & 127;
         const uint32_t t = tmem + ((uint32_t)(quad * 32) << 16) + wg * 256;
         const float scale = rsqrtf((float)D);
         const LinRows& out = GRAD ? a.dq : a.o;
-        uint8_t* stage = smem + L::kOffStage + (warp - 3) * L::kStage;
+        uint8_t* stage = smem + L::kOffStage + (warp - 3) * 2 * L::kStage;
         // l's powers, kept while the KV head stays; each group has tables of its own:
         // l^(x - 31) for x >= 31, else 0, and l^(31 - x).
         __shared__ float diag[2][64];
         __shared__ __align__(16) float up[2][32];
         int h_of = -1;
-        float rb[2], li1 = 0.f;                  // of blocks 2 half, 2 half + 1
+        float rb[3], li1 = 0.f;
         bool ok = true;
         for (; more; more = w.next()) {
             if (w.h != h_of) {
                 h_of = w.h;
                 const float g2 = lin_g2(a, w.h);
-                asm volatile("bar.sync %0, 256;" :: "r"(1 + wg) : "memory");     // nobody reads the old table any more
-                if (t256 < 64) diag[wg][t256] = t256 >= 31 ? lin_pow(g2, t256 - 31) : 0.f;
-                else if (t256 < 96) up[wg][t256 - 64] = lin_pow(g2, 95 - t256);
+                asm volatile("bar.sync %0, 128;" :: "r"(1 + wg) : "memory");     // nobody reads the old table any more
+                if (t128 < 64) diag[wg][t128] = t128 >= 31 ? lin_pow(g2, t128 - 31) : 0.f;
+                else if (t128 < 96) up[wg][t128 - 64] = lin_pow(g2, 95 - t128);
 #pragma unroll
-                for (int b = 0; b < 2; ++b) rb[b] = 2 * half + b < quad ? lin_pow(g2, i - 32 * (2 * half + b) - 31) : 0.f;
+                for (int b = 0; b < 3; ++b) rb[b] = b < quad ? lin_pow(g2, i - 32 * b - 31) : 0.f;
                 li1 = lin_pow(g2, i + 1);
-                asm volatile("bar.sync %0, 256;" :: "r"(1 + wg) : "memory");
+                asm volatile("bar.sync %0, 128;" :: "r"(1 + wg) : "memory");
             }
             // (After a failed wait the walk goes on, only to keep meeting the other warps at the barriers.)
             if ((w.it & 1) != wg || !ok) continue;
@@ -814,45 +814,53 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             if (ok && w.first) {
                 if (w.c.rows < kL) {             // what lies behind the sequence may be anything
                     ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.r_full, w.pair & 1, a.wait_err));
-                    if (ok) zero_tail<D>(smem + L::kOffR, w.c.rows, t256, 256);
+                    if (ok) zero_tail<D>(smem + L::kOffR, w.c.rows, t128, 128);
                     tc::fence_proxy_async_smem();
                 }
                 tc::mbar_arrive(&B.r_ready[w.pair & 1]);
             }
             if (!ok) continue;
             tc::tc_fence_after();
-            uint32_t pk[32];
+            // Blocks left of the diagonal's, then the diagonal's, then nothing.
+#pragma unroll 1
+            for (int b = 0; b < 4; ++b) {
+                uint32_t pk[16];
+                if (b > quad) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int block = 2 * half + b;
-                if (block > quad) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) pk[16 * b + e] = 0u;
-                    continue;
-                }
-                uint32_t r[32];
-                tc::tmem_ld32(t + 32 * block, r);
-                tc::tmem_wait_ld(r);
-                if (block < quad) {
-                    const float f = rb[b];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        pk[16 * b + e] = pack_bf16x2(__uint_as_float(r[2 * e]) * (up[wg][2 * e] * f),
-                                                     __uint_as_float(r[2 * e + 1]) * (up[wg][2 * e + 1] * f));
+                    for (int e = 0; e < 16; ++e) pk[e] = 0u;
                 } else {
+                    uint32_t r[32];
+                    tc::tmem_ld32(t + 32 * b, r);
+                    tc::tmem_wait_ld(r);
+                    if (b < quad) {
+                        const float f1 = b == 0 ? rb[0] : b == 1 ? rb[1] : rb[2];
+                        const f32x2 f = pack2(f1, f1);
+                        const ulonglong2* u = reinterpret_cast<const ulonglong2*>(up[wg]);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float x = 2 * e <= lane ? __uint_as_float(r[2 * e]) * diag[wg][lane - 2 * e + 31] : 0.f;
-                        const float y = 2 * e + 1 <= lane ? __uint_as_float(r[2 * e + 1]) * diag[wg][lane - 2 * e + 30] : 0.f;
-                        pk[16 * b + e] = pack_bf16x2(x, y);
+                        for (int e = 0; e < 16; e += 2) {
+                            const ulonglong2 k = u[e / 2];
+                            float x, y;
+                            unpack2(mul2(pack2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), mul2(k.x, f)), x, y);
+                            pk[e] = pack_bf16x2(x, y);
+                            unpack2(mul2(pack2(__uint_as_float(r[2 * e + 2]), __uint_as_float(r[2 * e + 3])), mul2(k.y, f)), x, y);
+                            pk[e + 1] = pack_bf16x2(x, y);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float x = 2 * e <= lane ? __uint_as_float(r[2 * e]) * diag[wg][lane - 2 * e + 31] : 0.f;
+                            const float y = 2 * e + 1 <= lane ? __uint_as_float(r[2 * e + 1]) * diag[wg][lane - 2 * e + 30] : 0.f;
+                            pk[e] = pack_bf16x2(x, y);
+                        }
                     }
                 }
+                tc::tmem_st16(t + 64 * (b >> 1) + 16 * (b & 1), pk);
             }
-            tc::tmem_st32(t + 64 * half, pk);
             ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.o_full[wg], 0, a.wait_err));
             if (!ok) continue;
             tc::tc_fence_after();
-            scale_half<D>(t + 128 + D / 2 * half, li1);
+            scale_half<D>(t + 128, li1);
+            scale_half<D>(t + 128 + D / 2, li1);
             tc::tmem_wait_st();
             tc::tc_fence_before();
             tc::mbar_arrive(&B.p_full[wg]);
@@ -860,11 +868,13 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             if (!ok) continue;
             tc::tc_fence_after();
             // The rows leave tensor memory first: the next head's products need not wait for the stores.
-            uint32_t o[D / 4];
-            load_half<D>(t + 128 + D / 2 * half, scale, o);
+            uint32_t o0[D / 4], o1[D / 4];
+            load_half<D>(t + 128, scale, o0);
+            load_half<D>(t + 128 + D / 2, scale, o1);
             tc::tc_fence_before();
             tc::mbar_arrive(&B.o_free[wg]);
-            store_half<D>(o, &map_out, stage, lane, w.c.rows - 32 * quad, D / 2 * half, w.head, w.c.row0 + 32 * quad, out);
+            store_half<D>(o0, &map_out, stage, lane, w.c.rows - 32 * quad, 0, w.head, w.c.row0 + 32 * quad, out);
+            store_half<D>(o1, &map_out, stage + L::kStage, lane, w.c.rows - 32 * quad, D / 2, w.head, w.c.row0 + 32 * quad, out);
         }
         if (lane == 0) bulk_wait();
     }
@@ -1177,30 +1187,32 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t sm
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// The chunks' sums and their scans: k v^T, in a backward (both) also q do^T.
-template <int D> cudaError_t states(const LinArgs& a, bool both, cudaStream_t s, std::string* why) {
+// The chunks' sums and their scans: k v^T, in a backward (BOTH) also q do^T. The
+// forward's sums kernel is held to registers that leave room for the scan's CTAs beside
+// it, so that their set-up overlaps (4096 rows, 4 KV heads of d 128: 1.7 us of 31); the
+// backward's is much longer and faster with more (0.64 us a stage instead of 0.75).
+template <int D, bool BOTH> cudaError_t states(const LinArgs& a, cudaStream_t s, std::string* why) {
     static SmemGrant grant;
-    cudaError_t e = allow_smem(lin_part_tc_kernel<D>, PartLayout<D>::kSmem, grant);
+    cudaError_t e = allow_smem(lin_part_tc_kernel<D, BOTH>, PartLayout<D>::kSmem, grant);
     if (e != cudaSuccess) return e;
-    const int nz = both ? 2 : 1;
+    const int nz = BOTH ? 2 : 1;
     if (a.n) {
         CUtensorMap k, v, q, go, out, gout;
         if (!rows_map(&k, a.k, a.Hkv, a, kPartRows, why) || !rows_map(&v, a.v, a.Hkv, a, kPartRows, why) || !sums_map(&out, a.part, a, why))
             return cudaErrorInvalidValue;
         q = k; go = v; gout = out;               // (unused by a forward)
-        if (both && (!rows_map(&q, a.q, a.Hq, a, kPartRows, why) || !rows_map(&go, a.dout, a.Hq, a, kPartRows, why) ||
+        if (BOTH && (!rows_map(&q, a.q, a.Hq, a, kPartRows, why) || !rows_map(&go, a.dout, a.Hq, a, kPartRows, why) ||
                      !sums_map(&gout, a.gpart, a, why)))
             return cudaErrorInvalidValue;
-        const int work = a.n_chunks * (a.Hkv + (both ? a.Hq : 0)), grid = std::min(a.n_chunks * a.Hkv * nz, sm_count());
+        const int grid = std::min(a.n_chunks * a.Hkv * nz, sm_count());
         ProfScope ps("lin_part_tc_kernel", s);
-        lin_part_tc_kernel<D><<<grid, kPartThreads, PartLayout<D>::kSmem, s>>>(q, k, v, go, out, gout, a, both,
-                                                                                     Cut{work / grid, work % grid});
+        lin_part_tc_kernel<D, BOTH><<<grid, kPartThreads, PartLayout<D>::kSmem, s>>>(q, k, v, go, out, gout, a);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     const dim3 grid((unsigned)(a.n_seq * a.Hkv * (D * D / 4 / kScanThreads)), nz);
     ProfScope ps("lin_scan_bf16_kernel", s);
     if (a.n) return launch_after(lin_scan_bf16_kernel<D>, grid, kScanThreads, 0, s, a);
-    lin_scan_bf16_kernel<D><<<grid, kScanThreads, 0, s>>>(a);          // no sums before it
+    lin_scan_bf16_kernel<D><<<grid, kScanThreads, 0, s>>>(a);                    // no sums before it
     return cudaGetLastError();
 }
 
@@ -1234,12 +1246,12 @@ template <int D> cudaError_t cols(const LinArgs& a, cudaStream_t s, std::string*
 }
 
 template <int D> cudaError_t fwd(const LinArgs& a, cudaStream_t s, std::string* why) {
-    const cudaError_t e = states<D>(a, false, s, why);
+    const cudaError_t e = states<D, false>(a, s, why);
     return e != cudaSuccess || !a.n ? e : rows<D, false>(a, s, why);
 }
 
 template <int D> cudaError_t bwd(const LinArgs& a, cudaStream_t s, std::string* why) {
-    cudaError_t e = states<D>(a, true, s, why);
+    cudaError_t e = states<D, true>(a, s, why);
     if (e == cudaSuccess && a.n) e = cols<D>(a, s, why);
     return e != cudaSuccess || !a.n ? e : rows<D, true>(a, s, why);
 }
