@@ -260,7 +260,7 @@ def prepare(case, seed):
         if case["op"] == "train":
             c.dstate[m:] = s.pop("dlast")
         at = torch.arange(m, dtype=torch.int32, device="cuda")
-        s["batch"] = c.B.lin_batch(m, cu=s["cu"], slot_in=at if case["start"] else None, slot_out=at + m)
+        s["batch"] = c.B.lin_batch(m, cu=s["cu"], slot_in=at, slot_out=at + m)  # (a new store's states are zero)
     return s
 
 
