@@ -538,8 +538,9 @@ pkv_status pkv_lin_check(pkv_lin* lin);
  * and a slot that is not in -1 .. n_slots - 1 are recorded for pkv_lin_check (that
  * sequence is left out, others of the call may come out wrong; the slot counts
  * as -1). A slot must not be written for
- * two sequences of a call, nor be written for one and read for another; several
- * may start from one slot in the forward. */
+ * two sequences of a call, nor be written for one and read for another (recorded
+ * too; its state is then undefined). Several sequences may start from one slot in
+ * the forward, not in the backward, where each writes a gradient of its own. */
 typedef struct pkv_lin_batch {
     const int64_t* cu;         /* device int64 [n_seq + 1], or NULL: one sequence, all rows */
     const int32_t* slot_in;    /* device int32 [n_seq], or NULL: all start from zero     */
@@ -550,7 +551,10 @@ typedef struct pkv_lin_batch {
 /* O [n, Hq, d] of Q [n, Hq, d], K, V [n, Hkv, d]. Operands have row strides as
  * for the rotation calls (0 = dense; 16-byte alignment; no overlap of an output
  * with anything). log_decay: device float32 [Hkv], or NULL for no decay; 0 is no
- * decay, -inf a memory of the token itself alone. */
+ * decay, -inf a memory of the token itself alone. A NaN or an infinity in a token
+ * reaches all later ones of its sequence, and earlier ones of its chunk (128 rows on
+ * the tensor cores, else 64; a zero weight times infinity is NaN); nothing in other
+ * sequences, and nothing in rows of no sequence reaches anything. */
 pkv_status pkv_lin_attn_fwd(pkv_lin* lin, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                             const void* v, int64_t v_stride, void* o, int64_t o_stride, int64_t n,
                             const float* log_decay, const pkv_lin_batch* batch, void* stream);
@@ -568,7 +572,8 @@ pkv_status pkv_lin_attn_bwd(pkv_lin* lin, const void* q, int64_t q_stride, const
 
 /* One token for each of n sequences: row i advances the state of slot slots[i]
  * (device int32 [n]) in place and writes o's row i. A row with slot -1 is
- * padding: its o is left as it was. No slot may appear twice. */
+ * padding: its o is left as it was. No slot may appear twice (recorded for
+ * pkv_lin_check; both rows and the state are then undefined). */
 pkv_status pkv_lin_attn_step(pkv_lin* lin, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                              const void* v, int64_t v_stride, void* o, int64_t o_stride, int64_t n,
                              const float* log_decay, const int32_t* slots, void* stream);

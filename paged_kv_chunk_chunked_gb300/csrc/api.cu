@@ -242,6 +242,7 @@ pkv_status pkv::take_device_error(int* d_err, const char* who) {
                      : h == pkv::kErrSlots       ? "more pages staged than device slots"
                      : h == pkv::kErrBadSeq      ? "a sequence's rows were not a range of the call's rows"
                      : h == pkv::kErrBadSlot     ? "a state slot was out of range"
+                     : h == pkv::kErrSlotTwice   ? "a state slot was given to two sequences of a call"
                                                  : "unknown device error";
     return fail(PKV_ERR_DEVICE_FAULT, std::string("device error ") + std::to_string(h) + ": " + what);
 }

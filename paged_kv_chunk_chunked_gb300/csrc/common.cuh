@@ -17,6 +17,7 @@ enum DeviceError : int {
     kErrSlots = 4,           // more pages requested for staging than device slots
     kErrBadSeq = 5,          // a sequence's rows are no range of the call's rows
     kErrBadSlot = 6,         // a state slot out of range
+    kErrSlotTwice = 7,       // a state slot given to two sequences of a call
 };
 
 __device__ __forceinline__ void report_error(int* err, int code) {

@@ -145,6 +145,18 @@ __device__ __forceinline__ int64_t lin_slot(const LinArgs& a, const int32_t* slo
     return slots ? lin_good_slot(a, slots[b]) : -1;
 }
 
+// By all threads of a CTA, for one sequence: records whether `mine`, which sequence b
+// writes, is written for one before it or read for any other (`read` may be null).
+__device__ __forceinline__ void lin_check_alone(const LinArgs& a, const int32_t* written, const int32_t* read, int64_t b, int64_t mine,
+                                                int64_t n) {
+    if (mine < 0) return;
+    bool twice = false;
+    for (int64_t j = threadIdx.x; j < b; j += blockDim.x) twice |= written[j] == mine;
+    if (read)
+        for (int64_t j = threadIdx.x; j < n; j += blockDim.x) twice |= j != b && read[j] == mine;
+    if (twice) report_error(a.err, kErrSlotTwice);
+}
+
 // CUDA-core kernels (chunks of kLinSimtChunk rows).
 constexpr int kLinSimtChunk = 64;
 cudaError_t launch_lin_fwd_simt(const LinArgs& a, cudaStream_t s);

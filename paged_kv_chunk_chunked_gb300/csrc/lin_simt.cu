@@ -108,6 +108,7 @@ __global__ void __launch_bounds__(kThreads) lin_scan_kernel(LinArgs a) {
     if (!lin_range(a, b, lo, hi)) return;
     const float g2 = lin_g2(a, h);
     const int64_t first = lin_slot(a, GRAD ? a.slot_out : a.slot_in, b), last = lin_slot(a, GRAD ? a.slot_in : a.slot_out, b);
+    if (blockIdx.x % (V / kThreads * a.Hkv) == 0) lin_check_alone(a, GRAD ? a.slot_in : a.slot_out, GRAD ? a.slot_out : a.slot_in, b, last, a.n_seq);
     float* store = GRAD ? a.dstate : a.state;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (first >= 0) s = reinterpret_cast<const float4*>(store + ((size_t)first * a.Hkv + h) * D * D)[e];

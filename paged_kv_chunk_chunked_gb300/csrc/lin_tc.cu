@@ -503,6 +503,7 @@ __global__ void __launch_bounds__(kScanThreads, 5) lin_scan_bf16_kernel(const Li
     float4* store = reinterpret_cast<float4*>(grad ? a.dstate : a.state);
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (good && first >= 0) s = store[((size_t)first * a.Hkv + h) * V + e];      // (older than the kernel before)
+    if (blockIdx.x % (V / kScanThreads * a.Hkv) == 0) lin_check_alone(a, to, from, b, last, a.n_seq);
     wait_for_kernels();
     if (!good) return;
     const int64_t nc = (hi - lo + kL - 1) / kL;

@@ -287,6 +287,39 @@ def test_bad_ranges_and_slots_are_recorded(dtype):
         assert torch.equal(good, fwd([0, n]))
 
 
+@pytest.mark.parametrize("dtype,flags,Hkv", [("bf16", 0, 1), ("bf16", B.PKV_FLAG_SIMT_ONLY, 2), ("f32", 0, 2)])
+def test_a_slot_given_twice_is_recorded(dtype, flags, Hkv):
+    """Two sequences of one call on one slot: recorded (every access stays inside the store);
+    what is allowed, a slot read for several or read and written for one, is not."""
+    dt = DT[dtype][0]
+    n, m = 300, 200
+    q, k, v, do = _rows(n, (2 * Hkv, Hkv, Hkv, 2 * Hkv), 64, dt, False, 1)
+    dev = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    cu = torch.arange(m + 1, device="cuda")
+    ids = list(range(m))
+    last = ids[:-1] + [3]                        # the last sequence's is the fourth's
+    other = [-1] * (m - 1) + [7]                 # the last starts from what the eighth writes
+    with Store(dtype, 2 * Hkv, Hkv, 64, m, flags=flags) as c:
+        def check(bad):
+            if not bad:
+                return B.pkv_lin_check(c.lin)
+            with pytest.raises(B.PkvError, match="two sequences"):
+                B.pkv_lin_check(c.lin)
+        for start, end, bad in ((None, ids, False), (ids, ids, False), ([5] * m, None, False), (None, last, True), (other, ids, True),
+                                (other, [-1] * m, False)):
+            start, end = (None if x is None else dev(x) for x in (start, end))
+            B.pkv_lin_attn_fwd(c.lin, q, k, v, torch.empty_like(q), n, None, B.lin_batch(m, cu, start, end))
+            check(bad)
+        for start, end, bad in ((ids, ids, False), (ids, None, False), (last, None, True), ([5] * m, None, True), (ids, other, True)):
+            start, end = (None if x is None else dev(x) for x in (start, end))
+            g = [torch.empty_like(t) for t in (q, k, v)]
+            B.pkv_lin_attn_bwd(c.lin, q, k, v, do, *g, n, None, B.lin_batch(m, cu, start, end))
+            check(bad)
+        for slots, bad in ((ids, False), (last, True), ([-1] * m, False), ([0, -1] + [9] * (m - 2), True)):
+            B.pkv_lin_attn_step(c.lin, q[:m], k[:m], v[:m], torch.empty_like(q[:m]), m, None, dev(slots))
+            check(bad)
+
+
 @pytest.mark.parametrize("dtype,flags", [("bf16", 0), ("bf16", B.PKV_FLAG_SIMT_ONLY), ("f32", 0)])
 def test_graphs_streams_and_repeats(dtype, flags):
     """The same bits on another stream, from a captured graph replayed on new inputs, and again."""
