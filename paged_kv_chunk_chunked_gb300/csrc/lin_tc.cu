@@ -148,10 +148,20 @@ __device__ __forceinline__ void split3(f32x2 p, uint32_t& hi, uint32_t& mid, uin
     lo = cut();
 }
 
-// Work laid end to end, cut into one length a CTA: `per` each, one more for the first `more`.
+// Heads of the rows kernel for each CTA: laid end to end and cut into one length a CTA,
+// `per` each, one more for the first `more`; or (units > 0) whole units of g heads, every
+// grid-th from the last one down: all CTAs are at neighbouring chunks then, those first
+// whose states the scan wrote last. The former where a unit more or less would show; the
+// latter from 8 units a CTA on (16 heads of 32768 rows: 284.6 us instead of 289.0).
 struct Cut {
-    int per, more;
-    __device__ __forceinline__ int begin(unsigned cta) const { return per * (int)cta + min((int)cta, more); }
+    int per, more, units;
+    __device__ __forceinline__ int begin(int g) const {
+        return units ? 0 : per * (int)blockIdx.x + min((int)blockIdx.x, more);
+    }
+    __device__ __forceinline__ int end(int g) const {
+        return units ? (units - 1 - (int)blockIdx.x) / (int)gridDim.x * g + g : begin(g) + per + ((int)blockIdx.x < more);
+    }
+    __device__ __forceinline__ int unit(int q) const { return units ? units - 1 - (int)(blockIdx.x + q * gridDim.x) : q; }
 };
 
 // The units of a CTA, chunks of a KV head: numbers blockIdx.x, + gridDim.x, ...; a
@@ -174,6 +184,7 @@ struct PartWalk {
             const int u = both && !grad ? i - per_kind : i;
             f = u / a.Hkv;
             h = u - f * a.Hkv;
+            if (!both) f = a.n_chunks - 1 - f;   // the scan begins with the sums that were written last
             if (!lin_chunk<kL>(a, cuts, f, c)) continue;
             ++it;
             return true;
@@ -483,7 +494,10 @@ constexpr int kScanThreads = 128, kScanAhead = 16;
 // that multiply by them get them in bf16. A thread owns four elements all along
 // (so slot_in may be slot_out) and has kScanAhead chunks' sums on their way at once:
 // what bounds the scan is the latency of these rounds and of what comes before them,
-// which overlaps the kernel before where an SM has room beside it.
+// which overlaps the kernel before where an SM has room beside it. Past L2's size HBM bounds
+// it (16 heads of 32768 rows of d 128: 75 us for 402 MB; 88 with the sums written in the
+// scan's own order and these loads and stores unmarked). More chunks at once, or each next
+// one asked for as one is used up, were slower: up to 145 us.
 template <int D>
 __global__ void __launch_bounds__(kScanThreads, 5) lin_scan_bf16_kernel(const LinArgs a) {
     constexpr int V = D * D / 4;
@@ -517,13 +531,13 @@ __global__ void __launch_bounds__(kScanThreads, 5) lin_scan_bf16_kernel(const Li
         const float4* p = in;
 #pragma unroll
         for (int u = 0; u < kScanAhead; ++u) {
-            if (u < m) x[u] = __ldcs(p);
+            if (u < m) x[u] = __ldcg(p);
             p += step;
         }
 #pragma unroll
         for (int u = 0; u < kScanAhead; ++u)
             if (u < m) {
-                *out = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+                __stcs(out, make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w)));
                 out += step;
                 const float l = i + u == (grad ? 0 : nc - 1) ? ltail : lfull;
                 s.x = fmaf(l, s.x, x[u].x);
@@ -563,19 +577,21 @@ struct RowsBarriers {
 // group), each role of the kernel walking them for itself.
 struct HeadWalk {
     const LinArgs& a;
-    int idx, end, unit = -1;
-    int g, it = -1, pair = -1, f = 0, h = 0, head = 0;
+    Cut cut;
+    int g, idx, end, run = -1;                   // run: of g numbers
+    int it = -1, pair = -1, f = 0, h = 0, head = 0;
     bool first = false, live = false;
     LinChunk c{};
     const LinCuts* cuts;
 
-    __device__ __forceinline__ HeadWalk(const LinArgs& args, int from, int to, const LinCuts* first)
-        : a(args), idx(from - 1), end(to), g(args.Hq / args.Hkv), cuts(first) {}
+    __device__ __forceinline__ HeadWalk(const LinArgs& args, Cut c, const LinCuts* first)
+        : a(args), cut(c), g(args.Hq / args.Hkv), idx(c.begin(g) - 1), end(c.end(g)), cuts(first) {}
     // The next head: it counts heads, pair (chunk, KV head)s; first: the first head of its pair here.
     __device__ __forceinline__ bool next() {
         while (++idx < end) {
-            if (unit < 0 || idx >= (unit + 1) * g) {
-                unit = idx / g;
+            if (run < 0 || idx >= (run + 1) * g) {
+                run = idx / g;
+                const int unit = cut.unit(run);
                 f = unit / a.Hkv;
                 h = unit - f * a.Hkv;
                 live = lin_chunk<kL>(a, cuts, f, c);
@@ -585,11 +601,11 @@ struct HeadWalk {
                 first = false;
             }
             if (!live) {
-                idx = (unit + 1) * g - 1;
+                idx = (run + 1) * g - 1;
                 continue;
             }
             ++it;
-            head = h * g + (idx - unit * g);
+            head = h * g + (idx - run * g);
             return true;
         }
         return false;
@@ -649,7 +665,7 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
-    HeadWalk w(a, cut.begin(blockIdx.x), cut.begin(blockIdx.x + 1), &cuts);
+    HeadWalk w(a, cut, &cuts);
     bool more = w.next();
     launch_dependents();
     const uint32_t tmem = B.tmem_base;
@@ -1226,10 +1242,10 @@ template <int D, bool GRAD> cudaError_t rows(const LinArgs& a, cudaStream_t s, s
         !rows_map(&r, GRAD ? a.k : a.v, a.Hkv, a, kL, why) || !states_map(&st, a.sbf, a, why) ||
         !half_map(&out, GRAD ? a.dq : a.o, a.Hq, a, why))
         return cudaErrorInvalidValue;
-    const int heads = a.n_chunks * a.Hq, grid = std::min(heads, sm_count());
+    const int heads = a.n_chunks * a.Hq, units = a.n_chunks * a.Hkv, grid = std::min(heads, sm_count());
     ProfScope ps("lin_rows_tc_kernel", s);
     return launch_after(lin_rows_tc_kernel<D, GRAD>, dim3(grid), kRowsThreads, RowsLayout<D>::kSmem, s, x, c, r, st,
-                        out, a, Cut{heads / grid, heads % grid});
+                        out, a, Cut{heads / grid, heads % grid, units >= 8 * grid ? units : 0});
 }
 
 template <int D> cudaError_t cols(const LinArgs& a, cudaStream_t s, std::string* why) {

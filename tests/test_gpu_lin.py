@@ -320,6 +320,33 @@ def test_a_slot_given_twice_is_recorded(dtype, flags, Hkv):
             check(bad)
 
 
+@pytest.mark.parametrize("Hq,Hkv,d,n,dtype", [(16, 16, 128, 10000, "bf16"), (32, 16, 64, 11111, "bf16"), (3, 1, 64, 5000, "f32")])
+def test_a_long_call_equals_its_pieces(Hq, Hkv, d, n, dtype):
+    """Pieces of whole chunks, their states handed on through slots: the same sums in the same
+    order, so the same bits, however the work is laid out over the GPU."""
+    q, k, v, do = _rows(n, (Hq, Hkv, Hkv, Hq), d, DT[dtype][0], False, 5)
+    cuts = [0, 1280, 1408, 4096, n]
+    g2 = _decays("spread", Hkv).cuda()
+    i = torch.arange(len(cuts), dtype=torch.int32, device="cuda")
+    got = []
+    for ends in ([0, n], cuts):
+        with Store(dtype, Hq, Hkv, d, len(cuts)) as c:
+            gen = torch.Generator(device="cuda").manual_seed(9)
+            c.state[0] = torch.randn(Hkv, d, d, device="cuda", generator=gen)
+            c.dstate[len(ends) - 1] = torch.randn(Hkv, d, d, device="cuda", generator=gen)
+            o, dq, dk, dv = (torch.empty_like(t) for t in (q, q, k, v))
+            spans = list(enumerate(zip(ends, ends[1:])))
+            batch = lambda x: B.lin_batch(1, None, i[x:x + 1], i[x + 1:x + 2])  # noqa: E731
+            for x, (a, b) in spans:
+                B.pkv_lin_attn_fwd(c.lin, q[a:b], k[a:b], v[a:b], o[a:b], b - a, g2, batch(x))
+            for x, (a, b) in reversed(spans):
+                B.pkv_lin_attn_bwd(c.lin, q[a:b], k[a:b], v[a:b], do[a:b], dq[a:b], dk[a:b], dv[a:b], b - a, g2, batch(x))
+            B.pkv_lin_check(c.lin)
+            got.append([o, dq, dk, dv, c.state[len(ends) - 1].clone(), c.dstate[0].clone()])
+    for name, a, b in zip(("o", "dq", "dk", "dv", "state", "dstate"), *got):
+        assert torch.equal(a, b), name
+
+
 @pytest.mark.parametrize("dtype,flags", [("bf16", 0), ("bf16", B.PKV_FLAG_SIMT_ONLY), ("f32", 0)])
 def test_graphs_streams_and_repeats(dtype, flags):
     """The same bits on another stream, from a captured graph replayed on new inputs, and again."""
