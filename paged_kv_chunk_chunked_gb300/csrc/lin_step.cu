@@ -5,8 +5,9 @@
 // head for 4 d^2 multiply-adds per query head), so HBM bounds it. A CTA takes 32
 // columns of one state, a thread four columns of D / 16 rows, held in registers
 // from the load to the last query head's product. Loads and stores are marked as
-// streaming: 187 states of 4 heads of d 128 take 20.8 us so (4.8 TB/s), 24.8 us not.
-// More or fewer CTAs an SM (by registers) were slower.
+// streaming: 187 states of 4 heads of d 128 take 21.5 us so (4.6 TB/s), 25 us not.
+// More or fewer CTAs an SM (by registers) were slower. One CTA of a row looks for its slot
+// in the rows before (0.7 of the 21.5 us).
 #include <cuda_bf16.h>
 
 #include "lin.cuh"

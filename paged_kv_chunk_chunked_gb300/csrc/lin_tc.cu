@@ -61,7 +61,7 @@ template <int D> __device__ __forceinline__ void load_half(uint32_t tmem, float 
 
 // The warp's 32 rows to global memory: by TMA through `stage` (a thread's own row
 // in stores of its own, 32 rows apart from each other, kept the shared-memory
-// pipeline from the tensor core: rows of 24 us became 20), but row by row where the
+// pipeline from the tensor core: the rows kernel's 24 us became 20), but row by row where the
 // sequence ends inside. left: rows of the chunk from this warp's first on; at: (column, head, row).
 template <int D>
 __device__ __forceinline__ void store_half(const uint32_t (&o)[D / 4], const CUtensorMap* map, uint8_t* stage, int lane, int left,
@@ -200,8 +200,11 @@ struct PartWalk {
 // 64 rows of both operands at a time (TMA). Eight warps weight A, split it into three
 // terms and put them into tensor memory, transposed: a thread has one column of A
 // (a lane) and 32 rows. Warp 1 issues the products, R (MN-major) from shared memory;
-// four warps write sums out. With A's terms in shared memory too, the products'
-// and the weighting's traffic there was the bound: 0.85 us a stage instead of 0.45.
+// four warps write sums out. With A's terms in shared memory too, the products' and the
+// weighting's traffic there was the bound. Now the weighting is, by its arithmetic: it is
+// four fifths of a stage's time, and 16 warps at it were no faster than eight (mean of a
+// training chunk's two launches 19.5 us, 18.6 with eight). 4096 rows, 28/4 heads of d 128:
+// 10 us, with q do^T 23; 32768 rows of 16 heads: 84 us for 537 MB (6.4 TB/s, HBM's bound).
 // The sums of q do^T have an accumulator for the large term and one for the small
 // ones: each addition rounds in fp32, and the small terms' would triple their number;
 // those of k v^T, of 128 rows alone, have one, and two units alternate between both.
@@ -622,6 +625,9 @@ struct HeadWalk {
 // made each second product wait for the other group's output to be read: 2.1 us a head.)
 // Weights l^(i-j): for 32 x 32 blocks under the diagonal l^(i - 32 b - 31) (one per
 // row and block) times l^(31 - (j - 32 b)), both with exponents >= 0; on it from a table.
+// A group takes about 3 us from a head to its next, a chain of two products, their reading
+// and writing in tensor memory, and the store. 4096 rows, 28/4 heads of d 128: 20 us (six
+// heads a CTA; 67 MB); 32768 rows of 16 heads, a state for each: 120 us for 671 MB (5.6 TB/s).
 template <int D, bool GRAD>
 __global__ void __launch_bounds__(kRowsThreads, 1)
 lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_c,
@@ -926,7 +932,9 @@ struct ColsBarriers {
 // columns [0, 128) for one group of eight warps (dV), V dO^T in [128, 256) for
 // another (dK), each with an issuing warp of its own; their weighted bf16 values
 // overwrite them as A operands. dV and dK stay in tensor memory over all heads; they start as
-// K G and V G^T, scaled there by l^(m-1-j) / scale.
+// K G and V G^T, scaled there by l^(m-1-j) / scale. What bounds it is a head's chain of
+// score product, weighting and second product, 2 us, in each of a unit's g heads: 4096 rows,
+// 28/4 heads of d 128 (128 CTAs of seven heads) take 23 us.
 template <int D>
 __global__ void __launch_bounds__(kColsThreads, 1)
 lin_cols_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
