@@ -539,7 +539,7 @@ pkv_status pkv_lin_check(pkv_lin* lin);
  * sequence is left out, others of the call may come out wrong; the slot counts
  * as -1). A slot must not be written for
  * two sequences of a call, nor be written for one and read for another (recorded
- * too; its state is then undefined). Several sequences may start from one slot in
+ * too, in calls of up to 8192 sequences; its state is then undefined). Several sequences may start from one slot in
  * the forward, not in the backward, where each writes a gradient of its own. */
 typedef struct pkv_lin_batch {
     const int64_t* cu;         /* device int64 [n_seq + 1], or NULL: one sequence, all rows */
@@ -573,7 +573,7 @@ pkv_status pkv_lin_attn_bwd(pkv_lin* lin, const void* q, int64_t q_stride, const
 /* One token for each of n sequences: row i advances the state of slot slots[i]
  * (device int32 [n]) in place and writes o's row i. A row with slot -1 is
  * padding: its o is left as it was. No slot may appear twice (recorded for
- * pkv_lin_check; both rows and the state are then undefined). */
+ * pkv_lin_check if n <= 8192; both rows and the state are then undefined). */
 pkv_status pkv_lin_attn_step(pkv_lin* lin, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                              const void* v, int64_t v_stride, void* o, int64_t o_stride, int64_t n,
                              const float* log_decay, const int32_t* slots, void* stream);

@@ -79,7 +79,7 @@ struct LinChunk {
     int rows;                        // 1 .. L
 };
 
-// The first 32 sequences' rows: kernels that look many chunks up load them once, into
+// The sequences' rows, of up to 32: kernels that look many chunks up load them once, into
 // shared memory (registers are short where it is read).
 struct LinCuts {
     int64_t lo[32], hi[32];
@@ -93,32 +93,34 @@ struct LinCuts {
 };
 
 // The rows of chunk number f; false: there is no such chunk. Called by whole warps.
-// first: the first sequences' rows, or null.
+// first: the sequences' rows (used if they are all there), or null.
 template <int L> __device__ __forceinline__ bool lin_chunk(const LinArgs& a, const LinCuts* first, int f, LinChunk& c) {
     int64_t b = 0, lo = 0, hi = a.n;
     if (a.cu) {
-        // The last sequence whose chunks start at or before f (numbers ascend with b): lane x
-        // holds sequence b0 + x, so one round of loads finds it and its rows.
+        // The last sequence whose chunks start at or before f (numbers ascend with b): narrowed
+        // down to 32 neighbours by 32 probes at a time, then found among them with its rows.
         const int lane = threadIdx.x % 32;
-        b = -1;
-        for (int64_t b0 = 0; b0 < a.n_seq; b0 += 32) {
-            int64_t l = 0, r = 0;
-            if (first && b0 == 0) {
-                l = first->lo[lane];
-                r = first->hi[lane];
-            } else if (b0 + lane < a.n_seq) {
-                l = a.cu[b0 + lane];
-                r = a.cu[b0 + lane + 1];
-            }
-            const int k = __popc(__ballot_sync(0xffffffffu, b0 + lane < a.n_seq && l / L + b0 + lane <= f));
-            if (k > 0) {
-                b = b0 + k - 1;
-                lo = __shfl_sync(0xffffffffu, l, k - 1);
-                hi = __shfl_sync(0xffffffffu, r, k - 1);
-            }
-            if (k < 32) break;
+        int64_t len = a.n_seq;
+        while (len > 32) {
+            const int64_t step = (len + 31) / 32, x = b + lane * step;
+            const int k = __popc(__ballot_sync(0xffffffffu, lane * step < len && a.cu[x] / L + x <= f));
+            if (k == 0) return false;
+            b += (k - 1) * step;
+            len = min64(step, len - (k - 1) * step);
         }
-        if (b < 0) return false;
+        int64_t l = 0, r = 0;
+        if (first && a.n_seq <= 32) {
+            l = first->lo[lane];
+            r = first->hi[lane];
+        } else if (lane < len) {
+            l = a.cu[b + lane];
+            r = a.cu[b + lane + 1];
+        }
+        const int k = __popc(__ballot_sync(0xffffffffu, lane < len && l / L + b + lane <= f));
+        if (k == 0) return false;
+        lo = __shfl_sync(0xffffffffu, l, k - 1);
+        hi = __shfl_sync(0xffffffffu, r, k - 1);
+        b += k - 1;
     }
     if (!lin_good(a, lo, hi)) return false;
     const int64_t off = ((int64_t)f - (lo / L + b)) * L;
@@ -146,14 +148,17 @@ __device__ __forceinline__ int64_t lin_slot(const LinArgs& a, const int32_t* slo
 }
 
 // By all threads of a CTA, for one sequence: records whether `mine`, which sequence b
-// writes, is written for one before it or read for any other (`read` may be null).
+// writes, is written for one before it or read for any other (`read` may be null). In calls
+// of many sequences, where looking at all pairs would cost more than the states, it is left out.
+constexpr int64_t kCheckedSeqs = 8192;
 __device__ __forceinline__ void lin_check_alone(const LinArgs& a, const int32_t* written, const int32_t* read, int64_t b, int64_t mine,
                                                 int64_t n) {
-    if (mine < 0) return;
+    if (mine < 0 || n > kCheckedSeqs) return;
     bool twice = false;
-    for (int64_t j = threadIdx.x; j < b; j += blockDim.x) twice |= written[j] == mine;
-    if (read)
-        for (int64_t j = threadIdx.x; j < n; j += blockDim.x) twice |= j != b && read[j] == mine;
+    for (int j = threadIdx.x; j < n; j += blockDim.x) {
+        if (j < b) twice |= written[j] == mine;
+        if (read && j != b) twice |= read[j] == mine;
+    }
     if (twice) report_error(a.err, kErrSlotTwice);
 }
 

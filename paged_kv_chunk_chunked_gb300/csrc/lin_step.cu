@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kThreads) lin_step_kernel(LinArgs a) {
             Elem<T>::store(orow + e * D + c, (red[0][e][c] + red[1][e][c]) + (red[2][e][c] + red[3][e][c]));
         }
     }
-    if (h == 0 && c0 == 0) lin_check_alone(a, a.slots, nullptr, i, slot, 0);
+    if (h == 0 && c0 == 0) lin_check_alone(a, a.slots, nullptr, i, slot, a.n);
 }
 
 template <typename T, int D> cudaError_t step(const LinArgs& a, cudaStream_t s) {

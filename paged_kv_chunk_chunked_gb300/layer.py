@@ -299,6 +299,11 @@ class LinearRecurrentBlock:
             self._batches[c] = tuple(B.lin_batch(m, cu, at, dev(out, torch.int32)) for out in (slot_out, back))
         return self._batches[c]
 
+    def _check_rows(self, c: int, x):
+        s, e = self.w.chunk_range(c)
+        if len(x) != max(0, e - s):
+            raise ValueError(f"chunk {c} has {max(0, e - s)} rows, got {len(x)}")
+
     def _qkv(self, h):
         w = self.w
         return [(h @ self.weights[name]).view(len(h), -1, w.d) for name in ("wq", "wk", "wv")]
@@ -308,6 +313,7 @@ class LinearRecurrentBlock:
         stream = torch.cuda.current_stream()
         ys = []
         for c, x in enumerate(xs):
+            self._check_rows(c, x)
             h, _, _ = self.norm.forward(x, stream)
             q, k, v = self._qkv(h)
             a = torch.empty_like(q)
@@ -320,11 +326,14 @@ class LinearRecurrentBlock:
         """Chunks in reverse, on the current stream, after ``forward`` of the same inputs
         (activations are recomputed, states are not). Returns every chunk's input
         gradient and the weight gradients (float32)."""
+        if len(xs) != self.w.n_chunks or len(dys) != len(xs):
+            raise ValueError(f"the backward goes over all {self.w.n_chunks} chunks, got {len(xs)} and {len(dys)}")
         W, stream = self.weights, torch.cuda.current_stream()
         g = {n: torch.zeros(t.shape, dtype=torch.float32, device="cuda") for n, t in W.items()}
         dxs = [None] * len(xs)
         for c in reversed(range(len(xs))):
             x, dy, n = xs[c], dys[c], len(xs[c])
+            self._check_rows(c, x)
             batch, back = self._batch(c)
             h, *stats = self.norm.forward(x, stream)
             q, k, v = self._qkv(h)

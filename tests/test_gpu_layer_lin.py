@@ -146,3 +146,19 @@ def test_bad_documents_are_refused():
     for starts in ([], [1, 5], [0, 5, 5], [0, 256]):
         with pytest.raises(ValueError):
             LinearRecurrentBlock(w, 32, None, doc_starts=starts)
+
+
+def test_chunks_of_other_lengths_are_refused():
+    w = synth.workload("tiny_dense_f32")
+    blk = LinearRecurrentBlock(w, 32, None)
+    try:
+        xs = [torch.zeros(w.C, 32, device="cuda") for _ in range(w.n_chunks)]
+        for bad in ([xs[0][:-1]], [xs[0], torch.cat(xs[:2])], xs + [xs[0]]):
+            with pytest.raises(ValueError, match="rows"):
+                blk.forward(bad)
+        blk.forward(xs)
+        with pytest.raises(ValueError, match="all"):
+            blk.backward(xs[:-1], xs[:-1])
+        blk.forward(xs[:2])                          # a beginning is allowed
+    finally:
+        blk.close()

@@ -347,6 +347,41 @@ def test_a_long_call_equals_its_pieces(Hq, Hkv, d, n, dtype):
         assert torch.equal(a, b), name
 
 
+@pytest.mark.parametrize("dtype,m", [("bf16", 33), ("bf16", 1025), ("f32", 1100), ("bf16", 9000)])
+def test_many_sequences_equal_each_by_itself(dtype, m):
+    """More sequences than a warp has lanes, or than its square: the bits of calls of 30 at a time
+    (every chunk of every sequence is found), both ways; 9000 by a sample of those."""
+    g = torch.Generator().manual_seed(m)
+    lens = torch.randint(0, 5, (m,), generator=g)
+    lens[torch.randint(0, m, (3,), generator=g)] = 300
+    cu = torch.cat([torch.zeros(1, dtype=torch.int64), lens.cumsum(0)]) + 2
+    n = int(cu[-1]) + 3
+    Hq, Hkv, d = 2, 1, 64
+    q, k, v, do = _rows(n, (Hq, Hkv, Hkv, Hq), d, DT[dtype][0], False, 6)
+    g2 = _decays("spread", Hkv).cuda()
+    ids = torch.arange(m, dtype=torch.int32, device="cuda")
+    starts = list(range(0, m, 30)) if m < 2000 else [0, 1020, 4980, 8970]
+    with Store(dtype, Hq, Hkv, d, m) as c:
+        first = torch.randn(m, Hkv, d, d, device="cuda")
+        got = []
+        for calls in ([(0, m)], [(b, min(m, b + 30)) for b in starts]):
+            c.state.copy_(first)
+            c.dstate.copy_(first)
+            o, dq, dk, dv = (torch.full_like(t, 3.0) for t in (q, q, k, v))
+            for a, b in calls:
+                batch = B.lin_batch(b - a, cu[a:b + 1].cuda(), ids[a:b], ids[a:b])
+                B.pkv_lin_attn_bwd(c.lin, q, k, v, do, dq, dk, dv, n, g2, batch)
+                B.pkv_lin_attn_fwd(c.lin, q, k, v, o, n, g2, batch)
+            B.pkv_lin_check(c.lin)
+            got.append([o, dq, dk, dv, c.state.clone(), c.dstate.clone()])
+        for x, (a, b) in enumerate(zip(*got)):
+            for s in starts:
+                e = min(m, s + 30)
+                at = slice(s, e) if x >= 4 else slice(int(cu[s]), int(cu[e]))
+                assert torch.equal(a[at], b[at]), (x, s)
+            assert x >= 4 or ((a[:2] == 3.0).all() and (a[int(cu[-1]):] == 3.0).all())
+
+
 @pytest.mark.parametrize("dtype,flags", [("bf16", 0), ("bf16", B.PKV_FLAG_SIMT_ONLY), ("f32", 0)])
 def test_graphs_streams_and_repeats(dtype, flags):
     """The same bits on another stream, from a captured graph replayed on new inputs, and again."""
