@@ -62,13 +62,11 @@ template <int D> __device__ __forceinline__ void load_half(uint32_t tmem, float 
 // The warp's 32 rows to global memory: by TMA through `stage` (a thread's own row
 // in stores of its own, 32 rows apart from each other, kept the shared-memory
 // pipeline from the tensor core: the rows kernel's 24 us became 20), but row by row where the
-// sequence ends inside. left: rows of the chunk from this warp's first on; at: (column, head, row).
+// sequence ends inside. left: rows of the chunk from this warp's first on. The stage is free.
 template <int D>
 __device__ __forceinline__ void store_half(const uint32_t (&o)[D / 4], const CUtensorMap* map, uint8_t* stage, int lane, int left,
                                            int column, int head, int64_t row, const LinRows& out) {
     if (left >= 32) {
-        if (lane == 0) tc::bulk_wait_read();     // the last box has left the stage
-        __syncwarp();
 #pragma unroll
         for (int v = 0; v < D / 16; ++v)
             *reinterpret_cast<uint4*>(stage + swizzled<D>(lane * D + v * 16)) = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
@@ -887,6 +885,8 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             tc::tmem_wait_st();
             tc::tc_fence_before();
             tc::mbar_arrive(&B.p_full[wg]);
+            if (lane == 0) tc::bulk_wait_read();     // the last head's boxes have left the stages
+            __syncwarp();
             ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.o_full[wg], 1, a.wait_err));
             if (!ok) continue;
             tc::tc_fence_after();
