@@ -676,56 +676,68 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     if (warp == 0) {
         // ------------------------------------------------------------ loads
         bool waited = false;
-        int n_x = 0, n_pair = 0, n_r = 0;
+        int n_x = 0, n_c = 0, n_s = 0, n_r = 0;
+        auto tiles = [&](uint32_t at, const CUtensorMap* map, uint64_t* full, int head) {
+            if (lane == 0) {
+                tc::mbar_arrive_expect_tx(full, L::kTile);
+#pragma unroll
+                for (int b = 0; b < D / 64; ++b) tc::tma_load_3d(smem + at + b * 16384, map, full, 64 * b, head, (int)w.c.row0);
+            }
+        };
+        auto load_x = [&]() {
+            tiles(L::kOffX + (w.it & 1) * L::kTile, &map_x, &B.x_full[w.it & 1], w.head);
+            n_x = w.it + 1;
+        };
+        auto load_s = [&](int state) {
+            if (lane == 0) {
+                tc::mbar_arrive_expect_tx(&B.st_full, L::kState);
+#pragma unroll
+                for (int b = 0; b < D / 64; ++b) tc::tma_load_2d(smem + L::kOffS + b * (D * 128), &map_s, &B.st_full, 64 * b, state * D);
+            }
+            ++n_s;
+        };
+        auto load_c = [&]() {
+            tiles(0, &map_c, &B.c_full, w.h);
+            ++n_c;
+        };
+        auto load_r = [&]() {
+            tiles(L::kOffR, &map_r, &B.r_full, w.h);
+            ++n_r;
+        };
+        // Until the states are there (the operands are older than the kernels before): the first
+        // pair's C and R and the first two heads' X, if both are that pair's.
+        if (more) {
+            const int state = w.f * a.Hkv + w.h;
+            load_c();
+            load_x();
+            load_r();
+            if ((more = w.next()) && !w.first) {
+                load_x();
+                more = w.next();
+            }
+            wait_for_kernels();
+            waited = true;
+            load_s(state);
+        }
         for (; more; more = w.next()) {
-            const int row = (int)w.c.row0;
             if (w.first) {
-                if (w.pair >= 1 && !tc::warp_wait(&B.pair_empty, (w.pair - 1) & 1, a.wait_err)) break;
-                if (lane == 0) {
-                    tc::mbar_arrive_expect_tx(&B.c_full, L::kTile);
-#pragma unroll
-                    for (int b = 0; b < D / 64; ++b) tc::tma_load_3d(smem + b * 16384, &map_c, &B.c_full, 64 * b, w.h, row);
-                }
+                if (!tc::warp_wait(&B.pair_empty, (w.pair - 1) & 1, a.wait_err)) break;
+                load_c();
             }
-            {
-                const int s = w.it & 1;
-                if (w.it >= 2 && !tc::warp_wait(&B.x_empty[s], ((w.it >> 1) - 1) & 1, a.wait_err)) break;
-                if (lane == 0) {
-                    tc::mbar_arrive_expect_tx(&B.x_full[s], L::kTile);
-#pragma unroll
-                    for (int b = 0; b < D / 64; ++b)
-                        tc::tma_load_3d(smem + L::kOffX + s * L::kTile + b * 16384, &map_x, &B.x_full[s], 64 * b, w.head, row);
-                }
-                n_x = w.it + 1;
-            }
+            if (w.it >= 2 && !tc::warp_wait(&B.x_empty[w.it & 1], ((w.it >> 1) - 1) & 1, a.wait_err)) break;
+            load_x();
             if (w.first) {
-                if (!waited) wait_for_kernels(); // the states; Q, K, V and dO are older than the kernels before
-                waited = true;
-                if (lane == 0) {
-                    tc::mbar_arrive_expect_tx(&B.st_full, L::kState);
-#pragma unroll
-                    for (int b = 0; b < D / 64; ++b)
-                        tc::tma_load_2d(smem + L::kOffS + b * (D * 128), &map_s, &B.st_full, 64 * b, (w.f * a.Hkv + w.h) * D);
-                }
-                n_pair = w.pair + 1;
-                if (w.pair >= 1 && !tc::warp_wait(&B.r_empty, (w.pair - 1) & 1, a.wait_err)) break;
-                if (lane == 0) {
-                    tc::mbar_arrive_expect_tx(&B.r_full, L::kTile);
-#pragma unroll
-                    for (int b = 0; b < D / 64; ++b)
-                        tc::tma_load_3d(smem + L::kOffR + b * 16384, &map_r, &B.r_full, 64 * b, w.h, row);
-                }
-                n_r = w.pair + 1;
+                load_s(w.f * a.Hkv + w.h);
+                if (!tc::warp_wait(&B.r_empty, (w.pair - 1) & 1, a.wait_err)) break;
+                load_r();
             }
         }
         if (!waited) wait_for_kernels();         // a kernel never ends before the one it may overlap
         // None of this CTA's copies may still be landing when it exits.
         if (lane == 0) {
             for (int i = max(0, n_x - 2); i < n_x; ++i) tc::drain_wait(&B.x_full[i & 1], (i >> 1) & 1);
-            if (n_pair > 0) {
-                tc::drain_wait(&B.c_full, (n_pair - 1) & 1);
-                tc::drain_wait(&B.st_full, (n_pair - 1) & 1);
-            }
+            if (n_c > 0) tc::drain_wait(&B.c_full, (n_c - 1) & 1);
+            if (n_s > 0) tc::drain_wait(&B.st_full, (n_s - 1) & 1);
             if (n_r > 0) tc::drain_wait(&B.r_full, (n_r - 1) & 1);
         }
     } else if (warp <= 2) {
@@ -763,9 +775,8 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             const int n = w.it >> 1;             // heads of this group before
             if (!tc::warp_wait(&B.c_full, w.pair & 1, a.wait_err)) break;
             if (!tc::warp_wait(&B.x_full[wg], n & 1, a.wait_err)) break;
-            if (n > 0 && !tc::warp_wait(&B.o_free[wg], (n - 1) & 1, a.wait_err)) break;
             tc::tc_fence_after();
-            if (leader) {
+            if (leader) {                        // (over the weights of the head before: its second product is ahead of this one)
                 const uint64_t dc = tc::sdesc(sm, 16, 1024);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
@@ -776,6 +787,7 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             }
             __syncwarp();
             if (!tc::warp_wait(&B.st_full, w.pair & 1, a.wait_err)) break;
+            if (n > 0 && !tc::warp_wait(&B.o_free[wg], (n - 1) & 1, a.wait_err)) break;
             tc::tc_fence_after();
             if (leader) {
                 const uint64_t ds = GRAD ? tc::sdesc(sm + L::kOffS, 16, 1024) : tc::sdesc(sm + L::kOffS, D * 128, 1024);
