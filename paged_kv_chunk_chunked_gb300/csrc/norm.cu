@@ -13,10 +13,14 @@
 // are better than many warps. In the backward a team keeps to one group of columns,
 // so that its share of dw and db stays in registers, and walks rows; a CTA's teams
 // add their shares in shared memory, a second kernel adds the CTAs', both in a fixed
-// order. 4096 rows of 3584 columns in bf16: forward 16.6 us (3.5 TB/s), backward 25.9 (3.4)
-// and 4.7 for the second kernel: issue slots (58% used) and the sums' latency bound them as
-// much as HBM. Rows of more than 8192 columns (bf16) do not fit the registers of a backward's
-// thread and are slower by their spills.
+// order. Rows of more columns than that holds have a backward of two kernels that read x
+// and dy twice.
+// Replayed on the same buffers (partly in L2), bf16: 4096 rows of 3584 columns forward
+// 11.8 us (5.0 TB/s), backward 24.3 (3.6 TB/s; 4.7 of it the second kernel); 28 groups of
+// 128 columns 12.0 and 23.2; 2048 rows of 16384 columns 45 and 90. Where rows come from HBM
+// the first pair takes 16.6 and 25 us. The sums' latency and issue slots (58% used)
+// bound them as much as HBM; a forward CTA that takes several rows and loads the next one
+// ahead was slower (13.2 us at best).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -32,8 +36,8 @@ namespace {
 constexpr int kThreads = 256;                    // of a CTA of lane teams
 constexpr int kMaxTeam = 512;                    // threads of a CTA of teams of warps, but for the widest rows
 // Rows that a team of the backward has on the way: 128 KB of x and dy at most, and none of single
-// elements or the widest rows.
-template <int EPV, int NV> constexpr int kAhead = EPV == 1 || NV * EPV == 32 ? 0 : 8 / NV;
+// elements.
+template <int EPV, int NV> constexpr int kAhead = EPV == 1 ? 0 : 8 / NV;
 constexpr int kBatch = 4;
 constexpr int64_t kMaxWidth = 32768, kMaxGrid = (int64_t(1) << 31) - 1;
 
@@ -148,6 +152,11 @@ template <typename W, int EPV> __device__ __forceinline__ void load_w(const void
     pairs<EPV>(f, x);
 }
 
+// The kernel that adds the shares of dw and db is launched as the one before it ends, and
+// waits for its writes (0.5 us sooner than an ordinary launch; started any earlier, it
+// slowed the other by 1.3 us).
+__device__ __forceinline__ void wait_for_kernels() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Sums of N values over a team of lanes.
 template <int N> __device__ __forceinline__ void lane_sum(float (&x)[N], int lanes) {
     for (int d = 1; d < lanes; d *= 2)
@@ -245,9 +254,9 @@ __global__ void __launch_bounds__(EPV == 1 && NV == 32 ? 1024 : kMaxTeam) layer_
 // own (no other thread reads them, so no barrier is needed): registers for one row
 // alone are in use, and with rows loaded to registers HBM idled during each row's sums.
 template <typename T, int EPV, int NV>
-__global__ void __launch_bounds__(NV * EPV == 32 ? 1024 : kMaxTeam) layer_norm_bwd_kernel(NormArgs a) {
+__global__ void __launch_bounds__(kMaxTeam, 1) layer_norm_bwd_kernel(NormArgs a) {
     constexpr int A = kAhead<EPV, NV>;
-    extern __shared__ uint4 ahead[];             // [A][2][NV][threads]; at the end float [2][width], the teams' shares
+    extern __shared__ uint4 ahead[];             // [A][2][NV][threads]; at the end float [teams][2][width], their shares
     __shared__ float red[2][32 * 2];             // rows in turn
     const int team = a.team, t = threadIdx.x % team, me = threadIdx.x / team, teams = blockDim.x / team;
     const int grp = blockIdx.y;
@@ -351,32 +360,119 @@ __global__ void __launch_bounds__(NV * EPV == 32 ? 1024 : kMaxTeam) layer_norm_b
         }
     }
     if (!a.part) return;
-    // The teams' shares, one team after another.
-    float* share = reinterpret_cast<float*>(ahead);
+    // The teams' shares, added in the order of the teams.
     const int64_t cols = (int64_t)a.groups * a.width;
-    float* pw = a.part + blockIdx.x * 2 * cols + c0;
-    for (int m = 0; m < teams; ++m) {
-        __syncthreads();
-        if (m != me) continue;
+    float *share = reinterpret_cast<float*>(ahead), *pw = a.part + blockIdx.x * 2 * cols + c0;
+    if (teams > 1) __syncthreads();              // every team is through with its copies
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            float gw[EPV], gb[EPV];
-            singles<EPV>(dw[v], gw);
-            singles<EPV>(db[v], gb);
+    for (int v = 0; v < NV; ++v) {
+        float gw[EPV], gb[EPV];
+        singles<EPV>(dw[v], gw);
+        singles<EPV>(db[v], gb);
+        const int c = (t + v * team) * EPV;
+        if (c >= a.width) continue;
+        float *ow = teams > 1 ? share + me * 2 * a.width + c : pw + c, *ob = teams > 1 ? ow + a.width : ow + cols;
 #pragma unroll
-            for (int e = 0; e < EPV; ++e) {
-                const int c = (t + v * team) * EPV + e;
-                if (c >= a.width) continue;
-                const float p = m ? share[c] + gw[e] : gw[e], q = m ? share[a.width + c] + gb[e] : gb[e];
-                if (m + 1 < teams) {
-                    share[c] = p;
-                    share[a.width + c] = q;
-                } else {
-                    pw[c] = p;
-                    pw[cols + c] = q;
-                }
+        for (int e = 0; e < EPV; ++e) {
+            ow[e] = gw[e];
+            ob[e] = gb[e];
+        }
+    }
+    if (teams == 1) return;
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * a.width; c += blockDim.x) {
+        float sum = share[c];
+        for (int m = 1; m < teams; ++m) sum += share[m * 2 * a.width + c];
+        pw[c < a.width ? c : cols + c - a.width] = sum;
+    }
+}
+
+// ---- backward of rows too wide for a thread's registers: dx by a CTA a (row, group), which
+// reads its row twice (the second time from L1 or L2), and the columns' sums by themselves,
+// from x and dy read again (2048 rows of 16384 columns in bf16 90 us, with the kernel
+// above and its spills 410; of 8191, by single elements, 80 and 596)
+template <typename T, int EPV> __global__ void __launch_bounds__(kMaxTeam) layer_norm_wide_dx_kernel(NormArgs a) {
+    __shared__ float red[2 * 32];
+    const int64_t unit = blockIdx.x, row = a.groups == 1 ? unit : unit / a.groups, c0 = (unit - row * a.groups) * a.width;
+    const T *x = static_cast<const T*>(a.x) + row * a.xs + c0, *dy = static_cast<const T*>(a.dy) + row * a.dys + c0;
+    T* dx = static_cast<T*>(a.dx) + row * a.dxs + c0;
+    const float mean = a.mean[unit], rstd = a.rstd[unit];
+    using P = Pk<EPV>;
+    constexpr int N = kPk<EPV>;
+    const P minus = both<P>(-mean), scale = both<P>(rstd);
+    auto run = [&](auto type) {
+        P s0 = both<P>(0.f), s1 = s0;
+#pragma unroll 4
+        for (int c = threadIdx.x * EPV; c < a.width; c += kMaxTeam * EPV) {
+            Raw<T, EPV> rx, rd;
+            rx.load(x + c);
+            rd.load(dy + c);
+            P f[N], d[N], w[N];
+            rx.widen(f);
+            rd.widen(d);
+            load_w<decltype(type), EPV>(a.w, c0 + c, 1.f, w);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const P u = mul2(d[e], w[e]);
+                s0 = add2(s0, u);
+                s1 = fma2(u, mul2(add2(f[e], minus), scale), s1);
             }
         }
+        float s[2] = {total(s0), total(s1)};
+        warps_sum<2>(s, kMaxTeam, 0, red);
+        const P m1 = both<P>(-s[0] * a.inv_width * rstd), m2 = both<P>(-s[1] * a.inv_width * rstd);
+#pragma unroll 4
+        for (int c = threadIdx.x * EPV; c < a.width; c += kMaxTeam * EPV) {
+            Raw<T, EPV> rx, rd;
+            rx.load(x + c);
+            rd.load(dy + c);
+            P f[N], d[N], w[N];
+            rx.widen(f);
+            rd.widen(d);
+            load_w<decltype(type), EPV>(a.w, c0 + c, 1.f, w);
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                d[e] = fma2(mul2(add2(f[e], minus), scale), m2, fma2(mul2(d[e], w[e]), scale, m1));
+            store<T, EPV>(dx + c, d);
+        }
+    };
+    if (a.w_f32) run(float());
+    else run(__nv_bfloat16());
+}
+
+// A thread has EPV columns (all groups' laid end to end) of rows blockIdx.y, + slots, ...
+template <typename T, int EPV> __global__ void __launch_bounds__(kThreads) layer_norm_wide_cols_kernel(NormArgs a) {
+    const int64_t cols = (int64_t)a.groups * a.width, c = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * EPV;
+    if (c >= cols) return;
+    const int grp = (int)(c / a.width);
+    using P = Pk<EPV>;
+    constexpr int N = kPk<EPV>;
+    P dw[N], db[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) dw[e] = db[e] = both<P>(0.f);
+    const T *x = static_cast<const T*>(a.x) + c, *dy = static_cast<const T*>(a.dy) + c;
+#pragma unroll 4
+    for (int64_t row = blockIdx.y; row < a.n; row += a.slots) {
+        Raw<T, EPV> rx, rd;
+        rx.load(x + row * a.xs);
+        rd.load(dy + row * a.dys);
+        const P minus = both<P>(-a.mean[row * a.groups + grp]), scale = both<P>(a.rstd[row * a.groups + grp]);
+        P f[N], d[N];
+        rx.widen(f);
+        rd.widen(d);
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            dw[e] = fma2(d[e], mul2(add2(f[e], minus), scale), dw[e]);
+            db[e] = add2(db[e], d[e]);
+        }
+    }
+    float gw[EPV], gb[EPV], *pw = a.part + blockIdx.y * 2 * cols + c;
+    singles<EPV>(dw, gw);
+    singles<EPV>(db, gb);
+#pragma unroll
+    for (int e = 0; e < EPV; ++e) {
+        pw[e] = gw[e];
+        pw[cols + e] = gb[e];
     }
 }
 
@@ -397,7 +493,8 @@ struct LaneTeam {
     }
 };
 
-template <typename T, int EPV> __global__ void __launch_bounds__(kThreads) layer_norm_lanes_fwd_kernel(NormArgs a) {
+// (CTAs an SM, by registers: 4096 rows of 28 groups of 128 took 17.6 us with two instead of 12.0, backward 44 with one)
+template <typename T, int EPV> __global__ void __launch_bounds__(kThreads, 3) layer_norm_lanes_fwd_kernel(NormArgs a) {
     const LaneTeam k(a);
     const int c = k.t * EPV;
     const bool mine = c < a.width && k.slot < a.slots;
@@ -461,7 +558,7 @@ template <typename T, int EPV> __global__ void __launch_bounds__(kThreads) layer
     }
 }
 
-template <typename T, int EPV> __global__ void __launch_bounds__(kThreads) layer_norm_lanes_bwd_kernel(NormArgs a) {
+template <typename T, int EPV> __global__ void __launch_bounds__(kThreads, 2) layer_norm_lanes_bwd_kernel(NormArgs a) {
     const LaneTeam k(a);
     const int c = k.t * EPV;
     const bool mine = c < a.width && k.slot < a.slots;
@@ -539,6 +636,7 @@ template <typename T, int EPV> __global__ void __launch_bounds__(kThreads) layer
 // dw and db from the slots' shares: 32 columns a CTA, 8 runs of slots, added in order.
 __global__ void __launch_bounds__(256) layer_norm_sum_kernel(NormArgs a) {
     __shared__ float red[8][33];
+    wait_for_kernels();
     const int64_t cols = (int64_t)a.groups * a.width;
     const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
     const int64_t c = (int64_t)blockIdx.x * 32 + tx;
@@ -580,11 +678,14 @@ template <typename T> Shape shape_of(int64_t width, bool vec, bool bwd) {
     return bwd ? shape_for(width / kVec<T>, 2, 32 / kVec<T>, kMaxTeam) : shape_for(width / kVec<T>, 4, 16, kMaxTeam);
 }
 
-// Lane teams, or CTAs, that share a group's rows: what fills the GPU, but eight rows each
-// at least (every share of dw and db is written and read again).
-int slots_of(int64_t n, int groups, const Shape& sh) {
-    const int64_t all = sh.lanes ? 152 * 4 * (kThreads / sh.team) : 152;
-    return (int)std::max<int64_t>(1, std::min<int64_t>((n + 7) / 8, (all + groups - 1) / groups));
+// Lane teams, or CTAs, that share a group's rows: what the GPU holds at once and no more
+// (4096 rows of 28 heads of 128 columns, backward: 23.7 us, with a few CTAs above it 33),
+// but four rows each at least (64 rows of 3584 columns: 10.0 us, with eight 11.9; two were no
+// faster), and in the backward 608 lane teams at most, as every share of dw and db is
+// written and read again (8192 rows of 128 columns: 16.3 us; with 2048 teams 21.7).
+int slots_of(int64_t n, int groups, const Shape& sh, bool bwd) {
+    const int64_t all = sh.lanes ? 152 * (bwd ? 2 : 3) * (kThreads / sh.team) / groups : (152 + groups - 1) / groups;
+    return (int)std::max<int64_t>(1, std::min({(n + 3) / 4, all, int64_t(bwd && sh.lanes ? 608 : 1 << 30)}));
 }
 
 template <typename T, int EPV, int NV> cudaError_t run(NormArgs& a, bool bwd, cudaStream_t s) {
@@ -596,15 +697,29 @@ template <typename T, int EPV, int NV> cudaError_t run(NormArgs& a, bool bwd, cu
             return cudaGetLastError();
         }
     }
-    if constexpr (NV * EPV <= 32) {              // (shape_of)
+    if constexpr (NV * EPV <= 16) {              // (wider ones: run_wide)
         const int teams = std::max(1, kMaxTeam / a.team), threads = teams * a.team;
         const size_t copies = (size_t)kAhead<EPV, NV> * 2 * NV * threads * 16;
-        const size_t smem = std::max(copies, teams > 1 && a.part ? 2 * a.width * sizeof(float) : 0);
+        const size_t smem = std::max(copies, teams > 1 && a.part ? teams * 2 * a.width * sizeof(float) : 0);
         static SmemGrant grant;
         const cudaError_t e = allow_smem(layer_norm_bwd_kernel<T, EPV, NV>, smem, grant);
         if (e != cudaSuccess) return e;
         layer_norm_bwd_kernel<T, EPV, NV><<<dim3(a.slots, a.groups), threads, smem, s>>>(a);
     }
+    return cudaGetLastError();
+}
+
+template <typename T, int EPV> cudaError_t run_wide(NormArgs& a, cudaStream_t s) {
+    if (a.dx) {
+        if (a.n * a.groups > kMaxGrid) return cudaErrorInvalidConfiguration;
+        ProfScope ps("layer_norm_wide_dx_kernel", s);
+        layer_norm_wide_dx_kernel<T, EPV><<<(unsigned)(a.n * a.groups), kMaxTeam, 0, s>>>(a);
+    }
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !a.part) return e;
+    ProfScope ps("layer_norm_wide_cols_kernel", s);
+    const int64_t tiles = ((int64_t)a.groups * a.width / EPV + kThreads - 1) / kThreads;
+    layer_norm_wide_cols_kernel<T, EPV><<<dim3((unsigned)tiles, a.slots), kThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -620,9 +735,10 @@ template <typename T, int EPV> cudaError_t run_lanes(NormArgs& a, bool bwd, cuda
 template <typename T> cudaError_t launch(NormArgs& a, bool bwd, bool vec, cudaStream_t s) {
     const Shape sh = shape_of<T>(a.width, vec, bwd);
     a.team = sh.team;
-    a.slots = slots_of(a.n, a.groups, sh);
+    a.slots = slots_of(a.n, a.groups, sh, bwd);
     a.inv_width = 1.f / (float)a.width;
     if (sh.lanes) return vec ? run_lanes<T, kVec<T>>(a, bwd, s) : run_lanes<T, 1>(a, bwd, s);
+    if (bwd && (vec ? sh.nv * kVec<T> > 16 : sh.nv > 8)) return vec ? run_wide<T, kVec<T>>(a, s) : run_wide<T, 1>(a, s);
     if (!vec) return sh.nv == 8 ? run<T, 1, 8>(a, bwd, s) : run<T, 1, 32>(a, bwd, s);
     if (sh.nv == 2) return run<T, kVec<T>, 2>(a, bwd, s);
     if (sh.nv == 4) return run<T, kVec<T>, 4>(a, bwd, s);
@@ -670,7 +786,7 @@ bool whole_vectors(const pkv_norm* norm) {
 
 int slots_for(const pkv_norm* norm, int64_t n, bool vec) {
     const Shape sh = norm->dtype == PKV_BF16 ? shape_of<__nv_bfloat16>(norm->width, vec, true) : shape_of<float>(norm->width, vec, true);
-    return slots_of(n, norm->groups, sh);
+    return slots_of(n, norm->groups, sh, true);
 }
 
 }  // namespace
@@ -744,8 +860,13 @@ pkv_status pkv_layer_norm_bwd(const void* dy, int64_t dy_stride, const void* x, 
         // (no rows: dw and db are sums of nothing)
         ProfScope ps("layer_norm_sum_kernel", cs);
         const int64_t cols = norm->groups * norm->width;
-        layer_norm_sum_kernel<<<dim3((unsigned)((cols + 31) / 32), 2), 256, 0, cs>>>(a);
-        const cudaError_t e = cudaGetLastError();
+        cudaLaunchConfig_t cfg{};
+        cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cfg.gridDim = dim3((unsigned)((cols + 31) / 32), 2); cfg.blockDim = dim3(256); cfg.stream = cs;
+        cfg.attrs = &attr; cfg.numAttrs = 1;
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, layer_norm_sum_kernel, a);
         return e == cudaSuccess ? PKV_OK : cuda_fail(e, "pkv_layer_norm_bwd: launch");
     });
 }

@@ -60,6 +60,12 @@ CASES = [
     ("f32", "f32", 2, 1, 32767, 0, True, 0.0),
     ("f32", "f32", 310, 1, 1024, 0, False, 0.0),
     ("bf16", "f32", 5000, 1, 16, 0, True, 0.0),
+    ("bf16", "f32", 70, 2, 5001, 3, True, 0.5),          # wide rows by single elements
+    ("bf16", "bf16", 600, 1, 8208, 0, True, 0.0),        # and by vectors, more rows than shares
+    ("f32", "f32", 9, 2, 8200, 4, True, 0.0),
+    ("f32", None, 30, 3, 4099, 0, False, 1.0),
+    ("bf16", "bf16", 3000, 1, 512, 0, True, 0.0),        # many teams a CTA
+    ("bf16", "bf16", 4096, 28, 128, 0, True, 0.0),
 ]
 
 
