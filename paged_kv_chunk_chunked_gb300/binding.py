@@ -185,6 +185,7 @@ def _torch_dtype(dtype):
 
 
 _HERE = contextlib.nullcontext()
+_DTYPES = {}                                  # by name
 
 
 def _device(stream):
@@ -588,12 +589,21 @@ def lin_batch(n_seq: int = 1, cu=None, slot_in=None, slot_out=None) -> pkv_lin_b
 
 
 def _array(x, name: str, dtype: str, n, dev):
-    """_typed of a call's array, on its device."""
-    if x is None or isinstance(x, int):
+    """_typed of a call's array, on its device. Usual ones pass by the first comparison."""
+    if x is None or x.__class__ is int:
         return x
+    if x.get_device() == dev and x.dtype is _dtypes()[dtype] and x.numel() == n and x.is_contiguous():
+        return x.data_ptr()
     if x.get_device() != dev:
         _on_device(x, dev)
     return _typed(x, name, dtype, n)
+
+
+def _dtypes():
+    if not _DTYPES:
+        import torch
+        _DTYPES.update(float32=torch.float32, int32=torch.int32, int64=torch.int64)
+    return _DTYPES
 
 
 def _lin_operands(lin, n, operands, dev):
