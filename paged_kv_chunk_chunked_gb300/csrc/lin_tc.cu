@@ -623,9 +623,12 @@ struct HeadWalk {
 // made each second product wait for the other group's output to be read: 2.1 us a head.)
 // Weights l^(i-j): for 32 x 32 blocks under the diagonal l^(i - 32 b - 31) (one per
 // row and block) times l^(31 - (j - 32 b)), both with exponents >= 0; on it from a table.
-// A group takes about 3 us from a head to its next, a chain of two products, their reading
-// and writing in tensor memory, and the store. 4096 rows, 28/4 heads of d 128: 20 us (six
-// heads a CTA; 67 MB); 32768 rows of 16 heads, a state for each: 120 us for 671 MB (5.6 TB/s).
+// A group takes about 2.4 us from a head to its next: X's load, a chain of two products and
+// their reading and writing in tensor memory, and the store. 4096 rows, 28/4 heads of d 128:
+// 20 us (six heads a CTA; 67 MB), of which the last 12 follow the states; 32768 rows of 16
+// heads, a state for each: 122 us for 671 MB (5.5 TB/s). X asked for further ahead, to L2 or
+// to a second tile a group, was slower (training chunk 95 us instead of 91), as those loads
+// come before the kernels that the states still wait for.
 template <int D, bool GRAD>
 __global__ void __launch_bounds__(kRowsThreads, 1)
 lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_c,
