@@ -2,12 +2,12 @@
 // place, o = scale q^T S for the group's query heads.
 //
 // A stream over the states: each is read and written once (8 d^2 bytes per KV
-// head for 4 d^2 multiply-adds per query head), so HBM bounds it. A CTA takes 32
+// head for 4 d^2 multiply-adds per query head), so HBM bounds it. A CTA takes 64
 // columns of one state, a thread four columns of D / 16 rows, held in registers
 // from the load to the last query head's product. Loads and stores are marked as
-// streaming: 187 states of 4 heads of d 128 take 21.5 us so (4.6 TB/s), 25 us not.
-// More or fewer CTAs an SM (by registers) were slower. One CTA of a row looks for its slot
-// in the rows before (0.7 of the 21.5 us).
+// streaming (4 us of 25). 187 states of 4 heads of d 128 take 20.1 us (4.9 TB/s) so,
+// with 32 columns a CTA 21.5, with 128 21.8; with four query heads at once 20.4. One
+// CTA of a row looks for its slot in the rows before (0.7 us).
 #include <cuda_bf16.h>
 
 #include "lin.cuh"
@@ -15,21 +15,21 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 128, kCols = 32, kRowGroups = 16;
-constexpr int kHeads = 16;                       // query heads whose partial sums shared memory holds at once
+constexpr int kCols = 64, kRowGroups = 16, kLanes = kCols / 4, kThreads = kLanes * kRowGroups, kWarps = kThreads / 32;
+constexpr int kHeads = 8;                        // query heads whose partial sums shared memory holds at once
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) lin_step_kernel(LinArgs a) {
     constexpr int R = D / kRowGroups;            // rows of a thread
-    static_assert(kThreads == 128 && kRowGroups * kCols / 4 == kThreads && D <= kThreads, "four warps' sums are added below");
+    static_assert(kLanes <= 32 && D % kCols == 0 && D <= kThreads, "a warp has whole rows of the columns; a thread loads one k");
     __shared__ float ks[D];
     __shared__ float qs[kHeads][D];
-    __shared__ float red[kThreads / 32][kHeads][kCols];
+    __shared__ float red[kWarps][kHeads][kCols];
     const int64_t i = blockIdx.x / (a.Hkv * (D / kCols));
     const int h = blockIdx.x / (D / kCols) % a.Hkv, c0 = blockIdx.x % (D / kCols) * kCols;
     const int64_t slot = lin_slot(a, a.slots, i);
     if (slot < 0) return;
-    const int tid = threadIdx.x, tx = tid % 8, rg = tid / 8;
+    const int tid = threadIdx.x, tx = tid % kLanes, rg = tid / kLanes;
     float4* S = reinterpret_cast<float4*>(a.state + ((size_t)slot * a.Hkv + h) * D * D + (size_t)rg * R * D + c0) + tx;
     float4 s[R];
 #pragma unroll
@@ -62,17 +62,20 @@ __global__ void __launch_bounds__(kThreads) lin_step_kernel(LinArgs a) {
                 o.z = fmaf(q, s[r].z, o.z); o.w = fmaf(q, s[r].w, o.w);
             }
 #pragma unroll
-            for (int d = 8; d < 32; d *= 2) {    // the warp's four row groups
+            for (int d = kLanes; d < 32; d *= 2) {       // the warp's row groups
                 o.x += __shfl_xor_sync(0xffffffffu, o.x, d); o.y += __shfl_xor_sync(0xffffffffu, o.y, d);
                 o.z += __shfl_xor_sync(0xffffffffu, o.z, d); o.w += __shfl_xor_sync(0xffffffffu, o.w, d);
             }
-            if (tid % 32 < 8) *reinterpret_cast<float4*>(&red[tid / 32][e][4 * tx]) = o;
+            if (tid % 32 < kLanes) *reinterpret_cast<float4*>(&red[tid / 32][e][4 * tx]) = o;
         }
         __syncthreads();
         T* orow = static_cast<T*>(a.o.p) + i * a.o.stride + (int64_t)(h * g + e0) * D + c0;
         for (int x = tid; x < ne * kCols; x += kThreads) {
             const int e = x / kCols, c = x % kCols;
-            Elem<T>::store(orow + e * D + c, (red[0][e][c] + red[1][e][c]) + (red[2][e][c] + red[3][e][c]));
+            float o = red[0][e][c];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) o += red[w][e][c];
+            Elem<T>::store(orow + e * D + c, o);
         }
     }
     if (h == 0 && c0 == 0) lin_check_alone(a, a.slots, nullptr, i, slot, a.n);
