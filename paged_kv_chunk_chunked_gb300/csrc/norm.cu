@@ -18,7 +18,7 @@
 // Replayed on the same buffers (partly in L2), bf16: 4096 rows of 3584 columns forward
 // 11.8 us (5.0 TB/s), backward 24.3 (3.6 TB/s; 4.7 of it the second kernel); 28 groups of
 // 128 columns 12.0 and 23.2; 2048 rows of 16384 columns 45 and 90. Where rows come from HBM
-// the first pair takes 16.6 and 25 us. The sums' latency and issue slots (58% used)
+// the first pair takes 16.6 and 25 us. The sums' latency and issue slots (56% used)
 // bound them as much as HBM; a forward CTA that takes several rows and loads the next one
 // ahead was slower (13.2 us at best).
 #include <cuda_bf16.h>
