@@ -451,3 +451,70 @@ def test_several_sequences_may_start_from_one_state():
                                B.lin_batch(1, None, src[b:b + 1], dst[b:b + 1]))
         B.pkv_lin_check(c.lin)
         assert torch.equal(*one) and torch.equal(last, c.state[1:])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_calls_at_once_and_outgrown_scratch(dtype):
+    """Two stores on two streams, steps on different slots of one store on two streams, and a graph
+    that was captured before its store's scratch was outgrown: the bits of each by itself."""
+    dt, Hq, Hkv, d, n = DT[dtype][0], 4, 2, 128, 900
+    g2 = _decays("spread", Hkv).cuda()
+    sets = [_rows(n, (Hq, Hkv, Hkv, Hq), d, dt, False, s) for s in (1, 2)]
+    i = torch.arange(2, dtype=torch.int32, device="cuda")
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    with Store(dtype, Hq, Hkv, d, 2) as a, Store(dtype, Hq, Hkv, d, 2) as b:
+        batch = B.lin_batch(1, None, i[:1], i[1:])
+
+        def run(c, x, o, grads, stream, m=n):
+            B.pkv_lin_attn_fwd(c.lin, *(t[:m] for t in x[:3]), o[:m], m, g2, batch, stream)
+            B.pkv_lin_attn_bwd(c.lin, *(t[:m] for t in x), *(t[:m] for t in grads), m, g2, batch, stream)
+
+        def fresh():
+            return [torch.zeros_like(sets[0][0])] + [torch.zeros_like(t) for t in sets[0][:3]]
+        want = []
+        for x in sets:
+            out = fresh()
+            run(a, x, out[0], out[1:], torch.cuda.current_stream())
+            torch.cuda.synchronize()
+            want.append(out)
+        for _ in range(3):
+            outs = [fresh(), fresh()]
+            torch.cuda.synchronize()
+            for c, x, out, stream in zip((a, b), sets, outs, streams):
+                run(c, x, out[0], out[1:], stream)
+            torch.cuda.synchronize()
+            assert all(torch.equal(p, q) for out, w in zip(outs, want) for p, q in zip(out, w))
+        # A graph of a short call, then a longer call that needs more scratch, then the graph again.
+        with Store(dtype, Hq, Hkv, d, 2) as c:
+            out, short = fresh(), fresh()
+            run(c, sets[0], short[0], short[1:], torch.cuda.current_stream(), 300)
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=streams[0]):
+                run(c, sets[0], out[0], out[1:], streams[0], 300)
+            long = fresh()
+            run(c, sets[1], long[0], long[1:], torch.cuda.current_stream())
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(p, q) for p, q in zip(out, short)) and all(torch.equal(p, q) for p, q in zip(long, want[1]))
+            B.pkv_lin_check(c.lin)
+        # Single tokens: slot 0 on one stream, slot 1 on the other, five tokens each.
+        states = []
+        for at_once in (False, True):
+            for c in (a, b):
+                c.state.fill_(0.5)
+            torch.cuda.synchronize()
+            os = [torch.zeros(5, Hq, d, dtype=dt, device="cuda") for _ in range(2)]
+            torch.cuda.synchronize()
+            for s in range(2):
+                for t in range(5):
+                    q, k, v = (z[t:t + 1] for z in sets[s][:3])
+                    B.pkv_lin_attn_step(a.lin, q, k, v, os[s][t:t + 1], 1, g2, i[s:s + 1], streams[s])
+                if not at_once:
+                    torch.cuda.synchronize()
+            torch.cuda.synchronize()
+            states.append([a.state.clone(), *os])
+        assert all(torch.equal(p, q) for p, q in zip(*states))
+        B.pkv_lin_check(a.lin)
+        B.pkv_lin_check(b.lin)

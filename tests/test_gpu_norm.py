@@ -190,3 +190,43 @@ def test_graphs_and_streams(width, groups):
     torch.cuda.synchronize()
     for o in got:
         assert all(torch.equal(a, b) for a, b in zip(o, want))
+
+
+@pytest.mark.parametrize("n,width,groups", [(300, 512, 1), (70, 8208, 1), (200, 64, 14)])
+def test_calls_at_once(n, width, groups):
+    """Two backward passes on two streams, each with scratch of its own, and two graphs that share
+    one replayed in turn: the bits of each by itself."""
+    cols = groups * width
+    g = torch.Generator().manual_seed(n)
+    xs, dys = ([torch.randn(n, cols, generator=g).bfloat16().cuda() for _ in range(2)] for _ in range(2))
+    w = torch.randn(cols, generator=g).bfloat16().cuda()
+    m = B.norm(width, groups, 1e-5, w, None, B.PKV_BF16)
+    stats = [[torch.empty(n, groups, device="cuda") for _ in range(2)] for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for x, (mean, rstd) in zip(xs, stats):
+        B.pkv_layer_norm_fwd(x, torch.empty_like(x), mean, rstd, n, m)
+    scratch = [torch.empty(B.pkv_layer_norm_scratch(m, n), device="cuda") for _ in range(2)]
+
+    def outs():
+        return [[torch.zeros_like(xs[0]), torch.zeros(cols, device="cuda"), torch.zeros(cols, device="cuda")] for _ in range(2)]
+
+    def run(s, out, sc, stream):
+        B.pkv_layer_norm_bwd(dys[s], xs[s], *stats[s], *out, n, m, sc, stream=stream)
+    want, got, replayed = outs(), outs(), outs()
+    for s in range(2):
+        run(s, want[s], scratch[0], torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for s in range(2):
+            run(s, got[s], scratch[s], streams[s])
+    torch.cuda.synchronize()
+    graphs = []
+    for s in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[s], stream=streams[0]):
+            run(s, replayed[s], scratch[0], streams[0])
+    for s in (0, 1, 0, 1):
+        graphs[s].replay()
+    torch.cuda.synchronize()
+    for s in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(got[s], want[s])) and all(torch.equal(a, b) for a, b in zip(replayed[s], want[s]))
