@@ -17,7 +17,7 @@
 // and dy twice.
 // Replayed on the same buffers (partly in L2), bf16: 4096 rows of 3584 columns forward
 // 11.8 us (5.0 TB/s), backward 24.3 (3.6 TB/s; 4.7 of it the second kernel); 28 groups of
-// 128 columns 12.0 and 23.2; 2048 rows of 16384 columns 45 and 90. Where rows come from HBM
+// 128 columns 12.0 and 23.2; 2048 rows of 16384 columns 45 and 93. Where rows come from HBM
 // the first pair takes 16.6 and 25 us. The sums' latency and issue slots (56% used)
 // bound them as much as HBM; a forward CTA that takes several rows and loads the next one
 // ahead was slower (13.2 us at best).
@@ -387,10 +387,10 @@ __global__ void __launch_bounds__(kMaxTeam, 1) layer_norm_bwd_kernel(NormArgs a)
     }
 }
 
-// ---- backward of rows too wide for a thread's registers: dx by a CTA a (row, group), which
-// reads its row twice (the second time from L1 or L2), and the columns' sums by themselves,
-// from x and dy read again (2048 rows of 16384 columns in bf16 90 us, with the kernel
-// above and its spills 410; of 8191, by single elements, 80 and 596)
+// ---- backward of rows too wide for a thread's registers: the columns' sums by themselves, then
+// dx by a CTA a (row, group), which reads its row twice (the second time from L1 or L2). 2048
+// rows of 16384 columns in bf16 93 us, with the kernel above and its spills 410; of 8191, by
+// single elements, 80 and 596.
 template <typename T, int EPV> __global__ void __launch_bounds__(kMaxTeam) layer_norm_wide_dx_kernel(NormArgs a) {
     __shared__ float red[2 * 32];
     const int64_t unit = blockIdx.x, row = a.groups == 1 ? unit : unit / a.groups, c0 = (unit - row * a.groups) * a.width;
@@ -709,17 +709,19 @@ template <typename T, int EPV, int NV> cudaError_t run(NormArgs& a, bool bwd, cu
     return cudaGetLastError();
 }
 
+// The columns first: dx may be dy itself, which they read.
 template <typename T, int EPV> cudaError_t run_wide(NormArgs& a, cudaStream_t s) {
-    if (a.dx) {
-        if (a.n * a.groups > kMaxGrid) return cudaErrorInvalidConfiguration;
-        ProfScope ps("layer_norm_wide_dx_kernel", s);
-        layer_norm_wide_dx_kernel<T, EPV><<<(unsigned)(a.n * a.groups), kMaxTeam, 0, s>>>(a);
+    if (a.dx && a.n * a.groups > kMaxGrid) return cudaErrorInvalidConfiguration;
+    if (a.part) {
+        ProfScope ps("layer_norm_wide_cols_kernel", s);
+        const int64_t tiles = ((int64_t)a.groups * a.width / EPV + kThreads - 1) / kThreads;
+        layer_norm_wide_cols_kernel<T, EPV><<<dim3((unsigned)tiles, a.slots), kThreads, 0, s>>>(a);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
     }
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || !a.part) return e;
-    ProfScope ps("layer_norm_wide_cols_kernel", s);
-    const int64_t tiles = ((int64_t)a.groups * a.width / EPV + kThreads - 1) / kThreads;
-    layer_norm_wide_cols_kernel<T, EPV><<<dim3((unsigned)tiles, a.slots), kThreads, 0, s>>>(a);
+    if (!a.dx) return cudaSuccess;
+    ProfScope ps("layer_norm_wide_dx_kernel", s);
+    layer_norm_wide_dx_kernel<T, EPV><<<(unsigned)(a.n * a.groups), kMaxTeam, 0, s>>>(a);
     return cudaGetLastError();
 }
 
