@@ -963,9 +963,9 @@ lin_cols_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     __shared__ float diag[64];
     __shared__ __align__(16) float pw[32];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, f = blockIdx.x, h = blockIdx.y;
-    launch_dependents();
     LinChunk c;
     if (!lin_chunk<kL>(a, f, c)) {
+        launch_dependents();
         wait_for_kernels();                      // a kernel never ends before the one it may overlap
         return;
     }
@@ -999,6 +999,9 @@ lin_cols_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
+    // (only now: the next kernel could otherwise be given an SM's tensor memory before this
+    // one, which waits for room there, and then wait for this one)
+    launch_dependents();
     const uint32_t tmem = B.tmem_base;
     if (warp == 0) {
         // ------------------------------------------------------------ loads
