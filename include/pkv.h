@@ -75,8 +75,10 @@ typedef enum pkv_residency {
     PKV_RES_META = 2           /* no page memory: block-table and free-list logic only   */
 } pkv_residency;
 
-/* Pool flags. */
+/* Flags of pools and stores. */
 #define PKV_FLAG_SIMT_ONLY 1u  /* use the CUDA-core kernels even where tensor-core ones exist */
+/* Flag of pkv_lin stores: bf16 calls on the tensor cores round scores and states to bf16 (see there). */
+#define PKV_FLAG_LIN_ONE_TERM 2u
 
 typedef struct pkv_pool_desc {
     int32_t page_size;         /* P, tokens per page; multiple of 8                      */
@@ -491,10 +493,12 @@ pkv_status pkv_stage_stats(pkv_seq* seq, int64_t* kv_in, int64_t* grads_in, int6
  *   S_t = l S_{t-1} + k_t v_t^T        l = exp(log_decay[head]), float32 S
  *   o_t = q_t^T S_t / sqrt(d)          query head h reads the state of KV head h / (Hq / Hkv)
  * Long inputs are computed in chunks by matrix products, one token at a time by
- * the recurrence itself. Products, sums and states are float32; bf16 calls on
- * the tensor cores round the weighted scores of a chunk and the states that
- * chunks start from to bf16 once, as operands of the products, and states (and
- * their gradients) themselves not at all.
+ * the recurrence itself. Products, sums and states are float32, but that bf16
+ * calls on the tensor cores take the weighted scores of a chunk, and the states
+ * that chunks start from (the gradients of those they end with), to 16 bits as
+ * operands of the products, 2^-16 of each value. With PKV_FLAG_LIN_ONE_TERM they
+ * take them to bf16, 2^-8, in 10 to 15% less time. States and their gradients
+ * themselves are not rounded.
  *
  * pkv_lin is a store of states, as pkv_pool is one of pages: n_slots states of
  * all KV heads, float32 [n_slots, Hkv, d, d], and with grads = 1 as many

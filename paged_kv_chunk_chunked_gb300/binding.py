@@ -22,6 +22,7 @@ STATUS_NAMES = {0: "PKV_OK", 1: "PKV_ERR_INVALID", 2: "PKV_ERR_OOM", 3: "PKV_ERR
 PKV_BF16, PKV_F32 = 0, 1
 PKV_RES_DEVICE, PKV_RES_PINNED_HOST, PKV_RES_META = 0, 1, 2
 PKV_FLAG_SIMT_ONLY = 1
+PKV_FLAG_LIN_ONE_TERM = 2
 PKV_STAGE_KV, PKV_STAGE_GRADS = 1, 2
 
 

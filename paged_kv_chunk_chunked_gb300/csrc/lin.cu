@@ -33,6 +33,7 @@ pkv_status begin(const pkv_lin* lin, int64_t n, const float* log_decay, LinArgs*
     a->Hq = lin->desc.n_q_heads; a->Hkv = lin->desc.n_kv_heads; a->d = lin->desc.head_dim; a->dtype = lin->desc.dtype;
     a->n = n; a->n_slots = lin->desc.n_slots;
     a->log_decay = log_decay;
+    a->one_term = lin->desc.flags & PKV_FLAG_LIN_ONE_TERM;
     a->state = lin->state; a->dstate = lin->dstate; a->err = lin->d_err; a->wait_err = lin->d_err ? lin->d_err + 1 : nullptr;
     return PKV_OK;
 }
@@ -69,7 +70,7 @@ pkv_status chunk_states(pkv_lin* lin, LinArgs* a, bool bwd, cudaStream_t cs, con
     const bool tc = on_tensor_cores(lin);
     a->n_chunks = (int)lin_chunks(a->n, a->n_seq, tc ? kLinTcChunk : kLinSimtChunk);
     if ((int64_t)a->n_chunks * std::max(a->Hkv * a->d, a->Hkv + a->Hq) > kMaxGrid / 2) return fail(PKV_ERR_UNSUPPORTED, std::string(who) + ": too many rows");
-    const size_t one = (size_t)a->n_chunks * a->Hkv * a->d * a->d, set = tc ? one + one / 2 : one, floats = set * (bwd ? 2 : 1);
+    const size_t one = (size_t)a->n_chunks * a->Hkv * a->d * a->d, floats = one * (bwd ? 2 : 1);
     if (lin->scratch_floats < floats) {
         if (capturing(cs))
             return fail(PKV_ERR_INVALID, std::string(who) + ": needs a larger scratch buffer than the store has; run the call "
@@ -86,9 +87,7 @@ pkv_status chunk_states(pkv_lin* lin, LinArgs* a, bool bwd, cudaStream_t cs, con
         lin->scratch_floats = floats;
     }
     a->part = lin->scratch;
-    a->gpart = bwd ? lin->scratch + set : nullptr;
-    a->sbf = tc ? reinterpret_cast<__nv_bfloat16*>(a->part + one) : nullptr;
-    a->gbf = tc && bwd ? reinterpret_cast<__nv_bfloat16*>(a->gpart + one) : nullptr;
+    a->gpart = bwd ? lin->scratch + one : nullptr;
     return PKV_OK;
 }
 
@@ -121,7 +120,7 @@ pkv_status pkv_lin_create(const pkv_lin_desc* d, pkv_lin** out) {
         if (d->grads != 0 && d->grads != 1) return fail(PKV_ERR_INVALID, "pkv_lin_create: grads must be 0 or 1");
         if (d->n_slots <= 0 || d->n_slots > (int64_t(1) << 30))
             return fail(PKV_ERR_INVALID, "pkv_lin_create: n_slots must be in 1 .. 2^30");
-        if (d->flags & ~PKV_FLAG_SIMT_ONLY) return fail(PKV_ERR_INVALID, "pkv_lin_create: unknown flags");
+        if (d->flags & ~(PKV_FLAG_SIMT_ONLY | PKV_FLAG_LIN_ONE_TERM)) return fail(PKV_ERR_INVALID, "pkv_lin_create: unknown flags");
         pkv_lin* lin = new pkv_lin();
         lin->desc = *d;
         if (d->residency == PKV_RES_META) {

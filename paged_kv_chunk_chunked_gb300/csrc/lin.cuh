@@ -48,9 +48,9 @@ struct LinArgs {
     float* dstate;
     float* part;                     // scratch [chunks, Hkv, d, d]: each chunk's sum, then the state before it
     float* gpart;                    // the same of the gradients: the gradient of the state after it
-    __nv_bfloat16* sbf;              // tensor-core kernels: scratch [chunks, Hkv, d, d], the states before the chunks
-    __nv_bfloat16* gbf;              // and the gradients of the states after them, in bf16 (part keeps the sums)
+                                     // (tensor-core kernels: states and gradients as rows of d first and d second bf16 terms)
     int n_chunks;                    // lin_chunks
+    bool one_term;                   // tensor-core kernels: PKV_FLAG_LIN_ONE_TERM
     int* err;                        // word of bad arguments
     int* wait_err;                   // word of the bounded waits: these give up once it is set
 };

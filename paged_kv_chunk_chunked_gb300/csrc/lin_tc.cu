@@ -6,10 +6,14 @@
 // rows O (lin_rows_tc_kernel). The backward forms both sums and both scans, then
 // the rows dQ (the same kernel) and the columns dV and dK (lin_cols_tc_kernel).
 //
-// Roundings to bf16, beside the outputs': the weighted scores of a chunk and the
-// states before (after) a chunk, each once, as operands of products. Sums and
-// scans stay in fp32: a weighted operand of the sums is given to the tensor core
-// as three bf16 terms that add up to it (24 bits).
+// Only the outputs are rounded to bf16. What the tensor core multiplies in bf16 goes there
+// as terms that add up: a weighted operand of the sums as three (24 bits, as what they
+// add up to stays in fp32 through the scans), the weighted scores of a chunk and the
+// states before (after) a chunk as two (16 bits: off by 2^-16 where one term is by 2^-8,
+// as much as an output's own rounding). The error of O, dQ, dK and dV against 64 bits is
+// that rounding then, 0.0017 relative. TERMS = 1 is the caller's choice
+// (PKV_FLAG_LIN_ONE_TERM): 0.0023 to 0.0025, and 10 to 15% less time (4096 rows, 28/4 heads
+// of d 128: forward 29.0 us instead of 33.2, both ways 90.2 instead of 105.7).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -44,8 +48,9 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void*
 }
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// Eight warps share an accumulator: a warp has 32 rows (its quadrant of tensor
-// memory) and half of the columns.
+// An accumulator's rows lie in the four quadrants of tensor memory, a warp's 32 rows in one.
+// In the rows kernel four warps share an accumulator and take half of their rows' columns
+// at a time; in the columns kernel eight do, a half of the columns each.
 
 // D / 2 columns of this thread's row, times f, as bf16 pairs.
 template <int D> __device__ __forceinline__ void load_half(uint32_t tmem, float f, uint32_t (&o)[D / 4]) {
@@ -97,8 +102,30 @@ template <int D> __device__ __forceinline__ void scale_half(uint32_t tmem, float
 }
 
 // Tensor-memory column, within a tile of scores, of the weighted scores' inner
-// indices 16 k .. 16 k + 15: each half of the columns overwrites its own.
-__device__ __forceinline__ constexpr uint32_t p_col(int k) { return (k >> 2) * 64 + (k & 3) * 8; }
+// indices 16 k .. 16 k + 15, their first (second) terms: each 32 columns are overwritten
+// by their own two terms.
+__device__ __forceinline__ constexpr uint32_t p_col(int k, int term) { return (k >> 1) * 32 + term * 16 + (k & 1) * 8; }
+
+// Two floats as two bf16 terms each, the nearest and the nearest to what is left, or as the first alone.
+template <int TERMS> __device__ __forceinline__ void split(f32x2 p, uint32_t& hi, uint32_t& lo) {
+    float x, y;
+    unpack2(p, x, y);
+    hi = pack_bf16x2(x, y);
+    if constexpr (TERMS == 2) {
+        unpack2(fma2(pack2(bf16lo(hi), bf16hi(hi)), pack2(-1.f, -1.f), p), x, y);
+        lo = pack_bf16x2(x, y);
+    }
+}
+
+// 32 weighted scores of this thread's row, 16 pairs of first terms and 16 of second ones: pair e
+// is put in, all of them stored.
+template <int TERMS> __device__ __forceinline__ void put_pair_terms(uint32_t (&pk)[16 * TERMS], int e, f32x2 p) {
+    split<TERMS>(p, pk[e], pk[16 * (TERMS - 1) + e]);
+}
+template <int TERMS> __device__ __forceinline__ void store_block(uint32_t tmem, const uint32_t (&pk)[16 * TERMS]) {
+    if constexpr (TERMS == 2) tc::tmem_st32(tmem, pk);
+    else tc::tmem_st16(tmem, pk);
+}
 
 // Zeroes rows [m, 128) of a 128-row tile of D / 64 blocks, by `threads` threads:
 // what lies behind a sequence may be anything, and 0 * NaN is NaN.
@@ -491,15 +518,19 @@ lin_part_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 constexpr int kScanThreads = 128, kScanAhead = 16;
 
 // From a sequence's chunk sums to the states before its chunks (y 0, in order) or
-// the gradients of the states after them (y 1, in reverse), in fp32; the kernels
-// that multiply by them get them in bf16. A thread owns four elements all along
-// (so slot_in may be slot_out) and has kScanAhead chunks' sums on their way at once:
+// the gradients of the states after them (y 1, in reverse), in fp32. The kernels
+// that multiply by them get them as bf16 terms, which take the place of the sums: a row
+// of D sums becomes D first terms and D second ones. A row is a warp's (D 64: two are), which
+// has read it when it writes. (In memory of their own: 314.6 us instead of 312.0 for a
+// forward of 16 heads of 32768 rows, and twice the scratch.) A thread owns four elements all
+// along (so slot_in may be slot_out) and has kScanAhead chunks' sums on their way at once:
 // what bounds the scan is the latency of these rounds and of what comes before them,
 // which overlaps the kernel before where an SM has room beside it. Past L2's size HBM bounds
-// it (16 heads of 32768 rows of d 128: 75 us for 402 MB; 88 with the sums written in the
-// scan's own order and these loads and stores unmarked). More chunks at once, or each next
-// one asked for as one is used up, were slower: up to 145 us.
-template <int D>
+// it (16 heads of 32768 rows of d 128: 100 us for 537 MB; with one term 76 for 402). More
+// chunks at once, or each next one asked for as one is used up, were slower, up to twice
+// the time; so were stores marked as streaming (forward of 4096 rows, 28/4 heads: 33.3 us
+// instead of 33.0), as the rows kernel reads them next.
+template <int D, int TERMS>
 __global__ void __launch_bounds__(kScanThreads, 5) lin_scan_bf16_kernel(const LinArgs a) {
     constexpr int V = D * D / 4;
     const bool grad = blockIdx.y;
@@ -521,46 +552,50 @@ __global__ void __launch_bounds__(kScanThreads, 5) lin_scan_bf16_kernel(const Li
     if (blockIdx.x % (V / kScanThreads * a.Hkv) == 0) lin_check_alone(a, to, from, b, last, a.n_seq);
     wait_for_kernels();
     if (!good) return;
-    const int64_t nc = (hi - lo + kL - 1) / kL;
-    const float lfull = lin_pow(g2, kL), ltail = lin_pow(g2, (int)(hi - lo - (nc - 1) * kL));    // the last chunk's rows
-    const int64_t at = ((lo / kL + b + (grad ? nc - 1 : 0)) * a.Hkv + h) * V + e, step = (int64_t)a.Hkv * V * (grad ? -1 : 1);
-    const float4* in = reinterpret_cast<const float4*>(grad ? a.gpart : a.part) + at;
-    uint2* out = reinterpret_cast<uint2*>(grad ? a.gbf : a.sbf) + at;
-    for (int64_t i = 0; i < nc; i += kScanAhead) {
-        const int m = (int)min64(kScanAhead, nc - i);
+    const int nc = (int)((hi - lo + kL - 1) / kL);
+    const float lfull = lin_pow(g2, kL), ltail = lin_pow(g2, (int)(hi - lo - (int64_t)(nc - 1) * kL));     // the last chunk's rows
+    const int64_t at = ((lo / kL + b + (grad ? nc - 1 : 0)) * a.Hkv + h) * V, step = (int64_t)a.Hkv * V * (grad ? -1 : 1);
+    const float4* in = reinterpret_cast<const float4*>(grad ? a.gpart : a.part) + at + e;
+    uint2* out = reinterpret_cast<uint2*>((grad ? a.gpart : a.part) + 4 * at) + e / (D / 4) * (D / 2) + e % (D / 4);
+    float4* end = last >= 0 ? store + ((size_t)last * a.Hkv + h) * V + e : nullptr;
+    for (int i = 0; i < nc; i += kScanAhead) {
+        const int m = min(kScanAhead, nc - i);
         float4 x[kScanAhead];
-        const float4* p = in;
 #pragma unroll
         for (int u = 0; u < kScanAhead; ++u) {
-            if (u < m) x[u] = __ldcg(p);
-            p += step;
+            if (u < m) x[u] = __ldcg(in);
+            in += step;
         }
+        __syncwarp();                            // the warp has read what it overwrites
 #pragma unroll
         for (int u = 0; u < kScanAhead; ++u)
             if (u < m) {
-                __stcs(out, make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w)));
-                out += step;
+                uint2 hi, lo;
+                split<TERMS>(pack2(s.x, s.y), hi.x, lo.x);
+                split<TERMS>(pack2(s.z, s.w), hi.y, lo.y);
+                *out = hi;
+                if (TERMS == 2) out[D / 4] = lo;
+                out += 2 * step;
                 const float l = i + u == (grad ? 0 : nc - 1) ? ltail : lfull;
                 s.x = fmaf(l, s.x, x[u].x);
                 s.y = fmaf(l, s.y, x[u].y);
                 s.z = fmaf(l, s.z, x[u].z);
                 s.w = fmaf(l, s.w, x[u].w);
             }
-        in = p;
     }
-    if (last >= 0) store[((size_t)last * a.Hkv + h) * V + e] = s;
+    if (end) *end = s;
 }
 
 // ------------------------------------------------------------------ rows
 
-// Shared memory of the rows kernel: C, S and R of a (chunk, KV head) pair, an X
+// Shared memory of the rows kernel: C, S (two terms) and R of a (chunk, KV head) pair, an X
 // tile for each group of warps, a box of outputs for each warp.
-template <int D> struct RowsLayout {
+template <int D, int TERMS> struct RowsLayout {
     static constexpr uint32_t kTile = D / 64 * 16384;                // 128 rows
     static constexpr uint32_t kState = D / 64 * D * 128;             // D rows
-    static constexpr uint32_t kOffS = kTile, kOffR = kOffS + kState, kOffX = kOffR + kTile, kOffStage = kOffX + 2 * kTile;
+    static constexpr uint32_t kOffS = kTile, kOffR = kOffS + TERMS * kState, kOffX = kOffR + kTile, kOffStage = kOffX + 2 * kTile;
     static constexpr uint32_t kStage = 32 * D;
-    static constexpr uint32_t kSmem = kOffStage + 16 * kStage + 1024;
+    static constexpr uint32_t kSmem = kOffStage + 8 * kStage + 1024;
 };
 constexpr int kRowsThreads = 3 * 32 + 2 * 128;
 
@@ -570,7 +605,7 @@ struct RowsBarriers {
     // may still have to see a pair's when the other group is at the next pair's; the one after that
     // needs C's place, which both warps give up only after they have seen this one.
     uint64_t r_ready[2];
-    uint64_t x_full[2], x_empty[2], s_full[2], p_full[2], o_full[2], o_free[2], drain[2];        // by group
+    uint64_t x_full[2], x_empty[2], s_full[2], p_half[2], p_full[2], o_full[2], o_free[2], drain[2];     // by group
     uint32_t tmem_base;
 };
 
@@ -615,26 +650,29 @@ struct HeadWalk {
 
 // out = scale [((X C^T) o M) R + diag(l^(i+1)) X S']. O: X, C, R, S' = Q, K, V, S;
 // dQ (GRAD): dO, V, K, S^T. A persistent CTA takes a run of heads. Warp 0 loads
-// (TMA); two groups of eight warps take the heads in turn, each with a warp (1, 2)
+// (TMA); two groups of four warps take the heads in turn, each with a warp (1, 2)
 // that issues its products and 256 columns of tensor memory of its own: scores
-// [0, 128), which the weighted scores in bf16 overwrite as the A operand of the
+// [0, 128), which the weighted scores' bf16 terms overwrite as the A operand of the
 // second product, and the output [128, 128 + D), which is X S' first and is scaled
-// by l^(i+1) there before the second product adds to it. (One issuing warp for both
+// by l^(i+1) there before the second product adds to it, in two halves: that of keys
+// 0 .. 63 runs while the weights of the others are formed (ragged prompts, 64/8 heads of
+// d 64: 39.6 -> 38.4 us). (One issuing warp for both
 // made each second product wait for the other group's output to be read: 2.1 us a head.)
 // Weights l^(i-j): for 32 x 32 blocks under the diagonal l^(i - 32 b - 31) (one per
 // row and block) times l^(31 - (j - 32 b)), both with exponents >= 0; on it from a table.
-// A group takes about 2.4 us from a head to its next: X's load, a chain of two products and
-// their reading and writing in tensor memory, and the store. 4096 rows, 28/4 heads of d 128:
-// 20 us (six heads a CTA; 67 MB), of which the last 12 follow the states; 32768 rows of 16
-// heads, a state for each: 122 us for 671 MB (5.5 TB/s). X asked for further ahead, to L2 or
-// to a second tile a group, was slower (training chunk 95 us instead of 91), as those loads
-// come before the kernels that the states still wait for.
-template <int D, bool GRAD>
+// What bounds it is a group's chain from a head to its next: X's load, two products and
+// their reading and writing in tensor memory, and the store; the tensor pipe is busy for a third
+// of the time. 4096 rows, 28/4 heads of d 128: 23 us (six heads a CTA; 71 MB), of which the
+// last 14 follow the states; with one term 20. 32768 rows of 16 heads, a state for each:
+// 137 us for 805 MB (5.9 TB/s). X asked for further ahead, to L2 or to a second tile a group,
+// was slower (one term, both ways of the 4096 rows 95 us instead of 91), as those loads come
+// before the kernels that the states still wait for.
+template <int D, bool GRAD, int TERMS>
 __global__ void __launch_bounds__(kRowsThreads, 1)
 lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_c,
                    const __grid_constant__ CUtensorMap map_r, const __grid_constant__ CUtensorMap map_s,
                    const __grid_constant__ CUtensorMap map_out, const LinArgs a, Cut cut) {
-    using L = RowsLayout<D>;
+    using L = RowsLayout<D, TERMS>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ __align__(8) RowsBarriers B;
@@ -645,6 +683,7 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             tc::mbar_init(&B.x_full[s], 1);
             tc::mbar_init(&B.x_empty[s], 1);
             tc::mbar_init(&B.s_full[s], 1);
+            tc::mbar_init(&B.p_half[s], 128);
             tc::mbar_init(&B.p_full[s], 128);
             tc::mbar_init(&B.o_full[s], 1);
             tc::mbar_init(&B.o_free[s], 128);
@@ -693,9 +732,9 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         };
         auto load_s = [&](int state) {
             if (lane == 0) {
-                tc::mbar_arrive_expect_tx(&B.st_full, L::kState);
+                tc::mbar_arrive_expect_tx(&B.st_full, TERMS * L::kState);
 #pragma unroll
-                for (int b = 0; b < D / 64; ++b) tc::tma_load_2d(smem + L::kOffS + b * (D * 128), &map_s, &B.st_full, 64 * b, state * D);
+                for (int b = 0; b < TERMS * D / 64; ++b) tc::tma_load_2d(smem + L::kOffS + b * (D * 128), &map_s, &B.st_full, 64 * b, state * D);
             }
             ++n_s;
         };
@@ -795,19 +834,30 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             if (leader) {
                 const uint64_t ds = GRAD ? tc::sdesc(sm + L::kOffS, 16, 1024) : tc::sdesc(sm + L::kOffS, D * 128, 1024);
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    tc::mma_bf16(t + 128, tc::sdesc_at(dx, (k >> 2) * 16384 + (k & 3) * 32),
-                                 tc::sdesc_at(ds, GRAD ? (k >> 2) * (D * 128) + (k & 3) * 32 : k * 2048), idesc_s, k > 0);
+                for (int k = 0; k < TERMS * D / 16; ++k) {       // the first terms' inner indices, then the second ones'
+                    const int c = k % (D / 16), term = k / (D / 16) * L::kState;
+                    tc::mma_bf16(t + 128, tc::sdesc_at(dx, (c >> 2) * 16384 + (c & 3) * 32),
+                                 tc::sdesc_at(ds, term + (GRAD ? (c >> 2) * (D * 128) + (c & 3) * 32 : c * 2048)), idesc_s, k > 0);
+                }
                 tc::mma_commit(&B.o_full[wg]);   // X S': the output's first phase of a head
                 tc::mma_commit(&B.x_empty[wg]);
             }
             __syncwarp();
             if (!r_seen && !wait_r(w.pair)) break;
+            // (the weights of keys 64 .. are still being formed during the first half)
+            if (!tc::warp_wait(&B.p_half[wg], n & 1, a.wait_err)) break;
+            tc::tc_fence_after();
+            if (leader)
+#pragma unroll
+                for (int k = 0; k < 4 * TERMS; ++k)
+                    tc::mma_bf16_ts(t + 128, t + p_col(k & 3, k >> 2), tc::sdesc_at(dr, (k & 3) * 2048), idesc_r, 1u);
+            __syncwarp();
             if (!tc::warp_wait(&B.p_full[wg], n & 1, a.wait_err)) break;
             tc::tc_fence_after();
             if (leader) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) tc::mma_bf16_ts(t + 128, t + p_col(k), tc::sdesc_at(dr, k * 2048), idesc_r, 1u);
+                for (int k = 0; k < 4 * TERMS; ++k)
+                    tc::mma_bf16_ts(t + 128, t + p_col(4 + (k & 3), k >> 2), tc::sdesc_at(dr, (4 + (k & 3)) * 2048), idesc_r, 1u);
                 tc::mma_commit(&B.o_full[wg]);   // the whole output: its second phase
             }
             __syncwarp();
@@ -824,7 +874,7 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         const uint32_t t = tmem + ((uint32_t)(quad * 32) << 16) + wg * 256;
         const float scale = rsqrtf((float)D);
         const LinRows& out = GRAD ? a.dq : a.o;
-        uint8_t* stage = smem + L::kOffStage + (warp - 3) * 2 * L::kStage;
+        uint8_t* stage = smem + L::kOffStage + (warp - 3) * L::kStage;
         // l's powers, kept while the KV head stays; each group has tables of its own:
         // l^(x - 31) for x >= 31, else 0, and l^(31 - x).
         __shared__ float diag[2][64];
@@ -832,6 +882,17 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         int h_of = -1;
         float rb[3], li1 = 0.f;
         bool ok = true;
+        // A warp's box holds half of its columns. The other half's turn is behind the next head's
+        // weights, when the first has long left (shared memory has no room for both).
+        uint32_t o1[D / 4];
+        int left1 = 0, head1 = 0, row1 = 0;
+        auto put_second = [&]() {
+            if (left1 <= 0) return;
+            if (lane == 0) tc::bulk_wait_read();
+            __syncwarp();
+            store_half<D>(o1, &map_out, stage, lane, left1, D / 2, head1, row1, out);
+            left1 = 0;
+        };
         for (; more; more = w.next()) {
             if (w.h != h_of) {
                 h_of = w.h;
@@ -860,10 +921,10 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             // Blocks left of the diagonal's, then the diagonal's, then nothing.
 #pragma unroll 1
             for (int b = 0; b < 4; ++b) {
-                uint32_t pk[16];
+                uint32_t pk[16 * TERMS];         // first terms, second ones
                 if (b > quad) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) pk[e] = 0u;
+                    for (int e = 0; e < 16 * TERMS; ++e) pk[e] = 0u;
                 } else {
                     uint32_t r[32];
                     tc::tmem_ld32(t + 32 * b, r);
@@ -875,45 +936,52 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
 #pragma unroll
                         for (int e = 0; e < 16; e += 2) {
                             const ulonglong2 k = u[e / 2];
-                            float x, y;
-                            unpack2(mul2(pack2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), mul2(k.x, f)), x, y);
-                            pk[e] = pack_bf16x2(x, y);
-                            unpack2(mul2(pack2(__uint_as_float(r[2 * e + 2]), __uint_as_float(r[2 * e + 3])), mul2(k.y, f)), x, y);
-                            pk[e + 1] = pack_bf16x2(x, y);
+                            put_pair_terms<TERMS>(pk, e, mul2(pack2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), mul2(k.x, f)));
+                            put_pair_terms<TERMS>(pk, e + 1, mul2(pack2(__uint_as_float(r[2 * e + 2]), __uint_as_float(r[2 * e + 3])), mul2(k.y, f)));
                         }
                     } else {
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             const float x = 2 * e <= lane ? __uint_as_float(r[2 * e]) * diag[wg][lane - 2 * e + 31] : 0.f;
                             const float y = 2 * e + 1 <= lane ? __uint_as_float(r[2 * e + 1]) * diag[wg][lane - 2 * e + 30] : 0.f;
-                            pk[e] = pack_bf16x2(x, y);
+                            put_pair_terms<TERMS>(pk, e, pack2(x, y));
                         }
                     }
                 }
-                tc::tmem_st16(t + 64 * (b >> 1) + 16 * (b & 1), pk);
+                store_block<TERMS>(t + 32 * b, pk);
+                if (b == 1) {                    // X S', scaled: the first half of the second product may start
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.o_full[wg], 0, a.wait_err));
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    scale_half<D>(t + 128, li1);
+                    scale_half<D>(t + 128 + D / 2, li1);
+                    tc::tmem_wait_st();
+                    tc::tc_fence_before();
+                    tc::mbar_arrive(&B.p_half[wg]);
+                }
             }
-            ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.o_full[wg], 0, a.wait_err));
             if (!ok) continue;
-            tc::tc_fence_after();
-            scale_half<D>(t + 128, li1);
-            scale_half<D>(t + 128 + D / 2, li1);
             tc::tmem_wait_st();
             tc::tc_fence_before();
             tc::mbar_arrive(&B.p_full[wg]);
-            if (lane == 0) tc::bulk_wait_read();     // the last head's boxes have left the stages
+            put_second();
+            if (lane == 0) tc::bulk_wait_read();     // the last head's boxes have left the stage
             __syncwarp();
             ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.o_full[wg], 1, a.wait_err));
             if (!ok) continue;
             tc::tc_fence_after();
             // The rows leave tensor memory first: the next head's products need not wait for the stores.
-            uint32_t o0[D / 4], o1[D / 4];
+            uint32_t o0[D / 4];
             load_half<D>(t + 128, scale, o0);
             load_half<D>(t + 128 + D / 2, scale, o1);
             tc::tc_fence_before();
             tc::mbar_arrive(&B.o_free[wg]);
-            store_half<D>(o0, &map_out, stage, lane, w.c.rows - 32 * quad, 0, w.head, w.c.row0 + 32 * quad, out);
-            store_half<D>(o1, &map_out, stage + L::kStage, lane, w.c.rows - 32 * quad, D / 2, w.head, w.c.row0 + 32 * quad, out);
+            left1 = w.c.rows - 32 * quad;
+            head1 = w.head;
+            row1 = w.c.row0 + 32 * quad;
+            store_half<D>(o0, &map_out, stage, lane, left1, 0, head1, row1, out);
         }
+        put_second();
         if (lane == 0) bulk_wait();
     }
     tc::tc_fence_before();
@@ -929,6 +997,7 @@ lin_rows_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
 template <int D> struct ColsLayout {
     static constexpr uint32_t kTile = D / 64 * 16384, kState = D / 64 * D * 128;
     static constexpr uint32_t kOffV = kTile, kOffG = 2 * kTile, kOffQ = kOffG + kState, kOffDo = kOffQ + 2 * kTile;
+    static constexpr uint32_t kOffG2 = kOffQ + kTile;                // G's second terms, then the second head's Q
     static constexpr uint32_t kSmem = kOffDo + 2 * kTile + 1024;
     static constexpr uint32_t kColDv = 256, kColDk = 256 + D;
 };
@@ -937,7 +1006,7 @@ constexpr int kColsThreads = 3 * 32 + 2 * 256;
 struct ColsBarriers {
     uint64_t k_full, v_full, g_full, q_full[2], do_full[2], q_empty[2], do_empty[2];
     uint64_t q_ready[2], do_ready[2];            // their tails zeroed (a chunk of less than 128 rows)
-    uint64_t s_full[2], init_full[2], p_full[2], acc_full[2];                     // by group
+    uint64_t s_full[2], init_full[2], p_half[2], p_full[2], acc_full[2];          // by group
     uint32_t tmem_base;
 };
 
@@ -945,12 +1014,13 @@ struct ColsBarriers {
 // sum_heads ((dO V^T) o M)^T Q + diag(l^(m-1-j)) V G^T of one chunk and KV head.
 // Scores are formed transposed (keys are the accumulator's rows): K Q^T in
 // columns [0, 128) for one group of eight warps (dV), V dO^T in [128, 256) for
-// another (dK), each with an issuing warp of its own; their weighted bf16 values
-// overwrite them as A operands. dV and dK stay in tensor memory over all heads; they start as
+// another (dK), each with an issuing warp of its own; their weighted values' bf16 terms
+// overwrite them as A operands, in two halves of the queries, so that the second product of
+// one runs while the weights of the other are formed. dV and dK stay in tensor memory over all heads; they start as
 // K G and V G^T, scaled there by l^(m-1-j) / scale. What bounds it is a head's chain of
-// score product, weighting and second product, 2 us, in each of a unit's g heads: 4096 rows,
-// 28/4 heads of d 128 (128 CTAs of seven heads) take 23 us.
-template <int D>
+// score product, weighting and second product, 2.6 us, in each of a unit's g heads: 4096 rows,
+// 28/4 heads of d 128 (128 CTAs of seven heads) take 28 us, with one term 23.
+template <int D, int TERMS>
 __global__ void __launch_bounds__(kColsThreads, 1)
 lin_cols_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
@@ -984,6 +1054,7 @@ lin_cols_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             tc::mbar_init(&B.do_ready[s], 256);
             tc::mbar_init(&B.s_full[s], 1);
             tc::mbar_init(&B.init_full[s], 1);
+            tc::mbar_init(&B.p_half[s], 256);
             tc::mbar_init(&B.p_full[s], 256);
             tc::mbar_init(&B.acc_full[s], 1);
         }
@@ -1009,6 +1080,8 @@ lin_cols_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         int n = 0;
         for (int i = 0; i < g; ++i) {
             const int s = i & 1;
+            if (TERMS == 2 && i == 1)            // the second head's Q takes the place of G's second terms
+                if (!tc::warp_wait(&B.init_full[0], 0, a.wait_err) || !tc::warp_wait(&B.init_full[1], 0, a.wait_err)) break;
             if (i >= 2 && !tc::warp_wait(&B.q_empty[s], ((i >> 1) - 1) & 1, a.wait_err)) break;
             if (i >= 2 && !tc::warp_wait(&B.do_empty[s], ((i >> 1) - 1) & 1, a.wait_err)) break;
             if (lane == 0) {
@@ -1033,10 +1106,12 @@ lin_cols_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             if (i == 0) {
                 wait_for_kernels();              // the gradients of the states
                 if (lane == 0) {
-                    tc::mbar_arrive_expect_tx(&B.g_full, L::kState);
+                    tc::mbar_arrive_expect_tx(&B.g_full, TERMS * L::kState);
 #pragma unroll
-                    for (int b = 0; b < D / 64; ++b)
+                    for (int b = 0; b < D / 64; ++b) {
                         tc::tma_load_2d(smem + L::kOffG + b * (D * 128), &map_g, &B.g_full, 64 * b, (f * a.Hkv + h) * D);
+                        if (TERMS == 2) tc::tma_load_2d(smem + L::kOffG2 + b * (D * 128), &map_g, &B.g_full, D + 64 * b, (f * a.Hkv + h) * D);
+                    }
                 }
             }
         }
@@ -1084,20 +1159,33 @@ lin_cols_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 if (leader) {
                     const uint64_t dg = x ? tc::sdesc(sm + L::kOffG, 16, 1024) : tc::sdesc(sm + L::kOffG, D * 128, 1024);
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        tc::mma_bf16(acc, tc::sdesc_at(dc, (k >> 2) * 16384 + (k & 3) * 32),
-                                     tc::sdesc_at(dg, x ? (k >> 2) * (D * 128) + (k & 3) * 32 : k * 2048), id_g, k > 0);
+                    for (int k = 0; k < TERMS * D / 16; ++k) {   // the first terms' inner indices, then the second ones'
+                        const int c = k % (D / 16), term = k / (D / 16) * (L::kOffG2 - L::kOffG);
+                        tc::mma_bf16(acc, tc::sdesc_at(dc, (c >> 2) * 16384 + (c & 3) * 32),
+                                     tc::sdesc_at(dg, term + (x ? (c >> 2) * (D * 128) + (c & 3) * 32 : c * 2048)), id_g, k > 0);
+                    }
                     tc::mma_commit(&B.init_full[x]);
                 }
                 __syncwarp();
             }
-            if (!tc::warp_wait(&B.p_full[x], i & 1, a.wait_err)) break;
+            // (the weights of the other blocks of queries are still being formed during the first half)
+            if (!tc::warp_wait(&B.p_half[x], i & 1, a.wait_err)) break;
             if (!tc::warp_wait(&other_full[s], (i >> 1) & 1, a.wait_err)) break;
             tc::tc_fence_after();
-            if (leader) {
-                const uint64_t db = tc::sdesc(sm + other + s * L::kTile, 16384, 1024);
+            const uint64_t db = tc::sdesc(sm + other + s * L::kTile, 16384, 1024);
+            auto product = [&](int first) {      // blocks first, first + 2
 #pragma unroll
-                for (int k = 0; k < 8; ++k) tc::mma_bf16_ts(acc, t + p_col(k), tc::sdesc_at(db, k * 2048), id_acc, 1u);
+                for (int n = 0; n < 4 * TERMS; ++n) {
+                    const int k = 2 * first + (n & 2) * 2 + (n & 1);
+                    tc::mma_bf16_ts(acc, t + p_col(k, n >> 2), tc::sdesc_at(db, k * 2048), id_acc, 1u);
+                }
+            };
+            if (leader) product(0);
+            __syncwarp();
+            if (!tc::warp_wait(&B.p_full[x], i & 1, a.wait_err)) break;
+            tc::tc_fence_after();
+            if (leader) {
+                product(1);
                 tc::mma_commit(&other_empty[s]);
             }
             __syncwarp();
@@ -1129,51 +1217,59 @@ lin_cols_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         for (int b = 0; b < 2; ++b) rb[b] = 2 * half + b > quad ? lin_pow(g2, 32 * (2 * half + b) - j) : 0.f;
         bool ok = !tail || tails(0);
         for (int i = 0; ok && i < g; ++i) {
-            if (tail && i + 1 < g && !(ok = tails(i + 1))) break;
+            if (tail && i > 0 && i + 1 < g && !(ok = tails(i + 1))) break;
             ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.s_full[x], i & 1, a.wait_err));
             if (!ok) break;
             tc::tc_fence_after();
-            uint32_t pk[32];
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 const int block = 2 * half + b;  // queries 32 block ..
+                uint32_t pk[16 * TERMS];         // first terms, second ones
+                uint32_t r[32];
+                if (block >= quad) {
+                    tc::tmem_ld32(t + 32 * block, r);
+                    tc::tmem_wait_ld(r);
+                    const int left = c.rows - 32 * block;
+                    if (left < 32) {             // queries behind the sequence: anything
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) r[e] = e < left ? r[e] : 0u;
+                    }
+                }
                 if (block < quad) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) pk[16 * b + e] = 0u;
-                    continue;
-                }
-                uint32_t r[32];
-                tc::tmem_ld32(t + 32 * block, r);
-                tc::tmem_wait_ld(r);
-                const int left = c.rows - 32 * block;
-                if (left < 32) {                 // queries behind the sequence: anything
+                    for (int e = 0; e < 16 * TERMS; ++e) pk[e] = 0u;
+                } else if (block > quad) {
+                    const f32x2 f = pack2(rb[b], rb[b]);
+                    const ulonglong2* u = reinterpret_cast<const ulonglong2*>(pw);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) r[e] = e < left ? r[e] : 0u;
-                }
-                if (block > quad) {
-                    const float f = rb[b];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        pk[16 * b + e] = pack_bf16x2(__uint_as_float(r[2 * e]) * (pw[2 * e] * f), __uint_as_float(r[2 * e + 1]) * (pw[2 * e + 1] * f));
+                    for (int e = 0; e < 16; e += 2) {
+                        const ulonglong2 k = u[e / 2];
+                        put_pair_terms<TERMS>(pk, e, mul2(pack2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), mul2(k.x, f)));
+                        put_pair_terms<TERMS>(pk, e + 1, mul2(pack2(__uint_as_float(r[2 * e + 2]), __uint_as_float(r[2 * e + 3])), mul2(k.y, f)));
+                    }
                 } else {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const float p0 = 2 * e >= lane ? __uint_as_float(r[2 * e]) * diag[2 * e - lane + 31] : 0.f;
                         const float p1 = 2 * e + 1 >= lane ? __uint_as_float(r[2 * e + 1]) * diag[2 * e + 32 - lane] : 0.f;
-                        pk[16 * b + e] = pack_bf16x2(p0, p1);
+                        put_pair_terms<TERMS>(pk, e, pack2(p0, p1));
                     }
                 }
+                store_block<TERMS>(t + 32 * block, pk);
+                if (b == 0 && i == 0) continue;  // (the first head's products wait for G: all weights first)
+                if (i == 0) {
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.init_full[x], 0, a.wait_err));
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    scale_half<D>(acc, j < c.rows ? lin_pow(g2, c.rows - 1 - j) / scale : 0.f);
+                }
+                tc::tmem_wait_st();
+                tc::tc_fence_before();
+                if (b == 0 || i == 0) tc::mbar_arrive(&B.p_half[x]);
+                if (b == 1) tc::mbar_arrive(&B.p_full[x]);
             }
-            tc::tmem_st32(t + 64 * half, pk);
-            if (i == 0) {
-                ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.init_full[x], 0, a.wait_err));
-                if (!ok) break;
-                tc::tc_fence_after();
-                scale_half<D>(acc, j < c.rows ? lin_pow(g2, c.rows - 1 - j) / scale : 0.f);
-            }
-            tc::tmem_wait_st();
-            tc::tc_fence_before();
-            tc::mbar_arrive(&B.p_full[x]);
+            if (!ok) break;
+            if (tail && i == 0 && g > 1) ok = tails(1);      // (behind the products with G, whose place Q's second tile takes)
         }
         if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&B.acc_full[x], 0, a.wait_err));
         if (ok) {
@@ -1207,8 +1303,9 @@ bool half_map(CUtensorMap* m, const LinRows& x, int H, const LinArgs& a, std::st
 bool sums_map(CUtensorMap* m, const float* p, const LinArgs& a, std::string* why) {
     return make_tmap_2d(m, p, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.d, (uint64_t)a.n_chunks * a.Hkv * a.d, a.d * 4, 32, 32, why);
 }
-bool states_map(CUtensorMap* m, const void* p, const LinArgs& a, std::string* why) {
-    return make_tmap_2d(m, p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.d, (uint64_t)a.n_chunks * a.Hkv * a.d, a.d * 2, 64, a.d, why);
+// The states as the scan leaves them: rows of d first and d second terms.
+bool states_map(CUtensorMap* m, const float* p, const LinArgs& a, std::string* why) {
+    return make_tmap_2d(m, p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2 * a.d, (uint64_t)a.n_chunks * a.Hkv * a.d, a.d * 4, 64, a.d, why);
 }
 
 // Launches a kernel that may start before the stream's last kernel, one of this
@@ -1234,7 +1331,7 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t sm
 // forward's sums kernel is held to registers that leave room for the scan's CTAs beside
 // it, so that their set-up overlaps (4096 rows, 4 KV heads of d 128: 1.7 us of 31); the
 // backward's is much longer and faster with more (0.64 us a stage instead of 0.75).
-template <int D, bool BOTH> cudaError_t states(const LinArgs& a, cudaStream_t s, std::string* why) {
+template <int D, int TERMS, bool BOTH> cudaError_t states(const LinArgs& a, cudaStream_t s, std::string* why) {
     static SmemGrant grant;
     cudaError_t e = allow_smem(lin_part_tc_kernel<D, BOTH>, PartLayout<D>::kSmem, grant);
     if (e != cudaSuccess) return e;
@@ -1254,59 +1351,61 @@ template <int D, bool BOTH> cudaError_t states(const LinArgs& a, cudaStream_t s,
     }
     const dim3 grid((unsigned)(a.n_seq * a.Hkv * (D * D / 4 / kScanThreads)), nz);
     ProfScope ps("lin_scan_bf16_kernel", s);
-    if (a.n) return launch_after(lin_scan_bf16_kernel<D>, grid, kScanThreads, 0, s, a);
-    lin_scan_bf16_kernel<D><<<grid, kScanThreads, 0, s>>>(a);                    // no sums before it
+    if (a.n) return launch_after(lin_scan_bf16_kernel<D, TERMS>, grid, kScanThreads, 0, s, a);
+    lin_scan_bf16_kernel<D, TERMS><<<grid, kScanThreads, 0, s>>>(a);                    // no sums before it
     return cudaGetLastError();
 }
 
-template <int D, bool GRAD> cudaError_t rows(const LinArgs& a, cudaStream_t s, std::string* why) {
+template <int D, int TERMS, bool GRAD> cudaError_t rows(const LinArgs& a, cudaStream_t s, std::string* why) {
     static SmemGrant grant;
-    const cudaError_t e = allow_smem(lin_rows_tc_kernel<D, GRAD>, RowsLayout<D>::kSmem, grant);
+    const cudaError_t e = allow_smem(lin_rows_tc_kernel<D, GRAD, TERMS>, RowsLayout<D, TERMS>::kSmem, grant);
     if (e != cudaSuccess) return e;
     CUtensorMap x, c, r, st, out;
     if (!rows_map(&x, GRAD ? a.dout : a.q, a.Hq, a, kL, why) || !rows_map(&c, GRAD ? a.v : a.k, a.Hkv, a, kL, why) ||
-        !rows_map(&r, GRAD ? a.k : a.v, a.Hkv, a, kL, why) || !states_map(&st, a.sbf, a, why) ||
+        !rows_map(&r, GRAD ? a.k : a.v, a.Hkv, a, kL, why) || !states_map(&st, a.part, a, why) ||
         !half_map(&out, GRAD ? a.dq : a.o, a.Hq, a, why))
         return cudaErrorInvalidValue;
     const int heads = a.n_chunks * a.Hq, units = a.n_chunks * a.Hkv, grid = std::min(heads, sm_count());
     ProfScope ps("lin_rows_tc_kernel", s);
-    return launch_after(lin_rows_tc_kernel<D, GRAD>, dim3(grid), kRowsThreads, RowsLayout<D>::kSmem, s, x, c, r, st,
+    return launch_after(lin_rows_tc_kernel<D, GRAD, TERMS>, dim3(grid), kRowsThreads, RowsLayout<D, TERMS>::kSmem, s, x, c, r, st,
                         out, a, Cut{heads / grid, heads % grid, units >= 8 * grid ? units : 0});
 }
 
-template <int D> cudaError_t cols(const LinArgs& a, cudaStream_t s, std::string* why) {
+template <int D, int TERMS> cudaError_t cols(const LinArgs& a, cudaStream_t s, std::string* why) {
     static SmemGrant grant;
-    const cudaError_t e = allow_smem(lin_cols_tc_kernel<D>, ColsLayout<D>::kSmem, grant);
+    const cudaError_t e = allow_smem(lin_cols_tc_kernel<D, TERMS>, ColsLayout<D>::kSmem, grant);
     if (e != cudaSuccess) return e;
     CUtensorMap q, k, v, go, gs, dv, dk;
     if (!rows_map(&q, a.q, a.Hq, a, kL, why) || !rows_map(&k, a.k, a.Hkv, a, kL, why) || !rows_map(&v, a.v, a.Hkv, a, kL, why) ||
-        !rows_map(&go, a.dout, a.Hq, a, kL, why) || !states_map(&gs, a.gbf, a, why) ||
+        !rows_map(&go, a.dout, a.Hq, a, kL, why) || !states_map(&gs, a.gpart, a, why) ||
         !half_map(&dv, a.dv, a.Hkv, a, why) || !half_map(&dk, a.dk, a.Hkv, a, why))
         return cudaErrorInvalidValue;
     ProfScope ps("lin_cols_tc_kernel", s);
-    return launch_after(lin_cols_tc_kernel<D>, dim3(a.n_chunks, a.Hkv), kColsThreads, ColsLayout<D>::kSmem, s, q, k, v, go, gs, dv,
+    return launch_after(lin_cols_tc_kernel<D, TERMS>, dim3(a.n_chunks, a.Hkv), kColsThreads, ColsLayout<D>::kSmem, s, q, k, v, go, gs, dv,
                         dk, a);
 }
 
-template <int D> cudaError_t fwd(const LinArgs& a, cudaStream_t s, std::string* why) {
-    const cudaError_t e = states<D, false>(a, s, why);
-    return e != cudaSuccess || !a.n ? e : rows<D, false>(a, s, why);
+template <int D, int TERMS> cudaError_t fwd(const LinArgs& a, cudaStream_t s, std::string* why) {
+    const cudaError_t e = states<D, TERMS, false>(a, s, why);
+    return e != cudaSuccess || !a.n ? e : rows<D, TERMS, false>(a, s, why);
 }
 
-template <int D> cudaError_t bwd(const LinArgs& a, cudaStream_t s, std::string* why) {
-    cudaError_t e = states<D, true>(a, s, why);
-    if (e == cudaSuccess && a.n) e = cols<D>(a, s, why);
-    return e != cudaSuccess || !a.n ? e : rows<D, true>(a, s, why);
+template <int D, int TERMS> cudaError_t bwd(const LinArgs& a, cudaStream_t s, std::string* why) {
+    cudaError_t e = states<D, TERMS, true>(a, s, why);
+    if (e == cudaSuccess && a.n) e = cols<D, TERMS>(a, s, why);
+    return e != cudaSuccess || !a.n ? e : rows<D, TERMS, true>(a, s, why);
 }
 
 }  // namespace
 
 cudaError_t launch_lin_fwd_tc(const LinArgs& a, cudaStream_t s, std::string* why) {
-    return a.d == 128 ? fwd<128>(a, s, why) : fwd<64>(a, s, why);
+    if (a.one_term) return a.d == 128 ? fwd<128, 1>(a, s, why) : fwd<64, 1>(a, s, why);
+    return a.d == 128 ? fwd<128, 2>(a, s, why) : fwd<64, 2>(a, s, why);
 }
 
 cudaError_t launch_lin_bwd_tc(const LinArgs& a, cudaStream_t s, std::string* why) {
-    return a.d == 128 ? bwd<128>(a, s, why) : bwd<64>(a, s, why);
+    if (a.one_term) return a.d == 128 ? bwd<128, 1>(a, s, why) : bwd<64, 1>(a, s, why);
+    return a.d == 128 ? bwd<128, 2>(a, s, why) : bwd<64, 2>(a, s, why);
 }
 
 }  // namespace pkv

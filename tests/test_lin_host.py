@@ -167,3 +167,12 @@ def test_binding_norm_tensors(lin):
             B.pkv_layer_norm_fwd(64, 64, bad, bad, 4, m)
     with pytest.raises(ValueError, match="scratch"):
         B.pkv_layer_norm_bwd(64, 64, 64, 64, None, 64, None, 4, m, torch.zeros(3))
+
+
+def test_flags_of_a_store():
+    for flags in (0, B.PKV_FLAG_SIMT_ONLY, B.PKV_FLAG_LIN_ONE_TERM, B.PKV_FLAG_SIMT_ONLY | B.PKV_FLAG_LIN_ONE_TERM):
+        B.pkv_lin_destroy(B.pkv_lin_create(2, 4, 64, residency=B.PKV_RES_META, flags=flags))
+    for flags in (4, 4 | B.PKV_FLAG_LIN_ONE_TERM, 1 << 31):
+        with pytest.raises(B.PkvError) as e:
+            B.pkv_lin_create(2, 4, 64, residency=B.PKV_RES_META, flags=flags)
+        assert e.value.status == B.PKV_ERR_INVALID
