@@ -507,7 +507,9 @@ pkv_status pkv_stage_stats(pkv_seq* seq, int64_t* kv_in, int64_t* grads_in, int6
  * starts from, so that the backward sweep finds it again. Calls on one store
  * must not overlap on the GPU, but for pkv_lin_attn_step calls on different
  * slots: the others share its scratch memory, grown on demand (a stream
- * capture needs an earlier call of the same sizes, else PKV_ERR_INVALID). */
+ * capture needs an earlier call of the same sizes, else PKV_ERR_INVALID) and kept
+ * until the store is destroyed, outgrown parts too, as captured graphs may use
+ * them: less than four times what the largest call needs, where memory allows. */
 typedef struct pkv_lin_desc {
     int32_t n_kv_heads;        /* Hkv                                                    */
     int32_t n_q_heads;         /* Hq, a multiple of Hkv                                  */

@@ -76,15 +76,23 @@ pkv_status chunk_states(pkv_lin* lin, LinArgs* a, bool bwd, cudaStream_t cs, con
             return fail(PKV_ERR_INVALID, std::string(who) + ": needs a larger scratch buffer than the store has; run the call "
                                                             "once before capturing it");
         lin->retired.reserve(lin->retired.size() + 1);
+        // At least twice the old buffer, so that all that were outgrown, which stay, are together
+        // smaller than the new one; just what is needed where that is all there is room for.
+        size_t size = std::max(floats, 2 * lin->scratch_floats);
         float* p = nullptr;
-        const cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&p), floats * sizeof(float));
+        cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&p), size * sizeof(float));
+        if (e != cudaSuccess && size > floats) {
+            cudaGetLastError();
+            size = floats;
+            e = cudaMalloc(reinterpret_cast<void**>(&p), size * sizeof(float));
+        }
         if (e != cudaSuccess) {
             cudaGetLastError();                  // reported here, not left for the next launch check
             return cuda_fail(e, (std::string(who) + ": scratch").c_str());
         }
         if (lin->scratch) lin->retired.push_back(lin->scratch);
         lin->scratch = p;
-        lin->scratch_floats = floats;
+        lin->scratch_floats = size;
     }
     a->part = lin->scratch;
     a->gpart = bwd ? lin->scratch + one : nullptr;
