@@ -281,7 +281,8 @@ class LinearRecurrentBlock:
 
     def _batch(self, c: int):
         """Chunk c's sequences: pieces of documents. The first goes on from slot c if its
-        document began before the chunk, the last leaves slot c + 1 if its goes on after it."""
+        document began before the chunk, the last leaves slot c + 1 if its goes on after it.
+        Of the forward, of its recomputation (which leaves no state) and of the backward."""
         if c not in self._batches:
             s, e = self.w.chunk_range(c)
             first = self.first
@@ -296,7 +297,8 @@ class LinearRecurrentBlock:
             back[-1] = c + 1 if goes_on(e) else -1               # no gradient comes from behind the end
             dev = lambda a, t: torch.tensor(a, dtype=t, device="cuda")  # noqa: E731
             cu, at = dev([t - s for t in cuts] + [e - s], torch.int64), dev(slot_in, torch.int32)
-            self._batches[c] = tuple(B.lin_batch(m, cu, at, dev(out, torch.int32)) for out in (slot_out, back))
+            self._batches[c] = tuple(B.lin_batch(m, cu, at, None if out is None else dev(out, torch.int32))
+                                     for out in (slot_out, None, back))
         return self._batches[c]
 
     def _check_rows(self, c: int, x):
@@ -324,8 +326,9 @@ class LinearRecurrentBlock:
 
     def backward(self, xs: list, dys: list):
         """Chunks in reverse, on the current stream, after ``forward`` of the same inputs
-        (activations are recomputed, states are not). Returns every chunk's input
-        gradient and the weight gradients (float32)."""
+        (activations are recomputed, from the states that it left; the backward writes none, so
+        tokens may be generated in between). Returns every chunk's input gradient and the
+        weight gradients (float32)."""
         if len(xs) != self.w.n_chunks or len(dys) != len(xs):
             raise ValueError(f"the backward goes over all {self.w.n_chunks} chunks, got {len(xs)} and {len(dys)}")
         W, stream = self.weights, torch.cuda.current_stream()
@@ -334,11 +337,11 @@ class LinearRecurrentBlock:
         for c in reversed(range(len(xs))):
             x, dy, n = xs[c], dys[c], len(xs[c])
             self._check_rows(c, x)
-            batch, back = self._batch(c)
+            _, again, back = self._batch(c)
             h, *stats = self.norm.forward(x, stream)
             q, k, v = self._qkv(h)
             a = torch.empty_like(q)
-            B.pkv_lin_attn_fwd(self.lin, q, k, v, a, n, self.log_decay, batch, stream)
+            B.pkv_lin_attn_fwd(self.lin, q, k, v, a, n, self.log_decay, again, stream)
             a = a.view(n, -1)
             z, *head_stats = self.head_norm.forward(a, stream)
             g["wo"] += (z.t() @ dy).float()
