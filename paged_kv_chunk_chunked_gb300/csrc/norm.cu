@@ -678,9 +678,12 @@ template <typename T> Shape shape_of(int64_t width, bool vec, bool bwd) {
     return bwd ? shape_for(width / kVec<T>, 2, 32 / kVec<T>, kMaxTeam) : shape_for(width / kVec<T>, 4, 16, kMaxTeam);
 }
 
-// Lane teams, or CTAs, that share a group's rows: what the GPU holds at once and no more
-// (4096 rows of 28 heads of 128 columns, backward: 23.7 us, with a few CTAs above it 33),
-// but four rows each at least (64 rows of 3584 columns: 10.0 us, with eight 11.9; two were no
+// Lane teams, or CTAs, that share a group's rows. Lane teams: what the GPU holds at once and
+// no more (4096 rows of 28 heads of 128 columns, backward: 23.7 us, with a few CTAs above it
+// 33). CTAs, of which an SM holds one: for each group the SMs' share rounded up, which is more
+// than all hold at once where the groups do not divide 152 (28 groups: 168 CTAs, a second
+// wave of 16). 152 is a constant, as the scratch's size must not depend on the current
+// device. But four rows each at least (64 rows of 3584 columns: 10.0 us, with eight 11.9; two were no
 // faster), and in the backward 608 lane teams at most, as every share of dw and db is
 // written and read again (8192 rows of 128 columns: 16.3 us; with 2048 teams 21.7).
 int slots_of(int64_t n, int groups, const Shape& sh, bool bwd) {
